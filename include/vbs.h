@@ -315,11 +315,46 @@ int kv_paged_init(vbs_pkv** pkv, const vbs_kv_desc* desc, int batch, int W, int 
  * K/V through the table of the sentence's first row and calls
  * kv_paged_prepare(P) before the first generated position is written.
  * Synchronises the stream (the tables are built on the host, once per decode).
- * Drops copies still pending.
+ * Drops copies still pending.  kv_paged_build is the form for prompts of
+ * different lengths, without the synchronisation.
  * Errors: VBS_EINVAL (P < 0, or the prompt needs more blocks than a sentence
  *   owns or a table row holds), VBS_ECUDA.
  */
 int kv_paged_prefill(vbs_pkv* pkv, int P);
+/*
+ * The prompts, each of its own length, laid out on the GPU: lens[batch] (device
+ * int32) are the sentences' prompt lengths.  Sentence b gets ceil(lens[b] / block)
+ * blocks b*S, b*S + 1, ... that all W of its rows point at (table entries past them
+ * are -1).  From here on t_write and t_valid of kv_paged_prepare, kv_paged_reorder
+ * and bs_step_paged count positions after each sentence's own prompt (position
+ * lens[b] + t); kv_paged_prefill returns to absolute positions.
+ * Optionally also the prompts' slot map, the tokens of all sentences one after the
+ * other: slots[i] (int64) = block * block_size + offset of token i in a layer's pool,
+ * pos[i] its position and row[i] the first row of its sentence (int32, may be NULL),
+ * entries from the last token to `cap` are -1; cu[batch + 1] (may be NULL) the
+ * exclusive sums of the lengths.  slots NULL (cap 0): no slot map.
+ * No host synchronisation.  Drops copies still pending.
+ * Errors: VBS_EINVAL (NULL pkv or lens, cap outside [0, 2^31) or without slots),
+ *   VBS_ECUDA; a length below 0 or beyond what the sentence's blocks or table hold is
+ *   taken as 0, and that or more tokens than cap is VBS_EINVAL in kv_paged_status().
+ */
+int kv_paged_build(vbs_pkv* pkv, const int32_t* lens, int64_t cap, int64_t* slots, int32_t* pos, int32_t* row,
+                   int32_t* cu);
+/*
+ * A slot map from the tables: request i of n covers positions [start[i], start[i] +
+ * count[i]) (device int32) of row i (n = batch * W), or of the first row of sentence i
+ * (n = batch).  Outputs as kv_paged_build's.  A position that the row's table does
+ * not cover gets slot -1 and VBS_EINVAL in kv_paged_status().
+ * Errors: VBS_EINVAL (n neither batch nor batch * W, NULL pointers, cap), VBS_ECUDA.
+ */
+int kv_paged_slots(vbs_pkv* pkv, int n, const int32_t* start, const int32_t* count, int64_t cap, int64_t* slots,
+                   int32_t* pos, int32_t* row, int32_t* cu);
+/* The device addresses of the allocator's state (library-owned, valid until
+   kv_paged_destroy, read-only): table [R][max_blocks], nblk [R] blocks per row, refcnt
+   [batch * blocks_per_sentence], the sentences' free stacks [batch][blocks_per_sentence]
+   and their heights top [batch].  Errors: VBS_EINVAL (NULL arguments). */
+int kv_paged_state(vbs_pkv* pkv, const int32_t** table, const int32_t** nblk, const int32_t** refcnt,
+                   const int32_t** stack, const int32_t** top);
 /*
  * Make the block that position t_write lands in exclusive to every live row:
  * a row whose table ends at that block boundary gets a fresh block; of the
@@ -327,7 +362,8 @@ int kv_paged_prefill(vbs_pkv* pkv, int P);
  * gets a copy of its t_write % block filled slots (copy-on-write).
  * Errors: VBS_EINVAL (t_write < 0, or a block index beyond max_blocks),
  *   VBS_ESTATE (copies recorded by bs_step_paged still pending), VBS_ECUDA;
- *   an exhausted free stack is VBS_ENOMEM in kv_paged_status().
+ *   an exhausted free stack is VBS_ENOMEM in kv_paged_status(), a position past
+ *   the table's end after kv_paged_build VBS_EINVAL.
  */
 int kv_paged_prepare(vbs_pkv* pkv, int t_write);
 /*

@@ -12,6 +12,8 @@ Modules
 ``bpd``   blockwise parallel decoding: predict, verify, accept, and the greedy
           decoder it must reproduce ("Blockwise Parallel Decoding for Deep
           Autoregressive Models", §2-§4).
+``attn``  block tables and slot maps, the 8-bit paged cache, attention over it and over an
+          encoder's states.
 ``kv``    KV-cache reorder: the naive gather and a paged block table with
           copy-on-write ("9.2 贪心搜索与束搜索", §9.2.2 and §9.2.4).
 

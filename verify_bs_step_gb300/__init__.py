@@ -49,6 +49,9 @@ SIGNATURES = {
     "vbs_stateless_status": (_c_int, [_vp]),
     "kv_paged_init": (_c_int, [_pp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
     "kv_paged_prefill": (_c_int, [_vp, _c_int]),
+    "kv_paged_build": (_c_int, [_vp, _vp, _c_i64, _vp, _vp, _vp, _vp]),
+    "kv_paged_slots": (_c_int, [_vp, _c_int, _vp, _vp, _c_i64, _vp, _vp, _vp, _vp]),
+    "kv_paged_state": (_c_int, [_vp, _pp, _pp, _pp, _pp, _pp]),
     "kv_paged_prepare": (_c_int, [_vp, _c_int]),
     "kv_paged_reorder": (_c_int, [_vp, _vp, _c_int]),
     "bs_step_two_pass": (_c_int, [_vp, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp]),
@@ -147,6 +150,35 @@ def _dtype_code(dt) -> int:
     if dt == torch.float32:
         return F32
     raise ValueError(f"logits dtype must be bfloat16 or float32, got {dt}")
+
+
+class _DeviceArray:
+    """Device memory of the library as an array that torch.as_tensor() takes without a copy."""
+
+    def __init__(self, ptr: int, shape, typestr: str):
+        self.__cuda_array_interface__ = {"data": (ptr, False), "shape": tuple(shape), "typestr": typestr,
+                                         "strides": None, "version": 2}
+
+
+class _StreamOrder:
+    """Orders a call on a context's stream after, and what follows it before, the work of the stream
+    that is current when the call is made, where the two differ; `tensors` stay allocated until then."""
+
+    def __init__(self, ctx_stream, device, *tensors):
+        cur = torch.cuda.current_stream(device)
+        self.cur = None if cur.cuda_stream == ctx_stream.cuda_stream else cur
+        self.ctx, self.tensors = ctx_stream, tensors
+
+    def __enter__(self):
+        if self.cur is not None:
+            self.ctx.wait_stream(self.cur)
+
+    def __exit__(self, *exc):
+        if self.cur is not None:
+            self.cur.wait_stream(self.ctx)
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.ctx)
 
 
 class BeamSearch:
@@ -382,19 +414,68 @@ class PagedKV:
         if pool is None:
             pool = torch.zeros(batch * blocks_per_sentence, L, 2, H, block, D, dtype=dtype, device=self.device)
         self.pool = pool
-        self.stream = _vp(torch.cuda.current_stream(self.device).cuda_stream)
+        self._stream_obj = torch.cuda.current_stream(self.device)
+        self.stream = _vp(self._stream_obj.cuda_stream)
         desc = _KvDesc(L, H, D, max_blocks * block, pool.element_size())
         ctx = _vp()
         _check(lib().kv_paged_init(ctypes.byref(ctx), ctypes.byref(desc), batch, W, blocks_per_sentence, block,
                                    max_blocks, _dev_ptr(pool, "pool"), self.stream), "kv_paged_init")
         self.ctx = ctx
-        ptr = _vp()
-        mb = _c_int()
-        _check(lib().kv_paged_table(self.ctx, ctypes.byref(ptr), ctypes.byref(mb)), "kv_paged_table")
-        self._table_ptr = ptr.value
+        ptr = [_vp() for _ in range(5)]
+        _check(lib().kv_paged_state(self.ctx, *[ctypes.byref(p) for p in ptr]), "kv_paged_state")
+        shapes = ((self.R, max_blocks), (self.R,), (batch * self.S,), (batch * self.S,), (batch,))
+        self._views = tuple(torch.as_tensor(_DeviceArray(p.value, s, "<i4"), device=self.device)
+                            for p, s in zip(ptr, shapes))
 
     def prefill(self, P: int):
         _check(lib().kv_paged_prefill(self.ctx, P), "kv_paged_prefill")
+
+    def build(self, lens: torch.Tensor, cap: int | None = None):
+        """prefill() for prompts of different lengths, laid out on the GPU with no host round trip.
+
+        lens: int32 [batch] on the device.  Afterwards prepare(t), reorder(.., t) and
+        BeamSearch.step_paged(.., t) count positions after each sentence's own prompt.  With cap (room
+        for that many tokens): returns the prompts' slot map (slots int64 [cap], pos int32 [cap],
+        row int32 [cap], cu int32 [batch + 1]); unused entries are -1."""
+        if lens.shape != (self.batch,) or not lens.is_contiguous():
+            raise ValueError(f"lens must be a contiguous int32 [{self.batch}] tensor")
+        lp = _dev_ptr(lens, "lens", torch.int32)
+        out = self._slot_outputs(self.batch, cap) if cap is not None else None
+        with _StreamOrder(self._stream_obj, self.device, lens, *(out or ())):
+            _check(lib().kv_paged_build(self.ctx, lp, *self._slot_args(out)), "kv_paged_build")
+        return out
+
+    def slot_map(self, start: torch.Tensor, count: torch.Tensor, cap: int):
+        """The slot map of positions [start[i], start[i] + count[i]) of every row (tensors of R entries) or
+        of every sentence's first row (batch entries), int32 on the device, as build() returns it."""
+        n = start.numel()
+        if n not in (self.batch, self.R) or start.shape != (n,) or count.shape != (n,):
+            raise ValueError(f"start and count must have {self.R} (or {self.batch}) entries each")
+        if not (start.is_contiguous() and count.is_contiguous()):
+            raise ValueError("start and count must be contiguous")
+        sp, cp = _dev_ptr(start, "start", torch.int32), _dev_ptr(count, "count", torch.int32)
+        out = self._slot_outputs(n, cap)
+        with _StreamOrder(self._stream_obj, self.device, start, count, *out):
+            _check(lib().kv_paged_slots(self.ctx, n, sp, cp, *self._slot_args(out)), "kv_paged_slots")
+        return out
+
+    def _slot_outputs(self, n: int, cap: int):
+        if cap < 0:
+            raise ValueError("cap must not be negative")
+        i32 = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device)
+        return (torch.empty(cap, dtype=torch.int64, device=self.device), i32[:cap], i32[cap:2 * cap], i32[2 * cap:])
+
+    @staticmethod
+    def _slot_args(out):
+        if out is None:
+            return 0, None, None, None, None
+        return (out[0].numel(),) + tuple(_vp(t.data_ptr()) for t in out)
+
+    def views(self):
+        """The allocator's state as int32 tensors on the library's own memory (no copy; valid until close(),
+        not to be written): table [R, max_blocks], blocks per row [R], reference counts, free stacks
+        [batch * blocks_per_sentence] and their heights [batch]."""
+        return self._views
 
     def prepare(self, t_write: int):
         _check(lib().kv_paged_prepare(self.ctx, t_write), "kv_paged_prepare")

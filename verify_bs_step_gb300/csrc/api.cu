@@ -11,9 +11,11 @@
 
 #include "common.cuh"
 #include "bs_internal.h"
+#include "host.h"
 
-#define VBS_EXPORT extern "C" __attribute__((visibility("default")))
-
+using vbs::aligned16;
+using vbs::Carver;
+using vbs::num_sms;
 using vbs::u64;
 
 namespace {
@@ -21,32 +23,11 @@ namespace {
 // Status word of the stateless calls (kv_reorder), in static device memory.
 __device__ int g_stateless_status;
 
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
-  return n;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // lp(|y|) of "9.2 贪心搜索与束搜索" §9.2.3: GNMT ((5 + |y|) / 6)^alpha or |y|^alpha; alpha = 0 gives 1.
 double length_penalty(int n, double alpha, int kind) {
   if (alpha == 0.0) return 1.0;
   return kind == VBS_LP_GNMT ? std::pow((5.0 + n) / 6.0, alpha) : std::pow(static_cast<double>(n), alpha);
 }
-
-// One device allocation carved into 256-byte aligned pieces.
-struct Carver {
-  size_t off = 0;
-  char* base = nullptr;
-  template <class T> T* take(size_t n) {
-    off = (off + 255) & ~static_cast<size_t>(255);
-    T* p = reinterpret_cast<T*>(base ? base + off : nullptr);
-    off += n * sizeof(T);
-    return p;
-  }
-};
 
 }  // namespace
 
@@ -59,18 +40,6 @@ struct vbs_bs {
   int32_t* seqs_bound;          // the sequence buffer of the current decode
   int32_t* own_seqs;
   void* dev_block;
-};
-
-struct vbs_pkv {
-  vbs::PagedArgs a;
-  cudaStream_t stream;
-  int32_t* identity;
-  int R;
-  void* dev_block;
-  char* state;           // table .. top: one contiguous range of the allocation
-  char* saved;           // its copy (kv_paged_save / kv_paged_restore)
-  size_t state_bytes;
-  bool copy_pending;     // bs_step_paged recorded copies that kv_paged_copy has not run
 };
 
 VBS_EXPORT const char* vbs_strerror(int status) {
@@ -502,6 +471,7 @@ VBS_EXPORT int kv_paged_init(vbs_pkv** out, const vbs_kv_desc* d, int batch, int
     a.refcnt = cv.take<int32_t>(NB);
     a.stack = cv.take<int32_t>(NB);
     a.top = cv.take<int32_t>(batch);
+    a.base = cv.take<int32_t>(batch);
     const size_t state_end = cv.off;
     c->saved = cv.take<char>(state_end);
     c->state = reinterpret_cast<char*>(a.table);
@@ -511,6 +481,7 @@ VBS_EXPORT int kv_paged_init(vbs_pkv** out, const vbs_kv_desc* d, int batch, int
     a.cow_slots = cv.take<unsigned long long>(1);
     a.status = cv.take<int>(1);
     c->identity = cv.take<int32_t>(R);
+    c->scan = cv.take<int32_t>(R + 1);
     if (pass == 0) {
       void* p = nullptr;
       if (cudaMalloc(&p, cv.off) != cudaSuccess) {
@@ -571,10 +542,42 @@ VBS_EXPORT int kv_paged_prefill(vbs_pkv* c, int P) {
   ok = ok && cudaMemcpyAsync(a.refcnt, refcnt.data(), refcnt.size() * 4, cudaMemcpyHostToDevice, c->stream) == cudaSuccess;
   ok = ok && cudaMemcpyAsync(a.stack, stack.data(), stack.size() * 4, cudaMemcpyHostToDevice, c->stream) == cudaSuccess;
   ok = ok && cudaMemcpyAsync(a.top, top.data(), top.size() * 4, cudaMemcpyHostToDevice, c->stream) == cudaSuccess;
+  ok = ok && cudaMemsetAsync(a.base, 0, sizeof(int32_t) * a.B, c->stream) == cudaSuccess;
   ok = ok && cudaMemsetAsync(a.tasks, 0, sizeof(int4) * c->R, c->stream) == cudaSuccess;
   ok = ok && cudaStreamSynchronize(c->stream) == cudaSuccess;
   c->copy_pending = false;
   return ok ? VBS_OK : VBS_ECUDA;
+}
+
+VBS_EXPORT int kv_paged_build(vbs_pkv* c, const int32_t* lens, int64_t cap, int64_t* slots, int32_t* pos, int32_t* row,
+                              int32_t* cu) {
+  if (!c || !lens || cap < 0 || cap >= (int64_t{1} << 31)) return VBS_EINVAL;
+  if (cap > 0 && !slots) return VBS_EINVAL;
+  const vbs::SlotArgs s{c->a.B, nullptr, lens, cap, slots, pos, row, cu, c->scan};
+  // copies still pending refer to the tables being replaced: forget them
+  if (cudaMemsetAsync(c->a.tasks, 0, sizeof(int4) * c->R, c->stream) != cudaSuccess) return VBS_ECUDA;
+  c->copy_pending = false;
+  return vbs::launch_kv_build(c->a, s, true, num_sms(), c->stream);
+}
+
+VBS_EXPORT int kv_paged_slots(vbs_pkv* c, int n, const int32_t* start, const int32_t* count, int64_t cap,
+                              int64_t* slots, int32_t* pos, int32_t* row, int32_t* cu) {
+  if (!c || !start || !count || cap < 0 || cap >= (int64_t{1} << 31)) return VBS_EINVAL;
+  if (n != c->a.B && n != c->R) return VBS_EINVAL;
+  if (cap > 0 && !slots) return VBS_EINVAL;
+  const vbs::SlotArgs s{n, start, count, cap, slots, pos, row, cu, c->scan};
+  return vbs::launch_kv_build(c->a, s, false, num_sms(), c->stream);
+}
+
+VBS_EXPORT int kv_paged_state(vbs_pkv* c, const int32_t** table, const int32_t** nblk, const int32_t** refcnt,
+                              const int32_t** stack, const int32_t** top) {
+  if (!c || !table || !nblk || !refcnt || !stack || !top) return VBS_EINVAL;
+  *table = c->a.table;
+  *nblk = c->a.nblk;
+  *refcnt = c->a.refcnt;
+  *stack = c->a.stack;
+  *top = c->a.top;
+  return VBS_OK;
 }
 
 VBS_EXPORT int kv_paged_prepare(vbs_pkv* c, int t_write) {

@@ -59,6 +59,7 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
     p = __ldcg(bi + r0 + tid);                            // a fused caller wrote it in this kernel
   }
   if (tid == 0) top = a.top[b];
+  const int base = a.base[b];
   for (int i0 = 0; i0 < nt || i0 < S; i0 += NT * LU) {
     int tv[LU], rv[LU], sv[LU];
 #pragma unroll
@@ -131,7 +132,8 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
     // the block holding position t_valid must be exclusive to each live row: a row whose
     // parent ends just before it takes a fresh block (kind 1); a row whose parent's block
     // there is shared keeps it if it is the lowest such row, else copies it (kind 2)
-    const int i = t_valid / a.block, fill = t_valid % a.block;
+    const int t_abs = base + t_valid;
+    const int i = t_abs / a.block, fill = t_abs % a.block;
     const u32 lt = (1u << lane) - 1u;
     int kind = 0, blk = -1, nnew = 0;
     if (lane < W) {
@@ -141,7 +143,9 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
       } else {
         const int n = sh.nold[p - r0];
         nnew = n;
-        if (n == i) {
+        if (i >= MB) {
+          set_status(a.status, VBS_EINVAL);               // past the table's end (ragged lengths)
+        } else if (n == i) {
           kind = 1;
         } else if (n == i + 1) {
           blk = old[(p - r0) * MB + i];
@@ -193,7 +197,7 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
   __syncthreads();
 
   // write back
-  const int ti = t_valid / a.block;
+  const int ti = (base + t_valid) / a.block;
   for (int i = tid; i < W * MB; i += NT) {
     const int w = i / MB, s = i - w * MB;
     const int p = sh.par[w];

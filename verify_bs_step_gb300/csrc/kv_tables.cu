@@ -1,0 +1,133 @@
+// Block tables and slot maps from request lengths, on the GPU (sm_103a).
+//
+// For request lengths len[b], sentence b gets n = ceil(len / block) blocks b*S, b*S + 1, ...
+// named by all W rows' tables, reference counts W on them, and a free stack that hands out
+// the rest in ascending order.  The flat token list of n requests is laid out one request after
+// the other (cu = exclusive sums of the counts); the token at position p of request i lives in slot
+// table[row][p / block] * block + p % block of a layer's pool.
+//
+// Both are stores with no reuse (16 bytes a token, 4 a table entry), so the time is the
+// launch plus the bytes at the write bandwidth; the only dependence between requests is the
+// sum of the counts before them.
+
+#include "common.cuh"
+#include "kv_tables.h"
+
+namespace vbs {
+
+constexpr int TAB_NT = 256;
+
+// A request's length if the cache can hold it, else 0 (and the status says so).
+__device__ __forceinline__ int valid_len(const PagedArgs& a, int len) {
+  const int most = a.S < a.MB ? a.S : a.MB;
+  if (len >= 0 && (static_cast<int64_t>(len) + a.block - 1) / a.block <= most) return len;
+  set_status(a.status, VBS_EINVAL);
+  return 0;
+}
+
+__device__ __forceinline__ int valid_count(const PagedArgs& a, const SlotArgs& s, int i, bool build) {
+  const int c = s.count[i];
+  if (build) return valid_len(a, c);
+  const int st = s.start ? s.start[i] : 0;
+  if (c >= 0 && st >= 0 && static_cast<int64_t>(st) + c <= static_cast<int64_t>(a.MB) * a.block) return c;
+  set_status(a.status, VBS_EINVAL);
+  return 0;
+}
+
+// Exclusive sums of the counts into scan[0..n] (and cu): one CTA.
+__global__ void __launch_bounds__(1024) kv_scan_kernel(const PagedArgs a, const SlotArgs s, bool build) {
+  __shared__ int64_t warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  int64_t carry = 0;
+  for (int i0 = 0; i0 < s.n; i0 += 1024) {
+    const int i = i0 + tid;
+    const int64_t v = i < s.n ? valid_count(a, s, i, build) : 0;
+    int64_t x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sum[wid] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int64_t t = warp_sum[w];
+      if (w < wid) before += t;
+      all += t;
+    }
+    const int64_t ex = carry + before + x - v;
+    if (i < s.n) {
+      const int e = static_cast<int>(ex < INT32_MAX ? ex : INT32_MAX);
+      s.scan[i] = e;
+      if (s.cu) s.cu[i] = e;
+    }
+    carry += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    const int e = static_cast<int>(carry < INT32_MAX ? carry : INT32_MAX);
+    s.scan[s.n] = e;
+    if (s.cu) s.cu[s.n] = e;
+    if (carry > s.cap && s.slots) set_status(a.status, VBS_EINVAL);
+  }
+}
+
+// CTA (i, c): chunk c of request i's table rows and tokens.
+__global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, const SlotArgs s, bool build) {
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * TAB_NT;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * TAB_NT + tid;
+  const int count = valid_count(a, s, i, build);
+  const int start = s.start ? s.start[i] : 0;
+  const int first = s.scan[i];
+  const int row = build || s.n == a.B ? i * a.W : i;
+  const int32_t* tab = a.table + static_cast<int64_t>(row) * a.MB;
+  if (build) {
+    const int nb = (count + a.block - 1) / a.block;
+    for (int64_t j = t0; j < static_cast<int64_t>(a.W) * a.MB; j += step) {
+      const int c = static_cast<int>(j % a.MB);
+      a.table[static_cast<int64_t>(row) * a.MB + j] = c < nb ? i * a.S + c : -1;
+    }
+    for (int64_t j = t0; j < a.S; j += step) {
+      a.refcnt[static_cast<int64_t>(i) * a.S + j] = j < nb ? a.W : 0;
+      a.stack[static_cast<int64_t>(i) * a.S + j] = i * a.S + (a.S - 1 - static_cast<int>(j));
+    }
+    if (t0 < a.W) a.nblk[row + t0] = nb;
+    if (t0 == 0) {
+      a.top[i] = a.S - nb;
+      a.base[i] = count;
+    }
+  }
+  if (!s.slots) return;
+  for (int64_t k = t0; k < count; k += step) {
+    const int64_t o = first + k;
+    if (o >= s.cap) break;
+    const int p = start + static_cast<int>(k);
+    const int j = p / a.block;
+    const int blk = build ? i * a.S + j : (j < a.nblk[row] ? tab[j] : -1);
+    if (blk < 0) set_status(a.status, VBS_EINVAL);          // a position that the table does not cover
+    s.slots[o] = blk < 0 ? -1 : static_cast<int64_t>(blk) * a.block + (p - j * a.block);
+    if (s.pos) s.pos[o] = p;
+    if (s.row) s.row[o] = row;
+  }
+  // the entries past the last token, shared out over all CTAs
+  const int64_t all = static_cast<int64_t>(gridDim.x) * step;
+  for (int64_t o = s.scan[s.n] + i * step + t0; o < s.cap; o += all) {
+    s.slots[o] = -1;
+    if (s.pos) s.pos[o] = -1;
+    if (s.row) s.row[o] = -1;
+  }
+}
+
+int launch_kv_build(const PagedArgs& a, const SlotArgs& s, bool build, int num_sms, cudaStream_t stream) {
+  kv_scan_kernel<<<1, 1024, 0, stream>>>(a, s, build);
+  // enough CTAs to fill the GPU when the requests are few and long
+  const int64_t most = std::max<int64_t>(static_cast<int64_t>(a.MB) * a.block, static_cast<int64_t>(a.W) * a.MB);
+  const int64_t want = (4 * static_cast<int64_t>(num_sms) + s.n - 1) / s.n;
+  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>({want, (most + 2 * TAB_NT - 1) / (2 * TAB_NT), 65535}));
+  kv_build_kernel<<<dim3(s.n, static_cast<unsigned>(chunks)), TAB_NT, 0, stream>>>(a, s, build);
+  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+}
+
+}  // namespace vbs
