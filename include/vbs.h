@@ -432,6 +432,59 @@ int kv_paged_status(vbs_pkv* pkv);
    caller's).  NULL is a no-op.  Returns VBS_OK. */
 int kv_paged_destroy(vbs_pkv* pkv);
 
+/* =============================================================================
+ * The paged cache in 8 bits.  The pages name the K/V cache, its paging and its cost;
+ * holding it in 8 bits, and the attention that reads it, have no pages' counterpart.
+ * ============================================================================= */
+
+/* 8-bit formats: two's complement integers, and float8 e4m3 (no infinities, largest 448) */
+enum { VBS_I8 = 0, VBS_E4M3 = 1 };
+
+typedef struct vbs_kv8 vbs_kv8;
+
+/*
+ * Hold the cache `pkv` (created with elem_bytes = 1) in 8 bits: every (block, layer, k/v,
+ * head) run of codes has one fp32 scale in scales[num_blocks][L][2][H] (device, caller-owned),
+ * a power of two between 2^-60 and 2^60; a value is code * scale.  From here on
+ * copy-on-write copies a block's scales with its slots.
+ *   q_heads  query heads of the attention (a multiple of H); max_q  the most query
+ *            tokens per row of one attention call (1..32)
+ * All work goes to pkv's stream; device-side errors go to kv_paged_status(pkv).
+ * The context must be destroyed before pkv.
+ * Errors: VBS_EINVAL (elem_bytes not 1, head_dim not a multiple of 16 up to 256, NULL
+ *   pointers, q_heads, max_q or format out of range), VBS_EALIGN (pool not 16-byte
+ *   aligned), VBS_ESTATE (pkv already has such a context), VBS_ENOMEM.  *ctx is NULL on error.
+ */
+int kv8_init(vbs_kv8** ctx, vbs_pkv* pkv, int format, float* scales, int q_heads, int max_q);
+/*
+ * Write n tokens' K and V rows into `layer`: token i's head h is at k + i * k_tok + h * k_head
+ * (elements of dtype VBS_BF16 or VBS_F32, head_dim contiguous; v likewise) and goes to slot
+ * slots[i] (int64 device, block * block_size + offset; -1 is skipped).  Tokens of one block stand
+ * next to each other in ascending order, as kv_paged_build and kv_paged_slots list
+ * them, and no other token of the call goes to that block.
+ * A run of tokens that starts a block sets its scale: the smallest power of two s with
+ * largest magnitude <= QMAX * s (QMAX 127 or 448).  A run that continues a block keeps
+ * the larger of that and the block's scale, and where it grows the codes before the run are
+ * rounded again to it.  Codes are rounded to nearest, ties to even.
+ * Infinities are held as +-QMAX of the finite values' scale and NaN as 0, with VBS_EINPUT
+ * in kv_paged_status(); magnitudes above QMAX * 2^60 are held at it.  A slot outside
+ * the pool is skipped, with VBS_EINVAL there.
+ * Errors: VBS_EINVAL (layer, n or dtype out of range, NULL pointers with n > 0), VBS_ECUDA.
+ */
+int kv8_append(vbs_kv8* ctx, int layer, const void* k, const void* v, int64_t k_tok, int64_t k_head, int64_t v_tok,
+               int64_t v_head, int dtype, int64_t n, const int64_t* slots);
+/*
+ * The values that slots hold (code * scale, exact in bf16): k_out, v_out [n][H][head_dim]
+ * bf16 (device, dense); zeros for slot -1.
+ * Errors: VBS_EINVAL (layer or n out of range, NULL pointers with n > 0), VBS_EALIGN (outputs not
+ *   16-byte aligned), VBS_ECUDA; a slot outside the pool reads as zeros, with VBS_EINVAL
+ *   in kv_paged_status().
+ */
+int kv8_read(vbs_kv8* ctx, int layer, int64_t n, const int64_t* slots, void* k_out, void* v_out);
+/* Free the context (synchronises the stream first; pkv and the scales stay).  NULL is a no-op.
+   Returns VBS_OK. */
+int kv8_destroy(vbs_kv8* ctx);
+
 /* Synchronise `stream` and return (then clear) the status word of the calls
    that have no context (kv_reorder's and bpd_verify's bounded waits,
    bs_expand_static's input checks).  VBS_ECUDA when the synchronisation or the

@@ -13,11 +13,12 @@ import os
 
 import torch
 
-__all__ = ["BeamSearch", "PagedKV", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
+__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
            "LP_GNMT", "LP_POWER", "ES_FALSE", "ES_TRUE", "ES_NEVER", "F32", "BF16", "BPD_EXACT", "BPD_TOPK",
            "BPD_DISTANCE", "gather_shard_partials"]
 
 F32, BF16 = 0, 1
+I8, E4M3 = 0, 1
 LP_GNMT, LP_POWER = 0, 1
 BPD_EXACT, BPD_TOPK, BPD_DISTANCE = 0, 1, 2
 ES_FALSE, ES_TRUE, ES_NEVER = 0, 1, 2
@@ -51,6 +52,10 @@ SIGNATURES = {
     "kv_paged_prefill": (_c_int, [_vp, _c_int]),
     "kv_paged_build": (_c_int, [_vp, _vp, _c_i64, _vp, _vp, _vp, _vp]),
     "kv_paged_slots": (_c_int, [_vp, _c_int, _vp, _vp, _c_i64, _vp, _vp, _vp, _vp]),
+    "kv8_init": (_c_int, [_pp, _vp, _c_int, _vp, _c_int, _c_int]),
+    "kv8_append": (_c_int, [_vp, _c_int, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_i64, _vp]),
+    "kv8_read": (_c_int, [_vp, _c_int, _c_i64, _vp, _vp, _vp]),
+    "kv8_destroy": (_c_int, [_vp]),
     "kv_paged_state": (_c_int, [_vp, _pp, _pp, _pp, _pp, _pp]),
     "kv_paged_prepare": (_c_int, [_vp, _c_int]),
     "kv_paged_reorder": (_c_int, [_vp, _vp, _c_int]),
@@ -528,6 +533,72 @@ class PagedKV:
             self.close()
         except Exception:
             pass
+
+
+class PagedKV8(PagedKV):
+    """A PagedKV held in 8 bits (torch.int8 or torch.float8_e4m3fn), with one power-of-two scale per
+    (block, layer, k/v, head) in `scales` [batch * blocks_per_sentence, L, 2, H] (fp32), and the
+    attention that reads it.
+
+    `heads` is the number of query heads (a multiple of H), `max_q` the most query tokens per row of one
+    attend() call (up to 32).  D is a multiple of 16 up to 256.
+    """
+
+    def __init__(self, batch: int, W: int, L: int, H: int, D: int, *, heads: int, blocks_per_sentence: int,
+                 max_blocks: int, block: int = 16, max_q: int = 1, dtype=torch.float8_e4m3fn, device="cuda",
+                 pool=None, scales=None):
+        self.ctx8 = _vp()
+        if dtype not in (torch.int8, torch.float8_e4m3fn):
+            raise ValueError(f"dtype must be int8 or float8_e4m3fn, got {dtype}")
+        NB = batch * blocks_per_sentence
+        if pool is not None and (pool.dtype != dtype or not pool.is_contiguous()
+                                 or pool.shape != (NB, L, 2, H, block, D)):
+            raise ValueError(f"pool must be a contiguous {dtype} [{NB}, {L}, 2, {H}, {block}, {D}] tensor")
+        super().__init__(batch, W, L, H, D, blocks_per_sentence=blocks_per_sentence, max_blocks=max_blocks,
+                         block=block, dtype=dtype, device=device, pool=pool)
+        if scales is None:
+            scales = torch.zeros(NB, L, 2, H, dtype=torch.float32, device=self.device)
+        if scales.shape != (NB, L, 2, H) or not scales.is_contiguous():
+            raise ValueError(f"scales must be a contiguous float32 [{NB}, {L}, 2, {H}] tensor")
+        self.scales, self.heads, self.max_q = scales, heads, max_q
+        _check(lib().kv8_init(ctypes.byref(self.ctx8), self.ctx, I8 if dtype == torch.int8 else E4M3,
+                              _dev_ptr(scales, "scales", torch.float32), heads, max_q), "kv8_init")
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
+        """Write k, v [N, H, D] (bfloat16 or float32, unit stride along D) at slots (int64 [N], -1: skipped).
+
+        Tokens of one block stand next to each other in ascending order, as build() and slot_map() list
+        them; a run that starts a block sets its scales, one that continues it can only raise them."""
+        N = slots.numel()
+        for name, t in (("k", k), ("v", v)):
+            if t.shape != (N, self.H, self.D) or (self.D > 1 and t.stride(2) != 1):
+                raise ValueError(f"{name} must be [{N}, {self.H}, {self.D}] with unit stride along D")
+        if k.dtype != v.dtype:
+            raise ValueError("k and v must have one dtype")
+        if slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous int64 [N] tensor")
+        args = (_dev_ptr(k, "k"), _dev_ptr(v, "v"), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                _dtype_code(k.dtype), N, _dev_ptr(slots, "slots", torch.int64))
+        with _StreamOrder(self._stream_obj, self.device, k, v, slots):
+            _check(lib().kv8_append(self.ctx8, layer, *args), "kv8_append")
+
+    def read(self, layer: int, slots: torch.Tensor):
+        """(k, v) bfloat16 [N, H, D]: the values that slots (int64 [N]) hold, exactly; zeros for -1."""
+        if slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous int64 [N] tensor")
+        sp = _dev_ptr(slots, "slots", torch.int64)
+        k = torch.empty(slots.numel(), self.H, self.D, dtype=torch.bfloat16, device=self.device)
+        v = torch.empty_like(k)
+        with _StreamOrder(self._stream_obj, self.device, slots, k, v):
+            _check(lib().kv8_read(self.ctx8, layer, slots.numel(), sp, _vp(k.data_ptr()), _vp(v.data_ptr())),
+                   "kv8_read")
+        return k, v
+
+    def close(self):
+        if getattr(self, "ctx8", None) is not None and self.ctx8.value:
+            lib().kv8_destroy(self.ctx8)
+            self.ctx8 = _vp()
+        super().close()
 
 
 def bpd_propose(logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:

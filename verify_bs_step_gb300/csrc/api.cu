@@ -458,6 +458,7 @@ VBS_EXPORT int kv_paged_init(vbs_pkv** out, const vbs_kv_desc* d, int batch, int
   a.L = d->layers;
   a.H = d->heads;
   a.slot_bytes = static_cast<int64_t>(d->head_dim) * d->elem_bytes;
+  c->elem_bytes = d->elem_bytes;
   a.block_bytes = static_cast<int64_t>(a.L) * 2 * a.H * block * a.slot_bytes;
   a.pool = static_cast<char*>(pool);
   c->stream = reinterpret_cast<cudaStream_t>(stream);

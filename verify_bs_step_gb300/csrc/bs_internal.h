@@ -24,6 +24,7 @@ struct PagedArgs {
   int32_t* top;                   // [B]
   int32_t* base;                  // [B] the sentence's prompt length when built from lengths, else 0:
                                   // t_valid and t_write count positions from it
+  float* scales;                  // [NB][L][2][H] of an 8-bit cache (copied with a page), else NULL
   int4* tasks;                    // [R]: sentence b's tasks in [b*W, (b+1)*W) (src block, dst block, filled slots, -)
   int task_cap;                   // R
   unsigned long long* cow_slots;  // filled slots copied, summed (x L*2*H runs)

@@ -40,6 +40,7 @@ struct vbs_pkv {
   cudaStream_t stream;
   int32_t* identity;
   int R;
+  int elem_bytes;
   void* dev_block;
   char* state;           // table .. base: one contiguous range of the allocation
   char* saved;           // its copy (kv_paged_save / kv_paged_restore)
