@@ -156,3 +156,21 @@ def test_build_on_another_stream_is_ordered_with_it():
     assert total.item() == 120 and (slots >= 0).all()
     assert kv.status() == 0
     kv.close()
+
+
+def test_views_outlive_their_cache():
+    """The views keep the library's memory: a cache that is closed or collected does not free it under them."""
+    import gc
+    kv = _cache(2, 1, 3, 3, 8)
+    kv.build(_i32([20, 3]))
+    views = kv.views()
+    kv.close()
+    del kv
+    gc.collect()
+    other = _cache(2, 1, 3, 3, 8)                 # would take the freed memory
+    other.build(_i32([0, 24]))
+    assert views[0].tolist() == [[0, 1, 2], [3, -1, -1]] and views[4].tolist() == [0, 2]
+    del views
+    gc.collect()
+    assert other.status() == 0
+    other.close()

@@ -157,10 +157,22 @@ def _dtype_code(dt) -> int:
     raise ValueError(f"logits dtype must be bfloat16 or float32, got {dt}")
 
 
-class _DeviceArray:
-    """Device memory of the library as an array that torch.as_tensor() takes without a copy."""
+class _Context:
+    """A context of the library, destroyed when its last holder lets go of it."""
 
-    def __init__(self, ptr: int, shape, typestr: str):
+    def __init__(self, ptr: _vp, destroy):
+        self.ptr, self.destroy = ptr, destroy
+
+    def __del__(self):
+        self.destroy(self.ptr)
+
+
+class _DeviceArray:
+    """Device memory of a context as an array that torch.as_tensor() takes without a copy; the tensor
+    holds it, and it holds the context."""
+
+    def __init__(self, context: _Context, ptr: int, shape, typestr: str):
+        self.context = context
         self.__cuda_array_interface__ = {"data": (ptr, False), "shape": tuple(shape), "typestr": typestr,
                                          "strides": None, "version": 2}
 
@@ -426,10 +438,11 @@ class PagedKV:
         _check(lib().kv_paged_init(ctypes.byref(ctx), ctypes.byref(desc), batch, W, blocks_per_sentence, block,
                                    max_blocks, _dev_ptr(pool, "pool"), self.stream), "kv_paged_init")
         self.ctx = ctx
+        self._context = _Context(ctx, lib().kv_paged_destroy)
         ptr = [_vp() for _ in range(5)]
         _check(lib().kv_paged_state(self.ctx, *[ctypes.byref(p) for p in ptr]), "kv_paged_state")
         shapes = ((self.R, max_blocks), (self.R,), (batch * self.S,), (batch * self.S,), (batch,))
-        self._views = tuple(torch.as_tensor(_DeviceArray(p.value, s, "<i4"), device=self.device)
+        self._views = tuple(torch.as_tensor(_DeviceArray(self._context, p.value, s, "<i4"), device=self.device)
                             for p, s in zip(ptr, shapes))
 
     def prefill(self, P: int):
@@ -477,8 +490,8 @@ class PagedKV:
         return (out[0].numel(),) + tuple(_vp(t.data_ptr()) for t in out)
 
     def views(self):
-        """The allocator's state as int32 tensors on the library's own memory (no copy; valid until close(),
-        not to be written): table [R, max_blocks], blocks per row [R], reference counts, free stacks
+        """The allocator's state as int32 tensors on the library's own memory (no copy; they keep it
+        allocated and are not to be written): table [R, max_blocks], blocks per row [R], reference counts, free stacks
         [batch * blocks_per_sentence] and their heights [batch]."""
         return self._views
 
@@ -524,9 +537,9 @@ class PagedKV:
         return lib().kv_paged_status(self.ctx)
 
     def close(self):
-        if getattr(self, "ctx", None) is not None and self.ctx.value:
-            lib().kv_paged_destroy(self.ctx)
-            self.ctx = _vp()
+        # the library's memory goes with the last of this object and the views() still held
+        self._views = self._context = None
+        self.ctx = _vp()
 
     def __del__(self):
         try:
