@@ -481,9 +481,71 @@ int kv8_append(vbs_kv8* ctx, int layer, const void* k, const void* v, int64_t k_
  *   in kv_paged_status().
  */
 int kv8_read(vbs_kv8* ctx, int layer, int64_t n, const int64_t* slots, void* k_out, void* v_out);
+/*
+ * Prepare the attention of one step: ctx_len[R] (device int32) is the number of cached
+ * positions of each row, the step's n_q new tokens among them (1 <= n_q <= max_q).  Reads the
+ * block tables: call it again whenever they or the lengths have changed (once a step; the
+ * step's layers share it).
+ * Errors: VBS_EINVAL (NULL pointers, n_q out of range), VBS_ECUDA; a length below 0 or beyond
+ *   what the row's table covers is held to that range, with VBS_EINVAL in kv_paged_status().
+ */
+int kv8_plan(vbs_kv8* ctx, const int32_t* ctx_len, int n_q);
+/*
+ * Attention of the planned step over `layer`: for query token i (0..n_q-1) of row r and
+ * query head h, which reads K/V head h / (q_heads / H),
+ *   out = sum_p softmax_p(scale * q . k_p) v_p  over positions p < ctx_len[r] - n_q + 1 + i
+ * (the cached positions up to the token's own).  A token that sees no position gives zeros.
+ * q and out are bf16 (device); token i of row r, head h is at q + r * q_row + i * q_tok +
+ * h * q_head (elements, head_dim contiguous), out likewise.  Blocks that several rows of a sentence
+ * share are read once.  Scores, softmax statistics and sums are fp32; q is scaled
+ * by a power of two per row and held in fp16, the softmax weights are rounded to fp16.
+ * Errors: VBS_EINVAL (layer out of range, NULL pointers, scale not finite), VBS_ESTATE (no
+ *   kv8_plan yet), VBS_ECUDA.
+ */
+int kv8_attention(vbs_kv8* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,
+                  void* out, int64_t o_row, int64_t o_tok, int64_t o_head);
 /* Free the context (synchronises the stream first; pkv and the scales stay).  NULL is a no-op.
    Returns VBS_OK. */
 int kv8_destroy(vbs_kv8* ctx);
+
+/* =============================================================================
+ * Cross attention to an encoder's states.  The pages name encoder-decoder translation as a
+ * use of the beam step; the operator itself has no pages' counterpart.
+ * ============================================================================= */
+
+typedef struct vbs_xattn vbs_xattn;
+
+/*
+ * Create a context for `batch` sentences of W decoder rows, q_heads query and kv_heads K/V heads
+ * of head_dim (a multiple of 8 up to 256), at most max_q query tokens per row and max_len
+ * encoder positions; allocates the workspace of the split over a long source.  All work goes to
+ * `stream`.
+ * Errors: VBS_EINVAL (a size out of range, W outside 1..16, q_heads not a multiple of kv_heads,
+ *   batch * W * q_heads * max_q >= 2^31), VBS_ENOMEM, VBS_ECUDA.  *ctx is NULL on error.
+ */
+int xattn_init(vbs_xattn** ctx, int batch, int W, int q_heads, int kv_heads, int head_dim, int max_q, int max_len,
+               vbs_stream_t stream);
+/*
+ * out = sum_s softmax_s(scale * q . k_s) v_s over the positions s < enc_len[b] (device int32
+ * [batch], 0..len) of the row's sentence b = r / W, for each of the n_q tokens of R = batch * W rows
+ * and each query head h, which reads K/V head h / (q_heads / kv_heads).  A sentence of length 0
+ * gives zeros.  All bf16 (device), head_dim contiguous: q at q + r * q_row + i * q_tok +
+ * h * q_head, k at k + b * k_sent + s * k_pos + h * k_head (elements, s < len), v and out
+ * likewise.  K and V at positions >= enc_len[b] are not used, whatever they hold.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded before the product
+ * with V.
+ * Errors: VBS_EINVAL (n_q, len out of range, NULL pointers, scale not finite), VBS_ECUDA; a
+ *   length outside 0..len is held to that range, with VBS_EINVAL in xattn_status().
+ */
+int xattn_run(vbs_xattn* ctx, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, int n_q, const void* k,
+              int64_t k_sent, int64_t k_pos, int64_t k_head, const void* v, int64_t v_sent, int64_t v_pos,
+              int64_t v_head, int len, const int32_t* enc_len, float scale, void* out, int64_t o_row, int64_t o_tok,
+              int64_t o_head);
+/* Synchronise the stream and return (then clear) the device status word.  VBS_EINVAL for NULL,
+   VBS_ECUDA when the synchronisation or the read fails. */
+int xattn_status(vbs_xattn* ctx);
+/* Free the context (synchronises its stream first).  NULL is a no-op.  Returns VBS_OK. */
+int xattn_destroy(vbs_xattn* ctx);
 
 /* Synchronise `stream` and return (then clear) the status word of the calls
    that have no context (kv_reorder's and bpd_verify's bounded waits,

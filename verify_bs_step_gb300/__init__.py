@@ -13,7 +13,7 @@ import os
 
 import torch
 
-__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
+__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "CrossAttention", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
            "LP_GNMT", "LP_POWER", "ES_FALSE", "ES_TRUE", "ES_NEVER", "F32", "BF16", "BPD_EXACT", "BPD_TOPK",
            "BPD_DISTANCE", "gather_shard_partials"]
 
@@ -55,7 +55,14 @@ SIGNATURES = {
     "kv8_init": (_c_int, [_pp, _vp, _c_int, _vp, _c_int, _c_int]),
     "kv8_append": (_c_int, [_vp, _c_int, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_i64, _vp]),
     "kv8_read": (_c_int, [_vp, _c_int, _c_i64, _vp, _vp, _vp]),
+    "kv8_plan": (_c_int, [_vp, _vp, _c_int]),
+    "kv8_attention": (_c_int, [_vp, _c_int, _vp, _c_i64, _c_i64, _c_i64, _c_f, _vp, _c_i64, _c_i64, _c_i64]),
     "kv8_destroy": (_c_int, [_vp]),
+    "xattn_init": (_c_int, [_pp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "xattn_run": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _c_i64,
+                           _c_i64, _c_int, _vp, _c_f, _vp, _c_i64, _c_i64, _c_i64]),
+    "xattn_status": (_c_int, [_vp]),
+    "xattn_destroy": (_c_int, [_vp]),
     "kv_paged_state": (_c_int, [_vp, _pp, _pp, _pp, _pp, _pp]),
     "kv_paged_prepare": (_c_int, [_vp, _c_int]),
     "kv_paged_reorder": (_c_int, [_vp, _vp, _c_int]),
@@ -607,11 +614,100 @@ class PagedKV8(PagedKV):
                    "kv8_read")
         return k, v
 
+    def plan(self, ctx_len: torch.Tensor, n_q: int = 1):
+        """Prepare a step's attention: ctx_len (int32 [R] on the device) is each row's number of cached
+        positions, its n_q new tokens among them.  Call it whenever the tables or lengths have changed."""
+        if ctx_len.shape != (self.R,) or not ctx_len.is_contiguous():
+            raise ValueError(f"ctx_len must be a contiguous int32 [{self.R}] tensor")
+        cp = _dev_ptr(ctx_len, "ctx_len", torch.int32)
+        with _StreamOrder(self._stream_obj, self.device, ctx_len):
+            _check(lib().kv8_plan(self.ctx8, cp, n_q), "kv8_plan")
+        self._n_q = n_q
+
+    def attend(self, layer: int, q: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None):
+        """softmax(scale q k^T) v of q [R, n_q, heads, D] (bfloat16, unit stride along D) over each row's
+        cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
+        shape = (self.R, getattr(self, "_n_q", q.shape[1] if q.dim() > 1 else 0), self.heads, self.D)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        _rows4(q, "q", shape)
+        _rows4(out, "out", shape)
+        with _StreamOrder(self._stream_obj, self.device, q, out):
+            _check(lib().kv8_attention(self.ctx8, layer, _vp(q.data_ptr()), q.stride(0), q.stride(1), q.stride(2),
+                                       self.D ** -0.5 if scale is None else scale, _vp(out.data_ptr()),
+                                       out.stride(0), out.stride(1), out.stride(2)), "kv8_attention")
+        return out
+
     def close(self):
         if getattr(self, "ctx8", None) is not None and self.ctx8.value:
             lib().kv8_destroy(self.ctx8)
             self.ctx8 = _vp()
         super().close()
+
+
+def _rows4(t: torch.Tensor, name: str, shape):
+    if t.shape != shape or t.stride(3) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit stride along the last axis, got {list(t.shape)}")
+    _dev_ptr(t, name, torch.bfloat16)
+
+
+class CrossAttention:
+    """Attention of decoder rows to their sentence's encoder states (libvbs xattn_*).
+
+    `batch` sentences of W rows each read one set of keys and values; `heads` query heads share
+    `kv_heads`.  Work goes on the stream that is current at construction.
+    """
+
+    def __init__(self, batch: int, W: int, heads: int, D: int, *, kv_heads: int | None = None, max_q: int = 1,
+                 max_len: int = 1024, device="cuda"):
+        self.ctx = _vp()
+        self.batch, self.W, self.R, self.heads, self.D = batch, W, batch * W, heads, D
+        self.kv_heads = heads if kv_heads is None else kv_heads
+        self.max_q, self.max_len = max_q, max_len
+        self.device = torch.device(device)
+        self._stream_obj = torch.cuda.current_stream(self.device)
+        _check(lib().xattn_init(ctypes.byref(self.ctx), batch, W, heads, self.kv_heads, D, max_q, max_len,
+                                _vp(self._stream_obj.cuda_stream)), "xattn_init")
+
+    def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, enc_len: torch.Tensor,
+               scale: float | None = None, out: torch.Tensor | None = None):
+        """softmax(scale q k^T) v: q [R, n_q, heads, D], k and v [batch, S, kv_heads, D] (bfloat16, unit stride
+        along D), over positions below enc_len (int32 [batch]) of the row's sentence; zeros where that is 0.
+        scale defaults to D ** -0.5."""
+        n_q = q.shape[1] if q.dim() == 4 else 0
+        S = k.shape[1] if k.dim() == 4 else 0
+        shape = (self.R, n_q, self.heads, self.D)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        _rows4(q, "q", shape)
+        _rows4(out, "out", shape)
+        _rows4(k, "k", (self.batch, S, self.kv_heads, self.D))
+        _rows4(v, "v", (self.batch, S, self.kv_heads, self.D))
+        if enc_len.shape != (self.batch,) or not enc_len.is_contiguous():
+            raise ValueError(f"enc_len must be a contiguous int32 [{self.batch}] tensor")
+        lp = _dev_ptr(enc_len, "enc_len", torch.int32)
+        with _StreamOrder(self._stream_obj, self.device, q, k, v, enc_len, out):
+            _check(lib().xattn_run(self.ctx, _vp(q.data_ptr()), q.stride(0), q.stride(1), q.stride(2), n_q,
+                                   _vp(k.data_ptr()), k.stride(0), k.stride(1), k.stride(2),
+                                   _vp(v.data_ptr()), v.stride(0), v.stride(1), v.stride(2), S, lp,
+                                   self.D ** -0.5 if scale is None else scale,
+                                   _vp(out.data_ptr()), out.stride(0), out.stride(1), out.stride(2)), "xattn_run")
+        return out
+
+    def status(self) -> int:
+        """Synchronise and return the device status word (0 = OK)."""
+        return lib().xattn_status(self.ctx)
+
+    def close(self):
+        if getattr(self, "ctx", None) is not None and self.ctx.value:
+            lib().xattn_destroy(self.ctx)
+            self.ctx = _vp()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def bpd_propose(logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
