@@ -1,144 +1,135 @@
-// Attention over the 8-bit paged cache and over an encoder's states (sm_103a).
+// The plan of a step's attention over the 8-bit paged cache (sm_103a).
 //
-//   o = sum_p softmax_p(scale q . k_p) v_p   over the positions p that a query sees
-//
-// with the running maximum m and sum l of a one-pass softmax, in fp32: a chunk of scores with
-// maximum m' moves l and o to the new reference by 2^(m - max(m, m')).  A query that sees nothing
-// gives zeros.
-//
-// One warp per (row, query token, query head): a lane scores one of 32 positions at a time, then the
-// lanes share the head's dims for the weighted sum of the values.
-
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
+// The plan turns the block tables into each sentence's list of distinct pages: a page that several
+// beams share stands in it once, with the beams that see it, so that attention reads it once.  It is a
+// pass over R x pages table entries, made once a step and shared by the layers.
 
 #include "attn.h"
+#include "attn_split.cuh"
 #include "common.cuh"
 
 namespace vbs {
 
-constexpr int AT_NT = 128;
-constexpr int AT_DMAX = 256;
+constexpr int PLAN_NT = 256;
 
-template <int FMT> struct Paged8 {
-  PagedArgs a;
-  Kv8Geom g;
-  const int32_t* seen;            // [R] cached positions of each row
-  int h;
-  int row;
-  __device__ int count(int r) const { return seen[r]; }
-  __device__ float load(int kv, int p, int d) const {
-    const int64_t page = a.table[static_cast<int64_t>(row) * a.MB + p / g.block];
-    const int64_t run = g.run(page, kv, h);
-    const uint8_t c = reinterpret_cast<const uint8_t*>(g.pool)[(run * g.block + p % g.block) * g.D + d];
-    if (FMT == VBS_I8) return static_cast<float>(static_cast<int8_t>(c)) * g.scales[run];
-    __nv_fp8_e4m3 f;
-    f.__x = c;
-    return static_cast<float>(f) * g.scales[run];
-  }
-};
-
-struct EncRows {
-  EncKV e;
-  int h, row;
-  __device__ int count(int r) const {
-    const int n = e.len[r / e.W];
-    if (n >= 0 && n <= e.S) return n;
-    set_status(e.status, VBS_EINVAL);
-    return n < 0 ? 0 : e.S;
-  }
-  __device__ float load(int kv, int p, int d) const {
-    const int64_t b = row / e.W;
-    const uint16_t x = kv ? e.v[b * e.v_sent + p * e.v_pos + h * e.v_head + d]
-                          : e.k[b * e.k_sent + p * e.k_pos + h * e.k_head + d];
-    return __uint_as_float(static_cast<u32>(x) << 16);
-  }
-};
-
-template <class KV>
-__global__ void __launch_bounds__(AT_NT) attn_warp_kernel(KV kv, const QO io, int64_t items, int H, int D, bool causal) {
-  __shared__ float qs[AT_NT / 32][AT_DMAX];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (AT_NT / 32) + w;
-  if (item >= items) return;
-  const int hq = static_cast<int>(item % io.Hq);
-  const int i = static_cast<int>(item / io.Hq % io.n_q);
-  const int row = static_cast<int>(item / io.Hq / io.n_q);
-  kv.h = hq / (io.Hq / H);
-  kv.row = row;
-  const uint16_t* q = io.q + row * io.q_row + i * io.q_tok + hq * io.q_head;
-  for (int d = lane; d < D; d += 32) qs[w][d] = __uint_as_float(static_cast<u32>(q[d]) << 16) * io.scale * LOG2E_F;
-  __syncwarp();
-  const int T = kv.count(row) - (causal ? io.n_q - 1 - i : 0);
-  float m = -INFINITY, l = 0.f, o[AT_DMAX / 32];
-#pragma unroll
-  for (int u = 0; u < AT_DMAX / 32; ++u) o[u] = 0.f;
-  for (int p0 = 0; p0 < T; p0 += 32) {
-    const int p = p0 + lane;
-    float s = -INFINITY;
-    if (p < T) {
-      s = 0.f;
-      for (int d = 0; d < D; ++d) s += qs[w][d] * kv.load(0, p, d);
-    }
-    float mx = s;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, k));
-    const float mn = fmaxf(m, mx);
-    const float corr = ex2(m - mn);
-    const float pr = ex2(s - mn);
-    float sum = pr;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(FULL, sum, k);
-    l = l * corr + sum;
-    m = mn;
-#pragma unroll
-    for (int u = 0; u < AT_DMAX / 32; ++u) o[u] *= corr;
-    const int n = min(32, T - p0);
-    for (int j = 0; j < n; ++j) {
-      const float pj = __shfl_sync(FULL, pr, j);
-#pragma unroll
-      for (int u = 0; u < AT_DMAX / 32; ++u)
-        if (u * 32 + lane < D) o[u] += pj * kv.load(1, p0 + j, u * 32 + lane);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-  uint16_t* out = io.o + row * io.o_row + i * io.o_tok + hq * io.o_head;
-#pragma unroll
-  for (int u = 0; u < AT_DMAX / 32; ++u)
-    if (u * 32 + lane < D) out[u * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(o[u] * inv));
-}
-
-// Each row's cached positions, held to what its table covers.
-__global__ void kv8_plan_kernel(const PagedArgs a, const int32_t* ctx, int32_t* seen, int R) {
-  const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= R) return;
+// A row's cached positions, held to what its table covers.
+__device__ __forceinline__ int held_len(const PagedArgs& a, const int32_t* ctx, int r) {
   const int n = ctx[r];
   const int64_t most = static_cast<int64_t>(a.nblk[r]) * a.block;
   if (n < 0 || n > most) set_status(a.status, VBS_EINVAL);
-  seen[r] = n < 0 ? 0 : static_cast<int>(n < most ? n : most);
+  return n < 0 ? 0 : static_cast<int>(n < most ? n : most);
 }
 
-int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, int32_t* seen, cudaStream_t s) {
-  const int R = a.B * a.W;
-  kv8_plan_kernel<<<(R + 127) / 128, 128, 0, s>>>(a, ctx, seen, R);
+// A CTA a sentence; a thread looks at one table column of its W rows at a time.
+__global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, const int32_t* ctx, const Kv8Plan p) {
+  __shared__ int seen[WMAX];
+  __shared__ int sums[PLAN_NT / 32];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, W = a.W;
+  if (tid < W) {
+    seen[tid] = held_len(a, ctx, b * W + tid);
+    p.seen[b * W + tid] = seen[tid];
+  }
+  __syncthreads();
+  int most = 0;
+  for (int w = 0; w < W; ++w) most = max(most, seen[w]);
+  const int cols = (most + a.block - 1) / a.block;
+  const int32_t* tab = a.table + static_cast<int64_t>(b) * W * a.MB;
+  int4* list = p.list + static_cast<int64_t>(b) * a.S;
+  int carry = 0;
+  for (int j0 = 0; j0 < cols; j0 += PLAN_NT) {
+    const int j = j0 + tid;
+    int id[WMAX];
+    u32 lead = 0;                                   // the beams that name a page first
+    if (j < cols)
+      for (int w = 0; w < W; ++w) {
+        id[w] = j * a.block < seen[w] ? tab[static_cast<int64_t>(w) * a.MB + j] : -1;
+        if (id[w] < 0) continue;
+        if (id[w] < b * a.S || id[w] >= (b + 1) * a.S) {   // not a page of this sentence
+          set_status(a.status, VBS_EINVAL);
+          id[w] = -1;
+          continue;
+        }
+        bool first = true;
+        for (int x = 0; x < w; ++x) first = first && id[x] != id[w];
+        if (first) lead |= 1u << w;
+      }
+    const int n = __popc(lead);
+    int at = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(FULL, at, d);
+      if (lane >= d) at += y;
+    }
+    if (lane == 31) sums[wid] = at;
+    __syncthreads();
+    int all = 0;
+    at += carry - n;
+    for (int w = 0; w < PLAN_NT / 32; ++w) {
+      if (w < wid) at += sums[w];
+      all += sums[w];
+    }
+    for (int w = 0; w < W; ++w) {
+      if (!(lead >> w & 1u)) continue;
+      u32 rows = 0;
+      int to = 0;
+      for (int x = w; x < W; ++x)
+        if (id[x] == id[w]) {
+          rows |= 1u << x;
+          to = max(to, seen[x]);
+        }
+      if (at < a.S) list[at] = make_int4(id[w], j * a.block, static_cast<int>(rows), min(a.block, to - j * a.block));
+      else set_status(a.status, VBS_EINVAL);        // a page in two columns: not a table of this library
+      ++at;
+    }
+    carry += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    // a sentence with nothing to see has one page of no positions: its rows get their zeros from it
+    if (carry == 0) list[0] = make_int4(0, 0, 0, 0);
+    p.n_pages[b] = max(1, min(carry, a.S));
+  }
+}
+
+// One row a sentence: the list is the table's row; CTA (b, c) copies every c-th chunk of it.
+__global__ void __launch_bounds__(PLAN_NT) kv8_plan_rows_kernel(const PagedArgs a, const int32_t* ctx, const Kv8Plan p) {
+  const int b = blockIdx.x;
+  const int seen = held_len(a, ctx, b);
+  const int cols = (seen + a.block - 1) / a.block;
+  int4* list = p.list + static_cast<int64_t>(b) * a.S;
+  for (int j = blockIdx.y * PLAN_NT + threadIdx.x; j < min(cols, a.S); j += gridDim.y * PLAN_NT) {
+    const int id = a.table[static_cast<int64_t>(b) * a.MB + j];
+    const bool ok = id >= b * a.S && id < (b + 1) * a.S;
+    if (!ok) set_status(a.status, VBS_EINVAL);
+    list[j] = make_int4(ok ? id : 0, j * a.block, ok ? 1 : 0, ok ? min(a.block, seen - j * a.block) : 0);
+  }
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (cols == 0) list[0] = make_int4(0, 0, 0, 0);
+    p.n_pages[b] = max(1, min(cols, a.S));
+    p.seen[b] = seen;
+  }
+}
+
+int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, const Kv8Plan& p, cudaStream_t s) {
+  if (a.W == 1) {
+    const int chunks = std::min((std::min(a.MB, a.S) + PLAN_NT - 1) / PLAN_NT, 64);
+    kv8_plan_rows_kernel<<<dim3(a.B, chunks), PLAN_NT, 0, s>>>(a, ctx, p);
+  } else {
+    kv8_plan_kernel<<<a.B, PLAN_NT, 0, s>>>(a, ctx, p);
+  }
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
-int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const int32_t* seen, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(a.B) * a.W * io.n_q * io.Hq;
-  const unsigned grid = static_cast<unsigned>((items + AT_NT / 32 - 1) / (AT_NT / 32));
-  if (g.fmt == VBS_I8)
-    attn_warp_kernel<<<grid, AT_NT, 0, s>>>(Paged8<VBS_I8>{a, g, seen, 0, 0}, io, items, g.H, g.D, true);
-  else
-    attn_warp_kernel<<<grid, AT_NT, 0, s>>>(Paged8<VBS_E4M3>{a, g, seen, 0, 0}, io, items, g.H, g.D, true);
-  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+int64_t attn_part_floats(int D, int num_sms) { return split_part_floats(D, num_sms); }
+
+int64_t attn_segments(int B, int W, int H, int D, int Hq, int n_q) {
+  return static_cast<int64_t>(B) * H * split_chunks(W * n_q * (Hq / H), D);
 }
 
-int launch_xattn(const EncKV& e, const QO& io, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(e.B) * e.W * io.n_q * io.Hq;
-  const unsigned grid = static_cast<unsigned>((items + AT_NT / 32 - 1) / (AT_NT / 32));
-  attn_warp_kernel<<<grid, AT_NT, 0, s>>>(EncRows{e, 0, 0}, io, items, e.H, e.D, false);
-  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
+                         int* arrived, int num_sms, cudaStream_t s) {
+  return g.fmt == VBS_I8 ? launch_kv8_attention_i8(a, g, io, p, part, arrived, num_sms, s)
+                         : launch_kv8_attention_e4m3(a, g, io, p, part, arrived, num_sms, s);
 }
 
 }  // namespace vbs

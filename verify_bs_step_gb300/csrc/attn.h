@@ -28,8 +28,25 @@ struct EncKV {
   int* status;
 };
 
-int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, int32_t* seen, cudaStream_t s);
-int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const int32_t* seen, cudaStream_t s);
-int launch_xattn(const EncKV& kv, const QO& io, cudaStream_t s);
+// A step over the paged cache, from the block tables: each sentence's distinct pages
+// (page, first position, the beams that see it, positions), their number, and the rows' lengths.
+struct Kv8Plan {
+  int4* list;                     // [B][S]
+  int* n_pages;                   // [B]
+  int* seen;                      // [R]
+};
+
+int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, const Kv8Plan& p, cudaStream_t s);
+
+// Partials of the split: workspace of split_part_floats(D) floats, and one zeroed counter per segment.
+int64_t attn_part_floats(int D, int num_sms);
+int64_t attn_segments(int B, int W, int H, int D, int Hq, int n_q);
+int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
+                         int* arrived, int num_sms, cudaStream_t s);
+int launch_kv8_attention_i8(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
+                            int* arrived, int num_sms, cudaStream_t s);
+int launch_kv8_attention_e4m3(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
+                              int* arrived, int num_sms, cudaStream_t s);
+int launch_xattn(const EncKV& kv, const QO& io, float* part, int* arrived, int num_sms, cudaStream_t s);
 
 }  // namespace vbs

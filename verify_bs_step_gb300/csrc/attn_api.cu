@@ -16,7 +16,9 @@ struct vbs_kv8 {
   vbs::Kv8Geom g;                 // layer is set per call
   int q_heads, max_q;
   int n_q;                        // of the last plan, 0: none yet
-  int32_t* seen;                  // [R]
+  vbs::Kv8Plan plan;
+  float* part;                    // partials of rows split over CTAs, and their arrival counters
+  int* arrived;
   void* dev_block;
 };
 
@@ -24,6 +26,8 @@ struct vbs_xattn {
   vbs::EncKV e;                   // the tensors are set per call
   cudaStream_t stream;
   int q_heads, max_q, max_len;
+  float* part;
+  int* arrived;
   void* dev_block;
 };
 
@@ -53,7 +57,11 @@ VBS_EXPORT int kv8_init(vbs_kv8** out, vbs_pkv* kv, int format, float* scales, i
   g.status = a.status;
   vbs::Carver cv;
   for (int pass = 0; pass < 2; ++pass) {
-    c->seen = cv.take<int32_t>(kv->R);
+    c->plan.list = cv.take<int4>(g.NB);
+    c->plan.n_pages = cv.take<int>(a.B);
+    c->plan.seen = cv.take<int>(kv->R);
+    c->part = cv.take<float>(vbs::attn_part_floats(g.D, num_sms()));
+    c->arrived = cv.take<int>(vbs::attn_segments(a.B, a.W, g.H, g.D, q_heads, max_q));
     if (pass == 0) {
       if (cudaMalloc(&c->dev_block, cv.off) != cudaSuccess) {
         cudaGetLastError();
@@ -63,6 +71,11 @@ VBS_EXPORT int kv8_init(vbs_kv8** out, vbs_pkv* kv, int format, float* scales, i
       cv = vbs::Carver{};
       cv.base = static_cast<char*>(c->dev_block);
     }
+  }
+  if (cudaMemsetAsync(c->dev_block, 0, cv.off, kv->stream) != cudaSuccess) {
+    cudaFree(c->dev_block);
+    delete c;
+    return VBS_ECUDA;
   }
   kv->a.scales = scales;          // copy-on-write carries a page's scales along
   *out = c;
@@ -90,7 +103,7 @@ VBS_EXPORT int kv8_read(vbs_kv8* c, int layer, int64_t n, const int64_t* slots, 
 
 VBS_EXPORT int kv8_plan(vbs_kv8* c, const int32_t* ctx_len, int n_q) {
   if (!c || !ctx_len || n_q < 1 || n_q > c->max_q) return VBS_EINVAL;
-  const int st = vbs::launch_kv8_plan(c->kv->a, ctx_len, c->seen, c->kv->stream);
+  const int st = vbs::launch_kv8_plan(c->kv->a, ctx_len, c->plan, c->kv->stream);
   c->n_q = st == VBS_OK ? n_q : 0;
   return st;
 }
@@ -103,7 +116,7 @@ VBS_EXPORT int kv8_attention(vbs_kv8* c, int layer, const void* q, int64_t q_row
                    o_head, c->n_q, c->q_heads, scale};
   vbs::Kv8Geom g = c->g;
   g.layer = layer;
-  return vbs::launch_kv8_attention(c->kv->a, g, io, c->seen, c->kv->stream);
+  return vbs::launch_kv8_attention(c->kv->a, g, io, c->plan, c->part, c->arrived, num_sms(), c->kv->stream);
 }
 
 VBS_EXPORT int kv8_destroy(vbs_kv8* c) {
@@ -141,6 +154,8 @@ VBS_EXPORT int xattn_init(vbs_xattn** out, int batch, int W, int q_heads, int kv
   vbs::Carver cv;
   for (int pass = 0; pass < 2; ++pass) {
     e.status = cv.take<int>(1);
+    c->part = cv.take<float>(vbs::attn_part_floats(head_dim, num_sms()));
+    c->arrived = cv.take<int>(vbs::attn_segments(batch, W, kv_heads, head_dim, q_heads, max_q));
     if (pass == 0) {
       if (cudaMalloc(&c->dev_block, cv.off) != cudaSuccess) {
         cudaGetLastError();
@@ -179,7 +194,7 @@ VBS_EXPORT int xattn_run(vbs_xattn* c, const void* q, int64_t q_row, int64_t q_t
   e.v_head = v_head;
   e.len = enc_len;
   e.S = len;
-  return vbs::launch_xattn(e, io, c->stream);
+  return vbs::launch_xattn(e, io, c->part, c->arrived, num_sms(), c->stream);
 }
 
 VBS_EXPORT int xattn_status(vbs_xattn* c) {

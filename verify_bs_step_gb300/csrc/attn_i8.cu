@@ -1,0 +1,13 @@
+// Attention over a cache of 8-bit integers: the split kernel's instances.
+
+#include "attn_split.cuh"
+
+namespace vbs {
+
+int launch_kv8_attention_i8(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
+                         int* arrived, int num_sms, cudaStream_t s) {
+  const PagedSrc<VBS_I8> src{g, p.list, p.n_pages, p.seen, a.S, (g.block + 15) / 16};
+  return launch_split<PagedSrc<VBS_I8>, true>(src, io, split_args(io, a.B, a.W, g.H, g.D, part, arrived), num_sms, s);
+}
+
+}  // namespace vbs

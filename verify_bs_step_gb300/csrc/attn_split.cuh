@@ -1,0 +1,721 @@
+// Attention of a few query rows over many cached positions: the split kernel (sm_103a).
+//
+// A segment is one sentence's K/V head with up to 16 MT of the query rows that read it (the W beams x
+// n_q tokens x q_heads / kv_heads rows that share it are numbered beam first).  Positions come in units
+// of at most 16.  All segments' units stand in one line, sentence by sentence; every CTA of one
+// resident wave takes an equal share of it, whatever the lengths, and its four warps take every fourth
+// unit.  A segment inside one share is written straight out; one that crosses shares leaves
+// (m, l, o) partials, and the CTA that arrives last joins them in order, so equal calls give equal bits.
+//
+// A warp holds 16 MT rows x head_dim of o in registers.  Units come through a ring of cp.async stages of
+// its own (no barrier between warps), stored with a XOR of 16-byte chunks so that both reads below
+// meet no bank twice:
+//   scores   S = Q K^T by mma.m16n8k16: a lane takes 16 bytes of a position's row, and the order of dims
+//            inside the contraction is whatever that gives (Q is laid out the same way);
+//   values   O += P V by mma.m16n8k16: a lane takes 16 bytes of four positions, pairs of positions are put
+//            side by side with byte permutes, and the order of the output dims is undone at the end.
+// What bounds it is the K/V stream; the mma's rate only matters where many rows share a K/V head.
+
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace vbs {
+
+constexpr int SP_WARPS = 4;
+constexpr int SP_NT = 32 * SP_WARPS;
+constexpr int SP_MIN = 4 * SP_WARPS;     // units a CTA takes at least: every warp's ring once
+
+// What the kernel needs to know of the split.
+struct SplitArgs {
+  int B, W, H, D;
+  int G;                          // query heads per K/V head
+  int M;                          // query rows per K/V head: W * n_q * G
+  int MC;                         // chunks of 16 MT of them
+  float* part;                    // [grid][2][16 MT][DP + 2]: o, m, l of a segment's piece
+  int* arrived;                   // [B * H * MC], zero between calls
+  bool out8;                      // outputs may be stored 8 bytes at a time
+};
+
+__device__ __forceinline__ void cp_async16(u32 dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(u32 a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds8(u32 a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+
+template <bool BF> __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, u32 b0, u32 b1) {
+  if (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// Four codes to two pairs of fp16 (exact).
+template <int FMT> __device__ __forceinline__ void codes4(u32 w, u32& lo, u32& hi) {
+  if (FMT == VBS_I8) {
+    // byte b + 128 under an exponent of 2^10: 1024 + 128 + b, less 1152
+    w ^= 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    u32 a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+    lo = *reinterpret_cast<u32*>(&x);
+    hi = *reinterpret_cast<u32*>(&y);
+  } else {
+    const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
+    const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+    lo = static_cast<u32>(x.x) | (static_cast<u32>(x.y) << 16);
+    hi = static_cast<u32>(y.x) | (static_cast<u32>(y.y) << 16);
+  }
+}
+
+__device__ __forceinline__ u32 pack_f16(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<u32*>(&h);
+}
+__device__ __forceinline__ u32 pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<u32*>(&h);
+}
+
+// What a unit's consumer needs of it.
+struct UnitHead {
+  int pos;                        // its first position
+  u32 rows;                       // the beams that see it
+  float ks, ve;                   // K's scale; log2 of V's scale
+};
+
+// ---------------------------------------------------------------------------------------
+// sources
+// ---------------------------------------------------------------------------------------
+
+// The 8-bit paged cache: a unit is up to 16 positions of one page of the plan's list.
+template <int FMT> struct PagedSrc {
+  static constexpr int EL = 1, FORMAT = FMT;
+  static constexpr bool BF = false;
+  Kv8Geom g;
+  const int4* list;               // [B][cap] (page, first position, beams, positions)
+  const int* n_pages;             // [B]
+  const int* seen;                // [R]
+  int cap, tpp;                   // list entries a sentence, units a page
+  struct Batch {                  // one unit per lane
+    int page, pos, off, n;
+    u32 rows;
+    float ks, vs;
+  };
+  __device__ int units(int b) const { return n_pages[b] * tpp; }
+  __device__ int limit(int b, int w, int i, int W, int n_q) const { return seen[b * W + w] - n_q + 1 + i; }
+  __device__ void fetch(Batch& t, int b, int h, int u, bool valid) const {
+    t = Batch{0, 0, 0, 0, 0u, 0.f, 1.f};
+    if (!valid) return;
+    const int e = u / tpp, sub = u - e * tpp;
+    const int4 x = list[static_cast<int64_t>(b) * cap + e];
+    t.page = x.x;
+    t.off = sub * 16;
+    t.pos = x.y + t.off;
+    t.rows = static_cast<u32>(x.z);
+    t.n = max(0, min(16, x.w - t.off));
+    if (t.n > 0) {
+      const int64_t run = g.run(x.x, 0, h);
+      t.ks = g.scales[run];
+      t.vs = g.scales[run + g.H];
+    }
+  }
+  // lane `k`'s unit: the loads of its K and V rows into a stage, and its head
+  template <class L> __device__ __forceinline__ UnitHead issue(const Batch& t, int k, int b, int h, const L& load) const {
+    const int page = __shfl_sync(FULL, t.page, k), off = __shfl_sync(FULL, t.off, k), n = __shfl_sync(FULL, t.n, k);
+    UnitHead u;
+    u.pos = __shfl_sync(FULL, t.pos, k);
+    u.rows = __shfl_sync(FULL, t.rows, k);
+    u.ks = __shfl_sync(FULL, t.ks, k);
+    u.ve = static_cast<float>((__float_as_int(__shfl_sync(FULL, t.vs, k)) >> 23) - 127);
+    const char* kp = g.pool + (g.run(page, 0, h) * g.block + off) * g.D;
+    load(kp, kp + static_cast<int64_t>(g.H) * g.block * g.D, g.D, g.D, n);
+    return u;
+  }
+};
+
+// An encoder's states: a unit is up to 16 positions of a sentence.
+struct EncSrc {
+  static constexpr int EL = 2, FORMAT = 0;
+  static constexpr bool BF = true;
+  EncKV e;
+  struct Batch { int u; };
+  __device__ int len(int b) const {
+    const int n = e.len[b];
+    if (n >= 0 && n <= e.S) return n;
+    set_status(e.status, VBS_EINVAL);
+    return n < 0 ? 0 : e.S;
+  }
+  __device__ int units(int b) const { return max(1, (len(b) + 15) >> 4); }
+  __device__ int limit(int b, int, int, int, int) const { return len(b); }
+  __device__ void fetch(Batch& t, int, int, int u, bool) const { t.u = u; }
+  template <class L> __device__ __forceinline__ UnitHead issue(const Batch& t, int k, int b, int h, const L& load) const {
+    const int pos = __shfl_sync(FULL, t.u, k) * 16;
+    const int n = max(0, min(16, len(b) - pos));
+    load(reinterpret_cast<const char*>(e.k + b * e.k_sent + h * e.k_head + (n > 0 ? pos * e.k_pos : 0)),
+         reinterpret_cast<const char*>(e.v + b * e.v_sent + h * e.v_head + (n > 0 ? pos * e.v_pos : 0)),
+         e.k_pos * 2, e.v_pos * 2, n);
+    return UnitHead{pos, 0xffffu, 1.f, 0.f};
+  }
+};
+
+// ---------------------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------------------
+
+template <int EL, int DP, int MT> struct SplitCfg {
+  static constexpr int CHK = 16 / EL;                       // dims in 16 bytes
+  static constexpr int KS = DP / 16;                        // contraction steps of the scores
+  static constexpr int NT = DP / 8;                         // output tiles of 8 dims
+  static constexpr int VCH = NT < CHK ? NT : CHK;           // dims of a position that a lane reads at once
+  static constexpr int STAGE = 2 * 16 * DP * EL;            // bytes of K and V of one unit
+  static constexpr int NS = STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
+  static constexpr int O_LD = DP + 4;                       // floats of an o row in shared memory
+  static constexpr int RING = NS * STAGE > MT * 16 * O_LD * 4 ? NS * STAGE : MT * 16 * O_LD * 4;
+  static constexpr int QBYTES = MT * KS * 512;              // Q in fragment order
+  static constexpr int PART = MT * 16 * (DP + 2);           // floats of a partial
+  static constexpr size_t SMEM = SP_WARPS * RING + QBYTES;
+  // resident CTAs a SM, by shared memory and by o's registers (MT * DP / 2 of a thread's)
+  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 ? 2 : 3);
+};
+
+// The order of output dims: column n of output tile j.
+template <int VCH> __device__ __forceinline__ int out_dim(int n, int j) {
+  return (j / VCH) * (8 * VCH) + n * VCH + j % VCH;
+}
+
+// The XOR of a position's 16-byte chunks: rows of 8 (or 16) chunks, or two positions to a line of 8.
+__device__ __forceinline__ int k_swz(int tok, int nc) { return (nc & 7) == 0 ? (tok & 1) << 2 : 0; }
+__device__ __forceinline__ int v_swz(int tok, int nc) { return (nc & 3) == 0 ? ((tok >> 1) & 3) << 1 : 0; }
+
+// EXACT: head_dim is DP; ALIGNED: K and V rows may be copied 16 bytes at a time.
+template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
+__global__ void __launch_bounds__(SP_NT, (SplitCfg<Src::EL, DP, MT>::CTAS))
+attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
+  using C = SplitCfg<Src::EL, DP, MT>;
+  constexpr int EL = Src::EL, ROWS = 16 * MT;
+  extern __shared__ __align__(128) unsigned char sp_smem[];
+  __shared__ UnitHead heads[SP_WARPS][C::NS];
+  __shared__ float row_f[ROWS];                             // a row's factor on its dot products
+  __shared__ float wm[SP_WARPS][ROWS], wl[SP_WARPS][ROWS];
+  __shared__ int64_t s_sum[SP_WARPS];
+  __shared__ int s_b;
+  __shared__ int64_t s_pos, s_total;
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c4 = lane & 3;
+  const int D = EXACT ? DP : sa.D;
+  const int nc = D / C::CHK;                                // 16-byte chunks of a row
+  unsigned char* ring = sp_smem + wid * C::RING;
+  const u32 ring_a = smem_u32(ring);
+  uint16_t* qf = reinterpret_cast<uint16_t*>(sp_smem + SP_WARPS * C::RING);
+  const u32 qf_a = smem_u32(qf);
+  const int HM = sa.H * sa.MC;
+
+  // ---- this CTA's share of the line ----
+  int b = 0;
+  int64_t at = 0, end, per;                                 // position within sentence b's units (all heads)
+  {
+    const int k = (sa.B + SP_NT - 1) / SP_NT;               // a thread's sentences: [tid * k, tid * k + k)
+    int64_t mine = 0;
+    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i);
+    int64_t inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) s_sum[wid] = inc;
+    __syncthreads();
+    int64_t before = inc - mine, all = 0;
+    for (int w = 0; w < SP_WARPS; ++w) {
+      if (w < wid) before += s_sum[w];
+      all += s_sum[w];
+    }
+    const int64_t total = all * HM;
+    per = max(static_cast<int64_t>(SP_MIN), (total + gridDim.x - 1) / gridDim.x);
+    const int64_t from = per * blockIdx.x;
+    end = min(total, from + per);
+    if (from >= total) return;
+    if (from >= before * HM && from < (before + mine) * HM) {
+      int64_t p = from - before * HM;
+      int i = tid * k;
+      for (; i < sa.B - 1; ++i) {
+        const int64_t n = static_cast<int64_t>(src.units(i)) * HM;
+        if (p < n) break;
+        p -= n;
+      }
+      s_b = i;
+      s_pos = p;
+    }
+    __syncthreads();
+    b = s_b;
+    at = s_pos;
+    end -= from;                                            // units left
+  }
+  int64_t line0 = per * blockIdx.x - at;                    // the line's position of sentence b's first unit
+
+  while (end > 0 && b < sa.B) {
+    const int n = src.units(b);
+    const int hm = static_cast<int>(at / n), h = hm / sa.MC, mc = hm - h * sa.MC;
+    const int u0 = static_cast<int>(at - static_cast<int64_t>(hm) * n);
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(n), u0 + end));
+    const int rho0 = mc * ROWS;
+    const int rows = min(ROWS, sa.M - rho0);
+
+    const int mine = u1 - u0 > wid ? (u1 - u0 - wid + SP_WARPS - 1) / SP_WARPS : 0;
+    typename Src::Batch batch;
+    auto issue = [&](int k) {                               // the warp's k-th unit into its stage
+      if (k < mine) {
+        if ((k & 31) == 0) src.fetch(batch, b, h, u0 + wid + (k + lane) * SP_WARPS, k + lane < mine);
+        const int st = k % C::NS;
+        const u32 base = ring_a + st * C::STAGE;
+        const UnitHead u = src.issue(batch, k & 31, b, h, [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
+#pragma unroll
+          for (int i = 0; i < (DP / C::CHK + 1) / 2; ++i) {
+            const int L = i * 32 + lane;
+            const int tok = L / nc, ch = L - tok * nc;
+            if (EXACT || tok < 16) {
+              const bool ok = tok < cnt;
+              const char* ks = kp + (ok ? tok * kld + ch * 16 : 0);
+              const char* vs = vp + (ok ? tok * vld + ch * 16 : 0);
+              const u32 kd = base + (L ^ k_swz(tok, nc)) * 16;
+              const u32 vd = base + C::STAGE / 2 + (L ^ v_swz(tok, nc)) * 16;
+              if (ALIGNED) {
+                cp_async16(kd, ks, ok);
+                cp_async16(vd, vs, ok);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint16_t x = ok ? reinterpret_cast<const uint16_t*>(ks)[e] : uint16_t{0};
+                  const uint16_t y = ok ? reinterpret_cast<const uint16_t*>(vs)[e] : uint16_t{0};
+                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(kd + e * 2), "h"(x) : "memory");
+                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(vd + e * 2), "h"(y) : "memory");
+                }
+              }
+            }
+          }
+        });
+        if (lane == 0) heads[wid][st] = u;
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < C::NS - 1; ++k) issue(k);
+
+    // ---- Q in fragment order, a warp a row ----
+    for (int r = wid; r < ROWS; r += SP_WARPS) {
+      const int rho = rho0 + r;
+      const bool live = r < rows;
+      const int gq = rho % sa.G, i = rho / sa.G % io.n_q, w = rho / sa.G / io.n_q;
+      const uint16_t* q = io.q + static_cast<int64_t>(b * sa.W + w) * io.q_row + i * io.q_tok + (h * sa.G + gq) * io.q_head;
+      u32 x[DP / 32];
+#pragma unroll
+      for (int t = 0; t < DP / 32; ++t) x[t] = live && t * 32 + lane < D ? q[t * 32 + lane] : 0;
+      float up = 1.f;                                       // the row's power of two: its largest element to [1, 2)
+      if (!Src::BF) {
+        u32 top = 0;
+#pragma unroll
+        for (int t = 0; t < DP / 32; ++t) top = max(top, x[t] & 0x7fffu);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(FULL, top, k));
+        const int ex = static_cast<int>(top >> 7);          // biased exponent
+        up = __int_as_float(max(1, min(254, 254 - ex)) << 23);
+      }
+      if (lane == 0) row_f[r] = io.scale * LOG2E_F / up;
+#pragma unroll
+      for (int t = 0; t < DP / 32; ++t) {
+        const int d = t * 32 + lane, ch = d / C::CHK, in = d % C::CHK;
+        const int ks = (ch >> 2) * (C::CHK / 4) + in / 4;
+        const int ln = (r & 7) * 4 + (ch & 3), reg = ((r >> 3) & 1) + (in & 2);
+        const uint16_t v = Src::BF ? static_cast<uint16_t>(x[t])
+                                   : __half_as_ushort(__float2half_rn(__uint_as_float(x[t] << 16) * up));
+        qf[((((r >> 4) * C::KS + ks) * 32 + ln) * 4 + reg) * 2 + (in & 1)] = v;
+      }
+    }
+    __syncthreads();
+
+    float o[MT][C::NT][4], m[MT][2], l[MT][2], f[MT][2];
+    int lim[MT][2], beam[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + x * 8 + g, rho = rho0 + r;
+        m[mt][x] = -INFINITY;
+        l[mt][x] = 0.f;
+        f[mt][x] = row_f[r];
+        const int w = rho / sa.G / io.n_q;
+        lim[mt][x] = r < rows ? src.limit(b, w, rho / sa.G % io.n_q, sa.W, io.n_q) : 1 << 30;
+        beam[mt][x] = r < rows ? w : 31;                    // padding rows see everything, and are not written
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j) o[mt][j][x * 2] = o[mt][j][x * 2 + 1] = 0.f;
+      }
+
+    for (int k = 0; k < mine; ++k) {
+      cp_wait<C::NS - 2>();
+      __syncwarp();
+      issue(k + C::NS - 1);
+      const int st = k % C::NS;
+      const u32 ka = ring_a + st * C::STAGE, va = ka + C::STAGE / 2;
+      const UnitHead u = heads[wid][st];
+
+      // ---- scores of 16 positions: two tiles of 8 ----
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[mt][t][0] = s[mt][t][1] = s[mt][t][2] = s[mt][t][3] = 0.f;
+#pragma unroll
+      for (int grp = 0; grp < DP / C::CHK / 4; ++grp) {
+        uint4 kw[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int tok = t * 8 + g, ch = grp * 4 + c4;
+          kw[t] = EXACT || ch < nc ? lds16(ka + ((tok * nc + ch) ^ k_swz(tok, nc)) * 16) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < C::CHK / 4; ++q4) {
+          const int ks = grp * (C::CHK / 4) + q4;
+          u32 b0[2], b1[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const u32 words[4] = {kw[t].x, kw[t].y, kw[t].z, kw[t].w};
+            if (EL == 1) {
+              codes4<Src::FORMAT>(words[q4], b0[t], b1[t]);
+            } else {
+              b0[t] = words[(q4 * 2) & 3];
+              b1[t] = words[(q4 * 2 + 1) & 3];
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint4 a = lds16(qf_a + ((mt * C::KS + ks) * 32 + lane) * 16);
+            mma16816<Src::BF>(s[mt][0], a, b0[0], b1[0]);
+            mma16816<Src::BF>(s[mt][1], a, b0[1], b1[1]);
+          }
+        }
+      }
+
+      // ---- softmax: weights relative to the running maximum of s + log2(V's scale) ----
+      uint4 p[MT], p2[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        int left[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) left[x] = (u.rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? lim[mt][x] - u.pos : 0;
+        const bool full = __all_sync(FULL, left[0] >= 16 && left[1] >= 16);
+        float mx[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float fk = f[mt][x] * u.ks;
+          mx[x] = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float& z = s[mt][t][x * 2 + y];
+              z = fmaf(z, fk, u.ve);
+              if (!full && t * 8 + c4 * 2 + y >= left[x]) z = -INFINITY;
+              mx[x] = fmaxf(mx[x], z);
+            }
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 1));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 2));
+          mx[x] = fmaxf(mx[x], m[mt][x]);
+        }
+        if (__any_sync(FULL, mx[0] > m[mt][0] || mx[1] > m[mt][1])) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float corr = m[mt][x] == -INFINITY ? 0.f : ex2(m[mt][x] - mx[x]);
+            l[mt][x] *= corr;
+#pragma unroll
+            for (int j = 0; j < C::NT; ++j) {
+              o[mt][j][x * 2] *= corr;
+              o[mt][j][x * 2 + 1] *= corr;
+            }
+            m[mt][x] = mx[x];
+          }
+        }
+        float w[2][4];                                      // [row][position]
+        const float vinv = Src::BF ? 1.f : __int_as_float((127 - static_cast<int>(u.ve)) << 23);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          // fp16 weights stand at 2^15 of the largest, so that small ones keep their bits
+          const float ref = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f);
+          float sum = 0.f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              w[x][t * 2 + y] = ex2(s[mt][t][x * 2 + y] - ref);
+              sum += w[x][t * 2 + y];
+            }
+          l[mt][x] = fmaf(sum, vinv, l[mt][x]);
+        }
+        if (Src::BF) {
+          // two bf16 parts of each weight: the products carry 16 bits of it
+          float r[2][4];
+          p[mt] = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
+                             pack_bf16(w[1][2], w[1][3]));
+          const u32 hi[2][2] = {{p[mt].x, p[mt].z}, {p[mt].y, p[mt].w}};
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              r[x][t * 2] = w[x][t * 2] - bf16_lo(hi[x][t]);
+              r[x][t * 2 + 1] = w[x][t * 2 + 1] - bf16_hi(hi[x][t]);
+            }
+          p2[mt] = make_uint4(pack_bf16(r[0][0], r[0][1]), pack_bf16(r[1][0], r[1][1]), pack_bf16(r[0][2], r[0][3]),
+                              pack_bf16(r[1][2], r[1][3]));
+        } else {
+          p[mt] = make_uint4(pack_f16(w[0][0], w[0][1]), pack_f16(w[1][0], w[1][1]), pack_f16(w[0][2], w[0][3]),
+                             pack_f16(w[1][2], w[1][3]));
+        }
+      }
+
+      // ---- o += P V ----
+      const int toks[4] = {c4 * 2, c4 * 2 + 1, c4 * 2 + 8, c4 * 2 + 9};
+#pragma unroll
+      for (int vc = 0; vc < C::NT / C::VCH; ++vc) {
+        u32 vw[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int dim = out_dim<C::VCH>(g, vc * C::VCH), ch = dim / C::CHK;
+          const u32 a = va + ((toks[t] * nc + ch) ^ v_swz(toks[t], nc)) * 16;
+          if (EXACT || dim < D) {
+            if (C::VCH * EL == 16) {
+              const uint4 q = lds16(a);
+              vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = q.z; vw[t][3] = q.w;
+            } else {
+              const uint2 q = lds8(a + (dim % C::CHK) * EL);
+              vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = vw[t][3] = 0;
+            }
+          } else {
+            vw[t][0] = vw[t][1] = vw[t][2] = vw[t][3] = 0;
+          }
+        }
+#pragma unroll
+        for (int wd = 0; wd < C::VCH * EL / 4; ++wd) {
+          if (EL == 1) {
+            u32 b0[4], b1[4];                               // four dims, positions 0,1 and 2,3 of the lane
+            codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x5140), b0[0], b0[1]);
+            codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x7362), b0[2], b0[3]);
+            codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x5140), b1[0], b1[1]);
+            codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x7362), b1[2], b1[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816<false>(o[mt][vc * C::VCH + wd * 4 + i], p[mt], b0[i], b1[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const u32 b0 = __byte_perm(vw[0][wd], vw[1][wd], i ? 0x7632 : 0x5410);
+              const u32 b1 = __byte_perm(vw[2][wd], vw[3][wd], i ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p[mt], b0, b1);
+                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt], b0, b1);
+              }
+            }
+          }
+        }
+      }
+    }
+
+    // ---- join the warps ----
+    cp_wait<0>();
+    __syncwarp();                                           // the ring is free: o goes there
+    float* mo = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + x * 8 + g;
+        float ls = l[mt][x];
+        ls += __shfl_xor_sync(FULL, ls, 1);
+        ls += __shfl_xor_sync(FULL, ls, 2);
+        if (c4 == 0) {
+          wm[wid][r] = mine ? m[mt][x] : -INFINITY;
+          wl[wid][r] = mine ? ls : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < C::NT; j += 4)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            *reinterpret_cast<float4*>(mo + r * C::O_LD + out_dim<C::VCH>(c4 * 2 + y, j)) =
+                make_float4(o[mt][j][x * 2 + y], o[mt][j + 1][x * 2 + y], o[mt][j + 2][x * 2 + y], o[mt][j + 3][x * 2 + y]);
+      }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == n;
+    const int64_t line = line0 + static_cast<int64_t>(hm) * n;   // the segment's place in the line
+    float* part = sa.part + (static_cast<int64_t>(blockIdx.x) * 2 + (u0 > 0 ? 0 : 1)) * C::PART;
+    if (tid < ROWS) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < SP_WARPS; ++w) top = fmaxf(top, wm[w][tid]);
+#pragma unroll
+      for (int w = 0; w < SP_WARPS; ++w) {
+        const float x = wm[w][tid] == -INFINITY ? 0.f : ex2(wm[w][tid] - top);
+        sum += wl[w][tid] * x;                              // (a NaN stays one)
+        wm[w][tid] = x;
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int w = 0; w < SP_WARPS; ++w) wm[w][tid] *= inv;
+      } else {
+        part[ROWS * DP + tid] = top;
+        part[ROWS * DP + ROWS + tid] = sum;
+      }
+    }
+    __syncthreads();
+    auto store = [&](int r, int d, const float4& v) {       // four dims of an output row
+      const int rho = rho0 + r;
+      const int gq = rho % sa.G, i = rho / sa.G % io.n_q, w = rho / sa.G / io.n_q;
+      uint16_t* out = io.o + static_cast<int64_t>(b * sa.W + w) * io.o_row + i * io.o_tok + (h * sa.G + gq) * io.o_head + d;
+      const uint2 q = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      if (sa.out8) {
+        *reinterpret_cast<uint2*>(out) = q;
+      } else {
+        out[0] = static_cast<uint16_t>(q.x);
+        out[1] = static_cast<uint16_t>(q.x >> 16);
+        out[2] = static_cast<uint16_t>(q.y);
+        out[3] = static_cast<uint16_t>(q.y >> 16);
+      }
+    };
+    for (int idx = tid; idx < rows * (DP / 4); idx += SP_NT) {
+      const int r = idx / (DP / 4), d = idx % (DP / 4) * 4;
+      if (!EXACT && d >= D) continue;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < SP_WARPS; ++w) {
+        const float x = wm[w][r];
+        if (x != 0.f) {
+          const float4 v = *reinterpret_cast<const float4*>(sp_smem + w * C::RING + (r * C::O_LD + d) * 4);
+          a.x += v.x * x; a.y += v.y * x; a.z += v.z * x; a.w += v.w * x;
+        }
+      }
+      if (whole) store(r, d, a);
+      else *reinterpret_cast<float4*>(part + r * DP + d) = a;
+    }
+
+    // ---- join the pieces of a segment that crosses shares ----
+    if (!whole) {
+      const int64_t seg = static_cast<int64_t>(b) * HM + hm;
+      const int first = static_cast<int>(line / per), last = static_cast<int>((line + n - 1) / per);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomic_add_acq_rel(sa.arrived + seg, 1) == last - first;
+      __syncthreads();
+      if (s_last) {
+        auto piece = [&](int c) { return sa.part + (static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * C::PART; };
+        if (tid < rows) {
+          float top = -INFINITY, sum = 0.f;
+          for (int c = first; c <= last; ++c) top = fmaxf(top, __ldcg(piece(c) + ROWS * DP + tid));
+          for (int c = first; c <= last; ++c) {
+            const float x = __ldcg(piece(c) + ROWS * DP + tid);
+            sum += __ldcg(piece(c) + ROWS * DP + ROWS + tid) * (x == -INFINITY ? 0.f : ex2(x - top));
+          }
+          wm[0][tid] = top;
+          wl[0][tid] = sum == 0.f ? 0.f : 1.f / sum;
+        }
+        __syncthreads();
+        for (int idx = tid; idx < rows * (DP / 4); idx += SP_NT) {
+          const int r = idx / (DP / 4), d = idx % (DP / 4) * 4;
+          if (!EXACT && d >= D) continue;
+          const float top = wm[0][r], inv = wl[0][r];
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int c = first; c <= last; ++c) {
+            const float* pp = piece(c);
+            const float mm = __ldcg(pp + ROWS * DP + r);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + r * DP + d));
+            const float x = mm == -INFINITY ? 0.f : ex2(mm - top) * inv;
+            a.x += v.x * x; a.y += v.y * x; a.z += v.z * x; a.w += v.w * x;
+          }
+          store(r, d, a);
+        }
+        if (tid == 0) sa.arrived[seg] = 0;
+      }
+    }
+    __syncthreads();                                        // the ring and the row statistics are free again
+    const int done = u1 - u0;
+    end -= done;
+    at += done;
+    if (at == static_cast<int64_t>(n) * HM) {
+      line0 += at;
+      at = 0;
+      ++b;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------------------
+
+// Rows of a segment: two mma tiles where more than 16 rows share a K/V head (K/V are unpacked once for
+// both); one at head_dim > 128, whose o does not fit the registers twice.
+inline int split_mt(int M, int D) { return M > 16 && D <= 128 ? 2 : 1; }
+inline int split_chunks(int M, int D) { return (M + 16 * split_mt(M, D) - 1) / (16 * split_mt(M, D)); }
+inline int split_dp(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
+// floats of the partials of a grid of 3 CTAs a SM, for any number of rows
+inline int64_t split_part_floats(int D, int num_sms) {
+  return static_cast<int64_t>(num_sms) * 3 * 2 * (D <= 128 ? 32 : 16) * (split_dp(D) + 2);
+}
+
+template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
+int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
+  using C = SplitCfg<Src::EL, DP, MT>;
+  static std::atomic<unsigned long long> attr_done{0};
+  auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
+  if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
+  kernel<<<num_sms * C::CTAS, SP_NT, C::SMEM, s>>>(src, io, sa);
+  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+}
+
+template <class Src, int DP, int MT, bool ALIGNED>
+int launch_split_dp(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
+  if constexpr (ALIGNED) {
+    if (sa.D == DP) return launch_split_as<Src, DP, MT, true, true>(src, io, sa, num_sms, s);
+  }
+  return launch_split_as<Src, DP, MT, false, ALIGNED>(src, io, sa, num_sms, s);
+}
+
+template <class Src, bool ALIGNED>
+int launch_split(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
+  const int mt = split_mt(sa.M, sa.D);
+  if (sa.D <= 64)
+    return mt == 2 ? launch_split_dp<Src, 64, 2, ALIGNED>(src, io, sa, num_sms, s)
+                   : launch_split_dp<Src, 64, 1, ALIGNED>(src, io, sa, num_sms, s);
+  if (sa.D <= 128)
+    return mt == 2 ? launch_split_dp<Src, 128, 2, ALIGNED>(src, io, sa, num_sms, s)
+                   : launch_split_dp<Src, 128, 1, ALIGNED>(src, io, sa, num_sms, s);
+  return launch_split_dp<Src, 256, 1, ALIGNED>(src, io, sa, num_sms, s);
+}
+
+inline SplitArgs split_args(const QO& io, int B, int W, int H, int D, float* part, int* arrived) {
+  SplitArgs sa{B, W, H, D, io.Hq / H, W * io.n_q * (io.Hq / H), 0, part, arrived, false};
+  sa.MC = split_chunks(sa.M, D);
+  sa.out8 = (reinterpret_cast<uintptr_t>(io.o) & 7) == 0 && io.o_row % 4 == 0 && io.o_tok % 4 == 0 && io.o_head % 4 == 0;
+  return sa;
+}
+
+}  // namespace vbs

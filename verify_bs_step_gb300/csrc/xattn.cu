@@ -1,0 +1,15 @@
+// Cross attention to an encoder's states: the split kernel's instances for bf16 keys and values.
+
+#include "attn_split.cuh"
+
+namespace vbs {
+
+int launch_xattn(const EncKV& e, const QO& io, float* part, int* arrived, int num_sms, cudaStream_t s) {
+  const EncSrc src{e};
+  const SplitArgs sa = split_args(io, e.B, e.W, e.H, e.D, part, arrived);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 &&
+                       (e.k_sent | e.k_pos | e.k_head | e.v_sent | e.v_pos | e.v_head) % 8 == 0;
+  return aligned ? launch_split<EncSrc, true>(src, io, sa, num_sms, s) : launch_split<EncSrc, false>(src, io, sa, num_sms, s);
+}
+
+}  // namespace vbs
