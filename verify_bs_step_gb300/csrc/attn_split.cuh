@@ -96,7 +96,7 @@ __device__ __forceinline__ u32 pack_bf16(float a, float b) {
 
 // What a unit's consumer needs of it.
 struct UnitHead {
-  int pos;                        // its first position
+  int pos, n;                     // its first position, and how many it has
   u32 rows;                       // the beams that see it
   float ks, ve;                   // K's scale; log2 of V's scale
 };
@@ -141,6 +141,7 @@ template <int FMT> struct PagedSrc {
   template <class L> __device__ __forceinline__ UnitHead issue(const Batch& t, int k, int b, int h, const L& load) const {
     const int page = __shfl_sync(FULL, t.page, k), off = __shfl_sync(FULL, t.off, k), n = __shfl_sync(FULL, t.n, k);
     UnitHead u;
+    u.n = n;
     u.pos = __shfl_sync(FULL, t.pos, k);
     u.rows = __shfl_sync(FULL, t.rows, k);
     u.ks = __shfl_sync(FULL, t.ks, k);
@@ -172,7 +173,7 @@ struct EncSrc {
     load(reinterpret_cast<const char*>(e.k + b * e.k_sent + h * e.k_head + (n > 0 ? pos * e.k_pos : 0)),
          reinterpret_cast<const char*>(e.v + b * e.v_sent + h * e.v_head + (n > 0 ? pos * e.v_pos : 0)),
          e.k_pos * 2, e.v_pos * 2, n);
-    return UnitHead{pos, 0xffffu, 1.f, 0.f};
+    return UnitHead{pos, n, 0xffffu, 1.f, 0.f};
   }
 };
 
@@ -420,7 +421,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       for (int mt = 0; mt < MT; ++mt) {
         int left[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) left[x] = (u.rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? lim[mt][x] - u.pos : 0;
+        for (int x = 0; x < 2; ++x) left[x] = (u.rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? min(lim[mt][x] - u.pos, u.n) : 0;
         const bool full = __all_sync(FULL, left[0] >= 16 && left[1] >= 16);
         float mx[2];
 #pragma unroll
