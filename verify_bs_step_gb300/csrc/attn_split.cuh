@@ -145,7 +145,8 @@ template <int FMT> struct PagedSrc {
     u.pos = __shfl_sync(FULL, t.pos, k);
     u.rows = __shfl_sync(FULL, t.rows, k);
     u.ks = __shfl_sync(FULL, t.ks, k);
-    u.ve = static_cast<float>((__float_as_int(__shfl_sync(FULL, t.vs, k)) >> 23) - 127);
+    // held to the scales' range: a page no append has written (scale 0) counts as zeros
+    u.ve = static_cast<float>(max(KV8_E_LO, min(KV8_E_HI, (__float_as_int(__shfl_sync(FULL, t.vs, k)) >> 23) - 127)));
     const char* kp = g.pool + (g.run(page, 0, h) * g.block + off) * g.D;
     load(kp, kp + static_cast<int64_t>(g.H) * g.block * g.D, g.D, g.D, n);
     return u;
