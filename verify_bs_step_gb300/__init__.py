@@ -184,25 +184,37 @@ class _DeviceArray:
                                          "strides": None, "version": 2}
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _StreamOrder:
-    """Orders a call on a context's stream after, and what follows it before, the work of the stream
-    that is current when the call is made, where the two differ; `tensors` stay allocated until then."""
+    """Orders a call on a context's stream after the work of the stream that is current when the call is
+    made, and what follows it there after the call, where the two differ."""
 
-    def __init__(self, ctx_stream, device, *tensors):
-        cur = torch.cuda.current_stream(device)
-        self.cur = None if cur.cuda_stream == ctx_stream.cuda_stream else cur
-        self.ctx, self.tensors = ctx_stream, tensors
+    def __init__(self, device):
+        self.device = torch.device(device)
+        self.stream = torch.cuda.current_stream(self.device)
+        self.index = self.stream.device.index
+        self.raw = self.stream.cuda_stream
 
-    def __enter__(self):
-        if self.cur is not None:
-            self.ctx.wait_stream(self.cur)
+    def run(self, fn, name: str, tensors, *args):
+        if _raw_stream(self.index) == self.raw:
+            st = fn(*args)
+        else:
+            cur = torch.cuda.current_stream(self.device)
+            self.stream.wait_stream(cur)
+            st = fn(*args)
+            cur.wait_stream(self.stream)
+            for t in tensors:                       # not to be reused before the context's stream is done
+                t.record_stream(self.stream)
+        if st != OK:
+            raise VbsError(st, name)
 
-    def __exit__(self, *exc):
-        if self.cur is not None:
-            self.cur.wait_stream(self.ctx)
-            for t in self.tensors:
-                if t is not None:
-                    t.record_stream(self.ctx)
+
+def _cuda(t: torch.Tensor, name: str, dtype) -> int:
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    return t.data_ptr()
 
 
 class BeamSearch:
@@ -438,8 +450,8 @@ class PagedKV:
         if pool is None:
             pool = torch.zeros(batch * blocks_per_sentence, L, 2, H, block, D, dtype=dtype, device=self.device)
         self.pool = pool
-        self._stream_obj = torch.cuda.current_stream(self.device)
-        self.stream = _vp(self._stream_obj.cuda_stream)
+        self._order = _StreamOrder(self.device)
+        self.stream = _vp(self._order.raw)
         desc = _KvDesc(L, H, D, max_blocks * block, pool.element_size())
         ctx = _vp()
         _check(lib().kv_paged_init(ctypes.byref(ctx), ctypes.byref(desc), batch, W, blocks_per_sentence, block,
@@ -464,10 +476,12 @@ class PagedKV:
         row int32 [cap], cu int32 [batch + 1]); unused entries are -1."""
         if lens.shape != (self.batch,) or not lens.is_contiguous():
             raise ValueError(f"lens must be a contiguous int32 [{self.batch}] tensor")
-        lp = _dev_ptr(lens, "lens", torch.int32)
-        out = self._slot_outputs(self.batch, cap) if cap is not None else None
-        with _StreamOrder(self._stream_obj, self.device, lens, *(out or ())):
-            _check(lib().kv_paged_build(self.ctx, lp, *self._slot_args(out)), "kv_paged_build")
+        lp = _cuda(lens, "lens", torch.int32)
+        if cap is None:
+            self._order.run(lib().kv_paged_build, "kv_paged_build", (lens,), self.ctx, lp, 0, None, None, None, None)
+            return None
+        out, args = self._slot_outputs(self.batch, cap)
+        self._order.run(lib().kv_paged_build, "kv_paged_build", (lens,) + out, self.ctx, lp, *args)
         return out
 
     def slot_map(self, start: torch.Tensor, count: torch.Tensor, cap: int):
@@ -478,23 +492,18 @@ class PagedKV:
             raise ValueError(f"start and count must have {self.R} (or {self.batch}) entries each")
         if not (start.is_contiguous() and count.is_contiguous()):
             raise ValueError("start and count must be contiguous")
-        sp, cp = _dev_ptr(start, "start", torch.int32), _dev_ptr(count, "count", torch.int32)
-        out = self._slot_outputs(n, cap)
-        with _StreamOrder(self._stream_obj, self.device, start, count, *out):
-            _check(lib().kv_paged_slots(self.ctx, n, sp, cp, *self._slot_args(out)), "kv_paged_slots")
+        sp, cp = _cuda(start, "start", torch.int32), _cuda(count, "count", torch.int32)
+        out, args = self._slot_outputs(n, cap)
+        self._order.run(lib().kv_paged_slots, "kv_paged_slots", (start, count) + out, self.ctx, n, sp, cp, *args)
         return out
 
     def _slot_outputs(self, n: int, cap: int):
         if cap < 0:
             raise ValueError("cap must not be negative")
-        i32 = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device)
-        return (torch.empty(cap, dtype=torch.int64, device=self.device), i32[:cap], i32[cap:2 * cap], i32[2 * cap:])
-
-    @staticmethod
-    def _slot_args(out):
-        if out is None:
-            return 0, None, None, None, None
-        return (out[0].numel(),) + tuple(_vp(t.data_ptr()) for t in out)
+        slots = torch.empty(cap, dtype=torch.int64, device=self.device)
+        pos, row, cu = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device).split((cap, cap, n + 1))
+        p = pos.data_ptr()
+        return (slots, pos, row, cu), (cap, slots.data_ptr(), p, p + 4 * cap, p + 8 * cap)
 
     def views(self):
         """The allocator's state as int32 tensors on the library's own memory (no copy; they keep it
@@ -581,6 +590,7 @@ class PagedKV8(PagedKV):
         if scales.shape != (NB, L, 2, H) or not scales.is_contiguous():
             raise ValueError(f"scales must be a contiguous float32 [{NB}, {L}, 2, {H}] tensor")
         self.scales, self.heads, self.max_q = scales, heads, max_q
+        self._q_shape = None                        # of the planned step
         _check(lib().kv8_init(ctypes.byref(self.ctx8), self.ctx, I8 if dtype == torch.int8 else E4M3,
                               _dev_ptr(scales, "scales", torch.float32), heads, max_q), "kv8_init")
 
@@ -590,28 +600,26 @@ class PagedKV8(PagedKV):
         Tokens of one block stand next to each other in ascending order, as build() and slot_map() list
         them; a run that starts a block sets its scales, one that continues it can only raise them."""
         N = slots.numel()
-        for name, t in (("k", k), ("v", v)):
-            if t.shape != (N, self.H, self.D) or (self.D > 1 and t.stride(2) != 1):
-                raise ValueError(f"{name} must be [{N}, {self.H}, {self.D}] with unit stride along D")
+        shape, ks, vs = (N, self.H, self.D), k.stride(), v.stride()
+        if k.shape != shape or v.shape != shape or ks[2] != 1 or vs[2] != 1:
+            raise ValueError(f"k and v must be [{N}, {self.H}, {self.D}] with unit stride along D")
         if k.dtype != v.dtype:
             raise ValueError("k and v must have one dtype")
         if slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots must be a contiguous int64 [N] tensor")
-        args = (_dev_ptr(k, "k"), _dev_ptr(v, "v"), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                _dtype_code(k.dtype), N, _dev_ptr(slots, "slots", torch.int64))
-        with _StreamOrder(self._stream_obj, self.device, k, v, slots):
-            _check(lib().kv8_append(self.ctx8, layer, *args), "kv8_append")
+        dt = k.dtype
+        code = _dtype_code(dt)
+        self._order.run(lib().kv8_append, "kv8_append", (k, v, slots), self.ctx8, layer, _cuda(k, "k", dt),
+                        _cuda(v, "v", dt), ks[0], ks[1], vs[0], vs[1], code, N, _cuda(slots, "slots", torch.int64))
 
     def read(self, layer: int, slots: torch.Tensor):
         """(k, v) bfloat16 [N, H, D]: the values that slots (int64 [N]) hold, exactly; zeros for -1."""
         if slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots must be a contiguous int64 [N] tensor")
-        sp = _dev_ptr(slots, "slots", torch.int64)
-        k = torch.empty(slots.numel(), self.H, self.D, dtype=torch.bfloat16, device=self.device)
-        v = torch.empty_like(k)
-        with _StreamOrder(self._stream_obj, self.device, slots, k, v):
-            _check(lib().kv8_read(self.ctx8, layer, slots.numel(), sp, _vp(k.data_ptr()), _vp(v.data_ptr())),
-                   "kv8_read")
+        n = slots.shape[0]
+        k, v = torch.empty(2, n, self.H, self.D, dtype=torch.bfloat16, device=self.device).unbind(0)
+        self._order.run(lib().kv8_read, "kv8_read", (slots, k), self.ctx8, layer, n,
+                        _cuda(slots, "slots", torch.int64), k.data_ptr(), v.data_ptr())
         return k, v
 
     def plan(self, ctx_len: torch.Tensor, n_q: int = 1):
@@ -619,23 +627,19 @@ class PagedKV8(PagedKV):
         positions, its n_q new tokens among them.  Call it whenever the tables or lengths have changed."""
         if ctx_len.shape != (self.R,) or not ctx_len.is_contiguous():
             raise ValueError(f"ctx_len must be a contiguous int32 [{self.R}] tensor")
-        cp = _dev_ptr(ctx_len, "ctx_len", torch.int32)
-        with _StreamOrder(self._stream_obj, self.device, ctx_len):
-            _check(lib().kv8_plan(self.ctx8, cp, n_q), "kv8_plan")
-        self._n_q = n_q
+        self._order.run(lib().kv8_plan, "kv8_plan", (ctx_len,), self.ctx8, _cuda(ctx_len, "ctx_len", torch.int32), n_q)
+        self._q_shape = (self.R, n_q, self.heads, self.D)
 
     def attend(self, layer: int, q: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None):
         """softmax(scale q k^T) v of q [R, n_q, heads, D] (bfloat16, unit stride along D) over each row's
         cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
-        shape = (self.R, getattr(self, "_n_q", q.shape[1] if q.dim() > 1 else 0), self.heads, self.D)
+        shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
+        qs = _rows4(q, "q", shape)
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        _rows4(q, "q", shape)
-        _rows4(out, "out", shape)
-        with _StreamOrder(self._stream_obj, self.device, q, out):
-            _check(lib().kv8_attention(self.ctx8, layer, _vp(q.data_ptr()), q.stride(0), q.stride(1), q.stride(2),
-                                       self.D ** -0.5 if scale is None else scale, _vp(out.data_ptr()),
-                                       out.stride(0), out.stride(1), out.stride(2)), "kv8_attention")
+        os_ = _rows4(out, "out", shape)
+        self._order.run(lib().kv8_attention, "kv8_attention", (q, out), self.ctx8, layer, q.data_ptr(), qs[0], qs[1], qs[2],
+                        self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
         return out
 
     def close(self):
@@ -646,9 +650,13 @@ class PagedKV8(PagedKV):
 
 
 def _rows4(t: torch.Tensor, name: str, shape):
-    if t.shape != shape or t.stride(3) != 1:
+    """The strides of a bfloat16 tensor of this shape."""
+    st = t.stride()
+    if t.shape != shape or st[3] != 1:
         raise ValueError(f"{name} must be {list(shape)} with unit stride along the last axis, got {list(t.shape)}")
-    _dev_ptr(t, name, torch.bfloat16)
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    return st
 
 
 class CrossAttention:
@@ -665,9 +673,9 @@ class CrossAttention:
         self.kv_heads = heads if kv_heads is None else kv_heads
         self.max_q, self.max_len = max_q, max_len
         self.device = torch.device(device)
-        self._stream_obj = torch.cuda.current_stream(self.device)
+        self._order = _StreamOrder(self.device)
         _check(lib().xattn_init(ctypes.byref(self.ctx), batch, W, heads, self.kv_heads, D, max_q, max_len,
-                                _vp(self._stream_obj.cuda_stream)), "xattn_init")
+                                _vp(self._order.raw)), "xattn_init")
 
     def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, enc_len: torch.Tensor,
                scale: float | None = None, out: torch.Tensor | None = None):
@@ -676,22 +684,17 @@ class CrossAttention:
         scale defaults to D ** -0.5."""
         n_q = q.shape[1] if q.dim() == 4 else 0
         S = k.shape[1] if k.dim() == 4 else 0
-        shape = (self.R, n_q, self.heads, self.D)
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        _rows4(q, "q", shape)
-        _rows4(out, "out", shape)
-        _rows4(k, "k", (self.batch, S, self.kv_heads, self.D))
-        _rows4(v, "v", (self.batch, S, self.kv_heads, self.D))
+        shape, kv_shape = (self.R, n_q, self.heads, self.D), (self.batch, S, self.kv_heads, self.D)
+        qs, ks, vs = _rows4(q, "q", shape), _rows4(k, "k", kv_shape), _rows4(v, "v", kv_shape)
         if enc_len.shape != (self.batch,) or not enc_len.is_contiguous():
             raise ValueError(f"enc_len must be a contiguous int32 [{self.batch}] tensor")
-        lp = _dev_ptr(enc_len, "enc_len", torch.int32)
-        with _StreamOrder(self._stream_obj, self.device, q, k, v, enc_len, out):
-            _check(lib().xattn_run(self.ctx, _vp(q.data_ptr()), q.stride(0), q.stride(1), q.stride(2), n_q,
-                                   _vp(k.data_ptr()), k.stride(0), k.stride(1), k.stride(2),
-                                   _vp(v.data_ptr()), v.stride(0), v.stride(1), v.stride(2), S, lp,
-                                   self.D ** -0.5 if scale is None else scale,
-                                   _vp(out.data_ptr()), out.stride(0), out.stride(1), out.stride(2)), "xattn_run")
+        lp = _cuda(enc_len, "enc_len", torch.int32)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        os_ = _rows4(out, "out", shape)
+        self._order.run(lib().xattn_run, "xattn_run", (q, k, v, enc_len, out), self.ctx, q.data_ptr(), qs[0], qs[1], qs[2],
+                        n_q, k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2], S, lp,
+                        self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
         return out
 
     def status(self) -> int:

@@ -555,8 +555,6 @@ VBS_EXPORT int kv_paged_build(vbs_pkv* c, const int32_t* lens, int64_t cap, int6
   if (!c || !lens || cap < 0 || cap >= (int64_t{1} << 31)) return VBS_EINVAL;
   if (cap > 0 && !slots) return VBS_EINVAL;
   const vbs::SlotArgs s{c->a.B, nullptr, lens, cap, slots, pos, row, cu, c->scan};
-  // copies still pending refer to the tables being replaced: forget them
-  if (cudaMemsetAsync(c->a.tasks, 0, sizeof(int4) * c->R, c->stream) != cudaSuccess) return VBS_ECUDA;
   c->copy_pending = false;
   return vbs::launch_kv_build(c->a, s, true, num_sms(), c->stream);
 }

@@ -78,10 +78,9 @@ template <int FMT> __device__ __forceinline__ void codes4(u32 w, u32& lo, u32& h
     lo = *reinterpret_cast<u32*>(&x);
     hi = *reinterpret_cast<u32*>(&y);
   } else {
-    const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
-    const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-    lo = static_cast<u32>(x.x) | (static_cast<u32>(x.y) << 16);
-    hi = static_cast<u32>(y.x) | (static_cast<u32>(y.y) << 16);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
   }
 }
 

@@ -8,7 +8,8 @@
 //
 // Both are stores with no reuse (16 bytes a token, 4 a table entry), so the time is the
 // launch plus the bytes at the write bandwidth; the only dependence between requests is the
-// sum of the counts before them.
+// sum of the counts before them: up to TAB_SCAN requests every CTA adds up the counts itself (n / 256
+// loads a thread, from L2, in one launch); more take a scan kernel first.
 
 #include "common.cuh"
 #include "kv_tables.h"
@@ -16,6 +17,7 @@
 namespace vbs {
 
 constexpr int TAB_NT = 256;
+constexpr int TAB_SCAN = 4096;
 
 // A request's length if the cache can hold it, else 0 (and the status says so).
 __device__ __forceinline__ int valid_len(const PagedArgs& a, int len) {
@@ -73,14 +75,57 @@ __global__ void __launch_bounds__(1024) kv_scan_kernel(const PagedArgs a, const 
   }
 }
 
-// CTA (i, c): chunk c of request i's table rows and tokens.
+// The sum of the counts before request i, and of all, added up by the whole CTA.
+__device__ __forceinline__ void sums_of(const PagedArgs& a, const SlotArgs& s, int i, bool build, int64_t& before,
+                                        int64_t& all) {
+  __shared__ int64_t part[2][TAB_NT / 32];
+  const int tid = threadIdx.x;
+  int64_t lo = 0, hi = 0;
+  for (int j = tid; j < s.n; j += TAB_NT) {
+    const int c = valid_count(a, s, j, build);
+    if (j < i) lo += c;
+    else hi += c;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    lo += __shfl_xor_sync(FULL, lo, m);
+    hi += __shfl_xor_sync(FULL, hi, m);
+  }
+  if ((tid & 31) == 0) {
+    part[0][tid >> 5] = lo;
+    part[1][tid >> 5] = hi;
+  }
+  __syncthreads();
+  before = all = 0;
+  for (int w = 0; w < TAB_NT / 32; ++w) {
+    before += part[0][w];
+    all += part[1][w];
+  }
+  all += before;
+}
+
+// CTA (i, c): chunk c of request i's table rows and tokens; SCANNED: s.scan holds the sums.
+template <bool SCANNED>
 __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, const SlotArgs s, bool build) {
   const int i = blockIdx.x, tid = threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.y) * TAB_NT;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * TAB_NT + tid;
   const int count = valid_count(a, s, i, build);
   const int start = s.start ? s.start[i] : 0;
-  const int first = s.scan[i];
+  int64_t first = 0, total = 0;
+  if (SCANNED) {
+    first = s.scan[i];
+    total = s.scan[s.n];
+  } else if (s.slots || s.cu) {
+    sums_of(a, s, i, build, first, total);
+    if (blockIdx.y == 0 && tid == 0) {
+      if (s.cu) s.cu[i] = static_cast<int>(first < INT32_MAX ? first : INT32_MAX);
+      if (i == s.n - 1) {
+        if (s.cu) s.cu[s.n] = static_cast<int>(total < INT32_MAX ? total : INT32_MAX);
+        if (total > s.cap && s.slots) set_status(a.status, VBS_EINVAL);
+      }
+    }
+  }
   const int row = build || s.n == a.B ? i * a.W : i;
   const int32_t* tab = a.table + static_cast<int64_t>(row) * a.MB;
   if (build) {
@@ -93,7 +138,10 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
       a.refcnt[static_cast<int64_t>(i) * a.S + j] = j < nb ? a.W : 0;
       a.stack[static_cast<int64_t>(i) * a.S + j] = i * a.S + (a.S - 1 - static_cast<int>(j));
     }
-    if (t0 < a.W) a.nblk[row + t0] = nb;
+    if (t0 < a.W) {
+      a.nblk[row + t0] = nb;
+      a.tasks[row + t0] = make_int4(0, 0, 0, 0);             // copies still pending refer to the tables before
+    }
     if (t0 == 0) {
       a.top[i] = a.S - nb;
       a.base[i] = count;
@@ -113,7 +161,7 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
   }
   // the entries past the last token, shared out over all CTAs
   const int64_t all = static_cast<int64_t>(gridDim.x) * step;
-  for (int64_t o = s.scan[s.n] + i * step + t0; o < s.cap; o += all) {
+  for (int64_t o = total + i * step + t0; o < s.cap; o += all) {
     s.slots[o] = -1;
     if (s.pos) s.pos[o] = -1;
     if (s.row) s.row[o] = -1;
@@ -121,12 +169,17 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
 }
 
 int launch_kv_build(const PagedArgs& a, const SlotArgs& s, bool build, int num_sms, cudaStream_t stream) {
-  kv_scan_kernel<<<1, 1024, 0, stream>>>(a, s, build);
   // enough CTAs to fill the GPU when the requests are few and long
   const int64_t most = std::max<int64_t>(static_cast<int64_t>(a.MB) * a.block, static_cast<int64_t>(a.W) * a.MB);
   const int64_t want = (4 * static_cast<int64_t>(num_sms) + s.n - 1) / s.n;
   const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>({want, (most + 2 * TAB_NT - 1) / (2 * TAB_NT), 65535}));
-  kv_build_kernel<<<dim3(s.n, static_cast<unsigned>(chunks)), TAB_NT, 0, stream>>>(a, s, build);
+  const dim3 grid(s.n, static_cast<unsigned>(chunks));
+  if (s.n > TAB_SCAN) {
+    kv_scan_kernel<<<1, 1024, 0, stream>>>(a, s, build);
+    kv_build_kernel<true><<<grid, TAB_NT, 0, stream>>>(a, s, build);
+  } else {
+    kv_build_kernel<false><<<grid, TAB_NT, 0, stream>>>(a, s, build);
+  }
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
