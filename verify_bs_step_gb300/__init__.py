@@ -501,8 +501,9 @@ class PagedKV:
         if cap < 0:
             raise ValueError("cap must not be negative")
         slots = torch.empty(cap, dtype=torch.int64, device=self.device)
-        pos, row, cu = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device).split((cap, cap, n + 1))
-        p = pos.data_ptr()
+        ints = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device)
+        pos, row, cu = ints.split((cap, cap, n + 1))
+        p = ints.data_ptr()
         return (slots, pos, row, cu), (cap, slots.data_ptr(), p, p + 4 * cap, p + 8 * cap)
 
     def views(self):
