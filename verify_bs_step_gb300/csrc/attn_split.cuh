@@ -218,7 +218,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   __shared__ float wm[SP_WARPS][ROWS], wl[SP_WARPS][ROWS];
   __shared__ int64_t s_sum[SP_WARPS];
   __shared__ int s_b;
-  __shared__ int64_t s_pos, s_total;
+  __shared__ int64_t s_pos;
   __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c4 = lane & 3;

@@ -1,0 +1,450 @@
+// Cross attention of many query rows: tcgen05 tiles (sm_103a).
+//
+// A CTA takes 128 of the query rows that share one sentence's K/V head (token by token, the heads of a
+// group side by side) over all of the sentence's positions, TC_N at a time:
+//   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, two buffers;
+//   softmax       four warps, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
+//   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes (positions are the contraction,
+//                 so V is the transposed operand), O in TMEM.
+// One warp brings K and V in by TMA (128-byte swizzle, zeros past head_dim and past the tensor's end), one
+// issues the products: S of the next tile is issued before it waits for the weights of this one.
+//
+// The running reference of the softmax only moves when a row's maximum has grown by 2^8 (in the weights'
+// own units): until then weights up to 256 are as good in bf16 as weights up to 1, and O stays where it is.
+// The weights' bf16 rounding is the one rounding besides the result's; their sum is taken before it.
+//
+// What bounds it: one exponential a score on the special function unit (16 a clock and SM), and beside it the
+// products (2 x 128 x TC_N x head_dim at 4096 a clock).  Two CTAs an SM, 256 TMEM columns each, so that one's
+// products and softmax fill the other's waits.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "attn.h"
+#include "common.cuh"
+#include "xattn_tc.h"
+
+namespace vbs {
+
+constexpr int TC_M = 128;                 // query rows a CTA
+constexpr int TC_N = 64;                  // positions a tile
+constexpr int TC_ST = 2;                  // stages of K, and of V
+constexpr int TC_NT = 192;                // four softmax warps, a load warp, a product warp
+constexpr int TC_COLS = 256;              // TMEM columns: S (2 x TC_N) and O (up to 128)
+constexpr u32 TC_SPIN = 1u << 20;         // bound of a wait, in tries
+
+struct TcArgs {
+  QO io;
+  const int32_t* len;
+  int* status;
+  int S, W, H, D, G, M;
+  bool q16, out16;                        // 16-byte loads of q, stores of out
+};
+
+template <int DP> struct TcCfg {
+  static constexpr int SLABS = DP / 64;                    // 64 dims: 128 bytes a row
+  static constexpr int QB = SLABS * TC_M * 128;
+  static constexpr int TB = SLABS * TC_N * 128;            // one tile of K or V
+  static constexpr size_t SMEM = QB + 2 * TC_ST * TB + 1024;
+};
+
+// ---- tcgen05 ----
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(u64* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(u32 d, u64 a, u64 b, u32 idesc, u32 acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(u32 d, u32 a, u64 b, u32 idesc, u32 acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void tc_ld32(u32 a, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
+        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
+        "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void tc_st32(u32 a, const float (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+        "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
+        "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31]), "r"(a)
+      : "memory");
+}
+
+// Shared-memory operand with the 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart;
+// `lbo`: between 64-element slabs of a transposed operand (bytes; unused by the other kind).
+__device__ __forceinline__ u64 tc_desc(u32 addr, u32 lbo) {
+  return static_cast<u64>((addr & 0x3ffff) >> 4) | (static_cast<u64>(lbo >> 4) << 16) | (static_cast<u64>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// fp32 += bf16 x bf16, 128 rows, n columns; `bt`: the second operand's contraction is its slow axis.
+__device__ __forceinline__ constexpr u32 tc_idesc(int n, bool bt) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (bt ? 1u << 16 : 0u) | (static_cast<u32>(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* bar, int x, int s, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(x), "r"(s), "r"(h), "r"(b), "r"(smem_u32(bar)) : "memory");
+}
+
+struct TcBars {
+  u64 q, kf[TC_ST], ke[TC_ST], vf[TC_ST], ve[TC_ST], s[2], p[2], pv;
+};
+
+// A bounded wait; gives up at once when another warp has.
+__device__ __forceinline__ bool tc_wait(u64* bar, u32 parity, volatile int* gone, int* status) {
+  for (u32 i = 0; i < TC_SPIN; i += 64) {
+    if (mbar_wait(bar, parity, 64)) return true;
+    if (*gone) return false;
+  }
+  *gone = 1;
+  set_status(status, VBS_ETIMEOUT);
+  return false;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                           const __grid_constant__ CUtensorMap vmap, const TcArgs a) {
+  using C = TcCfg<DP>;
+  extern __shared__ unsigned char tc_smem_raw[];
+  __shared__ __align__(8) TcBars bars;
+  __shared__ u32 tmem_base;
+  __shared__ volatile int gone;
+
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  unsigned char* smem = tc_smem_raw + ((1024 - (smem_u32(tc_smem_raw) & 1023)) & 1023);
+  const u32 q_a = smem_u32(smem), k_a = q_a + C::QB, v_a = k_a + TC_ST * C::TB;
+
+  const int rows0 = blockIdx.x * TC_M, h = blockIdx.y, b = blockIdx.z;
+  int len = a.len[b];
+  if (len < 0 || len > a.S) {
+    if (tid == 0) set_status(a.status, VBS_EINVAL);
+    len = len < 0 ? 0 : a.S;
+  }
+  const int n = (len + TC_N - 1) / TC_N;
+
+  if (tid == 0) {
+    mbar_init(&bars.q, 128);
+    for (int i = 0; i < TC_ST; ++i) {
+      mbar_init(&bars.kf[i], 1);
+      mbar_init(&bars.ke[i], 1);
+      mbar_init(&bars.vf[i], 1);
+      mbar_init(&bars.ve[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s[i], 1);
+      mbar_init(&bars.p[i], 128);
+    }
+    mbar_init(&bars.pv, 1);
+    fence_mbar_init();
+    gone = 0;
+  }
+  if (wid == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "r"(TC_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * TC_N;
+
+  if (wid < 4) {
+    // ---- Q, its sign turned for a negative scale ----
+    const u32 flip = a.io.scale < 0.f ? 0x80008000u : 0u;
+    for (int idx = tid; idx < TC_M * (DP / 8); idx += 128) {
+      const int r = idx / (DP / 8), c = idx % (DP / 8), rho = rows0 + r;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (rho < a.M && c * 8 < a.D) {
+        const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
+        const uint16_t* q = a.io.q + static_cast<int64_t>(b * a.W + w) * a.io.q_row + i * a.io.q_tok +
+                            (h * a.G + gq) * a.io.q_head + c * 8;
+        if (a.q16) {
+          x = *reinterpret_cast<const uint4*>(q);
+        } else {
+          x.x = q[0] | static_cast<u32>(q[1]) << 16;
+          x.y = q[2] | static_cast<u32>(q[3]) << 16;
+          x.z = q[4] | static_cast<u32>(q[5]) << 16;
+          x.w = q[6] | static_cast<u32>(q[7]) << 16;
+        }
+        x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+      }
+      *reinterpret_cast<uint4*>(smem + (c >> 3) * (TC_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_arrive(&bars.q);
+
+    // ---- softmax: thread = row ----
+    const u32 row = static_cast<u32>(wid * 32) << 16;
+    const float sc = fabsf(a.io.scale) * LOG2E_F;
+    float m = -INFINITY, l = 0.f;                  // the reference (in scaled units), the sum of weights
+    bool ok = true;
+    for (int j = 0; j < n && ok; ++j) {
+      ok = tc_wait(&bars.s[j & 1], (j >> 1) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const u32 sa = tm_s + (j & 1) * TC_N + row;
+      float s[2][32];
+      tc_ld32(sa, s[0]);
+      tc_ld32(sa + 32, s[1]);
+      tc_wait_ld();
+      const int left = len - j * TC_N;
+      if (left < TC_N) {
+#pragma unroll
+        for (int i = 0; i < TC_N; ++i)
+          if (i >= left) s[i >> 5][i & 31] = -INFINITY;
+      }
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < TC_N; ++i) top[i & 3] = fmaxf(top[i & 3], s[i >> 5][i & 31]);
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+      const bool grow = mx > m + 8.f;              // also the first tile: m = -inf
+      if (__any_sync(FULL, grow)) {
+        const float to = grow ? mx : m;
+        const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
+        if (j > 0) {                               // O holds the tiles before
+          ok = tc_wait(&bars.pv, (j - 1) & 1, &gone, a.status);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < DP; c += 32) {
+            float o[32];
+            tc_ld32(tm_o + row + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= corr;
+            tc_st32(tm_o + row + c, o);
+          }
+        }
+        l *= corr;
+        m = to;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float pk[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float x = ex2(fmaf(s[i >> 4][(2 * i) & 31], sc, -ref));
+        const float y = ex2(fmaf(s[i >> 4][(2 * i + 1) & 31], sc, -ref));
+        sum[i & 3] += x + y;
+        __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+        pk[i] = *reinterpret_cast<float*>(&p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc_st32(sa, pk);                             // the weights stand where their scores were
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars.p[j & 1]);
+    }
+
+    // ---- out ----
+    if (ok && n > 0) ok = tc_wait(&bars.pv, (n - 1) & 1, &gone, a.status);
+    ok = __all_sync(FULL, ok);
+    tc_fence_after();
+    if (ok) {
+      const int rho = rows0 + tid;
+      const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
+      uint16_t* out = a.io.o + static_cast<int64_t>(b * a.W + w) * a.io.o_row + i * a.io.o_tok + (h * a.G + gq) * a.io.o_head;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int c = 0; c < DP; c += 32) {
+        float o[32];
+        __syncwarp();
+        if (n > 0) {
+          tc_ld32(tm_o + row + c, o);
+          tc_wait_ld();
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          if (rho >= a.M || c + k >= a.D) continue;
+          u32 x[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const __nv_bfloat162 p = n > 0 ? __floats2bfloat162_rn(o[k + 2 * y] * inv, o[k + 2 * y + 1] * inv)
+                                           : __floats2bfloat162_rn(0.f, 0.f);
+            x[y] = *reinterpret_cast<const u32*>(&p);
+          }
+          if (a.out16) {
+            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(x[0], x[1], x[2], x[3]);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              out[c + k + 2 * y] = static_cast<uint16_t>(x[y]);
+              out[c + k + 2 * y + 1] = static_cast<uint16_t>(x[y] >> 16);
+            }
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  } else if (wid == 4) {
+    // ---- K and V ----
+    if (lane == 0) {
+      int issued = 0;
+      for (int j = 0; j < n; ++j, ++issued) {
+        const int st = j % TC_ST;
+        const u32 ph = (j / TC_ST) & 1;
+        if (j >= TC_ST && !tc_wait(&bars.ke[st], ph ^ 1, &gone, a.status)) break;
+        mbar_expect_tx(&bars.kf[st], C::TB);
+        for (int x = 0; x < C::SLABS; ++x)
+          tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, j * TC_N, h, b);
+        if (j >= TC_ST && !tc_wait(&bars.ve[st], ph ^ 1, &gone, a.status)) {
+          mbar_wait(&bars.kf[st], ph, 1u << 16);
+          break;
+        }
+        mbar_expect_tx(&bars.vf[st], C::TB);
+        for (int x = 0; x < C::SLABS; ++x)
+          tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, j * TC_N, h, b);
+      }
+      // no copy is in flight when the CTA ends: the last ones have landed
+      for (int j = max(0, issued - TC_ST); j < issued; ++j) {
+        mbar_wait(&bars.kf[j % TC_ST], (j / TC_ST) & 1, 1u << 16);
+        mbar_wait(&bars.vf[j % TC_ST], (j / TC_ST) & 1, 1u << 16);
+      }
+    }
+  } else {
+    // ---- products ----
+    bool ok = n > 0 && tc_wait(&bars.q, 0, &gone, a.status);
+    auto scores = [&](int j) {
+      const int st = j % TC_ST;
+      if (!tc_wait(&bars.kf[st], (j / TC_ST) & 1, &gone, a.status)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+          tc_mma_ss(tm_s + (j & 1) * TC_N, tc_desc(q_a + (k >> 2) * (TC_M * 128) + (k & 3) * 32, 16),
+                    tc_desc(k_a + st * C::TB + (k >> 2) * (TC_N * 128) + (k & 3) * 32, 16), tc_idesc(TC_N, false), k > 0);
+        tc_commit(&bars.s[j & 1]);
+        tc_commit(&bars.ke[st]);
+      }
+      __syncwarp();
+      return true;
+    };
+    ok = __all_sync(FULL, ok);
+    if (ok) ok = __all_sync(FULL, scores(0));
+    for (int j = 0; j < n && ok; ++j) {
+      if (j + 1 < n) ok = __all_sync(FULL, scores(j + 1));
+      const int st = j % TC_ST;
+      ok = ok && tc_wait(&bars.p[j & 1], (j >> 1) & 1, &gone, a.status);
+      ok = ok && tc_wait(&bars.vf[st], (j / TC_ST) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+      const int left = len - j * TC_N;
+      if (left < TC_N) {
+        // positions past the end: their weights are 0, and V's rows have to be finite
+        for (int x = lane; x < (TC_N - left) * 8 * C::SLABS; x += 32) {
+          const int c = x & 7, r = left + (x >> 3) % (TC_N - left), sl = (x >> 3) / (TC_N - left);
+          *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + r * 128 + c * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < TC_N / 16; ++k)
+          tc_mma_ts(tm_o, tm_s + (j & 1) * TC_N + k * 8, tc_desc(v_a + st * C::TB + k * 2048, TC_N * 128), tc_idesc(DP, true),
+                    j > 0 || k > 0);
+        tc_commit(&bars.ve[st]);
+        tc_commit(&bars.pv);
+      }
+      __syncwarp();
+    }
+    // the products in flight read shared memory and TMEM: the last one is done before either goes
+    if (ok && n > 0) tc_wait(&bars.pv, (n - 1) & 1, &gone, a.status);
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (wid == 5)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TC_COLS) : "memory");
+}
+
+// ---------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn tensor_map_encode() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// [B][H][S][D] bf16 with any strides that are multiples of 16 bytes, as tiles of TC_N positions x 64 dims
+static bool encode(CUtensorMap* map, const uint16_t* p, const EncKV& e, int64_t sent, int64_t pos, int64_t head) {
+  const EncodeFn fn = tensor_map_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(e.D), static_cast<cuuint64_t>(e.S), static_cast<cuuint64_t>(e.H),
+                              static_cast<cuuint64_t>(e.B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(e.S > 1 ? pos * 2 : 16), static_cast<cuuint64_t>(e.H > 1 ? head * 2 : 16),
+                                 static_cast<cuuint64_t>(e.B > 1 ? sent * 2 : 16)};
+  const cuuint32_t box[4] = {64, TC_N, 1, 1}, step[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
+  const int64_t M = static_cast<int64_t>(e.W) * io.n_q * (io.Hq / e.H);
+  if (e.D > 128 || e.S < 1 || M < 64 || M >= (1 << 30) || e.H > 65535 || e.B > 65535) return false;
+  // a CTA walks a sentence's positions alone; the split kernel shares them out
+  const double tiles = static_cast<double>(e.B) * e.H * ((M + TC_M - 1) / TC_M), units = static_cast<double>(e.B) * e.H * ((M + 31) / 32);
+  const double tc = (e.S + TC_N - 1) / TC_N * 0.55 * std::max(1.0, tiles / (2 * num_sms));
+  const double split = 5.0 + units * ((e.S + 15) / 16) * (e.D <= 64 ? 0.0011 : 0.002);
+  if (tc > split) return false;
+  auto stride_ok = [](int64_t s, int64_t extent) { return extent == 1 || (s > 0 && s % 8 == 0 && s < (int64_t{1} << 38)); };
+  return ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 && stride_ok(e.k_sent, e.B) &&
+         stride_ok(e.k_pos, e.S) && stride_ok(e.k_head, e.H) && stride_ok(e.v_sent, e.B) && stride_ok(e.v_pos, e.S) &&
+         stride_ok(e.v_head, e.H) && tensor_map_encode() != nullptr;
+}
+
+template <int DP>
+static int launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const TcArgs& a, int B, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr_done{0};
+  if (!smem_attr_once(xattn_tc_kernel<DP>, static_cast<int>(TcCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
+  const dim3 grid((a.M + TC_M - 1) / TC_M, a.H, B);
+  xattn_tc_kernel<DP><<<grid, TC_NT, TcCfg<DP>::SMEM, s>>>(km, vm, a);
+  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+}
+
+int launch_xattn_tc(const EncKV& e, const QO& io, cudaStream_t s) {
+  CUtensorMap km, vm;
+  if (!encode(&km, e.k, e, e.k_sent, e.k_pos, e.k_head) || !encode(&vm, e.v, e, e.v_sent, e.v_pos, e.v_head)) return VBS_ECUDA;
+  auto eights = [](const void* p, int64_t r, int64_t t, int64_t h) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (r | t | h) % 8 == 0;
+  };
+  const TcArgs a{io, e.len, e.status, e.S, e.W, e.H, e.D, io.Hq / e.H, e.W * io.n_q * (io.Hq / e.H),
+                 eights(io.q, io.q_row, io.q_tok, io.q_head), eights(io.o, io.o_row, io.o_tok, io.o_head)};
+  return e.D <= 64 ? launch_tc<64>(km, vm, a, e.B, s) : launch_tc<128>(km, vm, a, e.B, s);
+}
+
+}  // namespace vbs
