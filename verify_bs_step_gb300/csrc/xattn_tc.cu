@@ -104,8 +104,10 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* b
       ::"r"(dst), "l"(map), "r"(x), "r"(s), "r"(h), "r"(b), "r"(smem_u32(bar)) : "memory");
 }
 
+// Two of s, p and pv, in turn: who waits for a tile's phase knows that the one before the last is over, so
+// that a barrier stands in the phase waited for or in the next, and its parity tells them apart.
 struct TcBars {
-  u64 q, kf[TC_ST], ke[TC_ST], vf[TC_ST], ve[TC_ST], s[2], p[2], pv;
+  u64 q, kf[TC_ST], ke[TC_ST], vf[TC_ST], ve[TC_ST], s[2], p[2], pv[2];
 };
 
 // A bounded wait; gives up at once when another warp has.
@@ -151,8 +153,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s[i], 1);
       mbar_init(&bars.p[i], 128);
+      mbar_init(&bars.pv[i], 1);
     }
-    mbar_init(&bars.pv, 1);
     fence_mbar_init();
     gone = 0;
   }
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         const float to = grow ? mx : m;
         const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
         if (j > 0) {                               // O holds the tiles before
-          ok = tc_wait(&bars.pv, (j - 1) & 1, &gone, a.status);
+          ok = tc_wait(&bars.pv[(j - 1) & 1], ((j - 1) >> 1) & 1, &gone, a.status);
           ok = __all_sync(FULL, ok);
           if (!ok) break;
           tc_fence_after();
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     }
 
     // ---- out ----
-    if (ok && n > 0) ok = tc_wait(&bars.pv, (n - 1) & 1, &gone, a.status);
+    if (ok && n > 0) ok = tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
     ok = __all_sync(FULL, ok);
     tc_fence_after();
     if (ok) {
@@ -366,12 +368,12 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           tc_mma_ts(tm_o, tm_s + (j & 1) * TC_N + k * 8, tc_desc(v_a + st * C::TB + k * 2048, TC_N * 128), tc_idesc(DP, true),
                     j > 0 || k > 0);
         tc_commit(&bars.ve[st]);
-        tc_commit(&bars.pv);
+        tc_commit(&bars.pv[j & 1]);
       }
       __syncwarp();
     }
     // the products in flight read shared memory and TMEM: the last one is done before either goes
-    if (ok && n > 0) tc_wait(&bars.pv, (n - 1) & 1, &gone, a.status);
+    if (ok && n > 0) tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
   }
   __syncthreads();
   tc_fence_after();
