@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
 
     // ---- softmax: thread = row ----
     const u32 row = static_cast<u32>(wid * 32) << 16;
-    const float sc = fabsf(a.io.scale) * LOG2E_F;
+    // (a scale of 0 stays above it, so that a masked -inf stays one)
+    const float sc = fmaxf(fabsf(a.io.scale) * LOG2E_F, 1.17549435e-38f);
     float m = -INFINITY, l = 0.f;                  // the reference (in scaled units), the sum of weights
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
