@@ -242,11 +242,19 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         m = to;
       }
       const float ref = m == -INFINITY ? 0.f : m;
+      // scale and reference go into one fma, whose product is not rounded as the reference was: for
+      // large scores the difference is more than a weight can bear, and the product is rounded first
+      float f = sc;
+      if (__any_sync(FULL, fabsf(ref) > 65536.f)) {
+#pragma unroll
+        for (int i = 0; i < TC_N; ++i) s[i >> 5][i & 31] *= sc;
+        f = 1.f;
+      }
       float pk[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float x = ex2(fmaf(s[i >> 4][(2 * i) & 31], sc, -ref));
-        const float y = ex2(fmaf(s[i >> 4][(2 * i + 1) & 31], sc, -ref));
+        const float x = ex2(fmaf(s[i >> 4][(2 * i) & 31], f, -ref));
+        const float y = ex2(fmaf(s[i >> 4][(2 * i + 1) & 31], f, -ref));
         sum[i & 3] += x + y;
         __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
         pk[i] = *reinterpret_cast<float*>(&p);
