@@ -3,7 +3,8 @@
 // A CTA takes 128 of the query rows that share one sentence's K/V head (token by token, the heads of a
 // group side by side) over all of the sentence's positions, TC_N at a time:
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, two buffers;
-//   softmax       four warps, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
+//   softmax       eight warps, two threads a row, half of the tile's positions each: S from TMEM to registers,
+//                 weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes (positions are the contraction,
 //                 so V is the transposed operand), O in TMEM.
 // One warp brings K and V in by TMA (128-byte swizzle, zeros past head_dim and past the tensor's end), one
@@ -28,8 +29,9 @@ namespace vbs {
 
 constexpr int TC_M = 128;                 // query rows a CTA
 constexpr int TC_N = 64;                  // positions a tile
-constexpr int TC_ST = 2;                  // stages of K, and of V
-constexpr int TC_NT = 192;                // four softmax warps, a load warp, a product warp
+constexpr int TC_STMAX = 4;               // stages of K, and of V, at most
+constexpr int TC_SM = 256;                // softmax threads: two a row
+constexpr int TC_NT = TC_SM + 64;         // and a load warp, a product warp
 constexpr int TC_COLS = 256;              // TMEM columns: S (2 x TC_N) and O (up to 128)
 constexpr u32 TC_SPIN = 1u << 20;         // bound of a wait, in tries
 
@@ -45,7 +47,8 @@ template <int DP> struct TcCfg {
   static constexpr int SLABS = DP / 64;                    // 64 dims: 128 bytes a row
   static constexpr int QB = SLABS * TC_M * 128;
   static constexpr int TB = SLABS * TC_N * 128;            // one tile of K or V
-  static constexpr size_t SMEM = QB + 2 * TC_ST * TB + 1024;
+  static constexpr int ST = DP == 64 ? 4 : 2;              // stages: what two CTAs' shared memory holds
+  static constexpr size_t SMEM = QB + 2 * ST * TB + 1024;
 };
 
 // ---- tcgen05 ----
@@ -87,6 +90,42 @@ __device__ __forceinline__ void tc_st32(u32 a, const float (&r)[32]) {
       : "memory");
 }
 
+// ---- pairs of fp32 in one instruction, and the largest of three ----
+__device__ __forceinline__ u64 pair(float x, float y) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(u64 p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ void tc_st16(u32 a, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(a)
+      : "memory");
+}
+
 // Shared-memory operand with the 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart;
 // `lbo`: between 64-element slabs of a transposed operand (bytes; unused by the other kind).
 __device__ __forceinline__ u64 tc_desc(u32 addr, u32 lbo) {
@@ -107,7 +146,7 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* b
 // Two of s, p and pv, in turn: who waits for a tile's phase knows that the one before the last is over, so
 // that a barrier stands in the phase waited for or in the next, and its parity tells them apart.
 struct TcBars {
-  u64 q, kf[TC_ST], ke[TC_ST], vf[TC_ST], ve[TC_ST], s[2], p[2], pv[2];
+  u64 q, kf[TC_STMAX], ke[TC_STMAX], vf[TC_STMAX], ve[TC_STMAX], s[2], p[2], pv[2];
 };
 
 // A bounded wait; gives up at once when another warp has.
@@ -121,18 +160,35 @@ __device__ __forceinline__ bool tc_wait(u64* bar, u32 parity, volatile int* gone
   return false;
 }
 
+// Among the 64 threads of two warps that share rows: 0 (no one moves), 1 (some do), 2 (a wait gave up).
+__device__ __forceinline__ int pair_or(int id, int move, bool ok) {
+  int r;
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .u32 m, g;\n\t"
+               "setp.ne.s32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 m, 1, 0, q;\n\t"
+               "mov.u32 %0, m;\n\t}" : "=r"(r) : "r"(id), "r"(ok ? move : 1) : "memory");
+  if (r) {
+    int e;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\t"
+                 "selp.u32 %0, 2, 0, q;\n\t}" : "=r"(e) : "r"(id), "r"(ok ? 0 : 1) : "memory");
+    r |= e;
+  }
+  return r;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                                                            const __grid_constant__ CUtensorMap vmap, const TcArgs a) {
   using C = TcCfg<DP>;
+  constexpr int ST = C::ST;
   extern __shared__ unsigned char tc_smem_raw[];
   __shared__ __align__(8) TcBars bars;
   __shared__ u32 tmem_base;
   __shared__ volatile int gone;
+  __shared__ float xch[2][TC_M];                           // what the two threads of a row tell each other
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = tc_smem_raw + ((1024 - (smem_u32(tc_smem_raw) & 1023)) & 1023);
-  const u32 q_a = smem_u32(smem), k_a = q_a + C::QB, v_a = k_a + TC_ST * C::TB;
+  const u32 q_a = smem_u32(smem), k_a = q_a + C::QB, v_a = k_a + ST * C::TB;
 
   const int rows0 = blockIdx.x * TC_M, h = blockIdx.y, b = blockIdx.z;
   int len = a.len[b];
@@ -143,8 +199,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   const int n = (len + TC_N - 1) / TC_N;
 
   if (tid == 0) {
-    mbar_init(&bars.q, 128);
-    for (int i = 0; i < TC_ST; ++i) {
+    mbar_init(&bars.q, TC_SM);
+    for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
       mbar_init(&bars.ke[i], 1);
       mbar_init(&bars.vf[i], 1);
@@ -152,13 +208,13 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s[i], 1);
-      mbar_init(&bars.p[i], 128);
+      mbar_init(&bars.p[i], TC_SM);
       mbar_init(&bars.pv[i], 1);
     }
     fence_mbar_init();
     gone = 0;
   }
-  if (wid == 5) {
+  if (wid == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "r"(TC_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -168,10 +224,10 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * TC_N;
 
-  if (wid < 4) {
+  if (wid < 8) {
     // ---- Q, its sign turned for a negative scale ----
     const u32 flip = a.io.scale < 0.f ? 0x80008000u : 0u;
-    for (int idx = tid; idx < TC_M * (DP / 8); idx += 128) {
+    for (int idx = tid; idx < TC_M * (DP / 8); idx += TC_SM) {
       const int r = idx / (DP / 8), c = idx % (DP / 8), rho = rows0 + r;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (rho < a.M && c * 8 < a.D) {
@@ -193,49 +249,57 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     mbar_arrive(&bars.q);
 
-    // ---- softmax: thread = row ----
-    const u32 row = static_cast<u32>(wid * 32) << 16;
+    // ---- softmax: threads t and t + 128 share row t ----
+    const int half = wid >> 2, r = tid & 127, bar_id = 1 + (wid & 3);
+    const u32 row = static_cast<u32>((wid & 3) * 32) << 16;
     // (a scale of 0 stays above it, so that a masked -inf stays one)
     const float sc = fmaxf(fabsf(a.io.scale) * LOG2E_F, 1.17549435e-38f);
-    float m = -INFINITY, l = 0.f;                  // the reference (in scaled units), the sum of weights
+    float m = -INFINITY, l = 0.f;                  // the reference (in scaled units), the sum of this half's weights
     bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
+    for (int j = 0; j < n; ++j) {
       ok = tc_wait(&bars.s[j & 1], (j >> 1) & 1, &gone, a.status);
-      ok = __all_sync(FULL, ok);
-      if (!ok) break;
       tc_fence_after();
       const u32 sa = tm_s + (j & 1) * TC_N + row;
-      float s[2][32];
-      tc_ld32(sa, s[0]);
-      tc_ld32(sa + 32, s[1]);
+      float s[32];
+      __syncwarp();
+      tc_ld32(sa + half * 32, s);
       tc_wait_ld();
-      const int left = len - j * TC_N;
-      if (left < TC_N) {
+      const int left = len - j * TC_N - half * 32;
+      if (left < 32) {
 #pragma unroll
-        for (int i = 0; i < TC_N; ++i)
-          if (i >= left) s[i >> 5][i & 31] = -INFINITY;
+        for (int i = 0; i < 32; ++i)
+          if (i >= left) s[i] = -INFINITY;
       }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float top[2] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3])};
 #pragma unroll
-      for (int i = 0; i < TC_N; ++i) top[i & 3] = fmaxf(top[i & 3], s[i >> 5][i & 31]);
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
-      const bool grow = mx > m + 8.f;              // also the first tile: m = -inf
-      if (__any_sync(FULL, grow)) {
-        const float to = grow ? mx : m;
+      for (int i = 4; i < 32; i += 2) top[(i >> 1) & 1] = max3(top[(i >> 1) & 1], s[i], s[i + 1]);
+      const float mx = fmaxf(top[0], top[1]) * sc;
+      // both threads of a row have their scores now (the weights go over them), and agree on whether
+      // a reference moves in either warp; a warp whose wait gave up ends both
+      tc_fence_before();
+      const int vote = pair_or(bar_id, (mx > m + 8.f ? 1 : 0), ok);
+      tc_fence_after();
+      ok = vote < 2;
+      if (!ok) break;
+      if (vote) {
+        xch[half][r] = mx;
+        named_sync(bar_id, 64);
+        const float both = fmaxf(mx, xch[half ^ 1][r]);
+        const bool grow = both > m + 8.f;          // also in the first tile: m = -inf
+        const float to = grow ? both : m;
         const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
-        if (j > 0) {                               // O holds the tiles before
+        if (j > 0) {                               // O holds the tiles before: half of its columns each
           ok = tc_wait(&bars.pv[(j - 1) & 1], ((j - 1) >> 1) & 1, &gone, a.status);
-          ok = __all_sync(FULL, ok);
-          if (!ok) break;
           tc_fence_after();
+          __syncwarp();
 #pragma unroll
-          for (int c = 0; c < DP; c += 32) {
+          for (int c = 0; c < DP / 2; c += 32) {
             float o[32];
-            tc_ld32(tm_o + row + c, o);
+            tc_ld32(tm_o + row + half * (DP / 2) + c, o);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= corr;
-            tc_st32(tm_o + row + c, o);
+            for (int i = 0; i < 32; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
+            tc_st32(tm_o + row + half * (DP / 2) + c, o);
           }
         }
         l *= corr;
@@ -247,36 +311,46 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       float f = sc;
       if (__any_sync(FULL, fabsf(ref) > 65536.f)) {
 #pragma unroll
-        for (int i = 0; i < TC_N; ++i) s[i >> 5][i & 31] *= sc;
+        for (int i = 0; i < 32; ++i) s[i] *= sc;
         f = 1.f;
       }
-      float pk[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float pk[16];
+      u64 sum[2] = {0, 0};
+      const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float x = ex2(fmaf(s[i >> 4][(2 * i) & 31], f, -ref));
-        const float y = ex2(fmaf(s[i >> 4][(2 * i + 1) & 31], f, -ref));
-        sum[i & 3] += x + y;
+      for (int i = 0; i < 16; ++i) {
+        float x, y;
+        unpair(fma2(pair(s[2 * i], s[2 * i + 1]), f2, r2), x, y);
+        x = ex2(x);
+        y = ex2(y);
+        sum[i & 1] = add2(sum[i & 1], pair(x, y));
         __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
         pk[i] = *reinterpret_cast<float*>(&p);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc_st32(sa, pk);                             // the weights stand where their scores were
+      float l0, l1;
+      unpair(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
+      tc_st16(sa + half * 16, pk);                 // the weights stand where scores were
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(&bars.p[j & 1]);
     }
 
-    // ---- out ----
+    // ---- out: half of the columns each ----
     if (ok && n > 0) ok = tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
-    ok = __all_sync(FULL, ok);
+    ok = pair_or(bar_id, 0, ok) < 2;
     tc_fence_after();
     if (ok) {
-      const int rho = rows0 + tid;
+      xch[half][r] = l;
+      named_sync(bar_id, 64);
+      l += xch[half ^ 1][r];
+      const int rho = rows0 + r;
       const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
       uint16_t* out = a.io.o + static_cast<int64_t>(b * a.W + w) * a.io.o_row + i * a.io.o_tok + (h * a.G + gq) * a.io.o_head;
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int c = 0; c < DP; c += 32) {
+      for (int c0 = 0; c0 < DP / 2; c0 += 32) {
+        const int c = half * (DP / 2) + c0;
         float o[32];
         __syncwarp();
         if (n > 0) {
@@ -307,37 +381,44 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       }
     }
     tc_fence_before();
-  } else if (wid == 4) {
-    // ---- K and V ----
+  } else if (wid == 8) {
+    // ---- K and V: one lane, each operand as far ahead as its stages go ----
     if (lane == 0) {
-      int issued = 0;
-      for (int j = 0; j < n; ++j, ++issued) {
-        const int st = j % TC_ST;
-        const u32 ph = (j / TC_ST) & 1;
-        if (j >= TC_ST && !tc_wait(&bars.ke[st], ph ^ 1, &gone, a.status)) break;
-        mbar_expect_tx(&bars.kf[st], C::TB);
-        for (int x = 0; x < C::SLABS; ++x)
-          tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, j * TC_N, h, b);
-        if (j >= TC_ST && !tc_wait(&bars.ve[st], ph ^ 1, &gone, a.status)) {
-          mbar_wait(&bars.kf[st], ph, 1u << 16);
-          break;
+      int jk = 0, jv = 0;
+      for (u32 idle = 0; (jk < n || jv < n) && idle < TC_SPIN && !gone;) {
+        bool moved = false;
+        if (jk < n && (jk < ST || mbar_wait(&bars.ke[jk % ST], ((jk / ST) & 1) ^ 1, 1))) {
+          const int st = jk % ST;
+          mbar_expect_tx(&bars.kf[st], C::TB);
+          for (int x = 0; x < C::SLABS; ++x)
+            tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, jk * TC_N, h, b);
+          ++jk;
+          moved = true;
         }
-        mbar_expect_tx(&bars.vf[st], C::TB);
-        for (int x = 0; x < C::SLABS; ++x)
-          tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, j * TC_N, h, b);
+        if (jv < n && (jv < ST || mbar_wait(&bars.ve[jv % ST], ((jv / ST) & 1) ^ 1, 1))) {
+          const int st = jv % ST;
+          mbar_expect_tx(&bars.vf[st], C::TB);
+          for (int x = 0; x < C::SLABS; ++x)
+            tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, jv * TC_N, h, b);
+          ++jv;
+          moved = true;
+        }
+        idle = moved ? 0 : idle + 1;
+      }
+      if ((jk < n || jv < n) && !gone) {
+        gone = 1;
+        set_status(a.status, VBS_ETIMEOUT);
       }
       // no copy is in flight when the CTA ends: the last ones have landed
-      for (int j = max(0, issued - TC_ST); j < issued; ++j) {
-        mbar_wait(&bars.kf[j % TC_ST], (j / TC_ST) & 1, 1u << 16);
-        mbar_wait(&bars.vf[j % TC_ST], (j / TC_ST) & 1, 1u << 16);
-      }
+      for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[j % ST], (j / ST) & 1, 1u << 16);
+      for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[j % ST], (j / ST) & 1, 1u << 16);
     }
   } else {
     // ---- products ----
     bool ok = n > 0 && tc_wait(&bars.q, 0, &gone, a.status);
     auto scores = [&](int j) {
-      const int st = j % TC_ST;
-      if (!tc_wait(&bars.kf[st], (j / TC_ST) & 1, &gone, a.status)) return false;
+      const int st = j % ST;
+      if (!tc_wait(&bars.kf[st], (j / ST) & 1, &gone, a.status)) return false;
       tc_fence_after();
       if (lane == 0) {
 #pragma unroll
@@ -354,9 +435,9 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     if (ok) ok = __all_sync(FULL, scores(0));
     for (int j = 0; j < n && ok; ++j) {
       if (j + 1 < n) ok = __all_sync(FULL, scores(j + 1));
-      const int st = j % TC_ST;
+      const int st = j % ST;
       ok = ok && tc_wait(&bars.p[j & 1], (j >> 1) & 1, &gone, a.status);
-      ok = ok && tc_wait(&bars.vf[st], (j / TC_ST) & 1, &gone, a.status);
+      ok = ok && tc_wait(&bars.vf[st], (j / ST) & 1, &gone, a.status);
       ok = __all_sync(FULL, ok);
       if (!ok) break;
       const int left = len - j * TC_N;
@@ -386,7 +467,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   }
   __syncthreads();
   tc_fence_after();
-  if (wid == 5)
+  if (wid == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TC_COLS) : "memory");
 }
 
