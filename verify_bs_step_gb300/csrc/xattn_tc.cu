@@ -149,6 +149,13 @@ struct TcBars {
   u64 q, kf[TC_STMAX], ke[TC_STMAX], vf[TC_STMAX], ve[TC_STMAX], s[2], p[2], pv[2];
 };
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  u32 r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // A bounded wait; gives up at once when another warp has.
 __device__ __forceinline__ bool tc_wait(u64* bar, u32 parity, volatile int* gone, int* status) {
   for (u32 i = 0; i < TC_SPIN; i += 64) {
@@ -265,7 +272,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       tc_ld32(sa + half * 32, s);
       tc_wait_ld();
       const int left = len - j * TC_N - half * 32;
-      if (left < 32) {
+      if (left < 32) {                             // the sentence ends in this tile
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (i >= left) s[i] = -INFINITY;
@@ -330,6 +337,18 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       float l0, l1;
       unpair(add2(sum[0], sum[1]), l0, l1);
       l += l0 + l1;
+      if (len - j * TC_N < TC_N) {
+        // positions past the end: their weights are 0, and V's rows have to be finite
+        const int st = j % ST, from = len - j * TC_N;
+        ok = tc_wait(&bars.vf[st], (j / ST) & 1, &gone, a.status);
+        for (int x = tid; x < (TC_N - from) * 8 * C::SLABS; x += TC_SM) {
+          const int c = x & 7, vr = from + (x >> 3) % (TC_N - from), sl = (x >> 3) / (TC_N - from);
+          *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + vr * 128 + c * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
       tc_st16(sa + half * 16, pk);                 // the weights stand where scores were
       tc_wait_st();
       tc_fence_before();
@@ -414,56 +433,41 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[j % ST], (j / ST) & 1, 1u << 16);
     }
   } else {
-    // ---- products ----
-    bool ok = n > 0 && tc_wait(&bars.q, 0, &gone, a.status);
-    auto scores = [&](int j) {
-      const int st = j % ST;
-      if (!tc_wait(&bars.kf[st], (j / ST) & 1, &gone, a.status)) return false;
-      tc_fence_after();
-      if (lane == 0) {
+    // ---- products: one elected thread waits and issues ----
+    if (elect_one()) {
+      const u64 dq = tc_desc(q_a, 16), dk = tc_desc(k_a, 16), dv = tc_desc(v_a, TC_N * 128);
+      auto scores = [&](int j) {
+        const int st = j % ST;
+        if (!tc_wait(&bars.kf[st], (j / ST) & 1, &gone, a.status)) return false;
+        tc_fence_after();
+        const u64 d = dk + static_cast<u64>(st * (C::TB >> 4));
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k)
-          tc_mma_ss(tm_s + (j & 1) * TC_N, tc_desc(q_a + (k >> 2) * (TC_M * 128) + (k & 3) * 32, 16),
-                    tc_desc(k_a + st * C::TB + (k >> 2) * (TC_N * 128) + (k & 3) * 32, 16), tc_idesc(TC_N, false), k > 0);
+          tc_mma_ss(tm_s + (j & 1) * TC_N, dq + (((k >> 2) * (TC_M * 128) + (k & 3) * 32) >> 4),
+                    d + (((k >> 2) * (TC_N * 128) + (k & 3) * 32) >> 4), tc_idesc(TC_N, false), k > 0);
         tc_commit(&bars.s[j & 1]);
         tc_commit(&bars.ke[st]);
-      }
-      __syncwarp();
-      return true;
-    };
-    ok = __all_sync(FULL, ok);
-    if (ok) ok = __all_sync(FULL, scores(0));
-    for (int j = 0; j < n && ok; ++j) {
-      if (j + 1 < n) ok = __all_sync(FULL, scores(j + 1));
-      const int st = j % ST;
-      ok = ok && tc_wait(&bars.p[j & 1], (j >> 1) & 1, &gone, a.status);
-      ok = ok && tc_wait(&bars.vf[st], (j / ST) & 1, &gone, a.status);
-      ok = __all_sync(FULL, ok);
-      if (!ok) break;
-      const int left = len - j * TC_N;
-      if (left < TC_N) {
-        // positions past the end: their weights are 0, and V's rows have to be finite
-        for (int x = lane; x < (TC_N - left) * 8 * C::SLABS; x += 32) {
-          const int c = x & 7, r = left + (x >> 3) % (TC_N - left), sl = (x >> 3) / (TC_N - left);
-          *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + r * 128 + c * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      }
-      tc_fence_after();
-      if (lane == 0) {
+        return true;
+      };
+      bool ok = n > 0 && tc_wait(&bars.q, 0, &gone, a.status) && scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) ok = scores(j + 1);
+        const int st = j % ST;
+        ok = ok && tc_wait(&bars.vf[st], (j / ST) & 1, &gone, a.status);
+        ok = ok && tc_wait(&bars.p[j & 1], (j >> 1) & 1, &gone, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const u64 d = dv + static_cast<u64>(st * (C::TB >> 4));
 #pragma unroll
         for (int k = 0; k < TC_N / 16; ++k)
-          tc_mma_ts(tm_o, tm_s + (j & 1) * TC_N + k * 8, tc_desc(v_a + st * C::TB + k * 2048, TC_N * 128), tc_idesc(DP, true),
-                    j > 0 || k > 0);
-        tc_commit(&bars.ve[st]);
+          tc_mma_ts(tm_o, tm_s + (j & 1) * TC_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true), j > 0 || k > 0);
         tc_commit(&bars.pv[j & 1]);
+        tc_commit(&bars.ve[st]);
       }
-      __syncwarp();
+      // the products in flight read shared memory and TMEM: the last one is done before either goes
+      if (ok && n > 0) tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
     }
-    // the products in flight read shared memory and TMEM: the last one is done before either goes
-    if (ok && n > 0) tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
+    __syncwarp();
   }
   __syncthreads();
   tc_fence_after();
