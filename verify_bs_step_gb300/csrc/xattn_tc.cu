@@ -30,7 +30,10 @@ namespace vbs {
 constexpr int TC_M = 128;                 // query rows a CTA
 constexpr int TC_N = 64;                  // positions a tile
 constexpr int TC_STMAX = 4;               // stages of K, and of V, at most
-constexpr int TC_SM = 256;                // softmax threads: two a row
+constexpr int TC_TPR = 1;                 // softmax threads a row
+constexpr int TC_SM = TC_M * TC_TPR;
+constexpr int TC_SW = TC_SM / 32;         // softmax warps
+constexpr int TC_C = TC_N / TC_TPR;       // scores of a thread in a tile
 constexpr int TC_NT = TC_SM + 64;         // and a load warp, a product warp
 constexpr int TC_COLS = 256;              // TMEM columns: S (2 x TC_N) and O (up to 128)
 constexpr u32 TC_SPIN = 1u << 20;         // bound of a wait, in tries
@@ -69,7 +72,7 @@ __device__ __forceinline__ void tc_mma_ts(u32 d, u32 a, u64 b, u32 idesc, u32 ac
                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
-__device__ __forceinline__ void tc_ld32(u32 a, float (&r)[32]) {
+__device__ __forceinline__ void tc_ld32(u32 a, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -79,14 +82,18 @@ __device__ __forceinline__ void tc_ld32(u32 a, float (&r)[32]) {
         "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(a));
 }
-__device__ __forceinline__ void tc_st32(u32 a, const float (&r)[32]) {
+__device__ __forceinline__ void tc_ld16(u32 a, float (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tc_st16(u32 a, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
       ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
-        "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
-        "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31]), "r"(a)
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(a)
       : "memory");
 }
 
@@ -116,14 +123,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-__device__ __forceinline__ void tc_st16(u32 a, const float (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(a)
-      : "memory");
 }
 
 // Shared-memory operand with the 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart;
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     fence_mbar_init();
     gone = 0;
   }
-  if (wid == 9) {
+  if (wid == TC_SW + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "r"(TC_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * TC_N;
 
-  if (wid < 8) {
+  if (wid < TC_SW) {
     // ---- Q, its sign turned for a negative scale ----
     const u32 flip = a.io.scale < 0.f ? 0x80008000u : 0u;
     for (int idx = tid; idx < TC_M * (DP / 8); idx += TC_SM) {
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     mbar_arrive(&bars.q);
 
-    // ---- softmax: threads t and t + 128 share row t ----
+    // ---- softmax ----
     const int half = wid >> 2, r = tid & 127, bar_id = 1 + (wid & 3);
     const u32 row = static_cast<u32>((wid & 3) * 32) << 16;
     // (a scale of 0 stays above it, so that a masked -inf stays one)
@@ -267,32 +266,42 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       ok = tc_wait(&bars.s[j & 1], (j >> 1) & 1, &gone, a.status);
       tc_fence_after();
       const u32 sa = tm_s + (j & 1) * TC_N + row;
-      float s[32];
+      float s[TC_C];
       __syncwarp();
-      tc_ld32(sa + half * 32, s);
-      tc_wait_ld();
-      const int left = len - j * TC_N - half * 32;
-      if (left < 32) {                             // the sentence ends in this tile
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+      for (int c = 0; c < TC_C; c += 32) tc_ld32(sa + half * TC_C + c, s + c);
+      tc_wait_ld();
+      const int left = len - j * TC_N - half * TC_C;
+      if (left < TC_C) {                             // the sentence ends in this tile
+#pragma unroll
+        for (int i = 0; i < TC_C; ++i)
           if (i >= left) s[i] = -INFINITY;
       }
-      float top[2] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3])};
+      float top[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
 #pragma unroll
-      for (int i = 4; i < 32; i += 2) top[(i >> 1) & 1] = max3(top[(i >> 1) & 1], s[i], s[i + 1]);
-      const float mx = fmaxf(top[0], top[1]) * sc;
-      // both threads of a row have their scores now (the weights go over them), and agree on whether
-      // a reference moves in either warp; a warp whose wait gave up ends both
-      tc_fence_before();
-      const int vote = pair_or(bar_id, (mx > m + 8.f ? 1 : 0), ok);
-      tc_fence_after();
+      for (int i = 8; i < TC_C; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
+      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]) * sc;
+      bool grow = mx > m + 8.f;                    // also in the first tile: m = -inf
+      float both = mx;
+      int vote;
+      if (TC_TPR == 2) {
+        // both threads of a row have their scores now (the weights go over them), and agree on whether
+        // a reference moves in either warp; a warp whose wait gave up ends both
+        tc_fence_before();
+        vote = pair_or(bar_id, grow, ok);
+        tc_fence_after();
+      } else {
+        vote = !__all_sync(FULL, ok) ? 2 : __any_sync(FULL, grow);
+      }
       ok = vote < 2;
       if (!ok) break;
       if (vote) {
-        xch[half][r] = mx;
-        named_sync(bar_id, 64);
-        const float both = fmaxf(mx, xch[half ^ 1][r]);
-        const bool grow = both > m + 8.f;          // also in the first tile: m = -inf
+        if (TC_TPR == 2) {
+          xch[half][r] = mx;
+          named_sync(bar_id, 64);
+          both = fmaxf(mx, xch[half ^ 1][r]);
+          grow = both > m + 8.f;
+        }
         const float to = grow ? both : m;
         const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
         if (j > 0) {                               // O holds the tiles before: half of its columns each
@@ -300,13 +309,13 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           tc_fence_after();
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < DP / 2; c += 32) {
-            float o[32];
-            tc_ld32(tm_o + row + half * (DP / 2) + c, o);
+          for (int c = 0; c < DP / TC_TPR; c += 16) {
+            float o[16];
+            tc_ld16(tm_o + row + half * (DP / TC_TPR) + c, o);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
-            tc_st32(tm_o + row + half * (DP / 2) + c, o);
+            for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
+            tc_st16(tm_o + row + half * (DP / TC_TPR) + c, o);
           }
         }
         l *= corr;
@@ -318,21 +327,25 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       float f = sc;
       if (__any_sync(FULL, fabsf(ref) > 65536.f)) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] *= sc;
+        for (int i = 0; i < TC_C; ++i) s[i] *= sc;
         f = 1.f;
       }
-      float pk[16];
       u64 sum[2] = {0, 0};
       const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x, y;
-        unpair(fma2(pair(s[2 * i], s[2 * i + 1]), f2, r2), x, y);
-        x = ex2(x);
-        y = ex2(y);
-        sum[i & 1] = add2(sum[i & 1], pair(x, y));
-        __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
-        pk[i] = *reinterpret_cast<float*>(&p);
+      for (int c = 0; c < TC_C; c += 32) {
+        float pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x, y;
+          unpair(fma2(pair(s[c + 2 * i], s[c + 2 * i + 1]), f2, r2), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          sum[i & 1] = add2(sum[i & 1], pair(x, y));
+          __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+          pk[i] = *reinterpret_cast<float*>(&p);
+        }
+        tc_st16(sa + half * (TC_C / 2) + c / 2, pk);   // the weights stand where scores were
       }
       float l0, l1;
       unpair(add2(sum[0], sum[1]), l0, l1);
@@ -349,7 +362,6 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
       }
-      tc_st16(sa + half * 16, pk);                 // the weights stand where scores were
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(&bars.p[j & 1]);
@@ -357,19 +369,21 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
 
     // ---- out: half of the columns each ----
     if (ok && n > 0) ok = tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
-    ok = pair_or(bar_id, 0, ok) < 2;
+    ok = TC_TPR == 2 ? pair_or(bar_id, 0, ok) < 2 : __all_sync(FULL, ok);
     tc_fence_after();
     if (ok) {
-      xch[half][r] = l;
-      named_sync(bar_id, 64);
-      l += xch[half ^ 1][r];
+      if (TC_TPR == 2) {
+        xch[half][r] = l;
+        named_sync(bar_id, 64);
+        l += xch[half ^ 1][r];
+      }
       const int rho = rows0 + r;
       const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
       uint16_t* out = a.io.o + static_cast<int64_t>(b * a.W + w) * a.io.o_row + i * a.io.o_tok + (h * a.G + gq) * a.io.o_head;
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int c0 = 0; c0 < DP / 2; c0 += 32) {
-        const int c = half * (DP / 2) + c0;
+      for (int c0 = 0; c0 < DP / TC_TPR; c0 += 32) {
+        const int c = half * (DP / TC_TPR) + c0;
         float o[32];
         __syncwarp();
         if (n > 0) {
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       }
     }
     tc_fence_before();
-  } else if (wid == 8) {
+  } else if (wid == TC_SW) {
     // ---- K and V: one lane, each operand as far ahead as its stages go ----
     if (lane == 0) {
       int jk = 0, jv = 0;
@@ -471,7 +485,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   }
   __syncthreads();
   tc_fence_after();
-  if (wid == 9)
+  if (wid == TC_SW + 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(TC_COLS) : "memory");
 }
 
