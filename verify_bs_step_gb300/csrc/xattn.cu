@@ -6,7 +6,7 @@
 namespace vbs {
 
 int launch_xattn(const EncKV& e, const QO& io, float* part, int* arrived, int num_sms, cudaStream_t s) {
-  if (xattn_tc_takes(e, io, num_sms)) return launch_xattn_tc(e, io, s);
+  if (xattn_tc_takes(e, io, num_sms)) return launch_xattn_tc(e, io, num_sms, s);
   const EncSrc src{e};
   const SplitArgs sa = split_args(io, e.B, e.W, e.H, e.D, part, arrived);
   const bool aligned = ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 &&

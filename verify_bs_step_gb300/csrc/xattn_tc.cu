@@ -3,8 +3,7 @@
 // A CTA takes 128 of the query rows that share one sentence's K/V head (token by token, the heads of a
 // group side by side) over all of the sentence's positions, TC_N at a time:
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, two buffers;
-//   softmax       eight warps, two threads a row, half of the tile's positions each: S from TMEM to registers,
-//                 weights back to TMEM as bf16;
+//   softmax       four warps, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes (positions are the contraction,
 //                 so V is the transposed operand), O in TMEM.
 // One warp brings K and V in by TMA (128-byte swizzle, zeros past head_dim and past the tensor's end), one
@@ -30,10 +29,9 @@ namespace vbs {
 constexpr int TC_M = 128;                 // query rows a CTA
 constexpr int TC_N = 64;                  // positions a tile
 constexpr int TC_STMAX = 4;               // stages of K, and of V, at most
-constexpr int TC_TPR = 1;                 // softmax threads a row
-constexpr int TC_SM = TC_M * TC_TPR;
+constexpr int TC_SM = 128;                // softmax threads: one a row
 constexpr int TC_SW = TC_SM / 32;         // softmax warps
-constexpr int TC_C = TC_N / TC_TPR;       // scores of a thread in a tile
+constexpr int TC_SORT = 1024;             // sentences that are put in order of length
 constexpr int TC_NT = TC_SM + 64;         // and a load warp, a product warp
 constexpr int TC_COLS = 256;              // TMEM columns: S (2 x TC_N) and O (up to 128)
 constexpr u32 TC_SPIN = 1u << 20;         // bound of a wait, in tries
@@ -42,7 +40,8 @@ struct TcArgs {
   QO io;
   const int32_t* len;
   int* status;
-  int S, W, H, D, G, M;
+  int S, B, W, H, D, G, M;
+  int tiles;                              // of TC_M rows
   bool q16, out16;                        // 16-byte loads of q, stores of out
 };
 
@@ -145,8 +144,16 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* b
 // Two of s, p and pv, in turn: who waits for a tile's phase knows that the one before the last is over, so
 // that a barrier stands in the phase waited for or in the next, and its parity tells them apart.
 struct TcBars {
-  u64 q, kf[TC_STMAX], ke[TC_STMAX], vf[TC_STMAX], ve[TC_STMAX], s[2], p[2], pv[2];
+  u64 q, qe, of, kf[TC_STMAX], ke[TC_STMAX], vf[TC_STMAX], ve[TC_STMAX], s[2], p[2], pv[2];
 };
+
+// Whether a phase is over, without waiting (try_wait may hold the thread for a while).
+__device__ __forceinline__ bool mbar_test(u64* bar, u32 parity) {
+  u32 ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
 
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -166,19 +173,11 @@ __device__ __forceinline__ bool tc_wait(u64* bar, u32 parity, volatile int* gone
   return false;
 }
 
-// Among the 64 threads of two warps that share rows: 0 (no one moves), 1 (some do), 2 (a wait gave up).
-__device__ __forceinline__ int pair_or(int id, int move, bool ok) {
-  int r;
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .u32 m, g;\n\t"
-               "setp.ne.s32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 m, 1, 0, q;\n\t"
-               "mov.u32 %0, m;\n\t}" : "=r"(r) : "r"(id), "r"(ok ? move : 1) : "memory");
-  if (r) {
-    int e;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\t"
-                 "selp.u32 %0, 2, 0, q;\n\t}" : "=r"(e) : "r"(id), "r"(ok ? 0 : 1) : "memory");
-    r |= e;
-  }
-  return r;
+// The t-th item of this CTA, or -1: items are the sentences' (head, row tile) pairs, longest sentences first;
+// the CTAs take them in turn, back and forth, so that every CTA gets long and short ones.
+__device__ __forceinline__ int64_t item_of(int t, int64_t items) {
+  const int64_t i = static_cast<int64_t>(t) * gridDim.x + (t & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  return i < items ? i : -1;
 }
 
 template <int DP>
@@ -190,22 +189,17 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   __shared__ __align__(8) TcBars bars;
   __shared__ u32 tmem_base;
   __shared__ volatile int gone;
-  __shared__ float xch[2][TC_M];                           // what the two threads of a row tell each other
+  __shared__ uint16_t order[TC_SORT];                     // sentences, longest first
+  __shared__ int64_t q_at[TC_M];                          // element offsets of the item's query rows, -1: none
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = tc_smem_raw + ((1024 - (smem_u32(tc_smem_raw) & 1023)) & 1023);
   const u32 q_a = smem_u32(smem), k_a = q_a + C::QB, v_a = k_a + ST * C::TB;
 
-  const int rows0 = blockIdx.x * TC_M, h = blockIdx.y, b = blockIdx.z;
-  int len = a.len[b];
-  if (len < 0 || len > a.S) {
-    if (tid == 0) set_status(a.status, VBS_EINVAL);
-    len = len < 0 ? 0 : a.S;
-  }
-  const int n = (len + TC_N - 1) / TC_N;
-
   if (tid == 0) {
-    mbar_init(&bars.q, TC_SM);
+    mbar_init(&bars.q, 32);
+    mbar_init(&bars.qe, 1);
+    mbar_init(&bars.of, TC_SM);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
       mbar_init(&bars.ke[i], 1);
@@ -225,261 +219,336 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  const bool sorted = a.B > 1 && a.B <= TC_SORT;
+  if (sorted)
+    for (int x = tid; x < a.B; x += TC_NT) {
+      const int mine = a.len[x];
+      int rank = 0;
+      for (int y = 0; y < a.B; ++y) {
+        const int other = a.len[y];
+        rank += other > mine || (other == mine && y < x) ? 1 : 0;
+      }
+      order[rank] = static_cast<uint16_t>(x);
+    }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * TC_N;
 
-  if (wid < TC_SW) {
-    // ---- Q, its sign turned for a negative scale ----
-    const u32 flip = a.io.scale < 0.f ? 0x80008000u : 0u;
-    for (int idx = tid; idx < TC_M * (DP / 8); idx += TC_SM) {
-      const int r = idx / (DP / 8), c = idx % (DP / 8), rho = rows0 + r;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (rho < a.M && c * 8 < a.D) {
-        const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
-        const uint16_t* q = a.io.q + static_cast<int64_t>(b * a.W + w) * a.io.q_row + i * a.io.q_tok +
-                            (h * a.G + gq) * a.io.q_head + c * 8;
-        if (a.q16) {
-          x = *reinterpret_cast<const uint4*>(q);
-        } else {
-          x.x = q[0] | static_cast<u32>(q[1]) << 16;
-          x.y = q[2] | static_cast<u32>(q[3]) << 16;
-          x.z = q[4] | static_cast<u32>(q[5]) << 16;
-          x.w = q[6] | static_cast<u32>(q[7]) << 16;
-        }
-        x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
-      }
-      *reinterpret_cast<uint4*>(smem + (c >> 3) * (TC_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+  struct Item { int b, h, rows0, len, n; };
+  const int64_t items = static_cast<int64_t>(a.B) * a.H * a.tiles;
+  auto item_at = [&](int64_t i) {
+    Item it;
+    it.rows0 = static_cast<int>(i % a.tiles) * TC_M;
+    const int64_t bh = i / a.tiles;
+    it.h = static_cast<int>(bh % a.H);
+    const int x = static_cast<int>(bh / a.H);
+    it.b = sorted ? order[x] : x;
+    it.len = a.len[it.b];
+    if (it.len < 0 || it.len > a.S) {
+      set_status(a.status, VBS_EINVAL);
+      it.len = it.len < 0 ? 0 : a.S;
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive(&bars.q);
+    it.n = (it.len + TC_N - 1) / TC_N;
+    return it;
+  };
 
-    // ---- softmax ----
-    const int half = wid >> 2, r = tid & 127, bar_id = 1 + (wid & 3);
-    const u32 row = static_cast<u32>((wid & 3) * 32) << 16;
+  if (wid < TC_SW) {
+    // ---- softmax: thread = row ----
+    const u32 row = static_cast<u32>(wid * 32) << 16;
+    const bool neg = a.io.scale < 0.f;
     // (a scale of 0 stays above it, so that a masked -inf stays one)
     const float sc = fmaxf(fabsf(a.io.scale) * LOG2E_F, 1.17549435e-38f);
-    float m = -INFINITY, l = 0.f;                  // the reference (in scaled units), the sum of this half's weights
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = tc_wait(&bars.s[j & 1], (j >> 1) & 1, &gone, a.status);
-      tc_fence_after();
-      const u32 sa = tm_s + (j & 1) * TC_N + row;
-      float s[TC_C];
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < TC_C; c += 32) tc_ld32(sa + half * TC_C + c, s + c);
-      tc_wait_ld();
-      const int left = len - j * TC_N - half * TC_C;
-      if (left < TC_C) {                             // the sentence ends in this tile
-#pragma unroll
-        for (int i = 0; i < TC_C; ++i)
-          if (i >= left) s[i] = -INFINITY;
-      }
-      float top[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
-#pragma unroll
-      for (int i = 8; i < TC_C; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
-      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]) * sc;
-      bool grow = mx > m + 8.f;                    // also in the first tile: m = -inf
-      float both = mx;
-      int vote;
-      if (TC_TPR == 2) {
-        // both threads of a row have their scores now (the weights go over them), and agree on whether
-        // a reference moves in either warp; a warp whose wait gave up ends both
-        tc_fence_before();
-        vote = pair_or(bar_id, grow, ok);
+    int T = 0;                                     // tiles so far: all barriers count on across items
+    for (int t = 0; ok; ++t) {
+      const int64_t ii = item_of(t, items);
+      if (ii < 0) break;
+      const Item it = item_at(ii);
+      float m = -INFINITY, l = 0.f;                // the reference (in scaled units), the sum of weights
+      for (int j = 0; j < it.n; ++j, ++T) {
+        ok = tc_wait(&bars.s[T & 1], (T >> 1) & 1, &gone, a.status);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
         tc_fence_after();
-      } else {
-        vote = !__all_sync(FULL, ok) ? 2 : __any_sync(FULL, grow);
-      }
-      ok = vote < 2;
-      if (!ok) break;
-      if (vote) {
-        if (TC_TPR == 2) {
-          xch[half][r] = mx;
-          named_sync(bar_id, 64);
-          both = fmaxf(mx, xch[half ^ 1][r]);
-          grow = both > m + 8.f;
+        const u32 sa = tm_s + (T & 1) * TC_N + row;
+        float s[TC_N];
+        tc_ld32(sa, s);
+        tc_ld32(sa + 32, s + 32);
+        tc_wait_ld();
+        if (neg) {
+#pragma unroll
+          for (int i = 0; i < TC_N; ++i) s[i] = -s[i];
         }
-        const float to = grow ? both : m;
-        const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
-        if (j > 0) {                               // O holds the tiles before: half of its columns each
-          ok = tc_wait(&bars.pv[(j - 1) & 1], ((j - 1) >> 1) & 1, &gone, a.status);
-          tc_fence_after();
-          __syncwarp();
+        const int left = it.len - j * TC_N;
+        if (left < TC_N) {                         // the sentence ends in this tile
 #pragma unroll
-          for (int c = 0; c < DP / TC_TPR; c += 16) {
-            float o[16];
-            tc_ld16(tm_o + row + half * (DP / TC_TPR) + c, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
-            tc_st16(tm_o + row + half * (DP / TC_TPR) + c, o);
-          }
+          for (int i = 0; i < TC_N; ++i)
+            if (i >= left) s[i] = -INFINITY;
         }
-        l *= corr;
-        m = to;
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      // scale and reference go into one fma, whose product is not rounded as the reference was: for
-      // large scores the difference is more than a weight can bear, and the product is rounded first
-      float f = sc;
-      if (__any_sync(FULL, fabsf(ref) > 65536.f)) {
+        float top[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
 #pragma unroll
-        for (int i = 0; i < TC_C; ++i) s[i] *= sc;
-        f = 1.f;
-      }
-      u64 sum[2] = {0, 0};
-      const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
+        for (int i = 8; i < TC_N; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
+        const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]) * sc;
+        const bool grow = mx > m + 8.f;            // also in the first tile: m = -inf
+        if (__any_sync(FULL, grow)) {
+          const float to = grow ? mx : m;
+          const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
+          if (j > 0) {                             // O holds the tiles before
+            ok = tc_wait(&bars.pv[(T - 1) & 1], ((T - 1) >> 1) & 1, &gone, a.status);
+            ok = __all_sync(FULL, ok);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < TC_C; c += 32) {
-        float pk[16];
+            for (int c = 0; c < DP; c += 16) {
+              float o[16];
+              tc_ld16(tm_o + row + c, o);
+              tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x, y;
-          unpair(fma2(pair(s[c + 2 * i], s[c + 2 * i + 1]), f2, r2), x, y);
-          x = ex2(x);
-          y = ex2(y);
-          sum[i & 1] = add2(sum[i & 1], pair(x, y));
-          __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
-          pk[i] = *reinterpret_cast<float*>(&p);
-        }
-        tc_st16(sa + half * (TC_C / 2) + c / 2, pk);   // the weights stand where scores were
-      }
-      float l0, l1;
-      unpair(add2(sum[0], sum[1]), l0, l1);
-      l += l0 + l1;
-      if (len - j * TC_N < TC_N) {
-        // positions past the end: their weights are 0, and V's rows have to be finite
-        const int st = j % ST, from = len - j * TC_N;
-        ok = tc_wait(&bars.vf[st], (j / ST) & 1, &gone, a.status);
-        for (int x = tid; x < (TC_N - from) * 8 * C::SLABS; x += TC_SM) {
-          const int c = x & 7, vr = from + (x >> 3) % (TC_N - from), sl = (x >> 3) / (TC_N - from);
-          *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + vr * 128 + c * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      }
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars.p[j & 1]);
-    }
-
-    // ---- out: half of the columns each ----
-    if (ok && n > 0) ok = tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
-    ok = TC_TPR == 2 ? pair_or(bar_id, 0, ok) < 2 : __all_sync(FULL, ok);
-    tc_fence_after();
-    if (ok) {
-      if (TC_TPR == 2) {
-        xch[half][r] = l;
-        named_sync(bar_id, 64);
-        l += xch[half ^ 1][r];
-      }
-      const int rho = rows0 + r;
-      const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
-      uint16_t* out = a.io.o + static_cast<int64_t>(b * a.W + w) * a.io.o_row + i * a.io.o_tok + (h * a.G + gq) * a.io.o_head;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int c0 = 0; c0 < DP / TC_TPR; c0 += 32) {
-        const int c = half * (DP / TC_TPR) + c0;
-        float o[32];
-        __syncwarp();
-        if (n > 0) {
-          tc_ld32(tm_o + row + c, o);
-          tc_wait_ld();
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          if (rho >= a.M || c + k >= a.D) continue;
-          u32 x[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const __nv_bfloat162 p = n > 0 ? __floats2bfloat162_rn(o[k + 2 * y] * inv, o[k + 2 * y + 1] * inv)
-                                           : __floats2bfloat162_rn(0.f, 0.f);
-            x[y] = *reinterpret_cast<const u32*>(&p);
-          }
-          if (a.out16) {
-            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(x[0], x[1], x[2], x[3]);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              out[c + k + 2 * y] = static_cast<uint16_t>(x[y]);
-              out[c + k + 2 * y + 1] = static_cast<uint16_t>(x[y] >> 16);
+              for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
+              tc_st16(tm_o + row + c, o);
             }
           }
+          l *= corr;
+          m = to;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        // scale and reference go into one fma, whose product is not rounded as the reference was: for
+        // large scores the difference is more than a weight can bear, and the product is rounded first
+        float f = sc;
+        if (__any_sync(FULL, fabsf(ref) > 65536.f)) {
+#pragma unroll
+          for (int i = 0; i < TC_N; ++i) s[i] *= sc;
+          f = 1.f;
+        }
+        u64 sum[2] = {0, 0};
+        const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
+#pragma unroll
+        for (int c = 0; c < TC_N; c += 32) {
+          float pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpair(fma2(pair(s[c + 2 * i], s[c + 2 * i + 1]), f2, r2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[i & 1] = add2(sum[i & 1], pair(x, y));
+            __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+            pk[i] = *reinterpret_cast<float*>(&p);
+          }
+          tc_st16(sa + c / 2, pk);                 // the weights stand where scores were
+        }
+        float l0, l1;
+        unpair(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+        if (left < TC_N) {
+          // positions past the end: their weights are 0, and V's rows have to be finite
+          const int st = T % ST;
+          ok = tc_wait(&bars.vf[st], (T / ST) & 1, &gone, a.status);
+          for (int x = tid; x < (TC_N - left) * 8 * C::SLABS; x += TC_SM) {
+            const int c = x & 7, vr = left + (x >> 3) % (TC_N - left), sl = (x >> 3) / (TC_N - left);
+            *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + vr * 128 + c * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p[T & 1]);
+      }
+      if (ok && it.n > 0) ok = tc_wait(&bars.pv[(T - 1) & 1], ((T - 1) >> 1) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+      tc_fence_after();
+
+      // ---- out ----
+      const int rho = it.rows0 + tid;
+      const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
+      uint16_t* out = a.io.o + static_cast<int64_t>(it.b * a.W + w) * a.io.o_row + i * a.io.o_tok +
+                      (it.h * a.G + gq) * a.io.o_head;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      u32 x[DP / 2];
+#pragma unroll
+      for (int c = 0; c < DP; c += 16) {
+        float o[16];
+        if (it.n > 0) {
+          tc_ld16(tm_o + row + c, o);
+          tc_wait_ld();
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const __nv_bfloat162 p = it.n > 0 ? __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv) : __floats2bfloat162_rn(0.f, 0.f);
+          x[(c + k) / 2] = *reinterpret_cast<const u32*>(&p);
         }
       }
+      if (it.n > 0) {
+        tc_fence_before();
+        mbar_arrive(&bars.of);                     // O may be written again
+      }
+      if (rho < a.M) {
+#pragma unroll
+        for (int c = 0; c < DP; c += 8) {
+          if (c >= a.D) break;
+          if (a.out16) {
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(x[c / 2], x[c / 2 + 1], x[c / 2 + 2], x[c / 2 + 3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[c + k] = static_cast<uint16_t>(x[c / 2 + k / 2] >> (k & 1 ? 16 : 0));
+          }
+        }
+      }
+      __syncwarp();
     }
     tc_fence_before();
   } else if (wid == TC_SW) {
-    // ---- K and V: one lane, each operand as far ahead as its stages go ----
-    if (lane == 0) {
+    // ---- loads: Q by the whole warp, K and V by one lane, each as far ahead as its stages go ----
+    int T0 = 0, done = 0;                          // tiles before this item; items with tiles so far
+    bool ok = true;
+    for (int t = 0; ok; ++t) {
+      const int64_t ii = item_of(t, items);
+      if (ii < 0) break;
+      const Item it = item_at(ii);
+      if (it.n == 0) continue;
+      ok = done == 0 || tc_wait(&bars.qe, (done - 1) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+      // where the rows stand (four a lane, divided out once), then 16 bytes of them at a time
+      for (int r = lane; r < TC_M; r += 32) {
+        const int rho = it.rows0 + r;
+        const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
+        q_at[r] = rho < a.M ? static_cast<int64_t>(it.b * a.W + w) * a.io.q_row + i * a.io.q_tok + (it.h * a.G + gq) * a.io.q_head
+                            : -1;
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int idx = lane; idx < TC_M * (DP / 8); idx += 32) {
+        const int r = idx / (DP / 8), c = idx % (DP / 8);
+        const int64_t at = q_at[r];
+        const bool live = at >= 0 && c * 8 < a.D;
+        const uint16_t* q = live ? a.io.q + at + c * 8 : a.io.q;
+        const u32 to = (c >> 3) * (TC_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        if (a.q16) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_a + to), "l"(q), "r"(live ? 16 : 0) : "memory");
+        } else {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) {
+            x.x = q[0] | static_cast<u32>(q[1]) << 16;
+            x.y = q[2] | static_cast<u32>(q[3]) << 16;
+            x.z = q[4] | static_cast<u32>(q[5]) << 16;
+            x.w = q[6] | static_cast<u32>(q[7]) << 16;
+          }
+          *reinterpret_cast<uint4*>(smem + to) = x;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
       int jk = 0, jv = 0;
-      for (u32 idle = 0; (jk < n || jv < n) && idle < TC_SPIN && !gone;) {
-        bool moved = false;
-        if (jk < n && (jk < ST || mbar_wait(&bars.ke[jk % ST], ((jk / ST) & 1) ^ 1, 1))) {
-          const int st = jk % ST;
-          mbar_expect_tx(&bars.kf[st], C::TB);
-          for (int x = 0; x < C::SLABS; ++x)
-            tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, jk * TC_N, h, b);
-          ++jk;
-          moved = true;
+      auto feed = [&](int most) {                  // loads tiles until `most` of each are on their way
+        for (u32 idle = 0; (jk < most || jv < most) && idle < TC_SPIN && !gone;) {
+          bool moved = false;
+          if (jk < most) {
+            const int T = T0 + jk, st = T % ST;
+            if (T < ST || mbar_test(&bars.ke[st], ((T / ST) & 1) ^ 1)) {
+              mbar_expect_tx(&bars.kf[st], C::TB);
+              for (int x = 0; x < C::SLABS; ++x)
+                tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, jk * TC_N, it.h, it.b);
+              ++jk;
+              moved = true;
+            }
+          }
+          if (jv < most) {
+            const int T = T0 + jv, st = T % ST;
+            if (T < ST || mbar_test(&bars.ve[st], ((T / ST) & 1) ^ 1)) {
+              mbar_expect_tx(&bars.vf[st], C::TB);
+              for (int x = 0; x < C::SLABS; ++x)
+                tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, jv * TC_N, it.h, it.b);
+              ++jv;
+              moved = true;
+            }
+          }
+          idle = moved ? 0 : idle + 1;
         }
-        if (jv < n && (jv < ST || mbar_wait(&bars.ve[jv % ST], ((jv / ST) & 1) ^ 1, 1))) {
-          const int st = jv % ST;
-          mbar_expect_tx(&bars.vf[st], C::TB);
-          for (int x = 0; x < C::SLABS; ++x)
-            tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, jv * TC_N, h, b);
-          ++jv;
-          moved = true;
+        if ((jk < most || jv < most) && !gone) {
+          gone = 1;
+          set_status(a.status, VBS_ETIMEOUT);
         }
-        idle = moved ? 0 : idle + 1;
+        return jk >= most && jv >= most;
+      };
+      // the first K goes out before Q is waited for (its stage is free: the product that read it is done)
+      if (lane == 0 && (T0 < ST || mbar_test(&bars.ke[T0 % ST], ((T0 / ST) & 1) ^ 1))) {
+        const int st = T0 % ST;
+        mbar_expect_tx(&bars.kf[st], C::TB);
+        for (int x = 0; x < C::SLABS; ++x)
+          tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, 0, it.h, it.b);
+        jk = 1;
       }
-      if ((jk < n || jv < n) && !gone) {
-        gone = 1;
-        set_status(a.status, VBS_ETIMEOUT);
+      __syncwarp();
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&bars.q);
+      if (lane == 0) ok = feed(it.n);
+      ok = __all_sync(FULL, ok);
+      if (!ok && lane == 0) {                      // given up: the copies on their way land first
+        for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
+        for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
       }
-      // no copy is in flight when the CTA ends: the last ones have landed
-      for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[j % ST], (j / ST) & 1, 1u << 16);
-      for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[j % ST], (j / ST) & 1, 1u << 16);
+      T0 += it.n;
+      ++done;
     }
+    // no copy is in flight when the CTA ends: the last ones have landed
+    if (ok && lane == 0)
+      for (int j = max(0, T0 - ST); j < T0; ++j) {
+        mbar_wait(&bars.kf[j % ST], (j / ST) & 1, 1u << 16);
+        mbar_wait(&bars.vf[j % ST], (j / ST) & 1, 1u << 16);
+      }
   } else {
     // ---- products: one elected thread waits and issues ----
     if (elect_one()) {
       const u64 dq = tc_desc(q_a, 16), dk = tc_desc(k_a, 16), dv = tc_desc(v_a, TC_N * 128);
-      auto scores = [&](int j) {
-        const int st = j % ST;
-        if (!tc_wait(&bars.kf[st], (j / ST) & 1, &gone, a.status)) return false;
-        tc_fence_after();
-        const u64 d = dk + static_cast<u64>(st * (C::TB >> 4));
+      int T = 0, done = 0;
+      bool ok = true;
+      for (int t = 0; ok; ++t) {
+        const int64_t ii = item_of(t, items);
+        if (ii < 0) break;
+        const Item it = item_at(ii);
+        if (it.n == 0) continue;
+        auto scores = [&](int j) {                 // S of the item's tile j
+          const int X = T + j, st = X % ST;
+          if (!tc_wait(&bars.kf[st], (X / ST) & 1, &gone, a.status)) return false;
+          tc_fence_after();
+          const u64 d = dk + static_cast<u64>(st * (C::TB >> 4));
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k)
-          tc_mma_ss(tm_s + (j & 1) * TC_N, dq + (((k >> 2) * (TC_M * 128) + (k & 3) * 32) >> 4),
-                    d + (((k >> 2) * (TC_N * 128) + (k & 3) * 32) >> 4), tc_idesc(TC_N, false), k > 0);
-        tc_commit(&bars.s[j & 1]);
-        tc_commit(&bars.ke[st]);
-        return true;
-      };
-      bool ok = n > 0 && tc_wait(&bars.q, 0, &gone, a.status) && scores(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) ok = scores(j + 1);
-        const int st = j % ST;
-        ok = ok && tc_wait(&bars.vf[st], (j / ST) & 1, &gone, a.status);
-        ok = ok && tc_wait(&bars.p[j & 1], (j >> 1) & 1, &gone, a.status);
-        if (!ok) break;
-        tc_fence_after();
-        const u64 d = dv + static_cast<u64>(st * (C::TB >> 4));
+          for (int k = 0; k < DP / 16; ++k)
+            tc_mma_ss(tm_s + (X & 1) * TC_N, dq + (((k >> 2) * (TC_M * 128) + (k & 3) * 32) >> 4),
+                      d + (((k >> 2) * (TC_N * 128) + (k & 3) * 32) >> 4), tc_idesc(TC_N, false), k > 0);
+          tc_commit(&bars.s[X & 1]);
+          tc_commit(&bars.ke[st]);
+          if (j + 1 == it.n) tc_commit(&bars.qe);  // Q may be loaded again
+          return true;
+        };
+        ok = tc_wait(&bars.q, done & 1, &gone, a.status) && scores(0);
+        // the item before has read its O
+        ok = ok && (done == 0 || tc_wait(&bars.of, (done - 1) & 1, &gone, a.status));
+        for (int j = 0; j < it.n && ok; ++j) {
+          if (j + 1 < it.n) ok = scores(j + 1);
+          const int X = T + j, st = X % ST;
+          ok = ok && tc_wait(&bars.vf[st], (X / ST) & 1, &gone, a.status);
+          ok = ok && tc_wait(&bars.p[X & 1], (X >> 1) & 1, &gone, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const u64 d = dv + static_cast<u64>(st * (C::TB >> 4));
 #pragma unroll
-        for (int k = 0; k < TC_N / 16; ++k)
-          tc_mma_ts(tm_o, tm_s + (j & 1) * TC_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true), j > 0 || k > 0);
-        tc_commit(&bars.pv[j & 1]);
-        tc_commit(&bars.ve[st]);
+          for (int k = 0; k < TC_N / 16; ++k)
+            tc_mma_ts(tm_o, tm_s + (X & 1) * TC_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true), j > 0 || k > 0);
+          tc_commit(&bars.pv[X & 1]);
+          tc_commit(&bars.ve[st]);
+        }
+        T += it.n;
+        ++done;
       }
       // the products in flight read shared memory and TMEM: the last one is done before either goes
-      if (ok && n > 0) tc_wait(&bars.pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &gone, a.status);
+      if (ok && T > 0) tc_wait(&bars.pv[(T - 1) & 1], ((T - 1) >> 1) & 1, &gone, a.status);
     }
     __syncwarp();
   }
@@ -538,23 +607,24 @@ bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
 }
 
 template <int DP>
-static int launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const TcArgs& a, int B, cudaStream_t s) {
+static int launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const TcArgs& a, int num_sms, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   if (!smem_attr_once(xattn_tc_kernel<DP>, static_cast<int>(TcCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
-  const dim3 grid((a.M + TC_M - 1) / TC_M, a.H, B);
+  const int64_t items = static_cast<int64_t>(a.B) * a.H * a.tiles;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, 2 * num_sms));
   xattn_tc_kernel<DP><<<grid, TC_NT, TcCfg<DP>::SMEM, s>>>(km, vm, a);
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
-int launch_xattn_tc(const EncKV& e, const QO& io, cudaStream_t s) {
+int launch_xattn_tc(const EncKV& e, const QO& io, int num_sms, cudaStream_t s) {
   CUtensorMap km, vm;
   if (!encode(&km, e.k, e, e.k_sent, e.k_pos, e.k_head) || !encode(&vm, e.v, e, e.v_sent, e.v_pos, e.v_head)) return VBS_ECUDA;
   auto eights = [](const void* p, int64_t r, int64_t t, int64_t h) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (r | t | h) % 8 == 0;
   };
-  const TcArgs a{io, e.len, e.status, e.S, e.W, e.H, e.D, io.Hq / e.H, e.W * io.n_q * (io.Hq / e.H),
+  const TcArgs a{io, e.len, e.status, e.S, e.B, e.W, e.H, e.D, io.Hq / e.H, e.W * io.n_q * (io.Hq / e.H), (e.W * io.n_q * (io.Hq / e.H) + TC_M - 1) / TC_M,
                  eights(io.q, io.q_row, io.q_tok, io.q_head), eights(io.o, io.o_row, io.o_tok, io.o_head)};
-  return e.D <= 64 ? launch_tc<64>(km, vm, a, e.B, s) : launch_tc<128>(km, vm, a, e.B, s);
+  return e.D <= 64 ? launch_tc<64>(km, vm, a, num_sms, s) : launch_tc<128>(km, vm, a, num_sms, s);
 }
 
 }  // namespace vbs

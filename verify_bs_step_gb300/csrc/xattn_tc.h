@@ -7,6 +7,6 @@ namespace vbs {
 
 // Whether the tiles take this call: enough rows, and K and V that TMA can read.
 bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms);
-int launch_xattn_tc(const EncKV& e, const QO& io, cudaStream_t s);
+int launch_xattn_tc(const EncKV& e, const QO& io, int num_sms, cudaStream_t s);
 
 }  // namespace vbs
