@@ -141,10 +141,13 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* b
       ::"r"(dst), "l"(map), "r"(x), "r"(s), "r"(h), "r"(b), "r"(smem_u32(bar)) : "memory");
 }
 
-// Two of s, p and pv, in turn: who waits for a tile's phase knows that the one before the last is over, so
-// that a barrier stands in the phase waited for or in the next, and its parity tells them apart.
+// Rings of barriers: kf, vf (a tile's K or V has landed), s (its scores are done: so its K stage is free) and pv
+// (its products are in O: so its V stage is free), one per stage, and two of p (its weights are written).  Who waits
+// for a tile's phase knows that the ring's turn before it is over, so that a barrier stands in the phase
+// waited for or in the next, and its parity tells them apart.  q, qe, of: an item's Q has landed, is not read
+// any more, its O has been read.
 struct TcBars {
-  u64 q, qe, of, kf[TC_STMAX], ke[TC_STMAX], vf[TC_STMAX], ve[TC_STMAX], s[2], p[2], pv[2];
+  u64 q, qe, of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[2];
 };
 
 // Whether a phase is over, without waiting (try_wait may hold the thread for a while).
@@ -175,8 +178,8 @@ __device__ __forceinline__ bool tc_wait(u64* bar, u32 parity, volatile int* gone
 
 // The t-th item of this CTA, or -1: items are the sentences' (head, row tile) pairs, longest sentences first;
 // the CTAs take them in turn, back and forth, so that every CTA gets long and short ones.
-__device__ __forceinline__ int64_t item_of(int t, int64_t items) {
-  const int64_t i = static_cast<int64_t>(t) * gridDim.x + (t & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+__device__ __forceinline__ int item_of(int t, int items) {
+  const int i = t * gridDim.x + (t & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   return i < items ? i : -1;
 }
 
@@ -202,15 +205,11 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     mbar_init(&bars.of, TC_SM);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
-      mbar_init(&bars.ke[i], 1);
       mbar_init(&bars.vf[i], 1);
-      mbar_init(&bars.ve[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s[i], 1);
-      mbar_init(&bars.p[i], TC_SM);
       mbar_init(&bars.pv[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&bars.p[i], TC_SM);
     fence_mbar_init();
     gone = 0;
   }
@@ -235,14 +234,15 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * TC_N;
 
-  struct Item { int b, h, rows0, len, n; };
-  const int64_t items = static_cast<int64_t>(a.B) * a.H * a.tiles;
-  auto item_at = [&](int64_t i) {
-    Item it;
-    it.rows0 = static_cast<int>(i % a.tiles) * TC_M;
-    const int64_t bh = i / a.tiles;
-    it.h = static_cast<int>(bh % a.H);
-    const int x = static_cast<int>(bh / a.H);
+  struct Item { int b, h, rows0, len, n; };                // n: tiles of positions; b < 0: no more items
+  const int items = a.B * a.H * a.tiles;
+  auto item_at = [&](int t) {
+    Item it{-1, 0, 0, 0, 0};
+    const int i = item_of(t, items);
+    if (i < 0) return it;
+    const int bh = i / a.tiles, x = bh / a.H;
+    it.rows0 = (i - bh * a.tiles) * TC_M;
+    it.h = bh - x * a.H;
     it.b = sorted ? order[x] : x;
     it.len = a.len[it.b];
     if (it.len < 0 || it.len > a.S) {
@@ -261,13 +261,13 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     const float sc = fmaxf(fabsf(a.io.scale) * LOG2E_F, 1.17549435e-38f);
     bool ok = true;
     int T = 0;                                     // tiles so far: all barriers count on across items
-    for (int t = 0; ok; ++t) {
-      const int64_t ii = item_of(t, items);
-      if (ii < 0) break;
-      const Item it = item_at(ii);
+    Item next = item_at(0);
+    for (int t = 1; ok && next.b >= 0; ++t) {
+      const Item it = next;
+      next = item_at(t);
       float m = -INFINITY, l = 0.f;                // the reference (in scaled units), the sum of weights
       for (int j = 0; j < it.n; ++j, ++T) {
-        ok = tc_wait(&bars.s[T & 1], (T >> 1) & 1, &gone, a.status);
+        ok = tc_wait(&bars.s[T % ST], (T / ST) & 1, &gone, a.status);
         ok = __all_sync(FULL, ok);
         if (!ok) break;
         tc_fence_after();
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           const float to = grow ? mx : m;
           const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
           if (j > 0) {                             // O holds the tiles before
-            ok = tc_wait(&bars.pv[(T - 1) & 1], ((T - 1) >> 1) & 1, &gone, a.status);
+            ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
             ok = __all_sync(FULL, ok);
             if (!ok) break;
             tc_fence_after();
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         tc_fence_before();
         mbar_arrive(&bars.p[T & 1]);
       }
-      if (ok && it.n > 0) ok = tc_wait(&bars.pv[(T - 1) & 1], ((T - 1) >> 1) & 1, &gone, a.status);
+      if (ok && it.n > 0) ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
       ok = __all_sync(FULL, ok);
       if (!ok) break;
       tc_fence_after();
@@ -406,14 +406,10 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
     // ---- loads: Q by the whole warp, K and V by one lane, each as far ahead as its stages go ----
     int T0 = 0, done = 0;                          // tiles before this item; items with tiles so far
     bool ok = true;
-    for (int t = 0; ok; ++t) {
-      const int64_t ii = item_of(t, items);
-      if (ii < 0) break;
-      const Item it = item_at(ii);
+    for (int t = 0;; ++t) {
+      const Item it = item_at(t);
+      if (it.b < 0) break;
       if (it.n == 0) continue;
-      ok = done == 0 || tc_wait(&bars.qe, (done - 1) & 1, &gone, a.status);
-      ok = __all_sync(FULL, ok);
-      if (!ok) break;
       // where the rows stand (four a lane, divided out once), then 16 bytes of them at a time
       for (int r = lane; r < TC_M; r += 32) {
         const int rho = it.rows0 + r;
@@ -421,8 +417,10 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         q_at[r] = rho < a.M ? static_cast<int64_t>(it.b * a.W + w) * a.io.q_row + i * a.io.q_tok + (it.h * a.G + gq) * a.io.q_head
                             : -1;
       }
-      __syncwarp();
-#pragma unroll 4
+      ok = done == 0 || tc_wait(&bars.qe, (done - 1) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
+      if (!ok) break;
+#pragma unroll 8
       for (int idx = lane; idx < TC_M * (DP / 8); idx += 32) {
         const int r = idx / (DP / 8), c = idx % (DP / 8);
         const int64_t at = q_at[r];
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           bool moved = false;
           if (jk < most) {
             const int T = T0 + jk, st = T % ST;
-            if (T < ST || mbar_test(&bars.ke[st], ((T / ST) & 1) ^ 1)) {
+            if (T < ST || mbar_test(&bars.s[st], ((T / ST) & 1) ^ 1)) {
               mbar_expect_tx(&bars.kf[st], C::TB);
               for (int x = 0; x < C::SLABS; ++x)
                 tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, jk * TC_N, it.h, it.b);
@@ -459,7 +457,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           }
           if (jv < most) {
             const int T = T0 + jv, st = T % ST;
-            if (T < ST || mbar_test(&bars.ve[st], ((T / ST) & 1) ^ 1)) {
+            if (T < ST || mbar_test(&bars.pv[st], ((T / ST) & 1) ^ 1)) {
               mbar_expect_tx(&bars.vf[st], C::TB);
               for (int x = 0; x < C::SLABS; ++x)
                 tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, jv * TC_N, it.h, it.b);
@@ -476,7 +474,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         return jk >= most && jv >= most;
       };
       // the first K goes out before Q is waited for (its stage is free: the product that read it is done)
-      if (lane == 0 && (T0 < ST || mbar_test(&bars.ke[T0 % ST], ((T0 / ST) & 1) ^ 1))) {
+      if (lane == 0 && (T0 < ST || mbar_test(&bars.s[T0 % ST], ((T0 / ST) & 1) ^ 1))) {
         const int st = T0 % ST;
         mbar_expect_tx(&bars.kf[st], C::TB);
         for (int x = 0; x < C::SLABS; ++x)
@@ -495,6 +493,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       }
       T0 += it.n;
       ++done;
+      if (!ok) break;
     }
     // no copy is in flight when the CTA ends: the last ones have landed
     if (ok && lane == 0)
@@ -508,10 +507,10 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       const u64 dq = tc_desc(q_a, 16), dk = tc_desc(k_a, 16), dv = tc_desc(v_a, TC_N * 128);
       int T = 0, done = 0;
       bool ok = true;
-      for (int t = 0; ok; ++t) {
-        const int64_t ii = item_of(t, items);
-        if (ii < 0) break;
-        const Item it = item_at(ii);
+      Item next = item_at(0);
+      for (int t = 1; ok && next.b >= 0; ++t) {
+        const Item it = next;
+        next = item_at(t);
         if (it.n == 0) continue;
         auto scores = [&](int j) {                 // S of the item's tile j
           const int X = T + j, st = X % ST;
@@ -522,8 +521,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           for (int k = 0; k < DP / 16; ++k)
             tc_mma_ss(tm_s + (X & 1) * TC_N, dq + (((k >> 2) * (TC_M * 128) + (k & 3) * 32) >> 4),
                       d + (((k >> 2) * (TC_N * 128) + (k & 3) * 32) >> 4), tc_idesc(TC_N, false), k > 0);
-          tc_commit(&bars.s[X & 1]);
-          tc_commit(&bars.ke[st]);
+          tc_commit(&bars.s[st]);
           if (j + 1 == it.n) tc_commit(&bars.qe);  // Q may be loaded again
           return true;
         };
@@ -541,14 +539,13 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
 #pragma unroll
           for (int k = 0; k < TC_N / 16; ++k)
             tc_mma_ts(tm_o, tm_s + (X & 1) * TC_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true), j > 0 || k > 0);
-          tc_commit(&bars.pv[X & 1]);
-          tc_commit(&bars.ve[st]);
+          tc_commit(&bars.pv[st]);
         }
         T += it.n;
         ++done;
       }
       // the products in flight read shared memory and TMEM: the last one is done before either goes
-      if (ok && T > 0) tc_wait(&bars.pv[(T - 1) & 1], ((T - 1) >> 1) & 1, &gone, a.status);
+      if (ok && T > 0) tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
     }
     __syncwarp();
   }
@@ -594,7 +591,7 @@ static bool encode(CUtensorMap* map, const uint16_t* p, const EncKV& e, int64_t 
 
 bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
   const int64_t M = static_cast<int64_t>(e.W) * io.n_q * (io.Hq / e.H);
-  if (e.D > 128 || e.S < 1 || M < 64 || M >= (1 << 30) || e.H > 65535 || e.B > 65535) return false;
+  if (e.D > 128 || e.S < 1 || M < 64 || static_cast<double>(e.B) * e.H * M > 1e9) return false;
   // a CTA walks a sentence's positions alone; the split kernel shares them out
   const double tiles = static_cast<double>(e.B) * e.H * ((M + TC_M - 1) / TC_M), units = static_cast<double>(e.B) * e.H * ((M + 31) / 32);
   const double tc = (e.S + TC_N - 1) / TC_N * 0.55 * std::max(1.0, tiles / (2 * num_sms));
@@ -610,8 +607,7 @@ template <int DP>
 static int launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const TcArgs& a, int num_sms, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   if (!smem_attr_once(xattn_tc_kernel<DP>, static_cast<int>(TcCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
-  const int64_t items = static_cast<int64_t>(a.B) * a.H * a.tiles;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, 2 * num_sms));
+  const int grid = std::min(a.B * a.H * a.tiles, 2 * num_sms);
   xattn_tc_kernel<DP><<<grid, TC_NT, TcCfg<DP>::SMEM, s>>>(km, vm, a);
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
