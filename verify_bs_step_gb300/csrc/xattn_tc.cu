@@ -2,12 +2,12 @@
 //
 // A CTA takes 128 of the query rows that share one sentence's K/V head (token by token, the heads of a
 // group side by side) over all of the sentence's positions, TC_N at a time:
-//   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, two buffers;
+//   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, two or three buffers;
 //   softmax       four warps, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes (positions are the contraction,
 //                 so V is the transposed operand), O in TMEM.
 // One warp brings K and V in by TMA (128-byte swizzle, zeros past head_dim and past the tensor's end), one
-// issues the products: S of the next tile is issued before it waits for the weights of this one.
+// issues the products: S of the tiles ahead is issued before it waits for the weights of this one.
 //
 // The running reference of the softmax only moves when a row's maximum has grown by 2^8 (in the weights'
 // own units): until then weights up to 256 are as good in bf16 as weights up to 1, and O stays where it is.
@@ -33,7 +33,7 @@ constexpr int TC_SM = 128;                // softmax threads: one a row
 constexpr int TC_SW = TC_SM / 32;         // softmax warps
 constexpr int TC_SORT = 1024;             // sentences that are put in order of length
 constexpr int TC_NT = TC_SM + 64;         // and a load warp, a product warp
-constexpr int TC_COLS = 256;              // TMEM columns: S (2 x TC_N) and O (up to 128)
+constexpr int TC_COLS = 256;              // TMEM columns: S (3 x TC_N or 2 x TC_N) and O (64 or 128)
 constexpr u32 TC_SPIN = 1u << 20;         // bound of a wait, in tries
 
 struct TcArgs {
@@ -50,7 +50,9 @@ template <int DP> struct TcCfg {
   static constexpr int QB = SLABS * TC_M * 128;
   static constexpr int TB = SLABS * TC_N * 128;            // one tile of K or V
   static constexpr int ST = DP == 64 ? 4 : 2;              // stages: what two CTAs' shared memory holds
-  static constexpr size_t SMEM = QB + 2 * ST * TB + 1024;
+  static constexpr int NB = DP == 64 ? 3 : 2;              // S buffers, beside O in 256 TMEM columns
+  static constexpr int NQ = DP == 64 ? 2 : 1;              // Q buffers: the next item's rows come in early
+  static constexpr size_t SMEM = NQ * QB + 2 * ST * TB + 1024;
 };
 
 // ---- tcgen05 ----
@@ -142,12 +144,13 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* b
 }
 
 // Rings of barriers: kf, vf (a tile's K or V has landed), s (its scores are done: so its K stage is free) and pv
-// (its products are in O: so its V stage is free), one per stage, and two of p (its weights are written).  Who waits
+// (its products are in O: so its V stage is free), one per stage, and p (its weights are written),
+// one per S buffer.  Who waits
 // for a tile's phase knows that the ring's turn before it is over, so that a barrier stands in the phase
 // waited for or in the next, and its parity tells them apart.  q, qe, of: an item's Q has landed, is not read
 // any more, its O has been read.
 struct TcBars {
-  u64 q, qe, of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[2];
+  u64 q[2], qe[2], of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[3];
 };
 
 // Whether a phase is over, without waiting (try_wait may hold the thread for a while).
@@ -197,11 +200,13 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = tc_smem_raw + ((1024 - (smem_u32(tc_smem_raw) & 1023)) & 1023);
-  const u32 q_a = smem_u32(smem), k_a = q_a + C::QB, v_a = k_a + ST * C::TB;
+  const u32 q_a = smem_u32(smem), k_a = q_a + C::NQ * C::QB, v_a = k_a + ST * C::TB;
 
   if (tid == 0) {
-    mbar_init(&bars.q, 32);
-    mbar_init(&bars.qe, 1);
+    for (int i = 0; i < C::NQ; ++i) {
+      mbar_init(&bars.q[i], 32);
+      mbar_init(&bars.qe[i], 1);
+    }
     mbar_init(&bars.of, TC_SM);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       mbar_init(&bars.s[i], 1);
       mbar_init(&bars.pv[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&bars.p[i], TC_SM);
+    for (int i = 0; i < C::NB; ++i) mbar_init(&bars.p[i], TC_SM);
     fence_mbar_init();
     gone = 0;
   }
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * TC_N;
+  const u32 tm = tmem_base, tm_s = tm, tm_o = tm + C::NB * TC_N;
 
   struct Item { int b, h, rows0, len, n; };                // n: tiles of positions; b < 0: no more items
   const int items = a.B * a.H * a.tiles;
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         ok = __all_sync(FULL, ok);
         if (!ok) break;
         tc_fence_after();
-        const u32 sa = tm_s + (T & 1) * TC_N + row;
+        const u32 sa = tm_s + (T % C::NB) * TC_N + row;
         float s[TC_N];
         tc_ld32(sa, s);
         tc_ld32(sa + 32, s + 32);
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         }
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars.p[T & 1]);
+        mbar_arrive(&bars.p[T % C::NB]);
       }
       if (ok && it.n > 0) ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
       ok = __all_sync(FULL, ok);
@@ -417,7 +422,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         q_at[r] = rho < a.M ? static_cast<int64_t>(it.b * a.W + w) * a.io.q_row + i * a.io.q_tok + (it.h * a.G + gq) * a.io.q_head
                             : -1;
       }
-      ok = done == 0 || tc_wait(&bars.qe, (done - 1) & 1, &gone, a.status);
+      const int qb = done % C::NQ;
+      ok = done < C::NQ || tc_wait(&bars.qe[qb], (done / C::NQ - 1) & 1, &gone, a.status);
       ok = __all_sync(FULL, ok);
       if (!ok) break;
 #pragma unroll 8
@@ -426,7 +432,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         const int64_t at = q_at[r];
         const bool live = at >= 0 && c * 8 < a.D;
         const uint16_t* q = live ? a.io.q + at + c * 8 : a.io.q;
-        const u32 to = (c >> 3) * (TC_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        const u32 to = qb * C::QB + (c >> 3) * (TC_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
         if (a.q16) {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_a + to), "l"(q), "r"(live ? 16 : 0) : "memory");
         } else {
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         }
         return jk >= most && jv >= most;
       };
-      // the first K goes out before Q is waited for (its stage is free: the product that read it is done)
+      // the first K goes out before Q is waited for, where its stage is free
       if (lane == 0 && (T0 < ST || mbar_test(&bars.s[T0 % ST], ((T0 / ST) & 1) ^ 1))) {
         const int st = T0 % ST;
         mbar_expect_tx(&bars.kf[st], C::TB);
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       __syncwarp();
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&bars.q);
+      mbar_arrive(&bars.q[qb]);
       if (lane == 0) ok = feed(it.n);
       ok = __all_sync(FULL, ok);
       if (!ok && lane == 0) {                      // given up: the copies on their way land first
@@ -512,6 +518,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         const Item it = next;
         next = item_at(t);
         if (it.n == 0) continue;
+        const int qb = done % C::NQ;
+        const u64 dqi = dq + static_cast<u64>(qb * (C::QB >> 4));
         auto scores = [&](int j) {                 // S of the item's tile j
           const int X = T + j, st = X % ST;
           if (!tc_wait(&bars.kf[st], (X / ST) & 1, &gone, a.status)) return false;
@@ -519,26 +527,27 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           const u64 d = dk + static_cast<u64>(st * (C::TB >> 4));
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k)
-            tc_mma_ss(tm_s + (X & 1) * TC_N, dq + (((k >> 2) * (TC_M * 128) + (k & 3) * 32) >> 4),
+            tc_mma_ss(tm_s + (X % C::NB) * TC_N, dqi + (((k >> 2) * (TC_M * 128) + (k & 3) * 32) >> 4),
                       d + (((k >> 2) * (TC_N * 128) + (k & 3) * 32) >> 4), tc_idesc(TC_N, false), k > 0);
           tc_commit(&bars.s[st]);
-          if (j + 1 == it.n) tc_commit(&bars.qe);  // Q may be loaded again
+          if (j + 1 == it.n) tc_commit(&bars.qe[qb]);  // Q may be loaded again
           return true;
         };
-        ok = tc_wait(&bars.q, done & 1, &gone, a.status) && scores(0);
+        ok = tc_wait(&bars.q[qb], (done / C::NQ) & 1, &gone, a.status);
+        for (int j = 0; j < C::NB - 1 && j < it.n; ++j) ok = ok && scores(j);
         // the item before has read its O
         ok = ok && (done == 0 || tc_wait(&bars.of, (done - 1) & 1, &gone, a.status));
         for (int j = 0; j < it.n && ok; ++j) {
-          if (j + 1 < it.n) ok = scores(j + 1);
+          if (j + C::NB - 1 < it.n) ok = scores(j + C::NB - 1);
           const int X = T + j, st = X % ST;
           ok = ok && tc_wait(&bars.vf[st], (X / ST) & 1, &gone, a.status);
-          ok = ok && tc_wait(&bars.p[X & 1], (X >> 1) & 1, &gone, a.status);
+          ok = ok && tc_wait(&bars.p[X % C::NB], (X / C::NB) & 1, &gone, a.status);
           if (!ok) break;
           tc_fence_after();
           const u64 d = dv + static_cast<u64>(st * (C::TB >> 4));
 #pragma unroll
           for (int k = 0; k < TC_N / 16; ++k)
-            tc_mma_ts(tm_o, tm_s + (X & 1) * TC_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true), j > 0 || k > 0);
+            tc_mma_ts(tm_o, tm_s + (X % C::NB) * TC_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true), j > 0 || k > 0);
           tc_commit(&bars.pv[st]);
         }
         T += it.n;
