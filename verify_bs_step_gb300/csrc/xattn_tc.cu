@@ -153,14 +153,6 @@ struct TcBars {
   u64 q[2], qe[2], of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[3];
 };
 
-// Whether a phase is over, without waiting (try_wait may hold the thread for a while).
-__device__ __forceinline__ bool mbar_test(u64* bar, u32 parity) {
-  u32 ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   u32 r;
@@ -447,56 +439,31 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      // K and V by one lane, in turn, each waiting for its stage (asleep in try_wait: a loop of tests would
+      // keep the barriers from everyone else); the first K goes out before Q is waited for
       int jk = 0, jv = 0;
-      auto feed = [&](int most) {                  // loads tiles until `most` of each are on their way
-        for (u32 idle = 0; (jk < most || jv < most) && idle < TC_SPIN && !gone;) {
-          bool moved = false;
-          if (jk < most) {
-            const int T = T0 + jk, st = T % ST;
-            if (T < ST || mbar_test(&bars.s[st], ((T / ST) & 1) ^ 1)) {
-              mbar_expect_tx(&bars.kf[st], C::TB);
-              for (int x = 0; x < C::SLABS; ++x)
-                tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, jk * TC_N, it.h, it.b);
-              ++jk;
-              moved = true;
-            }
-          }
-          if (jv < most) {
-            const int T = T0 + jv, st = T % ST;
-            if (T < ST || mbar_test(&bars.pv[st], ((T / ST) & 1) ^ 1)) {
-              mbar_expect_tx(&bars.vf[st], C::TB);
-              for (int x = 0; x < C::SLABS; ++x)
-                tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, jv * TC_N, it.h, it.b);
-              ++jv;
-              moved = true;
-            }
-          }
-          idle = moved ? 0 : idle + 1;
-        }
-        if ((jk < most || jv < most) && !gone) {
-          gone = 1;
-          set_status(a.status, VBS_ETIMEOUT);
-        }
-        return jk >= most && jv >= most;
-      };
-      // the first K goes out before Q is waited for, where its stage is free
-      if (lane == 0 && (T0 < ST || mbar_test(&bars.s[T0 % ST], ((T0 / ST) & 1) ^ 1))) {
-        const int st = T0 % ST;
-        mbar_expect_tx(&bars.kf[st], C::TB);
+      auto load = [&](const CUtensorMap* map, u32 base, u64* full, u64* empty, int& j) {
+        const int T = T0 + j, st = T % ST;
+        if (T >= ST && !tc_wait(&empty[st], ((T / ST) & 1) ^ 1, &gone, a.status)) return false;
+        mbar_expect_tx(&full[st], C::TB);
         for (int x = 0; x < C::SLABS; ++x)
-          tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, 0, it.h, it.b);
-        jk = 1;
-      }
+          tma_load(base + st * C::TB + x * TC_N * 128, map, &full[st], x * 64, j * TC_N, it.h, it.b);
+        ++j;
+        return true;
+      };
+      if (lane == 0) ok = load(&kmap, k_a, bars.kf, bars.s, jk);
       __syncwarp();
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&bars.q[qb]);
-      if (lane == 0) ok = feed(it.n);
-      ok = __all_sync(FULL, ok);
-      if (!ok && lane == 0) {                      // given up: the copies on their way land first
-        for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
-        for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
+      if (lane == 0) {
+        while (ok && jv < it.n) ok = load(&vmap, v_a, bars.vf, bars.pv, jv) && (jk == it.n || load(&kmap, k_a, bars.kf, bars.s, jk));
+        if (!ok) {                                 // given up: the copies on their way land first
+          for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
+          for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
+        }
       }
+      ok = __all_sync(FULL, ok);
       T0 += it.n;
       ++done;
       if (!ok) break;
