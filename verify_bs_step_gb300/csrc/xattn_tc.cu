@@ -178,6 +178,13 @@ __device__ __forceinline__ int item_of(int t, int items) {
   return i < items ? i : -1;
 }
 
+// The same for a warp, by one of its lanes: 32 lanes on one barrier queue up behind one another.
+__device__ __forceinline__ bool tc_wait_warp(u64* bar, u32 parity, int lane, volatile int* gone, int* status) {
+  int ok = 1;
+  if (lane == 0) ok = tc_wait(bar, parity, gone, status);
+  return __shfl_sync(FULL, ok, 0) != 0;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                                                            const __grid_constant__ CUtensorMap vmap, const TcArgs a) {
@@ -196,17 +203,17 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
 
   if (tid == 0) {
     for (int i = 0; i < C::NQ; ++i) {
-      mbar_init(&bars.q[i], 32);
+      mbar_init(&bars.q[i], 1);
       mbar_init(&bars.qe[i], 1);
     }
-    mbar_init(&bars.of, TC_SM);
+    mbar_init(&bars.of, TC_SW);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
       mbar_init(&bars.vf[i], 1);
       mbar_init(&bars.s[i], 1);
       mbar_init(&bars.pv[i], 1);
     }
-    for (int i = 0; i < C::NB; ++i) mbar_init(&bars.p[i], TC_SM);
+    for (int i = 0; i < C::NB; ++i) mbar_init(&bars.p[i], TC_SW);
     fence_mbar_init();
     gone = 0;
   }
@@ -264,8 +271,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       next = item_at(t);
       float m = -INFINITY, l = 0.f;                // the reference (in scaled units), the sum of weights
       for (int j = 0; j < it.n; ++j, ++T) {
-        ok = tc_wait(&bars.s[T % ST], (T / ST) & 1, &gone, a.status);
-        ok = __all_sync(FULL, ok);
+        ok = tc_wait_warp(&bars.s[T % ST], (T / ST) & 1, lane, &gone, a.status);
         if (!ok) break;
         tc_fence_after();
         const u32 sa = tm_s + (T % C::NB) * TC_N + row;
@@ -292,8 +298,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           const float to = grow ? mx : m;
           const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
           if (j > 0) {                             // O holds the tiles before
-            ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
-            ok = __all_sync(FULL, ok);
+            ok = tc_wait_warp(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, lane, &gone, a.status);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -341,22 +346,21 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         if (left < TC_N) {
           // positions past the end: their weights are 0, and V's rows have to be finite
           const int st = T % ST;
-          ok = tc_wait(&bars.vf[st], (T / ST) & 1, &gone, a.status);
+          ok = tc_wait_warp(&bars.vf[st], (T / ST) & 1, lane, &gone, a.status);
+          if (!ok) break;
           for (int x = tid; x < (TC_N - left) * 8 * C::SLABS; x += TC_SM) {
             const int c = x & 7, vr = left + (x >> 3) % (TC_N - left), sl = (x >> 3) / (TC_N - left);
             *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + vr * 128 + c * 16) =
                 make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          ok = __all_sync(FULL, ok);
-          if (!ok) break;
         }
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars.p[T % C::NB]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p[T % C::NB]);
       }
-      if (ok && it.n > 0) ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
-      ok = __all_sync(FULL, ok);
+      if (ok && it.n > 0) ok = tc_wait_warp(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, lane, &gone, a.status);
       if (!ok) break;
       tc_fence_after();
 
@@ -382,7 +386,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       }
       if (it.n > 0) {
         tc_fence_before();
-        mbar_arrive(&bars.of);                     // O may be written again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.of);      // O may be written again
       }
       if (rho < a.M) {
 #pragma unroll
@@ -415,8 +420,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
                             : -1;
       }
       const int qb = done % C::NQ;
-      ok = done < C::NQ || tc_wait(&bars.qe[qb], (done / C::NQ - 1) & 1, &gone, a.status);
-      ok = __all_sync(FULL, ok);
+      ok = done < C::NQ || tc_wait_warp(&bars.qe[qb], (done / C::NQ - 1) & 1, lane, &gone, a.status);
       if (!ok) break;
 #pragma unroll 8
       for (int idx = lane; idx < TC_M * (DP / 8); idx += 32) {
@@ -455,7 +459,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       __syncwarp();
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&bars.q[qb]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q[qb]);
       if (lane == 0) {
         while (ok && jv < it.n) ok = load(&vmap, v_a, bars.vf, bars.pv, jv) && (jk == it.n || load(&kmap, k_a, bars.kf, bars.s, jk));
         if (!ok) {                                 // given up: the copies on their way land first
