@@ -153,6 +153,14 @@ struct TcBars {
   u64 q[2], qe[2], of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[3];
 };
 
+// Whether a phase is over, without waiting (try_wait may hold the thread for a while).
+__device__ __forceinline__ bool mbar_test(u64* bar, u32 parity) {
+  u32 ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   u32 r;
@@ -178,13 +186,6 @@ __device__ __forceinline__ int item_of(int t, int items) {
   return i < items ? i : -1;
 }
 
-// The same for a warp, by one of its lanes: 32 lanes on one barrier queue up behind one another.
-__device__ __forceinline__ bool tc_wait_warp(u64* bar, u32 parity, int lane, volatile int* gone, int* status) {
-  int ok = 1;
-  if (lane == 0) ok = tc_wait(bar, parity, gone, status);
-  return __shfl_sync(FULL, ok, 0) != 0;
-}
-
 template <int DP>
 __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                                                            const __grid_constant__ CUtensorMap vmap, const TcArgs a) {
@@ -203,17 +204,17 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
 
   if (tid == 0) {
     for (int i = 0; i < C::NQ; ++i) {
-      mbar_init(&bars.q[i], 1);
+      mbar_init(&bars.q[i], 32);
       mbar_init(&bars.qe[i], 1);
     }
-    mbar_init(&bars.of, TC_SW);
+    mbar_init(&bars.of, TC_SM);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
       mbar_init(&bars.vf[i], 1);
       mbar_init(&bars.s[i], 1);
       mbar_init(&bars.pv[i], 1);
     }
-    for (int i = 0; i < C::NB; ++i) mbar_init(&bars.p[i], TC_SW);
+    for (int i = 0; i < C::NB; ++i) mbar_init(&bars.p[i], TC_SM);
     fence_mbar_init();
     gone = 0;
   }
@@ -271,7 +272,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       next = item_at(t);
       float m = -INFINITY, l = 0.f;                // the reference (in scaled units), the sum of weights
       for (int j = 0; j < it.n; ++j, ++T) {
-        ok = tc_wait_warp(&bars.s[T % ST], (T / ST) & 1, lane, &gone, a.status);
+        ok = tc_wait(&bars.s[T % ST], (T / ST) & 1, &gone, a.status);
+        ok = __all_sync(FULL, ok);
         if (!ok) break;
         tc_fence_after();
         const u32 sa = tm_s + (T % C::NB) * TC_N + row;
@@ -298,7 +300,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
           const float to = grow ? mx : m;
           const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to)) : 1.f;
           if (j > 0) {                             // O holds the tiles before
-            ok = tc_wait_warp(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, lane, &gone, a.status);
+            ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
+            ok = __all_sync(FULL, ok);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -346,21 +349,22 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         if (left < TC_N) {
           // positions past the end: their weights are 0, and V's rows have to be finite
           const int st = T % ST;
-          ok = tc_wait_warp(&bars.vf[st], (T / ST) & 1, lane, &gone, a.status);
-          if (!ok) break;
+          ok = tc_wait(&bars.vf[st], (T / ST) & 1, &gone, a.status);
           for (int x = tid; x < (TC_N - left) * 8 * C::SLABS; x += TC_SM) {
             const int c = x & 7, vr = left + (x >> 3) % (TC_N - left), sl = (x >> 3) / (TC_N - left);
             *reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (TC_N * 128) + vr * 128 + c * 16) =
                 make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
         }
         tc_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p[T % C::NB]);
+        mbar_arrive(&bars.p[T % C::NB]);
       }
-      if (ok && it.n > 0) ok = tc_wait_warp(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, lane, &gone, a.status);
+      if (ok && it.n > 0) ok = tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
       if (!ok) break;
       tc_fence_after();
 
@@ -386,8 +390,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       }
       if (it.n > 0) {
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.of);      // O may be written again
+        mbar_arrive(&bars.of);                     // O may be written again
       }
       if (rho < a.M) {
 #pragma unroll
@@ -420,7 +423,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
                             : -1;
       }
       const int qb = done % C::NQ;
-      ok = done < C::NQ || tc_wait_warp(&bars.qe[qb], (done / C::NQ - 1) & 1, lane, &gone, a.status);
+      ok = done < C::NQ || tc_wait(&bars.qe[qb], (done / C::NQ - 1) & 1, &gone, a.status);
+      ok = __all_sync(FULL, ok);
       if (!ok) break;
 #pragma unroll 8
       for (int idx = lane; idx < TC_M * (DP / 8); idx += 32) {
@@ -443,32 +447,56 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      // K and V by one lane, in turn, each waiting for its stage (asleep in try_wait: a loop of tests would
-      // keep the barriers from everyone else); the first K goes out before Q is waited for
       int jk = 0, jv = 0;
-      auto load = [&](const CUtensorMap* map, u32 base, u64* full, u64* empty, int& j) {
-        const int T = T0 + j, st = T % ST;
-        if (T >= ST && !tc_wait(&empty[st], ((T / ST) & 1) ^ 1, &gone, a.status)) return false;
-        mbar_expect_tx(&full[st], C::TB);
-        for (int x = 0; x < C::SLABS; ++x)
-          tma_load(base + st * C::TB + x * TC_N * 128, map, &full[st], x * 64, j * TC_N, it.h, it.b);
-        ++j;
-        return true;
+      auto feed = [&](int most) {                  // loads tiles until `most` of each are on their way
+        for (u32 idle = 0; (jk < most || jv < most) && idle < TC_SPIN && !gone;) {
+          bool moved = false;
+          if (jk < most) {
+            const int T = T0 + jk, st = T % ST;
+            if (T < ST || mbar_test(&bars.s[st], ((T / ST) & 1) ^ 1)) {
+              mbar_expect_tx(&bars.kf[st], C::TB);
+              for (int x = 0; x < C::SLABS; ++x)
+                tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, jk * TC_N, it.h, it.b);
+              ++jk;
+              moved = true;
+            }
+          }
+          if (jv < most) {
+            const int T = T0 + jv, st = T % ST;
+            if (T < ST || mbar_test(&bars.pv[st], ((T / ST) & 1) ^ 1)) {
+              mbar_expect_tx(&bars.vf[st], C::TB);
+              for (int x = 0; x < C::SLABS; ++x)
+                tma_load(v_a + st * C::TB + x * TC_N * 128, &vmap, &bars.vf[st], x * 64, jv * TC_N, it.h, it.b);
+              ++jv;
+              moved = true;
+            }
+          }
+          idle = moved ? 0 : idle + 1;
+        }
+        if ((jk < most || jv < most) && !gone) {
+          gone = 1;
+          set_status(a.status, VBS_ETIMEOUT);
+        }
+        return jk >= most && jv >= most;
       };
-      if (lane == 0) ok = load(&kmap, k_a, bars.kf, bars.s, jk);
+      // the first K goes out before Q is waited for, where its stage is free
+      if (lane == 0 && (T0 < ST || mbar_test(&bars.s[T0 % ST], ((T0 / ST) & 1) ^ 1))) {
+        const int st = T0 % ST;
+        mbar_expect_tx(&bars.kf[st], C::TB);
+        for (int x = 0; x < C::SLABS; ++x)
+          tma_load(k_a + st * C::TB + x * TC_N * 128, &kmap, &bars.kf[st], x * 64, 0, it.h, it.b);
+        jk = 1;
+      }
       __syncwarp();
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q[qb]);
-      if (lane == 0) {
-        while (ok && jv < it.n) ok = load(&vmap, v_a, bars.vf, bars.pv, jv) && (jk == it.n || load(&kmap, k_a, bars.kf, bars.s, jk));
-        if (!ok) {                                 // given up: the copies on their way land first
-          for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
-          for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
-        }
-      }
+      mbar_arrive(&bars.q[qb]);
+      if (lane == 0) ok = feed(it.n);
       ok = __all_sync(FULL, ok);
+      if (!ok && lane == 0) {                      // given up: the copies on their way land first
+        for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
+        for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
+      }
       T0 += it.n;
       ++done;
       if (!ok) break;
