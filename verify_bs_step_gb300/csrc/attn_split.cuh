@@ -3,8 +3,8 @@
 // A segment is one sentence's K/V head with up to 16 MT of the query rows that read it (the W beams x
 // n_q tokens x q_heads / kv_heads rows that share it are numbered beam first).  Positions come in units
 // of at most 16.  All segments' units stand in one line, sentence by sentence; every CTA of one
-// resident wave takes an equal share of it, whatever the lengths, and its four warps take every fourth
-// unit.  A segment inside one share is written straight out; one that crosses shares leaves
+// resident wave takes an equal share of it, whatever the lengths (a segment counts SP_FIX units more than it
+// has, at its start), and its four warps take every fourth unit.  A segment inside one share is written straight out; one that crosses shares leaves
 // (m, l, o) partials, and the CTA that arrives last joins them in order, so equal calls give equal bits.
 //
 // A warp holds 16 MT rows x head_dim of o in registers.  Units come through a ring of cp.async stages of
@@ -30,6 +30,9 @@ namespace vbs {
 constexpr int SP_WARPS = 4;
 constexpr int SP_NT = 32 * SP_WARPS;
 constexpr int SP_MIN = 4 * SP_WARPS;     // units a CTA takes at least: every warp's ring once
+// What a segment costs besides its units (Q, the first loads, the join), in units: a share with many short
+// segments takes as long as one with a single long one.
+constexpr int SP_FIX = 8;
 
 // What the kernel needs to know of the split.
 struct SplitArgs {
@@ -94,10 +97,12 @@ __device__ __forceinline__ u32 pack_bf16(float a, float b) {
 }
 
 // What a unit's consumer needs of it.
-struct UnitHead {
+struct __align__(16) UnitHead {
   int pos, n;                     // its first position, and how many it has
   u32 rows;                       // the beams that see it
-  float ks, ve;                   // K's scale; log2 of V's scale
+  float ks;                       // K's scale
+  float ve, vinv;                 // log2 of V's scale, and its reciprocal
+  float pad[2];
 };
 
 // ---------------------------------------------------------------------------------------
@@ -114,41 +119,38 @@ template <int FMT> struct PagedSrc {
   const int* seen;                // [R]
   int cap, tpp;                   // list entries a sentence, units a page
   struct Batch {                  // one unit per lane
-    int page, pos, off, n;
-    u32 rows;
-    float ks, vs;
+    const char* k;                // its K rows; V's stand H runs further on
+    UnitHead u;
   };
   __device__ int units(int b) const { return n_pages[b] * tpp; }
   __device__ int limit(int b, int w, int i, int W, int n_q) const { return seen[b * W + w] - n_q + 1 + i; }
   __device__ void fetch(Batch& t, int b, int h, int u, bool valid) const {
-    t = Batch{0, 0, 0, 0, 0u, 0.f, 1.f};
+    t.k = g.pool;
+    t.u = UnitHead{0, 0, 0u, 0.f, 0.f, 1.f, {0.f, 0.f}};
     if (!valid) return;
-    const int e = u / tpp, sub = u - e * tpp;
+    const int e = u / tpp, off = (u - e * tpp) * 16;
     const int4 x = list[static_cast<int64_t>(b) * cap + e];
-    t.page = x.x;
-    t.off = sub * 16;
-    t.pos = x.y + t.off;
-    t.rows = static_cast<u32>(x.z);
-    t.n = max(0, min(16, x.w - t.off));
-    if (t.n > 0) {
+    t.u.pos = x.y + off;
+    t.u.n = max(0, min(16, x.w - off));
+    t.u.rows = static_cast<u32>(x.z);
+    if (t.u.n > 0) {
       const int64_t run = g.run(x.x, 0, h);
-      t.ks = g.scales[run];
-      t.vs = g.scales[run + g.H];
+      t.k = g.pool + (run * g.block + off) * g.D;
+      t.u.ks = g.scales[run];
+      // held to the scales' range: a page no append has written (scale 0) counts as zeros
+      const int ve = max(KV8_E_LO, min(KV8_E_HI, (__float_as_int(g.scales[run + g.H]) >> 23) - 127));
+      t.u.ve = static_cast<float>(ve);
+      t.u.vinv = __int_as_float((127 - ve) << 23);
     }
   }
   // lane `k`'s unit: the loads of its K and V rows into a stage, and its head
-  template <class L> __device__ __forceinline__ UnitHead issue(const Batch& t, int k, int b, int h, const L& load) const {
-    const int page = __shfl_sync(FULL, t.page, k), off = __shfl_sync(FULL, t.off, k), n = __shfl_sync(FULL, t.n, k);
-    UnitHead u;
-    u.n = n;
-    u.pos = __shfl_sync(FULL, t.pos, k);
-    u.rows = __shfl_sync(FULL, t.rows, k);
-    u.ks = __shfl_sync(FULL, t.ks, k);
-    // held to the scales' range: a page no append has written (scale 0) counts as zeros
-    u.ve = static_cast<float>(max(KV8_E_LO, min(KV8_E_HI, (__float_as_int(__shfl_sync(FULL, t.vs, k)) >> 23) - 127)));
-    const char* kp = g.pool + (g.run(page, 0, h) * g.block + off) * g.D;
+  template <class L>
+  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int, int, UnitHead* head, const L& load) const {
+    const u64 at = shfl64(reinterpret_cast<u64>(t.k), k);
+    const int n = __shfl_sync(FULL, t.u.n, k);
+    if (lane == k) *head = t.u;
+    const char* kp = reinterpret_cast<const char*>(at);
     load(kp, kp + static_cast<int64_t>(g.H) * g.block * g.D, g.D, g.D, n);
-    return u;
   }
 };
 
@@ -167,13 +169,14 @@ struct EncSrc {
   __device__ int units(int b) const { return max(1, (len(b) + 15) >> 4); }
   __device__ int limit(int b, int, int, int, int) const { return len(b); }
   __device__ void fetch(Batch& t, int, int, int u, bool) const { t.u = u; }
-  template <class L> __device__ __forceinline__ UnitHead issue(const Batch& t, int k, int b, int h, const L& load) const {
+  template <class L>
+  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int b, int h, UnitHead* head, const L& load) const {
     const int pos = __shfl_sync(FULL, t.u, k) * 16;
     const int n = max(0, min(16, len(b) - pos));
+    if (lane == 0) *head = UnitHead{pos, n, 0xffffu, 1.f, 0.f, 1.f, {0.f, 0.f}};
     load(reinterpret_cast<const char*>(e.k + b * e.k_sent + h * e.k_head + (n > 0 ? pos * e.k_pos : 0)),
          reinterpret_cast<const char*>(e.v + b * e.v_sent + h * e.v_head + (n > 0 ? pos * e.v_pos : 0)),
          e.k_pos * 2, e.v_pos * 2, n);
-    return UnitHead{pos, n, 0xffffu, 1.f, 0.f};
   }
 };
 
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(SP_NT, (SplitCfg<Src::EL, DP, MT>::CTAS))
 attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   using C = SplitCfg<Src::EL, DP, MT>;
   constexpr int EL = Src::EL, ROWS = 16 * MT;
+  constexpr float GROW = Src::BF ? 8.f : 4.f;
   extern __shared__ __align__(128) unsigned char sp_smem[];
   __shared__ UnitHead heads[SP_WARPS][C::NS];
   __shared__ float row_f[ROWS];                             // a row's factor on its dot products
@@ -236,7 +240,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   {
     const int k = (sa.B + SP_NT - 1) / SP_NT;               // a thread's sentences: [tid * k, tid * k + k)
     int64_t mine = 0;
-    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i);
+    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i) + SP_FIX;
     int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -251,7 +255,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       all += s_sum[w];
     }
     const int64_t total = all * HM;
-    per = max(static_cast<int64_t>(SP_MIN), (total + gridDim.x - 1) / gridDim.x);
+    per = max(static_cast<int64_t>(SP_MIN + SP_FIX), (total + gridDim.x - 1) / gridDim.x);
     const int64_t from = per * blockIdx.x;
     end = min(total, from + per);
     if (from >= total) return;
@@ -259,7 +263,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       int64_t p = from - before * HM;
       int i = tid * k;
       for (; i < sa.B - 1; ++i) {
-        const int64_t n = static_cast<int64_t>(src.units(i)) * HM;
+        const int64_t n = static_cast<int64_t>(src.units(i) + SP_FIX) * HM;
         if (p < n) break;
         p -= n;
       }
@@ -274,10 +278,25 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   int64_t line0 = per * blockIdx.x - at;                    // the line's position of sentence b's first unit
 
   while (end > 0 && b < sa.B) {
-    const int n = src.units(b);
-    const int hm = static_cast<int>(at / n), h = hm / sa.MC, mc = hm - h * sa.MC;
-    const int u0 = static_cast<int>(at - static_cast<int64_t>(hm) * n);
-    const int u1 = static_cast<int>(min(static_cast<int64_t>(n), u0 + end));
+    const int n = src.units(b), nf = n + SP_FIX;
+    const int hm = static_cast<int>(at / nf), h = hm / sa.MC, mc = hm - h * sa.MC;
+    const int f0 = static_cast<int>(at - static_cast<int64_t>(hm) * nf);   // on the line; u0, u1: units
+    const int f1 = static_cast<int>(min(static_cast<int64_t>(nf), f0 + end));
+    const int u0 = max(0, f0 - SP_FIX), u1 = f1 - SP_FIX;
+    auto advance = [&] {
+      const int done = f1 - f0;
+      end -= done;
+      at += done;
+      if (at == static_cast<int64_t>(nf) * HM) {
+        line0 += at;
+        at = 0;
+        ++b;
+      }
+    };
+    if (u1 <= u0) {                                         // the segment's units are all in the next share
+      advance();
+      continue;
+    }
     const int rho0 = mc * ROWS;
     const int rows = min(ROWS, sa.M - rho0);
 
@@ -288,7 +307,17 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         if ((k & 31) == 0) src.fetch(batch, b, h, u0 + wid + (k + lane) * SP_WARPS, k + lane < mine);
         const int st = k % C::NS;
         const u32 base = ring_a + st * C::STAGE;
-        const UnitHead u = src.issue(batch, k & 31, b, h, [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
+        src.issue(batch, k & 31, lane, b, h, &heads[wid][st], [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
+          if (EXACT && EL == 1 && cnt == 16) {              // a whole unit of contiguous rows: constant offsets
+            const char *ks = kp + lane * 16, *vs = vp + lane * 16;
+#pragma unroll
+            for (int i = 0; i < DP / C::CHK / 2; ++i) {
+              const int L = i * 32 + lane, tok = L / nc;
+              cp_async16(base + (L ^ k_swz(tok, nc)) * 16, ks + i * 512, true);
+              cp_async16(base + C::STAGE / 2 + (L ^ v_swz(tok, nc)) * 16, vs + i * 512, true);
+            }
+            return;
+          }
 #pragma unroll
           for (int i = 0; i < (DP / C::CHK + 1) / 2; ++i) {
             const int L = i * 32 + lane;
@@ -314,7 +343,6 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
             }
           }
         });
-        if (lane == 0) heads[wid][st] = u;
       }
       cp_commit();
     };
@@ -439,11 +467,12 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
             }
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 1));
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 2));
-          mx[x] = fmaxf(mx[x], m[mt][x]);
         }
-        if (__any_sync(FULL, mx[0] > m[mt][0] || mx[1] > m[mt][1])) {
+        // the reference moves once a maximum has outgrown it by 2^GROW
+        if (__any_sync(FULL, mx[0] > m[mt][0] + GROW || mx[1] > m[mt][1] + GROW)) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
+            mx[x] = fmaxf(mx[x], m[mt][x]);
             const float corr = m[mt][x] == -INFINITY ? 0.f : ex2(m[mt][x] - mx[x]);
             l[mt][x] *= corr;
 #pragma unroll
@@ -455,11 +484,10 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
           }
         }
         float w[2][4];                                      // [row][position]
-        const float vinv = Src::BF ? 1.f : __int_as_float((127 - static_cast<int>(u.ve)) << 23);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          // fp16 weights stand at 2^15 of the largest, so that small ones keep their bits
-          const float ref = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f);
+          // fp16 weights reach up to 2^15, so that small ones keep their bits
+          const float ref = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f - GROW);
           float sum = 0.f;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
@@ -468,7 +496,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
               w[x][t * 2 + y] = ex2(s[mt][t][x * 2 + y] - ref);
               sum += w[x][t * 2 + y];
             }
-          l[mt][x] = fmaf(sum, vinv, l[mt][x]);
+          l[mt][x] = Src::BF ? l[mt][x] + sum : fmaf(sum, u.vinv, l[mt][x]);
         }
         if (Src::BF) {
           // two bf16 parts of each weight: the products carry 16 bits of it
@@ -565,7 +593,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       }
     __syncthreads();
     const bool whole = u0 == 0 && u1 == n;
-    const int64_t line = line0 + static_cast<int64_t>(hm) * n;   // the segment's place in the line
+    const int64_t line = line0 + static_cast<int64_t>(hm) * nf;  // the segment's place in the line
     float* part = sa.part + (static_cast<int64_t>(blockIdx.x) * 2 + (u0 > 0 ? 0 : 1)) * C::PART;
     if (tid < ROWS) {
       float top = -INFINITY, sum = 0.f;
@@ -620,7 +648,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     // ---- join the pieces of a segment that crosses shares ----
     if (!whole) {
       const int64_t seg = static_cast<int64_t>(b) * HM + hm;
-      const int first = static_cast<int>(line / per), last = static_cast<int>((line + n - 1) / per);
+      const int first = static_cast<int>((line + SP_FIX) / per), last = static_cast<int>((line + nf - 1) / per);
       __threadfence();
       __syncthreads();
       if (tid == 0) s_last = atomic_add_acq_rel(sa.arrived + seg, 1) == last - first;
@@ -657,14 +685,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       }
     }
     __syncthreads();                                        // the ring and the row statistics are free again
-    const int done = u1 - u0;
-    end -= done;
-    at += done;
-    if (at == static_cast<int64_t>(n) * HM) {
-      line0 += at;
-      at = 0;
-      ++b;
-    }
+    advance();
   }
 }
 
