@@ -168,7 +168,8 @@ struct EncSrc {
   }
   __device__ int units(int b) const { return max(1, (len(b) + 15) >> 4); }
   __device__ int limit(int b, int, int, int, int) const { return len(b); }
-  __device__ void fetch(Batch& t, int, int, int u, bool) const { t.u = u; }
+  // (a lane without a unit stands past every end: no positions)
+  __device__ void fetch(Batch& t, int, int, int u, bool valid) const { t.u = valid ? u : 1 << 26; }
   template <class L>
   __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int b, int h, UnitHead* head, const L& load) const {
     const int pos = __shfl_sync(FULL, t.u, k) * 16;
@@ -184,20 +185,26 @@ struct EncSrc {
 // the kernel
 // ---------------------------------------------------------------------------------------
 
+constexpr int SP_SMS = 160;              // SMs the grid is laid out for at most (a join holds a factor a row and CTA)
+
 template <int EL, int DP, int MT> struct SplitCfg {
   static constexpr int CHK = 16 / EL;                       // dims in 16 bytes
   static constexpr int KS = DP / 16;                        // contraction steps of the scores
   static constexpr int NT = DP / 8;                         // output tiles of 8 dims
   static constexpr int VCH = NT < CHK ? NT : CHK;           // dims of a position that a lane reads at once
-  static constexpr int STAGE = 2 * 16 * DP * EL;            // bytes of K and V of one unit
+  static constexpr int UNIT = 2 * 16 * DP * EL;             // bytes of K and V of one unit
+  // Units of an iteration: two where the registers and the ring hold them, for twice the independent work
+  // between dependent steps (a score's sum over head_dim is a chain of mma's, the softmax a chain of shuffles).
+  static constexpr int U = MT == 1 && UNIT <= 4096 ? 2 : 1;
+  static constexpr int STAGE = U * UNIT;
   static constexpr int NS = STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
   static constexpr int O_LD = DP + 4;                       // floats of an o row in shared memory
   static constexpr int RING = NS * STAGE > MT * 16 * O_LD * 4 ? NS * STAGE : MT * 16 * O_LD * 4;
   static constexpr int QBYTES = MT * KS * 512;              // Q in fragment order
   static constexpr int PART = MT * 16 * (DP + 2);           // floats of a partial
   static constexpr size_t SMEM = SP_WARPS * RING + QBYTES;
-  // resident CTAs a SM, by shared memory and by o's registers (MT * DP / 2 of a thread's)
-  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 ? 2 : 3);
+  // resident CTAs a SM, by shared memory and by registers (o is MT * DP / 2 of a thread's)
+  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 || (U == 2 && DP > 64) ? 2 : 3);
 };
 
 // The order of output dims: column n of output tile j.
@@ -214,10 +221,10 @@ template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
 __global__ void __launch_bounds__(SP_NT, (SplitCfg<Src::EL, DP, MT>::CTAS))
 attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   using C = SplitCfg<Src::EL, DP, MT>;
-  constexpr int EL = Src::EL, ROWS = 16 * MT;
+  constexpr int EL = Src::EL, ROWS = 16 * MT, U = C::U;
   constexpr float GROW = Src::BF ? 8.f : 4.f;
   extern __shared__ __align__(128) unsigned char sp_smem[];
-  __shared__ UnitHead heads[SP_WARPS][C::NS];
+  __shared__ UnitHead heads[SP_WARPS][C::NS][C::U];
   __shared__ float row_f[ROWS];                             // a row's factor on its dot products
   __shared__ float wm[SP_WARPS][ROWS], wl[SP_WARPS][ROWS];
   __shared__ int64_t s_sum[SP_WARPS];
@@ -302,47 +309,54 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 
     const int mine = u1 - u0 > wid ? (u1 - u0 - wid + SP_WARPS - 1) / SP_WARPS : 0;
     typename Src::Batch batch;
-    auto issue = [&](int k) {                               // the warp's k-th unit into its stage
-      if (k < mine) {
-        if ((k & 31) == 0) src.fetch(batch, b, h, u0 + wid + (k + lane) * SP_WARPS, k + lane < mine);
+    auto issue = [&](int k) {                               // the warp's units of iteration k into its stage
+      if (k * U < mine) {
+        if ((k * U & 31) == 0) {
+          const int x = k * U + lane;
+          src.fetch(batch, b, h, u0 + wid + x * SP_WARPS, x < mine);
+        }
         const int st = k % C::NS;
-        const u32 base = ring_a + st * C::STAGE;
-        src.issue(batch, k & 31, lane, b, h, &heads[wid][st], [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
-          if (EXACT && EL == 1 && cnt == 16) {              // a whole unit of contiguous rows: constant offsets
-            const char *ks = kp + lane * 16, *vs = vp + lane * 16;
 #pragma unroll
-            for (int i = 0; i < DP / C::CHK / 2; ++i) {
-              const int L = i * 32 + lane, tok = L / nc;
-              cp_async16(base + (L ^ k_swz(tok, nc)) * 16, ks + i * 512, true);
-              cp_async16(base + C::STAGE / 2 + (L ^ v_swz(tok, nc)) * 16, vs + i * 512, true);
+        for (int un = 0; un < U; ++un) {
+          const u32 base = ring_a + st * C::STAGE + un * C::UNIT;
+          src.issue(batch, (k * U + un) & 31, lane, b, h, &heads[wid][st][un],
+                    [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
+            if (EXACT && EL == 1 && cnt == 16) {            // a whole unit of contiguous rows: constant offsets
+              const char *ks = kp + lane * 16, *vs = vp + lane * 16;
+#pragma unroll
+              for (int i = 0; i < DP / C::CHK / 2; ++i) {
+                const int L = i * 32 + lane, tok = L / nc;
+                cp_async16(base + (L ^ k_swz(tok, nc)) * 16, ks + i * 512, true);
+                cp_async16(base + C::UNIT / 2 + (L ^ v_swz(tok, nc)) * 16, vs + i * 512, true);
+              }
+              return;
             }
-            return;
-          }
 #pragma unroll
-          for (int i = 0; i < (DP / C::CHK + 1) / 2; ++i) {
-            const int L = i * 32 + lane;
-            const int tok = L / nc, ch = L - tok * nc;
-            if (EXACT || tok < 16) {
-              const bool ok = tok < cnt;
-              const char* ks = kp + (ok ? tok * kld + ch * 16 : 0);
-              const char* vs = vp + (ok ? tok * vld + ch * 16 : 0);
-              const u32 kd = base + (L ^ k_swz(tok, nc)) * 16;
-              const u32 vd = base + C::STAGE / 2 + (L ^ v_swz(tok, nc)) * 16;
-              if (ALIGNED) {
-                cp_async16(kd, ks, ok);
-                cp_async16(vd, vs, ok);
-              } else {
+            for (int i = 0; i < (DP / C::CHK + 1) / 2; ++i) {
+              const int L = i * 32 + lane;
+              const int tok = L / nc, ch = L - tok * nc;
+              if (EXACT || tok < 16) {
+                const bool ok = tok < cnt;
+                const char* ks = kp + (ok ? tok * kld + ch * 16 : 0);
+                const char* vs = vp + (ok ? tok * vld + ch * 16 : 0);
+                const u32 kd = base + (L ^ k_swz(tok, nc)) * 16;
+                const u32 vd = base + C::UNIT / 2 + (L ^ v_swz(tok, nc)) * 16;
+                if (ALIGNED) {
+                  cp_async16(kd, ks, ok);
+                  cp_async16(vd, vs, ok);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const uint16_t x = ok ? reinterpret_cast<const uint16_t*>(ks)[e] : uint16_t{0};
-                  const uint16_t y = ok ? reinterpret_cast<const uint16_t*>(vs)[e] : uint16_t{0};
-                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(kd + e * 2), "h"(x) : "memory");
-                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(vd + e * 2), "h"(y) : "memory");
+                  for (int e = 0; e < 8; ++e) {
+                    const uint16_t x = ok ? reinterpret_cast<const uint16_t*>(ks)[e] : uint16_t{0};
+                    const uint16_t y = ok ? reinterpret_cast<const uint16_t*>(vs)[e] : uint16_t{0};
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(kd + e * 2), "h"(x) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(vd + e * 2), "h"(y) : "memory");
+                  }
                 }
               }
             }
-          }
-        });
+          });
+        }
       }
       cp_commit();
     };
@@ -398,34 +412,37 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         for (int j = 0; j < C::NT; ++j) o[mt][j][x * 2] = o[mt][j][x * 2 + 1] = 0.f;
       }
 
-    for (int k = 0; k < mine; ++k) {
+    for (int k = 0; k * U < mine; ++k) {
       cp_wait<C::NS - 2>();
       __syncwarp();
       issue(k + C::NS - 1);
       const int st = k % C::NS;
-      const u32 ka = ring_a + st * C::STAGE, va = ka + C::STAGE / 2;
-      const UnitHead u = heads[wid][st];
+      const u32 ka = ring_a + st * C::STAGE;
+      UnitHead u[U];
+#pragma unroll
+      for (int un = 0; un < U; ++un) u[un] = heads[wid][st][un];
 
-      // ---- scores of 16 positions: two tiles of 8 ----
-      float s[MT][2][4];
+      // ---- scores: two tiles of 8 positions a unit ----
+      float s[MT][2 * U][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) s[mt][t][0] = s[mt][t][1] = s[mt][t][2] = s[mt][t][3] = 0.f;
+        for (int t = 0; t < 2 * U; ++t) s[mt][t][0] = s[mt][t][1] = s[mt][t][2] = s[mt][t][3] = 0.f;
 #pragma unroll
       for (int grp = 0; grp < DP / C::CHK / 4; ++grp) {
-        uint4 kw[2];
+        uint4 kw[2 * U];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int tok = t * 8 + g, ch = grp * 4 + c4;
-          kw[t] = EXACT || ch < nc ? lds16(ka + ((tok * nc + ch) ^ k_swz(tok, nc)) * 16) : make_uint4(0, 0, 0, 0);
+        for (int t = 0; t < 2 * U; ++t) {
+          const int tok = (t & 1) * 8 + g, ch = grp * 4 + c4;
+          kw[t] = EXACT || ch < nc ? lds16(ka + (t >> 1) * C::UNIT + ((tok * nc + ch) ^ k_swz(tok, nc)) * 16)
+                                   : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int q4 = 0; q4 < C::CHK / 4; ++q4) {
           const int ks = grp * (C::CHK / 4) + q4;
-          u32 b0[2], b1[2];
+          u32 b0[2 * U], b1[2 * U];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < 2 * U; ++t) {
             const u32 words[4] = {kw[t].x, kw[t].y, kw[t].z, kw[t].w};
             if (EL == 1) {
               codes4<Src::FORMAT>(words[q4], b0[t], b1[t]);
@@ -437,34 +454,41 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const uint4 a = lds16(qf_a + ((mt * C::KS + ks) * 32 + lane) * 16);
-            mma16816<Src::BF>(s[mt][0], a, b0[0], b1[0]);
-            mma16816<Src::BF>(s[mt][1], a, b0[1], b1[1]);
+#pragma unroll
+            for (int t = 0; t < 2 * U; ++t) mma16816<Src::BF>(s[mt][t], a, b0[t], b1[t]);
           }
         }
       }
 
       // ---- softmax: weights relative to the running maximum of s + log2(V's scale) ----
-      uint4 p[MT], p2[MT];
+      uint4 p[MT][U], p2[MT][U];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        int left[2];
+        int left[2][U];
+        bool all = true;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) left[x] = (u.rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? min(lim[mt][x] - u.pos, u.n) : 0;
-        const bool full = __all_sync(FULL, left[0] >= 16 && left[1] >= 16);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int un = 0; un < U; ++un) {
+            left[x][un] = (u[un].rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? min(lim[mt][x] - u[un].pos, u[un].n) : 0;
+            all = all && left[x][un] >= 16;
+          }
+        const bool full = __all_sync(FULL, all);
         float mx[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float fk = f[mt][x] * u.ks;
           mx[x] = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2 * U; ++t) {
+            const float fk = f[mt][x] * u[t >> 1].ks;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               float& z = s[mt][t][x * 2 + y];
-              z = fmaf(z, fk, u.ve);
-              if (!full && t * 8 + c4 * 2 + y >= left[x]) z = -INFINITY;
+              z = fmaf(z, fk, u[t >> 1].ve);
+              if (!full && (t & 1) * 8 + c4 * 2 + y >= left[x][t >> 1]) z = -INFINITY;
               mx[x] = fmaxf(mx[x], z);
             }
+          }
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 1));
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 2));
         }
@@ -483,84 +507,94 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
             m[mt][x] = mx[x];
           }
         }
-        float w[2][4];                                      // [row][position]
+        // fp16 weights reach up to 2^15, so that small ones keep their bits
+        float ref[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          // fp16 weights reach up to 2^15, so that small ones keep their bits
-          const float ref = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f - GROW);
-          float sum = 0.f;
+        for (int x = 0; x < 2; ++x) ref[x] = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f - GROW);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int un = 0; un < U; ++un) {
+          float w[2][4];                                    // [row][position]
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              w[x][t * 2 + y] = ex2(s[mt][t][x * 2 + y] - ref);
-              sum += w[x][t * 2 + y];
-            }
-          l[mt][x] = Src::BF ? l[mt][x] + sum : fmaf(sum, u.vinv, l[mt][x]);
-        }
-        if (Src::BF) {
-          // two bf16 parts of each weight: the products carry 16 bits of it
-          float r[2][4];
-          p[mt] = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
-                             pack_bf16(w[1][2], w[1][3]));
-          const u32 hi[2][2] = {{p[mt].x, p[mt].z}, {p[mt].y, p[mt].w}};
+          for (int x = 0; x < 2; ++x) {
+            float sum = 0.f;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              r[x][t * 2] = w[x][t * 2] - bf16_lo(hi[x][t]);
-              r[x][t * 2 + 1] = w[x][t * 2 + 1] - bf16_hi(hi[x][t]);
-            }
-          p2[mt] = make_uint4(pack_bf16(r[0][0], r[0][1]), pack_bf16(r[1][0], r[1][1]), pack_bf16(r[0][2], r[0][3]),
-                              pack_bf16(r[1][2], r[1][3]));
-        } else {
-          p[mt] = make_uint4(pack_f16(w[0][0], w[0][1]), pack_f16(w[1][0], w[1][1]), pack_f16(w[0][2], w[0][3]),
-                             pack_f16(w[1][2], w[1][3]));
+              for (int y = 0; y < 2; ++y) {
+                w[x][t * 2 + y] = ex2(s[mt][un * 2 + t][x * 2 + y] - ref[x]);
+                sum += w[x][t * 2 + y];
+              }
+            l[mt][x] = Src::BF ? l[mt][x] + sum : fmaf(sum, u[un].vinv, l[mt][x]);
+          }
+          if (Src::BF) {
+            // two bf16 parts of each weight: the products carry 16 bits of it
+            float r[2][4];
+            uint4& q = p[mt][un];
+            q = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
+                           pack_bf16(w[1][2], w[1][3]));
+            const u32 hi[2][2] = {{q.x, q.z}, {q.y, q.w}};
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                r[x][t * 2] = w[x][t * 2] - bf16_lo(hi[x][t]);
+                r[x][t * 2 + 1] = w[x][t * 2 + 1] - bf16_hi(hi[x][t]);
+              }
+            p2[mt][un] = make_uint4(pack_bf16(r[0][0], r[0][1]), pack_bf16(r[1][0], r[1][1]), pack_bf16(r[0][2], r[0][3]),
+                                    pack_bf16(r[1][2], r[1][3]));
+          } else {
+            p[mt][un] = make_uint4(pack_f16(w[0][0], w[0][1]), pack_f16(w[1][0], w[1][1]), pack_f16(w[0][2], w[0][3]),
+                                   pack_f16(w[1][2], w[1][3]));
+          }
         }
       }
 
       // ---- o += P V ----
       const int toks[4] = {c4 * 2, c4 * 2 + 1, c4 * 2 + 8, c4 * 2 + 9};
 #pragma unroll
-      for (int vc = 0; vc < C::NT / C::VCH; ++vc) {
-        u32 vw[4][4];
+      for (int un = 0; un < U; ++un) {
+        const u32 va = ka + un * C::UNIT + C::UNIT / 2;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int dim = out_dim<C::VCH>(g, vc * C::VCH), ch = dim / C::CHK;
-          const u32 a = va + ((toks[t] * nc + ch) ^ v_swz(toks[t], nc)) * 16;
-          if (EXACT || dim < D) {
-            if (C::VCH * EL == 16) {
-              const uint4 q = lds16(a);
-              vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = q.z; vw[t][3] = q.w;
+        for (int vc = 0; vc < C::NT / C::VCH; ++vc) {
+          u32 vw[4][4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int dim = out_dim<C::VCH>(g, vc * C::VCH), ch = dim / C::CHK;
+            const u32 a = va + ((toks[t] * nc + ch) ^ v_swz(toks[t], nc)) * 16;
+            if (EXACT || dim < D) {
+              if (C::VCH * EL == 16) {
+                const uint4 q = lds16(a);
+                vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = q.z; vw[t][3] = q.w;
+              } else {
+                const uint2 q = lds8(a + (dim % C::CHK) * EL);
+                vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = vw[t][3] = 0;
+              }
             } else {
-              const uint2 q = lds8(a + (dim % C::CHK) * EL);
-              vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = vw[t][3] = 0;
+              vw[t][0] = vw[t][1] = vw[t][2] = vw[t][3] = 0;
             }
-          } else {
-            vw[t][0] = vw[t][1] = vw[t][2] = vw[t][3] = 0;
           }
-        }
 #pragma unroll
-        for (int wd = 0; wd < C::VCH * EL / 4; ++wd) {
-          if (EL == 1) {
-            u32 b0[4], b1[4];                               // four dims, positions 0,1 and 2,3 of the lane
-            codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x5140), b0[0], b0[1]);
-            codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x7362), b0[2], b0[3]);
-            codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x5140), b1[0], b1[1]);
-            codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x7362), b1[2], b1[3]);
+          for (int wd = 0; wd < C::VCH * EL / 4; ++wd) {
+            if (EL == 1) {
+              u32 b0[4], b1[4];                             // four dims, positions 0,1 and 2,3 of the lane
+              codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x5140), b0[0], b0[1]);
+              codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x7362), b0[2], b0[3]);
+              codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x5140), b1[0], b1[1]);
+              codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x7362), b1[2], b1[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816<false>(o[mt][vc * C::VCH + wd * 4 + i], p[mt], b0[i], b1[i]);
-          } else {
+                for (int mt = 0; mt < MT; ++mt) mma16816<false>(o[mt][vc * C::VCH + wd * 4 + i], p[mt][un], b0[i], b1[i]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const u32 b0 = __byte_perm(vw[0][wd], vw[1][wd], i ? 0x7632 : 0x5410);
-              const u32 b1 = __byte_perm(vw[2][wd], vw[3][wd], i ? 0x7632 : 0x5410);
+              for (int i = 0; i < 2; ++i) {
+                const u32 b0 = __byte_perm(vw[0][wd], vw[1][wd], i ? 0x7632 : 0x5410);
+                const u32 b1 = __byte_perm(vw[2][wd], vw[3][wd], i ? 0x7632 : 0x5410);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p[mt], b0, b1);
-                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt], b0, b1);
+                for (int mt = 0; mt < MT; ++mt) {
+                  mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p[mt][un], b0, b1);
+                  mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt][un], b0, b1);
+                }
               }
             }
           }
@@ -655,28 +689,38 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       __syncthreads();
       if (s_last) {
         auto piece = [&](int c) { return sa.part + (static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * C::PART; };
-        if (tid < rows) {
+        // each piece's factor of each row: a warp a row, a lane a piece
+        float* fac = reinterpret_cast<float*>(sp_smem);     // [rows][pieces]
+        const int np = last - first + 1;
+        for (int r = wid; r < rows; r += SP_WARPS) {
           float top = -INFINITY, sum = 0.f;
-          for (int c = first; c <= last; ++c) top = fmaxf(top, __ldcg(piece(c) + ROWS * DP + tid));
-          for (int c = first; c <= last; ++c) {
-            const float x = __ldcg(piece(c) + ROWS * DP + tid);
-            sum += __ldcg(piece(c) + ROWS * DP + ROWS + tid) * (x == -INFINITY ? 0.f : ex2(x - top));
+          for (int c = lane; c < np; c += 32) {
+            const float mm = __ldcg(piece(first + c) + ROWS * DP + r);
+            fac[r * np + c] = mm;
+            top = fmaxf(top, mm);
           }
-          wm[0][tid] = top;
-          wl[0][tid] = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, k));
+          for (int c = lane; c < np; c += 32) {
+            const float mm = fac[r * np + c];
+            const float x = mm == -INFINITY ? 0.f : ex2(mm - top);
+            sum += __ldcg(piece(first + c) + ROWS * DP + ROWS + r) * x;     // (a NaN stays one)
+            fac[r * np + c] = x;
+          }
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(FULL, sum, k);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          for (int c = lane; c < np; c += 32) fac[r * np + c] *= inv;
         }
         __syncthreads();
         for (int idx = tid; idx < rows * (DP / 4); idx += SP_NT) {
           const int r = idx / (DP / 4), d = idx % (DP / 4) * 4;
           if (!EXACT && d >= D) continue;
-          const float top = wm[0][r], inv = wl[0][r];
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int c = first; c <= last; ++c) {
-            const float* pp = piece(c);
-            const float mm = __ldcg(pp + ROWS * DP + r);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + r * DP + d));
-            const float x = mm == -INFINITY ? 0.f : ex2(mm - top) * inv;
+#pragma unroll 8
+          for (int c = 0; c < np; ++c) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(first + c) + r * DP + d));
+            const float x = fac[r * np + c];
             a.x += v.x * x; a.y += v.y * x; a.z += v.z * x; a.w += v.w * x;
           }
           store(r, d, a);
@@ -709,7 +753,8 @@ int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_s
   static std::atomic<unsigned long long> attr_done{0};
   auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
   if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
-  kernel<<<num_sms * C::CTAS, SP_NT, C::SMEM, s>>>(src, io, sa);
+  static_assert(16 * MT * SP_SMS * C::CTAS * 4 <= SP_WARPS * C::RING, "the join's factors fit the ring");
+  kernel<<<std::min(num_sms, SP_SMS) * C::CTAS, SP_NT, C::SMEM, s>>>(src, io, sa);
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
