@@ -127,9 +127,9 @@ int64_t attn_segments(int B, int W, int H, int D, int Hq, int n_q) {
 }
 
 int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
-                         int* arrived, int num_sms, cudaStream_t s) {
-  return g.fmt == VBS_I8 ? launch_kv8_attention_i8(a, g, io, p, part, arrived, num_sms, s)
-                         : launch_kv8_attention_e4m3(a, g, io, p, part, arrived, num_sms, s);
+                         int2* pieces, int num_sms, cudaStream_t s) {
+  return g.fmt == VBS_I8 ? launch_kv8_attention_i8(a, g, io, p, part, pieces, num_sms, s)
+                         : launch_kv8_attention_e4m3(a, g, io, p, part, pieces, num_sms, s);
 }
 
 }  // namespace vbs

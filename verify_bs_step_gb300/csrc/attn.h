@@ -42,11 +42,11 @@ int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, const Kv8Plan& p, cu
 int64_t attn_part_floats(int D, int num_sms);
 int64_t attn_segments(int B, int W, int H, int D, int Hq, int n_q);
 int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
-                         int* arrived, int num_sms, cudaStream_t s);
+                         int2* pieces, int num_sms, cudaStream_t s);
 int launch_kv8_attention_i8(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
-                            int* arrived, int num_sms, cudaStream_t s);
+                            int2* pieces, int num_sms, cudaStream_t s);
 int launch_kv8_attention_e4m3(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
-                              int* arrived, int num_sms, cudaStream_t s);
-int launch_xattn(const EncKV& kv, const QO& io, float* part, int* arrived, int num_sms, cudaStream_t s);
+                              int2* pieces, int num_sms, cudaStream_t s);
+int launch_xattn(const EncKV& kv, const QO& io, float* part, int2* pieces, int num_sms, cudaStream_t s);
 
 }  // namespace vbs

@@ -18,7 +18,7 @@ struct vbs_kv8 {
   int n_q;                        // of the last plan, 0: none yet
   vbs::Kv8Plan plan;
   float* part;                    // partials of rows split over CTAs, and their arrival counters
-  int* arrived;
+  int2* pieces;
   void* dev_block;
 };
 
@@ -27,7 +27,7 @@ struct vbs_xattn {
   cudaStream_t stream;
   int q_heads, max_q, max_len;
   float* part;
-  int* arrived;
+  int2* pieces;
   void* dev_block;
 };
 
@@ -61,7 +61,7 @@ VBS_EXPORT int kv8_init(vbs_kv8** out, vbs_pkv* kv, int format, float* scales, i
     c->plan.n_pages = cv.take<int>(a.B);
     c->plan.seen = cv.take<int>(kv->R);
     c->part = cv.take<float>(vbs::attn_part_floats(g.D, num_sms()));
-    c->arrived = cv.take<int>(vbs::attn_segments(a.B, a.W, g.H, g.D, q_heads, max_q));
+    c->pieces = cv.take<int2>(vbs::attn_segments(a.B, a.W, g.H, g.D, q_heads, max_q));
     if (pass == 0) {
       if (cudaMalloc(&c->dev_block, cv.off) != cudaSuccess) {
         cudaGetLastError();
@@ -116,7 +116,7 @@ VBS_EXPORT int kv8_attention(vbs_kv8* c, int layer, const void* q, int64_t q_row
                    o_head, c->n_q, c->q_heads, scale};
   vbs::Kv8Geom g = c->g;
   g.layer = layer;
-  return vbs::launch_kv8_attention(c->kv->a, g, io, c->plan, c->part, c->arrived, num_sms(), c->kv->stream);
+  return vbs::launch_kv8_attention(c->kv->a, g, io, c->plan, c->part, c->pieces, num_sms(), c->kv->stream);
 }
 
 VBS_EXPORT int kv8_destroy(vbs_kv8* c) {
@@ -155,7 +155,7 @@ VBS_EXPORT int xattn_init(vbs_xattn** out, int batch, int W, int q_heads, int kv
   for (int pass = 0; pass < 2; ++pass) {
     e.status = cv.take<int>(1);
     c->part = cv.take<float>(vbs::attn_part_floats(head_dim, num_sms()));
-    c->arrived = cv.take<int>(vbs::attn_segments(batch, W, kv_heads, head_dim, q_heads, max_q));
+    c->pieces = cv.take<int2>(vbs::attn_segments(batch, W, kv_heads, head_dim, q_heads, max_q));
     if (pass == 0) {
       if (cudaMalloc(&c->dev_block, cv.off) != cudaSuccess) {
         cudaGetLastError();
@@ -194,7 +194,7 @@ VBS_EXPORT int xattn_run(vbs_xattn* c, const void* q, int64_t q_row, int64_t q_t
   e.v_head = v_head;
   e.len = enc_len;
   e.S = len;
-  return vbs::launch_xattn(e, io, c->part, c->arrived, num_sms(), c->stream);
+  return vbs::launch_xattn(e, io, c->part, c->pieces, num_sms(), c->stream);
 }
 
 VBS_EXPORT int xattn_status(vbs_xattn* c) {

@@ -5,9 +5,9 @@
 namespace vbs {
 
 int launch_kv8_attention_i8(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
-                         int* arrived, int num_sms, cudaStream_t s) {
+                         int2* pieces, int num_sms, cudaStream_t s) {
   const PagedSrc<VBS_I8> src{g, p.list, p.n_pages, p.seen, a.S, (g.block + 15) / 16};
-  return launch_split<PagedSrc<VBS_I8>, true>(src, io, split_args(io, a.B, a.W, g.H, g.D, part, arrived), num_sms, s);
+  return launch_split<PagedSrc<VBS_I8>, true>(src, io, split_args(io, a.B, a.W, g.H, g.D, part, pieces), num_sms, s);
 }
 
 }  // namespace vbs

@@ -3,8 +3,8 @@
 // A segment is one sentence's K/V head with up to 16 MT of the query rows that read it (the W beams x
 // n_q tokens x q_heads / kv_heads rows that share it are numbered beam first).  Positions come in units
 // of at most 16.  All segments' units stand in one line, sentence by sentence; every CTA of one
-// resident wave takes an equal share of it, whatever the lengths (a segment counts SP_FIX units more than it
-// has, at its start), and its four warps take every fourth unit.  A segment inside one share is written straight out; one that crosses shares leaves
+// resident wave takes an equal share of it, whatever the lengths (a segment counts some units more than it
+// has, at its start), and its warps (four, or one where segments are many) take every fourth or every unit.  A segment inside one share is written straight out; one that crosses shares leaves
 // (m, l, o) partials, and the CTA that arrives last joins them in order, so equal calls give equal bits.
 //
 // A warp holds 16 MT rows x head_dim of o in registers.  Units come through a ring of cp.async stages of
@@ -27,12 +27,11 @@
 
 namespace vbs {
 
-constexpr int SP_WARPS = 4;
-constexpr int SP_NT = 32 * SP_WARPS;
-constexpr int SP_MIN = 4 * SP_WARPS;     // units a CTA takes at least: every warp's ring once
-// What a segment costs besides its units (Q, the first loads, the join), in units: a share with many short
-// segments takes as long as one with a single long one.
-constexpr int SP_FIX = 8;
+constexpr int SP_MIN = 4;                // units a warp takes at least: its ring once
+// What a segment costs a warp besides its units (Q, the first loads, the join), in units: a share with many
+// short segments takes as long as one with a single long one.
+constexpr int SP_FIX = 6;
+constexpr int SP_MANY = 0;
 
 // What the kernel needs to know of the split.
 struct SplitArgs {
@@ -41,8 +40,8 @@ struct SplitArgs {
   int M;                          // query rows per K/V head: W * n_q * G
   int MC;                         // chunks of 16 MT of them
   float* part;                    // [grid][2][16 MT][DP + 2]: o, m, l of a segment's piece
-  int* arrived;                   // [B * H * MC], zero between calls
-  bool out8;                      // outputs may be stored 8 bytes at a time
+  int2* pieces;                   // [B * H * MC]: the first and last CTA of a segment in pieces, (0, -1) of a whole one
+  bool out8, q8;                  // outputs may be stored, queries loaded 8 bytes at a time
 };
 
 __device__ __forceinline__ void cp_async16(u32 dst, const void* src, bool valid) {
@@ -185,26 +184,21 @@ struct EncSrc {
 // the kernel
 // ---------------------------------------------------------------------------------------
 
-constexpr int SP_SMS = 160;              // SMs the grid is laid out for at most (a join holds a factor a row and CTA)
-
-template <int EL, int DP, int MT> struct SplitCfg {
+template <int EL, int DP, int MT, int NW> struct SplitCfg {
   static constexpr int CHK = 16 / EL;                       // dims in 16 bytes
   static constexpr int KS = DP / 16;                        // contraction steps of the scores
   static constexpr int NT = DP / 8;                         // output tiles of 8 dims
   static constexpr int VCH = NT < CHK ? NT : CHK;           // dims of a position that a lane reads at once
-  static constexpr int UNIT = 2 * 16 * DP * EL;             // bytes of K and V of one unit
-  // Units of an iteration: two where the registers and the ring hold them, for twice the independent work
-  // between dependent steps (a score's sum over head_dim is a chain of mma's, the softmax a chain of shuffles).
-  static constexpr int U = MT == 1 && UNIT <= 4096 ? 2 : 1;
-  static constexpr int STAGE = U * UNIT;
+  static constexpr int STAGE = 2 * 16 * DP * EL;            // bytes of K and V of one unit
   static constexpr int NS = STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
   static constexpr int O_LD = DP + 4;                       // floats of an o row in shared memory
   static constexpr int RING = NS * STAGE > MT * 16 * O_LD * 4 ? NS * STAGE : MT * 16 * O_LD * 4;
   static constexpr int QBYTES = MT * KS * 512;              // Q in fragment order
   static constexpr int PART = MT * 16 * (DP + 2);           // floats of a partial
-  static constexpr size_t SMEM = SP_WARPS * RING + QBYTES;
-  // resident CTAs a SM, by shared memory and by registers (o is MT * DP / 2 of a thread's)
-  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 || (U == 2 && DP > 64) ? 2 : 3);
+  static constexpr size_t SMEM = NW * RING + QBYTES;
+  // resident warps a SM, by shared memory and by o's registers (MT * DP / 2 of a thread's)
+  static constexpr size_t SMEM4 = 4 * RING + QBYTES;
+  static constexpr int CTAS = (SMEM4 > 113 * 1024 ? 1 : (SMEM4 > 75 * 1024 || MT * DP > 128 ? 2 : 3)) * 4 / NW;
 };
 
 // The order of output dims: column n of output tile j.
@@ -216,28 +210,43 @@ template <int VCH> __device__ __forceinline__ int out_dim(int n, int j) {
 __device__ __forceinline__ int k_swz(int tok, int nc) { return (nc & 7) == 0 ? (tok & 1) << 2 : 0; }
 __device__ __forceinline__ int v_swz(int tok, int nc) { return (nc & 3) == 0 ? ((tok >> 1) & 3) << 1 : 0; }
 
+// Four dims of an output row.
+__device__ __forceinline__ void store_out(uint16_t* out, const SplitArgs& sa, const float4& v) {
+  const uint2 q = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  if (sa.out8) {
+    *reinterpret_cast<uint2*>(out) = q;
+  } else {
+    out[0] = static_cast<uint16_t>(q.x);
+    out[1] = static_cast<uint16_t>(q.x >> 16);
+    out[2] = static_cast<uint16_t>(q.y);
+    out[3] = static_cast<uint16_t>(q.y >> 16);
+  }
+}
+
 // EXACT: head_dim is DP; ALIGNED: K and V rows may be copied 16 bytes at a time.
-template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
-__global__ void __launch_bounds__(SP_NT, (SplitCfg<Src::EL, DP, MT>::CTAS))
+template <class Src, int DP, int MT, int NW, bool EXACT, bool ALIGNED>
+__global__ void __launch_bounds__(32 * NW, (SplitCfg<Src::EL, DP, MT, NW>::CTAS))
 attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
-  using C = SplitCfg<Src::EL, DP, MT>;
-  constexpr int EL = Src::EL, ROWS = 16 * MT, U = C::U;
+  using C = SplitCfg<Src::EL, DP, MT, NW>;
+  constexpr int NT = 32 * NW, FIX = SP_FIX * NW;
+  constexpr int EL = Src::EL, ROWS = 16 * MT;
   constexpr float GROW = Src::BF ? 8.f : 4.f;
   extern __shared__ __align__(128) unsigned char sp_smem[];
-  __shared__ UnitHead heads[SP_WARPS][C::NS][C::U];
+  __shared__ UnitHead heads[NW][C::NS];
   __shared__ float row_f[ROWS];                             // a row's factor on its dot products
-  __shared__ float wm[SP_WARPS][ROWS], wl[SP_WARPS][ROWS];
-  __shared__ int64_t s_sum[SP_WARPS];
+  __shared__ int64_t row_q[ROWS], row_o[ROWS];              // its elements in q (-1: none) and out
+  __shared__ int row_lim[ROWS], row_beam[ROWS];
+  __shared__ float wm[NW][ROWS], wl[NW][ROWS];
+  __shared__ int64_t s_sum[NW];
   __shared__ int s_b;
   __shared__ int64_t s_pos;
-  __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c4 = lane & 3;
   const int D = EXACT ? DP : sa.D;
   const int nc = D / C::CHK;                                // 16-byte chunks of a row
   unsigned char* ring = sp_smem + wid * C::RING;
   const u32 ring_a = smem_u32(ring);
-  uint16_t* qf = reinterpret_cast<uint16_t*>(sp_smem + SP_WARPS * C::RING);
+  uint16_t* qf = reinterpret_cast<uint16_t*>(sp_smem + NW * C::RING);
   const u32 qf_a = smem_u32(qf);
   const int HM = sa.H * sa.MC;
 
@@ -245,9 +254,9 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   int b = 0;
   int64_t at = 0, end, per;                                 // position within sentence b's units (all heads)
   {
-    const int k = (sa.B + SP_NT - 1) / SP_NT;               // a thread's sentences: [tid * k, tid * k + k)
+    const int k = (sa.B + NT - 1) / NT;               // a thread's sentences: [tid * k, tid * k + k)
     int64_t mine = 0;
-    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i) + SP_FIX;
+    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i) + FIX;
     int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -257,12 +266,12 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     if (lane == 31) s_sum[wid] = inc;
     __syncthreads();
     int64_t before = inc - mine, all = 0;
-    for (int w = 0; w < SP_WARPS; ++w) {
+    for (int w = 0; w < NW; ++w) {
       if (w < wid) before += s_sum[w];
       all += s_sum[w];
     }
     const int64_t total = all * HM;
-    per = max(static_cast<int64_t>(SP_MIN + SP_FIX), (total + gridDim.x - 1) / gridDim.x);
+    per = max(static_cast<int64_t>(SP_MIN * NW + FIX), (total + gridDim.x - 1) / gridDim.x);
     const int64_t from = per * blockIdx.x;
     end = min(total, from + per);
     if (from >= total) return;
@@ -270,7 +279,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       int64_t p = from - before * HM;
       int i = tid * k;
       for (; i < sa.B - 1; ++i) {
-        const int64_t n = static_cast<int64_t>(src.units(i) + SP_FIX) * HM;
+        const int64_t n = static_cast<int64_t>(src.units(i) + FIX) * HM;
         if (p < n) break;
         p -= n;
       }
@@ -285,11 +294,11 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   int64_t line0 = per * blockIdx.x - at;                    // the line's position of sentence b's first unit
 
   while (end > 0 && b < sa.B) {
-    const int n = src.units(b), nf = n + SP_FIX;
+    const int n = src.units(b), nf = n + FIX;
     const int hm = static_cast<int>(at / nf), h = hm / sa.MC, mc = hm - h * sa.MC;
     const int f0 = static_cast<int>(at - static_cast<int64_t>(hm) * nf);   // on the line; u0, u1: units
     const int f1 = static_cast<int>(min(static_cast<int64_t>(nf), f0 + end));
-    const int u0 = max(0, f0 - SP_FIX), u1 = f1 - SP_FIX;
+    const int u0 = max(0, f0 - FIX), u1 = f1 - FIX;
     auto advance = [&] {
       const int done = f1 - f0;
       end -= done;
@@ -307,90 +316,114 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     const int rho0 = mc * ROWS;
     const int rows = min(ROWS, sa.M - rho0);
 
-    const int mine = u1 - u0 > wid ? (u1 - u0 - wid + SP_WARPS - 1) / SP_WARPS : 0;
+    const int mine = u1 - u0 > wid ? (u1 - u0 - wid + NW - 1) / NW : 0;
     typename Src::Batch batch;
-    auto issue = [&](int k) {                               // the warp's units of iteration k into its stage
-      if (k * U < mine) {
-        if ((k * U & 31) == 0) {
-          const int x = k * U + lane;
-          src.fetch(batch, b, h, u0 + wid + x * SP_WARPS, x < mine);
-        }
+    auto issue = [&](int k) {                               // the warp's k-th unit into its stage
+      if (k < mine) {
+        if ((k & 31) == 0) src.fetch(batch, b, h, u0 + wid + (k + lane) * NW, k + lane < mine);
         const int st = k % C::NS;
+        const u32 base = ring_a + st * C::STAGE;
+        src.issue(batch, k & 31, lane, b, h, &heads[wid][st], [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
+          if (EXACT && EL == 1 && cnt == 16) {              // a whole unit of contiguous rows: constant offsets
+            const char *ks = kp + lane * 16, *vs = vp + lane * 16;
 #pragma unroll
-        for (int un = 0; un < U; ++un) {
-          const u32 base = ring_a + st * C::STAGE + un * C::UNIT;
-          src.issue(batch, (k * U + un) & 31, lane, b, h, &heads[wid][st][un],
-                    [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
-            if (EXACT && EL == 1 && cnt == 16) {            // a whole unit of contiguous rows: constant offsets
-              const char *ks = kp + lane * 16, *vs = vp + lane * 16;
-#pragma unroll
-              for (int i = 0; i < DP / C::CHK / 2; ++i) {
-                const int L = i * 32 + lane, tok = L / nc;
-                cp_async16(base + (L ^ k_swz(tok, nc)) * 16, ks + i * 512, true);
-                cp_async16(base + C::UNIT / 2 + (L ^ v_swz(tok, nc)) * 16, vs + i * 512, true);
-              }
-              return;
+            for (int i = 0; i < DP / C::CHK / 2; ++i) {
+              const int L = i * 32 + lane, tok = L / nc;
+              cp_async16(base + (L ^ k_swz(tok, nc)) * 16, ks + i * 512, true);
+              cp_async16(base + C::STAGE / 2 + (L ^ v_swz(tok, nc)) * 16, vs + i * 512, true);
             }
+            return;
+          }
 #pragma unroll
-            for (int i = 0; i < (DP / C::CHK + 1) / 2; ++i) {
-              const int L = i * 32 + lane;
-              const int tok = L / nc, ch = L - tok * nc;
-              if (EXACT || tok < 16) {
-                const bool ok = tok < cnt;
-                const char* ks = kp + (ok ? tok * kld + ch * 16 : 0);
-                const char* vs = vp + (ok ? tok * vld + ch * 16 : 0);
-                const u32 kd = base + (L ^ k_swz(tok, nc)) * 16;
-                const u32 vd = base + C::UNIT / 2 + (L ^ v_swz(tok, nc)) * 16;
-                if (ALIGNED) {
-                  cp_async16(kd, ks, ok);
-                  cp_async16(vd, vs, ok);
-                } else {
+          for (int i = 0; i < (DP / C::CHK + 1) / 2; ++i) {
+            const int L = i * 32 + lane;
+            const int tok = L / nc, ch = L - tok * nc;
+            if (EXACT || tok < 16) {
+              const bool ok = tok < cnt;
+              const char* ks = kp + (ok ? tok * kld + ch * 16 : 0);
+              const char* vs = vp + (ok ? tok * vld + ch * 16 : 0);
+              const u32 kd = base + (L ^ k_swz(tok, nc)) * 16;
+              const u32 vd = base + C::STAGE / 2 + (L ^ v_swz(tok, nc)) * 16;
+              if (ALIGNED) {
+                cp_async16(kd, ks, ok);
+                cp_async16(vd, vs, ok);
+              } else {
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const uint16_t x = ok ? reinterpret_cast<const uint16_t*>(ks)[e] : uint16_t{0};
-                    const uint16_t y = ok ? reinterpret_cast<const uint16_t*>(vs)[e] : uint16_t{0};
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(kd + e * 2), "h"(x) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(vd + e * 2), "h"(y) : "memory");
-                  }
+                for (int e = 0; e < 8; ++e) {
+                  const uint16_t x = ok ? reinterpret_cast<const uint16_t*>(ks)[e] : uint16_t{0};
+                  const uint16_t y = ok ? reinterpret_cast<const uint16_t*>(vs)[e] : uint16_t{0};
+                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(kd + e * 2), "h"(x) : "memory");
+                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(vd + e * 2), "h"(y) : "memory");
                 }
               }
             }
-          });
-        }
+          }
+        });
       }
       cp_commit();
     };
 #pragma unroll
     for (int k = 0; k < C::NS - 1; ++k) issue(k);
 
-    // ---- Q in fragment order, a warp a row ----
-    for (int r = wid; r < ROWS; r += SP_WARPS) {
-      const int rho = rho0 + r;
-      const bool live = r < rows;
-      const int gq = rho % sa.G, i = rho / sa.G % io.n_q, w = rho / sa.G / io.n_q;
-      const uint16_t* q = io.q + static_cast<int64_t>(b * sa.W + w) * io.q_row + i * io.q_tok + (h * sa.G + gq) * io.q_head;
-      u32 x[DP / 32];
+    // ---- where the segment's rows stand and what they see, divided out once ----
+    if (tid < ROWS) {
+      const int rho = rho0 + tid, gq = rho % sa.G, iw = rho / sa.G, i = iw % io.n_q, w = iw / io.n_q;
+      const bool live = tid < rows;
+      const int64_t row = static_cast<int64_t>(b) * sa.W + w, head = h * sa.G + gq;
+      row_q[tid] = live ? row * io.q_row + i * io.q_tok + head * io.q_head : -1;
+      row_o[tid] = row * io.o_row + i * io.o_tok + head * io.o_head;
+      row_lim[tid] = live ? src.limit(b, w, i, sa.W, io.n_q) : 1 << 30;
+      row_beam[tid] = live ? w : 31;                        // padding rows see everything, and are not written
+    }
+    if (NW > 1) __syncthreads();
+    else __syncwarp();
+
+    // ---- Q in fragment order: a warp a row, four dims a lane, the loads of four rows at once ----
+    constexpr int QV = (DP + 127) / 128;
 #pragma unroll
-      for (int t = 0; t < DP / 32; ++t) x[t] = live && t * 32 + lane < D ? q[t * 32 + lane] : 0;
-      float up = 1.f;                                       // the row's power of two: its largest element to [1, 2)
-      if (!Src::BF) {
-        u32 top = 0;
+    for (int r0 = 0; r0 < ROWS; r0 += 4 * NW) {
+      uint2 x[4][QV];
 #pragma unroll
-        for (int t = 0; t < DP / 32; ++t) top = max(top, x[t] & 0x7fffu);
+      for (int k = 0; k < 4; ++k) {
+        const int64_t off = row_q[r0 + k * NW + wid];
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) top = max(top, __shfl_xor_sync(FULL, top, k));
-        const int ex = static_cast<int>(top >> 7);          // biased exponent
-        up = __int_as_float(max(1, min(254, 254 - ex)) << 23);
+        for (int v = 0; v < QV; ++v) {
+          const int d = v * 128 + lane * 4;
+          x[k][v] = make_uint2(0, 0);
+          if (off >= 0 && d < D) {
+            const uint16_t* q = io.q + off + d;
+            if (sa.q8) x[k][v] = *reinterpret_cast<const uint2*>(q);
+            else x[k][v] = make_uint2(q[0] | static_cast<u32>(q[1]) << 16, q[2] | static_cast<u32>(q[3]) << 16);
+          }
+        }
       }
-      if (lane == 0) row_f[r] = io.scale * LOG2E_F / up;
 #pragma unroll
-      for (int t = 0; t < DP / 32; ++t) {
-        const int d = t * 32 + lane, ch = d / C::CHK, in = d % C::CHK;
-        const int ks = (ch >> 2) * (C::CHK / 4) + in / 4;
-        const int ln = (r & 7) * 4 + (ch & 3), reg = ((r >> 3) & 1) + (in & 2);
-        const uint16_t v = Src::BF ? static_cast<uint16_t>(x[t])
-                                   : __half_as_ushort(__float2half_rn(__uint_as_float(x[t] << 16) * up));
-        qf[((((r >> 4) * C::KS + ks) * 32 + ln) * 4 + reg) * 2 + (in & 1)] = v;
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k * NW + wid;
+        float up = 1.f;                                     // the row's power of two: its largest element to [1, 2)
+        if (!Src::BF) {
+          u32 top = 0;
+#pragma unroll
+          for (int v = 0; v < QV; ++v)
+            top = max(max(top, max(x[k][v].x & 0x7fffu, x[k][v].x >> 16 & 0x7fffu)),
+                      max(x[k][v].y & 0x7fffu, x[k][v].y >> 16 & 0x7fffu));
+#pragma unroll
+          for (int e = 16; e > 0; e >>= 1) top = max(top, __shfl_xor_sync(FULL, top, e));
+          const int ex = static_cast<int>(top >> 7);        // biased exponent
+          up = __int_as_float(max(1, min(254, 254 - ex)) << 23);
+        }
+        if (lane == 0) row_f[r] = io.scale * LOG2E_F / up;
+#pragma unroll
+        for (int v = 0; v < QV; ++v) {
+          const int d = v * 128 + lane * 4, ch = d / C::CHK;
+          if (d >= DP) continue;
+          const int ks = (ch >> 2) * (C::CHK / 4) + d % C::CHK / 4;
+          const u32 to = (((r >> 4) * C::KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * 4 + ((r >> 3) & 1);
+          u32* qw = reinterpret_cast<u32*>(qf);
+          const uint2 y = x[k][v];
+          qw[to] = Src::BF ? y.x : pack_f16(bf16_lo(y.x) * up, bf16_hi(y.x) * up);
+          qw[to + 2] = Src::BF ? y.y : pack_f16(bf16_lo(y.y) * up, bf16_hi(y.y) * up);
+        }
       }
     }
     __syncthreads();
@@ -401,48 +434,44 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int r = mt * 16 + x * 8 + g, rho = rho0 + r;
+        const int r = mt * 16 + x * 8 + g;
         m[mt][x] = -INFINITY;
         l[mt][x] = 0.f;
         f[mt][x] = row_f[r];
-        const int w = rho / sa.G / io.n_q;
-        lim[mt][x] = r < rows ? src.limit(b, w, rho / sa.G % io.n_q, sa.W, io.n_q) : 1 << 30;
-        beam[mt][x] = r < rows ? w : 31;                    // padding rows see everything, and are not written
+        lim[mt][x] = row_lim[r];
+        beam[mt][x] = row_beam[r];
 #pragma unroll
         for (int j = 0; j < C::NT; ++j) o[mt][j][x * 2] = o[mt][j][x * 2 + 1] = 0.f;
       }
 
-    for (int k = 0; k * U < mine; ++k) {
+    for (int k = 0; k < mine; ++k) {
       cp_wait<C::NS - 2>();
       __syncwarp();
       issue(k + C::NS - 1);
       const int st = k % C::NS;
-      const u32 ka = ring_a + st * C::STAGE;
-      UnitHead u[U];
-#pragma unroll
-      for (int un = 0; un < U; ++un) u[un] = heads[wid][st][un];
+      const u32 ka = ring_a + st * C::STAGE, va = ka + C::STAGE / 2;
+      const UnitHead u = heads[wid][st];
 
-      // ---- scores: two tiles of 8 positions a unit ----
-      float s[MT][2 * U][4];
+      // ---- scores of 16 positions: two tiles of 8 ----
+      float s[MT][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < 2 * U; ++t) s[mt][t][0] = s[mt][t][1] = s[mt][t][2] = s[mt][t][3] = 0.f;
+        for (int t = 0; t < 2; ++t) s[mt][t][0] = s[mt][t][1] = s[mt][t][2] = s[mt][t][3] = 0.f;
 #pragma unroll
       for (int grp = 0; grp < DP / C::CHK / 4; ++grp) {
-        uint4 kw[2 * U];
+        uint4 kw[2];
 #pragma unroll
-        for (int t = 0; t < 2 * U; ++t) {
-          const int tok = (t & 1) * 8 + g, ch = grp * 4 + c4;
-          kw[t] = EXACT || ch < nc ? lds16(ka + (t >> 1) * C::UNIT + ((tok * nc + ch) ^ k_swz(tok, nc)) * 16)
-                                   : make_uint4(0, 0, 0, 0);
+        for (int t = 0; t < 2; ++t) {
+          const int tok = t * 8 + g, ch = grp * 4 + c4;
+          kw[t] = EXACT || ch < nc ? lds16(ka + ((tok * nc + ch) ^ k_swz(tok, nc)) * 16) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int q4 = 0; q4 < C::CHK / 4; ++q4) {
           const int ks = grp * (C::CHK / 4) + q4;
-          u32 b0[2 * U], b1[2 * U];
+          u32 b0[2], b1[2];
 #pragma unroll
-          for (int t = 0; t < 2 * U; ++t) {
+          for (int t = 0; t < 2; ++t) {
             const u32 words[4] = {kw[t].x, kw[t].y, kw[t].z, kw[t].w};
             if (EL == 1) {
               codes4<Src::FORMAT>(words[q4], b0[t], b1[t]);
@@ -454,41 +483,34 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const uint4 a = lds16(qf_a + ((mt * C::KS + ks) * 32 + lane) * 16);
-#pragma unroll
-            for (int t = 0; t < 2 * U; ++t) mma16816<Src::BF>(s[mt][t], a, b0[t], b1[t]);
+            mma16816<Src::BF>(s[mt][0], a, b0[0], b1[0]);
+            mma16816<Src::BF>(s[mt][1], a, b0[1], b1[1]);
           }
         }
       }
 
       // ---- softmax: weights relative to the running maximum of s + log2(V's scale) ----
-      uint4 p[MT][U], p2[MT][U];
+      uint4 p[MT], p2[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        int left[2][U];
-        bool all = true;
+        int left[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int un = 0; un < U; ++un) {
-            left[x][un] = (u[un].rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? min(lim[mt][x] - u[un].pos, u[un].n) : 0;
-            all = all && left[x][un] >= 16;
-          }
-        const bool full = __all_sync(FULL, all);
+        for (int x = 0; x < 2; ++x) left[x] = (u.rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? min(lim[mt][x] - u.pos, u.n) : 0;
+        const bool full = __all_sync(FULL, left[0] >= 16 && left[1] >= 16);
         float mx[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          const float fk = f[mt][x] * u.ks;
           mx[x] = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < 2 * U; ++t) {
-            const float fk = f[mt][x] * u[t >> 1].ks;
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               float& z = s[mt][t][x * 2 + y];
-              z = fmaf(z, fk, u[t >> 1].ve);
-              if (!full && (t & 1) * 8 + c4 * 2 + y >= left[x][t >> 1]) z = -INFINITY;
+              z = fmaf(z, fk, u.ve);
+              if (!full && t * 8 + c4 * 2 + y >= left[x]) z = -INFINITY;
               mx[x] = fmaxf(mx[x], z);
             }
-          }
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 1));
           mx[x] = fmaxf(mx[x], __shfl_xor_sync(FULL, mx[x], 2));
         }
@@ -507,94 +529,84 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
             m[mt][x] = mx[x];
           }
         }
-        // fp16 weights reach up to 2^15, so that small ones keep their bits
-        float ref[2];
+        float w[2][4];                                      // [row][position]
 #pragma unroll
-        for (int x = 0; x < 2; ++x) ref[x] = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f - GROW);
+        for (int x = 0; x < 2; ++x) {
+          // fp16 weights reach up to 2^15, so that small ones keep their bits
+          const float ref = (m[mt][x] == -INFINITY ? 0.f : m[mt][x]) - (Src::BF ? 0.f : 15.f - GROW);
+          float sum = 0.f;
 #pragma unroll
-        for (int un = 0; un < U; ++un) {
-          float w[2][4];                                    // [row][position]
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float sum = 0.f;
+            for (int y = 0; y < 2; ++y) {
+              w[x][t * 2 + y] = ex2(s[mt][t][x * 2 + y] - ref);
+              sum += w[x][t * 2 + y];
+            }
+          l[mt][x] = Src::BF ? l[mt][x] + sum : fmaf(sum, u.vinv, l[mt][x]);
+        }
+        if (Src::BF) {
+          // two bf16 parts of each weight: the products carry 16 bits of it
+          float r[2][4];
+          p[mt] = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
+                             pack_bf16(w[1][2], w[1][3]));
+          const u32 hi[2][2] = {{p[mt].x, p[mt].z}, {p[mt].y, p[mt].w}};
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                w[x][t * 2 + y] = ex2(s[mt][un * 2 + t][x * 2 + y] - ref[x]);
-                sum += w[x][t * 2 + y];
-              }
-            l[mt][x] = Src::BF ? l[mt][x] + sum : fmaf(sum, u[un].vinv, l[mt][x]);
-          }
-          if (Src::BF) {
-            // two bf16 parts of each weight: the products carry 16 bits of it
-            float r[2][4];
-            uint4& q = p[mt][un];
-            q = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
-                           pack_bf16(w[1][2], w[1][3]));
-            const u32 hi[2][2] = {{q.x, q.z}, {q.y, q.w}};
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                r[x][t * 2] = w[x][t * 2] - bf16_lo(hi[x][t]);
-                r[x][t * 2 + 1] = w[x][t * 2 + 1] - bf16_hi(hi[x][t]);
-              }
-            p2[mt][un] = make_uint4(pack_bf16(r[0][0], r[0][1]), pack_bf16(r[1][0], r[1][1]), pack_bf16(r[0][2], r[0][3]),
-                                    pack_bf16(r[1][2], r[1][3]));
-          } else {
-            p[mt][un] = make_uint4(pack_f16(w[0][0], w[0][1]), pack_f16(w[1][0], w[1][1]), pack_f16(w[0][2], w[0][3]),
-                                   pack_f16(w[1][2], w[1][3]));
-          }
+            for (int t = 0; t < 2; ++t) {
+              r[x][t * 2] = w[x][t * 2] - bf16_lo(hi[x][t]);
+              r[x][t * 2 + 1] = w[x][t * 2 + 1] - bf16_hi(hi[x][t]);
+            }
+          p2[mt] = make_uint4(pack_bf16(r[0][0], r[0][1]), pack_bf16(r[1][0], r[1][1]), pack_bf16(r[0][2], r[0][3]),
+                              pack_bf16(r[1][2], r[1][3]));
+        } else {
+          p[mt] = make_uint4(pack_f16(w[0][0], w[0][1]), pack_f16(w[1][0], w[1][1]), pack_f16(w[0][2], w[0][3]),
+                             pack_f16(w[1][2], w[1][3]));
         }
       }
 
       // ---- o += P V ----
       const int toks[4] = {c4 * 2, c4 * 2 + 1, c4 * 2 + 8, c4 * 2 + 9};
 #pragma unroll
-      for (int un = 0; un < U; ++un) {
-        const u32 va = ka + un * C::UNIT + C::UNIT / 2;
+      for (int vc = 0; vc < C::NT / C::VCH; ++vc) {
+        u32 vw[4][4];
 #pragma unroll
-        for (int vc = 0; vc < C::NT / C::VCH; ++vc) {
-          u32 vw[4][4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int dim = out_dim<C::VCH>(g, vc * C::VCH), ch = dim / C::CHK;
-            const u32 a = va + ((toks[t] * nc + ch) ^ v_swz(toks[t], nc)) * 16;
-            if (EXACT || dim < D) {
-              if (C::VCH * EL == 16) {
-                const uint4 q = lds16(a);
-                vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = q.z; vw[t][3] = q.w;
-              } else {
-                const uint2 q = lds8(a + (dim % C::CHK) * EL);
-                vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = vw[t][3] = 0;
-              }
+        for (int t = 0; t < 4; ++t) {
+          const int dim = out_dim<C::VCH>(g, vc * C::VCH), ch = dim / C::CHK;
+          const u32 a = va + ((toks[t] * nc + ch) ^ v_swz(toks[t], nc)) * 16;
+          if (EXACT || dim < D) {
+            if (C::VCH * EL == 16) {
+              const uint4 q = lds16(a);
+              vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = q.z; vw[t][3] = q.w;
             } else {
-              vw[t][0] = vw[t][1] = vw[t][2] = vw[t][3] = 0;
+              const uint2 q = lds8(a + (dim % C::CHK) * EL);
+              vw[t][0] = q.x; vw[t][1] = q.y; vw[t][2] = vw[t][3] = 0;
             }
+          } else {
+            vw[t][0] = vw[t][1] = vw[t][2] = vw[t][3] = 0;
           }
+        }
 #pragma unroll
-          for (int wd = 0; wd < C::VCH * EL / 4; ++wd) {
-            if (EL == 1) {
-              u32 b0[4], b1[4];                             // four dims, positions 0,1 and 2,3 of the lane
-              codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x5140), b0[0], b0[1]);
-              codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x7362), b0[2], b0[3]);
-              codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x5140), b1[0], b1[1]);
-              codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x7362), b1[2], b1[3]);
+        for (int wd = 0; wd < C::VCH * EL / 4; ++wd) {
+          if (EL == 1) {
+            u32 b0[4], b1[4];                               // four dims, positions 0,1 and 2,3 of the lane
+            codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x5140), b0[0], b0[1]);
+            codes4<Src::FORMAT>(__byte_perm(vw[0][wd], vw[1][wd], 0x7362), b0[2], b0[3]);
+            codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x5140), b1[0], b1[1]);
+            codes4<Src::FORMAT>(__byte_perm(vw[2][wd], vw[3][wd], 0x7362), b1[2], b1[3]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma16816<false>(o[mt][vc * C::VCH + wd * 4 + i], p[mt][un], b0[i], b1[i]);
-            } else {
+              for (int mt = 0; mt < MT; ++mt) mma16816<false>(o[mt][vc * C::VCH + wd * 4 + i], p[mt], b0[i], b1[i]);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const u32 b0 = __byte_perm(vw[0][wd], vw[1][wd], i ? 0x7632 : 0x5410);
-                const u32 b1 = __byte_perm(vw[2][wd], vw[3][wd], i ? 0x7632 : 0x5410);
+            for (int i = 0; i < 2; ++i) {
+              const u32 b0 = __byte_perm(vw[0][wd], vw[1][wd], i ? 0x7632 : 0x5410);
+              const u32 b1 = __byte_perm(vw[2][wd], vw[3][wd], i ? 0x7632 : 0x5410);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p[mt][un], b0, b1);
-                  mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt][un], b0, b1);
-                }
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p[mt], b0, b1);
+                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt], b0, b1);
               }
             }
           }
@@ -632,9 +644,9 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     if (tid < ROWS) {
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < SP_WARPS; ++w) top = fmaxf(top, wm[w][tid]);
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, wm[w][tid]);
 #pragma unroll
-      for (int w = 0; w < SP_WARPS; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float x = wm[w][tid] == -INFINITY ? 0.f : ex2(wm[w][tid] - top);
         sum += wl[w][tid] * x;                              // (a NaN stays one)
         wm[w][tid] = x;
@@ -642,94 +654,134 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       if (whole) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int w = 0; w < SP_WARPS; ++w) wm[w][tid] *= inv;
+        for (int w = 0; w < NW; ++w) wm[w][tid] *= inv;
       } else {
         part[ROWS * DP + tid] = top;
         part[ROWS * DP + ROWS + tid] = sum;
       }
     }
     __syncthreads();
-    auto store = [&](int r, int d, const float4& v) {       // four dims of an output row
-      const int rho = rho0 + r;
-      const int gq = rho % sa.G, i = rho / sa.G % io.n_q, w = rho / sa.G / io.n_q;
-      uint16_t* out = io.o + static_cast<int64_t>(b * sa.W + w) * io.o_row + i * io.o_tok + (h * sa.G + gq) * io.o_head + d;
-      const uint2 q = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-      if (sa.out8) {
-        *reinterpret_cast<uint2*>(out) = q;
-      } else {
-        out[0] = static_cast<uint16_t>(q.x);
-        out[1] = static_cast<uint16_t>(q.x >> 16);
-        out[2] = static_cast<uint16_t>(q.y);
-        out[3] = static_cast<uint16_t>(q.y >> 16);
-      }
-    };
-    for (int idx = tid; idx < rows * (DP / 4); idx += SP_NT) {
+    for (int idx = tid; idx < rows * (DP / 4); idx += NT) {
       const int r = idx / (DP / 4), d = idx % (DP / 4) * 4;
       if (!EXACT && d >= D) continue;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < SP_WARPS; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float x = wm[w][r];
         if (x != 0.f) {
           const float4 v = *reinterpret_cast<const float4*>(sp_smem + w * C::RING + (r * C::O_LD + d) * 4);
           a.x += v.x * x; a.y += v.y * x; a.z += v.z * x; a.w += v.w * x;
         }
       }
-      if (whole) store(r, d, a);
+      if (whole) store_out(io.o + row_o[r] + d, sa, a);
       else *reinterpret_cast<float4*>(part + r * DP + d) = a;
     }
 
-    // ---- join the pieces of a segment that crosses shares ----
-    if (!whole) {
-      const int64_t seg = static_cast<int64_t>(b) * HM + hm;
-      const int first = static_cast<int>((line + SP_FIX) / per), last = static_cast<int>((line + nf - 1) / per);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomic_add_acq_rel(sa.arrived + seg, 1) == last - first;
-      __syncthreads();
-      if (s_last) {
-        auto piece = [&](int c) { return sa.part + (static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * C::PART; };
-        // each piece's factor of each row: a warp a row, a lane a piece
-        float* fac = reinterpret_cast<float*>(sp_smem);     // [rows][pieces]
-        const int np = last - first + 1;
-        for (int r = wid; r < rows; r += SP_WARPS) {
-          float top = -INFINITY, sum = 0.f;
-          for (int c = lane; c < np; c += 32) {
-            const float mm = __ldcg(piece(first + c) + ROWS * DP + r);
-            fac[r * np + c] = mm;
-            top = fmaxf(top, mm);
-          }
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, k));
-          for (int c = lane; c < np; c += 32) {
-            const float mm = fac[r * np + c];
-            const float x = mm == -INFINITY ? 0.f : ex2(mm - top);
-            sum += __ldcg(piece(first + c) + ROWS * DP + ROWS + r) * x;     // (a NaN stays one)
-            fac[r * np + c] = x;
-          }
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(FULL, sum, k);
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          for (int c = lane; c < np; c += 32) fac[r * np + c] *= inv;
-        }
-        __syncthreads();
-        for (int idx = tid; idx < rows * (DP / 4); idx += SP_NT) {
-          const int r = idx / (DP / 4), d = idx % (DP / 4) * 4;
-          if (!EXACT && d >= D) continue;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int c = 0; c < np; ++c) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(first + c) + r * DP + d));
-            const float x = fac[r * np + c];
-            a.x += v.x * x; a.y += v.y * x; a.z += v.z * x; a.w += v.w * x;
-          }
-          store(r, d, a);
-        }
-        if (tid == 0) sa.arrived[seg] = 0;
-      }
-    }
+    // the CTA with a segment's first unit says where its pieces are
+    if (u0 == 0 && tid == 0)
+      sa.pieces[static_cast<int64_t>(b) * HM + hm] =
+          whole ? make_int2(0, -1) : make_int2(static_cast<int>((line + FIX) / per), static_cast<int>((line + nf - 1) / per));
     __syncthreads();                                        // the ring and the row statistics are free again
     advance();
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// the join of segments in pieces
+// ---------------------------------------------------------------------------------------
+
+constexpr int JN_WARPS = 4;
+
+// CTA (segment, c): rows 4 c .. 4 c + 3 of its segment, a warp each; where the pieces are many, all warps take
+// a row after the other and share its pieces.  A dependent launch: it is set up while the split kernel runs.
+template <int DP, int ROWS>
+__global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, const SplitArgs sa) {
+  constexpr int PART = ROWS * (DP + 2), V = DP / 128 > 0 ? DP / 128 : 1;   // float4s of a row that a lane holds
+  __shared__ float4 so[JN_WARPS][DP / 4];
+  __shared__ float sm[JN_WARPS], sl[JN_WARPS];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t seg = blockIdx.x;
+  const int2 at = __ldcg(sa.pieces + seg);
+  if (at.y < at.x) return;
+  const int mc = static_cast<int>(seg % sa.MC);
+  const int64_t bh = seg / sa.MC;
+  const int h = static_cast<int>(bh % sa.H), b = static_cast<int>(bh / sa.H);
+  const int rows = min(ROWS, sa.M - mc * ROWS), np = at.y - at.x + 1;
+  auto piece = [&](int c) { return sa.part + (static_cast<int64_t>(at.x + c) * 2 + (c == 0 ? 1 : 0)) * PART; };
+  // one row's pieces c0, c0 + step, ... : their reference, sum and weighted sum
+  auto gather = [&](int r, int c0, int step, float& top, float& sum, float4 (&a)[V]) {
+    top = -INFINITY;
+    for (int c = c0 + step * lane; c < np; c += step * 32) top = fmaxf(top, __ldcg(piece(c) + ROWS * DP + r));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, k));
+    sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+    for (int c = c0; c < np; c += step) {
+      const float* pp = piece(c);
+      const float mm = __ldcg(pp + ROWS * DP + r), ll = __ldcg(pp + ROWS * DP + ROWS + r);
+      const float x = mm == -INFINITY ? 0.f : ex2(mm - top);
+      sum += ll * x;                                        // (a NaN stays one)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (lane * 4 + v * 128 < DP) {
+          const float4 q = __ldcg(reinterpret_cast<const float4*>(pp + r * DP + v * 128) + lane);
+          a[v].x += q.x * x; a[v].y += q.y * x; a[v].z += q.z * x; a[v].w += q.w * x;
+        }
+    }
+  };
+  auto out_row = [&](int r) {
+    const int rho = mc * ROWS + r, gq = rho % sa.G, iw = rho / sa.G;
+    return io.o + (static_cast<int64_t>(b) * sa.W + iw / io.n_q) * io.o_row + iw % io.n_q * io.o_tok +
+           static_cast<int64_t>(h * sa.G + gq) * io.o_head;
+  };
+  float4 a[V];
+  float top, sum;
+  if (np <= 64 * JN_WARPS) {
+    const int r = blockIdx.y * JN_WARPS + wid;
+    if (r >= rows) return;
+    gather(r, 0, 1, top, sum, a);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int d = lane * 4 + v * 128;
+      if (d < sa.D) store_out(out_row(r) + d, sa, make_float4(a[v].x * inv, a[v].y * inv, a[v].z * inv, a[v].w * inv));
+    }
+    return;
+  }
+  for (int r = blockIdx.y * JN_WARPS; r < min(rows, (static_cast<int>(blockIdx.y) + 1) * JN_WARPS); ++r) {
+    gather(r, wid, JN_WARPS, top, sum, a);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane * 4 + v * 128 < DP) so[wid][lane + v * 32] = a[v];
+    if (lane == 0) {
+      sm[wid] = top;
+      sl[wid] = sum;
+    }
+    __syncthreads();
+    float all = sm[0];
+#pragma unroll
+    for (int w = 1; w < JN_WARPS; ++w) all = fmaxf(all, sm[w]);
+    float total = 0.f, f[JN_WARPS];
+#pragma unroll
+    for (int w = 0; w < JN_WARPS; ++w) {
+      f[w] = sm[w] == -INFINITY ? 0.f : ex2(sm[w] - all);
+      total += sl[w] * f[w];
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    for (int d = threadIdx.x * 4; d < sa.D; d += 32 * JN_WARPS * 4) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < JN_WARPS; ++w) {
+        const float4 q = so[w][d / 4];
+        const float x = f[w] * inv;
+        o.x += q.x * x; o.y += q.y * x; o.z += q.z * x; o.w += q.w * x;
+      }
+      store_out(out_row(r) + d, sa, o);
+    }
+    __syncthreads();
   }
 }
 
@@ -742,28 +794,49 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 inline int split_mt(int M, int D) { return M > 16 && D <= 128 ? 2 : 1; }
 inline int split_chunks(int M, int D) { return (M + 16 * split_mt(M, D) - 1) / (16 * split_mt(M, D)); }
 inline int split_dp(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
-// floats of the partials of a grid of 3 CTAs a SM, for any number of rows
+// floats of the partials of any grid: up to 12 warps a SM, of up to 32 rows
 inline int64_t split_part_floats(int D, int num_sms) {
-  return static_cast<int64_t>(num_sms) * 3 * 2 * (D <= 128 ? 32 : 16) * (split_dp(D) + 2);
+  return static_cast<int64_t>(num_sms) * 12 * 2 * 32 * (split_dp(D) + 2);
+}
+
+template <class Src, int DP, int MT, int NW, bool EXACT, bool ALIGNED>
+int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
+  using C = SplitCfg<Src::EL, DP, MT, NW>;
+  static std::atomic<unsigned long long> attr_done{0};
+  auto* kernel = attn_split_kernel<Src, DP, MT, NW, EXACT, ALIGNED>;
+  if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
+  kernel<<<num_sms * C::CTAS, 32 * NW, C::SMEM, s>>>(src, io, sa);
+  if (cudaGetLastError() != cudaSuccess) return VBS_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(sa.B) * sa.H * sa.MC), (std::min(sa.M, 16 * MT) + JN_WARPS - 1) / JN_WARPS);
+  cfg.blockDim = dim3(32 * JN_WARPS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP, 16 * MT>, io, sa) == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
 template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
-int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
-  using C = SplitCfg<Src::EL, DP, MT>;
-  static std::atomic<unsigned long long> attr_done{0};
-  auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
-  if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
-  static_assert(16 * MT * SP_SMS * C::CTAS * 4 <= SP_WARPS * C::RING, "the join's factors fit the ring");
-  kernel<<<std::min(num_sms, SP_SMS) * C::CTAS, SP_NT, C::SMEM, s>>>(src, io, sa);
-  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+int launch_split_nw(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
+  // With many segments for the CTAs of four warps, a share would hold several short pieces one after the
+  // other: single warps take them side by side, and the join does what the CTA's own would have.
+  if constexpr (DP <= 128) {
+    const int64_t segments = static_cast<int64_t>(sa.B) * sa.H * sa.MC;
+    if (segments * SP_MANY > static_cast<int64_t>(num_sms) * SplitCfg<Src::EL, DP, MT, 4>::CTAS)
+      return launch_split_as<Src, DP, MT, 1, EXACT, ALIGNED>(src, io, sa, num_sms, s);
+  }
+  return launch_split_as<Src, DP, MT, 4, EXACT, ALIGNED>(src, io, sa, num_sms, s);
 }
 
 template <class Src, int DP, int MT, bool ALIGNED>
 int launch_split_dp(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
   if constexpr (ALIGNED) {
-    if (sa.D == DP) return launch_split_as<Src, DP, MT, true, true>(src, io, sa, num_sms, s);
+    if (sa.D == DP) return launch_split_nw<Src, DP, MT, true, true>(src, io, sa, num_sms, s);
   }
-  return launch_split_as<Src, DP, MT, false, ALIGNED>(src, io, sa, num_sms, s);
+  return launch_split_nw<Src, DP, MT, false, ALIGNED>(src, io, sa, num_sms, s);
 }
 
 template <class Src, bool ALIGNED>
@@ -778,10 +851,11 @@ int launch_split(const Src& src, const QO& io, const SplitArgs& sa, int num_sms,
   return launch_split_dp<Src, 256, 1, ALIGNED>(src, io, sa, num_sms, s);
 }
 
-inline SplitArgs split_args(const QO& io, int B, int W, int H, int D, float* part, int* arrived) {
-  SplitArgs sa{B, W, H, D, io.Hq / H, W * io.n_q * (io.Hq / H), 0, part, arrived, false};
+inline SplitArgs split_args(const QO& io, int B, int W, int H, int D, float* part, int2* pieces) {
+  SplitArgs sa{B, W, H, D, io.Hq / H, W * io.n_q * (io.Hq / H), 0, part, pieces, false, false};
   sa.MC = split_chunks(sa.M, D);
-  sa.out8 = (reinterpret_cast<uintptr_t>(io.o) & 7) == 0 && io.o_row % 4 == 0 && io.o_tok % 4 == 0 && io.o_head % 4 == 0;
+  sa.out8 = (reinterpret_cast<uintptr_t>(io.o) & 7) == 0 && (io.o_row | io.o_tok | io.o_head) % 4 == 0;
+  sa.q8 = (reinterpret_cast<uintptr_t>(io.q) & 7) == 0 && (io.q_row | io.q_tok | io.q_head) % 4 == 0;
   return sa;
 }
 

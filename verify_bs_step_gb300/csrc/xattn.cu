@@ -5,10 +5,10 @@
 
 namespace vbs {
 
-int launch_xattn(const EncKV& e, const QO& io, float* part, int* arrived, int num_sms, cudaStream_t s) {
+int launch_xattn(const EncKV& e, const QO& io, float* part, int2* pieces, int num_sms, cudaStream_t s) {
   if (xattn_tc_takes(e, io, num_sms)) return launch_xattn_tc(e, io, num_sms, s);
   const EncSrc src{e};
-  const SplitArgs sa = split_args(io, e.B, e.W, e.H, e.D, part, arrived);
+  const SplitArgs sa = split_args(io, e.B, e.W, e.H, e.D, part, pieces);
   const bool aligned = ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 &&
                        (e.k_sent | e.k_pos | e.k_head | e.v_sent | e.v_pos | e.v_head) % 8 == 0;
   return aligned ? launch_split<EncSrc, true>(src, io, sa, num_sms, s) : launch_split<EncSrc, false>(src, io, sa, num_sms, s);
