@@ -25,6 +25,8 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, co
   __shared__ int seen[WMAX];
   __shared__ int sums[PLAN_NT / 32];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, W = a.W;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid < W) {
     seen[tid] = held_len(a, ctx, b * W + tid);
     p.seen[b * W + tid] = seen[tid];
@@ -94,6 +96,8 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, co
 // One row a sentence: the list is the table's row; CTA (b, c) copies every c-th chunk of it.
 __global__ void __launch_bounds__(PLAN_NT) kv8_plan_rows_kernel(const PagedArgs a, const int32_t* ctx, const Kv8Plan p) {
   const int b = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int seen = held_len(a, ctx, b);
   const int cols = (seen + a.block - 1) / a.block;
   int4* list = p.list + static_cast<int64_t>(b) * a.S;
@@ -113,11 +117,9 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_rows_kernel(const PagedArgs 
 int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, const Kv8Plan& p, cudaStream_t s) {
   if (a.W == 1) {
     const int chunks = std::min((std::min(a.MB, a.S) + PLAN_NT - 1) / PLAN_NT, 64);
-    kv8_plan_rows_kernel<<<dim3(a.B, chunks), PLAN_NT, 0, s>>>(a, ctx, p);
-  } else {
-    kv8_plan_kernel<<<a.B, PLAN_NT, 0, s>>>(a, ctx, p);
+    return launch_dependent(kv8_plan_rows_kernel, dim3(a.B, chunks), dim3(PLAN_NT), 0, s, a, ctx, p);
   }
-  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+  return launch_dependent(kv8_plan_kernel, dim3(a.B), dim3(PLAN_NT), 0, s, a, ctx, p);
 }
 
 int64_t attn_part_floats(int D, int num_sms) { return split_part_floats(D, num_sms); }

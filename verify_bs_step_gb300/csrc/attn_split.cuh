@@ -3,9 +3,11 @@
 // A segment is one sentence's K/V head with up to 16 MT of the query rows that read it (the W beams x
 // n_q tokens x q_heads / kv_heads rows that share it are numbered beam first).  Positions come in units
 // of at most 16.  All segments' units stand in one line, sentence by sentence; every CTA of one
-// resident wave takes an equal share of it, whatever the lengths (a segment counts some units more than it
-// has, at its start), and its warps (four, or one where segments are many) take every fourth or every unit.  A segment inside one share is written straight out; one that crosses shares leaves
-// (m, l, o) partials, and the CTA that arrives last joins them in order, so equal calls give equal bits.
+// resident wave takes an equal share of it, whatever the lengths (a segment counts SP_FIX units more than it
+// has, at its start), and its four warps take every fourth unit.  A segment inside one share is written
+// straight out; one that crosses shares leaves (m, l, o) partials, and a second, dependent launch joins them
+// in order, so equal calls give equal bits.  (Joining in the CTA that arrives last was slower: a fence and an
+// atomic a piece, and one CTA's loads in turn while the others are done.)
 //
 // A warp holds 16 MT rows x head_dim of o in registers.  Units come through a ring of cp.async stages of
 // its own (no barrier between warps), stored with a XOR of 16-byte chunks so that both reads below
@@ -27,11 +29,12 @@
 
 namespace vbs {
 
-constexpr int SP_MIN = 4;                // units a warp takes at least: its ring once
-// What a segment costs a warp besides its units (Q, the first loads, the join), in units: a share with many
-// short segments takes as long as one with a single long one.
-constexpr int SP_FIX = 6;
-constexpr int SP_MANY = 0;
+constexpr int NW = 4;                    // warps a CTA
+constexpr int SP_MIN = 4 * NW;           // units a CTA takes at least: every warp's ring once
+// What a segment costs besides its units (Q, the first loads, the warps' sums), in units: a share with many short
+// segments takes as long as one with a single long one (64 x 8 tokens over 1..4000 positions: 184 us with 8,
+// 139 with 20, 117 with 48 before the lookups were overlapped; 98 with 24 since).
+constexpr int SP_FIX = 24;
 
 // What the kernel needs to know of the split.
 struct SplitArgs {
@@ -184,7 +187,7 @@ struct EncSrc {
 // the kernel
 // ---------------------------------------------------------------------------------------
 
-template <int EL, int DP, int MT, int NW> struct SplitCfg {
+template <int EL, int DP, int MT> struct SplitCfg {
   static constexpr int CHK = 16 / EL;                       // dims in 16 bytes
   static constexpr int KS = DP / 16;                        // contraction steps of the scores
   static constexpr int NT = DP / 8;                         // output tiles of 8 dims
@@ -196,9 +199,8 @@ template <int EL, int DP, int MT, int NW> struct SplitCfg {
   static constexpr int QBYTES = MT * KS * 512;              // Q in fragment order
   static constexpr int PART = MT * 16 * (DP + 2);           // floats of a partial
   static constexpr size_t SMEM = NW * RING + QBYTES;
-  // resident warps a SM, by shared memory and by o's registers (MT * DP / 2 of a thread's)
-  static constexpr size_t SMEM4 = 4 * RING + QBYTES;
-  static constexpr int CTAS = (SMEM4 > 113 * 1024 ? 1 : (SMEM4 > 75 * 1024 || MT * DP > 128 ? 2 : 3)) * 4 / NW;
+  // resident CTAs a SM, by shared memory and by o's registers (MT * DP / 2 of a thread's)
+  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 ? 2 : 3);
 };
 
 // The order of output dims: column n of output tile j.
@@ -224,11 +226,11 @@ __device__ __forceinline__ void store_out(uint16_t* out, const SplitArgs& sa, co
 }
 
 // EXACT: head_dim is DP; ALIGNED: K and V rows may be copied 16 bytes at a time.
-template <class Src, int DP, int MT, int NW, bool EXACT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * NW, (SplitCfg<Src::EL, DP, MT, NW>::CTAS))
+template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
+__global__ void __launch_bounds__(32 * NW, (SplitCfg<Src::EL, DP, MT>::CTAS))
 attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
-  using C = SplitCfg<Src::EL, DP, MT, NW>;
-  constexpr int NT = 32 * NW, FIX = SP_FIX * NW;
+  using C = SplitCfg<Src::EL, DP, MT>;
+  constexpr int NT = 32 * NW;
   constexpr int EL = Src::EL, ROWS = 16 * MT;
   constexpr float GROW = Src::BF ? 8.f : 4.f;
   extern __shared__ __align__(128) unsigned char sp_smem[];
@@ -250,13 +252,17 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   const u32 qf_a = smem_u32(qf);
   const int HM = sa.H * sa.MC;
 
+  // a dependent launch (of the plan, or of what made q): set up before, reads nothing before its end
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // ---- this CTA's share of the line ----
   int b = 0;
   int64_t at = 0, end, per;                                 // position within sentence b's units (all heads)
   {
     const int k = (sa.B + NT - 1) / NT;               // a thread's sentences: [tid * k, tid * k + k)
     int64_t mine = 0;
-    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i) + FIX;
+    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i) + SP_FIX;
     int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -271,7 +277,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       all += s_sum[w];
     }
     const int64_t total = all * HM;
-    per = max(static_cast<int64_t>(SP_MIN * NW + FIX), (total + gridDim.x - 1) / gridDim.x);
+    per = max(static_cast<int64_t>(SP_MIN + SP_FIX), (total + gridDim.x - 1) / gridDim.x);
     const int64_t from = per * blockIdx.x;
     end = min(total, from + per);
     if (from >= total) return;
@@ -279,7 +285,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       int64_t p = from - before * HM;
       int i = tid * k;
       for (; i < sa.B - 1; ++i) {
-        const int64_t n = static_cast<int64_t>(src.units(i) + FIX) * HM;
+        const int64_t n = static_cast<int64_t>(src.units(i) + SP_FIX) * HM;
         if (p < n) break;
         p -= n;
       }
@@ -294,11 +300,11 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   int64_t line0 = per * blockIdx.x - at;                    // the line's position of sentence b's first unit
 
   while (end > 0 && b < sa.B) {
-    const int n = src.units(b), nf = n + FIX;
+    const int n = src.units(b), nf = n + SP_FIX;
     const int hm = static_cast<int>(at / nf), h = hm / sa.MC, mc = hm - h * sa.MC;
     const int f0 = static_cast<int>(at - static_cast<int64_t>(hm) * nf);   // on the line; u0, u1: units
     const int f1 = static_cast<int>(min(static_cast<int64_t>(nf), f0 + end));
-    const int u0 = max(0, f0 - FIX), u1 = f1 - FIX;
+    const int u0 = max(0, f0 - SP_FIX), u1 = f1 - SP_FIX;
     auto advance = [&] {
       const int done = f1 - f0;
       end -= done;
@@ -362,9 +368,6 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       }
       cp_commit();
     };
-#pragma unroll
-    for (int k = 0; k < C::NS - 1; ++k) issue(k);
-
     // ---- where the segment's rows stand and what they see, divided out once ----
     if (tid < ROWS) {
       const int rho = rho0 + tid, gq = rho % sa.G, iw = rho / sa.G, i = iw % io.n_q, w = iw / io.n_q;
@@ -375,14 +378,13 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       row_lim[tid] = live ? src.limit(b, w, i, sa.W, io.n_q) : 1 << 30;
       row_beam[tid] = live ? w : 31;                        // padding rows see everything, and are not written
     }
-    if (NW > 1) __syncthreads();
-    else __syncwarp();
+    __syncthreads();
 
-    // ---- Q in fragment order: a warp a row, four dims a lane, the loads of four rows at once ----
+    // ---- Q in fragment order: a warp a row, four dims a lane, the loads of four rows at once; the first four
+    // rows are on their way while the first units' addresses are looked up ----
     constexpr int QV = (DP + 127) / 128;
-#pragma unroll
-    for (int r0 = 0; r0 < ROWS; r0 += 4 * NW) {
-      uint2 x[4][QV];
+    uint2 x[4][QV];
+    auto load_q = [&](int r0) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int64_t off = row_q[r0 + k * NW + wid];
@@ -397,6 +399,14 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
           }
         }
       }
+    };
+    load_q(0);
+#pragma unroll
+    for (int k = 0; k < C::NS - 1; ++k) issue(k);
+
+#pragma unroll
+    for (int r0 = 0; r0 < ROWS; r0 += 4 * NW) {
+      if (r0 > 0) load_q(r0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = r0 + k * NW + wid;
@@ -680,7 +690,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     // the CTA with a segment's first unit says where its pieces are
     if (u0 == 0 && tid == 0)
       sa.pieces[static_cast<int64_t>(b) * HM + hm] =
-          whole ? make_int2(0, -1) : make_int2(static_cast<int>((line + FIX) / per), static_cast<int>((line + nf - 1) / per));
+          whole ? make_int2(0, -1) : make_int2(static_cast<int>((line + SP_FIX) / per), static_cast<int>((line + nf - 1) / per));
     __syncthreads();                                        // the ring and the row statistics are free again
     advance();
   }
@@ -789,6 +799,23 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
 // launch
 // ---------------------------------------------------------------------------------------
 
+// A launch that may be set up while its predecessor in the stream finishes; the kernel waits for it
+// (griddepcontrol.wait) before its first access to memory.
+template <typename... KArgs, typename... Args>
+int launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...) == cudaSuccess ? VBS_OK : VBS_ECUDA;
+}
+
 // Rows of a segment: two mma tiles where more than 16 rows share a K/V head (K/V are unpacked once for
 // both); one at head_dim > 128, whose o does not fit the registers twice.
 inline int split_mt(int M, int D) { return M > 16 && D <= 128 ? 2 : 1; }
@@ -799,44 +826,23 @@ inline int64_t split_part_floats(int D, int num_sms) {
   return static_cast<int64_t>(num_sms) * 12 * 2 * 32 * (split_dp(D) + 2);
 }
 
-template <class Src, int DP, int MT, int NW, bool EXACT, bool ALIGNED>
-int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
-  using C = SplitCfg<Src::EL, DP, MT, NW>;
-  static std::atomic<unsigned long long> attr_done{0};
-  auto* kernel = attn_split_kernel<Src, DP, MT, NW, EXACT, ALIGNED>;
-  if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
-  kernel<<<num_sms * C::CTAS, 32 * NW, C::SMEM, s>>>(src, io, sa);
-  if (cudaGetLastError() != cudaSuccess) return VBS_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(sa.B) * sa.H * sa.MC), (std::min(sa.M, 16 * MT) + JN_WARPS - 1) / JN_WARPS);
-  cfg.blockDim = dim3(32 * JN_WARPS);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP, 16 * MT>, io, sa) == cudaSuccess ? VBS_OK : VBS_ECUDA;
-}
-
 template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
-int launch_split_nw(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
-  // With many segments for the CTAs of four warps, a share would hold several short pieces one after the
-  // other: single warps take them side by side, and the join does what the CTA's own would have.
-  if constexpr (DP <= 128) {
-    const int64_t segments = static_cast<int64_t>(sa.B) * sa.H * sa.MC;
-    if (segments * SP_MANY > static_cast<int64_t>(num_sms) * SplitCfg<Src::EL, DP, MT, 4>::CTAS)
-      return launch_split_as<Src, DP, MT, 1, EXACT, ALIGNED>(src, io, sa, num_sms, s);
-  }
-  return launch_split_as<Src, DP, MT, 4, EXACT, ALIGNED>(src, io, sa, num_sms, s);
+int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
+  using C = SplitCfg<Src::EL, DP, MT>;
+  static std::atomic<unsigned long long> attr_done{0};
+  auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
+  if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
+  if (launch_dependent(kernel, dim3(num_sms * C::CTAS), dim3(32 * NW), C::SMEM, s, src, io, sa) != VBS_OK) return VBS_ECUDA;
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(sa.B) * sa.H * sa.MC), (std::min(sa.M, 16 * MT) + JN_WARPS - 1) / JN_WARPS);
+  return launch_dependent(attn_join_kernel<DP, 16 * MT>, grid, dim3(32 * JN_WARPS), 0, s, io, sa);
 }
 
 template <class Src, int DP, int MT, bool ALIGNED>
 int launch_split_dp(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
   if constexpr (ALIGNED) {
-    if (sa.D == DP) return launch_split_nw<Src, DP, MT, true, true>(src, io, sa, num_sms, s);
+    if (sa.D == DP) return launch_split_as<Src, DP, MT, true, true>(src, io, sa, num_sms, s);
   }
-  return launch_split_nw<Src, DP, MT, false, ALIGNED>(src, io, sa, num_sms, s);
+  return launch_split_as<Src, DP, MT, false, ALIGNED>(src, io, sa, num_sms, s);
 }
 
 template <class Src, bool ALIGNED>
