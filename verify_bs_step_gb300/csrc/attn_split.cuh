@@ -25,6 +25,7 @@
 #include <cuda_fp8.h>
 
 #include "attn.h"
+#include "codes.cuh"
 #include "common.cuh"
 
 namespace vbs {
@@ -70,23 +71,6 @@ template <bool BF> __device__ __forceinline__ void mma16816(float (&c)[4], const
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-// Four codes to two pairs of fp16 (exact).
-template <int FMT> __device__ __forceinline__ void codes4(u32 w, u32& lo, u32& hi) {
-  if (FMT == VBS_I8) {
-    // byte b + 128 under an exponent of 2^10: 1024 + 128 + b, less 1152
-    w ^= 0x80808080u;
-    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    u32 a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias), y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
-    lo = *reinterpret_cast<u32*>(&x);
-    hi = *reinterpret_cast<u32*>(&y);
-  } else {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-  }
 }
 
 __device__ __forceinline__ u32 pack_f16(float a, float b) {

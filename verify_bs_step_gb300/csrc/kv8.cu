@@ -8,11 +8,12 @@
 // it by an exact power of two and one more rounding, each at least twice as coarse as the one
 // before, so all of them together stay below one step of the final scale.
 //
-// A warp owns one run of consecutive tokens in one page, for one head of K or of V.
+// A warp owns one run of consecutive tokens in one page, for one head of K or of V.  Where the rows can be
+// loaded 16 bytes at a time it holds up to 16 tokens x 128 dims in registers between the maximum and the
+// rounding (longer runs are read again, from L2), with all loads in flight at once.  What bounds it is the
+// stream of the rows in and the codes out; a single token's step is latency: slot, scale, row.
 
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
+#include "codes.cuh"
 #include "common.cuh"
 #include "kv8.h"
 
@@ -54,34 +55,32 @@ template <int FMT> __device__ __forceinline__ int scale_exp(float amax) {
   return amax > 0.f ? max(KV8_E_LO, min(KV8_E_HI, e)) : KV8_E_LO;
 }
 
-// True if token i continues the page run of token i - 1.
-__device__ __forceinline__ bool continues(const int64_t* slots, int64_t i, int64_t s, int block) {
-  return i > 0 && s % block != 0 && slots[i - 1] == s - 1;
+// A page continued at slot `off` with rows that need the exponent e: the larger of that and the page's own; when
+// it grows, the codes before `off` are rounded to it.
+template <int FMT> __device__ __forceinline__ int regrow(const Kv8Geom& g, int64_t run, int off, int e, int lane) {
+  const int e_old = exp2i(g.scales[run]);
+  if (e_old >= e) return e_old;
+  const float f = e_old - e < -126 ? 0.f : pow2i(e_old - e);
+  uint4* codes = reinterpret_cast<uint4*>(g.pool + run * g.block * g.D);
+  for (int d = lane; d < off * g.D / 16; d += 32) {
+    const uint4 q = codes[d];
+    u32 w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      u32 a, b;
+      codes4<FMT>(w[y], a, b);
+      const float2 lo = __half22float2(*reinterpret_cast<__half2*>(&a)), hi = __half22float2(*reinterpret_cast<__half2*>(&b));
+      w[y] = encode4<FMT>(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+    }
+    codes[d] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return e;
 }
 
+// One run, element by element: rows of any alignment, and runs that hold NaN or infinities.
 template <int FMT, typename T>
-__global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, const Kv8Src src, int64_t n,
-                                                            const int64_t* __restrict__ slots) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (static_cast<int64_t>(blockIdx.x) * KV8_NT + threadIdx.x) >> 5;
-  if (item >= n * 2 * g.H) return;
-  const int64_t i = item / (2 * g.H);
-  const int kv = static_cast<int>(item % (2 * g.H)) / g.H, h = static_cast<int>(item % g.H);
-  const int64_t s = slots[i];
-  if (s < 0) return;
-  if (s >= g.NB * g.block) {                        // not a slot of this cache: nothing is written
-    if (lane == 0) set_status(g.status, VBS_EINVAL);
-    return;
-  }
-  if (continues(slots, i, s, g.block)) return;
-  const int64_t page = s / g.block;
-  const int off = static_cast<int>(s - page * g.block);
-  int len = 1;
-  while (off + len < g.block && i + len < n && slots[i + len] == s + len) ++len;
-
-  const void* base = kv ? src.v : src.k;
-  const int64_t tok = kv ? src.v_tok : src.k_tok;
-  const int64_t p0 = i * tok + h * (kv ? src.v_head : src.k_head);
+__device__ __noinline__ void append_elements(const Kv8Geom& g, const void* base, int64_t tok, int64_t p0, int64_t run, int off, int len,
+                                int lane) {
   float amax = 0.f;
   bool odd = false;
   for (int t = 0; t < len; ++t)
@@ -94,18 +93,8 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
   for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, m));
   if (odd) set_status(g.status, VBS_EINPUT);
   int e = scale_exp<FMT>(amax);
-  const int64_t run = g.run(page, kv, h);
   uint8_t* codes = reinterpret_cast<uint8_t*>(g.pool) + run * g.block * g.D;
-  if (off > 0) {
-    const int e_old = exp2i(g.scales[run]);
-    if (e_old < e) {
-      const float f = e_old - e < -126 ? 0.f : pow2i(e_old - e);
-      for (int d = lane; d < off * g.D; d += 32) codes[d] = Code<FMT>::enc(Code<FMT>::dec(codes[d]) * f);
-    } else {
-      e = e_old;
-    }
-    __syncwarp();
-  }
+  if (off > 0) e = regrow<FMT>(g, run, off, e, lane);
   const float inv = pow2i(-e);
   for (int t = 0; t < len; ++t)
     for (int d = lane; d < g.D; d += 32) {
@@ -115,60 +104,193 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
   if (lane == 0) g.scales[run] = pow2i(e);
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8Geom g, int64_t n, const int64_t* __restrict__ slots,
-                                                          uint16_t* k_out, uint16_t* v_out) {
-  const int per = g.D / 16;
-  const int64_t total = n * 2 * g.H * per;
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * KV8_NT + threadIdx.x; x < total;
-       x += static_cast<int64_t>(gridDim.x) * KV8_NT) {
-    const int c = static_cast<int>(x % per);
-    const int64_t y = x / per;
-    const int h = static_cast<int>(y % g.H);
-    const int64_t z = y / g.H;
-    const int kv = static_cast<int>(z & 1);
-    const int64_t i = z >> 1;
-    const int64_t s = slots[i];
-    uint4 q = make_uint4(0, 0, 0, 0);
-    float sc = 0.f;
-    if (s >= 0 && s < g.NB * g.block) {
-      const int64_t page = s / g.block, run = g.run(page, kv, h);
-      q = *reinterpret_cast<const uint4*>(g.pool + (run * g.block + (s - page * g.block)) * g.D + c * 16);
-      sc = g.scales[run];
-    } else if (s >= 0) {
-      set_status(g.status, VBS_EINVAL);
+// A CTA looks at 32 tokens; its warps (and those of the CTAs beside it along y) share out the runs that begin there,
+// each for every head of K and V.
+template <int FMT, typename T, bool VEC>
+__global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, const Kv8Src src, int64_t n,
+                                                            const int64_t* __restrict__ slots) {
+  constexpr int EPC = 16 / Elem<T>::BYTES;          // elements in 16 bytes
+  constexpr int NR = 16 * 128 / EPC / 32;           // 16-byte pieces a lane holds: 16 tokens x 128 dims a warp
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 32, i = i0 + lane;
+  const int64_t s = i < n ? slots[i] : -1;
+  bool valid = s >= 0, cont = false;
+  int64_t page = 0;
+  int off = 0;
+  if (valid && s >= g.NB * g.block) {               // not a slot of this cache: nothing is written
+    set_status(g.status, VBS_EINVAL);
+    valid = false;
+  }
+  if (valid) {
+    page = s / g.block;
+    off = static_cast<int>(s - page * g.block);
+    cont = off > 0 && i > 0 && slots[i - 1] == s - 1;
+  }
+  const u32 conts = __ballot_sync(FULL, cont);
+  u32 heads = __ballot_sync(FULL, valid && !cont);
+  const int per = 2 * g.H, runs = __popc(heads);
+  const int step = gridDim.y * (KV8_NT / 32);
+  int at = 0;                                       // runs taken off `heads` so far
+  for (int x = blockIdx.y * (KV8_NT / 32) + (threadIdx.x >> 5); x < runs * per; x += step) {
+    for (; at < x / per; ++at) heads &= heads - 1;
+    const int p = __ffs(heads) - 1, kvh = x % per, kv = kvh >= g.H ? 1 : 0, h = kvh - kv * g.H;
+    const int64_t pg = shfl64(static_cast<u64>(page), p), s0 = shfl64(static_cast<u64>(s), p);
+    const int o = __shfl_sync(FULL, off, p);
+    int len = __ffs(~(p < 31 ? conts >> (p + 1) : 0u));       // 1 + the tokens that go on
+    while (p + len >= 32 && o + len < g.block) {    // beyond the 32
+      const int64_t k = i0 + p + len + lane;
+      const u32 more = __ballot_sync(FULL, k < n && o + len + lane < g.block && slots[k] == s0 + len + lane);
+      const int m = __ffs(~more) - 1;
+      const int got = m < 0 ? 32 : m;
+      len += got;
+      if (got < 32) break;
     }
-    const uint8_t* b = reinterpret_cast<const uint8_t*>(&q);
-    __nv_bfloat162 o[8];
+    const void* base = kv ? src.v : src.k;
+    const int64_t tok = kv ? src.v_tok : src.k_tok;
+    const int64_t p0 = (i0 + p) * tok + h * (kv ? src.v_head : src.k_head);
+    const int64_t run = g.run(pg, kv, h);
+    if (!VEC) {
+      append_elements<FMT, T>(g, base, tok, p0, run, o, len, lane);
+      continue;
+    }
+    const char* rows = static_cast<const char*>(base) + p0 * Elem<T>::BYTES;
+    const int cpr = g.D / EPC, total = len * cpr;   // 16-byte pieces of a row, of the run
+    const int dt = 32 / cpr, dc = 32 - dt * cpr;    // from a lane's piece to its next
+    uint4 q[NR];
+    // the run's pieces c0 + lane, + 32, ... into q
+    auto load = [&](int c0) {
+      int t = (c0 + lane) / cpr, c = c0 + lane - t * cpr;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)                     // exact: a code has at most 7 bits
-      o[j] = __floats2bfloat162_rn(Code<FMT>::dec(b[2 * j]) * sc, Code<FMT>::dec(b[2 * j + 1]) * sc);
-    uint4* dst = reinterpret_cast<uint4*>((kv ? v_out : k_out) + (i * g.H + h) * g.D + c * 16);
-    dst[0] = reinterpret_cast<const uint4*>(o)[0];
-    dst[1] = reinterpret_cast<const uint4*>(o)[1];
+      for (int r = 0; r < NR; ++r) {
+        q[r] = make_uint4(0, 0, 0, 0);
+        if (c0 + r * 32 + lane < total) q[r] = ld_stream16(rows + (t * tok) * Elem<T>::BYTES + c * 16);
+        t += dt;
+        c += dc;
+        if (c >= cpr) {
+          c -= cpr;
+          ++t;
+        }
+      }
+    };
+    u32 top = 0;                                    // the largest magnitude's bits (NaN and infinities above all)
+    for (int c0 = 0; c0 < total; c0 += NR * 32) {
+      load(c0);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        if (Elem<T>::BYTES == 2) {
+          const u32 a = __vmaxu2(__vmaxu2(q[r].x & 0x7fff7fffu, q[r].y & 0x7fff7fffu),
+                                 __vmaxu2(q[r].z & 0x7fff7fffu, q[r].w & 0x7fff7fffu));
+          top = __vmaxu2(top, a);
+        } else {
+          top = max(max(max(top, q[r].x & 0x7fffffffu), q[r].y & 0x7fffffffu),
+                    max(q[r].z & 0x7fffffffu, q[r].w & 0x7fffffffu));
+        }
+      }
+    }
+    if (Elem<T>::BYTES == 2) top = max(top & 0xffff0000u, top << 16);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = max(top, __shfl_xor_sync(FULL, top, m));
+    if (top > 0x7f7fffffu) {                        // NaN or infinity
+      append_elements<FMT, T>(g, base, tok, p0, run, o, len, lane);
+      continue;
+    }
+    const float amax = __uint_as_float(top);
+    int e = scale_exp<FMT>(amax);
+    if (o > 0) e = regrow<FMT>(g, run, o, e, lane);
+    const float inv = pow2i(-e), lim = Code<FMT>::TOP * (1 << Code<FMT>::BITS);
+    const bool clamp = amax * inv > lim;            // only past the largest scale
+    uint8_t* codes = reinterpret_cast<uint8_t*>(g.pool) + (run * g.block + o) * g.D;
+    for (int c0 = 0; c0 < total; c0 += NR * 32) {
+      if (total > NR * 32) load(c0);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int c = c0 + r * 32 + lane;
+        if (c >= total) continue;
+        float v[EPC];
+        Vec16<T>::unpack(q[r], v);
+#pragma unroll
+        for (int y = 0; y < EPC; ++y) {
+          v[y] *= inv;
+          if (clamp) v[y] = fminf(fmaxf(v[y], -lim), lim);
+        }
+        const u32 w0 = encode4<FMT>(v[0], v[1], v[2], v[3]);
+        if (EPC == 8) *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(w0, encode4<FMT>(v[EPC - 4], v[EPC - 3], v[EPC - 2], v[EPC - 1]));
+        else *reinterpret_cast<u32*>(codes + c * 4) = w0;
+      }
+    }
+    if (lane == 0) g.scales[run] = pow2i(e);
   }
 }
 
-int launch_kv8_append(const Kv8Geom& g, const Kv8Src& src, int64_t n, const int64_t* slots, int, cudaStream_t s) {
-  if (n == 0) return VBS_OK;
-  const int64_t grid = (n * 2 * g.H + KV8_NT / 32 - 1) / (KV8_NT / 32);
-  if (grid >= (int64_t{1} << 31)) return VBS_EINVAL;
-  const unsigned gr = static_cast<unsigned>(grid);
-  if (g.fmt == VBS_I8) {
-    if (src.dtype == VBS_BF16) kv8_append_kernel<VBS_I8, bf16_t><<<gr, KV8_NT, 0, s>>>(g, src, n, slots);
-    else kv8_append_kernel<VBS_I8, float><<<gr, KV8_NT, 0, s>>>(g, src, n, slots);
-  } else {
-    if (src.dtype == VBS_BF16) kv8_append_kernel<VBS_E4M3, bf16_t><<<gr, KV8_NT, 0, s>>>(g, src, n, slots);
-    else kv8_append_kernel<VBS_E4M3, float><<<gr, KV8_NT, 0, s>>>(g, src, n, slots);
+// A warp a token: its 2 H D codes, 16 a lane, as bf16.
+template <int FMT>
+__global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8Geom g, int64_t n, const int64_t* __restrict__ slots,
+                                                          uint16_t* k_out, uint16_t* v_out) {
+  const int lane = threadIdx.x & 31, per = g.D / 16, all = 2 * g.H * per;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * KV8_NT + threadIdx.x) >> 5; i < n;
+       i += (static_cast<int64_t>(gridDim.x) * KV8_NT) >> 5) {
+    const int64_t s = slots[i];
+    const bool held = s >= 0 && s < g.NB * g.block;
+    if (s >= 0 && !held && lane == 0) set_status(g.status, VBS_EINVAL);
+    const int64_t page = held ? s / g.block : 0;
+    const int64_t run0 = g.run(page, 0, 0);
+    const char* codes = g.pool + (run0 * g.block + (held ? s - page * g.block : 0)) * g.D;
+#pragma unroll 4
+    for (int j = lane; j < all; j += 32) {
+      const int kvh = j / per, c = j - kvh * per;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      float sc = 0.f;
+      if (held) {
+        q = ld_stream16(codes + static_cast<int64_t>(kvh) * g.block * g.D + c * 16);
+        sc = g.scales[run0 + kvh];
+      }
+      const u32 w[4] = {q.x, q.y, q.z, q.w};
+      u32 o[8];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        u32 a, b;
+        codes4<FMT>(w[y], a, b);
+        const float2 lo = __half22float2(*reinterpret_cast<__half2*>(&a)), hi = __half22float2(*reinterpret_cast<__half2*>(&b));
+        const __nv_bfloat162 x = __floats2bfloat162_rn(lo.x * sc, lo.y * sc), z = __floats2bfloat162_rn(hi.x * sc, hi.y * sc);
+        o[2 * y] = *reinterpret_cast<const u32*>(&x);      // exact: a code has at most 7 bits
+        o[2 * y + 1] = *reinterpret_cast<const u32*>(&z);
+      }
+      uint16_t* out = (kvh < g.H ? k_out : v_out) + (i * g.H + (kvh < g.H ? kvh : kvh - g.H)) * g.D + c * 16;
+      reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
   }
+}
+
+template <int FMT, typename T>
+static int launch_append(const Kv8Geom& g, const Kv8Src& src, bool vec, int64_t n, const int64_t* slots, int num_sms,
+                         cudaStream_t s) {
+  // enough warps for a step of single tokens, where every token is a run
+  const int64_t chunks = (n + 31) / 32;
+  if (chunks >= (int64_t{1} << 31)) return VBS_EINVAL;
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(8 * g.H, 16 * num_sms / chunks));
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(y));
+  if (vec) kv8_append_kernel<FMT, T, true><<<grid, KV8_NT, 0, s>>>(g, src, n, slots);
+  else kv8_append_kernel<FMT, T, false><<<grid, KV8_NT, 0, s>>>(g, src, n, slots);
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+}
+
+int launch_kv8_append(const Kv8Geom& g, const Kv8Src& src, int64_t n, const int64_t* slots, int num_sms, cudaStream_t s) {
+  if (n == 0) return VBS_OK;
+  const int es = src.dtype == VBS_BF16 ? 2 : 4;
+  const bool vec = ((reinterpret_cast<uintptr_t>(src.k) | reinterpret_cast<uintptr_t>(src.v)) & 15) == 0 &&
+                   (src.k_tok | src.k_head | src.v_tok | src.v_head) * es % 16 == 0;
+  if (g.fmt == VBS_I8)
+    return src.dtype == VBS_BF16 ? launch_append<VBS_I8, bf16_t>(g, src, vec, n, slots, num_sms, s)
+                                 : launch_append<VBS_I8, float>(g, src, vec, n, slots, num_sms, s);
+  return src.dtype == VBS_BF16 ? launch_append<VBS_E4M3, bf16_t>(g, src, vec, n, slots, num_sms, s)
+                               : launch_append<VBS_E4M3, float>(g, src, vec, n, slots, num_sms, s);
 }
 
 int launch_kv8_read(const Kv8Geom& g, int64_t n, const int64_t* slots, void* k_out, void* v_out, int num_sms,
                     cudaStream_t s) {
   if (n == 0) return VBS_OK;
-  const int64_t total = n * 2 * g.H * (g.D / 16);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + KV8_NT - 1) / KV8_NT, static_cast<int64_t>(num_sms) * 32));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + KV8_NT / 32 - 1) / (KV8_NT / 32), static_cast<int64_t>(num_sms) * 32));
   auto* k = static_cast<uint16_t*>(k_out);
   auto* v = static_cast<uint16_t*>(v_out);
   if (g.fmt == VBS_I8) kv8_read_kernel<VBS_I8><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
