@@ -200,6 +200,8 @@ class _StreamOrder:
     def run(self, fn, name: str, tensors, *args):
         if _raw_stream(self.index) == self.raw:
             st = fn(*args)
+            if st == OK:
+                return
         else:
             cur = torch.cuda.current_stream(self.device)
             self.stream.wait_stream(cur)
@@ -207,8 +209,7 @@ class _StreamOrder:
             cur.wait_stream(self.stream)
             for t in tensors:                       # not to be reused before the context's stream is done
                 t.record_stream(self.stream)
-        if st != OK:
-            raise VbsError(st, name)
+        _check(st, name)
 
 
 def _cuda(t: torch.Tensor, name: str, dtype) -> int:
@@ -502,7 +503,7 @@ class PagedKV:
             raise ValueError("cap must not be negative")
         slots = torch.empty(cap, dtype=torch.int64, device=self.device)
         ints = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device)
-        pos, row, cu = ints.split((cap, cap, n + 1))
+        pos, row, cu = ints.narrow(0, 0, cap), ints.narrow(0, cap, cap), ints.narrow(0, 2 * cap, n + 1)
         p = ints.data_ptr()
         return (slots, pos, row, cu), (cap, slots.data_ptr(), p, p + 4 * cap, p + 8 * cap)
 
@@ -618,8 +619,9 @@ class PagedKV8(PagedKV):
         if slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots must be a contiguous int64 [N] tensor")
         n = slots.shape[0]
-        k, v = torch.empty(2, n, self.H, self.D, dtype=torch.bfloat16, device=self.device).unbind(0)
-        self._order.run(lib().kv8_read, "kv8_read", (slots, k), self.ctx8, layer, n,
+        k = torch.empty(n, self.H, self.D, dtype=torch.bfloat16, device=self.device)
+        v = torch.empty(n, self.H, self.D, dtype=torch.bfloat16, device=self.device)
+        self._order.run(lib().kv8_read, "kv8_read", (slots, k, v), self.ctx8, layer, n,
                         _cuda(slots, "slots", torch.int64), k.data_ptr(), v.data_ptr())
         return k, v
 

@@ -130,10 +130,9 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
   const int32_t* tab = a.table + static_cast<int64_t>(row) * a.MB;
   if (build) {
     const int nb = (count + a.block - 1) / a.block;
-    for (int64_t j = t0; j < static_cast<int64_t>(a.W) * a.MB; j += step) {
-      const int c = static_cast<int>(j % a.MB);
-      a.table[static_cast<int64_t>(row) * a.MB + j] = c < nb ? i * a.S + c : -1;
-    }
+    for (int w = 0; w < a.W; ++w)
+      for (int64_t c = t0; c < a.MB; c += step)
+        a.table[(static_cast<int64_t>(row) + w) * a.MB + c] = c < nb ? i * a.S + static_cast<int>(c) : -1;
     for (int64_t j = t0; j < a.S; j += step) {
       a.refcnt[static_cast<int64_t>(i) * a.S + j] = j < nb ? a.W : 0;
       a.stack[static_cast<int64_t>(i) * a.S + j] = i * a.S + (a.S - 1 - static_cast<int>(j));
@@ -148,12 +147,15 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
     }
   }
   if (!s.slots) return;
+  const bool pow2 = (a.block & (a.block - 1)) == 0;         // the usual block: a shift for the division
+  const int shift = __ffs(a.block) - 1;
+  const int blocks = build ? 0 : a.nblk[row];
   for (int64_t k = t0; k < count; k += step) {
     const int64_t o = first + k;
     if (o >= s.cap) break;
     const int p = start + static_cast<int>(k);
-    const int j = p / a.block;
-    const int blk = build ? i * a.S + j : (j < a.nblk[row] ? tab[j] : -1);
+    const int j = pow2 ? p >> shift : p / a.block;
+    const int blk = build ? i * a.S + j : (j < blocks ? tab[j] : -1);
     if (blk < 0) set_status(a.status, VBS_EINVAL);          // a position that the table does not cover
     s.slots[o] = blk < 0 ? -1 : static_cast<int64_t>(blk) * a.block + (p - j * a.block);
     if (s.pos) s.pos[o] = p;
