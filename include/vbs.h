@@ -450,7 +450,8 @@ typedef struct vbs_kv8 vbs_kv8;
  *   q_heads  query heads of the attention (a multiple of H); max_q  the most query
  *            tokens per row of one attention call (1..32)
  * All work goes to pkv's stream; device-side errors go to kv_paged_status(pkv).
- * The context must be destroyed before pkv.
+ * The calls below return VBS_ESTATE while copies recorded by bs_step_paged are
+ * pending (kv_paged_copy has not run).  The context must be destroyed before pkv.
  * Errors: VBS_EINVAL (elem_bytes not 1, head_dim not a multiple of 16 up to 256, NULL
  *   pointers, q_heads, max_q or format out of range), VBS_EALIGN (pool not 16-byte
  *   aligned), VBS_ESTATE (pkv already has such a context), VBS_ENOMEM.  *ctx is NULL on error.

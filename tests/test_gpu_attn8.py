@@ -219,3 +219,30 @@ def test_refusals():
             kv.attend(q=q, **kw)
         assert e.value.status == vbs.EINVAL
     kv.close()
+
+
+def test_calls_wait_for_pending_copies():
+    """Between BeamSearch.step_paged and PagedKV.copy the cache is neither read nor written."""
+    import verify_bs_step_gb300 as vbs
+    kv = vbs.PagedKV8(1, 2, 1, 1, 16, heads=1, blocks_per_sentence=8, max_blocks=4, block=4)
+    bs = vbs.BeamSearch(1, 2, 20, max_len=4)
+    kv.build(i32([3]))
+    kv.prepare(0)
+    k = torch.ones(2, 1, 16, device="cuda")
+    slots = kv.slot_map(i32([3, 3]), i32([1, 1]), 2)[0]
+    kv.append(0, k, k, slots)
+    kv.plan(i32([4, 4]))
+    q = torch.ones(2, 1, 1, 16, device="cuda", dtype=torch.bfloat16)
+    kv.attend(0, q)
+    bs.step_paged(torch.randn(2, 20, device="cuda").to(torch.bfloat16), kv, 1)
+    for call in (lambda: kv.append(0, k, k, slots), lambda: kv.read(0, slots), lambda: kv.plan(i32([4, 4])),
+                 lambda: kv.attend(0, q)):
+        with pytest.raises(vbs.VbsError) as e:
+            call()
+        assert e.value.status == vbs.ESTATE
+    kv.copy()
+    kv.plan(i32([4, 4]))
+    kv.attend(0, q)
+    assert kv.status() == 0
+    kv.close()
+    bs.close()

@@ -171,7 +171,10 @@ class _Context:
         self.ptr, self.destroy = ptr, destroy
 
     def __del__(self):
-        self.destroy(self.ptr)
+        try:
+            self.destroy(self.ptr)
+        except Exception:
+            pass
 
 
 class _DeviceArray:
@@ -184,7 +187,12 @@ class _DeviceArray:
                                          "strides": None, "version": 2}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without making a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 class _StreamOrder:

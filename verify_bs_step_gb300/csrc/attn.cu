@@ -42,19 +42,22 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, co
     const int j = j0 + tid;
     int id[WMAX];
     u32 lead = 0;                                   // the beams that name a page first
-    if (j < cols)
-      for (int w = 0; w < W; ++w) {
-        id[w] = j * a.block < seen[w] ? tab[static_cast<int64_t>(w) * a.MB + j] : -1;
-        if (id[w] < 0) continue;
-        if (id[w] < b * a.S || id[w] >= (b + 1) * a.S) {   // not a page of this sentence
-          set_status(a.status, VBS_EINVAL);
-          id[w] = -1;
-          continue;
-        }
-        bool first = true;
-        for (int x = 0; x < w; ++x) first = first && id[x] != id[w];
-        if (first) lead |= 1u << w;
+#pragma unroll
+    for (int w = 0; w < WMAX; ++w)                  // the column's entries, all on their way at once
+      id[w] = w < W && j < cols && j * a.block < seen[w] ? tab[static_cast<int64_t>(w) * a.MB + j] : -1;
+#pragma unroll
+    for (int w = 0; w < WMAX; ++w) {
+      if (id[w] < 0) continue;
+      if (id[w] < b * a.S || id[w] >= (b + 1) * a.S) {     // not a page of this sentence
+        set_status(a.status, VBS_EINVAL);
+        id[w] = -1;
+        continue;
       }
+      bool first = true;
+#pragma unroll
+      for (int x = 0; x < w; ++x) first = first && id[x] != id[w];
+      if (first) lead |= 1u << w;
+    }
     const int n = __popc(lead);
     int at = n;
 #pragma unroll
@@ -70,11 +73,13 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, co
       if (w < wid) at += sums[w];
       all += sums[w];
     }
-    for (int w = 0; w < W; ++w) {
+#pragma unroll
+    for (int w = 0; w < WMAX; ++w) {
       if (!(lead >> w & 1u)) continue;
       u32 rows = 0;
       int to = 0;
-      for (int x = w; x < W; ++x)
+#pragma unroll
+      for (int x = w; x < WMAX; ++x)
         if (id[x] == id[w]) {
           rows |= 1u << x;
           to = max(to, seen[x]);

@@ -86,6 +86,7 @@ VBS_EXPORT int kv8_append(vbs_kv8* c, int layer, const void* k, const void* v, i
                           int64_t v_tok, int64_t v_head, int dtype, int64_t n, const int64_t* slots) {
   if (!c || layer < 0 || layer >= c->g.L || n < 0 || (dtype != VBS_F32 && dtype != VBS_BF16)) return VBS_EINVAL;
   if (n > 0 && (!k || !v || !slots)) return VBS_EINVAL;
+  if (c->kv->copy_pending) return VBS_ESTATE;
   const vbs::Kv8Src src{k, v, k_tok, k_head, v_tok, v_head, dtype};
   vbs::Kv8Geom g = c->g;
   g.layer = layer;
@@ -96,6 +97,7 @@ VBS_EXPORT int kv8_read(vbs_kv8* c, int layer, int64_t n, const int64_t* slots, 
   if (!c || layer < 0 || layer >= c->g.L || n < 0) return VBS_EINVAL;
   if (n > 0 && (!slots || !k_out || !v_out)) return VBS_EINVAL;
   if (!aligned16(k_out) || !aligned16(v_out)) return VBS_EALIGN;
+  if (c->kv->copy_pending) return VBS_ESTATE;
   vbs::Kv8Geom g = c->g;
   g.layer = layer;
   return vbs::launch_kv8_read(g, n, slots, k_out, v_out, num_sms(), c->kv->stream);
@@ -103,6 +105,7 @@ VBS_EXPORT int kv8_read(vbs_kv8* c, int layer, int64_t n, const int64_t* slots, 
 
 VBS_EXPORT int kv8_plan(vbs_kv8* c, const int32_t* ctx_len, int n_q) {
   if (!c || !ctx_len || n_q < 1 || n_q > c->max_q) return VBS_EINVAL;
+  if (c->kv->copy_pending) return VBS_ESTATE;
   const int st = vbs::launch_kv8_plan(c->kv->a, ctx_len, c->plan, c->kv->stream);
   c->n_q = st == VBS_OK ? n_q : 0;
   return st;
@@ -111,7 +114,7 @@ VBS_EXPORT int kv8_plan(vbs_kv8* c, const int32_t* ctx_len, int n_q) {
 VBS_EXPORT int kv8_attention(vbs_kv8* c, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head,
                              float scale, void* out, int64_t o_row, int64_t o_tok, int64_t o_head) {
   if (!c || !q || !out || layer < 0 || layer >= c->g.L || !std::isfinite(scale)) return VBS_EINVAL;
-  if (c->n_q == 0) return VBS_ESTATE;
+  if (c->n_q == 0 || c->kv->copy_pending) return VBS_ESTATE;
   const vbs::QO io{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), q_row, q_tok, q_head, o_row, o_tok,
                    o_head, c->n_q, c->q_heads, scale};
   vbs::Kv8Geom g = c->g;

@@ -224,7 +224,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   __shared__ int row_lim[ROWS], row_beam[ROWS];
   __shared__ float wm[NW][ROWS], wl[NW][ROWS];
   __shared__ int64_t s_sum[NW];
-  __shared__ int s_b;
+  __shared__ int s_b, s_n;
   __shared__ int64_t s_pos;
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, c4 = lane & 3;
@@ -242,11 +242,16 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 
   // ---- this CTA's share of the line ----
   int b = 0;
+  int n = 1;                                                // sentence b's units
   int64_t at = 0, end, per;                                 // position within sentence b's units (all heads)
   {
     const int k = (sa.B + NT - 1) / NT;               // a thread's sentences: [tid * k, tid * k + k)
     int64_t mine = 0;
-    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) mine += src.units(i) + SP_FIX;
+    int own = 0;                                            // the last one's units
+    for (int i = tid * k; i < min(sa.B, tid * k + k); ++i) {
+      own = src.units(i);
+      mine += own + SP_FIX;
+    }
     int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -268,27 +273,32 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     if (from >= before * HM && from < (before + mine) * HM) {
       int64_t p = from - before * HM;
       int i = tid * k;
-      for (; i < sa.B - 1; ++i) {
-        const int64_t n = static_cast<int64_t>(src.units(i) + SP_FIX) * HM;
-        if (p < n) break;
-        p -= n;
-      }
+      if (k > 1)
+        for (; i < sa.B - 1; ++i) {
+          own = src.units(i);
+          const int64_t n = static_cast<int64_t>(own + SP_FIX) * HM;
+          if (p < n) break;
+          p -= n;
+        }
       s_b = i;
+      s_n = k > 1 ? src.units(i) : own;
       s_pos = p;
     }
     __syncthreads();
     b = s_b;
+    n = s_n;
     at = s_pos;
     end -= from;                                            // units left
   }
   int64_t line0 = per * blockIdx.x - at;                    // the line's position of sentence b's first unit
 
   while (end > 0 && b < sa.B) {
-    const int n = src.units(b), nf = n + SP_FIX;
+    const int nf = n + SP_FIX;
     const int hm = static_cast<int>(at / nf), h = hm / sa.MC, mc = hm - h * sa.MC;
     const int f0 = static_cast<int>(at - static_cast<int64_t>(hm) * nf);   // on the line; u0, u1: units
     const int f1 = static_cast<int>(min(static_cast<int64_t>(nf), f0 + end));
     const int u0 = max(0, f0 - SP_FIX), u1 = f1 - SP_FIX;
+    const int n_next = b + 1 < sa.B ? src.units(b + 1) : 1;  // on its way while this segment is worked on
     auto advance = [&] {
       const int done = f1 - f0;
       end -= done;
@@ -297,6 +307,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         line0 += at;
         at = 0;
         ++b;
+        n = n_next;
       }
     };
     if (u1 <= u0) {                                         // the segment's units are all in the next share
@@ -684,7 +695,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 // the join of segments in pieces
 // ---------------------------------------------------------------------------------------
 
-constexpr int JN_WARPS = 4;
+constexpr int JN_WARPS = 4, JN_FEW = 4;
 
 // CTA (segment, c): rows 4 c .. 4 c + 3 of its segment, a warp each; where the pieces are many, all warps take
 // a row after the other and share its pieces.  A dependent launch: it is set up while the split kernel runs.
@@ -736,7 +747,37 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
   if (np <= 64 * JN_WARPS) {
     const int r = blockIdx.y * JN_WARPS + wid;
     if (r >= rows) return;
-    gather(r, 0, 1, top, sum, a);
+    if (np <= JN_FEW) {                                     // few pieces: all loads at once
+      float mm[JN_FEW], ll[JN_FEW];
+      float4 q[JN_FEW][V];
+#pragma unroll
+      for (int c = 0; c < JN_FEW; ++c) {
+        const float* pp = piece(min(c, np - 1));
+        mm[c] = c < np ? __ldcg(pp + ROWS * DP + r) : -INFINITY;
+        ll[c] = c < np ? __ldcg(pp + ROWS * DP + ROWS + r) : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          q[c][v] = lane * 4 + v * 128 < DP ? __ldcg(reinterpret_cast<const float4*>(pp + r * DP + v * 128) + lane)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      top = mm[0];
+#pragma unroll
+      for (int c = 1; c < JN_FEW; ++c) top = fmaxf(top, mm[c]);
+      sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < JN_FEW; ++c) {
+        const float x = mm[c] == -INFINITY ? 0.f : ex2(mm[c] - top);
+        sum += ll[c] * x;                                   // (a NaN stays one)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          a[v].x += q[c][v].x * x; a[v].y += q[c][v].y * x; a[v].z += q[c][v].z * x; a[v].w += q[c][v].w * x;
+        }
+      }
+    } else {
+      gather(r, 0, 1, top, sum, a);
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
