@@ -600,11 +600,18 @@ static bool encode(CUtensorMap* map, const uint16_t* p, const EncKV& e, int64_t 
 
 bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
   const int64_t M = static_cast<int64_t>(e.W) * io.n_q * (io.Hq / e.H);
-  if (e.D > 128 || e.S < 1 || M < 64 || static_cast<double>(e.B) * e.H * M > 1e9) return false;
-  // a CTA walks a sentence's positions alone; the split kernel shares them out
-  const double tiles = static_cast<double>(e.B) * e.H * ((M + TC_M - 1) / TC_M), units = static_cast<double>(e.B) * e.H * ((M + 31) / 32);
-  const double tc = (e.S + TC_N - 1) / TC_N * 0.55 * std::max(1.0, tiles / (2 * num_sms));
-  const double split = 5.0 + units * ((e.S + 15) / 16) * (e.D <= 64 ? 0.0011 : 0.002);
+  if (e.D > 128 || e.S < 1 || M <= 16 || static_cast<double>(e.B) * e.H * M > 1e9) return false;
+  // The tiles walk a sentence's positions one after the other, the split kernel shares them out but pays for
+  // every 32 rows again.  Both sides in us, tiles / split, measured at full lengths (head_dim 64, then 128):
+  //   1 head, 32 rows x 1024 positions    14.8 / 15.0, 17.0 / 20.5;   x 8192   75.8 / 17.9, 81 / 23.5
+  //   32 heads, 128 rows x 1024           16.1 / 24.9, 18.7 / 28.8;   x 8192   79.0 / 69.7, 91 / 113
+  //   256 heads, 32 rows x 1024           18.0 / 30.0, 28.8 / 45.9;   512 rows x 8192   342 / 1786, 415 / 3111
+  // (and up to 16 rows, where the split kernel needs one mma tile, 14.9 / 10.8 and 92 / 100 at the ends).
+  const bool wide = e.D > 64;
+  const double heads = static_cast<double>(e.B) * e.H, tiles = heads * ((M + TC_M - 1) / TC_M);
+  const double tc = (wide ? 8.0 : 6.0) + (e.S + TC_N - 1) / TC_N * 0.56 * std::max(1.0, tiles / (2 * num_sms));
+  const double split = (wide ? std::min(24.0, std::max(12.0, 6.0 + e.S / 70.0)) : std::min(18.0, std::max(9.3, 5.0 + e.S / 100.0))) +
+                       heads * ((M + 31) / 32) * ((e.S + 15) / 16) * (wide ? 0.0015 : 0.00085);
   if (tc > split) return false;
   auto stride_ok = [](int64_t s, int64_t extent) { return extent == 1 || (s > 0 && s % 8 == 0 && s < (int64_t{1} << 38)); };
   return ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 && stride_ok(e.k_sent, e.B) &&
