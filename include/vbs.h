@@ -1,7 +1,8 @@
 /*
  * libvbs: one step of batched beam search over a vocabulary, the KV-cache
- * reorder that follows it, and the verify/accept step of blockwise parallel
- * decoding, as a C ABI for one NVIDIA GB300 (sm_103a).
+ * reorder that follows it, the verify/accept step of blockwise parallel
+ * decoding, and the attention of a decode step (an 8-bit paged cache and an
+ * encoder's states), as a C ABI for one NVIDIA GB300 (sm_103a).
  *
  * Sources of the operations (cited by page title and section):
  *   [BS] "Transformers中的Beam Search高效实现" (zhuanzhi.ai), section

@@ -2,7 +2,8 @@
 //
 // The plan turns the block tables into each sentence's list of distinct pages: a page that several
 // beams share stands in it once, with the beams that see it, so that attention reads it once.  It is a
-// pass over R x pages table entries, made once a step and shared by the layers.
+// pass over R x pages table entries, made once a step and shared by the layers; latency bounds it (lengths, block
+// counts, a column's entries together, the list: 64 sentences x 4 beams x 67 pages take 7 us alone).
 
 #include "attn.h"
 #include "attn_split.cuh"
@@ -99,7 +100,8 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, co
 }
 
 // One row a sentence: the list is the table's row; CTA (b, c) copies every c-th chunk of it.
-__global__ void __launch_bounds__(PLAN_NT) kv8_plan_rows_kernel(const PagedArgs a, const int32_t* ctx, const Kv8Plan p) {
+__global__ void __launch_bounds__(PLAN_NT)
+kv8_plan_rows_kernel(const PagedArgs a, const int32_t* ctx, const Kv8Plan p) {
   const int b = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

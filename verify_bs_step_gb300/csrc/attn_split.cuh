@@ -16,7 +16,13 @@
 //            inside the contraction is whatever that gives (Q is laid out the same way);
 //   values   O += P V by mma.m16n8k16: a lane takes 16 bytes of four positions, pairs of positions are put
 //            side by side with byte permutes, and the order of the output dims is undone at the end.
-// What bounds it is the K/V stream; the mma's rate only matters where many rows share a K/V head.
+// What bounds it is the K/V stream for one long row (250001 positions, 8 heads x 128 e4m3: 95 us with the plan and
+// the join, 5.4 TB/s, 81 % of the measured copy), the segments' fixed cost (some 5 us of lookups, Q and sums
+// each) for many short ones (64 sentences x 4 beams x 1064: 46 us, 3.4 TB/s), and issue slots where 32 rows share a
+// K/V head (64 x 8 tokens x 4 heads over 1..4000 positions, int8: 97 us, 2.8 TB/s: 750 instructions a unit and
+// warp, a quarter of them conversions, at 8 warps an SM).
+// Measured and not kept: two units an iteration (fewer instructions, 8 warps instead of 12: 102 and 65 us), CTAs
+// of one warp (91 us at 64 x 4 beams: four times the partials), a join in the CTA that arrives last (57).
 
 #pragma once
 
@@ -131,7 +137,8 @@ template <int FMT> struct PagedSrc {
   }
   // lane `k`'s unit: the loads of its K and V rows into a stage, and its head
   template <class L>
-  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int, int, UnitHead* head, const L& load) const {
+  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int, int, UnitHead* head,
+                                        const L& load) const {
     const u64 at = shfl64(reinterpret_cast<u64>(t.k), k);
     const int n = __shfl_sync(FULL, t.u.n, k);
     if (lane == k) *head = t.u;
@@ -157,7 +164,8 @@ struct EncSrc {
   // (a lane without a unit stands past every end: no positions)
   __device__ void fetch(Batch& t, int, int, int u, bool valid) const { t.u = valid ? u : 1 << 26; }
   template <class L>
-  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int b, int h, UnitHead* head, const L& load) const {
+  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int b, int h, UnitHead* head,
+                                        const L& load) const {
     const int pos = __shfl_sync(FULL, t.u, k) * 16;
     const int n = max(0, min(16, len(b) - pos));
     if (lane == 0) *head = UnitHead{pos, n, 0xffffu, 1.f, 0.f, 1.f, {0.f, 0.f}};
@@ -324,7 +332,8 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         if ((k & 31) == 0) src.fetch(batch, b, h, u0 + wid + (k + lane) * NW, k + lane < mine);
         const int st = k % C::NS;
         const u32 base = ring_a + st * C::STAGE;
-        src.issue(batch, k & 31, lane, b, h, &heads[wid][st], [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
+        src.issue(batch, k & 31, lane, b, h, &heads[wid][st],
+                  [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
           if (EXACT && EL == 1 && cnt == 16) {              // a whole unit of contiguous rows: constant offsets
             const char *ks = kp + lane * 16, *vs = vp + lane * 16;
 #pragma unroll

@@ -26,6 +26,14 @@ template <int FMT> __device__ __forceinline__ void codes4(u32 w, u32& lo, u32& h
   }
 }
 
+// Four codes as fp32 (exact).
+template <int FMT> __device__ __forceinline__ void decode4(u32 w, float2& lo, float2& hi) {
+  u32 a, b;
+  codes4<FMT>(w, a, b);
+  lo = __half22float2(*reinterpret_cast<__half2*>(&a));
+  hi = __half22float2(*reinterpret_cast<__half2*>(&b));
+}
+
 // Four values within the format's range (already scaled) to four codes, rounded to nearest, ties to even.
 template <int FMT> __device__ __forceinline__ u32 encode4(float a, float b, float c, float d) {
   if (FMT == VBS_I8) {

