@@ -9,8 +9,8 @@ DT = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 BF16 = torch.finfo(torch.bfloat16).eps / 2          # a rounding to bf16, relative
 FP16 = torch.finfo(torch.float16).eps / 2
 FP32 = torch.finfo(torch.float32).eps / 2
-# fp16 weights, the largest at 2^15: half the smallest fp16 step is 2^-40 of it, times a code of up to 448 in a
-# scale of up to 2^-6 of the largest value
+# fp16 weights, the largest between 2^12 and 2^15: half the smallest fp16 step (2^-25) is 2^-37 of it at most, and a
+# term is at most a code of QMAX in a scale below 2 / QMAX of the largest value
 FP16_FLOOR = 2.0 ** -36
 
 

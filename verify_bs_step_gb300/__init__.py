@@ -509,11 +509,12 @@ class PagedKV:
     def _slot_outputs(self, n: int, cap: int):
         if cap < 0:
             raise ValueError("cap must not be negative")
-        slots = torch.empty(cap, dtype=torch.int64, device=self.device)
-        ints = torch.empty(2 * cap + n + 1, dtype=torch.int32, device=self.device)
-        pos, row, cu = ints.narrow(0, 0, cap), ints.narrow(0, cap, cap), ints.narrow(0, 2 * cap, n + 1)
-        p = ints.data_ptr()
-        return (slots, pos, row, cu), (cap, slots.data_ptr(), p, p + 4 * cap, p + 8 * cap)
+        dev = self.device                           # (four allocations cost less than one and its views)
+        slots = torch.empty(cap, dtype=torch.int64, device=dev)
+        pos = torch.empty(cap, dtype=torch.int32, device=dev)
+        row = torch.empty(cap, dtype=torch.int32, device=dev)
+        cu = torch.empty(n + 1, dtype=torch.int32, device=dev)
+        return (slots, pos, row, cu), (cap, slots.data_ptr(), pos.data_ptr(), row.data_ptr(), cu.data_ptr())
 
     def views(self):
         """The allocator's state as int32 tensors on the library's own memory (no copy; they keep it

@@ -224,7 +224,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   using C = SplitCfg<Src::EL, DP, MT>;
   constexpr int NT = 32 * NW;
   constexpr int EL = Src::EL, ROWS = 16 * MT;
-  constexpr float GROW = Src::BF ? 8.f : 4.f;
+  constexpr float GROW = Src::BF ? 8.f : 3.f;
   extern __shared__ __align__(128) unsigned char sp_smem[];
   __shared__ UnitHead heads[NW][C::NS];
   __shared__ float row_f[ROWS];                             // a row's factor on its dot products

@@ -270,10 +270,10 @@ __global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8Geom g, int64
 template <int FMT, typename T>
 static int launch_append(const Kv8Geom& g, const Kv8Src& src, bool vec, int64_t n, const int64_t* slots, int num_sms,
                          cudaStream_t s) {
-  // enough warps for a step of single tokens, where every token is a run
+  // enough warps for a step of single tokens, where every token is a run; a prompt has a run a page
   const int64_t chunks = (n + 31) / 32;
   if (chunks >= (int64_t{1} << 31)) return VBS_EINVAL;
-  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(8 * g.H, 16 * num_sms / chunks));
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(8 * g.H, 4 * num_sms / chunks));
   const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(y));
   if (vec) kv8_append_kernel<FMT, T, true><<<grid, KV8_NT, 0, s>>>(g, src, n, slots);
   else kv8_append_kernel<FMT, T, false><<<grid, KV8_NT, 0, s>>>(g, src, n, slots);
