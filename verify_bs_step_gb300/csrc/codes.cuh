@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "pairs.cuh"
 
 namespace vbs {
 
@@ -47,6 +48,21 @@ template <int FMT> __device__ __forceinline__ u32 encode4(float a, float b, floa
   asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
       "mov.b32 %0, {x, y};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
+}
+
+// encode4 of a 2^-e, .. with inv = (2^-e, 2^-e): the product is exact, so that it and the rounding are one fma for int8.
+template <int FMT> __device__ __forceinline__ u32 encode4_scaled(float a, float b, float c, float d, u64 inv) {
+  if (FMT == VBS_I8) {
+    const u64 k = pair(12582912.f, 12582912.f);
+    unpair(fma2(pair(a, b), inv, k), a, b);
+    unpair(fma2(pair(c, d), inv, k), c, d);
+    const u32 lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+    const u32 hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+  }
+  unpair(mul2(pair(a, b), inv), a, b);
+  unpair(mul2(pair(c, d), inv), c, d);
+  return encode4<FMT>(a, b, c, d);
 }
 
 }  // namespace vbs

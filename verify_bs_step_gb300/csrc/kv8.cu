@@ -11,9 +11,9 @@
 // A warp owns one run of consecutive tokens in one page, for one head of K or of V.  Where the rows can be
 // loaded 16 bytes at a time it holds up to 16 tokens x 128 dims in registers between the maximum and the
 // rounding (longer runs are read again, from L2), with all loads in flight at once.  What bounds it is the
-// stream of the rows in and the codes out: 64 prompts of 1000 tokens, 8 heads x 128 dims, bf16 to int8, take 82 us
-// (262 MB read, 131 written: 4.8 TB/s, 71 % of the measured copy); a single token's step is latency: slot,
-// scale, row (256 rows x 8 heads: 10 us).
+// stream of the rows in and the codes out: 64 prompts of 1000 tokens, 8 heads x 128 dims, bf16 to int8, take 77 us
+// (262 MB read, 131 written: 5.1 TB/s, 75 % of the measured copy; 4 CTAs an SM instead of 3 took 83); a single
+// token's step is latency: slot, scale, row (256 rows x 8 heads: 10 us).
 
 #include "codes.cuh"
 #include "common.cuh"
@@ -78,7 +78,15 @@ template <int FMT> __device__ __forceinline__ int regrow(const Kv8Geom& g, int64
   return e;
 }
 
-// One run, element by element: rows of any alignment, and runs that hold NaN or infinities.
+// The larger magnitudes of two pairs of bf16, a NaN before all.
+__device__ __forceinline__ u32 max_abs2(u32 a, u32 b) {
+  const __nv_bfloat162 x = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&a));
+  const __nv_bfloat162 y = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b));
+  const __nv_bfloat162 z = __hmax2_nan(x, y);
+  return *reinterpret_cast<const u32*>(&z);
+}
+
+// One run, element by element: rows of any alignment, and runs that hold NaN, infinities or values past the largest scale.
 template <int FMT, typename T>
 __device__ __noinline__ void append_elements(const Kv8Geom& g, const void* base, int64_t tok, int64_t p0, int64_t run,
                                              int off, int len, int lane) {
@@ -154,22 +162,28 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
       append_elements<FMT, T>(g, base, tok, p0, run, o, len, lane);
       continue;
     }
-    const char* rows = static_cast<const char*>(base) + p0 * Elem<T>::BYTES;
     const int cpr = g.D / EPC, total = len * cpr;   // 16-byte pieces of a row, of the run
-    const int dt = 32 / cpr, dc = 32 - dt * cpr;    // from a lane's piece to its next
+    const int t0 = lane / cpr, q0 = lane - t0 * cpr;          // a lane's first piece; from one to its next:
+    const int dt = 32 / cpr, dc = 32 - dt * cpr;
+    const int64_t row = tok * Elem<T>::BYTES, ahead = dt * row + dc * 16, wrap = row - cpr * 16;
+    const char* const first = static_cast<const char*>(base) + p0 * Elem<T>::BYTES + t0 * row + q0 * 16;
+    const char* at_q = first;
+    int c_q = q0;
     uint4 q[NR];
-    // the run's pieces c0 + lane, + 32, ... into q
+    // the lane's next pieces, the first of them piece c0 + lane of the run, into q
     auto load = [&](int c0) {
-      int t = (c0 + lane) / cpr, c = c0 + lane - t * cpr;
+      const int left = total - c0 - lane;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         q[r] = make_uint4(0, 0, 0, 0);
-        if (c0 + r * 32 + lane < total) q[r] = ld_stream16(rows + (t * tok) * Elem<T>::BYTES + c * 16);
-        t += dt;
-        c += dc;
-        if (c >= cpr) {
-          c -= cpr;
-          ++t;
+        if (r * 32 < left) q[r] = ld_stream16(at_q);
+        at_q += ahead;
+        if (dc != 0) {
+          c_q += dc;
+          if (c_q >= cpr) {
+            c_q -= cpr;
+            at_q += wrap;
+          }
         }
       }
     };
@@ -179,9 +193,7 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         if (Elem<T>::BYTES == 2) {
-          const u32 a = __vmaxu2(__vmaxu2(q[r].x & 0x7fff7fffu, q[r].y & 0x7fff7fffu),
-                                 __vmaxu2(q[r].z & 0x7fff7fffu, q[r].w & 0x7fff7fffu));
-          top = __vmaxu2(top, a);
+          top = max_abs2(top, max_abs2(max_abs2(q[r].x, q[r].y), max_abs2(q[r].z, q[r].w)));
         } else {
           top = max(max(max(top, q[r].x & 0x7fffffffu), q[r].y & 0x7fffffffu),
                     max(q[r].z & 0x7fffffffu, q[r].w & 0x7fffffffu));
@@ -197,72 +209,102 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
     }
     const float amax = __uint_as_float(top);
     int e = scale_exp<FMT>(amax);
+    if (amax * pow2i(-e) > Code<FMT>::TOP * (1 << Code<FMT>::BITS)) {       // past the largest scale: clamped there
+      append_elements<FMT, T>(g, base, tok, p0, run, o, len, lane);
+      continue;
+    }
     if (o > 0) e = regrow<FMT>(g, run, o, e, lane);
-    const float inv = pow2i(-e), lim = Code<FMT>::TOP * (1 << Code<FMT>::BITS);
-    const bool clamp = amax * inv > lim;            // only past the largest scale
-    uint8_t* codes = reinterpret_cast<uint8_t*>(g.pool) + (run * g.block + o) * g.D;
+    const u64 inv = pair(pow2i(-e), pow2i(-e));
+    uint8_t* codes = reinterpret_cast<uint8_t*>(g.pool) + (run * g.block + o) * g.D + lane * EPC;
+    at_q = first;
+    c_q = q0;
     for (int c0 = 0; c0 < total; c0 += NR * 32) {
       if (total > NR * 32) load(c0);
+      const int left = total - c0 - lane;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const int c = c0 + r * 32 + lane;
-        if (c >= total) continue;
+        if (r * 32 >= left) continue;
         float v[EPC];
         Vec16<T>::unpack(q[r], v);
-#pragma unroll
-        for (int y = 0; y < EPC; ++y) {
-          v[y] *= inv;
-          if (clamp) v[y] = fminf(fmaxf(v[y], -lim), lim);
-        }
-        const u32 w0 = encode4<FMT>(v[0], v[1], v[2], v[3]);
+        const u32 w0 = encode4_scaled<FMT>(v[0], v[1], v[2], v[3], inv);
         if (EPC == 8) {
-          const u32 w1 = encode4<FMT>(v[EPC - 4], v[EPC - 3], v[EPC - 2], v[EPC - 1]);
-          *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(w0, w1);
+          const u32 w1 = encode4_scaled<FMT>(v[EPC - 4], v[EPC - 3], v[EPC - 2], v[EPC - 1], inv);
+          *reinterpret_cast<uint2*>(codes + r * 256) = make_uint2(w0, w1);
         } else {
-          *reinterpret_cast<u32*>(codes + c * 4) = w0;
+          *reinterpret_cast<u32*>(codes + r * 128) = w0;
         }
       }
+      codes += NR * 32 * EPC;
     }
     if (lane == 0) g.scales[run] = pow2i(e);
   }
 }
 
-// A warp a token: its 2 H D codes, 16 a lane, as bf16.
-template <int FMT>
-__global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8Geom g, int64_t n, const int64_t* __restrict__ slots,
+// A warp a token: its 2 H D codes, 16 a lane, as bf16; a lane's 32 bytes go out in one store where they may (WIDE:
+// 81 us against 87 when that was tried).  The chain of slot, codes and stores bounds a warp, so that many warps with two
+// pieces a lane do better than fewer with four: 64 prompts of 1000 tokens, 8 heads x 128 dims, take 72 us (131 MB read,
+// 262 written: 5.4 TB/s) against 79.
+constexpr int KV8_RD = 2;                           // pieces of 16 codes that a lane of the reading kernel holds
+template <int FMT, bool WIDE>
+__global__ void __launch_bounds__(KV8_NT, 6) kv8_read_kernel(const Kv8Geom g, int64_t n, const int64_t* __restrict__ slots,
                                                           uint16_t* k_out, uint16_t* v_out) {
   const int lane = threadIdx.x & 31, per = g.D / 16, all = 2 * g.H * per;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * KV8_NT + threadIdx.x) >> 5; i < n;
-       i += (static_cast<int64_t>(gridDim.x) * KV8_NT) >> 5) {
-    const int64_t s = slots[i];
+  const int dk = 32 / per, dc = 32 - dk * per;
+  const int64_t stride = (static_cast<int64_t>(gridDim.x) * KV8_NT) >> 5;
+  int64_t i = (static_cast<int64_t>(blockIdx.x) * KV8_NT + threadIdx.x) >> 5;
+  int64_t next = i < n ? slots[i] : -1;
+  for (; i < n; i += stride) {
+    const int64_t s = next;
+    if (i + stride < n) next = slots[i + stride];
     const bool held = s >= 0 && s < g.NB * g.block;
     if (s >= 0 && !held && lane == 0) set_status(g.status, VBS_EINVAL);
-    const int64_t page = held ? s / g.block : 0;
+    const int64_t page = !held ? 0 : s <= UINT32_MAX ? static_cast<u32>(s) / static_cast<u32>(g.block) : s / g.block;
     const int64_t run0 = g.run(page, 0, 0);
     const char* codes = g.pool + (run0 * g.block + (held ? s - page * g.block : 0)) * g.D;
-#pragma unroll 4
-    for (int j = lane; j < all; j += 32) {
-      const int kvh = j / per, c = j - kvh * per;
-      uint4 q = make_uint4(0, 0, 0, 0);
-      float sc = 0.f;
-      if (held) {
-        q = ld_stream16(codes + static_cast<int64_t>(kvh) * g.block * g.D + c * 16);
-        sc = g.scales[run0 + kvh];
-      }
-      const u32 w[4] = {q.x, q.y, q.z, q.w};
-      u32 o[8];
+    const int64_t head = static_cast<int64_t>(g.block) * g.D;
+    for (int j0 = blockIdx.y * KV8_RD * 32 + lane; j0 < all; j0 += gridDim.y * KV8_RD * 32) {
+      int kvh = j0 / per, c = j0 - kvh * per;
+      uint4 q[KV8_RD];
+      float sc[KV8_RD];
+      uint16_t* out[KV8_RD];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        float2 lo, hi;
-        decode4<FMT>(w[y], lo, hi);
-        const __nv_bfloat162 x = __floats2bfloat162_rn(lo.x * sc, lo.y * sc);   // exact: a code has at most 7 bits
-        const __nv_bfloat162 z = __floats2bfloat162_rn(hi.x * sc, hi.y * sc);
-        o[2 * y] = *reinterpret_cast<const u32*>(&x);
-        o[2 * y + 1] = *reinterpret_cast<const u32*>(&z);
+      for (int r = 0; r < KV8_RD; ++r) {
+        q[r] = make_uint4(0, 0, 0, 0);
+        sc[r] = 0.f;
+        if (held && j0 + r * 32 < all) {
+          q[r] = ld_stream16(codes + kvh * head + c * 16);
+          sc[r] = g.scales[run0 + kvh];
+        }
+        out[r] = (kvh < g.H ? k_out : v_out) + (i * g.H + (kvh < g.H ? kvh : kvh - g.H)) * g.D + c * 16;
+        kvh += dk;
+        c += dc;
+        if (c >= per) {
+          c -= per;
+          ++kvh;
+        }
       }
-      uint16_t* out = (kvh < g.H ? k_out : v_out) + (i * g.H + (kvh < g.H ? kvh : kvh - g.H)) * g.D + c * 16;
-      reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+      for (int r = 0; r < KV8_RD; ++r) {
+        if (j0 + r * 32 >= all) continue;
+        const u32 w[4] = {q[r].x, q[r].y, q[r].z, q[r].w};
+        u32 o[8];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float2 lo, hi;
+          decode4<FMT>(w[y], lo, hi);
+          const __nv_bfloat162 x = __floats2bfloat162_rn(lo.x * sc[r], lo.y * sc[r]);   // exact: a code has at most 7 bits
+          const __nv_bfloat162 z = __floats2bfloat162_rn(hi.x * sc[r], hi.y * sc[r]);
+          o[2 * y] = *reinterpret_cast<const u32*>(&x);
+          o[2 * y + 1] = *reinterpret_cast<const u32*>(&z);
+        }
+        if (WIDE) {
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out[r]), "r"(o[0]), "r"(o[1]),
+                       "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+        } else {
+          reinterpret_cast<uint4*>(out[r])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(out[r])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
     }
   }
 }
@@ -295,12 +337,21 @@ int launch_kv8_append(const Kv8Geom& g, const Kv8Src& src, int64_t n, const int6
 int launch_kv8_read(const Kv8Geom& g, int64_t n, const int64_t* slots, void* k_out, void* v_out, int num_sms,
                     cudaStream_t s) {
   if (n == 0) return VBS_OK;
-  const int64_t ctas = std::min<int64_t>((n + KV8_NT / 32 - 1) / (KV8_NT / 32), static_cast<int64_t>(num_sms) * 32);
-  const unsigned grid = static_cast<unsigned>(ctas);
+  // few tokens: a token's codes are shared out over CTAs as well (256 tokens of 2048 codes: 11 to 9 us)
+  const int64_t x = std::min<int64_t>((n + KV8_NT / 32 - 1) / (KV8_NT / 32), static_cast<int64_t>(num_sms) * 32);
+  const int64_t parts = (2 * static_cast<int64_t>(g.H) * g.D / 16 + 32 * KV8_RD - 1) / (32 * KV8_RD);
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>({parts, 4 * num_sms / x, 65535}));
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
   auto* k = static_cast<uint16_t*>(k_out);
   auto* v = static_cast<uint16_t*>(v_out);
-  if (g.fmt == VBS_I8) kv8_read_kernel<VBS_I8><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
-  else kv8_read_kernel<VBS_E4M3><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
+  if (g.fmt == VBS_I8) {
+    if (wide) kv8_read_kernel<VBS_I8, true><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
+    else kv8_read_kernel<VBS_I8, false><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
+  } else {
+    if (wide) kv8_read_kernel<VBS_E4M3, true><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
+    else kv8_read_kernel<VBS_E4M3, false><<<grid, KV8_NT, 0, s>>>(g, n, slots, k, v);
+  }
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
