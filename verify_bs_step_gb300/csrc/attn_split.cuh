@@ -7,7 +7,7 @@
 // has, at its start), and its four warps take every fourth unit.  A segment inside one share is written
 // straight out; one that crosses shares leaves (m, l, o) partials, and a second, dependent launch joins them
 // in order, so equal calls give equal bits.  (Joining in the CTA that arrives last was slower: a fence and an
-// atomic a piece, and one CTA's loads in turn while the others are done.)
+// atomic a piece, and one CTA's loads in turn while the others are done.)  Short segments are not split at all.
 //
 // A warp holds 16 MT rows x head_dim of o in registers.  Units come through a ring of cp.async stages of
 // its own (no barrier between warps), stored with a XOR of 16-byte chunks so that both reads below
@@ -52,6 +52,7 @@ struct SplitArgs {
   float* part;                    // [grid][2][16 MT][DP + 2]: o, m, l of a segment's piece
   int2* pieces;                   // [B * H * MC]: the first and last CTA of a segment in pieces, (0, -1) of a whole one
   bool out8, q8;                  // outputs may be stored, queries loaded 8 bytes at a time
+  bool whole;                     // a CTA a segment, none in pieces
 };
 
 __device__ __forceinline__ void cp_async16(u32 dst, const void* src, bool valid) {
@@ -110,6 +111,7 @@ template <int FMT> struct PagedSrc {
   const int* n_pages;             // [B]
   const int* seen;                // [R]
   int cap, tpp;                   // list entries a sentence, units a page
+  int64_t most() const { return static_cast<int64_t>(cap) * tpp; }
   struct Batch {                  // one unit per lane
     const char* k;                // its K rows; V's stand H runs further on
     UnitHead u;
@@ -153,6 +155,7 @@ struct EncSrc {
   static constexpr bool BF = true;
   EncKV e;
   struct Batch { int u; };
+  int64_t most() const { return (static_cast<int64_t>(e.S) + 15) / 16; }
   __device__ int len(int b) const {
     const int n = e.len[b];
     if (n >= 0 && n <= e.S) return n;
@@ -251,8 +254,13 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
   // ---- this CTA's share of the line ----
   int b = 0;
   int n = 1;                                                // sentence b's units
-  int64_t at = 0, end, per;                                 // position within sentence b's units (all heads)
-  {
+  int64_t at = 0, end, per = 1;                             // position within sentence b's units (all heads)
+  if (sa.whole) {
+    b = blockIdx.x / HM;
+    n = src.units(b);
+    end = n + SP_FIX;
+    at = (blockIdx.x - b * HM) * end;
+  } else {
     const int k = (sa.B + NT - 1) / NT;               // a thread's sentences: [tid * k, tid * k + k)
     int64_t mine = 0;
     int own = 0;                                            // the last one's units
@@ -692,7 +700,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
     }
 
     // the CTA with a segment's first unit says where its pieces are
-    if (u0 == 0 && tid == 0)
+    if (u0 == 0 && tid == 0 && !sa.whole)
       sa.pieces[static_cast<int64_t>(b) * HM + hm] =
           whole ? make_int2(0, -1) : make_int2(static_cast<int>((line + SP_FIX) / per), static_cast<int>((line + nf - 1) / per));
     __syncthreads();                                        // the ring and the row statistics are free again
@@ -866,8 +874,14 @@ int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_s
   static std::atomic<unsigned long long> attr_done{0};
   auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
   if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
+  const int64_t segments = static_cast<int64_t>(sa.B) * sa.H * sa.MC;
+  if (src.most() <= SP_WHOLE && segments < (int64_t{1} << 31)) {
+    SplitArgs one = sa;
+    one.whole = true;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(segments)), dim3(32 * NW), C::SMEM, s, src, io, one);
+  }
   if (launch_dependent(kernel, dim3(num_sms * C::CTAS), dim3(32 * NW), C::SMEM, s, src, io, sa) != VBS_OK) return VBS_ECUDA;
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(sa.B) * sa.H * sa.MC), (std::min(sa.M, 16 * MT) + JN_WARPS - 1) / JN_WARPS);
+  const dim3 grid(static_cast<unsigned>(segments), (std::min(sa.M, 16 * MT) + JN_WARPS - 1) / JN_WARPS);
   return launch_dependent(attn_join_kernel<DP, 16 * MT>, grid, dim3(32 * JN_WARPS), 0, s, io, sa);
 }
 
@@ -892,7 +906,7 @@ int launch_split(const Src& src, const QO& io, const SplitArgs& sa, int num_sms,
 }
 
 inline SplitArgs split_args(const QO& io, int B, int W, int H, int D, float* part, int2* pieces) {
-  SplitArgs sa{B, W, H, D, io.Hq / H, W * io.n_q * (io.Hq / H), 0, part, pieces, false, false};
+  SplitArgs sa{B, W, H, D, io.Hq / H, W * io.n_q * (io.Hq / H), 0, part, pieces, false, false, false};
   sa.MC = split_chunks(sa.M, D);
   sa.out8 = (reinterpret_cast<uintptr_t>(io.o) & 7) == 0 && (io.o_row | io.o_tok | io.o_head) % 4 == 0;
   sa.q8 = (reinterpret_cast<uintptr_t>(io.q) & 7) == 0 && (io.q_row | io.q_tok | io.q_head) % 4 == 0;

@@ -595,13 +595,23 @@ bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
   //   32 heads, 128 rows x 1024           16.1 / 24.9, 18.7 / 28.8;   x 8192   79.0 / 69.7, 91 / 113
   //   256 heads, 32 rows x 1024           18.0 / 30.0, 28.8 / 45.9;   512 rows x 8192   342 / 1786, 415 / 3111
   // (and up to 16 rows, where the split kernel needs one mma tile, 14.9 / 10.8 and 92 / 100 at the ends).
+  // Where the split kernel does not split (up to SP_WHOLE units) it wins on short sentences as long as its CTAs are
+  // resident at once, and by less where they share an SM:
+  //   up to 152 segments of 32 rows x 32    5.4 / 7.5 (split / tiles), 6.2 / 9.5;   x 256   8.1 / 8.6, 10.6 / 10.5
+  //   256 segments x 128                    8.7 / 8.9, 10.5 / 11.4;                 x 256   11.3 / 10.5, 14.0 / 12.8
+  //   512 segments x 32                     11.4 / 9.1, 14.4 / 11.0
   const bool wide = e.D > 64;
   const double heads = static_cast<double>(e.B) * e.H, tiles = heads * ((M + TC_M - 1) / TC_M);
   const double tc = (wide ? 8.0 : 6.0) + (e.S + TC_N - 1) / TC_N * 0.56 * std::max(1.0, tiles / (2 * num_sms));
   const double alone = wide ? std::min(24.0, std::max(12.0, 6.0 + e.S / 70.0))
                             : std::min(18.0, std::max(9.3, 5.0 + e.S / 100.0));
   const double split = alone + heads * ((M + 31) / 32) * ((e.S + 15) / 16) * (wide ? 0.0015 : 0.00085);
-  if (tc > split) return false;
+  if (e.S <= 16 * SP_WHOLE) {
+    const double segments = heads * ((M + 31) / 32);
+    if (segments <= 2 * num_sms && e.S <= (wide ? 256 : 384) / (segments > num_sms ? 2 : 1)) return false;
+  } else if (tc > split) {
+    return false;
+  }
   auto stride_ok = [](int64_t s, int64_t extent) { return extent == 1 || (s > 0 && s % 8 == 0 && s < (int64_t{1} << 38)); };
   return ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 && stride_ok(e.k_sent, e.B) &&
          stride_ok(e.k_pos, e.S) && stride_ok(e.k_head, e.H) && stride_ok(e.v_sent, e.B) && stride_ok(e.v_pos, e.S) &&
