@@ -647,9 +647,7 @@ class PagedKV8(PagedKV):
         cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
         shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
         qs = _rows4(q, "q", shape)
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        os_ = _rows4(out, "out", shape)
+        out, os_ = _output(out, shape, self.device)
         self._order.run(lib().kv8_attention, "kv8_attention", (q, out), self.ctx8, layer, q.data_ptr(), qs[0], qs[1], qs[2],
                         self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
         return out
@@ -669,6 +667,14 @@ def _rows4(t: torch.Tensor, name: str, shape):
     if not t.is_cuda or t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
     return st
+
+
+def _output(out, shape, device):
+    """The caller's output or a new one, and its strides."""
+    if out is not None:
+        return out, _rows4(out, "out", shape)
+    row = shape[2] * shape[3]
+    return torch.empty(shape, dtype=torch.bfloat16, device=device), (shape[1] * row, row, shape[3])
 
 
 class CrossAttention:
@@ -701,9 +707,7 @@ class CrossAttention:
         if enc_len.shape != (self.batch,) or not enc_len.is_contiguous():
             raise ValueError(f"enc_len must be a contiguous int32 [{self.batch}] tensor")
         lp = _cuda(enc_len, "enc_len", torch.int32)
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        os_ = _rows4(out, "out", shape)
+        out, os_ = _output(out, shape, self.device)
         self._order.run(lib().xattn_run, "xattn_run", (q, k, v, enc_len, out), self.ctx, q.data_ptr(), qs[0], qs[1], qs[2],
                         n_q, k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2], S, lp,
                         self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
