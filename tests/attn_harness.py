@@ -51,13 +51,13 @@ class Decode:
     """A ragged decode on a PagedKV8: prompts, then positions written one by one with reorders between."""
 
     def __init__(self, fmt, lens, W, heads, H, D, block, gen, *, max_q=1, L=2, layer=1, seed=0, spread=0.7,
-                 reorder_every=3, garbage=True):
+                 reorder_every=3, garbage=True, spare=0):
         import verify_bs_step_gb300 as vbs
         self.rng = np.random.default_rng(seed)
         self.lens, self.W, self.H, self.D, self.layer, self.spread = np.asarray(lens), W, H, D, layer, spread
         B = len(lens)
         self.R = B * W
-        S = -(-max(lens) // block) + W * (gen // block + 3)
+        S = -(-max(lens) // block) + W * (gen // block + 3) + spare
         MB = (max(lens) + gen) // block + 1
         self.kv = kv = vbs.PagedKV8(B, W, L, H, D, heads=heads, max_q=max_q, blocks_per_sentence=S, max_blocks=MB,
                                     block=block, dtype=DT[fmt])

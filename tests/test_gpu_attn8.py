@@ -68,6 +68,26 @@ def test_long_rows_are_split_and_joined(fmt):
         d.kv.close()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("lens,W,heads,H,D,block,n_q,gen", [
+    ([1], 1, 1, 1, 16, 1, 1, 0),
+    ([5, 0, 33, 16], 3, 4, 2, 64, 16, 1, 9),
+    ([19, 700, 7], 2, 6, 6, 80, 8, 1, 11),
+    ([90, 300], 5, 7, 1, 32, 24, 1, 3),
+    ([40, 65], 2, 4, 2, 256, 32, 1, 5),
+    ([8, 3, 150, 0, 64], 1, 8, 2, 128, 32, 8, 0),
+])
+def test_short_rows_in_a_cache_with_room_for_long_ones(fmt, lens, W, heads, H, D, block, n_q, gen):
+    """What is short but not bound to be: segments in pieces.  The same rows in a cache without that room, where a
+    CTA takes a whole one, are held to the same bound."""
+    for spare in (0, 800):
+        d = Decode(fmt, lens, W, heads, H, D, block, gen, max_q=n_q, seed=D + n_q, spare=spare)
+        q = _q(d, n_q, heads)
+        d.kv.plan(i32(d.ctx), n_q)
+        d.check(d.kv.attend(d.layer, q), q, what=f"{fmt} {spare}")
+        d.kv.close()
+
+
 def test_lengths_of_each_row():
     """ctx_len below what the tables cover, zero in some rows, different within a sentence."""
     d = Decode("e4m3", [37, 50], 4, 4, 2, 64, 16, 10)

@@ -67,6 +67,26 @@ def test_matches_the_oracle(B, W, n_q, Hq, H, S, D):
     x.close()
 
 
+@pytest.mark.parametrize("S", [768, 769, 2000])
+@pytest.mark.parametrize("W,n_q,Hq,H,D,offset", [
+    (4, 1, 8, 8, 64, 0), (2, 1, 3, 1, 80, 0), (1, 5, 2, 2, 128, 0), (5, 8, 2, 2, 64, 1), (3, 12, 1, 1, 256, 0), (2, 20, 2, 1, 128, 1),
+    (1, 24, 2, 2, 64, 0),
+])
+def test_short_sentences_beside_the_longest(S, W, n_q, Hq, H, D, offset):
+    """Lengths far below S, on both sides of the size up to which a segment is not split."""
+    import verify_bs_step_gb300 as vbs
+    lens = [S, 1, 0, 17, S - 1, 16]
+    B = len(lens)
+    x = vbs.CrossAttention(B, W, Hq, D, kv_heads=H, max_q=n_q, max_len=S)
+    q, k, v = _tensors(B, W, n_q, Hq, H, S, D, seed=S + D)
+    if offset:                                      # not 16-byte aligned: loaded element by element
+        k = torch.empty(1 + k.numel(), device="cuda", dtype=torch.bfloat16)[1:].view(k.shape).copy_(k)
+    out = x.attend(q, k, v, i32(lens))
+    _check(out, q, k, v, lens, W, sample=6)
+    assert x.status() == 0
+    x.close()
+
+
 @pytest.mark.parametrize("n_q", [1, 6, 64, 150])
 def test_what_lies_past_a_sentences_end_is_not_used(n_q):
     import verify_bs_step_gb300 as vbs
