@@ -124,6 +124,58 @@ def test_extreme_values(fmt):
     m.kv.close()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_extreme_values_in_bf16(fmt):
+    """What the paired comparisons of bf16 rows have to see: a NaN or infinity in either half, the largest and smallest."""
+    import verify_bs_step_gb300 as vbs
+    tiny = 2.0 ** -133
+    rows = torch.randn(12, 1, 32, device="cuda").to(torch.bfloat16)
+    rows[1] = 0
+    rows[2], rows[3] = tiny, -3.38e38
+    rows[4, 0, ::2], rows[5, 0, 1::2] = 3.38e38, 2.0 ** 100
+    m = Model(fmt, 1, 12, 1, 1, 32, 4)
+    slots = np.arange(12) * 4
+    m.append(0, rows, -rows, slots)
+    m.check()
+    m.append(0, rows.flip(0).contiguous(), rows, slots + 1)
+    m.check()
+    assert m.kv.status() == 0
+    bad = rows.clone()
+    for i, x in enumerate([float("nan"), float("inf"), float("-inf"), float("-nan")] * 3):
+        bad[i, 0, 5 * i % 32] = x
+    m.append(0, bad, rows, slots + 2)
+    m.check()
+    assert m.kv.status() == vbs.EINPUT
+    m.kv.close()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("H,D,block,N", [(5, 48, 24, 3), (1, 16, 1, 5000), (33, 256, 16, 40), (3, 80, 8, 7000), (8, 128, 16, 1)])
+def test_read_of_few_and_many_tokens(fmt, H, D, block, N):
+    """Any codes under any scales, into outputs that are 32-byte aligned and ones that are not."""
+    import verify_bs_step_gb300 as vbs
+    g = torch.Generator(device="cuda").manual_seed(N)
+    S = 300
+    kv = vbs.PagedKV8(1, 1, 2, H, D, heads=H, blocks_per_sentence=S, max_blocks=S, block=block, dtype=DT[fmt])
+    codes = torch.randint(-127, 127, kv.pool.shape, device="cuda", generator=g, dtype=torch.int8)
+    kv.pool.copy_(codes if fmt == "int8" else (codes.float() / 4).to(torch.float8_e4m3fn))
+    kv.scales.copy_(torch.exp2(torch.randint(-60, 61, kv.scales.shape, device="cuda", generator=g).float()))
+    slots = torch.randint(0, S * block, (N,), device="cuda", generator=g)
+    slots[::7] = -1
+    page, off = slots.clamp(min=0) // block, slots.clamp(min=0) % block
+    want = kv.pool.float()[page, 1, :, :, off] * kv.scales[page, 1][..., None]
+    want[slots < 0] = 0
+    k, v = kv.read(1, slots)
+    assert torch.equal(k.float(), want[:, 0]) and torch.equal(v.float(), want[:, 1])
+    flat = torch.full((2, N * H * D + 16), 3.0, device="cuda", dtype=torch.bfloat16)
+    st = vbs.lib().kv8_read(kv.ctx8, 1, N, slots.data_ptr(), flat[0, 8:].data_ptr(), flat[1, 8:].data_ptr())
+    assert st == vbs.OK and kv.status() == 0
+    got = flat[:, 8:-8].view(2, N, H, D)
+    assert torch.equal(got[0], k) and torch.equal(got[1], v)
+    assert (flat[:, :8] == 3).all() and (flat[:, -8:] == 3).all()
+    kv.close()
+
+
 def test_strides_offsets_and_skipped_slots():
     """K and V as slices of one projection, at an odd storage offset, with skipped tokens."""
     rng = np.random.default_rng(9)
