@@ -188,14 +188,18 @@ template <int EL, int DP, int MT> struct SplitCfg {
   static constexpr int NT = DP / 8;                         // output tiles of 8 dims
   static constexpr int VCH = NT < CHK ? NT : CHK;           // dims of a position that a lane reads at once
   static constexpr int STAGE = 2 * 16 * DP * EL;            // bytes of K and V of one unit
-  static constexpr int NS = STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
+  // one tile of rows over 8-bit codes of up to 64 dims: little to hold, so that a shorter ring (4 stages, not 8) and a
+  // fourth CTA an SM pay (1024 sentences x 8 heads x 64..1024 positions: 94 to 76 us .. 195 to 183; 64 x 512: 14.9 to 13.3;
+  // 16 sentences, which do not fill the GPU: 1..5 % slower)
+  static constexpr bool SMALL = EL == 1 && DP == 64 && MT == 1;
+  static constexpr int NS = SMALL ? 4 : STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
   static constexpr int O_LD = DP + 4;                       // floats of an o row in shared memory
   static constexpr int RING = NS * STAGE > MT * 16 * O_LD * 4 ? NS * STAGE : MT * 16 * O_LD * 4;
   static constexpr int QBYTES = MT * KS * 512;              // Q in fragment order
   static constexpr int PART = MT * 16 * (DP + 2);           // floats of a partial
   static constexpr size_t SMEM = NW * RING + QBYTES;
   // resident CTAs a SM, by shared memory and by o's registers (MT * DP / 2 of a thread's)
-  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 ? 2 : 3);
+  static constexpr int CTAS = SMEM > 113 * 1024 ? 1 : (SMEM > 75 * 1024 || MT * DP > 128 ? 2 : SMALL ? 4 : 3);
 };
 
 // The order of output dims: column n of output tile j.
@@ -863,14 +867,15 @@ int launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 inline int split_mt(int M, int D) { return M > 16 && D <= 128 ? 2 : 1; }
 inline int split_chunks(int M, int D) { return (M + 16 * split_mt(M, D) - 1) / (16 * split_mt(M, D)); }
 inline int split_dp(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
-// floats of the partials of any grid: up to 12 warps a SM, of up to 32 rows
+// floats of the partials of any grid: two pieces a CTA, up to 4 CTAs an SM of up to 32 rows
 inline int64_t split_part_floats(int D, int num_sms) {
-  return static_cast<int64_t>(num_sms) * 12 * 2 * 32 * (split_dp(D) + 2);
+  return static_cast<int64_t>(num_sms) * 4 * 2 * 32 * (split_dp(D) + 2);
 }
 
 template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
 int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
   using C = SplitCfg<Src::EL, DP, MT>;
+  static_assert(C::CTAS * MT * 16 <= 4 * 32, "split_part_floats");
   static std::atomic<unsigned long long> attr_done{0};
   auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
   if (!smem_attr_once(kernel, static_cast<int>(C::SMEM), attr_done)) return VBS_ECUDA;
