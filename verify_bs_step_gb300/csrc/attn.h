@@ -38,13 +38,14 @@ struct Kv8Plan {
 
 int launch_kv8_plan(const PagedArgs& a, const int32_t* ctx, const Kv8Plan& p, cudaStream_t s);
 
-// Where no sentence can have more units of 16 positions than this (the cache's or the encoder's size says so), a CTA of the split
-// kernel takes a whole segment, and the second launch is left out: 1.0 to 2 times as fast up to here over 8 to 16384 segments of head_dim 64 to
-// 256 and 4 to 128 rows (8 segments x 16 units: 9 to 7 us; 512 x 16: 15 to 13; 64 x 48: 14 to 11; at worst 512 x 48 of
-// head_dim 128: 31 to 33, and 16384 x 4: 206 to 223); with 64 units few segments lose (8 x 64: 14.5 to 15.6), with 128 most.
+// Where no sentence can have more units of 16 positions than this (the cache's or the encoder's size says so), a CTA
+// of the split kernel takes a whole segment, and the second launch is left out: up to 2 times as fast over 8 to 16384
+// segments of head_dim 64 to 256 and 4 to 128 rows (8 segments x 16 units: 9 to 7 us; 512 x 16: 15 to 13; 64 x 48: 14 to
+// 11; at worst 512 x 48 of head_dim 128: 31 to 33, and 16384 x 4: 206 to 223); with 64 units few segments lose (8 x 64:
+// 14.5 to 15.6), with 128 most.
 constexpr int SP_WHOLE = 48;
 
-// Partials of the split: workspace of split_part_floats(D) floats, and one zeroed counter per segment.
+// Workspace of the split: attn_part_floats floats of partials, and attn_segments entries of where each segment's are.
 int64_t attn_part_floats(int D, int num_sms);
 int64_t attn_segments(int B, int W, int H, int D, int Hq, int n_q);
 int launch_kv8_attention(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
