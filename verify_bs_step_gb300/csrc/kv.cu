@@ -226,7 +226,7 @@ struct CowMap {
     const int4 t = tasks[item / n_runs];
     const int64_t run = item % n_runs;
     if (t.z > 0 && VBS_CHECK(t.x >= 0 && t.x < n_blocks && t.y >= 0 && t.y < n_blocks, 11, t.x, status))
-      scales[t.y * n_runs + run] = scales[t.x * n_runs + run];
+      scales[static_cast<int64_t>(t.y) * n_runs + run] = scales[static_cast<int64_t>(t.x) * n_runs + run];
   }
   __device__ void operator()(int64_t item, const char*& s, char*& d, u32& bytes) const {
     const int q = static_cast<int>(item / n_runs);
