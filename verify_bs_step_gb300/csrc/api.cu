@@ -471,8 +471,7 @@ VBS_EXPORT int kv_paged_init(vbs_pkv** out, const vbs_kv_desc* d, int batch, int
     a.nblk = cv.take<int32_t>(R);
     a.refcnt = cv.take<int32_t>(NB);
     a.stack = cv.take<int32_t>(NB);
-    a.top = cv.take<int32_t>(batch);
-    a.base = cv.take<int32_t>(batch);
+    a.top = cv.take<int32_t>(2 * static_cast<size_t>(batch));
     const size_t state_end = cv.off;
     c->saved = cv.take<char>(state_end);
     c->state = reinterpret_cast<char*>(a.table);
@@ -522,7 +521,7 @@ static int paged_run(vbs_pkv* c, const int32_t* bi, int t_valid) {
   int st = vbs::launch_kv_paged_remap(c->a, bi, t_valid, c->stream);
   if (st != VBS_OK) return st;
   const bool bulk_ok = c->a.slot_bytes % 16 == 0 && aligned16(c->a.pool);
-  return vbs::launch_kv_paged_cow(c->a, bulk_ok, num_sms(), c->stream);
+  return vbs::launch_kv_paged_cow(c->a, c->scales, bulk_ok, num_sms(), c->stream);
 }
 
 VBS_EXPORT int kv_paged_prefill(vbs_pkv* c, int P) {
@@ -543,7 +542,7 @@ VBS_EXPORT int kv_paged_prefill(vbs_pkv* c, int P) {
   ok = ok && cudaMemcpyAsync(a.refcnt, refcnt.data(), refcnt.size() * 4, cudaMemcpyHostToDevice, c->stream) == cudaSuccess;
   ok = ok && cudaMemcpyAsync(a.stack, stack.data(), stack.size() * 4, cudaMemcpyHostToDevice, c->stream) == cudaSuccess;
   ok = ok && cudaMemcpyAsync(a.top, top.data(), top.size() * 4, cudaMemcpyHostToDevice, c->stream) == cudaSuccess;
-  ok = ok && cudaMemsetAsync(a.base, 0, sizeof(int32_t) * a.B, c->stream) == cudaSuccess;
+  ok = ok && cudaMemsetAsync(a.base(), 0, sizeof(int32_t) * a.B, c->stream) == cudaSuccess;
   ok = ok && cudaMemsetAsync(a.tasks, 0, sizeof(int4) * c->R, c->stream) == cudaSuccess;
   ok = ok && cudaStreamSynchronize(c->stream) == cudaSuccess;
   c->copy_pending = false;
@@ -618,7 +617,7 @@ VBS_EXPORT int bs_step_paged(vbs_bs* c, const void* logits, int64_t ld, float* s
 VBS_EXPORT int kv_paged_copy(vbs_pkv* c) {
   if (!c) return VBS_EINVAL;
   const bool bulk_ok = c->a.slot_bytes % 16 == 0 && aligned16(c->a.pool);
-  const int st = vbs::launch_kv_paged_cow(c->a, bulk_ok, num_sms(), c->stream);
+  const int st = vbs::launch_kv_paged_cow(c->a, c->scales, bulk_ok, num_sms(), c->stream);
   if (st == VBS_OK) c->copy_pending = false;
   return st;
 }

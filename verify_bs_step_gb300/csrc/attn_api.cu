@@ -39,7 +39,7 @@ VBS_EXPORT int kv8_init(vbs_kv8** out, vbs_pkv* kv, int format, float* scales, i
   if (kv->elem_bytes != 1 || a.slot_bytes % 16 != 0 || a.slot_bytes > 256) return VBS_EINVAL;
   if (q_heads < 1 || q_heads % a.H != 0 || max_q < 1 || max_q > 32) return VBS_EINVAL;
   if (!aligned16(a.pool)) return VBS_EALIGN;
-  if (a.scales) return VBS_ESTATE;
+  if (kv->scales) return VBS_ESTATE;
   vbs_kv8* c = new (std::nothrow) vbs_kv8{};
   if (!c) return VBS_ENOMEM;
   c->kv = kv;
@@ -77,7 +77,7 @@ VBS_EXPORT int kv8_init(vbs_kv8** out, vbs_pkv* kv, int format, float* scales, i
     delete c;
     return VBS_ECUDA;
   }
-  kv->a.scales = scales;          // copy-on-write carries a page's scales along
+  kv->scales = scales;
   *out = c;
   return VBS_OK;
 }
@@ -125,7 +125,7 @@ VBS_EXPORT int kv8_attention(vbs_kv8* c, int layer, const void* q, int64_t q_row
 VBS_EXPORT int kv8_destroy(vbs_kv8* c) {
   if (!c) return VBS_OK;
   cudaStreamSynchronize(c->kv->stream);
-  c->kv->a.scales = nullptr;
+  c->kv->scales = nullptr;
   cudaFree(c->dev_block);
   delete c;
   return VBS_OK;

@@ -41,6 +41,7 @@ struct vbs_pkv {
   int32_t* identity;
   int R;
   int elem_bytes;
+  float* scales;         // of an 8-bit cache (kv8_init), else NULL: copy-on-write carries a page's scales along
   void* dev_block;
   char* state;           // table .. base: one contiguous range of the allocation
   char* saved;           // its copy (kv_paged_save / kv_paged_restore)

@@ -22,6 +22,7 @@ namespace vbs {
 struct RemapShared {
   int nold[WMAX], par[WMAX], nnew[WMAX], tail[WMAX];
   int top;
+  int ti, fill;                        // the block that position t_valid falls into, the slots filled before it
 };
 
 // Shared-memory ints the remap needs besides RemapShared.
@@ -59,7 +60,9 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
     p = __ldcg(bi + r0 + tid);                            // a fused caller wrote it in this kernel
   }
   if (tid == 0) top = a.top[b];
-  const int base = a.base[b];
+  // one thread finds the block of the position while the tables are on their way
+  int t_abs = 0;
+  if (tid == NT - 1) t_abs = a.base()[b] + t_valid;
   for (int i0 = 0; i0 < nt || i0 < S; i0 += NT * LU) {
     int tv[LU], rv[LU], sv[LU];
 #pragma unroll
@@ -92,6 +95,10 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
     sh.par[tid] = p;
   }
   if (tid == 0) sh.top = top;
+  if (tid == NT - 1) {
+    sh.ti = t_abs / a.block;
+    sh.fill = t_abs % a.block;
+  }
   if (!__syncthreads_or(live)) {                          // a finished sentence: nothing moves
     if (tid < W) a.tasks[r0 + tid] = make_int4(0, 0, 0, 0);
     return;
@@ -132,8 +139,7 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
     // the block holding position t_valid must be exclusive to each live row: a row whose
     // parent ends just before it takes a fresh block (kind 1); a row whose parent's block
     // there is shared keeps it if it is the lowest such row, else copies it (kind 2)
-    const int t_abs = base + t_valid;
-    const int i = t_abs / a.block, fill = t_abs % a.block;
+    const int i = sh.ti, fill = sh.fill;
     const u32 lt = (1u << lane) - 1u;
     int kind = 0, blk = -1, nnew = 0;
     if (lane < W) {
@@ -197,7 +203,7 @@ __device__ void paged_remap_sentence(const PagedArgs& a, int b, const int32_t* b
   __syncthreads();
 
   // write back
-  const int ti = (base + t_valid) / a.block;
+  const int ti = sh.ti;
   for (int i = tid; i < W * MB; i += NT) {
     const int w = i / MB, s = i - w * MB;
     const int p = sh.par[w];

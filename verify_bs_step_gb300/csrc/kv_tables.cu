@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
     }
     if (t0 == 0) {
       a.top[i] = a.S - nb;
-      a.base[i] = count;
+      a.base()[i] = count;
     }
   }
   if (!s.slots) return;
