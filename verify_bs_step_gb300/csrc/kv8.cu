@@ -61,6 +61,7 @@ template <int FMT> __device__ __forceinline__ int scale_exp(float amax) {
 // it grows, the codes before `off` are rounded to it.
 template <int FMT> __device__ __forceinline__ int regrow(const Kv8Geom& g, int64_t run, int off, int e, int lane) {
   const int e_old = exp2i(g.scales[run]);
+  __syncwarp();                                     // read by all lanes before lane 0 writes the new one
   if (e_old >= e) return e_old;
   const float f = e_old - e < -126 ? 0.f : pow2i(e_old - e);
   uint4* codes = reinterpret_cast<uint4*>(g.pool + run * g.block * g.D);
