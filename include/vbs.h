@@ -463,8 +463,9 @@ int kv8_init(vbs_kv8** ctx, vbs_pkv* pkv, int format, float* scales, int q_heads
  * (elements of dtype VBS_BF16 or VBS_F32, head_dim contiguous; v likewise) and goes to slot
  * slots[i] (int64 device, block * block_size + offset; -1 is skipped).  Tokens of one block stand
  * next to each other in ascending order, as kv_paged_build and kv_paged_slots list
- * them, and no other token of the call goes to that block.
- * A run of tokens that starts a block sets its scale: the smallest power of two s with
+ * them, with nothing but skipped tokens between, and no other token of the call goes to that
+ * block.  Tokens of consecutive slots that stand side by side are a run; a block's runs are written one after
+ * the other.  A run that starts a block sets its scale: the smallest power of two s with
  * largest magnitude <= QMAX * s (QMAX 127 or 448).  A run that continues a block keeps
  * the larger of that and the block's scale, and where it grows the codes before the run are
  * rounded again to it.  Codes are rounded to nearest, ties to even.

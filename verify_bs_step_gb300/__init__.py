@@ -608,8 +608,8 @@ class PagedKV8(PagedKV):
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
         """Write k, v [N, H, D] (bfloat16 or float32, unit stride along D) at slots (int64 [N], -1: skipped).
 
-        Tokens of one block stand next to each other in ascending order, as build() and slot_map() list
-        them; a run that starts a block sets its scales, one that continues it can only raise them."""
+        Tokens of one block stand next to each other in ascending order (skipped ones may part them), as build()
+        and slot_map() list them; a run that starts a block sets its scales, one that continues it can only raise them."""
         N = slots.numel()
         shape, ks, vs = (N, self.H, self.D), k.stride(), v.stride()
         if k.shape != shape or v.shape != shape or ks[2] != 1 or vs[2] != 1:

@@ -8,7 +8,8 @@
 // it by an exact power of two and one more rounding, each at least twice as coarse as the one
 // before, so all of them together stay below one step of the final scale.
 //
-// A warp owns one run of consecutive tokens in one page, for one head of K or of V.  Where the rows can be
+// A warp owns one page's tokens in the call, for one head of K or of V: a run of consecutive slots, and what follows it
+// past skipped tokens (rare, element by element).  Where the rows can be
 // loaded 16 bytes at a time it holds up to 16 tokens x 128 dims in registers between the maximum and the
 // rounding (longer runs are read again, from L2), with all loads in flight at once.  What bounds it is the
 // stream of the rows in and the codes out: 64 prompts of 1000 tokens, 8 heads x 128 dims, bf16 to int8, take 77 us
@@ -114,47 +115,123 @@ __device__ __noinline__ void append_elements(const Kv8Geom& g, const void* base,
   if (lane == 0) g.scales[run] = pow2i(e);
 }
 
-// A CTA looks at 32 tokens; its warps (and those of the CTAs beside it along y) share out the runs that begin there,
-// each for every head of K and V.
+// Whether a slot is one of this cache's (others are skipped).
+__device__ __forceinline__ bool held(const Kv8Geom& g, int64_t s) { return s >= 0 && s < g.NB * g.block; }
+// Whether `s` goes on in the page of slot `from`, past it.
+__device__ __forceinline__ bool goes_on(const Kv8Geom& g, int64_t s, int64_t from, int64_t page) {
+  return s > from && s < (page + 1) * g.block;
+}
+
+// What follows the run at token t in its page past skipped tokens: runs one after the other, each as if it were a call of
+// its own.  kvh: the head of K (0..H-1) or V (H..2H-1).
+template <int FMT, typename T>
+__device__ __noinline__ void append_rest(const Kv8Geom& g, const Kv8Src& src, int kvh, int64_t t, int64_t n,
+                                         const int64_t* slots, int lane) {
+  const int kv = kvh >= g.H ? 1 : 0, h = kvh - kv * g.H;
+  const void* base = kv ? src.v : src.k;
+  const int64_t tok = kv ? src.v_tok : src.k_tok, head = h * (kv ? src.v_head : src.k_head);
+  const int64_t page = slots[t] / g.block, run = g.run(page, kv, h);
+  int64_t from = -1;                                // the last slot written; -1: the run at t is still to come
+  while (t < n) {
+    const int64_t s = t + lane < n ? slots[t + lane] : -1;
+    const u32 m = __ballot_sync(FULL, held(g, s));
+    if (m == 0) {
+      t += 32;
+      continue;
+    }
+    const int f = __ffs(m) - 1;
+    const int64_t s0 = shfl64(static_cast<u64>(s), f);
+    if (!goes_on(g, s0, from, page)) return;
+    t += f;
+    const int off = static_cast<int>(s0 - page * g.block);
+    int len = 1;
+    while (off + len < g.block) {
+      const int64_t k = t + len + lane;
+      const u32 more = __ballot_sync(FULL, k < n && off + len + lane < g.block && slots[k] == s0 + len + lane);
+      const int got = more == FULL ? 32 : __ffs(~more) - 1;
+      len += got;
+      if (got < 32) break;
+    }
+    __syncwarp();                                   // the run before: its codes and scale, written by other lanes
+    if (from >= 0) append_elements<FMT, T>(g, base, tok, t * tok + head, run, off, len, lane);
+    t += len;
+    from = s0 + len - 1;
+  }
+}
+
+// A CTA looks at 32 tokens; its warps (and those of the CTAs beside it along y) share out the pages whose tokens begin
+// there, each for every head of K and V: a run of consecutive slots first, then what skipped tokens part from it.
 template <int FMT, typename T, bool VEC>
-__global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, const Kv8Src src, int64_t n,
-                                                            const int64_t* __restrict__ slots) {
+__global__ void __launch_bounds__(KV8_NT, Elem<T>::BYTES == 2 ? 3 : 2) kv8_append_kernel(
+    const __grid_constant__ Kv8Geom g, const __grid_constant__ Kv8Src src, int64_t n,
+    const int64_t* __restrict__ slots) {
   constexpr int EPC = 16 / Elem<T>::BYTES;          // elements in 16 bytes
   constexpr int NR = 16 * 128 / EPC / 32;           // 16-byte pieces a lane holds: 16 tokens x 128 dims a warp
   const int lane = threadIdx.x & 31;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 32, i = i0 + lane;
   const int64_t s = i < n ? slots[i] : -1;
-  bool valid = s >= 0, cont = false;
+  const int64_t s_back = i0 > 0 ? slots[i - 32] : -1, s_fore = i + 32 < n ? slots[i + 32] : -1;
+  const bool valid = held(g, s);
   int64_t page = 0;
   int off = 0;
-  if (valid && s >= g.NB * g.block) {               // not a slot of this cache: nothing is written
-    set_status(g.status, VBS_EINVAL);
-    valid = false;
-  }
+  if (s >= 0 && !valid) set_status(g.status, VBS_EINVAL);     // not a slot of this cache: nothing is written
   if (valid) {
     page = s / g.block;
     off = static_cast<int>(s - page * g.block);
-    cont = off > 0 && i > 0 && slots[i - 1] == s - 1;
   }
-  const u32 conts = __ballot_sync(FULL, cont);
-  u32 heads = __ballot_sync(FULL, valid && !cont);
-  const int per = 2 * g.H, runs = __popc(heads);
+  const u32 valids = __ballot_sync(FULL, valid);
+  // the slot before, skipped tokens apart: where it lies in the same page, the token belongs to its run or follows it
+  const u32 below = valids & ((1u << lane) - 1u);
+  int64_t prev = static_cast<int64_t>(shfl64(static_cast<u64>(s), below ? 31 - __clz(below) : 0));
+  u32 back = __ballot_sync(FULL, held(g, s_back));
+  const bool beside = lane > 0 ? (below >> (lane - 1)) != 0 : (back >> 31) != 0;    // no skipped one between
+  int64_t last = static_cast<int64_t>(shfl64(static_cast<u64>(s_back), back ? 31 - __clz(back) : 0));
+  if (back == 0 && valids != 0 && __shfl_sync(FULL, off, __ffs(valids) - 1) > 0) {  // further back, for the first one
+    for (int64_t k = i0 - 64; back == 0 && k >= 0; k -= 32) {
+      last = slots[k + lane];
+      back = __ballot_sync(FULL, held(g, last));
+      last = static_cast<int64_t>(shfl64(static_cast<u64>(last), back ? 31 - __clz(back) : 0));
+    }
+  }
+  if (below == 0) prev = back ? last : -1;
+  const bool follows = valid && prev >= page * g.block && goes_on(g, s, prev, page);
+  const bool cont = follows && beside && prev == s - 1;
+  const u32 conts = __ballot_sync(FULL, cont), resumes = __ballot_sync(FULL, follows && !cont);
+  const u32 firsts = __ballot_sync(FULL, valid && !follows);
+  // the last run: how far it goes beyond the 32, and whether its page goes on past skipped tokens
+  int ext = 0;
+  bool far = false;
+  if (valids != 0) {
+    const int l = 31 - __clz(valids);
+    const int64_t s_l = shfl64(static_cast<u64>(s), l), end = (shfl64(static_cast<u64>(page), l) + 1) * g.block;
+    const int room = static_cast<int>(end - 1 - s_l);
+    int64_t v = s_fore;
+    for (int got = l == 31 ? 32 : 0; got == 32 && ext < room;) {
+      if (ext > 0) v = i + 32 + ext < n ? slots[i + 32 + ext] : -1;
+      const u32 on = __ballot_sync(FULL, ext + lane < room && v == s_l + 1 + ext + lane);
+      got = on == FULL ? 32 : __ffs(~on) - 1;
+      ext += got;
+    }
+    for (int64_t k = i0 + 32 + ext; ext < room && k < n; k += 32) {
+      if (k > i0 + 32) v = k + lane < n ? slots[k + lane] : -1;
+      const u32 m = __ballot_sync(FULL, held(g, v));
+      if (m == 0) continue;
+      const int64_t next = shfl64(static_cast<u64>(v), __ffs(m) - 1);
+      far = next > s_l && next < end;
+      break;
+    }
+  }
+  const int per = 2 * g.H, runs = __popc(firsts);
   const int step = gridDim.y * (KV8_NT / 32);
+  u32 heads = firsts;
   int at = 0;                                       // runs taken off `heads` so far
   for (int x = blockIdx.y * (KV8_NT / 32) + (threadIdx.x >> 5); x < runs * per; x += step) {
     for (; at < x / per; ++at) heads &= heads - 1;
     const int p = __ffs(heads) - 1, kvh = x % per, kv = kvh >= g.H ? 1 : 0, h = kvh - kv * g.H;
-    const int64_t pg = shfl64(static_cast<u64>(page), p), s0 = shfl64(static_cast<u64>(s), p);
+    const int64_t pg = shfl64(static_cast<u64>(page), p);
     const int o = __shfl_sync(FULL, off, p);
     int len = __ffs(~(p < 31 ? conts >> (p + 1) : 0u));       // 1 + the tokens that go on
-    while (p + len >= 32 && o + len < g.block) {    // beyond the 32
-      const int64_t k = i0 + p + len + lane;
-      const u32 more = __ballot_sync(FULL, k < n && o + len + lane < g.block && slots[k] == s0 + len + lane);
-      const int m = __ffs(~more) - 1;
-      const int got = m < 0 ? 32 : m;
-      len += got;
-      if (got < 32) break;
-    }
+    if (p + len == 32) len += ext;
     const void* base = kv ? src.v : src.k;
     const int64_t tok = kv ? src.v_tok : src.k_tok;
     const int64_t p0 = (i0 + p) * tok + h * (kv ? src.v_head : src.k_head);
@@ -238,6 +315,15 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8Geom g, con
       codes += NR * 32 * EPC;
     }
     if (lane == 0) g.scales[run] = pow2i(e);
+  }
+  if (resumes == 0 && !far) return;
+  // pages that go on past skipped tokens (rare): by the warp that wrote the run before (in a loop of its own: in the
+  // one above its state cost registers, 76 to 82 us for 64 prompts of 1000 tokens)
+  heads = firsts;
+  at = 0;
+  for (int x = blockIdx.y * (KV8_NT / 32) + (threadIdx.x >> 5); x < runs * per; x += step) {
+    for (; at < x / per; ++at) heads &= heads - 1;
+    append_rest<FMT, T>(g, src, x % per, i0 + __ffs(heads) - 1, n, slots, lane);
   }
 }
 
