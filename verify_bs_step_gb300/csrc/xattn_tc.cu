@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
                            (it.h * a.G + gq) * a.io.q_head;
         q_at[r] = rho < a.M ? at : -1;
       }
+      __syncwarp();                                // each lane reads what the others wrote
       const int qb = done % C::NQ;
       ok = done < C::NQ || tc_wait(&bars.qe[qb], (done / C::NQ - 1) & 1, &gone, a.status);
       ok = __all_sync(FULL, ok);
