@@ -133,9 +133,9 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, u64* b
 // one per S buffer.  Who waits
 // for a tile's phase knows that the ring's turn before it is over, so that a barrier stands in the phase
 // waited for or in the next, and its parity tells them apart.  q, qe, of: an item's Q has landed, is not read
-// any more, its O has been read.
+// any more, its O has been read.  end: every product that was issued is done.
 struct TcBars {
-  u64 q[2], qe[2], of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[3];
+  u64 q[2], qe[2], of, kf[TC_STMAX], vf[TC_STMAX], s[TC_STMAX], pv[TC_STMAX], p[3], end;
 };
 
 // Whether a phase is over, without waiting (try_wait may hold the thread for a while).
@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       mbar_init(&bars.qe[i], 1);
     }
     mbar_init(&bars.of, TC_SM);
+    mbar_init(&bars.end, 1);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
       mbar_init(&bars.vf[i], 1);
@@ -392,10 +393,12 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       }
       __syncwarp();
     }
+    tc_wait_st();                                  // (weights of a tile that was given up)
     tc_fence_before();
   } else if (wid == TC_SW) {
     // ---- loads: Q by the whole warp, K and V by one lane, each as far ahead as its stages go ----
     int T0 = 0, done = 0;                          // tiles before this item; items with tiles so far
+    int kt = 0, vt = 0;                            // tiles of K and of V that lane 0 has loaded
     bool ok = true;
     for (int t = 0;; ++t) {
       const Item it = item_at(t);
@@ -481,20 +484,17 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       mbar_arrive(&bars.q[qb]);
       if (lane == 0) ok = feed(it.n);
       ok = __all_sync(FULL, ok);
-      if (!ok && lane == 0) {                      // given up: the copies on their way land first
-        for (int j = max(0, jk - ST); j < jk; ++j) mbar_wait(&bars.kf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
-        for (int j = max(0, jv - ST); j < jv; ++j) mbar_wait(&bars.vf[(T0 + j) % ST], ((T0 + j) / ST) & 1, 1u << 16);
-      }
+      kt = T0 + jk;
+      vt = T0 + jv;
       T0 += it.n;
       ++done;
       if (!ok) break;
     }
-    // no copy is in flight when the CTA ends: the last ones have landed
-    if (ok && lane == 0)
-      for (int j = max(0, T0 - ST); j < T0; ++j) {
-        mbar_wait(&bars.kf[j % ST], (j / ST) & 1, 1u << 16);
-        mbar_wait(&bars.vf[j % ST], (j / ST) & 1, 1u << 16);
-      }
+    // no copy is in flight when the CTA ends, also where it gave up: the last ones have landed
+    if (lane == 0) {
+      for (int j = max(0, kt - ST); j < kt; ++j) mbar_wait(&bars.kf[j % ST], (j / ST) & 1, 1u << 16);
+      for (int j = max(0, vt - ST); j < vt; ++j) mbar_wait(&bars.vf[j % ST], (j / ST) & 1, 1u << 16);
+    }
   } else {
     // ---- products: one elected thread waits and issues ----
     if (elect_one()) {
@@ -541,8 +541,9 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
         T += it.n;
         ++done;
       }
-      // the products in flight read shared memory and TMEM: the last one is done before either goes
-      if (ok && T > 0) tc_wait(&bars.pv[(T - 1) % ST], ((T - 1) / ST) & 1, &gone, a.status);
+      // the products in flight read shared memory and TMEM: all are done before either goes, also where the CTA gave up
+      tc_commit(&bars.end);
+      mbar_wait(&bars.end, 0, 1u << 16);
     }
     __syncwarp();
   }
