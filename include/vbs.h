@@ -488,7 +488,9 @@ int kv8_read(vbs_kv8* ctx, int layer, int64_t n, const int64_t* slots, void* k_o
  * Prepare the attention of one step: ctx_len[R] (device int32) is the number of cached
  * positions of each row, the step's n_q new tokens among them (1 <= n_q <= max_q).  Reads the
  * block tables: call it again whenever they or the lengths have changed (once a step; the
- * step's layers share it).
+ * step's layers share it).  A plan holds until the next kv_paged_prefill, _build, _prepare, _reorder,
+ * _restore or bs_step_paged, whether or not that call changes an entry (a replayed graph of such calls
+ * is not seen: it has to hold the plan too).
  * Errors: VBS_EINVAL (NULL pointers, n_q out of range), VBS_ECUDA; a length below 0 or beyond
  *   what the row's table covers is held to that range, with VBS_EINVAL in kv_paged_status().
  */
@@ -503,7 +505,7 @@ int kv8_plan(vbs_kv8* ctx, const int32_t* ctx_len, int n_q);
  * share are read once.  Scores, softmax statistics and sums are fp32; q is scaled
  * by a power of two per row and held in fp16, the softmax weights are rounded to fp16.
  * Errors: VBS_EINVAL (layer out of range, NULL pointers, scale not finite), VBS_ESTATE (no
- *   kv8_plan yet), VBS_ECUDA.
+ *   kv8_plan since the tables last changed), VBS_ECUDA.
  */
 int kv8_attention(vbs_kv8* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,
                   void* out, int64_t o_row, int64_t o_tok, int64_t o_head);

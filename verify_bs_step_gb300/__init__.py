@@ -636,7 +636,9 @@ class PagedKV8(PagedKV):
 
     def plan(self, ctx_len: torch.Tensor, n_q: int = 1):
         """Prepare a step's attention: ctx_len (int32 [R] on the device) is each row's number of cached
-        positions, its n_q new tokens among them.  Call it whenever the tables or lengths have changed."""
+        positions, its n_q new tokens among them.  Call it whenever the tables or lengths have changed:
+        after build(), prefill(), prepare(), reorder(), restore() or a beam step, attend() refuses to go on with the
+        plan before."""
         if ctx_len.shape != (self.R,) or not ctx_len.is_contiguous():
             raise ValueError(f"ctx_len must be a contiguous int32 [{self.R}] tensor")
         self._order.run(lib().kv8_plan, "kv8_plan", (ctx_len,), self.ctx8, _cuda(ctx_len, "ctx_len", torch.int32), n_q)

@@ -518,6 +518,7 @@ static int paged_run(vbs_pkv* c, const int32_t* bi, int t_valid) {
   if (c->copy_pending) return VBS_ESTATE;
   const int64_t need = static_cast<int64_t>(t_valid) / c->a.block + 1;
   if (t_valid < 0 || need > c->a.MB) return VBS_EINVAL;
+  c->tables += 1;
   int st = vbs::launch_kv_paged_remap(c->a, bi, t_valid, c->stream);
   if (st != VBS_OK) return st;
   const bool bulk_ok = c->a.slot_bytes % 16 == 0 && aligned16(c->a.pool);
@@ -529,6 +530,7 @@ VBS_EXPORT int kv_paged_prefill(vbs_pkv* c, int P) {
   const vbs::PagedArgs& a = c->a;
   const int nb = (P + a.block - 1) / a.block;
   if (nb > a.S || nb > a.MB) return VBS_EINVAL;
+  c->tables += 1;
   const int64_t R = c->R, NB = static_cast<int64_t>(a.B) * a.S;
   std::vector<int32_t> table(R * a.MB, -1), nblk(R, nb), refcnt(NB, 0), stack(NB), top(a.B, a.S - nb);
   for (int b = 0; b < a.B; ++b) {
@@ -555,6 +557,7 @@ VBS_EXPORT int kv_paged_build(vbs_pkv* c, const int32_t* lens, int64_t cap, int6
   if (cap > 0 && !slots) return VBS_EINVAL;
   const vbs::SlotArgs s{c->a.B, nullptr, lens, cap, slots, pos, row, cu, c->scan};
   c->copy_pending = false;
+  c->tables += 1;
   return vbs::launch_kv_build(c->a, s, true, num_sms(), c->stream);
 }
 
@@ -599,6 +602,7 @@ VBS_EXPORT int bs_step_paged(vbs_bs* c, const void* logits, int64_t ld, float* s
   if (kv->copy_pending) return VBS_ESTATE;
   const int64_t need = static_cast<int64_t>(t_valid) / kv->a.block + 1;
   if (t_valid < 0 || need > kv->a.MB) return VBS_EINVAL;
+  kv->tables += 1;
   if (vbs::bs_can_fuse_remap(a, kv->a)) {
     a.kv_fuse = 1;
     a.kv_t = t_valid;
@@ -648,6 +652,7 @@ VBS_EXPORT int kv_paged_save(vbs_pkv* c) {
 
 VBS_EXPORT int kv_paged_restore(vbs_pkv* c) {
   if (!c) return VBS_EINVAL;
+  c->tables += 1;
   // copies still pending refer to the state being dropped: forget them
   if (cudaMemsetAsync(c->a.tasks, 0, sizeof(int4) * c->R, c->stream) != cudaSuccess) return VBS_ECUDA;
   c->copy_pending = false;

@@ -16,6 +16,7 @@ struct vbs_kv8 {
   vbs::Kv8Geom g;                 // layer is set per call
   int q_heads, max_q;
   int n_q;                        // of the last plan, 0: none yet
+  int64_t planned;                // kv->tables at the last plan
   vbs::Kv8Plan plan;
   float* part;                    // partials of rows split over CTAs, and their arrival counters
   int2* pieces;
@@ -108,13 +109,14 @@ VBS_EXPORT int kv8_plan(vbs_kv8* c, const int32_t* ctx_len, int n_q) {
   if (c->kv->copy_pending) return VBS_ESTATE;
   const int st = vbs::launch_kv8_plan(c->kv->a, ctx_len, c->plan, c->kv->stream);
   c->n_q = st == VBS_OK ? n_q : 0;
+  c->planned = c->kv->tables;
   return st;
 }
 
 VBS_EXPORT int kv8_attention(vbs_kv8* c, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head,
                              float scale, void* out, int64_t o_row, int64_t o_tok, int64_t o_head) {
   if (!c || !q || !out || layer < 0 || layer >= c->g.L || !std::isfinite(scale)) return VBS_EINVAL;
-  if (c->n_q == 0 || c->kv->copy_pending) return VBS_ESTATE;
+  if (c->n_q == 0 || c->planned != c->kv->tables || c->kv->copy_pending) return VBS_ESTATE;
   const vbs::QO io{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), q_row, q_tok, q_head, o_row, o_tok,
                    o_head, c->n_q, c->q_heads, scale};
   vbs::Kv8Geom g = c->g;

@@ -48,4 +48,5 @@ struct vbs_pkv {
   size_t state_bytes;
   bool copy_pending;     // bs_step_paged recorded copies that kv_paged_copy has not run
   int32_t* scan;         // [R + 1] exclusive sums of a slot map's counts
+  int64_t tables;        // how often the tables may have changed: an attention plan holds for the tables it was made from
 };
