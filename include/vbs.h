@@ -499,7 +499,8 @@ int kv8_plan(vbs_kv8* ctx, const int32_t* ctx_len, int n_q);
  * Attention of the planned step over `layer`: for query token i (0..n_q-1) of row r and
  * query head h, which reads K/V head h / (q_heads / H),
  *   out = sum_p softmax_p(scale * q . k_p) v_p  over positions p < ctx_len[r] - n_q + 1 + i
- * (the cached positions up to the token's own).  A token that sees no position gives zeros.
+ * (the cached positions up to the token's own).  A token that sees no position gives zeros; one that
+ * sees positions with no score above minus infinity gives NaN, as the formula does (also below).
  * q and out are bf16 (device); token i of row r, head h is at q + r * q_row + i * q_tok +
  * h * q_head (elements, head_dim contiguous), out likewise.  Blocks that several rows of a sentence
  * share are read once.  Scores, softmax statistics and sums are fp32; q is scaled

@@ -26,6 +26,8 @@
 
 #pragma once
 
+#include <cfloat>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -210,6 +212,9 @@ template <int VCH> __device__ __forceinline__ int out_dim(int n, int j) {
 // The XOR of a position's 16-byte chunks: rows of 8 (or 16) chunks, or two positions to a line of 8.
 __device__ __forceinline__ int k_swz(int tok, int nc) { return (nc & 7) == 0 ? (tok & 1) << 2 : 0; }
 __device__ __forceinline__ int v_swz(int tok, int nc) { return (nc & 3) == 0 ? ((tok >> 1) & 3) << 1 : 0; }
+
+// The factor on a row's sums: 0 without a position seen (no reference); infinite, for NaN, where all it sees score -inf.
+__device__ __forceinline__ float row_norm(float sum, float top) { return top == -INFINITY ? 0.f : 1.f / sum; }
 
 // Four dims of an output row.
 __device__ __forceinline__ void store_out(uint16_t* out, const SplitArgs& sa, const float4& v) {
@@ -677,8 +682,10 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         sum += wl[w][tid] * x;                              // (a NaN stays one)
         wm[w][tid] = x;
       }
+      // a row that sees positions, all of which score -inf, is told from one that sees none (softmax is 0 / 0 there)
+      if (top == -INFINITY && row_lim[tid] > 0) top = -FLT_MAX;
       if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = row_norm(sum, top);
 #pragma unroll
         for (int w = 0; w < NW; ++w) wm[w][tid] *= inv;
       } else {
@@ -799,7 +806,7 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
     } else {
       gather(r, 0, 1, top, sum, a);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = row_norm(sum, top);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int d = lane * 4 + v * 128;
@@ -826,7 +833,7 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
       f[w] = sm[w] == -INFINITY ? 0.f : ex2(sm[w] - all);
       total += sl[w] * f[w];
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const float inv = row_norm(total, all);
     for (int d = threadIdx.x * 4; d < sa.D; d += 32 * JN_WARPS * 4) {
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       const int gq = rho % a.G, i = rho / a.G % a.io.n_q, w = rho / a.G / a.io.n_q;
       uint16_t* out = a.io.o + static_cast<int64_t>(it.b * a.W + w) * a.io.o_row + i * a.io.o_tok +
                       (it.h * a.G + gq) * a.io.o_head;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = 1.f / l;                   // (0 / 0 where every score is -inf: NaN)
       u32 x[DP / 2];
 #pragma unroll
       for (int c = 0; c < DP; c += 16) {
