@@ -547,6 +547,9 @@ int xattn_run(vbs_xattn* ctx, const void* q, int64_t q_row, int64_t q_tok, int64
               int64_t k_sent, int64_t k_pos, int64_t k_head, const void* v, int64_t v_sent, int64_t v_pos,
               int64_t v_head, int len, const int32_t* enc_len, float scale, void* out, int64_t o_row, int64_t o_tok,
               int64_t o_head);
+/* The kernel that the context's last xattn_run took: *tiles 1 for the tcgen05 tiles, 0 for the split kernel,
+   -1 before the first run.  Errors: VBS_EINVAL (NULL arguments). */
+int xattn_kernel(vbs_xattn* ctx, int* tiles);
 /* Synchronise the stream and return (then clear) the device status word.  VBS_EINVAL for NULL,
    VBS_ECUDA when the synchronisation or the read fails. */
 int xattn_status(vbs_xattn* ctx);

@@ -61,6 +61,7 @@ SIGNATURES = {
     "xattn_init": (_c_int, [_pp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "xattn_run": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _c_i64,
                            _c_i64, _c_int, _vp, _c_f, _vp, _c_i64, _c_i64, _c_i64]),
+    "xattn_kernel": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
     "xattn_status": (_c_int, [_vp]),
     "xattn_destroy": (_c_int, [_vp]),
     "kv_paged_state": (_c_int, [_vp, _pp, _pp, _pp, _pp, _pp]),
@@ -714,6 +715,13 @@ class CrossAttention:
                         n_q, k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2], S, lp,
                         self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
         return out
+
+    @property
+    def tiles(self):
+        """Whether the last attend() took the tcgen05 tiles (many rows) or, False, the split kernel; None before it."""
+        n = _c_int()
+        _check(lib().xattn_kernel(self.ctx, ctypes.byref(n)), "xattn_kernel")
+        return None if n.value < 0 else bool(n.value)
 
     def status(self) -> int:
         """Synchronise and return the device status word (0 = OK)."""

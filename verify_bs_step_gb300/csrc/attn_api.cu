@@ -27,6 +27,7 @@ struct vbs_xattn {
   vbs::EncKV e;                   // the tensors are set per call
   cudaStream_t stream;
   int q_heads, max_q, max_len;
+  int tiles;                      // the kernel of the last run: 1 the tiles, 0 the split kernel, -1: no run yet
   float* part;
   int2* pieces;
   void* dev_block;
@@ -151,6 +152,7 @@ VBS_EXPORT int xattn_init(vbs_xattn** out, int batch, int W, int q_heads, int kv
   c->q_heads = q_heads;
   c->max_q = max_q;
   c->max_len = max_len;
+  c->tiles = -1;
   vbs::EncKV& e = c->e;
   e.B = batch;
   e.W = W;
@@ -199,7 +201,13 @@ VBS_EXPORT int xattn_run(vbs_xattn* c, const void* q, int64_t q_row, int64_t q_t
   e.v_head = v_head;
   e.len = enc_len;
   e.S = len;
-  return vbs::launch_xattn(e, io, c->part, c->pieces, num_sms(), c->stream);
+  return vbs::launch_xattn(e, io, c->part, c->pieces, num_sms(), c->stream, &c->tiles);
+}
+
+VBS_EXPORT int xattn_kernel(vbs_xattn* c, int* tiles) {
+  if (!c || !tiles) return VBS_EINVAL;
+  *tiles = c->tiles;
+  return VBS_OK;
 }
 
 VBS_EXPORT int xattn_status(vbs_xattn* c) {

@@ -5,8 +5,9 @@
 
 namespace vbs {
 
-int launch_xattn(const EncKV& e, const QO& io, float* part, int2* pieces, int num_sms, cudaStream_t s) {
-  if (xattn_tc_takes(e, io, num_sms)) return launch_xattn_tc(e, io, num_sms, s);
+int launch_xattn(const EncKV& e, const QO& io, float* part, int2* pieces, int num_sms, cudaStream_t s, int* tiles) {
+  *tiles = xattn_tc_takes(e, io, num_sms) ? 1 : 0;
+  if (*tiles) return launch_xattn_tc(e, io, num_sms, s);
   const EncSrc src{e};
   const SplitArgs sa = split_args(io, e.B, e.W, e.H, e.D, part, pieces);
   const bool aligned = ((reinterpret_cast<uintptr_t>(e.k) | reinterpret_cast<uintptr_t>(e.v)) & 15) == 0 &&
