@@ -205,3 +205,22 @@ def test_joins_of_several_hundred_pieces_of_a_cache(fmt):
     bound = BF16 * want.abs() + (2 * FP16 + 2.0 ** -17 * (D + 8) / 32 + 1000 * 2.0 ** -24) * size + n * FP16_FLOOR * vv.abs().max()
     assert ((a[0, 0].double() - want).abs() <= bound).all()
     kv.close()
+
+
+def test_an_encoder_as_long_as_32_bits_count():
+    """2^31 - 1 positions of equal weight: the last ones are seen."""
+    import verify_bs_step_gb300 as vbs
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    S, D = (1 << 31) - 1, 8
+    kv = torch.zeros(1, S, 1, D, device="cuda", dtype=torch.bfloat16)
+    kv[0, -16:] = 2.0 ** 30
+    q = torch.zeros(1, 1, 1, D, device="cuda", dtype=torch.bfloat16)
+    x = vbs.CrossAttention(1, 1, 1, D, max_len=S)
+    for n, want in ((S, 8.0), (S - 4, 6.0), (S - 14, 1.0)):
+        out = x.attend(q, kv, kv, i32([n]))
+        assert (out == want).all(), (n, out)
+    assert x.status() == 0
+    x.close()
+    del kv
+    torch.cuda.empty_cache()

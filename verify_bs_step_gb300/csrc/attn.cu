@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(PLAN_NT) kv8_plan_kernel(const PagedArgs a, co
   __syncthreads();
   int most = 0;
   for (int w = 0; w < W; ++w) most = max(most, seen[w]);
-  const int cols = (most + a.block - 1) / a.block;
+  const int cols = static_cast<int>((static_cast<u32>(most) + a.block - 1) / a.block);
   const int32_t* tab = a.table + static_cast<int64_t>(b) * W * a.MB;
   int4* list = p.list + static_cast<int64_t>(b) * a.S;
   int carry = 0;
@@ -106,7 +106,7 @@ kv8_plan_rows_kernel(const PagedArgs a, const int32_t* ctx, const Kv8Plan p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int seen = held_len(a, ctx, b);
-  const int cols = (seen + a.block - 1) / a.block;
+  const int cols = static_cast<int>((static_cast<u32>(seen) + a.block - 1) / a.block);
   int4* list = p.list + static_cast<int64_t>(b) * a.S;
   for (int j = blockIdx.y * PLAN_NT + threadIdx.x; j < min(cols, a.S); j += gridDim.y * PLAN_NT) {
     const int id = a.table[static_cast<int64_t>(b) * a.MB + j];

@@ -164,7 +164,7 @@ struct EncSrc {
     set_status(e.status, VBS_EINVAL);
     return n < 0 ? 0 : e.S;
   }
-  __device__ int units(int b) const { return max(1, (len(b) + 15) >> 4); }
+  __device__ int units(int b) const { return max(1, static_cast<int>((static_cast<u32>(len(b)) + 15) >> 4)); }
   __device__ int limit(int b, int, int, int, int) const { return len(b); }
   // (a lane without a unit stands past every end: no positions)
   __device__ void fetch(Batch& t, int, int, int u, bool valid) const { t.u = valid ? u : 1 << 26; }

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(TAB_NT) kv_build_kernel(const PagedArgs a, con
   const int row = build || s.n == a.B ? i * a.W : i;
   const int32_t* tab = a.table + static_cast<int64_t>(row) * a.MB;
   if (build) {
-    const int nb = (count + a.block - 1) / a.block;
+    const int nb = static_cast<int>((static_cast<u32>(count) + a.block - 1) / a.block);
     for (int w = 0; w < a.W; ++w)
       for (int64_t c = t0; c < a.MB; c += step)
         a.table[(static_cast<int64_t>(row) + w) * a.MB + c] = c < nb ? i * a.S + static_cast<int>(c) : -1;

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(TC_NT, 2) xattn_tc_kernel(const __grid_constan
       set_status(a.status, VBS_EINVAL);
       it.len = it.len < 0 ? 0 : a.S;
     }
-    it.n = (it.len + TC_N - 1) / TC_N;
+    it.n = static_cast<int>((static_cast<u32>(it.len) + TC_N - 1) / TC_N);
     return it;
   };
 
@@ -604,10 +604,10 @@ bool xattn_tc_takes(const EncKV& e, const QO& io, int num_sms) {
   //   512 segments x 32                     11.4 / 9.1, 14.4 / 11.0
   const bool wide = e.D > 64;
   const double heads = static_cast<double>(e.B) * e.H, tiles = heads * ((M + TC_M - 1) / TC_M);
-  const double tc = (wide ? 8.0 : 6.0) + (e.S + TC_N - 1) / TC_N * 0.56 * std::max(1.0, tiles / (2 * num_sms));
+  const double tc = (wide ? 8.0 : 6.0) + ((e.S - 1) / TC_N + 1) * 0.56 * std::max(1.0, tiles / (2 * num_sms));
   const double alone = wide ? std::min(24.0, std::max(12.0, 6.0 + e.S / 70.0))
                             : std::min(18.0, std::max(9.3, 5.0 + e.S / 100.0));
-  const double split = alone + heads * ((M + 31) / 32) * ((e.S + 15) / 16) * (wide ? 0.0015 : 0.00085);
+  const double split = alone + heads * ((M + 31) / 32) * ((e.S - 1) / 16 + 1) * (wide ? 0.0015 : 0.00085);
   if (e.S <= 16 * SP_WHOLE) {
     const double segments = heads * ((M + 31) / 32);
     if (segments <= 2 * num_sms && e.S <= (wide ? 256 : 384) / (segments > num_sms ? 2 : 1)) return false;
