@@ -18,7 +18,7 @@ struct vbs_kv8 {
   int n_q;                        // of the last plan, 0: none yet
   int64_t planned;                // kv->tables at the last plan
   vbs::Kv8Plan plan;
-  float* part;                    // partials of rows split over CTAs, and their arrival counters
+  float* part;                    // partials of segments in pieces (pieces: where each one's are)
   int2* pieces;
   void* dev_block;
 };

@@ -17,10 +17,11 @@
 //   values   O += P V by mma.m16n8k16: a lane takes 16 bytes of four positions, pairs of positions are put
 //            side by side with byte permutes, and the order of the output dims is undone at the end.
 // What bounds it is the K/V stream for one long row (250001 positions, 8 heads x 128 e4m3: 95 us with the plan and
-// the join, 5.4 TB/s, 81 % of the measured copy), the segments' fixed cost (some 5 us of lookups, Q and sums
-// each) for many short ones (64 sentences x 4 beams x 1064: 46 us, 3.4 TB/s), and issue slots where 32 rows share a
-// K/V head (64 x 8 tokens x 4 heads over 1..4000 positions, int8: 97 us, 2.8 TB/s: 750 instructions a unit and
-// warp, a quarter of them conversions, at 8 warps an SM).
+// the join, 5.4 TB/s, 80 % of the measured copy), the segments' fixed cost (some 5 us of lookups, Q and sums
+// each) for many short ones (64 sentences x 4 beams x 1064: 46 us, 39 of them this kernel at 4.1 TB/s), and latency at
+// few warps where 32 rows share a K/V head (64 x 8 tokens x 4 heads over 1..4000 positions, int8: 97 us, 2.8 TB/s: 254
+// registers leave two warps a scheduler; issue slots 43 % active, the tensor pipe 33 %, the first stall the fixed
+// latency of an instruction).
 // Measured and not kept: two units an iteration (fewer instructions, 8 warps instead of 12: 102 and 65 us), CTAs
 // of one warp (91 us at 64 x 4 beams: four times the partials), a join in the CTA that arrives last (57).
 

@@ -12,8 +12,8 @@
 // past skipped tokens (rare, element by element).  Where the rows can be
 // loaded 16 bytes at a time it holds up to 16 tokens x 128 dims in registers between the maximum and the
 // rounding (longer runs are read again, from L2), with all loads in flight at once.  What bounds it is the
-// stream of the rows in and the codes out: 64 prompts of 1000 tokens, 8 heads x 128 dims, bf16 to int8, take 77 us
-// (262 MB read, 131 written: 5.1 TB/s, 75 % of the measured copy; 4 CTAs an SM instead of 3 took 83); a single
+// stream of the rows in and the codes out: 64 prompts of 1000 tokens, 8 heads x 128 dims, bf16 to int8, take 76 us
+// (262 MB read, 131 written: 5.2 TB/s, 77 % of the measured copy; 4 CTAs an SM instead of 3 took 83); a single
 // token's step is latency: slot, scale, row (256 rows x 8 heads: 10 us).
 
 #include "codes.cuh"

@@ -16,9 +16,9 @@
 // What bounds it: the chain of one tile in one CTA (wait for S, 64 scores a thread to registers, maximum,
 // exponentials, weights back, signal: some 1340 clocks of a 128 x 64 tile), not a pipe: at head_dim 64 the products
 // take 256 of the 740 clocks that a tile costs an SM, the exponentials 256.  Two CTAs an SM, 256 TMEM columns each,
-// fill each other's waits; TMEM has no room for a third.  Persistent CTAs take the items longest sentence first.
-// 16 x 16 heads x 64, 1024 rows over 1000..2048 positions: 144 us (710 TFLOP/s, 36 % of the measured
-// peak); 4 x 8 heads x 128, 500 rows x 4 heads a group over 500..4000: 76 us (970 TFLOP/s, 50 %).
+// fill each other's waits; TMEM has no room for a third.  Persistent CTAs take the items longest sentence first
+// where that pays.  16 x 16 heads x 64, 1024 rows over 1000..2048 positions: 145 us (706 TFLOP/s, 37 % of the measured
+// peak); 4 x 8 heads x 128, 500 rows x 4 heads a group over 500..4000: 78 us (945 TFLOP/s, 50 %).
 // Measured and not kept: two threads a row (159 us, its vote a tile), a lane that waits for its warp (173), K and V
 // loads that block in turn (162), one CTA an SM (230).
 
