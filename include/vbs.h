@@ -1,8 +1,9 @@
 /*
  * libvbs: one step of batched beam search over a vocabulary, the KV-cache
  * reorder that follows it, the verify/accept step of blockwise parallel
- * decoding, and the attention of a decode step (an 8-bit paged cache and an
- * encoder's states), as a C ABI for one NVIDIA GB300 (sm_103a).
+ * decoding, and the attention of prompts and decode steps (a paged cache in 8 or
+ * 16 bits, an encoder's states, rotary positions), as a C ABI for one NVIDIA GB300
+ * (sm_103a).
  *
  * Sources of the operations (cited by page title and section):
  *   [BS] "Transformers中的Beam Search高效实现" (zhuanzhi.ai), section
@@ -515,6 +516,133 @@ int kv8_attention(vbs_kv8* ctx, int layer, const void* q, int64_t q_row, int64_t
 /* Free the context (synchronises the stream first; pkv and the scales stay).  NULL is a no-op.
    Returns VBS_OK. */
 int kv8_destroy(vbs_kv8* ctx);
+
+/* =============================================================================
+ * Rotary positions, the paged cache in 16 bits and the attention that reads it.  The pages name the K/V cache and its
+ * paging; these operators have no pages' counterpart.
+ * ============================================================================= */
+
+/* which dims make a pair: (i, i + rot / 2), or (2 i, 2 i + 1) */
+enum { VBS_ROPE_HALF = 0, VBS_ROPE_INTERLEAVED = 1 };
+/* how the frequencies are scaled for contexts longer than the original (rope_frequencies) */
+enum { VBS_ROPE_NONE = 0, VBS_ROPE_LINEAR = 1, VBS_ROPE_BASE = 2, VBS_ROPE_PARTS = 3 };
+/* the most query or K/V heads of the calls of this and the next section */
+enum { VBS_MAX_HEADS = 65536 };
+
+typedef struct vbs_rope vbs_rope;
+
+/*
+ * freq[i] = base^(-2 i / rot) (host, rot / 2 entries, radians a position), scaled:
+ *   VBS_ROPE_LINEAR  freq / factor
+ *   VBS_ROPE_BASE    base * factor^(rot / (rot - 2)) in place of base
+ *   VBS_ROPE_PARTS   by the turns r = original * freq / (2 pi) that a pair makes over the original length: freq where
+ *                    r >= high, freq / factor where r <= low, between them the mean of both weighted by
+ *                    (r - low) / (high - low)
+ * Errors: VBS_EINVAL (NULL, rot odd or outside 0..256, base or a parameter of the scaling out of range).
+ */
+int rope_frequencies(int rot, double base, int scaling, double factor, double original, double low, double high,
+                     double* freq);
+/*
+ * Rotary positions for heads of head_dim (1..256) dims, the first `rot` of which (even, 0..head_dim) are rotated:
+ * at position p the pair (a, b) of frequency f becomes amplitude * (a cos pf - b sin pf, b cos pf + a sin pf); dims from
+ * rot on stay as they are.  freq: rot / 2 radians a position (host).  Angles are exact to 2^-28 of a turn at every
+ * position; products and sums are fp32, rounded once to the output's type.  The context holds a table of
+ * the frequencies on the current device (synchronises once) and may be used on any stream of it.
+ * Errors: VBS_EINVAL (sizes, layout, NULL, a number not finite), VBS_ENOMEM, VBS_ECUDA.  *ctx is NULL on error.
+ */
+int rope_init(vbs_rope** ctx, int head_dim, int rot, int layout, const double* freq, double amplitude);
+/*
+ * Rotate n tokens' queries (q_heads heads) and keys (k_heads; either may be 0): token i's head h is at q + i * q_tok +
+ * h * q_head (elements of dtype VBS_BF16 or VBS_F32, head_dim contiguous), its result at q_out + i * qo_tok + h * qo_head
+ * of the same type, k likewise; pos[i] (device int32) its position.  Outputs are their inputs' memory (with the same
+ * strides) or apart from all inputs.  A token with a negative position is skipped: its outputs are left as they are.
+ * Errors: VBS_EINVAL (n outside 0..2^31 - 1, dtype or heads out of range, NULL pointers with n > 0), VBS_ECUDA.
+ */
+int rope_apply(const vbs_rope* ctx, int64_t n, const int32_t* pos, int dtype, const void* q, int64_t q_tok, int64_t q_head,
+               void* q_out, int64_t qo_tok, int64_t qo_head, int q_heads, const void* k, int64_t k_tok, int64_t k_head,
+               void* k_out, int64_t ko_tok, int64_t ko_head, int k_heads, vbs_stream_t stream);
+/* Free the context (work that uses it must have completed).  NULL is a no-op.  Returns VBS_OK. */
+int rope_destroy(vbs_rope* ctx);
+
+typedef struct vbs_kv16 vbs_kv16;
+
+/*
+ * Attention over the cache `pkv` (created with elem_bytes = 2) held in bf16, and the write into it.
+ *   q_heads  query heads of the attention (a multiple of H); max_q  the most query tokens per row of one
+ *            attention call (1..32)
+ * All work goes to pkv's stream; device-side errors go to kv_paged_status(pkv).  The calls below return VBS_ESTATE while
+ * copies recorded by bs_step_paged are pending.  The context must be destroyed before pkv.
+ * Errors: VBS_EINVAL (elem_bytes not 2, head_dim not a multiple of 8 up to 256, NULL pointers, q_heads or max_q out of
+ *   range), VBS_EALIGN (pool not 16-byte aligned), VBS_ENOMEM, VBS_ECUDA.  *ctx is NULL on error.
+ */
+int kv16_init(vbs_kv16** ctx, vbs_pkv* pkv, int q_heads, int max_q);
+/*
+ * Write n tokens' K and V rows into `layer`: token i's head h is at k + i * k_tok + h * k_head (elements of dtype
+ * VBS_BF16 or VBS_F32, head_dim contiguous; v likewise) and goes, rounded to bf16, to slot slots[i] (int64 device,
+ * block * block_size + offset; -1 is not written).  No slot is named twice in a call.
+ * With `rope` (of the pool's device; its head_dim the cache's): K is rotated to pos[i] (device int32) before it is
+ * written, and also stored to k_out where that is not NULL; with q, the tokens' q_heads queries are rotated into q_out.
+ * k_out and q_out are of dtype, laid out like k and q with strides of their own; each is its input's memory (with the
+ * same strides) or apart from all inputs.  A token with a negative position is skipped altogether.  Without rope, pos,
+ * k_out, q and q_out are NULL.
+ * Errors: VBS_EINVAL (layer, n or dtype out of range, NULL pointers with n > 0, q without q_out or the reverse, a rope
+ *   of another head_dim), VBS_ECUDA; a slot outside the pool is not written, with VBS_EINVAL in kv_paged_status().
+ */
+int kv16_append(vbs_kv16* ctx, int layer, int64_t n, const int64_t* slots, int dtype, const void* k, int64_t k_tok,
+                int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const vbs_rope* rope, const int32_t* pos,
+                void* k_out, int64_t ko_tok, int64_t ko_head, const void* q, int64_t q_tok, int64_t q_head, void* q_out,
+                int64_t qo_tok, int64_t qo_head);
+/* kv8_plan for this cache: the same arguments, results and errors; kv16_attention keeps to it as kv8_attention does. */
+int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
+/*
+ * Attention of the planned step over `layer`: as kv8_attention, over bf16 keys and values.  What a token does not see
+ * may hold anything.  Scores, softmax statistics and sums are fp32; the softmax weights are held to 16 bits (two bf16
+ * parts).
+ * Errors: those of kv8_attention.
+ */
+int kv16_attention(vbs_kv16* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,
+                   void* out, int64_t o_row, int64_t o_tok, int64_t o_head);
+/* Free the context (synchronises the stream first; pkv stays).  NULL is a no-op.  Returns VBS_OK. */
+int kv16_destroy(vbs_kv16* ctx);
+
+/* =============================================================================
+ * Attention of whole prompts to themselves.  The operator has no pages' counterpart.
+ * ============================================================================= */
+
+typedef struct vbs_pattn vbs_pattn;
+
+/*
+ * Create a context for q_heads query and kv_heads K/V heads of head_dim (a multiple of 8 up to 256).  All work goes to
+ * `stream`.
+ * Errors: VBS_EINVAL (a size out of range, q_heads not a multiple of kv_heads), VBS_ENOMEM, VBS_ECUDA.  *ctx is NULL on
+ *   error.
+ */
+int pattn_init(vbs_pattn** ctx, int q_heads, int kv_heads, int head_dim, vbs_stream_t stream);
+/*
+ * `batch` requests packed one after the other in n tokens: request b has the tokens cu[b] .. cu[b + 1] - 1 (device
+ * int32 [batch + 1], not falling, within 0..n; kv_paged_build's cu).  For each of them and each query head h, which reads
+ * K/V head h / (q_heads / kv_heads),
+ *   out = sum_j softmax_j(scale * q . k_j) v_j   over the request's tokens up to its own (causal), or over all of them.
+ * All bf16 (device), head_dim contiguous: token t's head h of q is at q + t * q_tok + h * q_head (elements), k, v and out
+ * likewise.  Tokens of no request are neither used nor written.  What a token does not see may hold anything.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to bf16 before the product with V (in
+ * the kernel for head_dim above 128, more than 128 heads a group, or q, k, v not aligned to 16 bytes they are not:
+ * pattn_kernel tells; it is many times slower).
+ * An infinite or NaN element of V counts for every token that sees it, as in the formula.
+ * Errors: VBS_EINVAL (n or batch outside 0..2^30, NULL pointers, scale not finite), VBS_ECUDA; a request that is not
+ *   within the tokens counts as none, with VBS_EINVAL in pattn_status().
+ */
+int pattn_run(vbs_pattn* ctx, int64_t n, int batch, const int32_t* cu, const void* q, int64_t q_tok, int64_t q_head,
+              const void* k, int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int causal,
+              float scale, void* out, int64_t o_tok, int64_t o_head);
+/* The kernel that the context's last pattn_run took: *tiles 1 for the tcgen05 tiles, 0 for the other, -1 before the
+   first run.  Errors: VBS_EINVAL (NULL arguments). */
+int pattn_kernel(vbs_pattn* ctx, int* tiles);
+/* Synchronise the stream and return (then clear) the device status word.  VBS_EINVAL for NULL,
+   VBS_ECUDA when the synchronisation or the read fails. */
+int pattn_status(vbs_pattn* ctx);
+/* Free the context (synchronises its stream first).  NULL is a no-op.  Returns VBS_OK. */
+int pattn_destroy(vbs_pattn* ctx);
 
 /* =============================================================================
  * Cross attention to an encoder's states.  The pages name encoder-decoder translation as a

@@ -1,4 +1,5 @@
-"""Block tables, the 8-bit paged cache, and attention over it and over an encoder's states.
+"""Block tables, the paged cache in 8 and 16 bits, attention over it, over an encoder's states and of prompts, rotary
+positions.
 
 TEST INFRASTRUCTURE.  Plain loops in fp64 (numpy); shares no code with the CUDA library.
 
@@ -10,6 +11,8 @@ What each function states:
   holds the page's largest magnitude, and codes rounded to nearest, ties to even.
 * ``append``: tokens written into pages in order; a page continued past its first slot never
   lowers its scale, and when the scale grows the codes already there are rounded again.
+* ``rotate``: a pair (a, b) of dims at position p becomes amp (a cos pf - b sin pf, b cos pf + a sin pf).
+* ``frequencies``: radians a position of each pair, scaled for long contexts.
 * ``attention``: softmax(scale q k^T) v over the positions a query sees; zeros where it sees none.
 """
 
@@ -113,4 +116,36 @@ def attention(q, k, v, seen, scale: float):
         s = (k[:t] @ q[i]) * scale
         p = np.exp(s - s.max())
         out[i] = (p[:, None] * v[:t]).sum(0) / p.sum()
+    return out
+
+
+def frequencies(rot: int, base: float, scaling=None, factor=1.0, original=8192.0, low=1.0, high=4.0):
+    out = []
+    for i in range(rot // 2):
+        b = base * factor ** (rot / (rot - 2)) if scaling == "base" else base
+        f = b ** (-2.0 * i / rot)
+        if scaling == "linear":
+            f = f / factor
+        if scaling == "parts":
+            turns = original * f / (2 * math.pi)
+            if turns <= low:
+                f = f / factor
+            elif turns < high:
+                x = (turns - low) / (high - low)
+                f = x * f + (1 - x) * f / factor
+        out.append(f)
+    return out
+
+
+def rotate(x, pos, freq, layout: str, amp: float = 1.0):
+    """x [n, heads, D] at positions pos [n] -> the same in fp64."""
+    x = np.asarray(x, dtype=np.float64)
+    out = x.copy()
+    half = len(freq)
+    for i, f in enumerate(freq):
+        a, b = (i, i + half) if layout == "half" else (2 * i, 2 * i + 1)
+        t = np.asarray(pos, dtype=np.float64) * f
+        c, s = amp * np.cos(t)[:, None], amp * np.sin(t)[:, None]
+        out[..., a] = x[..., a] * c - x[..., b] * s
+        out[..., b] = x[..., b] * c + x[..., a] * s
     return out

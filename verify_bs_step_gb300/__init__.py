@@ -13,12 +13,14 @@ import os
 
 import torch
 
-__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "CrossAttention", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
+__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "PagedKV16", "CrossAttention", "PromptAttention", "Rotary", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
            "LP_GNMT", "LP_POWER", "ES_FALSE", "ES_TRUE", "ES_NEVER", "F32", "BF16", "BPD_EXACT", "BPD_TOPK",
            "BPD_DISTANCE", "gather_shard_partials"]
 
 F32, BF16 = 0, 1
 I8, E4M3 = 0, 1
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
 LP_GNMT, LP_POWER = 0, 1
 BPD_EXACT, BPD_TOPK, BPD_DISTANCE = 0, 1, 2
 ES_FALSE, ES_TRUE, ES_NEVER = 0, 1, 2
@@ -27,7 +29,7 @@ OK, EINVAL, ECUDA, ENOMEM, ESTATE, EALIGN, ETIMEOUT, EINPUT, ESCRATCH, EBOUNDS =
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvbs.so")
 CHECKED_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvbs_checked.so")
 
-_c_int, _c_i64, _c_f, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+_c_int, _c_i64, _c_f, _c_d, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_void_p
 _pp = ctypes.POINTER(ctypes.c_void_p)
 
 # name -> (restype, argtypes); mirrors include/vbs.h
@@ -64,6 +66,23 @@ SIGNATURES = {
     "xattn_kernel": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
     "xattn_status": (_c_int, [_vp]),
     "xattn_destroy": (_c_int, [_vp]),
+    "rope_frequencies": (_c_int, [_c_int, _c_d, _c_int, _c_d, _c_d, _c_d, _c_d, ctypes.POINTER(_c_d)]),
+    "rope_init": (_c_int, [_pp, _c_int, _c_int, _c_int, ctypes.POINTER(_c_d), _c_d]),
+    "rope_apply": (_c_int, [_vp, _c_i64, _vp, _c_int, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_i64,
+                            _vp, _c_i64, _c_i64, _c_int, _vp]),
+    "rope_destroy": (_c_int, [_vp]),
+    "kv16_init": (_c_int, [_pp, _vp, _c_int, _c_int]),
+    "kv16_append": (_c_int, [_vp, _c_int, _c_i64, _vp, _c_int, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64,
+                             _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64]),
+    "kv16_plan": (_c_int, [_vp, _vp, _c_int]),
+    "kv16_attention": (_c_int, [_vp, _c_int, _vp, _c_i64, _c_i64, _c_i64, _c_f, _vp, _c_i64, _c_i64, _c_i64]),
+    "kv16_destroy": (_c_int, [_vp]),
+    "pattn_init": (_c_int, [_pp, _c_int, _c_int, _c_int, _vp]),
+    "pattn_run": (_c_int, [_vp, _c_i64, _c_int, _vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _c_int,
+                           _c_f, _vp, _c_i64, _c_i64]),
+    "pattn_kernel": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
+    "pattn_status": (_c_int, [_vp]),
+    "pattn_destroy": (_c_int, [_vp]),
     "kv_paged_state": (_c_int, [_vp, _pp, _pp, _pp, _pp, _pp]),
     "kv_paged_prepare": (_c_int, [_vp, _c_int]),
     "kv_paged_reorder": (_c_int, [_vp, _vp, _c_int]),
@@ -196,9 +215,13 @@ def _raw_stream(index: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _StreamOrder:
     """Orders a call on a context's stream after the work of the stream that is current when the call is
-    made, and what follows it there after the call, where the two differ."""
+    made, and what follows it there after the call, where the two differ.  The call is made with the context's
+    device current."""
 
     def __init__(self, device):
         self.device = torch.device(device)
@@ -207,6 +230,9 @@ class _StreamOrder:
         self.raw = self.stream.cuda_stream
 
     def run(self, fn, name: str, tensors, *args):
+        if _device_index() != self.index:
+            with torch.cuda.device(self.index):
+                return self.run(fn, name, tensors, *args)
         if _raw_stream(self.index) == self.raw:
             st = fn(*args)
             if st == OK:
@@ -678,6 +704,258 @@ def _output(out, shape, device):
         return out, _rows4(out, "out", shape)
     row = shape[2] * shape[3]
     return torch.empty(shape, dtype=torch.bfloat16, device=device), (shape[1] * row, row, shape[3])
+
+
+def _rows3(t: torch.Tensor, name: str, shape, dtype, index: int):
+    """The strides of a [tokens, heads, D] tensor of this shape and dtype on device `index`."""
+    st = t.stride()
+    if t.shape != shape or st[2] != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit stride along the last axis, got {list(t.shape)}")
+    if t.dtype != dtype or not t.is_cuda or t.device.index != index:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}")
+    return st
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype, index: int) -> int:
+    """The address of a contiguous [n] tensor of this dtype on device `index`."""
+    if t.shape != (n,) or not t.is_contiguous() or t.dtype != dtype or not t.is_cuda or t.device.index != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on cuda:{index}")
+    return t.data_ptr()
+
+
+class Rotary:
+    """Rotary positions of heads of D dims (libvbs rope_*): at position p a pair (a, b) of dims of frequency f becomes
+    (a cos pf - b sin pf, b cos pf + a sin pf).
+
+    `rot` dims (all by default, an even number) are rotated, the rest stay; a pair is (i, i + rot / 2) in the "half"
+    layout, (2i, 2i + 1) in the "interleaved" one; frequencies are base ** (-2i / rot).  For contexts longer than the
+    model's, scaling stretches them by `factor`: "linear" all alike, "base" by a larger base, "parts" by the turns a pair
+    makes over the `original` length (none where it makes `high` or more, all where `low` or fewer); `amplitude` is a factor
+    on the rotated values.  `freqs` (rot / 2 numbers, radians a position) replaces all of these.
+    """
+
+    def __init__(self, D: int, *, rot: int | None = None, base: float = 10000.0, layout: str = "half",
+                 scaling: str | None = None, factor: float = 1.0, original: float = 8192, low: float = 1.0, high: float = 4.0,
+                 amplitude: float = 1.0, freqs=None, device="cuda"):
+        self.ctx = _vp()
+        self.D, self.rot, self.layout = D, D if rot is None else rot, layout
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, got {layout!r}")
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
+        f = (_c_d * max(1, self.rot // 2))()
+        if freqs is None:
+            _check(lib().rope_frequencies(self.rot, base, ROPE_SCALINGS[scaling], factor, original, low, high, f), "rope_frequencies")
+        else:
+            freqs = [float(x) for x in freqs]
+            if len(freqs) != self.rot // 2:
+                raise ValueError(f"freqs must have {self.rot // 2} entries")
+            f[:len(freqs)] = freqs
+        self.freqs = tuple(f[:self.rot // 2])
+        self.device = torch.device(device)
+        with torch.cuda.device(self.device):
+            self.index = torch.cuda.current_device()
+            _check(lib().rope_init(ctypes.byref(self.ctx), D, self.rot, ROPE_LAYOUTS[layout], f, amplitude), "rope_init")
+
+    def apply(self, pos: torch.Tensor, q: torch.Tensor, k: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+              k_out: torch.Tensor | None = None):
+        """(q, k) [N, heads, D] (bfloat16 or float32, unit stride along D) rotated to pos (int32 [N]; a negative one: the
+        token is skipped), into new tensors or the given ones (q and k themselves for in place)."""
+        N, i = pos.numel(), self.index
+        dt = q.dtype
+        code = _dtype_code(dt)
+        pp = _vector(pos, "pos", N, torch.int32, i)
+        qs, qp, q_out, qo = self._pair(N, q, q_out, "q", dt)
+        if k is None:
+            if k_out is not None:
+                raise ValueError("k_out needs k")
+            ks, kp, ko, heads = (0, 0), None, (0, 0), 0
+        else:
+            ks, kp, k_out, ko = self._pair(N, k, k_out, "k", dt)
+            heads = k.shape[1]
+        args = (self.ctx, N, pp, code, qp, qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], q.shape[1], kp, ks[0], ks[1],
+                None if k is None else k_out.data_ptr(), ko[0], ko[1], heads)
+        if _device_index() == i:
+            st = lib().rope_apply(*args, _raw_stream(i))
+        else:
+            with torch.cuda.device(i):
+                st = lib().rope_apply(*args, _raw_stream(i))
+        if st != OK:
+            _check(st, "rope_apply")
+        return q_out, k_out
+
+    def _pair(self, N, x, out, name, dt):
+        shape = (N, x.shape[1] if x.dim() == 3 else 0, self.D)
+        st = _rows3(x, name, shape, dt, self.index)
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=x.device)
+        return st, x.data_ptr(), out, _rows3(out, name + "_out", shape, dt, self.index)
+
+    def close(self):
+        if getattr(self, "ctx", None) is not None and self.ctx.value:
+            if torch.cuda.is_initialized():
+                torch.cuda.synchronize(self.device)
+            lib().rope_destroy(self.ctx)
+            self.ctx = _vp()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagedKV16(PagedKV):
+    """A PagedKV in bfloat16 with the write of new rows, rotated on the way, and the attention that reads it.
+
+    `heads` is the number of query heads (a multiple of H), `max_q` the most query tokens per row of one
+    attend() call (up to 32).  D is a multiple of 8 up to 256.
+    """
+
+    def __init__(self, batch: int, W: int, L: int, H: int, D: int, *, heads: int, blocks_per_sentence: int,
+                 max_blocks: int, block: int = 16, max_q: int = 1, device="cuda", pool=None):
+        self.ctx16 = _vp()
+        NB = batch * blocks_per_sentence
+        if pool is not None and (pool.dtype != torch.bfloat16 or not pool.is_contiguous()
+                                 or pool.shape != (NB, L, 2, H, block, D)):
+            raise ValueError(f"pool must be a contiguous bfloat16 [{NB}, {L}, 2, {H}, {block}, {D}] tensor")
+        super().__init__(batch, W, L, H, D, blocks_per_sentence=blocks_per_sentence, max_blocks=max_blocks,
+                         block=block, dtype=torch.bfloat16, device=device, pool=pool)
+        self.heads, self.max_q = heads, max_q
+        self._q_shape = None                        # of the planned step
+        _check(lib().kv16_init(ctypes.byref(self.ctx16), self.ctx, heads, max_q), "kv16_init")
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rotary: Rotary | None = None,
+               pos: torch.Tensor | None = None, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+               k_out: torch.Tensor | None = None):
+        """Write k, v [N, H, D] (bfloat16 or float32, unit stride along D) at slots (int64 [N], no one twice, -1: not
+        written), and return (q, k) as rotated.
+
+        With rotary, k is rotated to pos (int32 [N]; a negative one: the token is skipped) on its way, and stored to
+        k_out too where that is given; q [N, heads, D] of k's dtype is rotated into q_out (new by default).  q_out and k_out may
+        be q and k themselves."""
+        N, i = slots.numel(), self._order.index
+        dt = k.dtype
+        code = _dtype_code(dt)
+        shape = (N, self.H, self.D)
+        ks, vs = _rows3(k, "k", shape, dt, i), _rows3(v, "v", shape, dt, i)
+        sp = _vector(slots, "slots", N, torch.int64, i)
+        tensors = [k, v, slots]
+        rope = pp = qp = qo = ko = None
+        qs = qos = kos = (0, 0)
+        if rotary is None:
+            if not (pos is None and q is None and q_out is None and k_out is None):
+                raise ValueError("pos, q, q_out and k_out need rotary")
+        else:
+            if rotary.D != self.D or rotary.index != i:
+                raise ValueError(f"rotary must be for {self.D} dims on cuda:{i}")
+            if pos is None:
+                raise ValueError("rotary needs pos")
+            rope, pp = rotary.ctx, _vector(pos, "pos", N, torch.int32, i)
+            tensors.append(pos)
+            if q is not None:
+                q_shape = (N, self.heads, self.D)
+                qs, qp = _rows3(q, "q", q_shape, dt, i), q.data_ptr()
+                if q_out is None:
+                    q_out = torch.empty(q_shape, dtype=dt, device=self.device)
+                qos, qo = _rows3(q_out, "q_out", q_shape, dt, i), q_out.data_ptr()
+                tensors += (q, q_out)
+            elif q_out is not None:
+                raise ValueError("q_out needs q")
+            if k_out is not None:
+                kos, ko = _rows3(k_out, "k_out", shape, dt, i), k_out.data_ptr()
+                tensors.append(k_out)
+        self._order.run(lib().kv16_append, "kv16_append", tensors, self.ctx16, layer, N, sp, code, k.data_ptr(), ks[0], ks[1],
+                        v.data_ptr(), vs[0], vs[1], rope, pp, ko, kos[0], kos[1], qp, qs[0], qs[1], qo, qos[0], qos[1])
+        return q_out, k_out
+
+    def plan(self, ctx_len: torch.Tensor, n_q: int = 1):
+        """Prepare a step's attention: ctx_len (int32 [R] on the device) is each row's number of cached
+        positions, its n_q new tokens among them.  Call it whenever the tables or lengths have changed, as
+        PagedKV8.plan()."""
+        cp = _vector(ctx_len, "ctx_len", self.R, torch.int32, self._order.index)
+        self._order.run(lib().kv16_plan, "kv16_plan", (ctx_len,), self.ctx16, cp, n_q)
+        self._q_shape = (self.R, n_q, self.heads, self.D)
+
+    def attend(self, layer: int, q: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None):
+        """softmax(scale q k^T) v of q [R, n_q, heads, D] (bfloat16, unit stride along D) over each row's
+        cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
+        shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
+        qs = _rows4(q, "q", shape)
+        out, os_ = _output(out, shape, self.device)
+        if q.device.index != self._order.index or out.device.index != self._order.index:
+            raise ValueError(f"q and out must be on cuda:{self._order.index}")
+        self._order.run(lib().kv16_attention, "kv16_attention", (q, out), self.ctx16, layer, q.data_ptr(), qs[0], qs[1], qs[2],
+                        self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
+        return out
+
+    def close(self):
+        if getattr(self, "ctx16", None) is not None and self.ctx16.value:
+            lib().kv16_destroy(self.ctx16)
+            self.ctx16 = _vp()
+        super().close()
+
+
+class PromptAttention:
+    """Attention of whole prompts, packed one after the other, to themselves (libvbs pattn_*).
+
+    `heads` query heads share `kv_heads`; D is a multiple of 8 up to 256.  Work goes on the stream that is current at
+    construction.
+    """
+
+    def __init__(self, heads: int, D: int, *, kv_heads: int | None = None, device="cuda"):
+        self.ctx = _vp()
+        self.heads, self.D = heads, D
+        self.kv_heads = heads if kv_heads is None else kv_heads
+        self.device = torch.device(device)
+        self._order = _StreamOrder(self.device)
+        with torch.cuda.device(self._order.index):
+            _check(lib().pattn_init(ctypes.byref(self.ctx), heads, self.kv_heads, D, _vp(self._order.raw)), "pattn_init")
+
+    def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, causal: bool = True,
+               scale: float | None = None, out: torch.Tensor | None = None):
+        """softmax(scale q k^T) v: q [N, heads, D], k and v [N, kv_heads, D] (bfloat16, unit stride along D) over each
+        token's own request, up to the token (causal) or the whole of it.  Request b has the tokens
+        cu[b] .. cu[b + 1] - 1 (int32 [batch + 1] on the device, as PagedKV.build() gives it); other tokens' rows of out
+        are left as they are.  scale defaults to D ** -0.5."""
+        i = self._order.index
+        N = q.shape[0] if q.dim() == 3 else 0
+        shape, kv_shape = (N, self.heads, self.D), (N, self.kv_heads, self.D)
+        bf = torch.bfloat16
+        qs, ks, vs = _rows3(q, "q", shape, bf, i), _rows3(k, "k", kv_shape, bf, i), _rows3(v, "v", kv_shape, bf, i)
+        batch = cu.numel() - 1
+        if batch < 0:
+            raise ValueError("cu must have batch + 1 entries")
+        cp = _vector(cu, "cu", batch + 1, torch.int32, i)
+        if out is None:
+            out = torch.empty(shape, dtype=bf, device=q.device)
+        os_ = _rows3(out, "out", shape, bf, i)
+        self._order.run(lib().pattn_run, "pattn_run", (q, k, v, cu, out), self.ctx, N, batch, cp, q.data_ptr(), qs[0], qs[1],
+                        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], 1 if causal else 0,
+                        self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1])
+        return out
+
+    @property
+    def tiles(self):
+        """Whether the last attend() took the tcgen05 tiles or, False, the kernel for other layouts; None before it."""
+        n = _c_int()
+        _check(lib().pattn_kernel(self.ctx, ctypes.byref(n)), "pattn_kernel")
+        return None if n.value < 0 else bool(n.value)
+
+    def status(self) -> int:
+        """Synchronise and return the device status word (0 = OK)."""
+        return lib().pattn_status(self.ctx)
+
+    def close(self):
+        if getattr(self, "ctx", None) is not None and self.ctx.value:
+            lib().pattn_destroy(self.ctx)
+            self.ctx = _vp()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class CrossAttention:

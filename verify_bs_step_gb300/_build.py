@@ -22,7 +22,7 @@ BUILD_CHECKED = os.path.join(ROOT, "_build", "vbs_checked")
 LIB_CHECKED = os.path.join(HERE, "libvbs_checked.so")
 
 SOURCES = ["api.cu", "bs_step.cu", "kv.cu", "kv_tables.cu", "kv8.cu", "attn.cu", "attn_i8.cu", "attn_e4m3.cu", "xattn.cu", "xattn_tc.cu", "attn_api.cu",
-           "bpd.cu", "peak.cu"]
+           "rope.cu", "attn_bf16.cu", "prompt.cu", "prompt_tc.cu", "kv16_api.cu", "bpd.cu", "peak.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

@@ -6,6 +6,7 @@
 
 #include "bs_internal.h"
 #include "kv8.h"
+#include "rope.h"
 
 namespace vbs {
 
@@ -54,6 +55,8 @@ int launch_kv8_attention_i8(const PagedArgs& a, const Kv8Geom& g, const QO& io, 
                             int2* pieces, int num_sms, cudaStream_t s);
 int launch_kv8_attention_e4m3(const PagedArgs& a, const Kv8Geom& g, const QO& io, const Kv8Plan& p, float* part,
                               int2* pieces, int num_sms, cudaStream_t s);
+int launch_kv16_attention(const PagedArgs& a, const Kv16Geom& g, const QO& io, const Kv8Plan& p, float* part,
+                          int2* pieces, int num_sms, cudaStream_t s);
 // *tiles: whether the tcgen05 tiles took the call
 int launch_xattn(const EncKV& kv, const QO& io, float* part, int2* pieces, int num_sms, cudaStream_t s, int* tiles);
 

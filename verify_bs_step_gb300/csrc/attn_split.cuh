@@ -36,6 +36,7 @@
 #include "attn.h"
 #include "codes.cuh"
 #include "common.cuh"
+#include "rope.h"
 
 namespace vbs {
 
@@ -74,6 +75,30 @@ __device__ __forceinline__ uint2 lds8(u32 a) {
   return r;
 }
 
+__device__ __forceinline__ float lds_bf16(u32 a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
+  return bf16_lo(r);
+}
+// Whether one of eight bf16 is an infinity or NaN, and eight in shared memory with such replaced by zeros.
+__device__ __forceinline__ bool not_finite16(const uint4& q) {
+  const u32 w[4] = {q.x, q.y, q.z, q.w};
+  u32 top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+  return top >= 0x7f80u;
+}
+__device__ __forceinline__ void drop_not_finite16(u32 a) {
+  const uint4 q = lds16(a);
+  u32 w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
+  }
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
 template <bool BF> __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, u32 b0, u32 b1) {
   if (BF)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -102,13 +127,14 @@ struct __align__(16) UnitHead {
 };
 
 // ---------------------------------------------------------------------------------------
-// sources
+// sources: elements of EL bytes (BF: bf16, else codes); DENSE: a unit's rows follow one another; RAW: what a row does
+// not see may hold infinities and NaN
 // ---------------------------------------------------------------------------------------
 
 // The 8-bit paged cache: a unit is up to 16 positions of one page of the plan's list.
 template <int FMT> struct PagedSrc {
   static constexpr int EL = 1, FORMAT = FMT;
-  static constexpr bool BF = false;
+  static constexpr bool BF = false, DENSE = true, RAW = false;
   Kv8Geom g;
   const int4* list;               // [B][cap] (page, first position, beams, positions)
   const int* n_pages;             // [B]
@@ -152,10 +178,48 @@ template <int FMT> struct PagedSrc {
   }
 };
 
+// The 16-bit paged cache, in the same units.
+struct Paged16Src {
+  static constexpr int EL = 2, FORMAT = 0;
+  static constexpr bool BF = true, DENSE = true, RAW = true;
+  Kv16Geom g;
+  const int4* list;               // [B][cap] (page, first position, beams, positions)
+  const int* n_pages;             // [B]
+  const int* seen;                // [R]
+  int cap, tpp;                   // list entries a sentence, units a page
+  int64_t most() const { return static_cast<int64_t>(cap) * tpp; }
+  struct Batch {                  // one unit per lane
+    const uint16_t* k;            // its K rows; V's stand H runs further on
+    int pos, n;
+    u32 rows;
+  };
+  __device__ int units(int b) const { return n_pages[b] * tpp; }
+  __device__ int limit(int b, int w, int i, int W, int n_q) const { return seen[b * W + w] - n_q + 1 + i; }
+  __device__ void fetch(Batch& t, int b, int h, int u, bool valid) const {
+    t = Batch{g.pool, 0, 0, 0u};
+    if (!valid) return;
+    const int e = u / tpp, off = (u - e * tpp) * 16;
+    const int4 x = list[static_cast<int64_t>(b) * cap + e];
+    t.pos = x.y + off;
+    t.n = max(0, min(16, x.w - off));
+    t.rows = static_cast<u32>(x.z);
+    if (t.n > 0) t.k = g.pool + (((static_cast<int64_t>(x.x) * g.L + g.layer) * 2 * g.H + h) * g.block + off) * g.D;
+  }
+  template <class L>
+  __device__ __forceinline__ void issue(const Batch& t, int k, int lane, int, int, UnitHead* head,
+                                        const L& load) const {
+    const u64 at = shfl64(reinterpret_cast<u64>(t.k), k);
+    const int n = __shfl_sync(FULL, t.n, k);
+    if (lane == k) *head = UnitHead{t.pos, t.n, t.rows, 1.f, 0.f, 1.f, {0.f, 0.f}};
+    const char* kp = reinterpret_cast<const char*>(at);
+    load(kp, kp + static_cast<int64_t>(g.H) * g.block * g.D * 2, g.D * 2, g.D * 2, n);
+  }
+};
+
 // An encoder's states: a unit is up to 16 positions of a sentence.
 struct EncSrc {
   static constexpr int EL = 2, FORMAT = 0;
-  static constexpr bool BF = true;
+  static constexpr bool BF = true, DENSE = false, RAW = false;
   EncKV e;
   struct Batch { int u; };
   int64_t most() const { return (static_cast<int64_t>(e.S) + 15) / 16; }
@@ -352,7 +416,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         const u32 base = ring_a + st * C::STAGE;
         src.issue(batch, k & 31, lane, b, h, &heads[wid][st],
                   [&](const char* kp, const char* vp, int64_t kld, int64_t vld, int cnt) {
-          if (EXACT && EL == 1 && cnt == 16) {              // a whole unit of contiguous rows: constant offsets
+          if (EXACT && Src::DENSE && cnt == 16) {           // a whole unit of contiguous rows: constant offsets
             const char *ks = kp + lane * 16, *vs = vp + lane * 16;
 #pragma unroll
             for (int i = 0; i < DP / C::CHK / 2; ++i) {
@@ -523,12 +587,14 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 
       // ---- softmax: weights relative to the running maximum of s + log2(V's scale) ----
       uint4 p[MT], p2[MT];
+      bool clear = true;                                    // every row sees the whole unit
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         int left[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) left[x] = (u.rows >> beam[mt][x]) & 1u || beam[mt][x] == 31 ? min(lim[mt][x] - u.pos, u.n) : 0;
         const bool full = __all_sync(FULL, left[0] >= 16 && left[1] >= 16);
+        clear = clear && full;
         float mx[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -594,6 +660,35 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         } else {
           p[mt] = make_uint4(pack_f16(w[0][0], w[0][1]), pack_f16(w[1][0], w[1][1]), pack_f16(w[0][2], w[0][3]),
                              pack_f16(w[1][2], w[1][3]));
+        }
+      }
+
+      // ---- V where some row does not see all of it: a weight of 0 times an infinity or NaN would be NaN.  Such elements
+      // go straight into the sums of the rows that see them (whatever their weights), and as zeros into the product ----
+      if (Src::RAW && !clear) {
+        bool odd = false;
+        for (int L = lane; L < 16 * nc; L += 32) odd = odd || not_finite16(lds16(va + L * 16));
+        if (__any_sync(FULL, odd)) {
+#pragma unroll 1
+          for (int t = 0; t < u.n; ++t)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                if (!((u.rows >> beam[mt][x]) & 1u) || t >= lim[mt][x] - u.pos) continue;
+#pragma unroll
+                for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    const int dim = out_dim<C::VCH>(c4 * 2 + y, j);
+                    if (!EXACT && dim >= D) continue;
+                    const float z = lds_bf16(va + ((t * nc + dim / 8) ^ v_swz(t, nc)) * 16 + dim % 8 * 2);
+                    if (!(fabsf(z) < INFINITY)) o[mt][j][x * 2 + y] += z;
+                  }
+              }
+          __syncwarp();
+          for (int L = lane; L < 16 * nc; L += 32) drop_not_finite16(va + L * 16);
+          __syncwarp();
         }
       }
 
@@ -852,23 +947,6 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
 // ---------------------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------------------
-
-// A launch that may be set up while its predecessor in the stream finishes; the kernel waits for it
-// (griddepcontrol.wait) before its first access to memory.
-template <typename... KArgs, typename... Args>
-int launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...) == cudaSuccess ? VBS_OK : VBS_ECUDA;
-}
 
 // Rows of a segment: two mma tiles where more than 16 rows share a K/V head (K/V are unpacked once for
 // both); one at head_dim > 128, whose o does not fit the registers twice.

@@ -80,14 +80,6 @@ template <int FMT> __device__ __forceinline__ int regrow(const Kv8Geom& g, int64
   return e;
 }
 
-// The larger magnitudes of two pairs of bf16, a NaN before all.
-__device__ __forceinline__ u32 max_abs2(u32 a, u32 b) {
-  const __nv_bfloat162 x = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&a));
-  const __nv_bfloat162 y = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b));
-  const __nv_bfloat162 z = __hmax2_nan(x, y);
-  return *reinterpret_cast<const u32*>(&z);
-}
-
 // One run, element by element: rows of any alignment, and runs that hold NaN, infinities or values past the largest scale.
 template <int FMT, typename T>
 __device__ __noinline__ void append_elements(const Kv8Geom& g, const void* base, int64_t tok, int64_t p0, int64_t run,

@@ -1,6 +1,8 @@
 // Two fp32 numbers in one instruction (sm_103a).
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 
 namespace vbs {
@@ -27,6 +29,14 @@ __device__ __forceinline__ u64 add2(u64 a, u64 b) {
   u64 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// The larger magnitudes of two pairs of bf16, a NaN before all.
+__device__ __forceinline__ u32 max_abs2(u32 a, u32 b) {
+  const __nv_bfloat162 x = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&a));
+  const __nv_bfloat162 y = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b));
+  const __nv_bfloat162 z = __hmax2_nan(x, y);
+  return *reinterpret_cast<const u32*>(&z);
 }
 
 }  // namespace vbs
