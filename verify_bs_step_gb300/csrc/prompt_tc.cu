@@ -29,9 +29,15 @@ namespace vbs {
 constexpr int PT_M = 128;                 // query rows a tile
 constexpr int PT_N = 128;                 // positions a tile
 constexpr int PT_SM = 256;                // softmax threads: one a row of both tiles
-constexpr int PT_NT = PT_SM + 128;        // and warps for K, V, the products and the items
-constexpr int PT_CU = 4096;               // request starts held in shared memory
+constexpr int PT_OUT = 128;               // threads that look through V and bring results out
+constexpr int PT_NT = PT_SM + PT_OUT + 128;   // and warps for the loads, each row tile's products, and the items
+constexpr int PT_W_OUT = PT_SM / 32, PT_W_LOAD = PT_W_OUT + PT_OUT / 32, PT_W_MMA = PT_W_LOAD + 1;
+constexpr int PT_RING = 4;                // items on their way
+constexpr int PT_CU = 2048;               // request starts held in shared memory
 constexpr int PT_STMAX = 4;
+// registers a thread: 65,536 / 512 at launch, then the softmax threads take what the others leave
+constexpr int PT_REGS = 128, PT_REGS_SM = 176, PT_REGS_OUT = 104, PT_REGS_REST = 56;
+static_assert(PT_SM * PT_REGS_SM + PT_OUT * PT_REGS_OUT + 128 * PT_REGS_REST <= PT_NT * PT_REGS, "registers of the block");
 
 struct PtArgs {
   PromptArgs p;
@@ -45,28 +51,47 @@ template <int DP> struct PtCfg {
   static constexpr int QB = SLABS * PT_M * 128;            // one row tile of Q
   static constexpr int TB = SLABS * PT_N * 128;            // one tile of K or V
   static constexpr int ST = DP == 64 ? 4 : 2;              // stages of K, and of V
-  static constexpr size_t SMEM = 2 * QB + 2 * ST * TB + PT_CU * 4 + 1024;
+  static constexpr int OUT = 32 * 64;                      // a warp's rows of 32 dims on their way out
+  static constexpr size_t SMEM = 2 * QB + 2 * ST * TB + PT_CU * 4 + PT_OUT / 32 * OUT + 1024;
 };
 
-// Rings of barriers: kf, vf (a tile has landed), ke, ve (it is not read any more); per row tile: s (scores are done),
-// p (weights are written), o (an item's sums are done), of (they have been read).  q, qe: an item's Q has landed, is not
-// read any more.  itf, ite: an item is worked out, is done with.  end: every product that was issued is done.
+// Rings of barriers: kf, vf (a tile has landed), ke, ve (it is not read any more); vx and vc in place of vf where not
+// every row sees the whole tile (it has landed, has been looked through): a barrier's phases count its own uses alone, so
+// that who waits for one is never two behind.  Per row tile: q, qe (an item's Q has
+// landed, is not read any more), s (scores are done), p (the weights of half a tile are written), o (an item's sums are
+// done), of (they have been read).  itf, ite: an item is worked out, is done with.  end: every product that was issued is
+// done.
 struct PtBars {
-  u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], s[2], p[2], o[2], of[2], q, qe, itf[2], ite[2], end;
+  u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], q[2], qe[2], s[2], p[2][2], o[2], of[2], vx[PT_STMAX], vc[PT_STMAX], itf[PT_RING],
+      ite[PT_RING], end;
 };
 
 struct PtItem {
   int tok, h;                             // first token; h < 0: no more items
   int base;                               // the first position
   int n;                                  // tiles of positions
-  int j0[2], j1[2];                       // a row tile's
-  int f0[2], f1[2];                       // of them, those that every row sees whole
+  int y1[2];                              // the end of what a row tile sees, counted from the first position
+  int j0[2], j1[2];                       // its tiles
+  int w0, w1;                             // tiles that every row of both sees whole: their V is used as it is
 };
 
-// Whether every row that works on tile j sees all of it: its V is used as it is.
-__device__ __forceinline__ bool seen_whole(const PtItem& it, int j) {
-  return (j < it.j0[0] || j >= it.j1[0] || (j >= it.f0[0] && j < it.f1[0])) &&
-         (j < it.j0[1] || j >= it.j1[1] || (j >= it.f0[1] && j < it.f1[1]));
+// Steps of 16 positions of tile j that a row tile sees some of.
+__device__ __forceinline__ int steps_of(int y1, int j) { return min(PT_N, y1 - j * PT_N + 15) >> 4; }
+
+// Adds to a row's 32 sums, from dim c on, the elements of V that were put to 0 for the product and that it sees: they
+// are outside the tiles that every row sees whole.
+__device__ __noinline__ void add_odd(const PromptArgs& p, const PtItem& it, int X, int x0, int x1, int c, float* o) {
+  for (int j = it.j0[X]; j < it.j1[X]; ++j) {
+    if (j >= it.w0 && j < it.w1) continue;
+    const int y1 = min(x1, (j + 1) * PT_N);
+    for (int y = max(x0, j * PT_N); y < y1; ++y) {
+      const uint16_t* v = p.v + static_cast<int64_t>(it.base + y) * p.v_tok + it.h * p.v_head + c;
+      for (int i = 0; i < 32 && c + i < p.D; ++i) {
+        const float z = bf16_lo(v[i]);
+        if (!(fabsf(z) < INFINITY)) o[i] += z;
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ void tma_load3(u32 dst, const CUtensorMap* map, u64* bar, int x, int h, int t) {
@@ -91,6 +116,18 @@ __device__ __forceinline__ int2 request_of(const PromptArgs& a, const int* cu, i
   return s >= 0 && s <= t && e > t && e <= a.N ? make_int2(s, e) : make_int2(0, 0);
 }
 
+// tc_wait in little code.
+__device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone, int* status) {
+#pragma unroll 1
+  for (u32 i = 0; !mbar_wait(bar, parity, 1); ++i)
+    if (i >= TC_SPIN || *gone) {
+      *gone = 1;
+      set_status(status, VBS_ETIMEOUT);
+      return false;
+    }
+  return true;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                                                             const __grid_constant__ CUtensorMap kmap,
@@ -102,13 +139,15 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   __shared__ u32 tmem_base;
   __shared__ volatile int gone;
   __shared__ volatile int odd;                            // an infinity or NaN of V was put to 0 (stays so)
-  __shared__ PtItem ring[2];
-  __shared__ int2 span[2][2 * PT_M];                      // positions [x, y) of an item's tokens
+  __shared__ PtItem ring[PT_RING];
+  __shared__ int2 span[PT_RING][2 * PT_M];                // positions [x, y) of an item's tokens
+  __shared__ float sums[2][2][PT_M];                      // of a row's weights, by the row tile's items in turn
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = pt_smem_raw + ((1024 - (smem_u32(pt_smem_raw) & 1023)) & 1023);
   const u32 q_a = smem_u32(smem), k_a = q_a + 2 * C::QB, v_a = k_a + ST * C::TB;
-  int* cu = reinterpret_cast<int*>(smem + 2 * C::QB + 2 * ST * C::TB);
+  unsigned char* out_s = smem + 2 * C::QB + 2 * ST * C::TB;
+  int* cu = reinterpret_cast<int*>(out_s + PT_OUT / 32 * C::OUT);
   const PromptArgs& p = a.p;
   const int every = (p.B + 1 + PT_CU - 1) / PT_CU;        // one start in `every` is held
   const int items = a.tiles * p.H;
@@ -116,26 +155,31 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kf[i], 1);
-      mbar_init(&bars.ke[i], 1);
+      mbar_init(&bars.ke[i], 2);
       mbar_init(&bars.vf[i], 1);
-      mbar_init(&bars.ve[i], 1);
+      mbar_init(&bars.ve[i], 2);
+      mbar_init(&bars.vx[i], 1);
+      mbar_init(&bars.vc[i], PT_OUT);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q[i], 1);
+      mbar_init(&bars.qe[i], 1);
       mbar_init(&bars.s[i], 1);
-      mbar_init(&bars.p[i], PT_M);
+      mbar_init(&bars.p[i][0], PT_M);
+      mbar_init(&bars.p[i][1], PT_M);
       mbar_init(&bars.o[i], 1);
-      mbar_init(&bars.of[i], PT_M);
-      mbar_init(&bars.itf[i], 1);
-      mbar_init(&bars.ite[i], PT_SM / 32 + 3);
+      mbar_init(&bars.of[i], PT_OUT);
     }
-    mbar_init(&bars.q, 1);
-    mbar_init(&bars.qe, 1);
-    mbar_init(&bars.end, 1);
+    for (int i = 0; i < PT_RING; ++i) {
+      mbar_init(&bars.itf[i], 1);
+      mbar_init(&bars.ite[i], (PT_SM + PT_OUT) / 32 + 3);
+    }
+    mbar_init(&bars.end, 2);
     fence_mbar_init();
     gone = 0;
     odd = 0;
   }
-  if (wid == PT_SM / 32 + 2) {
+  if (wid == PT_W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -149,327 +193,476 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * PT_N;
 
-  // the item in ring slot t & 1, once it is there; done with it, one arrival a warp
-  auto item_at = [&](int t) { return tc_wait(&bars.itf[t & 1], (t >> 1) & 1, &gone, p.status); };
+  auto item_at = [&](int t) { return pt_wait(&bars.itf[t % PT_RING], (t / PT_RING) & 1, &gone, p.status); };
 
-  if (wid < PT_SM / 32) {
+  if (wid < PT_W_OUT) {
     // ---- softmax: thread = row ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_REGS_SM));
     const int X = wid >> 2, r = tid & (PT_M - 1);          // row tile, row
     const u32 tl = static_cast<u32>((wid & 3) * 32) << 16;  // its TMEM lanes
     const u32 ts = tm_s + X * PT_N + tl, to = tm_o + X * DP + tl;
     const bool neg = p.scale < 0.f;
     // (a scale of 0 stays above it, so that a masked -inf stays one)
     const float sc = fmaxf(fabsf(p.scale) * LOG2E_F, 1.17549435e-38f);
-    const int tok_r = r / a.G, g = r - tok_r * a.G;
+    const int tok_r = r / a.G;
     bool ok = true;
-    int T = 0, S = 0, O = 0;                              // K/V tiles, score tiles and items of this row tile so far
+    int S = 0, O = 0;                                     // score tiles and items of this row tile so far
     for (int t = 0;; ++t) {
       ok = __all_sync(FULL, item_at(t));
-      const PtItem& it = ring[t & 1];
+      const PtItem& it = ring[t % PT_RING];
       if (!ok || it.h < 0) break;
-      const int2 sp = r < a.TT * a.G ? span[t & 1][X * a.TT + tok_r] : make_int2(0, 0);
-      const int x0 = sp.x - it.base, x1 = sp.y - it.base;  // counted from the item's first position
+      const int2 sp = r < a.TT * a.G ? span[t % PT_RING][X * a.TT + tok_r] : make_int2(0, 0);
+      // counted from the item's first position; rows that are not there see all of it (they are not written)
+      const int x0 = sp.y > 0 ? sp.x - it.base : 0, x1 = sp.y > 0 ? sp.y - it.base : INT_MAX / 2;
       const int j0 = it.j0[X], j1 = it.j1[X];
-      float m = -INFINITY, l = 0.f;                       // the reference (in scaled units), the sum of weights
+      // the reference and the largest score so far (in scaled units), the sum of weights
+      float m = 0.f, top = -INFINITY, l = 0.f;
       for (int j = j0; j < j1; ++j, ++S) {
-        ok = __all_sync(FULL, tc_wait(&bars.s[X], S & 1, &gone, p.status));
+        const int from = x0 - j * PT_N, left = x1 - j * PT_N;
+        ok = __all_sync(FULL, pt_wait(&bars.s[X], S & 1, &gone, p.status));
         if (!ok) break;
         tc_fence_after();
-        float s[PT_N];
+        if (__any_sync(FULL, from > 0 || left < PT_N) || neg) {
+          // scores that a row does not see become -inf where they stand (and all change their sign under a negative
+          // scale), 32 at a time where there are such, in little code: it is fetched anew every time
+          const int least = __reduce_min_sync(FULL, left), late = __reduce_max_sync(FULL, from);
+#pragma unroll 1
+          for (int c = 0; c < PT_N; c += 32) {
+            if (least >= c + 32 && late <= c && !neg) continue;
+            const int lo = max(0, from - c), hi = left - c;
+            u32 see = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+            see = lo >= 32 ? 0u : see & (~0u << lo);
+            float x[32];
+            tc_ld32(ts + c, x);
+            tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < PT_N; c += 32) tc_ld32(ts + c, s + c);
-        tc_wait_ld();
-        if (neg) {
-#pragma unroll
-          for (int i = 0; i < PT_N; ++i) s[i] = -s[i];
-        }
-        const int from = x0 - j * PT_N, left = x1 - j * PT_N;
-        if (__any_sync(FULL, from > 0 || left < PT_N)) {
-#pragma unroll
-          for (int i = 0; i < PT_N; ++i)
-            if (i < from || i >= left) s[i] = -INFINITY;
-        }
-        float top[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
-#pragma unroll
-        for (int i = 8; i < PT_N; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], s[i], s[i + 1]);
-        const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]) * sc;
-        const bool grow = mx > m + 8.f;                   // also in a row's first tile: m = -inf
-        if (__any_sync(FULL, grow)) {
-          const float to_m = grow ? mx : m;
-          const float corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to_m)) : 1.f;
-          if (j > j0) {
-            // O holds the tiles before (S of this one was issued after their products, and is done)
-#pragma unroll
-            for (int c = 0; c < DP; c += 16) {
-              float o[16];
-              tc_ld16(to + c, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
-              tc_st16(to + c, o);
-            }
+            for (int i = 0; i < 32; ++i) x[i] = see >> i & 1u ? (neg ? -x[i] : x[i]) : -INFINITY;
+            tc_st32(ts + c, x);
           }
-          l *= corr;
-          m = to_m;
+          tc_wait_st();
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        // scale and reference go into one fma, whose product is not rounded as the reference was: for
-        // large scores the difference is more than a weight can bear, and the product is rounded first
-        float f = sc;
-        if (__any_sync(FULL, fabsf(ref) > 65536.f)) {
-#pragma unroll
-          for (int i = 0; i < PT_N; ++i) s[i] *= sc;
-          f = 1.f;
-        }
-        u64 sum[2] = {0, 0};
-        const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
-#pragma unroll
-        for (int c = 0; c < PT_N; c += 32) {
-          float pk[16];
+        // sixteen pairs of weights relative to the reference, and their sum
+        auto weights = [](const float* s, u64 f2, u64 r2, u64 (&sum)[2], float (&pk)[16]) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x, y;
-            unpair(fma2(pair(s[c + 2 * i], s[c + 2 * i + 1]), f2, r2), x, y);
+            unpair(fma2(pair(s[2 * i], s[2 * i + 1]), f2, r2), x, y);
             x = ex2(x);
             y = ex2(y);
             sum[i & 1] = add2(sum[i & 1], pair(x, y));
             __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
             pk[i] = *reinterpret_cast<float*>(&w);
           }
-          tc_st16(ts + c / 2, pk);                        // the weights stand where scores were
+        };
+        // a reference that the largest score is within 2^16 of will do
+        auto strays = [&](float t) { return t > m + 16.f || (t < m - 16.f && t > -INFINITY) || fabsf(m) > 65536.f; };
+        u64 sum[2] = {0, 0};
+        float t_max;
+        bool handed;                                      // the weights are there
+        {
+          float s[PT_N];
+#pragma unroll
+          for (int c = 0; c < PT_N; c += 32) tc_ld32(ts + c, s + c);
+          tc_wait_ld();
+          // the first half's weights are worked out with the reference as it is, beside the tile's maximum
+          float pk[2][16];
+          const u64 f2 = pair(sc, sc), r2 = pair(-m, -m);
+          weights(s, f2, r2, sum, pk[0]);
+          weights(s + 32, f2, r2, sum, pk[1]);
+          float x[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
+#pragma unroll
+          for (int i = 8; i < PT_N; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
+          t_max = fmaxf(top, max3(fmaxf(x[0], x[1]), x[2], x[3]) * sc);
+          handed = !__any_sync(FULL, strays(t_max));
+          if (handed) {
+            tc_st16(ts, pk[0]);                           // the weights stand where scores were
+            tc_st16(ts + 16, pk[1]);
+            weights(s + 64, f2, r2, sum, pk[0]);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars.p[X][0]);
+            tc_st16(ts + 32, pk[0]);
+            weights(s + 96, f2, r2, sum, pk[1]);
+            tc_st16(ts + 48, pk[1]);
+          }
         }
+        if (!handed) {
+          const bool move = strays(t_max) && t_max != m;
+          if (__any_sync(FULL, move)) {
+            const float to_m = move && t_max > -INFINITY ? t_max : m;
+            const float corr = to_m == m ? 1.f : (top == -INFINITY ? 0.f : ex2(m - to_m));
+            if (j > j0) {
+              // O holds the tiles before (S of this one was issued after their products, and is done)
+#pragma unroll 1
+              for (int c = 0; c < DP; c += 16) {
+                float o[16];
+                tc_ld16(to + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
+                tc_st16(to + c, o);
+              }
+            }
+            l *= corr;
+            m = to_m;
+          }
+          // scale and reference go into one fma, whose product is not rounded as the reference was: for
+          // large scores the difference is more than a weight can bear, and the product is rounded first
+          const bool large = __any_sync(FULL, fabsf(m) > 65536.f);
+          const float f = large ? 1.f : sc;
+          const u64 f2 = pair(f, f), r2 = pair(-m, -m);
+          sum[0] = sum[1] = 0;
+#pragma unroll 1
+          for (int c = 0; c < PT_N; c += 32) {
+            float s[32], pk[16];
+            tc_ld32(ts + c, s);
+            tc_wait_ld();
+            if (large) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] *= sc;
+            }
+            weights(s, f2, r2, sum, pk);
+            if (c == PT_N / 2) {
+              tc_wait_st();
+              tc_fence_before();
+              mbar_arrive(&bars.p[X][0]);
+            }
+            tc_st16(ts + c / 2, pk);
+          }
+        }
+        top = t_max;
         float l0, l1;
         unpair(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
-        // V where a row does not see the whole tile: the first row tile that works on it looks it through
-        const bool mine = X == 0 || j < it.j0[0] || j >= it.j1[0];
-        if (mine && !seen_whole(it, j)) {
-          const int st = (T + j) % ST;
-          ok = tc_wait(&bars.vf[st], ((T + j) / ST) & 1, &gone, p.status);
-          ok = __all_sync(FULL, ok);
-          if (!ok) break;
-#pragma unroll
-          for (int sl = 0; sl < C::SLABS; ++sl) {
-            uint4* row = reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (PT_N * 128) + r * 128);
-            u32 worst = 0;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 w = row[(c + r) & 7];           // (eight rows meet eight different chunks)
-              worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
-            }
-            if ((worst & 0x7f80u) == 0x7f80u || (worst & 0x7f800000u) == 0x7f800000u) {
-              for (int c = 0; c < 8; ++c) {
-                uint4 w = row[c];
-                u32* e = &w.x;
-                for (int i = 0; i < 4; ++i) {
-                  if ((e[i] & 0x7f80u) == 0x7f80u) e[i] &= 0xffff0000u;
-                  if ((e[i] & 0x7f800000u) == 0x7f800000u) e[i] &= 0x0000ffffu;
-                }
-                row[c] = w;
-              }
-              odd = 1;
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
+        if (j + 1 == j1) sums[O & 1][X][r] = l;
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars.p[X]);
+        mbar_arrive(&bars.p[X][1]);
+      }
+      if (!ok) break;
+      if (j1 > j0) ++O;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.ite[t % PT_RING]);
+    }
+    tc_wait_st();                                         // (weights of a tile that was given up)
+    tc_fence_before();
+  } else if (wid < PT_W_LOAD) {
+    // ---- V where not every row sees the whole tile, and results: thread = position, then row ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_OUT));
+    const int r = tid & (PT_M - 1), tok_r = r / a.G, g = r - tok_r * a.G;
+    const u32 tl = static_cast<u32>((wid & 3) * 32) << 16;
+    unsigned char* mine = out_s + (wid - PT_W_OUT) * C::OUT;
+    bool ok = true;
+    int T = 0;
+    u32 turn = 0, o_turn = 0;                             // of each stage's vx, and of the row tiles' o
+    for (int t = 0;; ++t) {
+      ok = __all_sync(FULL, item_at(t));
+      const PtItem& it = ring[t % PT_RING];
+      if (!ok || it.h < 0) break;
+      for (int j = 0; j < it.n; ++j) {
+        if (j >= it.w0 && j < it.w1) continue;
+        const int st = (T + j) % ST;
+        ok = __all_sync(FULL, pt_wait(&bars.vx[st], turn >> st & 1, &gone, p.status));
+        if (!ok) break;
+        turn ^= 1u << st;
+#pragma unroll
+        for (int sl = 0; sl < C::SLABS; ++sl) {
+          uint4* row = reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (PT_N * 128) + r * 128);
+          u32 worst = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 w = row[(c + r) & 7];             // (eight rows meet eight different chunks)
+            worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
+          }
+          if ((worst & 0x7f80u) == 0x7f80u || (worst & 0x7f800000u) == 0x7f800000u) {
+            for (int c = 0; c < 8; ++c) {
+              uint4 w = row[c];
+              u32* e = &w.x;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if ((e[i] & 0x7f80u) == 0x7f80u) e[i] &= 0xffff0000u;
+                if ((e[i] & 0x7f800000u) == 0x7f800000u) e[i] &= 0x0000ffffu;
+              }
+              row[c] = w;
+            }
+            odd = 1;
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&bars.vc[st]);
       }
       T += it.n;
       if (!ok) break;
-      if (j1 > j0) {
-        ok = __all_sync(FULL, tc_wait(&bars.o[X], O & 1, &gone, p.status));
+#pragma unroll 1
+      for (int X = 0; X < 2; ++X) {
+        if (it.j1[X] <= it.j0[X]) continue;
+        ok = __all_sync(FULL, pt_wait(&bars.o[X], o_turn >> X & 1, &gone, p.status));
         if (!ok) break;
-        ++O;
         tc_fence_after();
-        // ---- out ----
-        const bool live = sp.y > sp.x;
-        const float inv = 1.f / l;                        // (0 / 0 where every score is -inf: NaN)
-        uint16_t* out = p.o + static_cast<int64_t>(it.tok + X * a.TT + tok_r) * p.o_tok +
-                        static_cast<int64_t>(it.h * a.G + g) * p.o_head;
+        const u32 to = tm_o + X * DP + tl;
+        const float inv = 1.f / sums[o_turn >> X & 1][X][r];   // (0 / 0 where every score is -inf: NaN)
+        o_turn ^= 1u << X;
+        const int2 sp = r < a.TT * a.G ? span[t % PT_RING][X * a.TT + tok_r] : make_int2(0, 0);
+        uint16_t* out = sp.y > sp.x ? p.o + static_cast<int64_t>(it.tok + X * a.TT + tok_r) * p.o_tok +
+                                          static_cast<int64_t>(it.h * a.G + g) * p.o_head
+                                    : nullptr;
         const bool look = odd;
+        u32 w[DP / 2];                                    // the row, rounded: O may be written again before it is stored
 #pragma unroll
         for (int c = 0; c < DP; c += 32) {
           float o[32];
           tc_ld32(to + c, o);
           tc_wait_ld();
           if (look) {
-            // what was put to 0, in the tiles that not every row sees whole
-            for (int j = j0; j < j1; ++j) {
-              if (seen_whole(it, j)) continue;
-              const int y1 = min(x1, (j + 1) * PT_N);
-              for (int y = max(x0, j * PT_N); y < y1; ++y) {
-                const uint16_t* v = p.v + static_cast<int64_t>(it.base + y) * p.v_tok + it.h * p.v_head + c;
+            float z[32];                                  // (a copy: only this is in memory)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float z = c + i < p.D ? bf16_lo(v[i]) : 0.f;
-                  if (!(fabsf(z) < INFINITY)) o[i] += z;
-                }
-              }
-            }
+            for (int i = 0; i < 32; ++i) z[i] = o[i];
+            add_odd(p, it, X, sp.x - it.base, sp.y - it.base, c, z);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = z[i];
           }
-          if (live) {
-            u32 w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
-              w[i] = *reinterpret_cast<const u32*>(&b);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              if (c + i >= p.D) break;
-              if (a.out16) {
-                *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) out[c + i + k] = static_cast<uint16_t>(w[i / 2 + k / 2] >> (k & 1 ? 16 : 0));
-              }
-            }
+          for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+            w[c / 2 + i] = *reinterpret_cast<const u32*>(&b);
           }
         }
         tc_fence_before();
-        mbar_arrive(&bars.of[X]);                         // O may be written again
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.ite[t & 1]);
-    }
-    tc_wait_st();                                         // (weights of a tile that was given up)
-    tc_fence_before();
-  } else if (wid < PT_SM / 32 + 2) {
-    // ---- loads: one lane each for Q and K, and for V ----
-    if (lane == 0) {
-      const bool kq = wid == PT_SM / 32;
-      u64 *full = kq ? bars.kf : bars.vf, *empty = kq ? bars.ke : bars.ve;
-      const CUtensorMap* map = kq ? &kmap : &vmap;
-      const u32 dst = kq ? k_a : v_a;
-      int T = 0, t = 0;                                   // tiles and items on their way
-      bool ok = true;
-      while (ok && item_at(t) && ring[t & 1].h >= 0) {
-        const PtItem it = ring[t & 1];
-        if (kq) {
-          if (t > 0 && !tc_wait(&bars.qe, (t - 1) & 1, &gone, p.status)) break;
-          const bool two = it.j1[1] > it.j0[1], one = it.j1[0] > it.j0[0];
-          mbar_expect_tx(&bars.q, ((one ? 1 : 0) + (two ? 1 : 0)) * C::SLABS * 128 * a.G * a.TT);
+        mbar_arrive(&bars.of[X]);
+        if (!a.out16) {
+          if (out) {
 #pragma unroll
-          for (int X = 0; X < 2; ++X)
-            if (X ? two : one)
-              for (int x = 0; x < C::SLABS; ++x)
-                tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q, x * 64, it.h * a.G, it.tok + X * a.TT);
+            for (int i = 0; i < DP; ++i)
+              if (i < p.D) out[i] = static_cast<uint16_t>(w[i / 2] >> (i & 1 ? 16 : 0));
+          }
+          continue;
         }
-        ++t;
-        for (int j = 0; j < it.n; ++j, ++T) {
-          const int st = T % ST;
-          ok = T < ST || tc_wait(&empty[st], ((T / ST) & 1) ^ 1, &gone, p.status);
+        // 32 dims at a time through shared memory, so that a warp stores 64 bytes of 8 rows at once (a lane a row
+        // takes 32 lines a store)
+        uint16_t* at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = reinterpret_cast<uint16_t*>(shfl64(reinterpret_cast<u64>(out), i * 8 + lane / 4));
+#pragma unroll
+        for (int c = 0; c < DP; c += 32) {
+          __syncwarp();                                   // the 32 dims before have been read
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(mine + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
+                make_uint4(w[c / 2 + 4 * i], w[c / 2 + 4 * i + 1], w[c / 2 + 4 * i + 2], w[c / 2 + 4 * i + 3]);
+          __syncwarp();
+          const int d = c + lane % 4 * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + lane / 4;
+            const uint4 x = *reinterpret_cast<const uint4*>(mine + row * 64 + ((lane % 4 ^ (row >> 1 & 3)) << 4));
+            if (at[i] && d < p.D) *reinterpret_cast<uint4*>(at[i] + d) = x;
+          }
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.ite[t % PT_RING]);
+    }
+    tc_fence_before();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_REST));
+    if (wid == PT_W_LOAD) {
+    // ---- loads: one lane ----
+    if (lane == 0) {
+      int T = 0;                                          // tiles of K and V on their way
+      u32 q_turn = 0, q_some = 0;                         // of the row tiles' Q, bit X, and whether there was one
+      u32 whole = 0, look = 0, kind = 0;                  // turns of each stage's vf and vx, and whether vx was the last
+      bool ok = true;
+      for (int t = 0; ok && item_at(t) && ring[t % PT_RING].h >= 0; ++t) {
+        const PtItem& it = ring[t % PT_RING];
+        const int n = it.n, h = it.h, base = it.base, w0 = it.w0, w1 = it.w1;
+        for (int X = 0; X < 2; ++X) {
+          if (it.j1[X] <= it.j0[X]) continue;
+          ok = !(q_some >> X & 1) || pt_wait(&bars.qe[X], (q_turn >> X & 1) ^ 1, &gone, p.status);
           if (!ok) break;
-          mbar_expect_tx(&full[st], C::TB);
+          mbar_expect_tx(&bars.q[X], C::SLABS * 128 * a.G * a.TT);
           for (int x = 0; x < C::SLABS; ++x)
-            tma_load3(dst + st * C::TB + x * PT_N * 128, map, &full[st], x * 64, it.h, it.base + j * PT_N);
+            tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, it.tok + X * a.TT);
+          q_turn ^= 1u << X;
+          q_some |= 1u << X;
         }
-        if (ok) mbar_arrive(&bars.ite[(t - 1) & 1]);
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = T % ST;
+          const u32 free_turn = ((T / ST) & 1) ^ 1;
+          ok = T < ST || pt_wait(&bars.ke[st], free_turn, &gone, p.status);
+          if (!ok) break;
+          mbar_expect_tx(&bars.kf[st], C::TB);
+          for (int x = 0; x < C::SLABS; ++x)
+            tma_load3(k_a + st * C::TB + x * PT_N * 128, &kmap, &bars.kf[st], x * 64, h, base + j * PT_N);
+          const bool odd_tile = j < w0 || j >= w1;
+          u64* bar = odd_tile ? &bars.vx[st] : &bars.vf[st];
+          ok = T < ST || pt_wait(&bars.ve[st], free_turn, &gone, p.status);
+          if (ok) {
+            mbar_expect_tx(bar, C::TB);
+            for (int x = 0; x < C::SLABS; ++x)
+              tma_load3(v_a + st * C::TB + x * PT_N * 128, &vmap, bar, x * 64, h, base + j * PT_N);
+            if (odd_tile) look ^= 1u << st;
+            else whole ^= 1u << st;
+            kind = (kind & ~(1u << st)) | (odd_tile ? 1u << st : 0u);
+          }
+          ++T;
+        }
+        if (ok) mbar_arrive(&bars.ite[t % PT_RING]);
       }
       // no copy is in flight when the CTA ends, also where it gave up: the last ones have landed
-      for (int j = max(0, T - ST); j < T; ++j) mbar_wait(&full[j % ST], (j / ST) & 1, 1u << 16);
-      if (kq && t > 0) mbar_wait(&bars.q, (t - 1) & 1, 1u << 16);
+      for (int x = max(0, T - ST); x < T; ++x) {
+        const int st = x % ST;
+        mbar_wait(&bars.kf[st], (x / ST) & 1, 1u << 16);
+        mbar_wait(kind >> st & 1 ? &bars.vx[st] : &bars.vf[st], ((kind >> st & 1 ? look : whole) >> st & 1) ^ 1, 1u << 16);
+      }
+      for (int X = 0; X < 2; ++X)
+        if (q_some >> X & 1) mbar_wait(&bars.q[X], (q_turn >> X & 1) ^ 1, 1u << 16);
     }
     __syncwarp();
-  } else if (wid == PT_SM / 32 + 2) {
-    // ---- products: one elected thread waits and issues ----
+    } else if (wid < PT_W_MMA + 2) {
+    // ---- products: a warp a row tile, of which one thread waits and issues.  The scores of the next tile, be it the
+    // next item's first, follow the product with V ----
     if (elect_one()) {
-      const u64 dq = tc_desc(q_a, 16), dk = tc_desc(k_a, 16), dv = tc_desc(v_a, PT_N * 128);
-      int T = 0, S[2] = {0, 0}, O[2] = {0, 0};            // K/V tiles; score tiles and items of a row tile
-      bool ok = true;
-      for (int t = 0; ok && item_at(t) && ring[t & 1].h >= 0; ++t) {
-        const PtItem it = ring[t & 1];
-        auto on = [&](int X, int j) { return j >= it.j0[X] && j < it.j1[X]; };
-        auto scores = [&](int X, int j) {                 // S of the row tile over the item's tile j
-          const u64 d = dk + static_cast<u64>((T + j) % ST * (C::TB >> 4)), e = dq + static_cast<u64>(X * (C::QB >> 4));
+      const int X = wid - PT_W_MMA;
+      const u32 dq = static_cast<u32>(tc_desc(q_a + X * C::QB, 16)), dk = static_cast<u32>(tc_desc(k_a, 16)),
+                dv = static_cast<u32>(tc_desc(v_a, PT_N * 128)), ts = tm_s + X * PT_N, to = tm_o + X * DP;
+      u32 p_turn = 0, o_turn = 1, q_turn = 0;             // of the row tile's barriers
+      u32 whole = 0, look = 0;                            // and of each stage's vf and vc
+      auto wait = [&](u64* bar, u32 parity) { return pt_wait(bar, parity, &gone, p.status); };
+      // What S of the row tile over tile j of an item, the ring's tile `at`, needs; the steps it takes.
+      auto ready = [&](const PtItem& i, int j, int at, int& steps, bool& last) {
+        const int j0 = i.j0[X], j1 = i.j1[X];
+        const bool on = j >= j0 && j < j1;
+        steps = on ? steps_of(i.y1[X], j) : 0;
+        last = j + 1 == j1;
+        if (on && j == j0) {
+          if (!wait(&bars.q[X], q_turn)) return false;
+          q_turn ^= 1;
+        }
+        return wait(&bars.kf[at % ST], (at / ST) & 1);
+      };
+      // S; its K, and after the item's last its Q, may be loaded again.
+      auto scores = [&](int at, int steps, bool last) {
+        const int st = at % ST;
+        const u32 d = dk + st * (C::TB >> 4);
+        if (steps == 0) {
+          mbar_arrive(&bars.ke[st]);
+          return;
+        }
+        if (steps == PT_N / 16) {
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k)
-            tc_mma_ss(tm_s + X * PT_N, e + (((k >> 2) * (PT_M * 128) + (k & 3) * 32) >> 4),
-                      d + (((k >> 2) * (PT_N * 128) + (k & 3) * 32) >> 4), tc_idesc(PT_N, false), k > 0);
-          tc_commit(&bars.s[X]);
-        };
-        auto k_done = [&](int j) {                        // both row tiles' S of tile j are issued
-          tc_commit(&bars.ke[(T + j) % ST]);
-          if (j + 1 == it.n) tc_commit(&bars.qe);
-        };
-        ok = tc_wait(&bars.q, t & 1, &gone, p.status) && tc_wait(&bars.kf[T % ST], (T / ST) & 1, &gone, p.status);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int X = 0; X < 2; ++X)
-          if (on(X, 0)) scores(X, 0);
-        k_done(0);
-        for (int j = 0; j < it.n; ++j) {
-          const int st = (T + j) % ST;
-          ok = tc_wait(&bars.vf[st], ((T + j) / ST) & 1, &gone, p.status);
-#pragma unroll
-          for (int X = 0; X < 2; ++X) {
-            if (!ok) break;
-            if (on(X, j)) {
-              // the item before has read its O
-              if (j == it.j0[X] && O[X] > 0) ok = tc_wait(&bars.of[X], (O[X] - 1) & 1, &gone, p.status);
-              ok = ok && tc_wait(&bars.p[X], S[X] & 1, &gone, p.status);
-              if (!ok) break;
-              ++S[X];
-              tc_fence_after();
-              const u64 d = dv + static_cast<u64>(st * (C::TB >> 4));
-#pragma unroll
-              for (int k = 0; k < PT_N / 16; ++k)
-                tc_mma_ts(tm_o + X * DP, tm_s + X * PT_N + k * 8, d + (k * 2048 >> 4), tc_idesc(DP, true),
-                          j > it.j0[X] || k > 0);
-              if (j + 1 == it.j1[X]) {
-                tc_commit(&bars.o[X]);
-                ++O[X];
-              }
-            }
-            if (j + 1 < it.n) {
-              if (X == 0) {
-                ok = tc_wait(&bars.kf[(T + j + 1) % ST], ((T + j + 1) / ST) & 1, &gone, p.status);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              if (on(X, j + 1)) scores(X, j + 1);
-            }
+          for (int k = 0; k < DP / 16; ++k) {
+            const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
+            tc_mma_ss_at(ts, dq + in, d + in, tc_idesc(PT_N, false), k > 0);
           }
-          if (!ok) break;
-          tc_commit(&bars.ve[st]);
-          if (j + 1 < it.n) k_done(j + 1);
+        } else {
+          const u32 what = tc_idesc(steps * 16, false);
+#pragma unroll 1
+          for (int k = 0; k < DP / 16; ++k) {
+            const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
+            tc_mma_ss_at(ts, dq + in, d + in, what, k > 0);
+          }
+        }
+        tc_commit(&bars.s[X]);
+        tc_commit(&bars.ke[st]);
+        if (last) tc_commit(&bars.qe[X]);
+      };
+      int at = 0, t = 0, j = 0, n_steps = 0;
+      bool n_last = false;
+      const PtItem* it = &ring[0];
+      bool ok = item_at(0), more = ok && it->h >= 0;
+      if (more) {
+        ok = ready(*it, 0, 0, n_steps, n_last);
+        if (ok) scores(0, n_steps, n_last);
+      }
+      while (ok && more) {
+        const int st = at % ST, steps = n_steps, nj = j + 1 < it->n ? j + 1 : 0;
+        const bool last = n_last, first = j == it->j0[X];
+        if (j >= it->w0 && j < it->w1) {
+          ok = wait(&bars.vf[st], whole >> st & 1);
+          whole ^= 1u << st;
+        } else {
+          ok = wait(&bars.vc[st], look >> st & 1);
+          look ^= 1u << st;
         }
         if (!ok) break;
-        T += it.n;
-        mbar_arrive(&bars.ite[t & 1]);
+        const u32 d = dv + st * (C::TB >> 4);
+        if (steps > 0) {
+          if (first) {                                    // the item before has been read
+            if (!(ok = wait(&bars.of[X], o_turn))) break;
+            o_turn ^= 1;
+          }
+          if (!(ok = wait(&bars.p[X][0], p_turn))) break;
+          tc_fence_after();
+          if (steps == PT_N / 16) {
+#pragma unroll
+            for (int k = 0; k < PT_N / 32; ++k)
+              tc_mma_ts_at(to, ts + k * 8, d + k * (2048 >> 4), tc_idesc(DP, true), k > 0 || !first ? 1u : 0u);
+          }
+        }
+        const PtItem* next = it;
+        if (nj == 0) {
+          if (!(ok = item_at(t + 1))) break;
+          next = &ring[(t + 1) % PT_RING];
+          more = next->h >= 0;
+        }
+        if (more && !(ok = ready(*next, nj, at + 1, n_steps, n_last))) break;
+        if (steps > 0) {
+          if (!(ok = wait(&bars.p[X][1], p_turn))) break;
+          p_turn ^= 1;
+          tc_fence_after();
+          if (steps == PT_N / 16) {
+#pragma unroll
+            for (int k = PT_N / 32; k < PT_N / 16; ++k) tc_mma_ts_at(to, ts + k * 8, d + k * (2048 >> 4), tc_idesc(DP, true), 1u);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k)
+              tc_mma_ts_at(to, ts + k * 8, d + k * (2048 >> 4), tc_idesc(DP, true), k > 0 || !first ? 1u : 0u);
+          }
+          tc_commit(&bars.ve[st]);                        // V may be loaded again
+          if (last) tc_commit(&bars.o[X]);
+        } else {
+          mbar_arrive(&bars.ve[st]);
+        }
+        if (more) scores(at + 1, n_steps, n_last);
+        if (nj == 0) {
+          mbar_arrive(&bars.ite[t % PT_RING]);
+          ++t;
+        }
+        it = next;
+        j = nj;
+        ++at;
       }
       // the products in flight read shared memory and TMEM: all are done before either goes, also where the CTA gave up
       tc_commit(&bars.end);
       mbar_wait(&bars.end, 0, 1u << 16);
     }
     __syncwarp();
-  } else {
+    } else {
     // ---- items: the last tokens first, which see the most ----
     int t = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; ok && i < items + static_cast<int>(gridDim.x); i += gridDim.x) {
+    for (int i = blockIdx.x; i < items + static_cast<int>(gridDim.x); i += gridDim.x) {
       const bool last = i >= items;
-      PtItem x;
-      x.h = last ? -1 : i % p.H;
-      x.tok = last ? 0 : (a.tiles - 1 - i / p.H) * 2 * a.TT;
-      int2 sp[2 * PT_M / 32];
+      // the slot's item before is done with
+      if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p.status))) break;
+      PtItem& x = ring[t % PT_RING];
+      const int tok0 = (a.tiles - 1 - i / p.H) * 2 * a.TT;
       int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
+      for (int w = lane; w < 2 * a.TT && !last; w += 32) {
+        const int tok = tok0 + w;
+        int2 sp = tok < p.N ? request_of(p, cu, every, tok) : make_int2(0, 0);
+        if (sp.y > 0) {
+          if (p.causal) sp.y = tok + 1;
 #pragma unroll
-      for (int k = 0; k < 2 * PT_M / 32; ++k) {
-        const int w = k * 32 + lane, tok = x.tok + w;
-        sp[k] = make_int2(0, 0);
-        if (last || w >= 2 * a.TT || tok >= p.N) continue;
-        sp[k] = request_of(p, cu, every, tok);
-        if (sp[k].y <= sp[k].x) continue;
-        if (p.causal) sp[k].y = tok + 1;
-        const int X = w >= a.TT ? 1 : 0;
-        y0[X] = min(y0[X], sp[k].x);
-        y1[X] = max(y1[X], sp[k].y);
-        z0[X] = max(z0[X], sp[k].x);
-        z1[X] = min(z1[X], sp[k].y);
+          for (int X = 0; X < 2; ++X)
+            if ((w >= a.TT) == (X == 1)) {
+              y0[X] = min(y0[X], sp.x);
+              y1[X] = max(y1[X], sp.y);
+              z0[X] = max(z0[X], sp.x);
+              z1[X] = min(z1[X], sp.y);
+            }
+        }
+        span[t % PT_RING][w] = sp;
       }
 #pragma unroll
       for (int X = 0; X < 2; ++X) {
@@ -478,31 +671,38 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         z0[X] = __reduce_max_sync(FULL, z0[X]);
         z1[X] = __reduce_min_sync(FULL, z1[X]);
       }
-      x.base = min(y0[0], y0[1]);
-      x.n = 0;
+      const int base = min(y0[0], y0[1]);
+      if (!last && max(y1[0], y1[1]) == 0) continue;      // tokens of no request
+      if (lane == 0) {
+        x.h = last ? -1 : i % p.H;
+        x.tok = tok0;
+        x.base = base;
+        int n = 0, w0 = 0, w1 = INT_MAX;
 #pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        const bool some = y1[X] > 0;
-        x.j0[X] = some ? (y0[X] - x.base) / PT_N : 0;
-        x.j1[X] = some ? (y1[X] - x.base + PT_N - 1) / PT_N : 0;
-        x.f0[X] = some ? (z0[X] - x.base + PT_N - 1) / PT_N : 0;
-        x.f1[X] = some ? (z1[X] - x.base) / PT_N : 0;
-        x.n = max(x.n, x.j1[X]);
+        for (int X = 0; X < 2; ++X) {
+          const bool some = y1[X] > 0;
+          x.y1[X] = some ? y1[X] - base : 0;
+          x.j0[X] = some ? (y0[X] - base) / PT_N : 0;
+          x.j1[X] = some ? (y1[X] - base + PT_N - 1) / PT_N : 0;
+          if (some) {
+            n = max(n, (y1[X] - base + PT_N - 1) / PT_N);
+            w0 = max(w0, (z0[X] - base + PT_N - 1) / PT_N);
+            w1 = min(w1, (z1[X] - base) / PT_N);
+          }
+        }
+        x.n = n;
+        x.w0 = w0;
+        x.w1 = w1;
       }
-      if (!last && x.n == 0) continue;                    // tokens of no request
-      if (t >= 2) ok = __all_sync(FULL, tc_wait(&bars.ite[t & 1], ((t >> 1) - 1) & 1, &gone, p.status));
-      if (!ok) break;
-#pragma unroll
-      for (int k = 0; k < 2 * PT_M / 32; ++k) span[t & 1][k * 32 + lane] = sp[k];
-      if (lane == 0) ring[t & 1] = x;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.itf[t & 1]);
+      if (lane == 0) mbar_arrive(&bars.itf[t % PT_RING]);
       ++t;
+    }
     }
   }
   __syncthreads();
   tc_fence_after();
-  if (wid == PT_SM / 32 + 2)
+  if (wid == PT_W_MMA)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
 }
 
