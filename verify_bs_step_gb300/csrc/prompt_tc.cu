@@ -36,13 +36,14 @@ constexpr int PT_RING = 4;                // items on their way
 constexpr int PT_CU = 2048;               // request starts held in shared memory
 constexpr int PT_STMAX = 4;
 // registers a thread: 65,536 / 512 at launch, then the softmax threads take what the others leave
-constexpr int PT_REGS = 128, PT_REGS_SM = 176, PT_REGS_OUT = 104, PT_REGS_REST = 56;
+constexpr int PT_REGS = 128, PT_REGS_SM = 176, PT_REGS_OUT = 112, PT_REGS_REST = 48;
 static_assert(PT_SM * PT_REGS_SM + PT_OUT * PT_REGS_OUT + 128 * PT_REGS_REST <= PT_NT * PT_REGS, "registers of the block");
 
 struct PtArgs {
   PromptArgs p;
   int G, TT;                              // heads a group, tokens a row tile
   int tiles;                              // of 2 TT tokens
+  int batch, many;                        // the grid's first `many` blocks stand for `batch` items each, the others for one
   bool out16;                             // stores of 16 bytes
 };
 
@@ -59,11 +60,11 @@ template <int DP> struct PtCfg {
 // every row sees the whole tile (it has landed, has been looked through): a barrier's phases count its own uses alone, so
 // that who waits for one is never two behind.  Per row tile: q, qe (an item's Q has
 // landed, is not read any more), s (scores are done), p (the weights of half a tile are written), o (an item's sums are
-// done), of (they have been read).  itf, ite: an item is worked out, is done with.  end: every product that was issued is
-// done.
+// done), of (they have been read).  itf, ite: an item is worked out, is done with.  claim: the answer of a claim is there.
+// end: every product that was issued is done.
 struct PtBars {
   u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], q[2], qe[2], s[2], p[2][2], o[2], of[2], vx[PT_STMAX], vc[PT_STMAX], itf[PT_RING],
-      ite[PT_RING], end;
+      ite[PT_RING], claim[2], end;
 };
 
 struct PtItem {
@@ -116,6 +117,25 @@ __device__ __forceinline__ int2 request_of(const PromptArgs& a, const int* cu, i
   return s >= 0 && s <= t && e > t && e <= a.N ? make_int2(s, e) : make_int2(0, 0);
 }
 
+// Claims a block of the grid that has not started, in place of its launch (16 bytes of answer, counted by `bar`).
+__device__ __forceinline__ void claim_block(uint4* answer, u64* bar) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the answer before has been read)
+  mbar_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(smem_u32(answer)), "r"(smem_u32(bar)) : "memory");
+}
+// The claimed block, or -1.
+__device__ __forceinline__ int claimed_block(const uint4* answer) {
+  u32 got, x;
+  asm volatile("{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+               "ld.shared.b128 h, [%2];\n\t"
+               "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+               "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+               : "=r"(got), "=r"(x) : "r"(smem_u32(answer)) : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
+
 // tc_wait in little code.
 __device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone, int* status) {
 #pragma unroll 1
@@ -139,6 +159,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   __shared__ u32 tmem_base;
   __shared__ volatile int gone;
   __shared__ volatile int odd;                            // an infinity or NaN of V was put to 0 (stays so)
+  __shared__ __align__(16) uint4 claims[2];
   __shared__ PtItem ring[PT_RING];
   __shared__ int2 span[PT_RING][2 * PT_M];                // positions [x, y) of an item's tokens
   __shared__ float sums[2][2][PT_M];                      // of a row's weights, by the row tile's items in turn
@@ -150,7 +171,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   int* cu = reinterpret_cast<int*>(out_s + PT_OUT / 32 * C::OUT);
   const PromptArgs& p = a.p;
   const int every = (p.B + 1 + PT_CU - 1) / PT_CU;        // one start in `every` is held
-  const int items = a.tiles * p.H;
 
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -174,6 +194,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       mbar_init(&bars.itf[i], 1);
       mbar_init(&bars.ite[i], (PT_SM + PT_OUT) / 32 + 3);
     }
+    mbar_init(&bars.claim[0], 1);
+    mbar_init(&bars.claim[1], 1);
     mbar_init(&bars.end, 2);
     fence_mbar_init();
     gone = 0;
@@ -640,11 +662,18 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     __syncwarp();
     } else {
     // ---- items: the last tokens first, which see the most ----
-    int t = 0;
-    for (int i = blockIdx.x; i < items + static_cast<int>(gridDim.x); i += gridDim.x) {
-      const bool last = i >= items;
-      // the slot's item before is done with
+    int t = 0, c = 0, i, left;                            // this item, and how many from it on are claimed; 0: none is
+    auto take = [&](int block) {
+      i = block < a.many ? block * a.batch : a.many * a.batch + block - a.many;
+      left = block < 0 ? 0 : (block < a.many ? a.batch : 1);
+    };
+    take(blockIdx.x);
+    while (true) {
+      const bool last = left == 0;
+      // the slot's item before is done with; the next items are claimed (no earlier: another CTA may be sooner) while the
+      // last of these is worked out
       if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p.status))) break;
+      if (left == 1 && lane == 0) claim_block(&claims[c & 1], &bars.claim[c & 1]);
       PtItem& x = ring[t % PT_RING];
       const int tok0 = (a.tiles - 1 - i / p.H) * 2 * a.TT;
       int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
@@ -672,19 +701,20 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         z1[X] = __reduce_min_sync(FULL, z1[X]);
       }
       const int base = min(y0[0], y0[1]);
-      if (!last && max(y1[0], y1[1]) == 0) continue;      // tokens of no request
-      if (lane == 0) {
-        x.h = last ? -1 : i % p.H;
+      const int h = last ? -1 : i % p.H;
+      const bool some = max(y1[0], y1[1]) > 0;            // (else: tokens of no request)
+      if ((some || last) && lane == 0) {
+        x.h = h;
         x.tok = tok0;
         x.base = base;
         int n = 0, w0 = 0, w1 = INT_MAX;
 #pragma unroll
         for (int X = 0; X < 2; ++X) {
-          const bool some = y1[X] > 0;
-          x.y1[X] = some ? y1[X] - base : 0;
-          x.j0[X] = some ? (y0[X] - base) / PT_N : 0;
-          x.j1[X] = some ? (y1[X] - base + PT_N - 1) / PT_N : 0;
-          if (some) {
+          const bool on = y1[X] > 0;
+          x.y1[X] = on ? y1[X] - base : 0;
+          x.j0[X] = on ? (y0[X] - base) / PT_N : 0;
+          x.j1[X] = on ? (y1[X] - base + PT_N - 1) / PT_N : 0;
+          if (on) {
             n = max(n, (y1[X] - base + PT_N - 1) / PT_N);
             w0 = max(w0, (z0[X] - base + PT_N - 1) / PT_N);
             w1 = min(w1, (z1[X] - base) / PT_N);
@@ -695,8 +725,22 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         x.w1 = w1;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.itf[t % PT_RING]);
-      ++t;
+      if (some || last) {
+        if (lane == 0) mbar_arrive(&bars.itf[t % PT_RING]);
+        ++t;
+      }
+      if (last) break;
+      if (left > 1) {
+        ++i;
+        --left;
+      } else {
+        if (!__all_sync(FULL, pt_wait(&bars.claim[c & 1], c >> 1 & 1, &gone, p.status))) {
+          mbar_wait(&bars.claim[c & 1], c >> 1 & 1, 1u << 16);   // (the answer is in flight)
+          break;
+        }
+        take(claimed_block(&claims[c & 1]));
+        ++c;
+      }
     }
     }
   }
@@ -733,12 +777,10 @@ bool prompt_tc_takes(const PromptArgs& p) {
 }
 
 template <int DP>
-static int launch_tc(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PtArgs& a, int num_sms,
-                     cudaStream_t s) {
+static int launch_tc(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PtArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   if (!smem_attr_once(prompt_tc_kernel<DP>, static_cast<int>(PtCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
-  const int grid = std::min(a.tiles * a.p.H, num_sms);
-  prompt_tc_kernel<DP><<<grid, PT_NT, PtCfg<DP>::SMEM, s>>>(qm, km, vm, a);
+  prompt_tc_kernel<DP><<<a.tiles * a.p.H - a.many * (a.batch - 1), PT_NT, PtCfg<DP>::SMEM, s>>>(qm, km, vm, a);
   return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
 }
 
@@ -748,9 +790,14 @@ int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
   if (!encode(&qm, p.q, p, p.Hq, p.q_tok, p.q_head, G, TT) || !encode(&km, p.k, p, p.H, p.k_tok, p.k_head, 1, PT_N) ||
       !encode(&vm, p.v, p, p.H, p.v_tok, p.v_head, 1, PT_N))
     return VBS_ECUDA;
-  const PtArgs a{p, G, TT, (p.N + 2 * TT - 1) / (2 * TT),
+  const int64_t tiles = (static_cast<int64_t>(p.N) + 2 * TT - 1) / (2 * TT), items = tiles * p.H;
+  if (items >= int64_t{1} << 31) return VBS_EINVAL;
+  // the GPU answers some 15 claims a microsecond: many items are claimed several at a time, the last quarter one by one
+  const int batch = static_cast<int>(std::max<int64_t>(1, items / (16 * num_sms)));
+  const int many = batch > 1 ? static_cast<int>(items * 3 / 4 / batch) : 0;
+  const PtArgs a{p, G, TT, static_cast<int>(tiles), batch, many,
                  (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && (p.o_tok | p.o_head) % 8 == 0};
-  return p.D <= 64 ? launch_tc<64>(qm, km, vm, a, num_sms, s) : launch_tc<128>(qm, km, vm, a, num_sms, s);
+  return p.D <= 64 ? launch_tc<64>(qm, km, vm, a, s) : launch_tc<128>(qm, km, vm, a, s);
 }
 
 }  // namespace vbs
