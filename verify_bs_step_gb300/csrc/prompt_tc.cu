@@ -35,8 +35,12 @@ constexpr int PT_W_OUT = PT_SM / 32, PT_W_LOAD = PT_W_OUT + PT_OUT / 32, PT_W_MM
 constexpr int PT_RING = 4;                // items on their way
 constexpr int PT_CU = 2048;               // request starts held in shared memory
 constexpr int PT_STMAX = 4;
+// Items of this many tiles and more: the row tiles' products go in turn, so that one's run while the other's softmax
+// does.  Left alone both fall into step and wait together (16001 tokens: 1605 us alone, 1432 in turn; 64 x 1000, whose
+// items have up to 9 tiles: 588 and 592; 128 sentences up to 256: 51 and 53).
+constexpr int PT_TURNS = 12;
 // registers a thread: 65,536 / 512 at launch, then the softmax threads take what the others leave
-constexpr int PT_REGS = 128, PT_REGS_SM = 176, PT_REGS_OUT = 112, PT_REGS_REST = 48;
+constexpr int PT_REGS = 128, PT_REGS_SM = 168, PT_REGS_OUT = 104, PT_REGS_REST = 72;
 static_assert(PT_SM * PT_REGS_SM + PT_OUT * PT_REGS_OUT + 128 * PT_REGS_REST <= PT_NT * PT_REGS, "registers of the block");
 
 struct PtArgs {
@@ -60,10 +64,10 @@ template <int DP> struct PtCfg {
 // every row sees the whole tile (it has landed, has been looked through): a barrier's phases count its own uses alone, so
 // that who waits for one is never two behind.  Per row tile: q, qe (an item's Q has
 // landed, is not read any more), s (scores are done), p (the weights of half a tile are written), o (an item's sums are
-// done), of (they have been read).  itf, ite: an item is worked out, is done with.  claim: the answer of a claim is there.
+// done), of (they have been read), go (it is its turn to issue).  itf, ite: an item is worked out, is done with.  claim: the answer of a claim is there.
 // end: every product that was issued is done.
 struct PtBars {
-  u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], q[2], qe[2], s[2], p[2][2], o[2], of[2], vx[PT_STMAX], vc[PT_STMAX], itf[PT_RING],
+  u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], q[2], qe[2], s[2], p[2][2], o[2], of[2], vx[PT_STMAX], vc[PT_STMAX], go[2], itf[PT_RING],
       ite[PT_RING], claim[2], end;
 };
 
@@ -101,20 +105,27 @@ __device__ __forceinline__ void tma_load3(u32 dst, const CUtensorMap* map, u64* 
       ::"r"(dst), "l"(map), "r"(x), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
-// request_of with one start in `every` at hand, in shared memory.
-__device__ __forceinline__ int2 request_of(const PromptArgs& a, const int* cu, int every, int t) {
-  int lo = 0, hi = a.B / every + 1;       // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (cu[m] <= t) lo = m;
-    else hi = m;
+// The last request that starts at or before token t, or 0, by a converged warp; one start in `every` is at hand in shared
+// memory.
+__device__ __forceinline__ int request_before(const PromptArgs& a, const int* cu, int every, int t, int lane) {
+  int lo = 0, n = a.B / every + 1;        // it is among the n held from lo on: the last of them not above t
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const u32 below = __ballot_sync(FULL, at < n && cu[lo + at] <= t);
+    const int k = max(0, 31 - __clz(below)) * step;
+    lo += k;
+    n = min(step, n - k);
   }
   int b = lo * every;
   if (every > 1)
-    while (b < a.B && b < lo * every + every && a.cu[b + 1] <= t) ++b;
+    while (b < a.B && b < lo * every + every - 1 && a.cu[b + 1] <= t) ++b;
+  return b;
+}
+// Request b's first token and its end; 0, 0 where it is not within the tokens.
+__device__ __forceinline__ int2 request_at(const PromptArgs& a, const int* cu, int every, int b) {
   if (b >= a.B) return make_int2(0, 0);
   const int s = every == 1 ? cu[b] : a.cu[b], e = every == 1 ? cu[b + 1] : a.cu[b + 1];
-  return s >= 0 && s <= t && e > t && e <= a.N ? make_int2(s, e) : make_int2(0, 0);
+  return s >= 0 && s < e && e <= a.N ? make_int2(s, e) : make_int2(0, 0);
 }
 
 // Claims a block of the grid that has not started, in place of its launch (16 bytes of answer, counted by `bar`).
@@ -140,7 +151,7 @@ __device__ __forceinline__ int claimed_block(const uint4* answer) {
 __device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone, int* status) {
 #pragma unroll 1
   for (u32 i = 0; !mbar_wait(bar, parity, 1); ++i)
-    if (i >= TC_SPIN || *gone) {
+    if (__builtin_expect(i >= TC_SPIN || *gone, 0)) {
       *gone = 1;
       set_status(status, VBS_ETIMEOUT);
       return false;
@@ -183,6 +194,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q[i], 1);
+      mbar_init(&bars.go[i], 1);
       mbar_init(&bars.qe[i], 1);
       mbar_init(&bars.s[i], 1);
       mbar_init(&bars.p[i][0], PT_M);
@@ -237,129 +249,114 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       // counted from the item's first position; rows that are not there see all of it (they are not written)
       const int x0 = sp.y > 0 ? sp.x - it.base : 0, x1 = sp.y > 0 ? sp.y - it.base : INT_MAX / 2;
       const int j0 = it.j0[X], j1 = it.j1[X];
-      // the reference and the largest score so far (in scaled units), the sum of weights
-      float m = 0.f, top = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;                       // the reference (in scaled units), the sum of weights
       for (int j = j0; j < j1; ++j, ++S) {
         const int from = x0 - j * PT_N, left = x1 - j * PT_N;
         ok = __all_sync(FULL, pt_wait(&bars.s[X], S & 1, &gone, p.status));
         if (!ok) break;
         tc_fence_after();
+        // (the code of a tile is kept short, in loops over its halves: of several warps' long code one pushes the other's
+        // out of the instruction cache, tile by tile)
         if (__any_sync(FULL, from > 0 || left < PT_N) || neg) {
           // scores that a row does not see become -inf where they stand (and all change their sign under a negative
-          // scale), 32 at a time where there are such, in little code: it is fetched anew every time
+          // scale), where there are such
           const int least = __reduce_min_sync(FULL, left), late = __reduce_max_sync(FULL, from);
 #pragma unroll 1
-          for (int c = 0; c < PT_N; c += 32) {
-            if (least >= c + 32 && late <= c && !neg) continue;
+          for (int c = 0; c < PT_N; c += 16) {
+            if (least >= c + 16 && late <= c && !neg) continue;
             const int lo = max(0, from - c), hi = left - c;
-            u32 see = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
-            see = lo >= 32 ? 0u : see & (~0u << lo);
-            float x[32];
-            tc_ld32(ts + c, x);
+            u32 see = hi >= 16 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+            see = lo >= 16 ? 0u : see & (~0u << lo);
+            float x[16];
+            tc_ld16(ts + c, x);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = see >> i & 1u ? (neg ? -x[i] : x[i]) : -INFINITY;
-            tc_st32(ts + c, x);
+            for (int i = 0; i < 16; ++i) x[i] = see >> i & 1u ? (neg ? -x[i] : x[i]) : -INFINITY;
+            tc_st16(ts + c, x);
           }
           tc_wait_st();
         }
-        // sixteen pairs of weights relative to the reference, and their sum
-        auto weights = [](const float* s, u64 f2, u64 r2, u64 (&sum)[2], float (&pk)[16]) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x, y;
-            unpair(fma2(pair(s[2 * i], s[2 * i + 1]), f2, r2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            sum[i & 1] = add2(sum[i & 1], pair(x, y));
-            __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
-            pk[i] = *reinterpret_cast<float*>(&w);
-          }
-        };
-        // a reference that the largest score is within 2^16 of will do
-        auto strays = [&](float t) { return t > m + 16.f || (t < m - 16.f && t > -INFINITY) || fabsf(m) > 65536.f; };
-        u64 sum[2] = {0, 0};
-        float t_max;
-        bool handed;                                      // the weights are there
-        {
-          float s[PT_N];
-#pragma unroll
-          for (int c = 0; c < PT_N; c += 32) tc_ld32(ts + c, s + c);
-          tc_wait_ld();
-          // the first half's weights are worked out with the reference as it is, beside the tile's maximum
-          float pk[2][16];
-          const u64 f2 = pair(sc, sc), r2 = pair(-m, -m);
-          weights(s, f2, r2, sum, pk[0]);
-          weights(s + 32, f2, r2, sum, pk[1]);
-          float x[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
-#pragma unroll
-          for (int i = 8; i < PT_N; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
-          t_max = fmaxf(top, max3(fmaxf(x[0], x[1]), x[2], x[3]) * sc);
-          handed = !__any_sync(FULL, strays(t_max));
-          if (handed) {
-            tc_st16(ts, pk[0]);                           // the weights stand where scores were
-            tc_st16(ts + 16, pk[1]);
-            weights(s + 64, f2, r2, sum, pk[0]);
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars.p[X][0]);
-            tc_st16(ts + 32, pk[0]);
-            weights(s + 96, f2, r2, sum, pk[1]);
-            tc_st16(ts + 48, pk[1]);
-          }
-        }
-        if (!handed) {
-          const bool move = strays(t_max) && t_max != m;
-          if (__any_sync(FULL, move)) {
-            const float to_m = move && t_max > -INFINITY ? t_max : m;
-            const float corr = to_m == m ? 1.f : (top == -INFINITY ? 0.f : ex2(m - to_m));
-            if (j > j0) {
-              // O holds the tiles before (S of this one was issued after their products, and is done)
+        float mx = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < DP; c += 16) {
-                float o[16];
-                tc_ld16(to + c, o);
-                tc_wait_ld();
+        for (int c = 0; c < PT_N; c += 64) {
+          float s[64];
+          tc_ld32(ts + c, s);
+          tc_ld32(ts + c + 32, s + 32);
+          tc_wait_ld();
+          float x[4] = {mx, fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5])};
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
-                tc_st16(to + c, o);
-              }
+          for (int i = 6; i < 64; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
+          mx = max3(fmaxf(x[0], x[1]), x[2], x[3]);
+        }
+        mx *= sc;
+        float f = sc;
+        const bool grow = mx > m + 8.f;                   // also in a row's first tile: m = -inf
+        if (__any_sync(FULL, grow || fabsf(m) > 65536.f)) {
+          const float to_m = grow ? mx : m, corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to_m)) : 1.f;
+          if (j > j0) {
+            // O holds the tiles before (S of this one was issued after their products, and is done)
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              float o[16];
+              tc_ld16(to + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) unpair(mul2(pair(o[i], o[i + 1]), pair(corr, corr)), o[i], o[i + 1]);
+              tc_st16(to + c, o);
             }
-            l *= corr;
-            m = to_m;
           }
+          l *= corr;
+          m = to_m;
           // scale and reference go into one fma, whose product is not rounded as the reference was: for
           // large scores the difference is more than a weight can bear, and the product is rounded first
-          const bool large = __any_sync(FULL, fabsf(m) > 65536.f);
-          const float f = large ? 1.f : sc;
-          const u64 f2 = pair(f, f), r2 = pair(-m, -m);
-          sum[0] = sum[1] = 0;
+          if (__any_sync(FULL, fabsf(m) > 65536.f && m > -INFINITY)) {
+            f = 1.f;
 #pragma unroll 1
-          for (int c = 0; c < PT_N; c += 32) {
-            float s[32], pk[16];
-            tc_ld32(ts + c, s);
-            tc_wait_ld();
-            if (large) {
+            for (int c = 0; c < PT_N; c += 16) {
+              float o[16];
+              tc_ld16(ts + c, o);
+              tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] *= sc;
+              for (int i = 0; i < 16; ++i) o[i] *= sc;
+              tc_st16(ts + c, o);
             }
-            weights(s, f2, r2, sum, pk);
-            if (c == PT_N / 2) {
-              tc_wait_st();
-              tc_fence_before();
-              mbar_arrive(&bars.p[X][0]);
-            }
-            tc_st16(ts + c / 2, pk);
           }
+          tc_wait_st();
         }
-        top = t_max;
-        float l0, l1;
-        unpair(add2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
-        if (j + 1 == j1) sums[O & 1][X][r] = l;
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars.p[X][1]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
+        u64 sum[2] = {0, 0};
+#pragma unroll 1
+        for (int c = 0; c < PT_N; c += 64) {
+          float s[64];
+          tc_ld32(ts + c, s);
+          tc_ld32(ts + c + 32, s + 32);
+          tc_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            float pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x, y;
+              unpair(fma2(pair(s[h + 2 * i], s[h + 2 * i + 1]), f2, r2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum[i & 1] = add2(sum[i & 1], pair(x, y));
+              __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
+              pk[i] = *reinterpret_cast<float*>(&w);
+            }
+            tc_st16(ts + (c + h) / 2, pk);                // the weights stand where scores were
+          }
+          if (c == 64) {
+            float l0, l1;
+            unpair(add2(sum[0], sum[1]), l0, l1);
+            l += l0 + l1;
+            if (j + 1 == j1) sums[O & 1][X][r] = l;
+          }
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars.p[X][c >> 6]);
+        }
       }
       if (!ok) break;
       if (j1 > j0) ++O;
@@ -369,22 +366,24 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     tc_wait_st();                                         // (weights of a tile that was given up)
     tc_fence_before();
   } else if (wid < PT_W_LOAD) {
-    // ---- V where not every row sees the whole tile, and results: thread = position, then row ----
+    // ---- V where not every row sees the whole tile (thread = position), and results (thread = row) ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_OUT));
     const int r = tid & (PT_M - 1), tok_r = r / a.G, g = r - tok_r * a.G;
     const u32 tl = static_cast<u32>((wid & 3) * 32) << 16;
     unsigned char* mine = out_s + (wid - PT_W_OUT) * C::OUT;
-    bool ok = true;
-    int T = 0;
+    auto wait = [&](u64* bar, u32 parity) { return __all_sync(FULL, pt_wait(bar, parity, &gone, p.status)) != 0; };
     u32 turn = 0, o_turn = 0;                             // of each stage's vx, and of the row tiles' o
-    for (int t = 0;; ++t) {
-      ok = __all_sync(FULL, item_at(t));
+    int T = 0;
+    bool ok = true;
+    for (int t = 0; ok; ++t) {
+      if (!wait(&bars.itf[t % PT_RING], (t / PT_RING) & 1)) break;
       const PtItem& it = ring[t % PT_RING];
-      if (!ok || it.h < 0) break;
+      if (it.h < 0) break;
+#pragma unroll 1
       for (int j = 0; j < it.n; ++j) {
         if (j >= it.w0 && j < it.w1) continue;
         const int st = (T + j) % ST;
-        ok = __all_sync(FULL, pt_wait(&bars.vx[st], turn >> st & 1, &gone, p.status));
+        ok = wait(&bars.vx[st], turn >> st & 1);
         if (!ok) break;
         turn ^= 1u << st;
 #pragma unroll
@@ -393,10 +392,11 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           u32 worst = 0;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint4 w = row[(c + r) & 7];             // (eight rows meet eight different chunks)
+            const uint4 w = row[(c + r) & 7];           // (eight rows meet eight different chunks)
             worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
           }
           if ((worst & 0x7f80u) == 0x7f80u || (worst & 0x7f800000u) == 0x7f800000u) {
+#pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint4 w = row[c];
               u32* e = &w.x;
@@ -414,11 +414,10 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         mbar_arrive(&bars.vc[st]);
       }
       T += it.n;
-      if (!ok) break;
 #pragma unroll 1
-      for (int X = 0; X < 2; ++X) {
+      for (int X = 0; X < 2 && ok; ++X) {
         if (it.j1[X] <= it.j0[X]) continue;
-        ok = __all_sync(FULL, pt_wait(&bars.o[X], o_turn >> X & 1, &gone, p.status));
+        ok = wait(&bars.o[X], o_turn >> X & 1);
         if (!ok) break;
         tc_fence_after();
         const u32 to = tm_o + X * DP + tl;
@@ -428,62 +427,60 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         uint16_t* out = sp.y > sp.x ? p.o + static_cast<int64_t>(it.tok + X * a.TT + tok_r) * p.o_tok +
                                           static_cast<int64_t>(it.h * a.G + g) * p.o_head
                                     : nullptr;
-        const bool look = odd;
-        u32 w[DP / 2];                                    // the row, rounded: O may be written again before it is stored
-#pragma unroll
-        for (int c = 0; c < DP; c += 32) {
-          float o[32];
-          tc_ld32(to + c, o);
-          tc_wait_ld();
-          if (look) {
-            float z[32];                                  // (a copy: only this is in memory)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = o[i];
-            add_odd(p, it, X, sp.x - it.base, sp.y - it.base, c, z);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = z[i];
+        if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            float o[32];
+            tc_ld32(to + c, o);
+            tc_wait_ld();
+            add_odd(p, it, X, sp.x - it.base, sp.y - it.base, c, o);
+            tc_st32(to + c, o);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
-            w[c / 2 + i] = *reinterpret_cast<const u32*>(&b);
-          }
-        }
-        tc_fence_before();
-        mbar_arrive(&bars.of[X]);
-        if (!a.out16) {
-          if (out) {
-#pragma unroll
-            for (int i = 0; i < DP; ++i)
-              if (i < p.D) out[i] = static_cast<uint16_t>(w[i / 2] >> (i & 1 ? 16 : 0));
-          }
-          continue;
+          tc_wait_st();
         }
         // 32 dims at a time through shared memory, so that a warp stores 64 bytes of 8 rows at once (a lane a row
         // takes 32 lines a store)
         uint16_t* at[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = reinterpret_cast<uint16_t*>(shfl64(reinterpret_cast<u64>(out), i * 8 + lane / 4));
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DP; c += 32) {
+          float o[32];
+          tc_ld32(to + c, o);
+          tc_wait_ld();
+          if (c + 32 == DP) {
+            tc_fence_before();
+            mbar_arrive(&bars.of[X]);                     // O may be written again
+          }
           __syncwarp();                                   // the 32 dims before have been read
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(mine + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
-                make_uint4(w[c / 2 + 4 * i], w[c / 2 + 4 * i + 1], w[c / 2 + 4 * i + 2], w[c / 2 + 4 * i + 3]);
+          for (int i = 0; i < 4; ++i) {
+            u32 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k] * inv, o[8 * i + 2 * k + 1] * inv);
+              w[k] = *reinterpret_cast<const u32*>(&b);
+            }
+            *reinterpret_cast<uint4*>(mine + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
           __syncwarp();
           const int d = c + lane % 4 * 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = i * 8 + lane / 4;
-            const uint4 x = *reinterpret_cast<const uint4*>(mine + row * 64 + ((lane % 4 ^ (row >> 1 & 3)) << 4));
-            if (at[i] && d < p.D) *reinterpret_cast<uint4*>(at[i] + d) = x;
+            const unsigned char* x = mine + row * 64 + ((lane % 4 ^ (row >> 1 & 3)) << 4);
+            if (!at[i] || d >= p.D) continue;
+            if (a.out16) {
+              *reinterpret_cast<uint4*>(at[i] + d) = *reinterpret_cast<const uint4*>(x);
+            } else {
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) at[i][d + k] = reinterpret_cast<const uint16_t*>(x)[k];
+            }
           }
         }
       }
-      if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.ite[t % PT_RING]);
+      if (ok && lane == 0) mbar_arrive(&bars.ite[t % PT_RING]);
     }
     tc_fence_before();
   } else {
@@ -548,112 +545,107 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       const int X = wid - PT_W_MMA;
       const u32 dq = static_cast<u32>(tc_desc(q_a + X * C::QB, 16)), dk = static_cast<u32>(tc_desc(k_a, 16)),
                 dv = static_cast<u32>(tc_desc(v_a, PT_N * 128)), ts = tm_s + X * PT_N, to = tm_o + X * DP;
+      u32 go_turn = X ? 0 : 1;                            // the first row tile's turn comes first
       u32 p_turn = 0, o_turn = 1, q_turn = 0;             // of the row tile's barriers
       u32 whole = 0, look = 0;                            // and of each stage's vf and vc
       auto wait = [&](u64* bar, u32 parity) { return pt_wait(bar, parity, &gone, p.status); };
-      // What S of the row tile over tile j of an item, the ring's tile `at`, needs; the steps it takes.
-      auto ready = [&](const PtItem& i, int j, int at, int& steps, bool& last) {
-        const int j0 = i.j0[X], j1 = i.j1[X];
-        const bool on = j >= j0 && j < j1;
-        steps = on ? steps_of(i.y1[X], j) : 0;
-        last = j + 1 == j1;
-        if (on && j == j0) {
-          if (!wait(&bars.q[X], q_turn)) return false;
-          q_turn ^= 1;
-        }
-        return wait(&bars.kf[at % ST], (at / ST) & 1);
+      int at = 0, t = 0, j = 0, n = 0, j0 = 0, j1 = 0, y1 = 0, w0 = 0, w1 = 0;
+      u32 turns = 0;                                      // whether the row tiles take turns over this item
+      // Item t, as the row tile sees it; whether there is one.
+      auto take = [&] {
+        if (!item_at(t)) return false;
+        const PtItem& i = ring[t % PT_RING];
+        n = i.n, j0 = i.j0[X], j1 = i.j1[X], y1 = i.y1[X], w0 = i.w0, w1 = i.w1, j = 0;
+        turns = n >= PT_TURNS ? 1u : 0u;
+        return i.h >= 0;
       };
-      // S; its K, and after the item's last its Q, may be loaded again.
-      auto scores = [&](int at, int steps, bool last) {
-        const int st = at % ST;
-        const u32 d = dk + st * (C::TB >> 4);
-        if (steps == 0) {
-          mbar_arrive(&bars.ke[st]);
-          return;
-        }
-        if (steps == PT_N / 16) {
+      bool go = take();
+      int steps = 0;                                      // of the tile whose weights come next; 0: not this row tile's
+      bool first = false, last = false;
+      // (the loop's first half has nothing to do yet)
+      for (bool begin = true; go; begin = false) {
+        if (!begin) {
+          const int st = at % ST;
+          const bool clear = j >= w0 && j < w1;
+          if (!wait(clear ? &bars.vf[st] : &bars.vc[st], (clear ? whole : look) >> st & 1)) break;
+          if (clear) whole ^= 1u << st;
+          else look ^= 1u << st;
+          if (steps > 0) {
+            if (first) {                                  // the item before has been read
+              if (!wait(&bars.of[X], o_turn)) break;
+              o_turn ^= 1;
+            }
+            const u32 d = dv + st * (C::TB >> 4);
+            u32 acc = first ? 0 : 1;
+            bool ok = true;
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
-            tc_mma_ss_at(ts, dq + in, d + in, tc_idesc(PT_N, false), k > 0);
-          }
-        } else {
-          const u32 what = tc_idesc(steps * 16, false);
+            for (int half = 0; half < 2; ++half) {
+              ok = wait(&bars.p[X][half], p_turn) && (half == 0 || !turns || wait(&bars.go[X], go_turn));
+              if (!ok) break;
+              tc_fence_after();
+              const u32 w = ts + half * (PT_N / 4), v = d + half * (PT_N / 2 * 128 >> 4);
+              if (steps >= (half + 1) * (PT_N / 32)) {
+#pragma unroll
+                for (int k = 0; k < PT_N / 32; ++k) tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
+              } else {
 #pragma unroll 1
-          for (int k = 0; k < DP / 16; ++k) {
-            const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
-            tc_mma_ss_at(ts, dq + in, d + in, what, k > 0);
-          }
-        }
-        tc_commit(&bars.s[X]);
-        tc_commit(&bars.ke[st]);
-        if (last) tc_commit(&bars.qe[X]);
-      };
-      int at = 0, t = 0, j = 0, n_steps = 0;
-      bool n_last = false;
-      const PtItem* it = &ring[0];
-      bool ok = item_at(0), more = ok && it->h >= 0;
-      if (more) {
-        ok = ready(*it, 0, 0, n_steps, n_last);
-        if (ok) scores(0, n_steps, n_last);
-      }
-      while (ok && more) {
-        const int st = at % ST, steps = n_steps, nj = j + 1 < it->n ? j + 1 : 0;
-        const bool last = n_last, first = j == it->j0[X];
-        if (j >= it->w0 && j < it->w1) {
-          ok = wait(&bars.vf[st], whole >> st & 1);
-          whole ^= 1u << st;
-        } else {
-          ok = wait(&bars.vc[st], look >> st & 1);
-          look ^= 1u << st;
-        }
-        if (!ok) break;
-        const u32 d = dv + st * (C::TB >> 4);
-        if (steps > 0) {
-          if (first) {                                    // the item before has been read
-            if (!(ok = wait(&bars.of[X], o_turn))) break;
-            o_turn ^= 1;
-          }
-          if (!(ok = wait(&bars.p[X][0], p_turn))) break;
-          tc_fence_after();
-          if (steps == PT_N / 16) {
-#pragma unroll
-            for (int k = 0; k < PT_N / 32; ++k)
-              tc_mma_ts_at(to, ts + k * 8, d + k * (2048 >> 4), tc_idesc(DP, true), k > 0 || !first ? 1u : 0u);
-          }
-        }
-        const PtItem* next = it;
-        if (nj == 0) {
-          if (!(ok = item_at(t + 1))) break;
-          next = &ring[(t + 1) % PT_RING];
-          more = next->h >= 0;
-        }
-        if (more && !(ok = ready(*next, nj, at + 1, n_steps, n_last))) break;
-        if (steps > 0) {
-          if (!(ok = wait(&bars.p[X][1], p_turn))) break;
-          p_turn ^= 1;
-          tc_fence_after();
-          if (steps == PT_N / 16) {
-#pragma unroll
-            for (int k = PT_N / 32; k < PT_N / 16; ++k) tc_mma_ts_at(to, ts + k * 8, d + k * (2048 >> 4), tc_idesc(DP, true), 1u);
+                for (int k = 0; k < steps - half * (PT_N / 32); ++k)
+                  tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
+              }
+              acc = 1;
+            }
+            if (!ok) break;
+            go_turn ^= turns;
+            p_turn ^= 1;
+            tc_commit(&bars.ve[st]);                      // V may be loaded again
+            if (last) tc_commit(&bars.o[X]);
           } else {
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              tc_mma_ts_at(to, ts + k * 8, d + k * (2048 >> 4), tc_idesc(DP, true), k > 0 || !first ? 1u : 0u);
+            mbar_arrive(&bars.ve[st]);
+            if (turns && !wait(&bars.go[X], go_turn)) break;
+            go_turn ^= turns;
           }
-          tc_commit(&bars.ve[st]);                        // V may be loaded again
-          if (last) tc_commit(&bars.o[X]);
+          ++at;
+          if (++j == n) {
+            if (turns) mbar_arrive(&bars.go[X ^ 1]);
+            mbar_arrive(&bars.ite[t % PT_RING]);
+            ++t;
+            go = take();
+            if (!go) break;
+          }
+        }
+        const int st = at % ST;
+        const bool on = j >= j0 && j < j1;
+        steps = on ? steps_of(y1, j) : 0;
+        first = j == j0;
+        last = j + 1 == j1;
+        if (!wait(&bars.kf[st], (at / ST) & 1)) break;
+        if (steps > 0) {
+          if (first) {
+            if (!wait(&bars.q[X], q_turn)) break;
+            q_turn ^= 1;
+          }
+          const u32 d = dk + st * (C::TB >> 4);
+          if (steps == PT_N / 16) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+              const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
+              tc_mma_ss_at(ts, dq + in, d + in, tc_idesc(PT_N, false), k > 0);
+            }
+          } else {
+            const u32 what = tc_idesc(steps * 16, false);
+#pragma unroll 1
+            for (int k = 0; k < DP / 16; ++k) {
+              const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
+              tc_mma_ss_at(ts, dq + in, d + in, what, k > 0);
+            }
+          }
+          tc_commit(&bars.s[X]);
+          tc_commit(&bars.ke[st]);                        // K, and after the item's last Q, may be loaded again
+          if (last) tc_commit(&bars.qe[X]);
         } else {
-          mbar_arrive(&bars.ve[st]);
+          mbar_arrive(&bars.ke[st]);
         }
-        if (more) scores(at + 1, n_steps, n_last);
-        if (nj == 0) {
-          mbar_arrive(&bars.ite[t % PT_RING]);
-          ++t;
-        }
-        it = next;
-        j = nj;
-        ++at;
+        if (!begin && j > 0 && turns) mbar_arrive(&bars.go[X ^ 1]);
       }
       // the products in flight read shared memory and TMEM: all are done before either goes, also where the CTA gave up
       tc_commit(&bars.end);
@@ -675,23 +667,35 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p.status))) break;
       if (left == 1 && lane == 0) claim_block(&claims[c & 1], &bars.claim[c & 1]);
       PtItem& x = ring[t % PT_RING];
-      const int tok0 = (a.tiles - 1 - i / p.H) * 2 * a.TT;
+      const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * 2 * a.TT;
       int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
-      for (int w = lane; w < 2 * a.TT && !last; w += 32) {
-        const int tok = tok0 + w;
-        int2 sp = tok < p.N ? request_of(p, cu, every, tok) : make_int2(0, 0);
-        if (sp.y > 0) {
-          if (p.causal) sp.y = tok + 1;
+      if (!last) {
+        int b = request_before(p, cu, every, tok0, lane);
+        int2 at = request_at(p, cu, every, b);
+        const int end = min(2 * a.TT, p.N - tok0);
+        for (int w = lane; w < 2 * PT_M; w += 32) {
+          const int tok = tok0 + w;
+          if (!__all_sync(FULL, (tok >= at.x && tok < at.y) || w >= end)) {
+            // the group's tokens are of several requests: each lane goes on to its own
+            while (b + 1 < p.B && (every == 1 ? cu[b + 1] : p.cu[b + 1]) <= tok && w < end) ++b;
+            __syncwarp();
+            at = request_at(p, cu, every, b);
+          }
+          const bool live = w < end && tok >= at.x && tok < at.y;
+          const int2 sp = live ? make_int2(at.x, p.causal ? tok + 1 : at.y) : make_int2(0, 0);
 #pragma unroll
           for (int X = 0; X < 2; ++X)
-            if ((w >= a.TT) == (X == 1)) {
+            if (live && (w >= a.TT) == (X == 1)) {
               y0[X] = min(y0[X], sp.x);
               y1[X] = max(y1[X], sp.y);
               z0[X] = max(z0[X], sp.x);
               z1[X] = min(z1[X], sp.y);
             }
+          span[t % PT_RING][w] = sp;
+          if (w + 32 - lane >= 2 * a.TT) break;
+          b = __shfl_sync(FULL, b, 31);                   // (the last token's)
+          at = make_int2(__shfl_sync(FULL, at.x, 31), __shfl_sync(FULL, at.y, 31));
         }
-        span[t % PT_RING][w] = sp;
       }
 #pragma unroll
       for (int X = 0; X < 2; ++X) {
@@ -701,7 +705,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         z1[X] = __reduce_min_sync(FULL, z1[X]);
       }
       const int base = min(y0[0], y0[1]);
-      const int h = last ? -1 : i % p.H;
       const bool some = max(y1[0], y1[1]) > 0;            // (else: tokens of no request)
       if ((some || last) && lane == 0) {
         x.h = h;
