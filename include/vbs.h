@@ -597,7 +597,8 @@ int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
 /*
  * Attention of the planned step over `layer`: as kv8_attention, over bf16 keys and values.  What a token does not see
  * may hold anything.  Scores, softmax statistics and sums are fp32; the softmax weights are held to 16 bits (two bf16
- * parts).
+ * parts) where up to 16 rows (beams x n_q x q_heads / H) of a sentence share a K/V head or head_dim is above 128, else
+ * rounded to one bf16 number.
  * Errors: those of kv8_attention.
  */
 int kv16_attention(vbs_kv16* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,

@@ -709,18 +709,17 @@ def _output(out, shape, device):
 def _rows3(t: torch.Tensor, name: str, shape, dtype, index: int):
     """The strides of a [tokens, heads, D] tensor of this shape and dtype on device `index`."""
     st = t.stride()
-    if t.shape != shape or st[2] != 1:
-        raise ValueError(f"{name} must be {list(shape)} with unit stride along the last axis, got {list(t.shape)}")
-    if t.dtype != dtype or not t.is_cuda or t.device.index != index:
-        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}")
-    return st
+    if t.shape == shape and st[2] == 1 and t.dtype is dtype and t.get_device() == index:
+        return st
+    raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on cuda:{index} with unit stride along the last axis, got "
+                     f"{t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _vector(t: torch.Tensor, name: str, n: int, dtype, index: int) -> int:
     """The address of a contiguous [n] tensor of this dtype on device `index`."""
-    if t.shape != (n,) or not t.is_contiguous() or t.dtype != dtype or not t.is_cuda or t.device.index != index:
-        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on cuda:{index}")
-    return t.data_ptr()
+    if t.shape == (n,) and t.dtype is dtype and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on cuda:{index}")
 
 
 class Rotary:
@@ -761,35 +760,38 @@ class Rotary:
               k_out: torch.Tensor | None = None):
         """(q, k) [N, heads, D] (bfloat16 or float32, unit stride along D) rotated to pos (int32 [N]; a negative one: the
         token is skipped), into new tensors or the given ones (q and k themselves for in place)."""
-        N, i = pos.numel(), self.index
-        dt = q.dtype
+        N, i, dt, D = pos.numel(), self.index, q.dtype, self.D
         code = _dtype_code(dt)
         pp = _vector(pos, "pos", N, torch.int32, i)
-        qs, qp, q_out, qo = self._pair(N, q, q_out, "q", dt)
-        if k is None:
-            if k_out is not None:
-                raise ValueError("k_out needs k")
-            ks, kp, ko, heads = (0, 0), None, (0, 0), 0
+        heads = q.shape[1] if q.dim() == 3 else 0
+        shape = (N, heads, D)
+        qs = _rows3(q, "q", shape, dt, i)
+        if q_out is None:
+            q_out, qo = torch.empty(shape, dtype=dt, device=q.device), (heads * D, D)
         else:
-            ks, kp, k_out, ko = self._pair(N, k, k_out, "k", dt)
-            heads = k.shape[1]
-        args = (self.ctx, N, pp, code, qp, qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], q.shape[1], kp, ks[0], ks[1],
-                None if k is None else k_out.data_ptr(), ko[0], ko[1], heads)
-        if _device_index() == i:
-            st = lib().rope_apply(*args, _raw_stream(i))
-        else:
+            qo = _rows3(q_out, "q_out", shape, dt, i)
+        kp = kop = None
+        ks = ko = (0, 0)
+        k_heads = 0
+        if k is not None:
+            k_heads = k.shape[1] if k.dim() == 3 else 0
+            shape = (N, k_heads, D)
+            ks = _rows3(k, "k", shape, dt, i)
+            if k_out is None:
+                k_out, ko = torch.empty(shape, dtype=dt, device=k.device), (k_heads * D, D)
+            else:
+                ko = _rows3(k_out, "k_out", shape, dt, i)
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+        elif k_out is not None:
+            raise ValueError("k_out needs k")
+        if _device_index() != i:
             with torch.cuda.device(i):
-                st = lib().rope_apply(*args, _raw_stream(i))
+                return self.apply(pos, q, k, q_out, k_out)
+        st = lib().rope_apply(self.ctx, N, pp, code, q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], heads, kp, ks[0],
+                              ks[1], kop, ko[0], ko[1], k_heads, _raw_stream(i))
         if st != OK:
             _check(st, "rope_apply")
         return q_out, k_out
-
-    def _pair(self, N, x, out, name, dt):
-        shape = (N, x.shape[1] if x.dim() == 3 else 0, self.D)
-        st = _rows3(x, name, shape, dt, self.index)
-        if out is None:
-            out = torch.empty(shape, dtype=dt, device=x.device)
-        return st, x.data_ptr(), out, _rows3(out, name + "_out", shape, dt, self.index)
 
     def close(self):
         if getattr(self, "ctx", None) is not None and self.ctx.value:
@@ -834,39 +836,37 @@ class PagedKV16(PagedKV):
         With rotary, k is rotated to pos (int32 [N]; a negative one: the token is skipped) on its way, and stored to
         k_out too where that is given; q [N, heads, D] of k's dtype is rotated into q_out (new by default).  q_out and k_out may
         be q and k themselves."""
-        N, i = slots.numel(), self._order.index
-        dt = k.dtype
+        N, order, dt = slots.numel(), self._order, k.dtype
+        i, H, D = order.index, self.H, self.D
         code = _dtype_code(dt)
-        shape = (N, self.H, self.D)
+        shape = (N, H, D)
         ks, vs = _rows3(k, "k", shape, dt, i), _rows3(v, "v", shape, dt, i)
         sp = _vector(slots, "slots", N, torch.int64, i)
-        tensors = [k, v, slots]
-        rope = pp = qp = qo = ko = None
-        qs = qos = kos = (0, 0)
-        if rotary is None:
-            if not (pos is None and q is None and q_out is None and k_out is None):
-                raise ValueError("pos, q, q_out and k_out need rotary")
-        else:
-            if rotary.D != self.D or rotary.index != i:
-                raise ValueError(f"rotary must be for {self.D} dims on cuda:{i}")
+        rope = pp = qp = qop = kop = None
+        qs = qo = ko = (0, 0)
+        if rotary is not None:
+            if rotary.D != D or rotary.index != i:
+                raise ValueError(f"rotary must be for {D} dims on cuda:{i}")
             if pos is None:
                 raise ValueError("rotary needs pos")
             rope, pp = rotary.ctx, _vector(pos, "pos", N, torch.int32, i)
-            tensors.append(pos)
             if q is not None:
-                q_shape = (N, self.heads, self.D)
-                qs, qp = _rows3(q, "q", q_shape, dt, i), q.data_ptr()
+                shape_q = (N, self.heads, D)
+                qs = _rows3(q, "q", shape_q, dt, i)
                 if q_out is None:
-                    q_out = torch.empty(q_shape, dtype=dt, device=self.device)
-                qos, qo = _rows3(q_out, "q_out", q_shape, dt, i), q_out.data_ptr()
-                tensors += (q, q_out)
+                    q_out, qo = torch.empty(shape_q, dtype=dt, device=self.device), (self.heads * D, D)
+                else:
+                    qo = _rows3(q_out, "q_out", shape_q, dt, i)
+                qp, qop = q.data_ptr(), q_out.data_ptr()
             elif q_out is not None:
                 raise ValueError("q_out needs q")
             if k_out is not None:
-                kos, ko = _rows3(k_out, "k_out", shape, dt, i), k_out.data_ptr()
-                tensors.append(k_out)
-        self._order.run(lib().kv16_append, "kv16_append", tensors, self.ctx16, layer, N, sp, code, k.data_ptr(), ks[0], ks[1],
-                        v.data_ptr(), vs[0], vs[1], rope, pp, ko, kos[0], kos[1], qp, qs[0], qs[1], qo, qos[0], qos[1])
+                ko, kop = _rows3(k_out, "k_out", shape, dt, i), k_out.data_ptr()
+        elif not (pos is None and q is None and q_out is None and k_out is None):
+            raise ValueError("pos, q, q_out and k_out need rotary")
+        order.run(lib().kv16_append, "kv16_append", [t for t in (k, v, slots, pos, q, q_out, k_out) if t is not None], self.ctx16,
+                  layer, N, sp, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], rope, pp, kop, ko[0], ko[1], qp,
+                  qs[0], qs[1], qop, qo[0], qo[1])
         return q_out, k_out
 
     def plan(self, ctx_len: torch.Tensor, n_q: int = 1):

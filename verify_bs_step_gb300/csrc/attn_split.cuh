@@ -249,7 +249,8 @@ struct EncSrc {
 // the kernel
 // ---------------------------------------------------------------------------------------
 
-template <int EL, int DP, int MT> struct SplitCfg {
+template <class Src, int DP, int MT> struct SplitCfg {
+  static constexpr int EL = Src::EL;
   static constexpr int CHK = 16 / EL;                       // dims in 16 bytes
   static constexpr int KS = DP / 16;                        // contraction steps of the scores
   static constexpr int NT = DP / 8;                         // output tiles of 8 dims
@@ -259,6 +260,9 @@ template <int EL, int DP, int MT> struct SplitCfg {
   // fourth CTA an SM pay (1024 sentences x 8 heads x 64..1024 positions: 94 to 76 us .. 195 to 183; 64 x 512: 14.9 to 13.3;
   // 16 sentences, which do not fill the GPU: 1..5 % slower)
   static constexpr bool SMALL = EL == 1 && DP == 64 && MT == 1;
+  // Over a 16-bit cache with more than 16 rows, the weights are rounded to one bf16 number instead of held in two: the second
+  // product is what bounds it there (64 rows x 8 tokens x 4 heads over 1..2500 positions: 93 us with two, 85 with one)
+  static constexpr bool ONE = Src::RAW && MT == 2;
   static constexpr int NS = SMALL ? 4 : STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
   static constexpr int O_LD = DP + 4;                       // floats of an o row in shared memory
   static constexpr int RING = NS * STAGE > MT * 16 * O_LD * 4 ? NS * STAGE : MT * 16 * O_LD * 4;
@@ -296,9 +300,9 @@ __device__ __forceinline__ void store_out(uint16_t* out, const SplitArgs& sa, co
 
 // EXACT: head_dim is DP; ALIGNED: K and V rows may be copied 16 bytes at a time.
 template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * NW, (SplitCfg<Src::EL, DP, MT>::CTAS))
+__global__ void __launch_bounds__(32 * NW, (SplitCfg<Src, DP, MT>::CTAS))
 attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
-  using C = SplitCfg<Src::EL, DP, MT>;
+  using C = SplitCfg<Src, DP, MT>;
   constexpr int NT = 32 * NW;
   constexpr int EL = Src::EL, ROWS = 16 * MT;
   constexpr float GROW = Src::BF ? 8.f : 3.f;
@@ -642,7 +646,10 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
             }
           l[mt][x] = Src::BF ? l[mt][x] + sum : fmaf(sum, u.vinv, l[mt][x]);
         }
-        if (Src::BF) {
+        if (C::ONE) {
+          p[mt] = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
+                             pack_bf16(w[1][2], w[1][3]));
+        } else if (Src::BF) {
           // two bf16 parts of each weight: the products carry 16 bits of it
           float r[2][4];
           p[mt] = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
@@ -733,7 +740,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p[mt], b0, b1);
-                mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt], b0, b1);
+                if (!C::ONE) mma16816<true>(o[mt][vc * C::VCH + wd * 2 + i], p2[mt], b0, b1);
               }
             }
           }
@@ -822,8 +829,9 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 constexpr int JN_WARPS = 4, JN_FEW = 4;
 
 // CTA (segment, c): rows 4 c .. 4 c + 3 of its segment, a warp each; where the pieces are many, all warps take
-// a row after the other and share its pieces.  A dependent launch: it is set up while the split kernel runs.
-template <int DP, int ROWS>
+// a row after the other and share its pieces.  WIDE, for few segments: CTA (segment, r), all warps share row r's pieces.  A
+// dependent launch: it is set up while the split kernel runs.
+template <int DP, int ROWS, bool WIDE = false>
 __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, const SplitArgs sa) {
   constexpr int PART = ROWS * (DP + 2), V = DP / 128 > 0 ? DP / 128 : 1;   // float4s of a row that a lane holds
   __shared__ float4 so[JN_WARPS][DP / 4];
@@ -868,7 +876,7 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
   };
   float4 a[V];
   float top, sum;
-  if (np <= 64 * JN_WARPS) {
+  if (!WIDE && np <= 64 * JN_WARPS) {
     const int r = blockIdx.y * JN_WARPS + wid;
     if (r >= rows) return;
     if (np <= JN_FEW) {                                     // few pieces: all loads at once
@@ -910,7 +918,8 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
     }
     return;
   }
-  for (int r = blockIdx.y * JN_WARPS; r < min(rows, (static_cast<int>(blockIdx.y) + 1) * JN_WARPS); ++r) {
+  constexpr int PER = WIDE ? 1 : JN_WARPS;
+  for (int r = blockIdx.y * PER; r < min(rows, (static_cast<int>(blockIdx.y) + 1) * PER); ++r) {
     gather(r, wid, JN_WARPS, top, sum, a);
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -960,7 +969,7 @@ inline int64_t split_part_floats(int D, int num_sms) {
 
 template <class Src, int DP, int MT, bool EXACT, bool ALIGNED>
 int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_sms, cudaStream_t s) {
-  using C = SplitCfg<Src::EL, DP, MT>;
+  using C = SplitCfg<Src, DP, MT>;
   static_assert(C::CTAS * MT * 16 <= 4 * 32, "split_part_floats");
   static std::atomic<unsigned long long> attr_done{0};
   auto* kernel = attn_split_kernel<Src, DP, MT, EXACT, ALIGNED>;
@@ -972,6 +981,12 @@ int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_s
     return launch_dependent(kernel, dim3(static_cast<unsigned>(segments)), dim3(32 * NW), C::SMEM, s, src, io, one);
   }
   if (launch_dependent(kernel, dim3(num_sms * C::CTAS), dim3(32 * NW), C::SMEM, s, src, io, sa) != VBS_OK) return VBS_ECUDA;
+  if constexpr (Src::RAW) {
+    // a row over 100003 positions x 8 heads has 38 pieces a head: 10.6 us with a warp a row, WIDE_US with four
+    if (segments * std::min(sa.M, 16 * MT) <= 2 * num_sms)
+      return launch_dependent(attn_join_kernel<DP, 16 * MT, true>, dim3(static_cast<unsigned>(segments), std::min(sa.M, 16 * MT)),
+                              dim3(32 * JN_WARPS), 0, s, io, sa);
+  }
   const dim3 grid(static_cast<unsigned>(segments), (std::min(sa.M, 16 * MT) + JN_WARPS - 1) / JN_WARPS);
   return launch_dependent(attn_join_kernel<DP, 16 * MT>, grid, dim3(32 * JN_WARPS), 0, s, io, sa);
 }

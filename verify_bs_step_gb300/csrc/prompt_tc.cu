@@ -218,6 +218,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // a dependent launch: set up before, reads and writes nothing before its predecessor's end
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = tid; i * every <= p.B; i += PT_NT) cu[i] = p.cu[i * every];
   if (blockIdx.x == 0)
     for (int b = tid; b < p.B; b += PT_NT)
@@ -783,8 +786,8 @@ template <int DP>
 static int launch_tc(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PtArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   if (!smem_attr_once(prompt_tc_kernel<DP>, static_cast<int>(PtCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
-  prompt_tc_kernel<DP><<<a.tiles * a.p.H - a.many * (a.batch - 1), PT_NT, PtCfg<DP>::SMEM, s>>>(qm, km, vm, a);
-  return cudaGetLastError() == cudaSuccess ? VBS_OK : VBS_ECUDA;
+  return launch_dependent(prompt_tc_kernel<DP>, dim3(static_cast<unsigned>(a.tiles * a.p.H - a.many * (a.batch - 1))), dim3(PT_NT),
+                          PtCfg<DP>::SMEM, s, qm, km, vm, a);
 }
 
 int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
