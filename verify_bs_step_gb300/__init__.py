@@ -243,7 +243,8 @@ class _StreamOrder:
             st = fn(*args)
             cur.wait_stream(self.stream)
             for t in tensors:                       # not to be reused before the context's stream is done
-                t.record_stream(self.stream)
+                if t is not None:
+                    t.record_stream(self.stream)
         _check(st, name)
 
 
@@ -864,8 +865,8 @@ class PagedKV16(PagedKV):
                 ko, kop = _rows3(k_out, "k_out", shape, dt, i), k_out.data_ptr()
         elif not (pos is None and q is None and q_out is None and k_out is None):
             raise ValueError("pos, q, q_out and k_out need rotary")
-        order.run(lib().kv16_append, "kv16_append", [t for t in (k, v, slots, pos, q, q_out, k_out) if t is not None], self.ctx16,
-                  layer, N, sp, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], rope, pp, kop, ko[0], ko[1], qp,
+        order.run(lib().kv16_append, "kv16_append", (k, v, slots, pos, q, q_out, k_out), self.ctx16, layer,
+                  N, sp, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], rope, pp, kop, ko[0], ko[1], qp,
                   qs[0], qs[1], qop, qo[0], qo[1])
         return q_out, k_out
 
