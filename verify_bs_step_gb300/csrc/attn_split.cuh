@@ -36,6 +36,7 @@
 #include "attn.h"
 #include "codes.cuh"
 #include "common.cuh"
+#include "launch.cuh"
 #include "rope.h"
 
 namespace vbs {

@@ -20,6 +20,7 @@
 
 #include <cuda_bf16.h>
 
+#include "launch.cuh"
 #include "pairs.cuh"
 #include "prompt.h"
 #include "tc.cuh"
