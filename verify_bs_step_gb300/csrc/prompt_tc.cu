@@ -266,17 +266,17 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           // scale), where there are such
           const int least = __reduce_min_sync(FULL, left), late = __reduce_max_sync(FULL, from);
 #pragma unroll 1
-          for (int c = 0; c < PT_N; c += 16) {
-            if (least >= c + 16 && late <= c && !neg) continue;
+          for (int c = 0; c < PT_N; c += 32) {
+            if (least >= c + 32 && late <= c && !neg) continue;
             const int lo = max(0, from - c), hi = left - c;
-            u32 see = hi >= 16 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
-            see = lo >= 16 ? 0u : see & (~0u << lo);
-            float x[16];
-            tc_ld16(ts + c, x);
+            u32 see = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+            see = lo >= 32 ? 0u : see & (~0u << lo);
+            float x[32];
+            tc_ld32(ts + c, x);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = see >> i & 1u ? (neg ? -x[i] : x[i]) : -INFINITY;
-            tc_st16(ts + c, x);
+            for (int i = 0; i < 32; ++i) x[i] = see >> i & 1u ? (neg ? -x[i] : x[i]) : -INFINITY;
+            tc_st32(ts + c, x);
           }
           tc_wait_st();
         }

@@ -67,7 +67,7 @@ __device__ __forceinline__ void tc_st16(u32 a, const float (&r)[16]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tc_st32(u32 a, const float (&r)[32]) {
+__device__ __forceinline__ void tc_st32(u32 a, const float* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
