@@ -626,9 +626,9 @@ int pattn_init(vbs_pattn** ctx, int q_heads, int kv_heads, int head_dim, vbs_str
  *   out = sum_j softmax_j(scale * q . k_j) v_j   over the request's tokens up to its own (causal), or over all of them.
  * All bf16 (device), head_dim contiguous: token t's head h of q is at q + t * q_tok + h * q_head (elements), k, v and out
  * likewise.  Tokens of no request are neither used nor written.  What a token does not see may hold anything.
- * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to bf16 before the product with V (in
- * the kernel for head_dim above 128, more than 128 heads a group, or q, k, v not aligned to 16 bytes they are not:
- * pattn_kernel tells; it is many times slower).
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to bf16 before the product with V (not
+ * in the kernel for more than 128 heads a group, or q, k, v whose addresses and strides are not multiples of 16 bytes:
+ * pattn_kernel tells; it is some 50 times slower).
  * An infinite or NaN element of V counts for every token that sees it, as in the formula.
  * Errors: VBS_EINVAL (n or batch outside 0..2^30, NULL pointers, scale not finite), VBS_ECUDA; a request that is not
  *   within the tokens counts as none, with VBS_EINVAL in pattn_status().

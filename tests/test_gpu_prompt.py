@@ -49,7 +49,8 @@ def check(out, q, k, v, cu, causal=True, scale=None, tokens=12, heads=None, what
 @pytest.mark.parametrize("lens,Hq,H,D", [
     ([1], 1, 1, 8), ([5, 0, 130, 1], 2, 2, 64), ([127, 128, 129], 4, 4, 64), ([300], 8, 2, 128), ([33, 600, 64], 8, 1, 128),
     ([70, 200], 6, 2, 80), ([513, 3], 10, 2, 40), ([40] * 9, 7, 1, 64), ([1] * 300, 4, 2, 64), ([257, 255], 1, 1, 128),
-    ([0, 0, 31, 0], 16, 1, 128), ([190, 77], 128, 1, 24), ([1025], 3, 3, 96), ([2000, 10], 5, 1, 64)])
+    ([0, 0, 31, 0], 16, 1, 128), ([190, 77], 128, 1, 24), ([1025], 3, 3, 96), ([2000, 10], 5, 1, 64),
+    ([70, 200], 6, 2, 200), ([33, 12], 40, 2, 256), ([3, 300, 500], 2, 2, 256), ([1, 130], 3, 1, 136)])
 def test_matches_the_oracle(lens, Hq, H, D, causal):
     import verify_bs_step_gb300 as vbs
     x = vbs.PromptAttention(Hq, D, kv_heads=H)
@@ -72,10 +73,10 @@ def test_matches_the_oracle(lens, Hq, H, D, causal):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("lens,Hq,H,D,shift", [([5, 0, 90, 1], 2, 2, 64, 1), ([70, 200], 6, 2, 200, 0), ([33, 12], 40, 2, 256, 0),
+@pytest.mark.parametrize("lens,Hq,H,D,shift", [([5, 0, 90, 1], 2, 2, 64, 1), ([70, 200], 6, 2, 200, 1), ([33, 12], 40, 2, 256, 1),
                                                ([300], 4, 1, 128, 1), ([64], 129, 1, 16, 0), ([3, 50], 3, 1, 136, 1)])
 def test_other_layouts(lens, Hq, H, D, shift, causal):
-    """head_dim above 128, many heads a group, rows 2 bytes off: the other kernel."""
+    """More than 128 heads a group, rows 2 bytes off: the other kernel."""
     import verify_bs_step_gb300 as vbs
     x = vbs.PromptAttention(Hq, D, kv_heads=H)
     cu = starts(lens)
@@ -118,7 +119,7 @@ def test_tokens_of_no_request_are_left(Hq, H, D, shift):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("D,Hq,H", [(64, 4, 1), (128, 2, 2), (192, 2, 1)])
+@pytest.mark.parametrize("D,Hq,H", [(64, 4, 1), (128, 2, 2), (192, 2, 1), (8, 3, 3)])
 def test_infinities_and_nan_reach_only_those_who_see_them(D, Hq, H, causal):
     """Rows that see no bad position are those of the same call without it; rows that do are not finite where the
     formula is not."""
@@ -140,10 +141,13 @@ def test_infinities_and_nan_reach_only_those_who_see_them(D, Hq, H, causal):
         a = int(cu[b])
         rows = slice(a + p if causal else a, a + lens[b])
         hit[rows, :G, d] = True
-        got = out[rows, :G, d]
-        # (a weight that has gone to 0 in fp32 makes NaN of an infinity in whole tiles)
-        assert got.isnan().all() if z != z else ((got == z) | got.isnan()).all(), (b, p, d)
-        assert (out[a + p, :G, d] == z).all() or z != z or not causal
+        # what a row sees of the bad elements of a dim adds up: infinities of both signs make NaN.  (A weight that has gone
+        # to 0 in fp32 makes NaN of an infinity in whole tiles.)
+        for t in range(rows.start - a, lens[b]):
+            z = sum(x for (b2, p2, d2), x in bad.items() if (b2, d2) == (b, d) and (p2 <= t or not causal))
+            got = out[a + t, :G, d]
+            assert got.isnan().all() if z != z else ((got == z) | got.isnan()).all(), (b, t, d)
+            assert (got == z).all() or z != z or t != p or not causal
     clean = ~hit
     assert torch.isfinite(out[clean]).all()
     check(torch.where(hit, want, out), q, k, v, cu, causal)
@@ -180,7 +184,7 @@ def test_scores_of_minus_infinity(D, Hq, H):
     x.close()
 
 
-@pytest.mark.parametrize("D,mul", [(64, 40.0), (128, 300.0), (128, 0.0)])
+@pytest.mark.parametrize("D,mul", [(64, 40.0), (128, 300.0), (128, 0.0), (256, 100.0)])
 def test_extreme_scores(D, mul):
     import verify_bs_step_gb300 as vbs
     x = vbs.PromptAttention(2, D)
@@ -213,7 +217,7 @@ def test_many_requests_and_a_long_one():
 
 def test_a_long_request():
     import verify_bs_step_gb300 as vbs
-    for D, Hq, H in ((128, 8, 1), (64, 3, 1)):
+    for D, Hq, H in ((128, 8, 1), (64, 3, 1), (256, 1, 1)):
         x = vbs.PromptAttention(Hq, D, kv_heads=H)
         cu = starts([9000, 5000, 1])
         q, k, v = tensors(14001, Hq, H, D, mul=1.5)

@@ -22,6 +22,8 @@
 // few warps where 32 rows share a K/V head (64 x 8 tokens x 4 heads over 1..4000 positions, int8: 97 us, 2.8 TB/s: 254
 // registers leave two warps a scheduler; issue slots 43 % active, the tensor pipe 33 %, the first stall the fixed
 // latency of an instruction).
+// Over bf16 pages: 64 sentences x 4 beams x 1064: 62 us with plan and join (55 this kernel, 5.6 TB/s); 100003 positions: 72 us
+// (64, 6.4 TB/s, 94 % of the measured copy); 64 x 8 tokens x 4 heads over 1..2500: 75 us (68, 4.9 TB/s).
 // Measured and not kept: two units an iteration (fewer instructions, 8 warps instead of 12: 102 and 65 us), CTAs
 // of one warp (91 us at 64 x 4 beams: four times the partials), a join in the CTA that arrives last (57).
 
@@ -983,7 +985,7 @@ int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_s
   }
   if (launch_dependent(kernel, dim3(num_sms * C::CTAS), dim3(32 * NW), C::SMEM, s, src, io, sa) != VBS_OK) return VBS_ECUDA;
   if constexpr (Src::RAW) {
-    // a row over 100003 positions x 8 heads has 38 pieces a head: 10.6 us with a warp a row, WIDE_US with four
+    // 100003 positions x 8 heads leave 38 pieces a head: the whole step takes 97 us (cold caches) with a warp a row, 95 with four
     if (segments * std::min(sa.M, 16 * MT) <= 2 * num_sms)
       return launch_dependent(attn_join_kernel<DP, 16 * MT, true>, dim3(static_cast<unsigned>(segments), std::min(sa.M, 16 * MT)),
                               dim3(32 * JN_WARPS), 0, s, io, sa);

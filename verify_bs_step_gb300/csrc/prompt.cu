@@ -1,9 +1,10 @@
-// Attention of packed prompts to themselves, for rows that TMA cannot read and for head_dim above 128 (sm_103a).
+// Attention of packed prompts to themselves, for rows that TMA cannot read and more than 128 heads a group (sm_103a).
 //
 // A CTA takes 16 query rows (tokens, the heads of a group side by side) of one K/V head over the positions that any of
 // them sees, 32 at a time: K and V come to shared memory in fp32, a lane scores one position for its warp's four rows,
 // and keeps D / 32 dims of their sums.  Scores, the running maximum and sum, and the sums are fp32, products plain
-// fp32 arithmetic: it is the form for layouts out of the ordinary, and bound by that arithmetic.
+// fp32 arithmetic: it is the form for layouts out of the ordinary, and bound by that arithmetic
+// (2000 tokens x 32 heads over 8 x 128: 2951 us, 11 TFLOP/s; the tiles take 60).
 
 #include <cuda_bf16.h>
 

@@ -35,7 +35,7 @@ __device__ __forceinline__ int2 request_of(const PromptArgs& a, int t) {
 }
 
 int launch_prompt_rows(const PromptArgs& a, cudaStream_t s);
-// Whether the tiles take this call: head_dim up to 128, up to 128 heads a group, and rows that TMA can read.
+// Whether the tiles take this call: up to 128 heads a group, and rows that TMA can read.
 bool prompt_tc_takes(const PromptArgs& a);
 int launch_prompt_tc(const PromptArgs& a, int num_sms, cudaStream_t s);
 

@@ -1,20 +1,36 @@
 // Attention of packed prompts to themselves: tcgen05 tiles (sm_103a).
 //
-// An item is 2 x 128 query rows of one K/V head (2 TT tokens in their packed order, whatever requests they are of, the
+// An item is 2 x 128 query rows (128 at head_dim above 128) of one K/V head (2 TT tokens in their packed order, whatever requests they are of, the
 // heads of a group side by side) over the positions that any of them sees, PT_N at a time:
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, one buffer a row tile;
 //   softmax       four warps a row tile, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes, O in TMEM.
-// The two row tiles share K and V, and one's products run while the other's softmax does.  A warp each loads K (and Q)
-// and V by TMA, issues the products, and works out the next item (which positions each of its tokens sees).
+// The row tiles share K and V.  Of the other warps one loads Q, K and V by TMA, one a row tile issues its products, four
+// look through V (below) and bring results out, and one works out the next items: which positions each token sees.
+// The grid has a block an item, but a CTA goes on with the items of blocks that have not started (cluster launch
+// control), so that CTAs share the work out whatever the requests' lengths, the longest rows first.
 //
-// A row sees the positions [x, y): its request's first token up to its own (causal) or its request's last.  Tiles
-// that some row does not see whole are masked row by row; there V may hold infinities or NaN that no weight of 0
-// makes harmless, so that such elements are put to 0 for the product, and added to the rows that see them at the end.
+// A row sees the positions [x, y): its request's first token up to its own (causal) or its request's last.  Scores past
+// them are set to -inf in TMEM, in the tiles that some row does not see whole.  There V may hold infinities or NaN that
+// a weight of 0 does not make harmless: such elements are put to 0 for the product, and added at the end to the rows that
+// see them.
 //
 // The running reference of the softmax only moves when a row's maximum has grown by 2^8 (in the weights'
 // own units): until then weights up to 256 are as good in bf16 as weights up to 1, and O stays where it is.
 // The weights' bf16 rounding is the one rounding besides the result's; their sum is taken before it.
+//
+// What bounds it is a row tile's chain: a tile of 128 x 128 at head_dim 128 costs 1100 to 1500 clocks of softmax (512 of
+// them exponentials, at 32 a clock and SM), the second half of its product with V and the next scores 768, and some 330 from
+// an instruction to its barrier, while S and P share their 128 TMEM columns; two chains fill 58 to 68 % of the tensor pipe
+// (16001 tokens x 32 heads: 1.45 ms, 1440 TFLOP/s, 76 % of the measured burst).  Requests of 1000 tokens add an item's start and
+// end, some 8000 of 22000 clocks (64 of them: 580 us, 906 TFLOP/s); 128 sentences of up to 256 tokens, 8 heads x 64, take
+// 42 us.  TMEM is full: two S and two O of 128 columns.
+// What counted on the way: all roles' code of a tile together has to stay short, or one warp's pushes another's out of the
+// instruction cache (unexecuted paths alone cost 733 against 633 us); results through shared memory (a lane a row took 6000
+// clocks an item); weights handed over in halves; a warp a row tile for the products; an item's V, results and next
+// item on warps of their own.  Measured and not kept: a lock around a row tile's products (1491 against 1466 us), whole warps
+// that issue (1665 against 1462), results and V in an event loop (735 against 690), each row tile's own K and V where the two
+// see different requests (no gain, and longer code).
 
 #include <climits>
 
@@ -47,7 +63,7 @@ static_assert(PT_SM * PT_REGS_SM + PT_OUT * PT_REGS_OUT + 128 * PT_REGS_REST <= 
 struct PtArgs {
   PromptArgs p;
   int G, TT;                              // heads a group, tokens a row tile
-  int tiles;                              // of 2 TT tokens
+  int tiles;                              // of an item's tokens
   int batch, many;                        // the grid's first `many` blocks stand for `batch` items each, the others for one
   bool out16;                             // stores of 16 bytes
 };
@@ -56,9 +72,10 @@ template <int DP> struct PtCfg {
   static constexpr int SLABS = DP / 64;                    // 64 dims: 128 bytes a row
   static constexpr int QB = SLABS * PT_M * 128;            // one row tile of Q
   static constexpr int TB = SLABS * PT_N * 128;            // one tile of K or V
-  static constexpr int ST = DP == 64 ? 4 : 2;              // stages of K, and of V
+  static constexpr int X = DP == 256 ? 1 : 2;              // row tiles an item: what fits TMEM
+  static constexpr int ST = DP == 64 ? 4 : (DP == 128 ? 2 : 1);   // stages of K, and of V
   static constexpr int OUT = 32 * 64;                      // a warp's rows of 32 dims on their way out
-  static constexpr size_t SMEM = 2 * QB + 2 * ST * TB + PT_CU * 4 + PT_OUT / 32 * OUT + 1024;
+  static constexpr size_t SMEM = X * QB + 2 * ST * TB + PT_CU * 4 + PT_OUT / 32 * OUT + 1024;
 };
 
 // Rings of barriers: kf, vf (a tile has landed), ke, ve (it is not read any more); vx and vc in place of vf where not
@@ -178,8 +195,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = pt_smem_raw + ((1024 - (smem_u32(pt_smem_raw) & 1023)) & 1023);
-  const u32 q_a = smem_u32(smem), k_a = q_a + 2 * C::QB, v_a = k_a + ST * C::TB;
-  unsigned char* out_s = smem + 2 * C::QB + 2 * ST * C::TB;
+  const u32 q_a = smem_u32(smem), k_a = q_a + C::X * C::QB, v_a = k_a + ST * C::TB;
+  unsigned char* out_s = smem + C::X * C::QB + 2 * ST * C::TB;
   int* cu = reinterpret_cast<int*>(out_s + PT_OUT / 32 * C::OUT);
   const PromptArgs& p = a.p;
   const int every = (p.B + 1 + PT_CU - 1) / PT_CU;        // one start in `every` is held
@@ -671,12 +688,12 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p.status))) break;
       if (left == 1 && lane == 0) claim_block(&claims[c & 1], &bars.claim[c & 1]);
       PtItem& x = ring[t % PT_RING];
-      const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * 2 * a.TT;
+      const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * C::X * a.TT;
       int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
       if (!last) {
         int b = request_before(p, cu, every, tok0, lane);
         int2 at = request_at(p, cu, every, b);
-        const int end = min(2 * a.TT, p.N - tok0);
+        const int end = min(C::X * a.TT, p.N - tok0);
         for (int w = lane; w < 2 * PT_M; w += 32) {
           const int tok = tok0 + w;
           if (!__all_sync(FULL, (tok >= at.x && tok < at.y) || w >= end)) {
@@ -696,7 +713,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
               z1[X] = min(z1[X], sp.y);
             }
           span[t % PT_RING][w] = sp;
-          if (w + 32 - lane >= 2 * a.TT) break;
+          if (w + 32 - lane >= C::X * a.TT) break;
           b = __shfl_sync(FULL, b, 31);                   // (the last token's)
           at = make_int2(__shfl_sync(FULL, at.x, 31), __shfl_sync(FULL, at.y, 31));
         }
@@ -778,7 +795,7 @@ static bool encode(CUtensorMap* map, const uint16_t* x, const PromptArgs& p, int
 bool prompt_tc_takes(const PromptArgs& p) {
   auto stride_ok = [](int64_t s, int64_t extent) { return extent == 1 || (s > 0 && s % 8 == 0 && s < (int64_t{1} << 38)); };
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v);
-  return p.D <= 128 && p.Hq / p.H <= PT_M && (at & 15) == 0 && stride_ok(p.q_tok, p.N) && stride_ok(p.q_head, p.Hq) &&
+  return p.Hq / p.H <= PT_M && (at & 15) == 0 && stride_ok(p.q_tok, p.N) && stride_ok(p.q_head, p.Hq) &&
          stride_ok(p.k_tok, p.N) && stride_ok(p.k_head, p.H) && stride_ok(p.v_tok, p.N) && stride_ok(p.v_head, p.H) &&
          tensor_map_encode() != nullptr;
 }
@@ -797,14 +814,16 @@ int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
   if (!encode(&qm, p.q, p, p.Hq, p.q_tok, p.q_head, G, TT) || !encode(&km, p.k, p, p.H, p.k_tok, p.k_head, 1, PT_N) ||
       !encode(&vm, p.v, p, p.H, p.v_tok, p.v_head, 1, PT_N))
     return VBS_ECUDA;
-  const int64_t tiles = (static_cast<int64_t>(p.N) + 2 * TT - 1) / (2 * TT), items = tiles * p.H;
+  const int per = (p.D <= 128 ? 2 : 1) * TT;              // an item's tokens
+  const int64_t tiles = (static_cast<int64_t>(p.N) + per - 1) / per, items = tiles * p.H;
   if (items >= int64_t{1} << 31) return VBS_EINVAL;
   // the GPU answers some 15 claims a microsecond: many items are claimed several at a time, the last quarter one by one
   const int batch = static_cast<int>(std::max<int64_t>(1, items / (16 * num_sms)));
   const int many = batch > 1 ? static_cast<int>(items * 3 / 4 / batch) : 0;
   const PtArgs a{p, G, TT, static_cast<int>(tiles), batch, many,
                  (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && (p.o_tok | p.o_head) % 8 == 0};
-  return p.D <= 64 ? launch_tc<64>(qm, km, vm, a, s) : launch_tc<128>(qm, km, vm, a, s);
+  if (p.D <= 64) return launch_tc<64>(qm, km, vm, a, s);
+  return p.D <= 128 ? launch_tc<128>(qm, km, vm, a, s) : launch_tc<256>(qm, km, vm, a, s);
 }
 
 }  // namespace vbs
