@@ -63,7 +63,7 @@ static_assert(PT_SM * PT_REGS_SM + PT_OUT * PT_REGS_OUT + 128 * PT_REGS_REST <= 
 struct PtArgs {
   PromptArgs p;
   int G, TT;                              // heads a group, tokens a row tile
-  int tiles;                              // of an item's tokens
+  int per, tiles;                         // an item's tokens, TT or 2 TT; items a K/V head
   int batch, many;                        // the grid's first `many` blocks stand for `batch` items each, the others for one
   bool out16;                             // stores of 16 bytes
 };
@@ -688,12 +688,12 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p.status))) break;
       if (left == 1 && lane == 0) claim_block(&claims[c & 1], &bars.claim[c & 1]);
       PtItem& x = ring[t % PT_RING];
-      const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * C::X * a.TT;
+      const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * a.per;
       int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
       if (!last) {
         int b = request_before(p, cu, every, tok0, lane);
         int2 at = request_at(p, cu, every, b);
-        const int end = min(C::X * a.TT, p.N - tok0);
+        const int end = min(a.per, p.N - tok0);
         for (int w = lane; w < 2 * PT_M; w += 32) {
           const int tok = tok0 + w;
           if (!__all_sync(FULL, (tok >= at.x && tok < at.y) || w >= end)) {
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
               z1[X] = min(z1[X], sp.y);
             }
           span[t % PT_RING][w] = sp;
-          if (w + 32 - lane >= C::X * a.TT) break;
+          if (w + 32 - lane >= a.per) break;
           b = __shfl_sync(FULL, b, 31);                   // (the last token's)
           at = make_int2(__shfl_sync(FULL, at.x, 31), __shfl_sync(FULL, at.y, 31));
         }
@@ -814,13 +814,17 @@ int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
   if (!encode(&qm, p.q, p, p.Hq, p.q_tok, p.q_head, G, TT) || !encode(&km, p.k, p, p.H, p.k_tok, p.k_head, 1, PT_N) ||
       !encode(&vm, p.v, p, p.H, p.v_tok, p.v_head, 1, PT_N))
     return VBS_ECUDA;
-  const int per = (p.D <= 128 ? 2 : 1) * TT;              // an item's tokens
+  // Two row tiles an item, but one where head_dim leaves no room for two, or where the GPU has an SM for each: one / two in
+  // us, 7000 tokens x 1 head x 128: 92 / 100; 16 sentences up to 256 x 8 x 64: 18.4 / 20.5; and with more than half an SM a
+  // pair, 32 such sentences: 26.6 / 22.5; 4000 tokens x 8 heads x 128: 73.8 / 65.5.
+  const int64_t pairs = (static_cast<int64_t>(p.N) + 2 * TT - 1) / (2 * TT) * p.H;
+  const int per = p.D > 128 || pairs <= num_sms / 2 ? TT : 2 * TT;
   const int64_t tiles = (static_cast<int64_t>(p.N) + per - 1) / per, items = tiles * p.H;
   if (items >= int64_t{1} << 31) return VBS_EINVAL;
   // the GPU answers some 15 claims a microsecond: many items are claimed several at a time, the last quarter one by one
   const int batch = static_cast<int>(std::max<int64_t>(1, items / (16 * num_sms)));
   const int many = batch > 1 ? static_cast<int>(items * 3 / 4 / batch) : 0;
-  const PtArgs a{p, G, TT, static_cast<int>(tiles), batch, many,
+  const PtArgs a{p, G, TT, per, static_cast<int>(tiles), batch, many,
                  (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && (p.o_tok | p.o_head) % 8 == 0};
   if (p.D <= 64) return launch_tc<64>(qm, km, vm, a, s);
   return p.D <= 128 ? launch_tc<128>(qm, km, vm, a, s) : launch_tc<256>(qm, km, vm, a, s);
