@@ -1,7 +1,8 @@
 // Attention of packed prompts to themselves: tcgen05 tiles (sm_103a).
 //
-// An item is 2 x 128 query rows (128 at head_dim above 128) of one K/V head (2 TT tokens in their packed order, whatever requests they are of, the
-// heads of a group side by side) over the positions that any of them sees, PT_N at a time:
+// An item is 2 x 128 query rows (128 at head_dim above 128, and where there are few) of one K/V head (2 TT tokens in
+// their packed order, whatever requests they are of, the heads of a group side by side) over the positions that any of
+// them sees, PT_N at a time:
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, one buffer a row tile;
 //   softmax       four warps a row tile, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes, O in TMEM.
@@ -82,11 +83,12 @@ template <int DP> struct PtCfg {
 // every row sees the whole tile (it has landed, has been looked through): a barrier's phases count its own uses alone, so
 // that who waits for one is never two behind.  Per row tile: q, qe (an item's Q has
 // landed, is not read any more), s (scores are done), p (the weights of half a tile are written), o (an item's sums are
-// done), of (they have been read), go (it is its turn to issue).  itf, ite: an item is worked out, is done with.  claim: the answer of a claim is there.
+// done), of (they have been read), go (it is its turn to issue).  itf, ite: an item is worked out, is done with.  near:
+// the load of its last tile begins.  claim: the answer of a claim is there.
 // end: every product that was issued is done.
 struct PtBars {
-  u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], q[2], qe[2], s[2], p[2][2], o[2], of[2], vx[PT_STMAX], vc[PT_STMAX], go[2], itf[PT_RING],
-      ite[PT_RING], claim[2], end;
+  u64 kf[PT_STMAX], ke[PT_STMAX], vf[PT_STMAX], ve[PT_STMAX], q[2], qe[2], s[2], p[2][2], o[2], of[2], vx[PT_STMAX],
+      vc[PT_STMAX], go[2], itf[PT_RING], ite[PT_RING], near[PT_RING], claim, end;
 };
 
 struct PtItem {
@@ -165,13 +167,14 @@ __device__ __forceinline__ int claimed_block(const uint4* answer) {
   return got ? static_cast<int>(x) : -1;
 }
 
-// tc_wait in little code.
-__device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone, int* status) {
+// tc_wait in little code.  Some waits are as long as an item, 128 tokens of whose prompt take up to 3 us: the limit grows by
+// a try, some 0.1 us, for each token there is.
+__device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone, const PromptArgs& p) {
 #pragma unroll 1
   for (u32 i = 0; !mbar_wait(bar, parity, 1); ++i)
-    if (__builtin_expect(i >= TC_SPIN || *gone, 0)) {
+    if (__builtin_expect(i >= TC_SPIN + p.N || *gone, 0)) {
       *gone = 1;
-      set_status(status, VBS_ETIMEOUT);
+      set_status(p.status, VBS_ETIMEOUT);
       return false;
     }
   return true;
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   __shared__ u32 tmem_base;
   __shared__ volatile int gone;
   __shared__ volatile int odd;                            // an infinity or NaN of V was put to 0 (stays so)
-  __shared__ __align__(16) uint4 claims[2];
+  __shared__ __align__(16) uint4 claim;
   __shared__ PtItem ring[PT_RING];
   __shared__ int2 span[PT_RING][2 * PT_M];                // positions [x, y) of an item's tokens
   __shared__ float sums[2][2][PT_M];                      // of a row's weights, by the row tile's items in turn
@@ -222,10 +225,10 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     }
     for (int i = 0; i < PT_RING; ++i) {
       mbar_init(&bars.itf[i], 1);
+      mbar_init(&bars.near[i], 1);
       mbar_init(&bars.ite[i], (PT_SM + PT_OUT) / 32 + 3);
     }
-    mbar_init(&bars.claim[0], 1);
-    mbar_init(&bars.claim[1], 1);
+    mbar_init(&bars.claim, 1);
     mbar_init(&bars.end, 2);
     fence_mbar_init();
     gone = 0;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * PT_N;
 
-  auto item_at = [&](int t) { return pt_wait(&bars.itf[t % PT_RING], (t / PT_RING) & 1, &gone, p.status); };
+  auto item_at = [&](int t) { return pt_wait(&bars.itf[t % PT_RING], (t / PT_RING) & 1, &gone, p); };
 
   if (wid < PT_W_OUT) {
     // ---- softmax: thread = row ----
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       float m = -INFINITY, l = 0.f;                       // the reference (in scaled units), the sum of weights
       for (int j = j0; j < j1; ++j, ++S) {
         const int from = x0 - j * PT_N, left = x1 - j * PT_N;
-        ok = __all_sync(FULL, pt_wait(&bars.s[X], S & 1, &gone, p.status));
+        ok = __all_sync(FULL, pt_wait(&bars.s[X], S & 1, &gone, p));
         if (!ok) break;
         tc_fence_after();
         // (the code of a tile is kept short, in loops over its halves: of several warps' long code one pushes the other's
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     const int r = tid & (PT_M - 1), tok_r = r / a.G, g = r - tok_r * a.G;
     const u32 tl = static_cast<u32>((wid & 3) * 32) << 16;
     unsigned char* mine = out_s + (wid - PT_W_OUT) * C::OUT;
-    auto wait = [&](u64* bar, u32 parity) { return __all_sync(FULL, pt_wait(bar, parity, &gone, p.status)) != 0; };
+    auto wait = [&](u64* bar, u32 parity) { return __all_sync(FULL, pt_wait(bar, parity, &gone, p)) != 0; };
     u32 turn = 0, o_turn = 0;                             // of each stage's vx, and of the row tiles' o
     int T = 0;
     bool ok = true;
@@ -507,265 +510,269 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PT_REGS_REST));
     if (wid == PT_W_LOAD) {
-    // ---- loads: one lane ----
-    if (lane == 0) {
-      int T = 0;                                          // tiles of K and V on their way
-      u32 q_turn = 0, q_some = 0;                         // of the row tiles' Q, bit X, and whether there was one
-      u32 whole = 0, look = 0, kind = 0;                  // turns of each stage's vf and vx, and whether vx was the last
-      bool ok = true;
-      for (int t = 0; ok && item_at(t) && ring[t % PT_RING].h >= 0; ++t) {
-        const PtItem& it = ring[t % PT_RING];
-        const int n = it.n, h = it.h, base = it.base, w0 = it.w0, w1 = it.w1;
-        for (int X = 0; X < 2; ++X) {
-          if (it.j1[X] <= it.j0[X]) continue;
-          ok = !(q_some >> X & 1) || pt_wait(&bars.qe[X], (q_turn >> X & 1) ^ 1, &gone, p.status);
-          if (!ok) break;
-          mbar_expect_tx(&bars.q[X], C::SLABS * 128 * a.G * a.TT);
-          for (int x = 0; x < C::SLABS; ++x)
-            tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, it.tok + X * a.TT);
-          q_turn ^= 1u << X;
-          q_some |= 1u << X;
-        }
-        for (int j = 0; ok && j < n; ++j) {
-          const int st = T % ST;
-          const u32 free_turn = ((T / ST) & 1) ^ 1;
-          ok = T < ST || pt_wait(&bars.ke[st], free_turn, &gone, p.status);
-          if (!ok) break;
-          mbar_expect_tx(&bars.kf[st], C::TB);
-          for (int x = 0; x < C::SLABS; ++x)
-            tma_load3(k_a + st * C::TB + x * PT_N * 128, &kmap, &bars.kf[st], x * 64, h, base + j * PT_N);
-          const bool odd_tile = j < w0 || j >= w1;
-          u64* bar = odd_tile ? &bars.vx[st] : &bars.vf[st];
-          ok = T < ST || pt_wait(&bars.ve[st], free_turn, &gone, p.status);
-          if (ok) {
-            mbar_expect_tx(bar, C::TB);
-            for (int x = 0; x < C::SLABS; ++x)
-              tma_load3(v_a + st * C::TB + x * PT_N * 128, &vmap, bar, x * 64, h, base + j * PT_N);
-            if (odd_tile) look ^= 1u << st;
-            else whole ^= 1u << st;
-            kind = (kind & ~(1u << st)) | (odd_tile ? 1u << st : 0u);
-          }
-          ++T;
-        }
-        if (ok) mbar_arrive(&bars.ite[t % PT_RING]);
-      }
-      // no copy is in flight when the CTA ends, also where it gave up: the last ones have landed
-      for (int x = max(0, T - ST); x < T; ++x) {
-        const int st = x % ST;
-        mbar_wait(&bars.kf[st], (x / ST) & 1, 1u << 16);
-        mbar_wait(kind >> st & 1 ? &bars.vx[st] : &bars.vf[st], ((kind >> st & 1 ? look : whole) >> st & 1) ^ 1, 1u << 16);
-      }
-      for (int X = 0; X < 2; ++X)
-        if (q_some >> X & 1) mbar_wait(&bars.q[X], (q_turn >> X & 1) ^ 1, 1u << 16);
-    }
-    __syncwarp();
-    } else if (wid < PT_W_MMA + 2) {
-    // ---- products: a warp a row tile, of which one thread waits and issues.  The scores of the next tile, be it the
-    // next item's first, follow the product with V ----
-    if (elect_one()) {
-      const int X = wid - PT_W_MMA;
-      const u32 dq = static_cast<u32>(tc_desc(q_a + X * C::QB, 16)), dk = static_cast<u32>(tc_desc(k_a, 16)),
-                dv = static_cast<u32>(tc_desc(v_a, PT_N * 128)), ts = tm_s + X * PT_N, to = tm_o + X * DP;
-      u32 go_turn = X ? 0 : 1;                            // the first row tile's turn comes first
-      u32 p_turn = 0, o_turn = 1, q_turn = 0;             // of the row tile's barriers
-      u32 whole = 0, look = 0;                            // and of each stage's vf and vc
-      auto wait = [&](u64* bar, u32 parity) { return pt_wait(bar, parity, &gone, p.status); };
-      int at = 0, t = 0, j = 0, n = 0, j0 = 0, j1 = 0, y1 = 0, w0 = 0, w1 = 0;
-      u32 turns = 0;                                      // whether the row tiles take turns over this item
-      // Item t, as the row tile sees it; whether there is one.
-      auto take = [&] {
-        if (!item_at(t)) return false;
-        const PtItem& i = ring[t % PT_RING];
-        n = i.n, j0 = i.j0[X], j1 = i.j1[X], y1 = i.y1[X], w0 = i.w0, w1 = i.w1, j = 0;
-        turns = n >= PT_TURNS ? 1u : 0u;
-        return i.h >= 0;
-      };
-      bool go = take();
-      int steps = 0;                                      // of the tile whose weights come next; 0: not this row tile's
-      bool first = false, last = false;
-      // (the loop's first half has nothing to do yet)
-      for (bool begin = true; go; begin = false) {
-        if (!begin) {
-          const int st = at % ST;
-          const bool clear = j >= w0 && j < w1;
-          if (!wait(clear ? &bars.vf[st] : &bars.vc[st], (clear ? whole : look) >> st & 1)) break;
-          if (clear) whole ^= 1u << st;
-          else look ^= 1u << st;
-          if (steps > 0) {
-            if (first) {                                  // the item before has been read
-              if (!wait(&bars.of[X], o_turn)) break;
-              o_turn ^= 1;
-            }
-            const u32 d = dv + st * (C::TB >> 4);
-            u32 acc = first ? 0 : 1;
-            bool ok = true;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              ok = wait(&bars.p[X][half], p_turn) && (half == 0 || !turns || wait(&bars.go[X], go_turn));
-              if (!ok) break;
-              tc_fence_after();
-              const u32 w = ts + half * (PT_N / 4), v = d + half * (PT_N / 2 * 128 >> 4);
-              if (steps >= (half + 1) * (PT_N / 32)) {
-#pragma unroll
-                for (int k = 0; k < PT_N / 32; ++k) tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
-              } else {
-#pragma unroll 1
-                for (int k = 0; k < steps - half * (PT_N / 32); ++k)
-                  tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
-              }
-              acc = 1;
-            }
+      // ---- loads: one lane ----
+      if (lane == 0) {
+        int T = 0;                                          // tiles of K and V on their way
+        u32 q_turn = 0, q_some = 0;                         // of the row tiles' Q, bit X, and whether there was one
+        u32 whole = 0, look = 0, kind = 0;                  // turns of each stage's vf and vx, and whether vx was the last
+        bool ok = true;
+        for (int t = 0; ok && item_at(t) && ring[t % PT_RING].h >= 0; ++t) {
+          const PtItem& it = ring[t % PT_RING];
+          const int n = it.n, h = it.h, base = it.base, w0 = it.w0, w1 = it.w1;
+          for (int X = 0; X < 2; ++X) {
+            if (it.j1[X] <= it.j0[X]) continue;
+            ok = !(q_some >> X & 1) || pt_wait(&bars.qe[X], (q_turn >> X & 1) ^ 1, &gone, p);
             if (!ok) break;
-            go_turn ^= turns;
-            p_turn ^= 1;
-            tc_commit(&bars.ve[st]);                      // V may be loaded again
-            if (last) tc_commit(&bars.o[X]);
-          } else {
-            mbar_arrive(&bars.ve[st]);
-            if (turns && !wait(&bars.go[X], go_turn)) break;
-            go_turn ^= turns;
+            mbar_expect_tx(&bars.q[X], C::SLABS * 128 * a.G * a.TT);
+            for (int x = 0; x < C::SLABS; ++x)
+              tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, it.tok + X * a.TT);
+            q_turn ^= 1u << X;
+            q_some |= 1u << X;
           }
-          ++at;
-          if (++j == n) {
-            if (turns) mbar_arrive(&bars.go[X ^ 1]);
-            mbar_arrive(&bars.ite[t % PT_RING]);
-            ++t;
-            go = take();
-            if (!go) break;
-          }
-        }
-        const int st = at % ST;
-        const bool on = j >= j0 && j < j1;
-        steps = on ? steps_of(y1, j) : 0;
-        first = j == j0;
-        last = j + 1 == j1;
-        if (!wait(&bars.kf[st], (at / ST) & 1)) break;
-        if (steps > 0) {
-          if (first) {
-            if (!wait(&bars.q[X], q_turn)) break;
-            q_turn ^= 1;
-          }
-          const u32 d = dk + st * (C::TB >> 4);
-          if (steps == PT_N / 16) {
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-              const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
-              tc_mma_ss_at(ts, dq + in, d + in, tc_idesc(PT_N, false), k > 0);
+          for (int j = 0; ok && j < n; ++j) {
+            if (j == n - 1) mbar_arrive(&bars.near[t % PT_RING]);
+            const int st = T % ST;
+            const u32 free_turn = ((T / ST) & 1) ^ 1;
+            ok = T < ST || pt_wait(&bars.ke[st], free_turn, &gone, p);
+            if (!ok) break;
+            mbar_expect_tx(&bars.kf[st], C::TB);
+            for (int x = 0; x < C::SLABS; ++x)
+              tma_load3(k_a + st * C::TB + x * PT_N * 128, &kmap, &bars.kf[st], x * 64, h, base + j * PT_N);
+            const bool odd_tile = j < w0 || j >= w1;
+            u64* bar = odd_tile ? &bars.vx[st] : &bars.vf[st];
+            ok = T < ST || pt_wait(&bars.ve[st], free_turn, &gone, p);
+            if (ok) {
+              mbar_expect_tx(bar, C::TB);
+              for (int x = 0; x < C::SLABS; ++x)
+                tma_load3(v_a + st * C::TB + x * PT_N * 128, &vmap, bar, x * 64, h, base + j * PT_N);
+              if (odd_tile) look ^= 1u << st;
+              else whole ^= 1u << st;
+              kind = (kind & ~(1u << st)) | (odd_tile ? 1u << st : 0u);
             }
-          } else {
-            const u32 what = tc_idesc(steps * 16, false);
-#pragma unroll 1
-            for (int k = 0; k < DP / 16; ++k) {
-              const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
-              tc_mma_ss_at(ts, dq + in, d + in, what, k > 0);
-            }
+            ++T;
           }
-          tc_commit(&bars.s[X]);
-          tc_commit(&bars.ke[st]);                        // K, and after the item's last Q, may be loaded again
-          if (last) tc_commit(&bars.qe[X]);
-        } else {
-          mbar_arrive(&bars.ke[st]);
+          if (ok) mbar_arrive(&bars.ite[t % PT_RING]);
         }
-        if (!begin && j > 0 && turns) mbar_arrive(&bars.go[X ^ 1]);
-      }
-      // the products in flight read shared memory and TMEM: all are done before either goes, also where the CTA gave up
-      tc_commit(&bars.end);
-      mbar_wait(&bars.end, 0, 1u << 16);
-    }
-    __syncwarp();
-    } else {
-    // ---- items: the last tokens first, which see the most ----
-    int t = 0, c = 0, i, left;                            // this item, and how many from it on are claimed; 0: none is
-    auto take = [&](int block) {
-      i = block < a.many ? block * a.batch : a.many * a.batch + block - a.many;
-      left = block < 0 ? 0 : (block < a.many ? a.batch : 1);
-    };
-    take(blockIdx.x);
-    while (true) {
-      const bool last = left == 0;
-      // the slot's item before is done with; the next items are claimed (no earlier: another CTA may be sooner) while the
-      // last of these is worked out
-      if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p.status))) break;
-      if (left == 1 && lane == 0) claim_block(&claims[c & 1], &bars.claim[c & 1]);
-      PtItem& x = ring[t % PT_RING];
-      const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * a.per;
-      int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
-      if (!last) {
-        int b = request_before(p, cu, every, tok0, lane);
-        int2 at = request_at(p, cu, every, b);
-        const int end = min(a.per, p.N - tok0);
-        for (int w = lane; w < 2 * PT_M; w += 32) {
-          const int tok = tok0 + w;
-          if (!__all_sync(FULL, (tok >= at.x && tok < at.y) || w >= end)) {
-            // the group's tokens are of several requests: each lane goes on to its own
-            while (b + 1 < p.B && (every == 1 ? cu[b + 1] : p.cu[b + 1]) <= tok && w < end) ++b;
-            __syncwarp();
-            at = request_at(p, cu, every, b);
-          }
-          const bool live = w < end && tok >= at.x && tok < at.y;
-          const int2 sp = live ? make_int2(at.x, p.causal ? tok + 1 : at.y) : make_int2(0, 0);
-#pragma unroll
-          for (int X = 0; X < 2; ++X)
-            if (live && (w >= a.TT) == (X == 1)) {
-              y0[X] = min(y0[X], sp.x);
-              y1[X] = max(y1[X], sp.y);
-              z0[X] = max(z0[X], sp.x);
-              z1[X] = min(z1[X], sp.y);
-            }
-          span[t % PT_RING][w] = sp;
-          if (w + 32 - lane >= a.per) break;
-          b = __shfl_sync(FULL, b, 31);                   // (the last token's)
-          at = make_int2(__shfl_sync(FULL, at.x, 31), __shfl_sync(FULL, at.y, 31));
+        // no copy is in flight when the CTA ends, also where it gave up: the last ones have landed
+        for (int x = max(0, T - ST); x < T; ++x) {
+          const int st = x % ST;
+          mbar_wait(&bars.kf[st], (x / ST) & 1, 1u << 16);
+          mbar_wait(kind >> st & 1 ? &bars.vx[st] : &bars.vf[st], ((kind >> st & 1 ? look : whole) >> st & 1) ^ 1, 1u << 16);
         }
-      }
-#pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        y0[X] = __reduce_min_sync(FULL, y0[X]);
-        y1[X] = __reduce_max_sync(FULL, y1[X]);
-        z0[X] = __reduce_max_sync(FULL, z0[X]);
-        z1[X] = __reduce_min_sync(FULL, z1[X]);
-      }
-      const int base = min(y0[0], y0[1]);
-      const bool some = max(y1[0], y1[1]) > 0;            // (else: tokens of no request)
-      if ((some || last) && lane == 0) {
-        x.h = h;
-        x.tok = tok0;
-        x.base = base;
-        int n = 0, w0 = 0, w1 = INT_MAX;
-#pragma unroll
-        for (int X = 0; X < 2; ++X) {
-          const bool on = y1[X] > 0;
-          x.y1[X] = on ? y1[X] - base : 0;
-          x.j0[X] = on ? (y0[X] - base) / PT_N : 0;
-          x.j1[X] = on ? (y1[X] - base + PT_N - 1) / PT_N : 0;
-          if (on) {
-            n = max(n, (y1[X] - base + PT_N - 1) / PT_N);
-            w0 = max(w0, (z0[X] - base + PT_N - 1) / PT_N);
-            w1 = min(w1, (z1[X] - base) / PT_N);
-          }
-        }
-        x.n = n;
-        x.w0 = w0;
-        x.w1 = w1;
+        for (int X = 0; X < 2; ++X)
+          if (q_some >> X & 1) mbar_wait(&bars.q[X], (q_turn >> X & 1) ^ 1, 1u << 16);
       }
       __syncwarp();
-      if (some || last) {
-        if (lane == 0) mbar_arrive(&bars.itf[t % PT_RING]);
-        ++t;
-      }
-      if (last) break;
-      if (left > 1) {
-        ++i;
-        --left;
-      } else {
-        if (!__all_sync(FULL, pt_wait(&bars.claim[c & 1], c >> 1 & 1, &gone, p.status))) {
-          mbar_wait(&bars.claim[c & 1], c >> 1 & 1, 1u << 16);   // (the answer is in flight)
-          break;
+    } else if (wid < PT_W_MMA + 2) {
+      // ---- products: a warp a row tile, of which one thread waits and issues.  The scores of the next tile, be it the
+      // next item's first, follow the product with V ----
+      if (elect_one()) {
+        const int X = wid - PT_W_MMA;
+        const u32 dq = static_cast<u32>(tc_desc(q_a + X * C::QB, 16)), dk = static_cast<u32>(tc_desc(k_a, 16)),
+                  dv = static_cast<u32>(tc_desc(v_a, PT_N * 128)), ts = tm_s + X * PT_N, to = tm_o + X * DP;
+        u32 go_turn = X ? 0 : 1;                            // the first row tile's turn comes first
+        u32 p_turn = 0, o_turn = 1, q_turn = 0;             // of the row tile's barriers
+        u32 whole = 0, look = 0;                            // and of each stage's vf and vc
+        auto wait = [&](u64* bar, u32 parity) { return pt_wait(bar, parity, &gone, p); };
+        int at = 0, t = 0, j = 0, n = 0, j0 = 0, j1 = 0, y1 = 0, w0 = 0, w1 = 0;
+        u32 turns = 0;                                      // whether the row tiles take turns over this item
+        // Item t, as the row tile sees it; whether there is one.
+        auto take = [&] {
+          if (!item_at(t)) return false;
+          const PtItem& i = ring[t % PT_RING];
+          n = i.n, j0 = i.j0[X], j1 = i.j1[X], y1 = i.y1[X], w0 = i.w0, w1 = i.w1, j = 0;
+          turns = n >= PT_TURNS ? 1u : 0u;
+          return i.h >= 0;
+        };
+        bool go = take();
+        int steps = 0;                                      // of the tile whose weights come next; 0: not this row tile's
+        bool first = false, last = false;
+        // (the loop's first half has nothing to do yet)
+        for (bool begin = true; go; begin = false) {
+          if (!begin) {
+            const int st = at % ST;
+            const bool clear = j >= w0 && j < w1;
+            if (!wait(clear ? &bars.vf[st] : &bars.vc[st], (clear ? whole : look) >> st & 1)) break;
+            if (clear) whole ^= 1u << st;
+            else look ^= 1u << st;
+            if (steps > 0) {
+              if (first) {                                  // the item before has been read
+                if (!wait(&bars.of[X], o_turn)) break;
+                o_turn ^= 1;
+              }
+              const u32 d = dv + st * (C::TB >> 4);
+              u32 acc = first ? 0 : 1;
+              bool ok = true;
+  #pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                ok = wait(&bars.p[X][half], p_turn) && (half == 0 || !turns || wait(&bars.go[X], go_turn));
+                if (!ok) break;
+                tc_fence_after();
+                const u32 w = ts + half * (PT_N / 4), v = d + half * (PT_N / 2 * 128 >> 4);
+                if (steps >= (half + 1) * (PT_N / 32)) {
+  #pragma unroll
+                  for (int k = 0; k < PT_N / 32; ++k) tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
+                } else {
+  #pragma unroll 1
+                  for (int k = 0; k < steps - half * (PT_N / 32); ++k)
+                    tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
+                }
+                acc = 1;
+              }
+              if (!ok) break;
+              go_turn ^= turns;
+              p_turn ^= 1;
+              tc_commit(&bars.ve[st]);                      // V may be loaded again
+              if (last) tc_commit(&bars.o[X]);
+            } else {
+              mbar_arrive(&bars.ve[st]);
+              if (turns && !wait(&bars.go[X], go_turn)) break;
+              go_turn ^= turns;
+            }
+            ++at;
+            if (++j == n) {
+              if (turns) mbar_arrive(&bars.go[X ^ 1]);
+              mbar_arrive(&bars.ite[t % PT_RING]);
+              ++t;
+              go = take();
+              if (!go) break;
+            }
+          }
+          const int st = at % ST;
+          const bool on = j >= j0 && j < j1;
+          steps = on ? steps_of(y1, j) : 0;
+          first = j == j0;
+          last = j + 1 == j1;
+          if (!wait(&bars.kf[st], (at / ST) & 1)) break;
+          if (steps > 0) {
+            if (first) {
+              if (!wait(&bars.q[X], q_turn)) break;
+              q_turn ^= 1;
+            }
+            const u32 d = dk + st * (C::TB >> 4);
+            if (steps == PT_N / 16) {
+  #pragma unroll
+              for (int k = 0; k < DP / 16; ++k) {
+                const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
+                tc_mma_ss_at(ts, dq + in, d + in, tc_idesc(PT_N, false), k > 0);
+              }
+            } else {
+              const u32 what = tc_idesc(steps * 16, false);
+  #pragma unroll 1
+              for (int k = 0; k < DP / 16; ++k) {
+                const u32 in = (k >> 2) * (PT_M * 128 >> 4) + (k & 3) * 2;
+                tc_mma_ss_at(ts, dq + in, d + in, what, k > 0);
+              }
+            }
+            tc_commit(&bars.s[X]);
+            tc_commit(&bars.ke[st]);                        // K, and after the item's last Q, may be loaded again
+            if (last) tc_commit(&bars.qe[X]);
+          } else {
+            mbar_arrive(&bars.ke[st]);
+          }
+          if (!begin && j > 0 && turns) mbar_arrive(&bars.go[X ^ 1]);
         }
-        take(claimed_block(&claims[c & 1]));
-        ++c;
+        // the products in flight read shared memory and TMEM: all are done before either goes, also where the CTA gave up
+        tc_commit(&bars.end);
+        mbar_wait(&bars.end, 0, 1u << 16);
       }
-    }
+      __syncwarp();
+    } else {
+      // ---- items: the last tokens first, which see the most ----
+      int t = 0, c = 0, i, left;                            // this item, and how many from it on are claimed; 0: none is
+      auto take = [&](int block) {
+        i = block < a.many ? block * a.batch : a.many * a.batch + block - a.many;
+        left = block < 0 ? 0 : (block < a.many ? a.batch : 1);
+      };
+      take(blockIdx.x);
+      while (true) {
+        const bool last = left == 0;
+        // the slot's item before is done with
+        if (t >= PT_RING && !__all_sync(FULL, pt_wait(&bars.ite[t % PT_RING], ((t / PT_RING) - 1) & 1, &gone, p))) break;
+        PtItem& x = ring[t % PT_RING];
+        const int tile = i / p.H, h = last ? -1 : i - tile * p.H, tok0 = (a.tiles - 1 - tile) * a.per;
+        int y0[2] = {INT_MAX, INT_MAX}, y1[2] = {0, 0}, z0[2] = {0, 0}, z1[2] = {INT_MAX, INT_MAX};   // of x and y of the spans
+        if (!last) {
+          int b = request_before(p, cu, every, tok0, lane);
+          int2 at = request_at(p, cu, every, b);
+          const int end = min(a.per, p.N - tok0);
+          for (int w = lane; w < 2 * PT_M; w += 32) {
+            const int tok = tok0 + w;
+            if (!__all_sync(FULL, (tok >= at.x && tok < at.y) || w >= end)) {
+              // the group's tokens are of several requests: each lane goes on to its own
+              while (b + 1 < p.B && (every == 1 ? cu[b + 1] : p.cu[b + 1]) <= tok && w < end) ++b;
+              __syncwarp();
+              at = request_at(p, cu, every, b);
+            }
+            const bool live = w < end && tok >= at.x && tok < at.y;
+            const int2 sp = live ? make_int2(at.x, p.causal ? tok + 1 : at.y) : make_int2(0, 0);
+  #pragma unroll
+            for (int X = 0; X < 2; ++X)
+              if (live && (w >= a.TT) == (X == 1)) {
+                y0[X] = min(y0[X], sp.x);
+                y1[X] = max(y1[X], sp.y);
+                z0[X] = max(z0[X], sp.x);
+                z1[X] = min(z1[X], sp.y);
+              }
+            span[t % PT_RING][w] = sp;
+            if (w + 32 - lane >= a.per) break;
+            b = __shfl_sync(FULL, b, 31);                   // (the last token's)
+            at = make_int2(__shfl_sync(FULL, at.x, 31), __shfl_sync(FULL, at.y, 31));
+          }
+        }
+  #pragma unroll
+        for (int X = 0; X < 2; ++X) {
+          y0[X] = __reduce_min_sync(FULL, y0[X]);
+          y1[X] = __reduce_max_sync(FULL, y1[X]);
+          z0[X] = __reduce_max_sync(FULL, z0[X]);
+          z1[X] = __reduce_min_sync(FULL, z1[X]);
+        }
+        const int base = min(y0[0], y0[1]);
+        const bool some = max(y1[0], y1[1]) > 0;            // (else: tokens of no request)
+        if ((some || last) && lane == 0) {
+          x.h = h;
+          x.tok = tok0;
+          x.base = base;
+          int n = 0, w0 = 0, w1 = INT_MAX;
+  #pragma unroll
+          for (int X = 0; X < 2; ++X) {
+            const bool on = y1[X] > 0;
+            x.y1[X] = on ? y1[X] - base : 0;
+            x.j0[X] = on ? (y0[X] - base) / PT_N : 0;
+            x.j1[X] = on ? (y1[X] - base + PT_N - 1) / PT_N : 0;
+            if (on) {
+              n = max(n, (y1[X] - base + PT_N - 1) / PT_N);
+              w0 = max(w0, (z0[X] - base + PT_N - 1) / PT_N);
+              w1 = min(w1, (z1[X] - base) / PT_N);
+            }
+          }
+          x.n = n;
+          x.w0 = w0;
+          x.w1 = w1;
+        }
+        __syncwarp();
+        if (some || last) {
+          if (lane == 0) mbar_arrive(&bars.itf[t % PT_RING]);
+          ++t;
+        }
+        if (last) break;
+        if (left > 1) {
+          ++i;
+          --left;
+        } else {
+          // the next is claimed when this one's last tile is about to be loaded: claimed as far ahead as the ring goes, items
+          // stay with a CTA that is late with them (6001 tokens x 32 heads: 250 against 223 us, 9000 x 8: 180 against 129,
+          // 16001 x 32: 1409 against 1393, 64 x 1000: 573 against 559; requests of a few tiles the same either way)
+          if (some && !__all_sync(FULL, pt_wait(&bars.near[(t - 1) % PT_RING], (t - 1) / PT_RING & 1, &gone, p))) break;
+          if (lane == 0) claim_block(&claim, &bars.claim);
+          if (!__all_sync(FULL, pt_wait(&bars.claim, c & 1, &gone, p))) {
+            mbar_wait(&bars.claim, c & 1, 1u << 16);   // (the answer is in flight)
+            break;
+          }
+          take(claimed_block(&claim));
+          ++c;
+        }
+      }
     }
   }
   __syncthreads();
