@@ -6,8 +6,9 @@
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, one buffer a row tile;
 //   softmax       four warps a row tile, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes, O in TMEM.
-// The row tiles share K and V.  Of the other warps one loads Q, K and V by TMA, one a row tile issues its products, four
-// look through V (below) and bring results out, and one works out the next items: which positions each token sees.
+// The row tiles share K and V.  Of the other warps one loads K and V by TMA, one a row tile issues its products, four
+// look through V (below) and bring results out, and one works out the next items (which positions each token sees) and
+// loads their Q.
 // The grid has a block an item, but a CTA goes on with the items of blocks that have not started (cluster launch
 // control), so that CTAs share the work out whatever the requests' lengths, the longest rows first.
 //
@@ -55,8 +56,9 @@ constexpr int PT_CU = 2048;               // request starts held in shared memor
 constexpr int PT_STMAX = 4;
 // Items of this many tiles and more: the row tiles' products go in turn, so that one's run while the other's softmax
 // does.  Left alone both fall into step and wait together (16001 tokens: 1605 us alone, 1432 in turn; 64 x 1000, whose
-// items have up to 9 tiles: 588 and 592; 128 sentences up to 256: 51 and 53).
-constexpr int PT_TURNS = 12;
+// items have up to 9 tiles: 567 alone, 553 in turn from 5 tiles on, 559 from 7; 128 sentences up to 256: 43 alone, 45 in
+// turn from 3 on).
+constexpr int PT_TURNS = 5;
 // registers a thread: 65,536 / 512 at launch, then the softmax threads take what the others leave
 constexpr int PT_REGS = 128, PT_REGS_SM = 168, PT_REGS_OUT = 104, PT_REGS_REST = 72;
 static_assert(PT_SM * PT_REGS_SM + PT_OUT * PT_REGS_OUT + 128 * PT_REGS_REST <= PT_NT * PT_REGS, "registers of the block");
@@ -399,45 +401,55 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     u32 turn = 0, o_turn = 0;                             // of each stage's vx, and of the row tiles' o
     int T = 0;
     bool ok = true;
+    int looked = 0;                                       // tiles of the next item that have been looked through
     for (int t = 0; ok; ++t) {
       if (!wait(&bars.itf[t % PT_RING], (t / PT_RING) & 1)) break;
-      const PtItem& it = ring[t % PT_RING];
-      if (it.h < 0) break;
+      if (ring[t % PT_RING].h < 0) break;
 #pragma unroll 1
-      for (int j = 0; j < it.n; ++j) {
-        if (j >= it.w0 && j < it.w1) continue;
-        const int st = (T + j) % ST;
-        ok = wait(&bars.vx[st], turn >> st & 1);
-        if (!ok) break;
-        turn ^= 1u << st;
-#pragma unroll
-        for (int sl = 0; sl < C::SLABS; ++sl) {
-          uint4* row = reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (PT_N * 128) + r * 128);
-          u32 worst = 0;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 w = row[(c + r) & 7];           // (eight rows meet eight different chunks)
-            worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
-          }
-          if ((worst & 0x7f80u) == 0x7f80u || (worst & 0x7f800000u) == 0x7f800000u) {
+      for (int u = t; u <= t + 1 && ok; ++u) {
+        // the next item's first tiles too, where it is there, so that they do not wait for this one's results
+        if (u > t && !__all_sync(FULL, mbar_wait(&bars.itf[u % PT_RING], (u / PT_RING) & 1, 1))) break;
+        const PtItem& it = ring[u % PT_RING];
+        if (it.h < 0) break;
+        const int e = u == t ? it.n : min(it.n, ST / 2);
 #pragma unroll 1
+        for (int j = u == t ? looked : 0; j < e; ++j) {
+          if (j >= it.w0 && j < it.w1) continue;
+          const int st = (T + j) % ST;
+          ok = wait(&bars.vx[st], turn >> st & 1);
+          if (!ok) break;
+          turn ^= 1u << st;
+#pragma unroll
+          for (int sl = 0; sl < C::SLABS; ++sl) {
+            uint4* row = reinterpret_cast<uint4*>(smem + (v_a - q_a) + st * C::TB + sl * (PT_N * 128) + r * 128);
+            u32 worst = 0;
+#pragma unroll
             for (int c = 0; c < 8; ++c) {
-              uint4 w = row[c];
-              u32* e = &w.x;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((e[i] & 0x7f80u) == 0x7f80u) e[i] &= 0xffff0000u;
-                if ((e[i] & 0x7f800000u) == 0x7f800000u) e[i] &= 0x0000ffffu;
-              }
-              row[c] = w;
+              const uint4 w = row[(c + r) & 7];           // (eight rows meet eight different chunks)
+              worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
             }
-            odd = 1;
+            if ((worst & 0x7f80u) == 0x7f80u || (worst & 0x7f800000u) == 0x7f800000u) {
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint4 w = row[c];
+                u32* e = &w.x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if ((e[i] & 0x7f80u) == 0x7f80u) e[i] &= 0xffff0000u;
+                  if ((e[i] & 0x7f800000u) == 0x7f800000u) e[i] &= 0x0000ffffu;
+                }
+                row[c] = w;
+              }
+              odd = 1;
+            }
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(&bars.vc[st]);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&bars.vc[st]);
+        if (u == t) T += it.n;
+        looked = u == t ? 0 : e;
       }
-      T += it.n;
+      const PtItem& it = ring[t % PT_RING];
 #pragma unroll 1
       for (int X = 0; X < 2 && ok; ++X) {
         if (it.j1[X] <= it.j0[X]) continue;
@@ -513,22 +525,11 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       // ---- loads: one lane ----
       if (lane == 0) {
         int T = 0;                                          // tiles of K and V on their way
-        u32 q_turn = 0, q_some = 0;                         // of the row tiles' Q, bit X, and whether there was one
         u32 whole = 0, look = 0, kind = 0;                  // turns of each stage's vf and vx, and whether vx was the last
         bool ok = true;
         for (int t = 0; ok && item_at(t) && ring[t % PT_RING].h >= 0; ++t) {
           const PtItem& it = ring[t % PT_RING];
           const int n = it.n, h = it.h, base = it.base, w0 = it.w0, w1 = it.w1;
-          for (int X = 0; X < 2; ++X) {
-            if (it.j1[X] <= it.j0[X]) continue;
-            ok = !(q_some >> X & 1) || pt_wait(&bars.qe[X], (q_turn >> X & 1) ^ 1, &gone, p);
-            if (!ok) break;
-            mbar_expect_tx(&bars.q[X], C::SLABS * 128 * a.G * a.TT);
-            for (int x = 0; x < C::SLABS; ++x)
-              tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, it.tok + X * a.TT);
-            q_turn ^= 1u << X;
-            q_some |= 1u << X;
-          }
           for (int j = 0; ok && j < n; ++j) {
             if (j == n - 1) mbar_arrive(&bars.near[t % PT_RING]);
             const int st = T % ST;
@@ -559,8 +560,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           mbar_wait(&bars.kf[st], (x / ST) & 1, 1u << 16);
           mbar_wait(kind >> st & 1 ? &bars.vx[st] : &bars.vf[st], ((kind >> st & 1 ? look : whole) >> st & 1) ^ 1, 1u << 16);
         }
-        for (int X = 0; X < 2; ++X)
-          if (q_some >> X & 1) mbar_wait(&bars.q[X], (q_turn >> X & 1) ^ 1, 1u << 16);
       }
       __syncwarp();
     } else if (wid < PT_W_MMA + 2) {
@@ -679,6 +678,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       __syncwarp();
     } else {
       // ---- items: the last tokens first, which see the most ----
+      u32 q_turn = 0, q_some = 0;                           // of the row tiles' Q, bit X, and whether there was one
       int t = 0, c = 0, i, left;                            // this item, and how many from it on are claimed; 0: none is
       auto take = [&](int block) {
         i = block < a.many ? block * a.batch : a.many * a.batch + block - a.many;
@@ -756,6 +756,24 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           ++t;
         }
         if (last) break;
+        if (some) {
+          // its Q, as soon as the item before does not read its own any more (here, so that K and V do not wait for that)
+          bool ok = true;
+#pragma unroll 1
+          for (int X = 0; X < 2; ++X) {
+            if ((X ? y1[1] : y1[0]) == 0) continue;
+            ok = !(q_some >> X & 1) || __all_sync(FULL, pt_wait(&bars.qe[X], (q_turn >> X & 1) ^ 1, &gone, p));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_expect_tx(&bars.q[X], C::SLABS * 128 * a.G * a.TT);
+              for (int x = 0; x < C::SLABS; ++x)
+                tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, tok0 + X * a.TT);
+            }
+            q_turn ^= 1u << X;
+            q_some |= 1u << X;
+          }
+          if (!ok) break;
+        }
         if (left > 1) {
           ++i;
           --left;
@@ -773,6 +791,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           ++c;
         }
       }
+      // (no copy is in flight when the CTA ends, also where it gave up)
+      for (int X = 0; X < 2; ++X)
+        if (q_some >> X & 1) mbar_wait(&bars.q[X], (q_turn >> X & 1) ^ 1, 1u << 16);
     }
   }
   __syncthreads();
