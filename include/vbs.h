@@ -561,6 +561,23 @@ int rope_init(vbs_rope** ctx, int head_dim, int rot, int layout, const double* f
 int rope_apply(const vbs_rope* ctx, int64_t n, const int32_t* pos, int dtype, const void* q, int64_t q_tok, int64_t q_head,
                void* q_out, int64_t qo_tok, int64_t qo_head, int q_heads, const void* k, int64_t k_tok, int64_t k_head,
                void* k_out, int64_t ko_tok, int64_t ko_head, int k_heads, vbs_stream_t stream);
+/* The same, its arguments in one struct (host, read before the call returns): where a foreign-function interface converts
+   them one by one, that costs as much as the launch does.  kv16_append and pattn_run have such a form too. */
+typedef struct vbs_rope_args {
+  int64_t n;
+  const int32_t* pos;
+  const void* q;
+  int64_t q_tok, q_head;
+  void* q_out;
+  int64_t qo_tok, qo_head;
+  const void* k;
+  int64_t k_tok, k_head;
+  void* k_out;
+  int64_t ko_tok, ko_head;
+  vbs_stream_t stream;
+  int dtype, q_heads, k_heads;
+} vbs_rope_args;
+int rope_apply_args(const vbs_rope* ctx, const vbs_rope_args* args);
 /* Free the context (work that uses it must have completed).  NULL is a no-op.  Returns VBS_OK. */
 int rope_destroy(vbs_rope* ctx);
 
@@ -592,6 +609,24 @@ int kv16_append(vbs_kv16* ctx, int layer, int64_t n, const int64_t* slots, int d
                 int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const vbs_rope* rope, const int32_t* pos,
                 void* k_out, int64_t ko_tok, int64_t ko_head, const void* q, int64_t q_tok, int64_t q_head, void* q_out,
                 int64_t qo_tok, int64_t qo_head);
+typedef struct vbs_kv16_args {
+  int64_t n;
+  const int64_t* slots;
+  const void* k;
+  int64_t k_tok, k_head;
+  const void* v;
+  int64_t v_tok, v_head;
+  const vbs_rope* rope;
+  const int32_t* pos;
+  void* k_out;
+  int64_t ko_tok, ko_head;
+  const void* q;
+  int64_t q_tok, q_head;
+  void* q_out;
+  int64_t qo_tok, qo_head;
+  int layer, dtype;
+} vbs_kv16_args;
+int kv16_append_args(vbs_kv16* ctx, const vbs_kv16_args* args);
 /* kv8_plan for this cache: the same arguments, results and errors; kv16_attention keeps to it as kv8_attention does. */
 int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
 /*
@@ -636,6 +671,21 @@ int pattn_init(vbs_pattn** ctx, int q_heads, int kv_heads, int head_dim, vbs_str
 int pattn_run(vbs_pattn* ctx, int64_t n, int batch, const int32_t* cu, const void* q, int64_t q_tok, int64_t q_head,
               const void* k, int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int causal,
               float scale, void* out, int64_t o_tok, int64_t o_head);
+typedef struct vbs_pattn_args {
+  int64_t n;
+  const int32_t* cu;
+  const void* q;
+  int64_t q_tok, q_head;
+  const void* k;
+  int64_t k_tok, k_head;
+  const void* v;
+  int64_t v_tok, v_head;
+  void* out;
+  int64_t o_tok, o_head;
+  int batch, causal;
+  float scale;
+} vbs_pattn_args;
+int pattn_run_args(vbs_pattn* ctx, const vbs_pattn_args* args);
 /* The kernel that the context's last pattn_run took: *tiles 1 for the tcgen05 tiles, 0 for the other, -1 before the
    first run.  Errors: VBS_EINVAL (NULL arguments). */
 int pattn_kernel(vbs_pattn* ctx, int* tiles);

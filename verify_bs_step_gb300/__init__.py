@@ -10,10 +10,12 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
-__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "PagedKV16", "CrossAttention", "PromptAttention", "Rotary", "kv_reorder", "bpd_propose", "bpd_verify", "VbsError", "lib",
+__all__ = ["BeamSearch", "PagedKV", "PagedKV8", "PagedKV16", "CrossAttention", "PromptAttention", "Rotary", "kv_reorder", "bpd_propose",
+           "bpd_verify", "VbsError", "lib",
            "LP_GNMT", "LP_POWER", "ES_FALSE", "ES_TRUE", "ES_NEVER", "F32", "BF16", "BPD_EXACT", "BPD_TOPK",
            "BPD_DISTANCE", "gather_shard_partials"]
 
@@ -30,6 +32,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvbs.so")
 CHECKED_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvbs_checked.so")
 
 _c_int, _c_i64, _c_f, _c_d, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_void_p
+_c_bytes = ctypes.c_char_p                     # a packed struct of arguments
 _pp = ctypes.POINTER(ctypes.c_void_p)
 
 # name -> (restype, argtypes); mirrors include/vbs.h
@@ -70,16 +73,19 @@ SIGNATURES = {
     "rope_init": (_c_int, [_pp, _c_int, _c_int, _c_int, ctypes.POINTER(_c_d), _c_d]),
     "rope_apply": (_c_int, [_vp, _c_i64, _vp, _c_int, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_i64,
                             _vp, _c_i64, _c_i64, _c_int, _vp]),
+    "rope_apply_args": (_c_int, [_vp, _c_bytes]),
     "rope_destroy": (_c_int, [_vp]),
     "kv16_init": (_c_int, [_pp, _vp, _c_int, _c_int]),
     "kv16_append": (_c_int, [_vp, _c_int, _c_i64, _vp, _c_int, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64,
                              _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64]),
+    "kv16_append_args": (_c_int, [_vp, _c_bytes]),
     "kv16_plan": (_c_int, [_vp, _vp, _c_int]),
     "kv16_attention": (_c_int, [_vp, _c_int, _vp, _c_i64, _c_i64, _c_i64, _c_f, _vp, _c_i64, _c_i64, _c_i64]),
     "kv16_destroy": (_c_int, [_vp]),
     "pattn_init": (_c_int, [_pp, _c_int, _c_int, _c_int, _vp]),
     "pattn_run": (_c_int, [_vp, _c_i64, _c_int, _vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _c_int,
                            _c_f, _vp, _c_i64, _c_i64]),
+    "pattn_run_args": (_c_int, [_vp, _c_bytes]),
     "pattn_kernel": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
     "pattn_status": (_c_int, [_vp]),
     "pattn_destroy": (_c_int, [_vp]),
@@ -723,6 +729,13 @@ def _vector(t: torch.Tensor, name: str, n: int, dtype, index: int) -> int:
     raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on cuda:{index}")
 
 
+# The C structs of arguments (vbs_rope_args, vbs_kv16_args, vbs_pattn_args): packing them takes a fraction of what ctypes
+# needs to convert as many arguments (18 of them: 0.4 against 1.5 us, of some 10 for a whole call).
+_ROPE_ARGS = struct.Struct("@qQ QqqQqq QqqQqq Q iii")
+_KV16_ARGS = struct.Struct("@qQ Qqq Qqq QQ Qqq QqqQqq ii")
+_PATTN_ARGS = struct.Struct("@qQ Qqq Qqq Qqq Qqq iif")
+
+
 class Rotary:
     """Rotary positions of heads of D dims (libvbs rope_*): at position p a pair (a, b) of dims of frequency f becomes
     (a cos pf - b sin pf, b cos pf + a sin pf).
@@ -771,7 +784,7 @@ class Rotary:
             q_out, qo = torch.empty(shape, dtype=dt, device=q.device), (heads * D, D)
         else:
             qo = _rows3(q_out, "q_out", shape, dt, i)
-        kp = kop = None
+        kp = kop = 0
         ks = ko = (0, 0)
         k_heads = 0
         if k is not None:
@@ -788,8 +801,8 @@ class Rotary:
         if _device_index() != i:
             with torch.cuda.device(i):
                 return self.apply(pos, q, k, q_out, k_out)
-        st = lib().rope_apply(self.ctx, N, pp, code, q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], heads, kp, ks[0],
-                              ks[1], kop, ko[0], ko[1], k_heads, _raw_stream(i))
+        st = lib().rope_apply_args(self.ctx, _ROPE_ARGS.pack(N, pp, q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], kp,
+                                                             ks[0], ks[1], kop, ko[0], ko[1], _raw_stream(i), code, heads, k_heads))
         if st != OK:
             _check(st, "rope_apply")
         return q_out, k_out
@@ -843,14 +856,14 @@ class PagedKV16(PagedKV):
         shape = (N, H, D)
         ks, vs = _rows3(k, "k", shape, dt, i), _rows3(v, "v", shape, dt, i)
         sp = _vector(slots, "slots", N, torch.int64, i)
-        rope = pp = qp = qop = kop = None
+        rope = pp = qp = qop = kop = 0
         qs = qo = ko = (0, 0)
         if rotary is not None:
             if rotary.D != D or rotary.index != i:
                 raise ValueError(f"rotary must be for {D} dims on cuda:{i}")
             if pos is None:
                 raise ValueError("rotary needs pos")
-            rope, pp = rotary.ctx, _vector(pos, "pos", N, torch.int32, i)
+            rope, pp = rotary.ctx.value or 0, _vector(pos, "pos", N, torch.int32, i)
             if q is not None:
                 shape_q = (N, self.heads, D)
                 qs = _rows3(q, "q", shape_q, dt, i)
@@ -865,9 +878,9 @@ class PagedKV16(PagedKV):
                 ko, kop = _rows3(k_out, "k_out", shape, dt, i), k_out.data_ptr()
         elif not (pos is None and q is None and q_out is None and k_out is None):
             raise ValueError("pos, q, q_out and k_out need rotary")
-        order.run(lib().kv16_append, "kv16_append", (k, v, slots, pos, q, q_out, k_out), self.ctx16, layer,
-                  N, sp, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], rope, pp, kop, ko[0], ko[1], qp,
-                  qs[0], qs[1], qop, qo[0], qo[1])
+        order.run(lib().kv16_append_args, "kv16_append", (k, v, slots, pos, q, q_out, k_out), self.ctx16,
+                  _KV16_ARGS.pack(N, sp, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], rope, pp, kop, ko[0], ko[1], qp,
+                                  qs[0], qs[1], qop, qo[0], qo[1], layer, code))
         return q_out, k_out
 
     def plan(self, ctx_len: torch.Tensor, n_q: int = 1):
@@ -884,9 +897,10 @@ class PagedKV16(PagedKV):
         shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
         qs = _rows4(q, "q", shape)
         out, os_ = _output(out, shape, self.device)
-        if q.device.index != self._order.index or out.device.index != self._order.index:
-            raise ValueError(f"q and out must be on cuda:{self._order.index}")
-        self._order.run(lib().kv16_attention, "kv16_attention", (q, out), self.ctx16, layer, q.data_ptr(), qs[0], qs[1], qs[2],
+        order = self._order
+        if q.get_device() != order.index or out.get_device() != order.index:
+            raise ValueError(f"q and out must be on cuda:{order.index}")
+        order.run(lib().kv16_attention, "kv16_attention", (q, out), self.ctx16, layer, q.data_ptr(), qs[0], qs[1], qs[2],
                         self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
         return out
 
@@ -929,11 +943,13 @@ class PromptAttention:
             raise ValueError("cu must have batch + 1 entries")
         cp = _vector(cu, "cu", batch + 1, torch.int32, i)
         if out is None:
-            out = torch.empty(shape, dtype=bf, device=q.device)
-        os_ = _rows3(out, "out", shape, bf, i)
-        self._order.run(lib().pattn_run, "pattn_run", (q, k, v, cu, out), self.ctx, N, batch, cp, q.data_ptr(), qs[0], qs[1],
-                        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], 1 if causal else 0,
-                        self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1])
+            out, os_ = torch.empty(shape, dtype=bf, device=q.device), (self.heads * self.D, self.D)
+        else:
+            os_ = _rows3(out, "out", shape, bf, i)
+        self._order.run(lib().pattn_run_args, "pattn_run", (q, k, v, cu, out), self.ctx,
+                        _PATTN_ARGS.pack(N, cp, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                         out.data_ptr(), os_[0], os_[1], batch, 1 if causal else 0,
+                                         self.D ** -0.5 if scale is None else scale))
         return out
 
     @property

@@ -113,6 +113,11 @@ VBS_EXPORT int rope_apply(const vbs_rope* c, int64_t n, const int32_t* pos, int 
   a.dtype = dtype;
   return vbs::launch_rope(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
 }
+VBS_EXPORT int rope_apply_args(const vbs_rope* c, const vbs_rope_args* a) {
+  if (!a) return VBS_EINVAL;
+  return rope_apply(c, a->n, a->pos, a->dtype, a->q, a->q_tok, a->q_head, a->q_out, a->qo_tok, a->qo_head, a->q_heads, a->k,
+                    a->k_tok, a->k_head, a->k_out, a->ko_tok, a->ko_head, a->k_heads, a->stream);
+}
 
 VBS_EXPORT int rope_destroy(vbs_rope* c) {
   if (!c) return VBS_OK;
@@ -195,6 +200,11 @@ VBS_EXPORT int kv16_append(vbs_kv16* c, int layer, int64_t n, const int64_t* slo
   a.dtype = dtype;
   return vbs::launch_rope(a, num_sms(), c->kv->stream);
 }
+VBS_EXPORT int kv16_append_args(vbs_kv16* c, const vbs_kv16_args* a) {
+  if (!a) return VBS_EINVAL;
+  return kv16_append(c, a->layer, a->n, a->slots, a->dtype, a->k, a->k_tok, a->k_head, a->v, a->v_tok, a->v_head, a->rope,
+                     a->pos, a->k_out, a->ko_tok, a->ko_head, a->q, a->q_tok, a->q_head, a->q_out, a->qo_tok, a->qo_head);
+}
 
 VBS_EXPORT int kv16_plan(vbs_kv16* c, const int32_t* ctx_len, int n_q) {
   if (!c || !ctx_len || n_q < 1 || n_q > c->max_q) return VBS_EINVAL;
@@ -267,6 +277,11 @@ VBS_EXPORT int pattn_run(vbs_pattn* c, int64_t n, int batch, const int32_t* cu, 
                           static_cast<int>(n), batch, c->q_heads, c->kv_heads, c->head_dim, causal != 0, scale, c->status};
   c->tiles = vbs::prompt_tc_takes(a) ? 1 : 0;
   return c->tiles ? vbs::launch_prompt_tc(a, num_sms(), c->stream) : vbs::launch_prompt_rows(a, c->stream);
+}
+VBS_EXPORT int pattn_run_args(vbs_pattn* c, const vbs_pattn_args* a) {
+  if (!a) return VBS_EINVAL;
+  return pattn_run(c, a->n, a->batch, a->cu, a->q, a->q_tok, a->q_head, a->k, a->k_tok, a->k_head, a->v, a->v_tok, a->v_head,
+                   a->causal, a->scale, a->out, a->o_tok, a->o_head);
 }
 
 VBS_EXPORT int pattn_kernel(vbs_pattn* c, int* tiles) {
