@@ -23,16 +23,16 @@
 //
 // What bounds it is a row tile's chain: a tile of 128 x 128 at head_dim 128 costs 1100 to 1500 clocks of softmax (512 of
 // them exponentials, at 32 a clock and SM), the second half of its product with V and the next scores 768, and some 330 from
-// an instruction to its barrier, while S and P share their 128 TMEM columns; two chains fill 58 to 68 % of the tensor pipe
-// (16001 tokens x 32 heads: 1.45 ms, 1440 TFLOP/s, 76 % of the measured burst).  Requests of 1000 tokens add an item's start and
-// end, some 8000 of 22000 clocks (64 of them: 580 us, 906 TFLOP/s); 128 sentences of up to 256 tokens, 8 heads x 64, take
-// 42 us.  TMEM is full: two S and two O of 128 columns.
+// an instruction to its barrier, while S and P share their 128 TMEM columns; two chains fill 60 to 65 % of the tensor pipe
+// (16001 tokens x 32 heads: 1.37 to 1.47 ms by the clock that power leaves, 1420 TFLOP/s and more, 75 % of the measured
+// burst).  Requests of 1000 tokens add an item's start and end, some 6000 of 20000 clocks (64 of them: 550 us, 950 TFLOP/s);
+// 128 sentences of up to 256 tokens, 8 heads x 64, take 39 us.  TMEM is full: two S and two O of 128 columns.
 // What counted on the way: all roles' code of a tile together has to stay short, or one warp's pushes another's out of the
 // instruction cache (unexecuted paths alone cost 733 against 633 us); results through shared memory (a lane a row took 6000
 // clocks an item); weights handed over in halves; a warp a row tile for the products; an item's V, results and next
 // item on warps of their own.  Measured and not kept: a lock around a row tile's products (1491 against 1466 us), whole warps
 // that issue (1665 against 1462), results and V in an event loop (735 against 690), each row tile's own K and V where the two
-// see different requests (no gain, and longer code).
+// see different requests (no gain, and longer code), Q taken to the L2 ahead of its load (561 against 557).
 
 #include <climits>
 
@@ -302,10 +302,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           }
           tc_wait_st();
         }
-        float mx = -INFINITY;
+        float mx = -INFINITY, s[64];
 #pragma unroll 1
         for (int c = 0; c < PT_N; c += 64) {
-          float s[64];
           tc_ld32(ts + c, s);
           tc_ld32(ts + c + 32, s + 32);
           tc_wait_ld();
@@ -346,18 +345,24 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
               for (int i = 0; i < 16; ++i) o[i] *= sc;
               tc_st16(ts + c, o);
             }
+            tc_wait_st();
+            tc_ld32(ts + 64, s);
+            tc_ld32(ts + 96, s + 32);
+            tc_wait_ld();
           }
           tc_wait_st();
         }
         const float ref = m == -INFINITY ? 0.f : m;
         const u64 f2 = pair(f, f), r2 = pair(-ref, -ref);
         u64 sum[2] = {0, 0};
+        // the second half first: its scores are still at hand (1388 us to 1366 for 16001 tokens)
 #pragma unroll 1
-        for (int c = 0; c < PT_N; c += 64) {
-          float s[64];
-          tc_ld32(ts + c, s);
-          tc_ld32(ts + c + 32, s + 32);
-          tc_wait_ld();
+        for (int c = 64; c >= 0; c -= 64) {
+          if (c == 0) {
+            tc_ld32(ts, s);
+            tc_ld32(ts + 32, s + 32);
+            tc_wait_ld();
+          }
 #pragma unroll
           for (int h = 0; h < 64; h += 32) {
             float pk[16];
@@ -371,9 +376,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
               __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
               pk[i] = *reinterpret_cast<float*>(&w);
             }
-            tc_st16(ts + (c + h) / 2, pk);                // the weights stand where scores were
+            tc_st16(ts + c + h / 2, pk);                  // the weights stand where scores were
           }
-          if (c == 64) {
+          if (c == 0) {
             float l0, l1;
             unpair(add2(sum[0], sum[1]), l0, l1);
             l += l0 + l1;
@@ -603,11 +608,11 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
               u32 acc = first ? 0 : 1;
               bool ok = true;
   #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                ok = wait(&bars.p[X][half], p_turn) && (half == 0 || !turns || wait(&bars.go[X], go_turn));
+              for (int half = 1; half >= 0; --half) {
+                ok = wait(&bars.p[X][half], p_turn) && (half == 1 || !turns || wait(&bars.go[X], go_turn));
                 if (!ok) break;
                 tc_fence_after();
-                const u32 w = ts + half * (PT_N / 4), v = d + half * (PT_N / 2 * 128 >> 4);
+                const u32 w = ts + half * (PT_N / 2), v = d + half * (PT_N / 2 * 128 >> 4);
                 if (steps >= (half + 1) * (PT_N / 32)) {
   #pragma unroll
                   for (int k = 0; k < PT_N / 32; ++k) tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
                   for (int k = 0; k < steps - half * (PT_N / 32); ++k)
                     tc_mma_ts_at(to, w + k * 8, v + k * (2048 >> 4), tc_idesc(DP, true), k > 0 ? 1u : acc);
                 }
-                acc = 1;
+                if (steps > half * (PT_N / 32)) acc = 1;
               }
               if (!ok) break;
               go_turn ^= turns;
