@@ -556,7 +556,8 @@ int rope_init(vbs_rope** ctx, int head_dim, int rot, int layout, const double* f
  * h * q_head (elements of dtype VBS_BF16 or VBS_F32, head_dim contiguous), its result at q_out + i * qo_tok + h * qo_head
  * of the same type, k likewise; pos[i] (device int32) its position.  Outputs are their inputs' memory (with the same
  * strides) or apart from all inputs.  A token with a negative position is skipped: its outputs are left as they are.
- * Errors: VBS_EINVAL (n outside 0..2^31 - 1, dtype or heads out of range, NULL pointers with n > 0), VBS_ECUDA.
+ * Errors: VBS_EINVAL (n outside 0..2^31 - 1, dtype or heads out of range, NULL pointers with n > 0, an output's rows at
+ *   one place by a stride of 0), VBS_ECUDA.
  */
 int rope_apply(const vbs_rope* ctx, int64_t n, const int32_t* pos, int dtype, const void* q, int64_t q_tok, int64_t q_head,
                void* q_out, int64_t qo_tok, int64_t qo_head, int q_heads, const void* k, int64_t k_tok, int64_t k_head,
@@ -603,7 +604,7 @@ int kv16_init(vbs_kv16** ctx, vbs_pkv* pkv, int q_heads, int max_q);
  * same strides) or apart from all inputs.  A token with a negative position is skipped altogether.  Without rope, pos,
  * k_out, q and q_out are NULL.
  * Errors: VBS_EINVAL (layer, n or dtype out of range, NULL pointers with n > 0, q without q_out or the reverse, a rope
- *   of another head_dim), VBS_ECUDA; a slot outside the pool is not written, with VBS_EINVAL in kv_paged_status().
+ *   of another head_dim, an output's rows at one place by a stride of 0), VBS_ECUDA; a slot outside the pool is not written, with VBS_EINVAL in kv_paged_status().
  */
 int kv16_append(vbs_kv16* ctx, int layer, int64_t n, const int64_t* slots, int dtype, const void* k, int64_t k_tok,
                 int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const vbs_rope* rope, const int32_t* pos,
@@ -634,7 +635,7 @@ int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
  * may hold anything.  Scores, softmax statistics and sums are fp32; the softmax weights are held to 16 bits (two bf16
  * parts) where up to 16 rows (beams x n_q x q_heads / H) of a sentence share a K/V head or head_dim is above 128, else
  * rounded to one bf16 number.
- * Errors: those of kv8_attention.
+ * Errors: those of kv8_attention, and VBS_EINVAL where a stride of 0 puts rows of out at one place.
  */
 int kv16_attention(vbs_kv16* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,
                    void* out, int64_t o_row, int64_t o_tok, int64_t o_head);
@@ -660,12 +661,14 @@ int pattn_init(vbs_pattn** ctx, int q_heads, int kv_heads, int head_dim, vbs_str
  * K/V head h / (q_heads / kv_heads),
  *   out = sum_j softmax_j(scale * q . k_j) v_j   over the request's tokens up to its own (causal), or over all of them.
  * All bf16 (device), head_dim contiguous: token t's head h of q is at q + t * q_tok + h * q_head (elements), k, v and out
- * likewise.  Tokens of no request are neither used nor written.  What a token does not see may hold anything.
+ * likewise; out is apart from the inputs.  Tokens of no request are neither used nor written.  What a token does not see
+ * may hold anything.
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to bf16 before the product with V (not
  * in the kernel for more than 128 heads a group, or q, k, v whose addresses and strides are not multiples of 16 bytes:
  * pattn_kernel tells; it is some 50 times slower).
  * An infinite or NaN element of V counts for every token that sees it, as in the formula.
- * Errors: VBS_EINVAL (n or batch outside 0..2^30, NULL pointers, scale not finite), VBS_ECUDA; a request that is not
+ * Errors: VBS_EINVAL (n or batch outside 0..2^30, NULL pointers, scale not finite, rows of out at one place by a stride of
+ *   0), VBS_ECUDA; a request that is not
  *   within the tokens counts as none, with VBS_EINVAL in pattn_status().
  */
 int pattn_run(vbs_pattn* ctx, int64_t n, int batch, const int32_t* cu, const void* q, int64_t q_tok, int64_t q_head,

@@ -318,3 +318,86 @@ def test_refusals():
             f()
     assert x.status() == 0
     x.close()
+
+
+@pytest.mark.parametrize("per", [1, 5000, 400000])
+def test_any_number_of_empty_requests(per):
+    import verify_bs_step_gb300 as vbs
+    at = np.array([0, 3, 130, 131, 400, 500])
+    cu = np.repeat(at, per)
+    x = vbs.PromptAttention(3, 64, kv_heads=1)
+    q, k, v = tensors(510, 3, 1, 64)
+    out = torch.full((510, 3, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    for causal in (True, False):
+        x.attend(q, k, v, i32(cu), causal=causal, out=out)
+        check(out, q, k, v, at, causal, what=str(per))
+        assert (out[500:] == 7).all()
+    assert x.status() == 0
+    x.close()
+
+
+@pytest.mark.parametrize("more", [0, 1])
+def test_items_of_one_and_of_two_row_tiles(more):
+    """One row tile an item up to half an SM a pair of them, two beyond: both sides, D of each tile shape."""
+    import verify_bs_step_gb300 as vbs
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for D, G in ((64, 2), (128, 1)):
+        N = 2 * (128 // G) * (sms // 2) + more
+        cu = starts([N // 3, 1, 0, N // 2, N - N // 3 - 1 - N // 2])
+        x = vbs.PromptAttention(G, D, kv_heads=1)
+        q, k, v = tensors(N, G, 1, D, seed=more)
+        check(x.attend(q, k, v, i32(cu)), q, k, v, cu, tokens=6)
+        assert x.tiles and x.status() == 0
+        x.close()
+
+
+def test_two_calls_at_once():
+    import verify_bs_step_gb300 as vbs
+    lens = np.random.default_rng(3).integers(1, 900, 20)
+    cu = starts(lens)
+    q, k, v = tensors(int(cu[-1]), 8, 2, 128)
+    side = [torch.cuda.Stream() for _ in range(3)]
+    xs = []
+    for s in side:
+        with torch.cuda.stream(s):
+            xs.append(vbs.PromptAttention(8, 128, kv_heads=2))
+    want = xs[0].attend(q, k, v, i32(cu))
+    torch.cuda.synchronize()
+    got = []
+    cu_ = i32(cu)
+    for _ in range(4):
+        for s, x in zip(side, xs):
+            with torch.cuda.stream(s):
+                got.append(x.attend(q, k, v, cu_))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    for x in xs:
+        assert x.status() == 0
+        x.close()
+
+
+def test_outputs_whose_rows_are_one_place_are_refused():
+    import verify_bs_step_gb300 as vbs
+    bf = torch.bfloat16
+    x = vbs.PromptAttention(4, 64, kv_heads=2)
+    q, k, v = tensors(10, 4, 2, 64)
+    wide, tall = torch.zeros(10, 1, 64, device="cuda", dtype=bf).expand(10, 4, 64), torch.zeros(1, 4, 64, device="cuda", dtype=bf).expand(10, 4, 64)
+    rope = vbs.Rotary(64)
+    kv = vbs.PagedKV16(1, 2, 1, 2, 64, heads=4, blocks_per_sentence=4, max_blocks=4, block=16)
+    kv.build(i32([5]))
+    kv.plan(i32([5, 5]))
+    pos, slots = i32(range(10)), torch.full((10,), -1, device="cuda", dtype=torch.int64)
+    q4 = torch.ones(2, 1, 4, 64, device="cuda", dtype=bf)
+    for bad in (wide, tall):
+        for f in (lambda: x.attend(q, k, v, i32([0, 10]), out=bad), lambda: rope.apply(pos, q, q_out=bad),
+                  lambda: rope.apply(pos, q, k, k_out=bad[:, :2]), lambda: kv.append(0, k, v, slots, rotary=rope, pos=pos, q=q, q_out=bad),
+                  lambda: kv.append(0, k, v, slots, rotary=rope, pos=pos, k_out=bad[:, :2]), lambda: kv.attend(0, q4, out=bad[:2, None])):
+            with pytest.raises(vbs.VbsError):
+                f()
+    # one row or head has no other to meet
+    one = vbs.PromptAttention(1, 64)
+    out = torch.zeros(10, 1, 64, device="cuda", dtype=bf)
+    one.attend(q[:, :1], k[:, :1], v[:, :1], i32([0, 10]), out=out.as_strided((10, 1, 64), (64, 0, 1)))
+    check(out, q[:, :1], k[:, :1], v[:, :1], [0, 10])
+    for c in (x, one, kv, rope):
+        c.close()

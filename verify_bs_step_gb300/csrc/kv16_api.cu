@@ -37,6 +37,9 @@ struct vbs_pattn {
   int* status;
 };
 
+// Whether an output's rows (n by tok, heads by head elements apart) are different memory, as far as strides of 0 go.
+static bool apart(int64_t n, int64_t tok, int64_t heads, int64_t head) { return (n < 2 || tok != 0) && (heads < 2 || head != 0); }
+
 // =====================================================================================
 // rotary positions
 // =====================================================================================
@@ -103,6 +106,7 @@ VBS_EXPORT int rope_apply(const vbs_rope* c, int64_t n, const int32_t* pos, int 
     return VBS_EINVAL;
   if (n == 0 || q_heads + k_heads == 0) return VBS_OK;
   if (!pos || (q_heads > 0 && (!q || !q_out)) || (k_heads > 0 && (!k || !k_out))) return VBS_EINVAL;
+  if (!apart(q_heads > 0 ? n : 0, qo_tok, q_heads, qo_head) || !apart(k_heads > 0 ? n : 0, ko_tok, k_heads, ko_head)) return VBS_EINVAL;
   vbs::RopeArgs a{};
   a.n = n;
   a.pos = pos;
@@ -185,6 +189,7 @@ VBS_EXPORT int kv16_append(vbs_kv16* c, int layer, int64_t n, const int64_t* slo
     return VBS_EINVAL;
   if (rope ? rope->D != c->g.D || (n > 0 && !pos) : pos || k_out || q || q_out) return VBS_EINVAL;
   if (n > 0 && (!k || !v || !slots || (q != nullptr) != (q_out != nullptr))) return VBS_EINVAL;
+  if ((q_out && !apart(n, qo_tok, c->q_heads, qo_head)) || (k_out && !apart(n, ko_tok, c->g.H, ko_head))) return VBS_EINVAL;
   if (c->kv->copy_pending) return VBS_ESTATE;
   vbs::RopeArgs a{};
   a.n = n;
@@ -219,6 +224,7 @@ VBS_EXPORT int kv16_attention(vbs_kv16* c, int layer, const void* q, int64_t q_r
                               void* out, int64_t o_row, int64_t o_tok, int64_t o_head) {
   if (!c || !q || !out || layer < 0 || layer >= c->g.L || !std::isfinite(scale)) return VBS_EINVAL;
   if (c->n_q == 0 || c->planned != c->kv->tables || c->kv->copy_pending) return VBS_ESTATE;
+  if (!apart(c->kv->R, o_row, c->q_heads, o_head) || !apart(c->n_q, o_tok, 0, 0)) return VBS_EINVAL;
   const vbs::QO io{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), q_row, q_tok, q_head, o_row, o_tok,
                    o_head, c->n_q, c->q_heads, scale};
   vbs::Kv16Geom g = c->g;
@@ -271,7 +277,7 @@ VBS_EXPORT int pattn_run(vbs_pattn* c, int64_t n, int batch, const int32_t* cu, 
                          float scale, void* out, int64_t o_tok, int64_t o_head) {
   if (!c || n < 0 || n > (1 << 30) || batch < 0 || batch > (1 << 30) || !std::isfinite(scale)) return VBS_EINVAL;
   if (n == 0 || batch == 0) return VBS_OK;
-  if (!cu || !q || !k || !v || !out) return VBS_EINVAL;
+  if (!cu || !q || !k || !v || !out || !apart(n, o_tok, c->q_heads, o_head)) return VBS_EINVAL;
   const vbs::PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                           static_cast<uint16_t*>(out), q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head, cu,
                           static_cast<int>(n), batch, c->q_heads, c->kv_heads, c->head_dim, causal != 0, scale, c->status};

@@ -127,6 +127,18 @@ __device__ __forceinline__ void tma_load3(u32 dst, const CUtensorMap* map, u64* 
       ::"r"(dst), "l"(map), "r"(x), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
+// The last request from b (which starts at or before token t, or is taken for it) to `last` that starts at or before t: by
+// steps that double and then halve, as any number of requests may be empty and start there too.
+__device__ __forceinline__ int request_after(const int* cu, int b, int last, int t) {
+  int step = 1;
+  while (step <= last - b && cu[b + step] <= t) {
+    b += step;
+    step *= 2;
+  }
+  for (; step > 0; step >>= 1)
+    if (step <= last - b && cu[b + step] <= t) b += step;
+  return b;
+}
 // The last request that starts at or before token t, or 0, by a converged warp; one start in `every` is at hand in shared
 // memory.
 __device__ __forceinline__ int request_before(const PromptArgs& a, const int* cu, int every, int t, int lane) {
@@ -138,10 +150,7 @@ __device__ __forceinline__ int request_before(const PromptArgs& a, const int* cu
     lo += k;
     n = min(step, n - k);
   }
-  int b = lo * every;
-  if (every > 1)
-    while (b < a.B && b < lo * every + every - 1 && a.cu[b + 1] <= t) ++b;
-  return b;
+  return every > 1 ? request_after(a.cu, lo * every, min(a.B, lo * every + every - 1), t) : lo;
 }
 // Request b's first token and its end; 0, 0 where it is not within the tokens.
 __device__ __forceinline__ int2 request_at(const PromptArgs& a, const int* cu, int every, int b) {
@@ -705,7 +714,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             const int tok = tok0 + w;
             if (!__all_sync(FULL, (tok >= at.x && tok < at.y) || w >= end)) {
               // the group's tokens are of several requests: each lane goes on to its own
-              while (b + 1 < p.B && (every == 1 ? cu[b + 1] : p.cu[b + 1]) <= tok && w < end) ++b;
+              if (w < end) b = request_after(every == 1 ? cu : p.cu, b, p.B - 1, tok);
               __syncwarp();
               at = request_at(p, cu, every, b);
             }
