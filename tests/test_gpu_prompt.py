@@ -401,3 +401,33 @@ def test_outputs_whose_rows_are_one_place_are_refused():
     check(out, q[:, :1], k[:, :1], v[:, :1], [0, 10])
     for c in (x, one, kv, rope):
         c.close()
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_offsets_past_32_bits(shift):
+    """Rows 2^31 elements and more behind the first, in the tiles and (shifted by one element) in the other kernel; and
+    the rotary positions of such rows."""
+    import verify_bs_step_gb300 as vbs
+    N, wide = 70000, 32768
+    buf = torch.zeros(N * wide + 8, device="cuda", dtype=torch.bfloat16)
+    rows = buf[shift:shift + N * wide].view(N, wide)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rows[:, :256] = torch.randn(N, 256, device="cuda", generator=g).to(torch.bfloat16)
+    q, k, v, out = (rows[:, i * 64:i * 64 + 64].unsqueeze(1) for i in (0, 1, 2, 4))
+    cu = starts([300] * 10 + [N - 6000] + [300] * 10)
+    x = vbs.PromptAttention(1, 64)
+    if shift:                                          # (the other kernel: a few tokens behind the 2^31st)
+        q, k, v, out, cu = q[68000:], k[68000:], v[68000:], out[68000:], starts([1100, 0, 900])
+        assert q.storage_offset() > 2 ** 31
+    x.attend(q, k, v, i32(cu), out=out)
+    assert x.tiles is (shift == 0)
+    check(out, q, k, v, cu, tokens=3)
+    if shift == 0:
+        rope = vbs.Rotary(64)
+        pos = i32(np.arange(N) % 1000)
+        want = rope.apply(pos, q.contiguous())[0]
+        assert torch.equal(rope.apply(pos, q, q_out=out)[0], want)
+        far = rows[:, 1:257].view(N, 4, 64)            # (rows of no 16-byte alignment)
+        assert torch.equal(rope.apply(pos, far)[0], rope.apply(pos, far.contiguous())[0])
+        rope.close()
+    x.close()
