@@ -338,11 +338,11 @@ def test_any_number_of_empty_requests(per):
 
 @pytest.mark.parametrize("more", [0, 1])
 def test_items_of_one_and_of_two_row_tiles(more):
-    """One row tile an item up to half an SM a pair of them, two beyond: both sides, D of each tile shape."""
+    """One row tile an item, its positions split, up to an SM a pair of them, two beyond: both sides, D of each tile shape."""
     import verify_bs_step_gb300 as vbs
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     for D, G in ((64, 2), (128, 1)):
-        N = 2 * (128 // G) * (sms // 2) + more
+        N = 2 * (128 // G) * sms + more
         cu = starts([N // 3, 1, 0, N // 2, N - N // 3 - 1 - N // 2])
         x = vbs.PromptAttention(G, D, kv_heads=1)
         q, k, v = tensors(N, G, 1, D, seed=more)
@@ -430,4 +430,62 @@ def test_offsets_past_32_bits(shift):
         far = rows[:, 1:257].view(N, 4, 64)            # (rows of no 16-byte alignment)
         assert torch.equal(rope.apply(pos, far)[0], rope.apply(pos, far.contiguous())[0])
         rope.close()
+    x.close()
+
+
+def filled(vbs, tokens):
+    """PromptAttention with one more request of so many tokens behind the caller's in each call: then items have two row
+    tiles."""
+    class Filled(vbs.PromptAttention):
+        def attend(self, q, k, v, cu, **kw):
+            g = torch.Generator(device="cuda").manual_seed(9)
+            N = q.shape[0]
+            q, k, v = (torch.cat([x, torch.randn(tokens, *x.shape[1:], device="cuda", generator=g).to(x.dtype)]) for x in (q, k, v))
+            return super().attend(q, k, v, torch.cat([cu, cu[-1:] + tokens]).contiguous(), **kw)[:N]
+    return Filled
+
+
+@pytest.mark.parametrize("causal", [True, False])   # (of the first two)
+@pytest.mark.parametrize("test,args", [
+    ("test_matches_the_oracle", ([5, 0, 130, 1], 2, 2, 64)), ("test_matches_the_oracle", ([127, 128, 129], 4, 4, 64)),
+    ("test_matches_the_oracle", ([300], 8, 2, 128)), ("test_matches_the_oracle", ([33, 600, 64], 8, 1, 128)),
+    ("test_matches_the_oracle", ([70, 200], 6, 2, 80)), ("test_matches_the_oracle", ([1] * 300, 4, 2, 64)),
+    ("test_matches_the_oracle", ([2000, 10], 5, 1, 64)), ("test_matches_the_oracle", ([1025], 3, 3, 96)),
+    ("test_infinities_and_nan_reach_only_those_who_see_them", (64, 4, 1)),
+    ("test_infinities_and_nan_reach_only_those_who_see_them", (128, 2, 2)),
+    ("test_infinities_and_nan_reach_only_those_who_see_them", (8, 3, 3)),
+    ("test_scores_of_minus_infinity", (64, 2, 1)), ("test_scores_of_minus_infinity", (128, 2, 1)),
+    ("test_extreme_scores", (64, 40.0)), ("test_extreme_scores", (128, 300.0)), ("test_extreme_scores", (128, 0.0))])
+def test_with_two_row_tiles_an_item(test, args, causal, monkeypatch):
+    import verify_bs_step_gb300 as vbs
+    Hq, H = args[1:3] if len(args) > 2 else (2, 2)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    monkeypatch.setattr(vbs, "PromptAttention", filled(vbs, 2 * (128 * H // Hq) * (sms // H + 1)))
+    globals()[test](*args, causal) if test in ("test_matches_the_oracle", "test_infinities_and_nan_reach_only_those_who_see_them") else \
+        globals()[test](*args)
+
+
+@pytest.mark.parametrize("n", [128, 129, 255, 256, 257, 384, 640, 900])
+@pytest.mark.parametrize("D", [64, 128])
+def test_positions_split_at_every_count_of_tiles(n, D):
+    """Items of 1, 2, 3 .. 8 tiles; rows that see only the first half's, and bad values in either half."""
+    import verify_bs_step_gb300 as vbs
+    x = vbs.PromptAttention(2, D, kv_heads=1)
+    cu = starts([n, 77, n + 40])
+    q, k, v = tensors(int(cu[-1]), 2, 1, D, seed=n)
+    for causal in (True, False):
+        check(x.attend(q, k, v, i32(cu), causal=causal), q, k, v, cu, causal, tokens=30)
+    for p in (n // 4, n - 1):
+        v2 = v.clone()
+        v2[p, 0, 5] = float("inf")
+        out = x.attend(q, k, v2, i32(cu))
+        assert (out[p, :, 5] == float("inf")).all() and (out[p:n, :, 5] == float("inf")).sum() + out[p:n, :, 5].isnan().sum() == 2 * (n - p)
+        out[p:n, :, 5] = x.attend(q, k, v, i32(cu))[p:n, :, 5]
+        check(out, q, k, v, cu, tokens=30)
+    # a request whose largest scores are in its first half, or all in its second
+    for at in (0, n - n // 3):
+        k2 = k.clone()
+        k2[at:at + n // 3] = (k2[at:at + n // 3].float() * 60).to(torch.bfloat16)
+        check(x.attend(q, k2, v, i32(cu)), q, k2, v, cu, tokens=30)
+    assert x.status() == 0
     x.close()

@@ -2,7 +2,7 @@
 //
 // An item is 2 x 128 query rows (128 at head_dim above 128, and where there are few) of one K/V head (2 TT tokens in
 // their packed order, whatever requests they are of, the heads of a group side by side) over the positions that any of
-// them sees, PT_N at a time:
+// them sees, PT_N at a time (where there are few rows, each of two chains takes half of the positions):
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle), S in TMEM, one buffer a row tile;
 //   softmax       four warps a row tile, one thread a row: S from TMEM to registers, weights back to TMEM as bf16;
 //   O += P V      tcgen05.mma, P from TMEM, V in shared memory as it comes, O in TMEM.
@@ -191,12 +191,15 @@ __device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone
   return true;
 }
 
-template <int DP>
+// SPLIT: an item is one row tile, the first and the second half of whose positions the two chains take; their sums are
+// joined when they are brought out.
+template <int DP, bool SPLIT>
 __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                                                             const __grid_constant__ CUtensorMap kmap,
                                                             const __grid_constant__ CUtensorMap vmap, const PtArgs a) {
   using C = PtCfg<DP>;
-  constexpr int ST = C::ST;
+  constexpr int ST = C::ST, STEP = SPLIT ? 2 : 1;
+  static_assert(!SPLIT || C::X == 2, "a chain each");
   extern __shared__ unsigned char pt_smem_raw[];
   __shared__ __align__(8) PtBars bars;
   __shared__ u32 tmem_base;
@@ -206,6 +209,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   __shared__ PtItem ring[PT_RING];
   __shared__ int2 span[PT_RING][2 * PT_M];                // positions [x, y) of an item's tokens
   __shared__ float sums[2][2][PT_M];                      // of a row's weights, by the row tile's items in turn
+  __shared__ float refs[SPLIT ? 2 : 1][2][PT_M];          // and what they are relative to
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = pt_smem_raw + ((1024 - (smem_u32(pt_smem_raw) & 1023)) & 1023);
@@ -262,6 +266,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   tc_fence_after();
   const u32 tm = tmem_base, tm_s = tm, tm_o = tm + 2 * PT_N;
 
+  // the place among an item's tiles of positions of the j-th that is loaded; a chain takes every STEP-th
+  auto place = [](int n, int j) { return SPLIT ? (j & 1) * ((n + 1) / 2) + (j >> 1) : j; };
   auto item_at = [&](int t) { return pt_wait(&bars.itf[t % PT_RING], (t / PT_RING) & 1, &gone, p); };
 
   if (wid < PT_W_OUT) {
@@ -280,13 +286,13 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       ok = __all_sync(FULL, item_at(t));
       const PtItem& it = ring[t % PT_RING];
       if (!ok || it.h < 0) break;
-      const int2 sp = r < a.TT * a.G ? span[t % PT_RING][X * a.TT + tok_r] : make_int2(0, 0);
+      const int2 sp = r < a.TT * a.G ? span[t % PT_RING][(SPLIT ? 0 : X) * a.TT + tok_r] : make_int2(0, 0);
       // counted from the item's first position; rows that are not there see all of it (they are not written)
       const int x0 = sp.y > 0 ? sp.x - it.base : 0, x1 = sp.y > 0 ? sp.y - it.base : INT_MAX / 2;
       const int j0 = it.j0[X], j1 = it.j1[X];
       float m = -INFINITY, l = 0.f;                       // the reference (in scaled units), the sum of weights
-      for (int j = j0; j < j1; ++j, ++S) {
-        const int from = x0 - j * PT_N, left = x1 - j * PT_N;
+      for (int j = j0; j < j1; j += STEP, ++S) {
+        const int y = place(it.n, j) * PT_N, from = x0 - y, left = x1 - y;
         ok = __all_sync(FULL, pt_wait(&bars.s[X], S & 1, &gone, p));
         if (!ok) break;
         tc_fence_after();
@@ -391,7 +397,10 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             float l0, l1;
             unpair(add2(sum[0], sum[1]), l0, l1);
             l += l0 + l1;
-            if (j + 1 == j1) sums[O & 1][X][r] = l;
+            if (j + STEP >= j1) {
+              sums[O & 1][X][r] = l;
+              if (SPLIT) refs[O & 1][X][r] = m;
+            }
           }
           tc_wait_st();
           tc_fence_before();
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         const int e = u == t ? it.n : min(it.n, ST / 2);
 #pragma unroll 1
         for (int j = u == t ? looked : 0; j < e; ++j) {
-          if (j >= it.w0 && j < it.w1) continue;
+          if (place(it.n, j) >= it.w0 && place(it.n, j) < it.w1) continue;
           const int st = (T + j) % ST;
           ok = wait(&bars.vx[st], turn >> st & 1);
           if (!ok) break;
@@ -465,19 +474,36 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       }
       const PtItem& it = ring[t % PT_RING];
 #pragma unroll 1
-      for (int X = 0; X < 2 && ok; ++X) {
+      for (int X = 0; X < (SPLIT ? 1 : 2) && ok; ++X) {
         if (it.j1[X] <= it.j0[X]) continue;
         ok = wait(&bars.o[X], o_turn >> X & 1);
         if (!ok) break;
+        const bool both = SPLIT && it.n > 1;
+        if (both) {
+          ok = wait(&bars.o[1], o_turn >> 1);
+          if (!ok) break;
+        }
         tc_fence_after();
         const u32 to = tm_o + X * DP + tl;
-        const float inv = 1.f / sums[o_turn >> X & 1][X][r];   // (0 / 0 where every score is -inf: NaN)
-        o_turn ^= 1u << X;
+        float inv, other = 0.f;                           // what the sums are multiplied by (0 / 0 where every score is -inf: NaN)
+        if (SPLIT) {
+          const float m0 = refs[o_turn & 1][0][r], m1 = both ? refs[o_turn >> 1][1][r] : -INFINITY;
+          const float l1 = both ? sums[o_turn >> 1][1][r] : 0.f, m = fmaxf(m0, m1), ref = m == -INFINITY ? 0.f : m;
+          inv = ex2(m0 - ref);
+          other = ex2(m1 - ref);
+          const float k = 1.f / (sums[o_turn & 1][0][r] * inv + l1 * other);
+          inv *= k;
+          other *= k;
+          o_turn ^= both ? 3u : 1u;
+        } else {
+          inv = 1.f / sums[o_turn >> X & 1][X][r];
+          o_turn ^= 1u << X;
+        }
         const int2 sp = r < a.TT * a.G ? span[t % PT_RING][X * a.TT + tok_r] : make_int2(0, 0);
         uint16_t* out = sp.y > sp.x ? p.o + static_cast<int64_t>(it.tok + X * a.TT + tok_r) * p.o_tok +
                                           static_cast<int64_t>(it.h * a.G + g) * p.o_head
                                     : nullptr;
-        if (__builtin_expect(odd, 0)) {
+        if (!SPLIT && __builtin_expect(odd, 0)) {
 #pragma unroll 1
           for (int c = 0; c < DP; c += 32) {
             float o[32];
@@ -495,12 +521,28 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         for (int i = 0; i < 4; ++i) at[i] = reinterpret_cast<uint16_t*>(shfl64(reinterpret_cast<u64>(out), i * 8 + lane / 4));
 #pragma unroll 1
         for (int c = 0; c < DP; c += 32) {
-          float o[32];
+          float o[32], o1[32];
           tc_ld32(to + c, o);
+          if (both) tc_ld32(to + DP + c, o1);
           tc_wait_ld();
           if (c + 32 == DP) {
             tc_fence_before();
             mbar_arrive(&bars.of[X]);                     // O may be written again
+            if (both) mbar_arrive(&bars.of[1]);
+          }
+          if (SPLIT) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+            if (both) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], other, o[i]);
+            }
+            if (__builtin_expect(odd, 0)) {
+              float z[32];
+              for (int i = 0; i < 32; ++i) z[i] = 0.f;
+              add_odd(p, it, X, sp.x - it.base, sp.y - it.base, c, z);
+              for (int i = 0; i < 32; ++i) o[i] += z[i];
+            }
           }
           __syncwarp();                                   // the 32 dims before have been read
 #pragma unroll
@@ -508,7 +550,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             u32 w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k] * inv, o[8 * i + 2 * k + 1] * inv);
+              const float f = SPLIT ? 1.f : inv;
+              const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k] * f, o[8 * i + 2 * k + 1] * f);
               w[k] = *reinterpret_cast<const u32*>(&b);
             }
             *reinterpret_cast<uint4*>(mine + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -552,14 +595,14 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             if (!ok) break;
             mbar_expect_tx(&bars.kf[st], C::TB);
             for (int x = 0; x < C::SLABS; ++x)
-              tma_load3(k_a + st * C::TB + x * PT_N * 128, &kmap, &bars.kf[st], x * 64, h, base + j * PT_N);
-            const bool odd_tile = j < w0 || j >= w1;
+              tma_load3(k_a + st * C::TB + x * PT_N * 128, &kmap, &bars.kf[st], x * 64, h, base + place(n, j) * PT_N);
+            const bool odd_tile = place(n, j) < w0 || place(n, j) >= w1;
             u64* bar = odd_tile ? &bars.vx[st] : &bars.vf[st];
             ok = T < ST || pt_wait(&bars.ve[st], free_turn, &gone, p);
             if (ok) {
               mbar_expect_tx(bar, C::TB);
               for (int x = 0; x < C::SLABS; ++x)
-                tma_load3(v_a + st * C::TB + x * PT_N * 128, &vmap, bar, x * 64, h, base + j * PT_N);
+                tma_load3(v_a + st * C::TB + x * PT_N * 128, &vmap, bar, x * 64, h, base + place(n, j) * PT_N);
               if (odd_tile) look ^= 1u << st;
               else whole ^= 1u << st;
               kind = (kind & ~(1u << st)) | (odd_tile ? 1u << st : 0u);
@@ -594,7 +637,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           if (!item_at(t)) return false;
           const PtItem& i = ring[t % PT_RING];
           n = i.n, j0 = i.j0[X], j1 = i.j1[X], y1 = i.y1[X], w0 = i.w0, w1 = i.w1, j = 0;
-          turns = n >= PT_TURNS ? 1u : 0u;
+          turns = !SPLIT && n >= PT_TURNS ? 1u : 0u;
           return i.h >= 0;
         };
         bool go = take();
@@ -604,7 +647,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         for (bool begin = true; go; begin = false) {
           if (!begin) {
             const int st = at % ST;
-            const bool clear = j >= w0 && j < w1;
+            const bool clear = place(n, j) >= w0 && place(n, j) < w1;
             if (!wait(clear ? &bars.vf[st] : &bars.vc[st], (clear ? whole : look) >> st & 1)) break;
             if (clear) whole ^= 1u << st;
             else look ^= 1u << st;
@@ -652,10 +695,10 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             }
           }
           const int st = at % ST;
-          const bool on = j >= j0 && j < j1;
-          steps = on ? steps_of(y1, j) : 0;
+          const bool on = j >= j0 && j < j1 && (!SPLIT || (j & 1) == X);
+          steps = on ? steps_of(y1, place(n, j)) : 0;
           first = j == j0;
-          last = j + 1 == j1;
+          last = j + STEP >= j1;
           if (!wait(&bars.kf[st], (at / ST) & 1)) break;
           if (steps > 0) {
             if (first) {
@@ -742,6 +785,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           z1[X] = __reduce_min_sync(FULL, z1[X]);
         }
         const int base = min(y0[0], y0[1]);
+        if (SPLIT && y1[0] - base > PT_N) y0[1] = y0[0], y1[1] = y1[0], z0[1] = z0[0], z1[1] = z1[0];   // (the same rows)
         const bool some = max(y1[0], y1[1]) > 0;            // (else: tokens of no request)
         if ((some || last) && lane == 0) {
           x.h = h;
@@ -752,7 +796,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           for (int X = 0; X < 2; ++X) {
             const bool on = y1[X] > 0;
             x.y1[X] = on ? y1[X] - base : 0;
-            x.j0[X] = on ? (y0[X] - base) / PT_N : 0;
+            x.j0[X] = on ? (SPLIT ? X : (y0[X] - base) / PT_N) : 0;
             x.j1[X] = on ? (y1[X] - base + PT_N - 1) / PT_N : 0;
             if (on) {
               n = max(n, (y1[X] - base + PT_N - 1) / PT_N);
@@ -781,7 +825,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             if (lane == 0) {
               mbar_expect_tx(&bars.q[X], C::SLABS * 128 * a.G * a.TT);
               for (int x = 0; x < C::SLABS; ++x)
-                tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, tok0 + X * a.TT);
+                tma_load3(q_a + X * C::QB + x * PT_M * 128, &qmap, &bars.q[X], x * 64, h * a.G, tok0 + (SPLIT ? 0 : X * a.TT));
             }
             q_turn ^= 1u << X;
             q_some |= 1u << X;
@@ -842,11 +886,11 @@ bool prompt_tc_takes(const PromptArgs& p) {
          tensor_map_encode() != nullptr;
 }
 
-template <int DP>
+template <int DP, bool SPLIT>
 static int launch_tc(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PtArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
-  if (!smem_attr_once(prompt_tc_kernel<DP>, static_cast<int>(PtCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
-  return launch_dependent(prompt_tc_kernel<DP>, dim3(static_cast<unsigned>(a.tiles * a.p.H - a.many * (a.batch - 1))), dim3(PT_NT),
+  if (!smem_attr_once(prompt_tc_kernel<DP, SPLIT>, static_cast<int>(PtCfg<DP>::SMEM), attr_done)) return VBS_ECUDA;
+  return launch_dependent(prompt_tc_kernel<DP, SPLIT>, dim3(static_cast<unsigned>(a.tiles * a.p.H - a.many * (a.batch - 1))), dim3(PT_NT),
                           PtCfg<DP>::SMEM, s, qm, km, vm, a);
 }
 
@@ -856,11 +900,13 @@ int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
   if (!encode(&qm, p.q, p, p.Hq, p.q_tok, p.q_head, G, TT) || !encode(&km, p.k, p, p.H, p.k_tok, p.k_head, 1, PT_N) ||
       !encode(&vm, p.v, p, p.H, p.v_tok, p.v_head, 1, PT_N))
     return VBS_ECUDA;
-  // Two row tiles an item, but one where head_dim leaves no room for two, or where the GPU has an SM for each: one / two in
-  // us, 7000 tokens x 1 head x 128: 92 / 100; 16 sentences up to 256 x 8 x 64: 18.4 / 20.5; and with more than half an SM a
-  // pair, 32 such sentences: 26.6 / 22.5; 4000 tokens x 8 heads x 128: 73.8 / 65.5.
+  // Two row tiles an item, but one where head_dim leaves no room for two, or, its positions split, where the GPU has an SM
+  // for each pair.  Split / not in us: 7000 tokens x 1 head x 128: 63 / 90; 4000 x 8: 43 / 65; 2000 x 4 heads over 1: 27 / 35;
+  // 32 sentences up to 256 x 8 x 64: 20.5 / 22.5; and with more pairs than SMs, 2000 x 32 over 8: 47 / 39; 9000 x 8 over 1:
+  // 143 / 125; 64 such sentences: 33 / 31 (K and V are loaded for each row tile, and each brings out two sums).
   const int64_t pairs = (static_cast<int64_t>(p.N) + 2 * TT - 1) / (2 * TT) * p.H;
-  const int per = p.D > 128 || pairs <= num_sms / 2 ? TT : 2 * TT;
+  const bool split = p.D <= 128 && pairs <= num_sms;
+  const int per = p.D > 128 || split ? TT : 2 * TT;
   const int64_t tiles = (static_cast<int64_t>(p.N) + per - 1) / per, items = tiles * p.H;
   if (items >= int64_t{1} << 31) return VBS_EINVAL;
   // the GPU answers some 15 claims a microsecond: many items are claimed several at a time, the last quarter one by one
@@ -868,8 +914,9 @@ int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
   const int many = batch > 1 ? static_cast<int>(items * 3 / 4 / batch) : 0;
   const PtArgs a{p, G, TT, per, static_cast<int>(tiles), batch, many,
                  (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && (p.o_tok | p.o_head) % 8 == 0};
-  if (p.D <= 64) return launch_tc<64>(qm, km, vm, a, s);
-  return p.D <= 128 ? launch_tc<128>(qm, km, vm, a, s) : launch_tc<256>(qm, km, vm, a, s);
+  if (p.D <= 64) return split ? launch_tc<64, true>(qm, km, vm, a, s) : launch_tc<64, false>(qm, km, vm, a, s);
+  if (p.D <= 128) return split ? launch_tc<128, true>(qm, km, vm, a, s) : launch_tc<128, false>(qm, km, vm, a, s);
+  return launch_tc<256, false>(qm, km, vm, a, s);
 }
 
 }  // namespace vbs
