@@ -264,7 +264,7 @@ template <class Src, int DP, int MT> struct SplitCfg {
   // 16 sentences, which do not fill the GPU: 1..5 % slower)
   static constexpr bool SMALL = EL == 1 && DP == 64 && MT == 1;
   // Over a 16-bit cache with more than 16 rows, the weights are rounded to one bf16 number instead of held in two: the second
-  // product is what bounds it there (64 rows x 8 tokens x 4 heads over 1..2500 positions: 93 us with two, 85 with one)
+  // product is what bounds it there (64 rows x 8 tokens x 4 heads over 1..2500 positions: 86 us with two, 75 with one)
   static constexpr bool ONE = Src::RAW && MT == 2;
   static constexpr int NS = SMALL ? 4 : STAGE <= 2048 ? 8 : STAGE <= 4096 ? 4 : (STAGE <= 8192 ? 3 : 2);
   static constexpr int O_LD = DP + 4;                       // floats of an o row in shared memory
