@@ -32,7 +32,8 @@
 // clocks an item); weights handed over in halves; a warp a row tile for the products; an item's V, results and next
 // item on warps of their own.  Measured and not kept: a lock around a row tile's products (1491 against 1466 us), whole warps
 // that issue (1665 against 1462), results and V in an event loop (735 against 690), each row tile's own K and V where the two
-// see different requests (no gain, and longer code), Q taken to the L2 ahead of its load (561 against 557).
+// see different requests (no gain, and longer code), Q taken to the L2 ahead of its load (561 against 557), the halves of a
+// tile that no row of a warp sees left out (571 against 549: the code), masks and maxima in one pass (553 against 549).
 
 #include <climits>
 
@@ -330,8 +331,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         }
         mx *= sc;
         float f = sc;
-        const bool grow = mx > m + 8.f;                   // also in a row's first tile: m = -inf
-        if (__any_sync(FULL, grow || fabsf(m) > 65536.f)) {
+        const bool grow = mx > m + 8.f;                   // also in the first tile that a row sees: m = -inf
+        if (__any_sync(FULL, grow || (fabsf(m) > 65536.f && m > -INFINITY))) {
           const float to_m = grow ? mx : m, corr = grow ? (m == -INFINITY ? 0.f : ex2(m - to_m)) : 1.f;
           if (j > j0) {
             // O holds the tiles before (S of this one was issued after their products, and is done)
