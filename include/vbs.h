@@ -628,7 +628,9 @@ typedef struct vbs_kv16_args {
   int layer, dtype;
 } vbs_kv16_args;
 int kv16_append_args(vbs_kv16* ctx, const vbs_kv16_args* args);
-/* kv8_plan for this cache: the same arguments, results and errors; kv16_attention keeps to it as kv8_attention does. */
+/* kv8_plan for this cache: the same arguments, results and errors; kv16_attention keeps to it as kv8_attention does.  The
+   plan and the partial sums of the attention are the context's memory: two graphs that hold its calls are replayed one
+   after the other, not at once. */
 int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
 /*
  * Attention of the planned step over `layer`: as kv8_attention, over bf16 keys and values.  What a token does not see

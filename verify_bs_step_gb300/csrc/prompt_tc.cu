@@ -25,7 +25,7 @@
 // them exponentials, at 32 a clock and SM), the second half of its product with V and the next scores 768, and some 330 from
 // an instruction to its barrier, while S and P share their 128 TMEM columns; two chains fill 60 to 65 % of the tensor pipe
 // (16001 tokens x 32 heads: 1.37 to 1.47 ms by the clock that power leaves, 1420 TFLOP/s and more, 75 % of the measured
-// burst).  Requests of 1000 tokens add an item's start and end, some 6000 of 20000 clocks (64 of them: 550 us, 950 TFLOP/s);
+// burst).  Requests of 1000 tokens add an item's start and end, some 6000 of 20000 clocks (64 of them: 540 us, 970 TFLOP/s);
 // 128 sentences of up to 256 tokens, 8 heads x 64, take 39 us.  TMEM is full: two S and two O of 128 columns.
 // What counted on the way: all roles' code of a tile together has to stay short, or one warp's pushes another's out of the
 // instruction cache (unexecuted paths alone cost 733 against 633 us); results through shared memory (a lane a row took 6000
