@@ -563,7 +563,7 @@ int rope_apply(const vbs_rope* ctx, int64_t n, const int32_t* pos, int dtype, co
                void* q_out, int64_t qo_tok, int64_t qo_head, int q_heads, const void* k, int64_t k_tok, int64_t k_head,
                void* k_out, int64_t ko_tok, int64_t ko_head, int k_heads, vbs_stream_t stream);
 /* The same, its arguments in one struct (host, read before the call returns): where a foreign-function interface converts
-   them one by one, that costs as much as the launch does.  kv16_append and pattn_run have such a form too. */
+   them one by one, that costs as much as the launch does.  The calls below have such a form too. */
 typedef struct vbs_rope_args {
   int64_t n;
   const int32_t* pos;
@@ -641,6 +641,15 @@ int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
  */
 int kv16_attention(vbs_kv16* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,
                    void* out, int64_t o_row, int64_t o_tok, int64_t o_head);
+typedef struct vbs_kv16_query {
+  const void* q;
+  int64_t q_row, q_tok, q_head;
+  void* out;
+  int64_t o_row, o_tok, o_head;
+  int layer;
+  float scale;
+} vbs_kv16_query;
+int kv16_attention_args(vbs_kv16* ctx, const vbs_kv16_query* args);
 /* Free the context (synchronises the stream first; pkv stays).  NULL is a no-op.  Returns VBS_OK. */
 int kv16_destroy(vbs_kv16* ctx);
 

@@ -61,7 +61,7 @@ def test_prompts(L):
     assert L.pattn_destroy(None) == vbs.OK
 
 
-@pytest.mark.parametrize("name", ["rope", "kv16", "pattn"])
+@pytest.mark.parametrize("name", ["rope_args", "kv16_args", "kv16_query", "pattn_args"])
 def test_structs_of_arguments(L, name):
     """The binding packs them as the header declares them; NULL is refused."""
     import os
@@ -70,14 +70,15 @@ def test_structs_of_arguments(L, name):
     import verify_bs_step_gb300 as vbs
     from verify_bs_step_gb300 import _build
     text = open(os.path.join(_build.INCLUDE, "vbs.h")).read()
-    body = re.search(r"typedef struct vbs_%s_args \{(.*?)\}" % name, text, re.S).group(1)
+    body = re.search(r"typedef struct vbs_%s \{(.*?)\}" % name, text, re.S).group(1)
     code = ""
     for line in body.split(";"):
         kind, names = re.match(r"\s*(const \w+ ?\*|void ?\*|vbs_stream_t|int64_t|int|float)\s*(.*)", line + " ", re.S).groups() if line.strip() else ("", "")
         code += {"int64_t": "q", "int": "i", "float": "f"}.get(kind, "Q" if kind else "") * (names.count(",") + 1 if names.strip() else 0)
-    packed = {"rope": vbs._ROPE_ARGS, "kv16": vbs._KV16_ARGS, "pattn": vbs._PATTN_ARGS}[name]
-    assert len(code) > 15 and packed.format.replace(" ", "") == "@" + code
+    packed = {"rope_args": vbs._ROPE_ARGS, "kv16_args": vbs._KV16_ARGS, "kv16_query": vbs._KV16_QUERY, "pattn_args": vbs._PATTN_ARGS}[name]
+    assert len(code) > 9 and packed.format.replace(" ", "") == "@" + code
     assert packed.size == struct.calcsize("@" + code)
-    call = {"rope": L.rope_apply_args, "kv16": L.kv16_append_args, "pattn": L.pattn_run_args}[name]
+    call = {"rope_args": L.rope_apply_args, "kv16_args": L.kv16_append_args, "kv16_query": L.kv16_attention_args,
+            "pattn_args": L.pattn_run_args}[name]
     assert call(None, None) == vbs.EINVAL
     assert call(None, packed.pack(*([0] * len(code)))) == vbs.EINVAL

@@ -81,6 +81,7 @@ SIGNATURES = {
     "kv16_append_args": (_c_int, [_vp, _c_bytes]),
     "kv16_plan": (_c_int, [_vp, _vp, _c_int]),
     "kv16_attention": (_c_int, [_vp, _c_int, _vp, _c_i64, _c_i64, _c_i64, _c_f, _vp, _c_i64, _c_i64, _c_i64]),
+    "kv16_attention_args": (_c_int, [_vp, _c_bytes]),
     "kv16_destroy": (_c_int, [_vp]),
     "pattn_init": (_c_int, [_pp, _c_int, _c_int, _c_int, _vp]),
     "pattn_run": (_c_int, [_vp, _c_i64, _c_int, _vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _c_int,
@@ -713,10 +714,10 @@ def _output(out, shape, device):
     return torch.empty(shape, dtype=torch.bfloat16, device=device), (shape[1] * row, row, shape[3])
 
 
-def _rows3(t: torch.Tensor, name: str, shape, dtype, index: int):
-    """The strides of a [tokens, heads, D] tensor of this shape and dtype on device `index`."""
+def _rows(t: torch.Tensor, name: str, shape, dtype, index: int):
+    """The strides of a [.., heads, D] tensor of this shape and dtype on device `index`."""
     st = t.stride()
-    if t.shape == shape and st[2] == 1 and t.dtype is dtype and t.get_device() == index:
+    if t.shape == shape and st[-1] == 1 and t.dtype is dtype and t.get_device() == index:
         return st
     raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on cuda:{index} with unit stride along the last axis, got "
                      f"{t.dtype} {list(t.shape)} on {t.device}")
@@ -729,10 +730,11 @@ def _vector(t: torch.Tensor, name: str, n: int, dtype, index: int) -> int:
     raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on cuda:{index}")
 
 
-# The C structs of arguments (vbs_rope_args, vbs_kv16_args, vbs_pattn_args): packing them takes a fraction of what ctypes
-# needs to convert as many arguments (18 of them: 0.4 against 1.5 us, of some 10 for a whole call).
+# The C structs of arguments (vbs_rope_args, vbs_kv16_args, vbs_kv16_query, vbs_pattn_args): packing them takes a fraction of
+# what ctypes needs to convert as many arguments (18 of them: 0.4 against 1.5 us, of some 10 for a whole call).
 _ROPE_ARGS = struct.Struct("@qQ QqqQqq QqqQqq Q iii")
 _KV16_ARGS = struct.Struct("@qQ Qqq Qqq QQ Qqq QqqQqq ii")
+_KV16_QUERY = struct.Struct("@Qqqq Qqqq if")
 _PATTN_ARGS = struct.Struct("@qQ Qqq Qqq Qqq Qqq iif")
 
 
@@ -779,22 +781,22 @@ class Rotary:
         pp = _vector(pos, "pos", N, torch.int32, i)
         heads = q.shape[1] if q.dim() == 3 else 0
         shape = (N, heads, D)
-        qs = _rows3(q, "q", shape, dt, i)
+        qs = _rows(q, "q", shape, dt, i)
         if q_out is None:
             q_out, qo = torch.empty(shape, dtype=dt, device=q.device), (heads * D, D)
         else:
-            qo = _rows3(q_out, "q_out", shape, dt, i)
+            qo = _rows(q_out, "q_out", shape, dt, i)
         kp = kop = 0
         ks = ko = (0, 0)
         k_heads = 0
         if k is not None:
             k_heads = k.shape[1] if k.dim() == 3 else 0
             shape = (N, k_heads, D)
-            ks = _rows3(k, "k", shape, dt, i)
+            ks = _rows(k, "k", shape, dt, i)
             if k_out is None:
                 k_out, ko = torch.empty(shape, dtype=dt, device=k.device), (k_heads * D, D)
             else:
-                ko = _rows3(k_out, "k_out", shape, dt, i)
+                ko = _rows(k_out, "k_out", shape, dt, i)
             kp, kop = k.data_ptr(), k_out.data_ptr()
         elif k_out is not None:
             raise ValueError("k_out needs k")
@@ -854,7 +856,7 @@ class PagedKV16(PagedKV):
         i, H, D = order.index, self.H, self.D
         code = _dtype_code(dt)
         shape = (N, H, D)
-        ks, vs = _rows3(k, "k", shape, dt, i), _rows3(v, "v", shape, dt, i)
+        ks, vs = _rows(k, "k", shape, dt, i), _rows(v, "v", shape, dt, i)
         sp = _vector(slots, "slots", N, torch.int64, i)
         rope = pp = qp = qop = kop = 0
         qs = qo = ko = (0, 0)
@@ -866,16 +868,16 @@ class PagedKV16(PagedKV):
             rope, pp = rotary.ctx.value or 0, _vector(pos, "pos", N, torch.int32, i)
             if q is not None:
                 shape_q = (N, self.heads, D)
-                qs = _rows3(q, "q", shape_q, dt, i)
+                qs = _rows(q, "q", shape_q, dt, i)
                 if q_out is None:
                     q_out, qo = torch.empty(shape_q, dtype=dt, device=self.device), (self.heads * D, D)
                 else:
-                    qo = _rows3(q_out, "q_out", shape_q, dt, i)
+                    qo = _rows(q_out, "q_out", shape_q, dt, i)
                 qp, qop = q.data_ptr(), q_out.data_ptr()
             elif q_out is not None:
                 raise ValueError("q_out needs q")
             if k_out is not None:
-                ko, kop = _rows3(k_out, "k_out", shape, dt, i), k_out.data_ptr()
+                ko, kop = _rows(k_out, "k_out", shape, dt, i), k_out.data_ptr()
         elif not (pos is None and q is None and q_out is None and k_out is None):
             raise ValueError("pos, q, q_out and k_out need rotary")
         order.run(lib().kv16_append_args, "kv16_append", (k, v, slots, pos, q, q_out, k_out), self.ctx16,
@@ -895,13 +897,16 @@ class PagedKV16(PagedKV):
         """softmax(scale q k^T) v of q [R, n_q, heads, D] (bfloat16, unit stride along D) over each row's
         cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
         shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
-        qs = _rows4(q, "q", shape)
-        out, os_ = _output(out, shape, self.device)
-        order = self._order
-        if q.get_device() != order.index or out.get_device() != order.index:
-            raise ValueError(f"q and out must be on cuda:{order.index}")
-        order.run(lib().kv16_attention, "kv16_attention", (q, out), self.ctx16, layer, q.data_ptr(), qs[0], qs[1], qs[2],
-                        self.D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1], os_[2])
+        order, bf = self._order, torch.bfloat16
+        qs = _rows(q, "q", shape, bf, order.index)
+        if out is None:
+            row = shape[2] * shape[3]
+            out, os_ = torch.empty(shape, dtype=bf, device=self.device), (shape[1] * row, row, shape[3])
+        else:
+            os_ = _rows(out, "out", shape, bf, order.index)
+        order.run(lib().kv16_attention_args, "kv16_attention", (q, out), self.ctx16,
+                  _KV16_QUERY.pack(q.data_ptr(), qs[0], qs[1], qs[2], out.data_ptr(), os_[0], os_[1], os_[2], layer,
+                                   self.D ** -0.5 if scale is None else scale))
         return out
 
     def close(self):
@@ -937,7 +942,7 @@ class PromptAttention:
         N = q.shape[0] if q.dim() == 3 else 0
         shape, kv_shape = (N, self.heads, self.D), (N, self.kv_heads, self.D)
         bf = torch.bfloat16
-        qs, ks, vs = _rows3(q, "q", shape, bf, i), _rows3(k, "k", kv_shape, bf, i), _rows3(v, "v", kv_shape, bf, i)
+        qs, ks, vs = _rows(q, "q", shape, bf, i), _rows(k, "k", kv_shape, bf, i), _rows(v, "v", kv_shape, bf, i)
         batch = cu.numel() - 1
         if batch < 0:
             raise ValueError("cu must have batch + 1 entries")
@@ -945,7 +950,7 @@ class PromptAttention:
         if out is None:
             out, os_ = torch.empty(shape, dtype=bf, device=q.device), (self.heads * self.D, self.D)
         else:
-            os_ = _rows3(out, "out", shape, bf, i)
+            os_ = _rows(out, "out", shape, bf, i)
         self._order.run(lib().pattn_run_args, "pattn_run", (q, k, v, cu, out), self.ctx,
                         _PATTN_ARGS.pack(N, cp, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
                                          out.data_ptr(), os_[0], os_[1], batch, 1 if causal else 0,

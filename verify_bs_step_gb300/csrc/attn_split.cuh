@@ -25,7 +25,9 @@
 // Over bf16 pages: 64 sentences x 4 beams x 1064: 62 us with plan and join (55 this kernel, 5.6 TB/s); 100003 positions: 72 us
 // (64, 6.4 TB/s, 94 % of the measured copy); 64 x 8 tokens x 4 heads over 1..2500: 75 us (68, 4.9 TB/s).
 // Measured and not kept: two units an iteration (fewer instructions, 8 warps instead of 12: 102 and 65 us), CTAs
-// of one warp (91 us at 64 x 4 beams: four times the partials), a join in the CTA that arrives last (57).
+// of one warp (91 us at 64 x 4 beams: four times the partials), a join in the CTA that arrives last (57); over bf16, V by
+// ldmatrix.trans in place of byte permutes (an eighth fewer instructions, no case faster), all that a segment waits for at its
+// start asked for at once (64 x 8 tokens 2 % faster, 64 x 4 beams 2 % slower).
 
 #pragma once
 

@@ -231,6 +231,10 @@ VBS_EXPORT int kv16_attention(vbs_kv16* c, int layer, const void* q, int64_t q_r
   g.layer = layer;
   return vbs::launch_kv16_attention(c->kv->a, g, io, c->plan, c->part, c->pieces, num_sms(), c->kv->stream);
 }
+VBS_EXPORT int kv16_attention_args(vbs_kv16* c, const vbs_kv16_query* a) {
+  if (!a) return VBS_EINVAL;
+  return kv16_attention(c, a->layer, a->q, a->q_row, a->q_tok, a->q_head, a->scale, a->out, a->o_row, a->o_tok, a->o_head);
+}
 
 VBS_EXPORT int kv16_destroy(vbs_kv16* c) {
   if (!c) return VBS_OK;
