@@ -489,3 +489,23 @@ def test_positions_split_at_every_count_of_tiles(n, D):
         check(x.attend(q, k2, v, i32(cu)), q, k2, v, cu, tokens=30)
     assert x.status() == 0
     x.close()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tokens_of_no_request_in_items_of_two_row_tiles(D, causal):
+    """Tokens before the first, behind the last request; items with one row tile of tokens, one of none."""
+    import verify_bs_step_gb300 as vbs
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    N = 256 * sms + 700
+    for first, last in ((100, N - 130), (140, 256 * 20 + 5), (256 * sms, N - 300)):
+        cu = starts([(last - first) // 2, last - first - (last - first) // 2], first)
+        x = vbs.PromptAttention(1, D)
+        q, k, v = tensors(N, 1, 1, D, seed=first)
+        v[:first], v[last:], k[:first], k[last:] = float("nan"), float("inf"), float("nan"), float("inf")
+        out = torch.full((N, 1, D), 7.0, device="cuda", dtype=torch.bfloat16)
+        x.attend(q, k, v, i32(cu), causal=causal, out=out)
+        assert (out[:first] == 7).all() and (out[last:] == 7).all() and torch.isfinite(out).all()
+        check(out, q, k, v, cu, causal, tokens=8)
+        assert x.tiles and x.status() == 0
+        x.close()
