@@ -677,7 +677,8 @@ int pattn_init(vbs_pattn** ctx, int q_heads, int kv_heads, int head_dim, vbs_str
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to bf16 before the product with V (not
  * in the kernel for more than 128 heads a group, or q, k, v whose addresses and strides are not multiples of 16 bytes:
  * pattn_kernel tells; it is some 50 times slower).
- * An infinite or NaN element of V counts for every token that sees it, as in the formula.
+ * An infinite or NaN element of V counts for every token that sees it, as in the formula: a position that scores -inf has
+ * weight 0, which makes NaN of an infinity; one whose weight is too small for fp32 makes either of it.
  * Errors: VBS_EINVAL (n or batch outside 0..2^30, NULL pointers, scale not finite, rows of out at one place by a stride of
  *   0), VBS_ECUDA; a request that is not
  *   within the tokens counts as none, with VBS_EINVAL in pattn_status().

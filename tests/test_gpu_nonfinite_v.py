@@ -1,0 +1,75 @@
+"""Infinities and NaN of V that a row sees: their product with the weight as held in fp32, in every kernel alike.
+
+A weight is positive for a finite score, so that an infinity stays one; it is 0 for a score of -inf, which makes NaN of an
+infinity.  A weight that is too small for fp32 may count as either, but the element is never left out."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.attn_harness import BF16, check_rows, i32
+from tests.test_gpu_prompt import filled, starts, tensors
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from verify_bs_step_gb300 import _build
+    _build.build()
+    import verify_bs_step_gb300 as vbs
+    return vbs.lib()
+
+
+# how a prompt is brought to each form: items of one row tile, of two, and rows 2 bytes off for the other kernel
+def prompts(form, D):
+    import verify_bs_step_gb300 as vbs
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return (filled(vbs, 2 * 64 * (sms + 1)) if form == "two" else vbs.PromptAttention)(2, D, kv_heads=1)
+
+
+def shifted(x):
+    flat = torch.empty(x.numel() + 1, device="cuda", dtype=x.dtype)[1:].view(x.shape)
+    return flat.copy_(x)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("form,D", [("one", 64), ("one", 128), ("one", 136), ("two", 64), ("two", 128), ("rows", 64)])
+def test_prompts(form, D, causal):
+    x = prompts(form, D)
+    n = 20
+    cu = starts([n, 300])
+    q, k, v = tensors(n + 300, 2, 1, D)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    k[:7, 0, 0] = -INF                               # request 0's first seven positions have no weight
+    k[9, 0, 0], k[11, 0, 0] = -3e3 * D ** 0.5, -3e3 * D ** 0.5   # and these less than fp32 holds
+    v[3, 0, 5], v[4, 0, 6], v[5, 0, 7] = INF, -INF, NAN
+    v[9, 0, 8], v[11, 0, 9] = INF, -INF
+    v[14, 0, 10], v[15, 0, 11] = INF, -INF           # these have some
+    if form == "rows":
+        q, k, v = shifted(q), shifted(k), shifted(v)
+    out = x.attend(q, k, v, i32(cu), causal=causal)
+    assert x.tiles is (form != "rows")
+    see = np.arange(n)[:, None] >= np.arange(n)[None] if causal else np.ones((n, n), dtype=bool)   # token, position
+    none = ~see[:, 7:].any(1)                        # all that these see scores -inf
+    assert out[:n][none].isnan().all() and torch.isfinite(out[n:]).all()
+    some = torch.tensor(~none)
+    for p, d, z in ((3, 5, NAN), (4, 6, NAN), (5, 7, NAN), (14, 10, INF), (15, 11, -INF)):
+        at = torch.tensor(see[:, p]) & some
+        got = out[:n][at][..., d]
+        assert (got.isnan() if z != z else got == z).all(), (p, d)
+        assert torch.isfinite(out[:n][some & ~at][..., d]).all(), (p, d)
+    for p, d in ((9, 8), (11, 9)):
+        at = torch.tensor(see[:, p]) & some
+        assert not torch.isfinite(out[:n][at][..., d]).any() and torch.isfinite(out[:n][some & ~at][..., d]).all(), (p, d)
+    # all else is the attention of the positions that have weight
+    o, qq, kk, vv = (t.double().cpu().numpy() for t in (out, q, k, v))
+    o[..., 5:12] = vv[..., 5:12] = 0
+    for t in np.flatnonzero(~none):
+        live = np.flatnonzero(see[t] & (kk[:n, 0, 0] > -100))
+        for h in range(2):
+            check_rows(o[t:t + 1, h], qq[t:t + 1, h], kk[live, 0], vv[live, 0], [len(live)], D ** -0.5, BF16,
+                       f"token {t} head {h}")
+    assert x.status() == 0
+    x.close()

@@ -14,8 +14,8 @@
 //
 // A row sees the positions [x, y): its request's first token up to its own (causal) or its request's last.  Scores past
 // them are set to -inf in TMEM, in the tiles that some row does not see whole.  There V may hold infinities or NaN that
-// a weight of 0 does not make harmless: such elements are put to 0 for the product, and added at the end to the rows that
-// see them.
+// a weight of 0 does not make harmless: such elements are put to 0 for the product, and added at the end, times their
+// weights, to the rows that see them.
 //
 // The running reference of the softmax only moves when a row's maximum has grown by 2^8 (in the weights'
 // own units): until then weights up to 256 are as good in bf16 as weights up to 1, and O stays where it is.
@@ -106,17 +106,33 @@ struct PtItem {
 // Steps of 16 positions of tile j that a row tile sees some of.
 __device__ __forceinline__ int steps_of(int y1, int j) { return min(PT_N, y1 - j * PT_N + 15) >> 4; }
 
-// Adds to a row's 32 sums, from dim c on, the elements of V that were put to 0 for the product and that it sees: they
-// are outside the tiles that every row sees whole.
-__device__ __noinline__ void add_odd(const PromptArgs& p, const PtItem& it, int X, int x0, int x1, int c, float* o) {
-  for (int j = it.j0[X]; j < it.j1[X]; ++j) {
+// Adds to a chain's 32 sums of row r of row tile X, from dim c on, the elements of V in its tiles j0 .. j1 - 1 that were
+// put to 0 for the product and that the row sees, times their weights relative to the chain's reference (0 times an
+// infinity is NaN, as in the product): they are outside the tiles that every row sees whole.
+__device__ __noinline__ void add_odd(const PtArgs& a, const PtItem& it, const int2* spans, int X, int r, int j0, int j1,
+                                     float ref, int c, float* o) {
+  const PromptArgs& p = a.p;
+  if (r >= a.TT * a.G) return;
+  const int t = X * a.TT + r / a.G, x0 = spans[t].x - it.base, x1 = spans[t].y - it.base;
+  const uint16_t* q = p.q + static_cast<int64_t>(it.tok + t) * p.q_tok + static_cast<int64_t>(it.h * a.G + r % a.G) * p.q_head;
+  for (int j = j0; j < j1; ++j) {
     if (j >= it.w0 && j < it.w1) continue;
     const int y1 = min(x1, (j + 1) * PT_N);
     for (int y = max(x0, j * PT_N); y < y1; ++y) {
       const uint16_t* v = p.v + static_cast<int64_t>(it.base + y) * p.v_tok + it.h * p.v_head + c;
+      u32 worst = 0;
+      for (int i = 0; i < 32 && c + i < p.D; i += 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(v + i);
+        worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
+      }
+      if ((worst & 0x7f80u) != 0x7f80u && (worst & 0x7f800000u) != 0x7f800000u) continue;
+      const uint16_t* k = p.k + static_cast<int64_t>(it.base + y) * p.k_tok + it.h * p.k_head;
+      float s = 0.f;
+      for (int d = 0; d < p.D; ++d) s = fmaf(bf16_lo(q[d]), bf16_lo(k[d]), s);
+      const float w = ex2(s * (p.scale * LOG2E_F) - ref);
       for (int i = 0; i < 32 && c + i < p.D; ++i) {
         const float z = bf16_lo(v[i]);
-        if (!(fabsf(z) < INFINITY)) o[i] += z;
+        if (!(fabsf(z) < INFINITY)) o[i] += z * w;
       }
     }
   }
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   __shared__ PtItem ring[PT_RING];
   __shared__ int2 span[PT_RING][2 * PT_M];                // positions [x, y) of an item's tokens
   __shared__ float sums[2][2][PT_M];                      // of a row's weights, by the row tile's items in turn
-  __shared__ float refs[SPLIT ? 2 : 1][2][PT_M];          // and what they are relative to
+  __shared__ float refs[2][2][PT_M];                      // and what they are relative to
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   unsigned char* smem = pt_smem_raw + ((1024 - (smem_u32(pt_smem_raw) & 1023)) & 1023);
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             l += l0 + l1;
             if (j + STEP >= j1) {
               sums[O & 1][X][r] = l;
-              if (SPLIT) refs[O & 1][X][r] = m;
+              refs[O & 1][X][r] = m;
             }
           }
           tc_wait_st();
@@ -486,6 +502,19 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         }
         tc_fence_after();
         const u32 to = tm_o + X * DP + tl;
+        if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+          for (int c = 0; c < (both ? 2 * DP : DP); c += 32) {   // (the chains' sums stand side by side)
+            const int Y = SPLIT ? c / DP : X, half = (it.n + 1) / 2;
+            float o[32];
+            tc_ld32(to + c, o);
+            tc_wait_ld();
+            add_odd(a, it, span[t % PT_RING], X, r, SPLIT ? Y * half : it.j0[X], SPLIT ? (Y ? it.n : half) : it.j1[X],
+                    refs[o_turn >> Y & 1][Y][r], c % DP, o);
+            tc_st32(to + c, o);
+          }
+          tc_wait_st();
+        }
         float inv, other = 0.f;                           // what the sums are multiplied by (0 / 0 where every score is -inf: NaN)
         if (SPLIT) {
           const float m0 = refs[o_turn & 1][0][r], m1 = both ? refs[o_turn >> 1][1][r] : -INFINITY;
@@ -504,17 +533,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         uint16_t* out = sp.y > sp.x ? p.o + static_cast<int64_t>(it.tok + X * a.TT + tok_r) * p.o_tok +
                                           static_cast<int64_t>(it.h * a.G + g) * p.o_head
                                     : nullptr;
-        if (!SPLIT && __builtin_expect(odd, 0)) {
-#pragma unroll 1
-          for (int c = 0; c < DP; c += 32) {
-            float o[32];
-            tc_ld32(to + c, o);
-            tc_wait_ld();
-            add_odd(p, it, X, sp.x - it.base, sp.y - it.base, c, o);
-            tc_st32(to + c, o);
-          }
-          tc_wait_st();
-        }
         // 32 dims at a time through shared memory, so that a warp stores 64 bytes of 8 rows at once (a lane a row
         // takes 32 lines a store)
         uint16_t* at[4];
@@ -537,12 +555,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
             if (both) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], other, o[i]);
-            }
-            if (__builtin_expect(odd, 0)) {
-              float z[32];
-              for (int i = 0; i < 32; ++i) z[i] = 0.f;
-              add_odd(p, it, X, sp.x - it.base, sp.y - it.base, c, z);
-              for (int i = 0; i < 32; ++i) o[i] += z[i];
             }
           }
           __syncwarp();                                   // the 32 dims before have been read
