@@ -73,3 +73,53 @@ def test_prompts(form, D, causal):
                        f"token {t} head {h}")
     assert x.status() == 0
     x.close()
+
+
+def cache(lens, W, n_q, heads, H, D, spare=0):
+    from tests.test_gpu_attn16 import Decode16
+    d = Decode16(lens, W, heads, H, D, 16, 0, max_q=n_q, seed=D, spare=spare)
+    q = d.q(n_q, heads)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    d.kv.plan(i32(d.ctx), n_q)
+    pages = d.kv.table()[0].tolist()                 # sentence 0's, which all its beams share
+
+    def cell(side, p, dim):                          # of K/V head 0
+        return (pages[p // 16], d.layer, side, 0, p % 16, dim)
+    return d, q, cell
+
+
+def seen(out, n_q, W, G, p, length):
+    """Which rows of out [R, n_q, heads] read position p of sentence 0 through K/V head 0."""
+    m = torch.zeros(out.shape[:3], dtype=torch.bool)
+    for i in range(n_q):
+        m[:W, i, :G] = p < length - n_q + 1 + i
+    return m
+
+
+PAGED = [(1, 1, 64, 4, 2), (4, 1, 128, 4, 2), (1, 4, 80, 4, 1), (1, 8, 128, 8, 2), (3, 2, 64, 8, 2), (2, 8, 96, 4, 2), (1, 2, 256, 4, 2),
+         (1, 12, 256, 4, 2)]                         # W, n_q, D, heads, H
+
+
+@pytest.mark.parametrize("spare", [0, 900])         # segments whole and in pieces
+@pytest.mark.parametrize("W,n_q,D,heads,H", PAGED)
+def test_cache_however_small_the_weight_it_is_not_left_out(W, n_q, D, heads, H, spare):
+    """Also where such a position is all that a warp or a piece of the line has seen."""
+    length = 33                                      # position 32 stands in a unit of its own
+    d, q, cell = cache([length, 90], W, n_q, heads, H, D, spare)
+    want = d.kv.attend(d.layer, q)
+    G = heads // H
+    for p in (0, 15, 16, 20, 32):
+        k_at, v_at = cell(0, p, 0), cell(1, p, 5)
+        old = d.kv.pool[k_at].clone(), d.kv.pool[v_at].clone()
+        d.kv.pool[k_at] = -3e3 * D ** 0.5
+        clean = d.kv.attend(d.layer, q)
+        assert torch.isfinite(clean).all()
+        d.kv.pool[v_at] = INF
+        out = d.kv.attend(d.layer, q)
+        m = torch.zeros(out.shape, dtype=torch.bool)
+        m[..., 5] = seen(out, n_q, W, G, p, length)
+        assert not torch.isfinite(out[m]).any(), (p, out[m])
+        assert torch.equal(out[~m], clean[~m]), p
+        d.kv.pool[k_at], d.kv.pool[v_at] = old
+    assert torch.equal(d.kv.attend(d.layer, q), want) and d.kv.status() == 0
+    d.kv.close()

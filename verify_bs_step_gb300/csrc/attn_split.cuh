@@ -809,7 +809,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
         const float x = wm[w][r];
-        if (x != 0.f) {
+        if (Src::RAW || x != 0.f) {                         // (over the cache what is not finite stays so under a factor of 0)
           const float4 v = *reinterpret_cast<const float4*>(sp_smem + w * C::RING + (r * C::O_LD + d) * 4);
           a.x += v.x * x; a.y += v.y * x; a.z += v.z * x; a.w += v.w * x;
         }
