@@ -634,8 +634,9 @@ int kv16_append_args(vbs_kv16* ctx, const vbs_kv16_args* args);
 int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
 /*
  * Attention of the planned step over `layer`: as kv8_attention, over bf16 keys and values.  What a token does not see
- * may hold anything; an infinite or NaN element of V that it sees makes that element of its result infinite or NaN,
- * however small its weight.  Scores, softmax statistics and sums are fp32; the softmax weights are held to 16 bits (two bf16
+ * may hold anything; an infinite or NaN element of V that it sees counts as in the formula: a position that
+ * scores -inf has weight 0, which makes NaN of an infinity; one whose weight is too small for fp32 makes either of it.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are held to 16 bits (two bf16
  * parts) where up to 16 rows (beams x n_q x q_heads / H) of a sentence share a K/V head or head_dim is above 128, else
  * rounded to one bf16 number.
  * Errors: those of kv8_attention, and VBS_EINVAL where a stride of 0 puts rows of out at one place.

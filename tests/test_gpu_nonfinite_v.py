@@ -123,3 +123,27 @@ def test_cache_however_small_the_weight_it_is_not_left_out(W, n_q, D, heads, H, 
         d.kv.pool[k_at], d.kv.pool[v_at] = old
     assert torch.equal(d.kv.attend(d.layer, q), want) and d.kv.status() == 0
     d.kv.close()
+
+
+@pytest.mark.parametrize("spare", [0, 900])
+@pytest.mark.parametrize("W,n_q,D,heads,H", PAGED)
+def test_cache_a_position_without_weight_makes_nan_of_an_infinity(W, n_q, D, heads, H, spare):
+    length = 33                                      # position 32 stands in a unit of its own
+    d, q, cell = cache([length, 90], W, n_q, heads, H, D, spare)
+    want = d.kv.attend(d.layer, q)
+    G = heads // H
+    for p in (0, 15, 16, 20, 32):
+        k_at, v_at = cell(0, p, 0), cell(1, p, 5)
+        old = d.kv.pool[k_at].clone(), d.kv.pool[v_at].clone()
+        d.kv.pool[k_at] = -INF
+        clean = d.kv.attend(d.layer, q)
+        assert torch.isfinite(clean).all()
+        d.kv.pool[v_at] = INF
+        out = d.kv.attend(d.layer, q)
+        m = torch.zeros(out.shape, dtype=torch.bool)
+        m[..., 5] = seen(out, n_q, W, G, p, length)
+        assert out[m].isnan().all(), (p, out[m])
+        assert torch.equal(out[~m], clean[~m]), p
+        d.kv.pool[k_at], d.kv.pool[v_at] = old
+    assert torch.equal(d.kv.attend(d.layer, q), want) and d.kv.status() == 0
+    d.kv.close()

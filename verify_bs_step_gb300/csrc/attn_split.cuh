@@ -676,7 +676,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
       }
 
       // ---- V where some row does not see all of it: a weight of 0 times an infinity or NaN would be NaN.  Such elements
-      // go straight into the sums of the rows that see them (whatever their weights), and as zeros into the product ----
+      // go into the sums of the rows that see them, times the weights' first parts, and as zeros into the product ----
       if (Src::RAW && !clear) {
         bool odd = false;
         for (int L = lane; L < 16 * nc; L += 32) odd = odd || not_finite16(lds16(va + L * 16));
@@ -687,6 +687,9 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
+                const u32 two = t < 8 ? (x ? p[mt].y : p[mt].x) : (x ? p[mt].w : p[mt].z);
+                const u32 at = __shfl_sync(FULL, two, (lane & ~3) | (t >> 1 & 3));   // (the lane that holds the position's)
+                const float w = t & 1 ? bf16_hi(at) : bf16_lo(at);
                 if (!((u.rows >> beam[mt][x]) & 1u) || t >= lim[mt][x] - u.pos) continue;
 #pragma unroll
                 for (int j = 0; j < C::NT; ++j)
@@ -695,7 +698,7 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
                     const int dim = out_dim<C::VCH>(c4 * 2 + y, j);
                     if (!EXACT && dim >= D) continue;
                     const float z = lds_bf16(va + ((t * nc + dim / 8) ^ v_swz(t, nc)) * 16 + dim % 8 * 2);
-                    if (!(fabsf(z) < INFINITY)) o[mt][j][x * 2 + y] += z;
+                    if (!(fabsf(z) < INFINITY)) o[mt][j][x * 2 + y] += z * w;
                   }
               }
           __syncwarp();
