@@ -147,3 +147,27 @@ def test_cache_a_position_without_weight_makes_nan_of_an_infinity(W, n_q, D, hea
         d.kv.pool[k_at], d.kv.pool[v_at] = old
     assert torch.equal(d.kv.attend(d.layer, q), want) and d.kv.status() == 0
     d.kv.close()
+
+
+@pytest.mark.parametrize("spare", [0, 900])         # segments whole and in pieces
+@pytest.mark.parametrize("W,n_q,D,heads,H", PAGED)
+def test_cache_an_infinity_that_has_weight_stays_one(W, n_q, D, heads, H, spare):
+    length = 150
+    d, q, cell = cache([length, 90], W, n_q, heads, H, D, spare)
+    want = d.kv.attend(d.layer, q)
+    d.check(want, q)
+    for p in (0, 1, 7, 15, 16, 40, 63, 64, 100, 129, 143, 144, length - n_q, length - 1):
+        for dim, z in ((5, INF), (D - 1, -INF)):
+            at = cell(1, p, dim)
+            old = d.kv.pool[at].clone()
+            d.kv.pool[at] = z
+            out = d.kv.attend(d.layer, q)
+            m = torch.zeros(out.shape, dtype=torch.bool)
+            m[..., dim] = seen(out, n_q, W, heads // H, p, length)
+            assert (out[m] == z).all(), (p, dim, out[m])
+            assert torch.equal(out[~m], want[~m]), (p, dim)
+            d.kv.pool[at] = old
+    assert d.kv.status() == 0
+    d.kv.close()
+
+

@@ -654,6 +654,18 @@ attn_split_kernel(const Src src, const QO io, const SplitArgs sa) {
         if (C::ONE) {
           p[mt] = make_uint4(pack_bf16(w[0][0], w[0][1]), pack_bf16(w[1][0], w[1][1]), pack_bf16(w[0][2], w[0][3]),
                              pack_bf16(w[1][2], w[1][3]));
+        } else if (Src::RAW) {
+          // two bf16 parts of each weight, the first cut and not rounded, the second 2^-23 of the weight larger: both are
+          // above 0 where the weight is, so that an infinity of V stays one under each.  The products carry 16 bits.
+          float r[2][4];
+          const auto top = [](float lo, float hi) { return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632); };
+          p[mt] = make_uint4(top(w[0][0], w[0][1]), top(w[1][0], w[1][1]), top(w[0][2], w[0][3]), top(w[1][2], w[1][3]));
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) r[x][y] = fmaf(w[x][y], 1.f + 1.1920929e-7f, -bf16_hi(__float_as_uint(w[x][y])));
+          p2[mt] = make_uint4(pack_bf16(r[0][0], r[0][1]), pack_bf16(r[1][0], r[1][1]), pack_bf16(r[0][2], r[0][3]),
+                              pack_bf16(r[1][2], r[1][3]));
         } else if (Src::BF) {
           // two bf16 parts of each weight: the products carry 16 bits of it
           float r[2][4];
