@@ -307,7 +307,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
       // counted from the item's first position; rows that are not there see all of it (they are not written)
       const int x0 = sp.y > 0 ? sp.x - it.base : 0, x1 = sp.y > 0 ? sp.y - it.base : INT_MAX / 2;
       const int j0 = it.j0[X], j1 = it.j1[X];
-      float m = -INFINITY, l = 0.f;                       // the reference (in scaled units), the sum of weights
+      // the reference (in scaled units), the sum of weights.  Rows that are not there, whose scores are what shared memory
+      // and TMEM held before, have NaN, which stays one and is never above a limit: they have no say in the votes below
+      float m = sp.y > 0 ? -INFINITY : __int_as_float(0x7fffffff), l = 0.f;
       for (int j = j0; j < j1; j += STEP, ++S) {
         const int y = place(it.n, j) * PT_N, from = x0 - y, left = x1 - y;
         ok = __all_sync(FULL, pt_wait(&bars.s[X], S & 1, &gone, p));
