@@ -93,3 +93,24 @@ def test_blocks_that_stand_for_several_items(G, H, D, batch, even, causal):
             want = p @ v[lo:hi, h // G].float()
             assert (got[a:e, h] - want).abs().max() < bound, (h, a)
     x.close()
+
+
+@pytest.mark.parametrize("kv_heads,tokens,batch", [(1, 40, 3), (8, 9000, 7), (64, 20000, 300), (3, 2000, 5000), (1, 300, 300000)])
+def test_one_bad_start_among_many_is_told(kv_heads, tokens, batch):
+    """Wherever it stands, and whatever CTA works on which tokens."""
+    import verify_bs_step_gb300 as vbs
+    x = vbs.PromptAttention(kv_heads, 64)
+    q, k, v = tensors(tokens, kv_heads, kv_heads, 64)
+    good = np.sort(np.random.default_rng(batch).integers(0, tokens + 1, batch + 1))
+    x.attend(q, k, v, i32(good))
+    assert x.status() == 0
+    at = {0, 1, batch // 2, batch - 1, batch, min(31, batch), min(32, batch), min(33, batch), min(4864, batch), min(20000, batch)}
+    for b in sorted(at):
+        for bad in (-1, tokens + 1):
+            cu = good.copy()
+            cu[b] = bad
+            x.attend(q, k, v, i32(cu))
+            assert x.status() == vbs.EINVAL, (b, bad)
+    x.attend(q, k, v, i32(good))
+    assert x.status() == 0
+    x.close()

@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = tid; i * every <= p.B; i += PT_NT) cu[i] = p.cu[i * every];
-  if (blockIdx.x == 0)
-    for (int b = tid; b < p.B; b += PT_NT)
-      if (p.cu[b] < 0 || p.cu[b] > p.cu[b + 1] || p.cu[b + 1] > p.N) set_status(p.status, VBS_EINVAL);
+  // every CTA looks at all requests: no block is certain to be launched, as others may claim its items
+  for (int b = tid; b < p.B; b += PT_NT)
+    if (p.cu[b] < 0 || p.cu[b] > p.cu[b + 1] || p.cu[b + 1] > p.N) set_status(p.status, VBS_EINVAL);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
