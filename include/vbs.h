@@ -545,8 +545,8 @@ int rope_frequencies(int rot, double base, int scaling, double factor, double or
 /*
  * Rotary positions for heads of head_dim (1..256) dims, the first `rot` of which (even, 0..head_dim) are rotated:
  * at position p the pair (a, b) of frequency f becomes amplitude * (a cos pf - b sin pf, b cos pf + a sin pf); dims from
- * rot on stay as they are.  freq: rot / 2 radians a position (host).  Angles are exact to 2^-28 of a turn at every
- * position; products and sums are fp32, rounded once to the output's type.  The context holds a table of
+ * rot on stay as they are.  freq: rot / 2 radians a position (host).  An angle is within 2^-27 of a turn of the position
+ * times freq as given, at every position (and any freq up to 2^48); products and sums are fp32, rounded once to the output's type.  The context holds a table of
  * the frequencies on the current device (synchronises once) and may be used on any stream of it.
  * Errors: VBS_EINVAL (sizes, layout, NULL, a number not finite), VBS_ENOMEM, VBS_ECUDA.  *ctx is NULL on error.
  */

@@ -67,6 +67,20 @@ VBS_EXPORT int rope_frequencies(int rot, double base, int scaling, double factor
   return VBS_OK;
 }
 
+// x modulo 1 in units of 2^-64 (cut, so that x and -x make 0).
+static unsigned long long fraction(double x) {
+  const double r = x - std::nearbyint(x);   // exact
+  const unsigned long long u = static_cast<unsigned long long>(std::ldexp(std::fabs(r), 64));
+  return r < 0 ? 0 - u : u;
+}
+// The turns that a position makes, modulo 1, in units of 2^-64: freq times 1 / (2 pi) in two doubles, which leave some
+// 2^-108 freq of it.  (One double leaves up to 2^-55 freq: 2^-24 of a turn at position 2^31 for a frequency of 1.)
+static unsigned long long turn_fraction(double freq) {
+  constexpr double HI = 0x1.45f306dc9c883p-3, LO = -0x1.6b01ec5417056p-57;
+  const double p = freq * HI;
+  return fraction(p) + fraction(std::fma(freq, HI, -p) + freq * LO);
+}
+
 VBS_EXPORT int rope_init(vbs_rope** out, int head_dim, int rot, int layout, const double* freq, double amplitude) {
   if (!out) return VBS_EINVAL;
   *out = nullptr;
@@ -75,10 +89,7 @@ VBS_EXPORT int rope_init(vbs_rope** out, int head_dim, int rot, int layout, cons
   unsigned long long turns[vbs::ROPE_MAX_D / 2] = {};
   for (int i = 0; i < rot / 2; ++i) {
     if (!std::isfinite(freq[i])) return VBS_EINVAL;
-    // the fraction of a turn that a position makes, in units of 2^-64 (a double of it below 1 - 2^-53: no overflow)
-    double t = freq[i] / 6.283185307179586476925;
-    t -= std::floor(t);
-    turns[i] = t < 1.0 ? static_cast<unsigned long long>(std::ldexp(t, 64)) : 0;
+    turns[i] = turn_fraction(freq[i]);
   }
   vbs_rope* c = new (std::nothrow) vbs_rope{};
   if (!c) return VBS_ENOMEM;

@@ -2,8 +2,9 @@
 //
 // A token at position p turns the pair (a, b) of dims by p f: a' = a cos - b sin, b' = b cos + a sin, where the pair is
 // (i, i + rot / 2) or (2 i, 2 i + 1) and f its frequency.  Frequencies are held as turns a position in units of 2^-64,
-// so that p f modulo a turn is one 64-bit product that wraps, exact at any position; what is left of the nearest quarter
-// of a turn goes to sincospi in fp32.  Products and sums are fp32; a value is rounded once, to its output's type.
+// so that p f modulo a turn is one 64-bit product that wraps, off by 2^-32 of a turn at position 2^31; what is left of the
+// nearest quarter of a turn goes to sincospi in fp32.  Products and sums are fp32; a value is rounded once, to its
+// output's type.
 //
 // A warp takes a token and some of its heads (queries, keys and values in one line): it works out the token's angles
 // once, two or so a lane, into shared memory, and every lane keeps those of its 16 dims in registers over the heads.
