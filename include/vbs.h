@@ -538,7 +538,8 @@ typedef struct vbs_rope vbs_rope;
  *   VBS_ROPE_PARTS   by the turns r = original * freq / (2 pi) that a pair makes over the original length: freq where
  *                    r >= high, freq / factor where r <= low, between them the mean of both weighted by
  *                    (r - low) / (high - low)
- * Errors: VBS_EINVAL (NULL, rot odd or outside 0..256, base or a parameter of the scaling out of range).
+ * Errors: VBS_EINVAL (NULL, rot odd or outside 0..256, base or a parameter of the scaling out of range, a frequency that is
+ *   not finite).
  */
 int rope_frequencies(int rot, double base, int scaling, double factor, double original, double low, double high,
                      double* freq);
@@ -548,7 +549,8 @@ int rope_frequencies(int rot, double base, int scaling, double factor, double or
  * rot on stay as they are.  freq: rot / 2 radians a position (host).  An angle is within 2^-27 of a turn of the position
  * times freq as given, at every position (and any freq up to 2^48); products and sums are fp32, rounded once to the output's type.  The context holds a table of
  * the frequencies on the current device (synchronises once) and may be used on any stream of it.
- * Errors: VBS_EINVAL (sizes, layout, NULL, a number not finite), VBS_ENOMEM, VBS_ECUDA.  *ctx is NULL on error.
+ * Errors: VBS_EINVAL (sizes, layout, NULL, a number not finite, an amplitude past fp32), VBS_ENOMEM, VBS_ECUDA.  *ctx is
+ *   NULL on error.
  */
 int rope_init(vbs_rope** ctx, int head_dim, int rot, int layout, const double* freq, double amplitude);
 /*

@@ -54,6 +54,7 @@ VBS_EXPORT int rope_frequencies(int rot, double base, int scaling, double factor
                                     !std::isfinite(high)))
     return VBS_EINVAL;
   if (scaling == VBS_ROPE_BASE) base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+  if (!(base > 0) || !std::isfinite(base)) return VBS_EINVAL;
   for (int i = 0; i < rot / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rot);
     if (scaling == VBS_ROPE_LINEAR) f /= factor;
@@ -62,6 +63,7 @@ VBS_EXPORT int rope_frequencies(int rot, double base, int scaling, double factor
       const double keep = std::fmin(1.0, std::fmax(0.0, (turns - low) / (high - low)));
       f = f * keep + f / factor * (1.0 - keep);
     }
+    if (!std::isfinite(f)) return VBS_EINVAL;
     freq[i] = f;
   }
   return VBS_OK;
@@ -85,7 +87,8 @@ VBS_EXPORT int rope_init(vbs_rope** out, int head_dim, int rot, int layout, cons
   if (!out) return VBS_EINVAL;
   *out = nullptr;
   if (head_dim < 1 || head_dim > vbs::ROPE_MAX_D || rot < 0 || rot > head_dim || rot % 2 != 0) return VBS_EINVAL;
-  if ((layout != VBS_ROPE_HALF && layout != VBS_ROPE_INTERLEAVED) || !std::isfinite(amplitude) || (rot > 0 && !freq)) return VBS_EINVAL;
+  if ((layout != VBS_ROPE_HALF && layout != VBS_ROPE_INTERLEAVED) || !std::isfinite(static_cast<float>(amplitude)) || (rot > 0 && !freq))
+    return VBS_EINVAL;
   unsigned long long turns[vbs::ROPE_MAX_D / 2] = {};
   for (int i = 0; i < rot / 2; ++i) {
     if (!std::isfinite(freq[i])) return VBS_EINVAL;
