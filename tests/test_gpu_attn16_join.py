@@ -50,3 +50,29 @@ def test_many_segments(W, n_q, heads, H, D):
 def test_a_segment_of_several_hundred_pieces_among_many():
     """One long row among short ones: four warps share its pieces, also where rows have a warp each."""
     check([40000] + [30 + b for b in range(24)], 4, 1, 4, 1, 64)
+
+
+@pytest.mark.parametrize("length", [700, 1500, 4000])
+@pytest.mark.parametrize("W,n_q,heads,H,D", [(4, 1, 16, 4, 64), (4, 2, 8, 2, 128), (1, 17, 12, 3, 128), (1, 4, 8, 2, 256)])
+def test_an_infinity_stays_one_through_the_joins(W, n_q, heads, H, D, length):
+    """Of a value that all rows see, in the first, a middle and the last piece of its segment, few pieces and many."""
+    G = heads // H
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count // (min(W * n_q * G, 16) * H) + 1   # a warp a row
+    d = Decode16([length] + [60] * (B - 1), W, heads, H, D, 16, 0, max_q=n_q, spare=900, L=1, layer=0)
+    q = d.q(n_q, heads)
+    d.kv.plan(i32(d.ctx), n_q)
+    want = d.kv.attend(0, q)
+    assert torch.isfinite(want).all()
+    pages = d.kv.table()[0].tolist()
+    for p in (0, 17, length // 3, length // 2, 2 * length // 3, length - n_q - 40, length - n_q):
+        at = (pages[p // 16], 0, 1, H - 1, p % 16, 7)
+        old = d.kv.pool[at].clone()
+        d.kv.pool[at] = -float("inf")
+        out = d.kv.attend(0, q)
+        hit = torch.zeros(out.shape, dtype=torch.bool)
+        hit[:W, :, (H - 1) * G:, 7] = True
+        assert (out[hit] == -float("inf")).all(), (p, out[hit])
+        assert torch.equal(out[~hit], want[~hit]), p
+        d.kv.pool[at] = old
+    assert d.kv.status() == 0
+    d.kv.close()
