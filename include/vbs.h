@@ -547,8 +547,9 @@ int rope_frequencies(int rot, double base, int scaling, double factor, double or
  * Rotary positions for heads of head_dim (1..256) dims, the first `rot` of which (even, 0..head_dim) are rotated:
  * at position p the pair (a, b) of frequency f becomes amplitude * (a cos pf - b sin pf, b cos pf + a sin pf); dims from
  * rot on stay as they are.  freq: rot / 2 radians a position (host).  An angle is within 2^-27 of a turn of the position
- * times freq as given, at every position (and any freq up to 2^48); products and sums are fp32, rounded once to the output's type.  The context holds a table of
- * the frequencies on the current device (synchronises once) and may be used on any stream of it.
+ * times freq as given, at every position (and any freq up to 2^48); products and sums are fp32, rounded once to the
+ * output's type.  The context holds a table of the frequencies on the current device (synchronises once) and may be used
+ * on any stream of it.
  * Errors: VBS_EINVAL (sizes, layout, NULL, a number not finite, an amplitude past fp32), VBS_ENOMEM, VBS_ECUDA.  *ctx is
  *   NULL on error.
  */
@@ -606,7 +607,8 @@ int kv16_init(vbs_kv16** ctx, vbs_pkv* pkv, int q_heads, int max_q);
  * same strides) or apart from all inputs.  A token with a negative position is skipped altogether.  Without rope, pos,
  * k_out, q and q_out are NULL.
  * Errors: VBS_EINVAL (layer, n or dtype out of range, NULL pointers with n > 0, q without q_out or the reverse, a rope
- *   of another head_dim, an output's rows at one place by a stride of 0), VBS_ECUDA; a slot outside the pool is not written, with VBS_EINVAL in kv_paged_status().
+ *   of another head_dim, an output's rows at one place by a stride of 0), VBS_ECUDA; a slot outside the pool is not
+ *   written, with VBS_EINVAL in kv_paged_status().
  */
 int kv16_append(vbs_kv16* ctx, int layer, int64_t n, const int64_t* slots, int dtype, const void* k, int64_t k_tok,
                 int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, const vbs_rope* rope, const int32_t* pos,
@@ -636,11 +638,11 @@ int kv16_append_args(vbs_kv16* ctx, const vbs_kv16_args* args);
 int kv16_plan(vbs_kv16* ctx, const int32_t* ctx_len, int n_q);
 /*
  * Attention of the planned step over `layer`: as kv8_attention, over bf16 keys and values.  What a token does not see
- * may hold anything; an infinite or NaN element of V that it sees counts as in the formula: a position that
- * scores -inf has weight 0, which makes NaN of an infinity; one whose weight is too small for fp32 makes either of it.
- * Scores, softmax statistics and sums are fp32; the softmax weights are held to 16 bits (two bf16
- * parts) where up to 16 rows (beams x n_q x q_heads / H) of a sentence share a K/V head or head_dim is above 128, else
- * rounded to one bf16 number.
+ * may hold anything; an infinite or NaN element of V that it sees counts as in the formula: a position that scores
+ * -inf has weight 0, which makes NaN of an infinity; one whose weight is too small for fp32 makes either of it.
+ * Scores, softmax statistics and sums are fp32 (the sums of weights up to 2^8, before they are normalised: elements
+ * of V above 2^96 may overflow); the softmax weights are held to 16 bits (two bf16 parts) where up to 16 rows (beams
+ * x n_q x q_heads / H) of a sentence share a K/V head or head_dim is above 128, else rounded to one bf16 number.
  * Errors: those of kv8_attention, and VBS_EINVAL where a stride of 0 puts rows of out at one place.
  */
 int kv16_attention(vbs_kv16* ctx, int layer, const void* q, int64_t q_row, int64_t q_tok, int64_t q_head, float scale,
@@ -678,14 +680,14 @@ int pattn_init(vbs_pattn** ctx, int q_heads, int kv_heads, int head_dim, vbs_str
  * All bf16 (device), head_dim contiguous: token t's head h of q is at q + t * q_tok + h * q_head (elements), k, v and out
  * likewise; out is apart from the inputs.  Tokens of no request are neither used nor written.  What a token does not see
  * may hold anything.
- * Scores, softmax statistics and sums are fp32; the softmax weights are rounded to bf16 before the product with V (not
+ * Scores, softmax statistics and sums are fp32 (the sums of weights up to 2^8, before they are normalised: elements of V
+ * above 2^96 may overflow); the softmax weights are rounded to bf16 before the product with V (not
  * in the kernel for more than 128 heads a group, or q, k, v whose addresses and strides are not multiples of 16 bytes:
- * pattn_kernel tells; it is some 50 times slower).
+ * pattn_kernel tells; it is some 90 times slower: 2.9 ms for 2000 tokens x 32 heads over 8 x 128).
  * An infinite or NaN element of V counts for every token that sees it, as in the formula: a position that scores -inf has
  * weight 0, which makes NaN of an infinity; one whose weight is too small for fp32 makes either of it.
  * Errors: VBS_EINVAL (n or batch outside 0..2^30, NULL pointers, scale not finite, rows of out at one place by a stride of
- *   0), VBS_ECUDA; a request that is not
- *   within the tokens counts as none, with VBS_EINVAL in pattn_status().
+ *   0), VBS_ECUDA; a request that is not within the tokens counts as none, with VBS_EINVAL in pattn_status().
  */
 int pattn_run(vbs_pattn* ctx, int64_t n, int batch, const int32_t* cu, const void* q, int64_t q_tok, int64_t q_head,
               const void* k, int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int causal,

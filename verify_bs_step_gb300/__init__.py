@@ -681,7 +681,10 @@ class PagedKV8(PagedKV):
 
     def attend(self, layer: int, q: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None):
         """softmax(scale q k^T) v of q [R, n_q, heads, D] (bfloat16, unit stride along D) over each row's
-        cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
+        cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5.
+
+        The softmax weights are held to 16 bits, but rounded to bf16 where more than 16 rows of a sentence (beams x
+        n_q x heads / H) share a K/V head and D is up to 128."""
         shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
         qs = _rows4(q, "q", shape)
         out, os_ = _output(out, shape, self.device)
@@ -895,7 +898,10 @@ class PagedKV16(PagedKV):
 
     def attend(self, layer: int, q: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None):
         """softmax(scale q k^T) v of q [R, n_q, heads, D] (bfloat16, unit stride along D) over each row's
-        cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5."""
+        cached positions up to the token's own (plan() has set n_q); scale defaults to D ** -0.5.
+
+        The softmax weights are held to 16 bits, but rounded to bf16 where more than 16 rows of a sentence (beams x
+        n_q x heads / H) share a K/V head and D is up to 128."""
         shape = self._q_shape or (self.R, q.shape[1] if q.dim() > 1 else 0, self.heads, self.D)
         order, bf = self._order, torch.bfloat16
         qs = _rows(q, "q", shape, bf, order.index)
@@ -937,7 +943,9 @@ class PromptAttention:
         """softmax(scale q k^T) v: q [N, heads, D], k and v [N, kv_heads, D] (bfloat16, unit stride along D) over each
         token's own request, up to the token (causal) or the whole of it.  Request b has the tokens
         cu[b] .. cu[b + 1] - 1 (int32 [batch + 1] on the device, as PagedKV.build() gives it); other tokens' rows of out
-        are left as they are.  scale defaults to D ** -0.5."""
+        are left as they are.  scale defaults to D ** -0.5.
+
+        The softmax weights are rounded to bf16 for the product with v (not in the kernel for other layouts, `tiles`)."""
         i = self._order.index
         N = q.shape[0] if q.dim() == 3 else 0
         shape, kv_shape = (N, self.heads, self.D), (N, self.kv_heads, self.D)

@@ -1002,7 +1002,12 @@ int launch_split_as(const Src& src, const QO& io, const SplitArgs& sa, int num_s
   }
   if (launch_dependent(kernel, dim3(num_sms * C::CTAS), dim3(32 * NW), C::SMEM, s, src, io, sa) != VBS_OK) return VBS_ECUDA;
   if constexpr (Src::RAW) {
-    // 100003 positions x 8 heads leave 38 pieces a head: the whole step takes 97 us (cold caches) with a warp a row, 95 with four
+    // Few rows: four warps share a row's pieces.  A warp a row / four, us a call (sentences x rows of a segment x K/V heads x
+    // head_dim x positions).  Up to 2 rows a SM: 1 x 1 x 8 x 128 x 100003: 74.0 / 72.8; 1 x 16 x 8 x 128 x 30000: 36.3 / 33.1;
+    // 1 x 8 x 8 x 64 x 8000: 18.2 / 14.4; 1 x 32 x 8 x 128 x 30000: 39.3 / 37.0; 1 x 4 x 1 x 256 x 60000: 38.9 / 26.0; 4 x 4 x 8 x
+    // 128 x 9000: 36.7 / 34.7; 8 x 4 x 8 x 64 x 2000: 16.4 / 16.4.  More: 10 x 4 x 8 x 128 x 4000: 36.8 / 35.7; 12: 41.0 / 41.1;
+    // 20: 58.6 / 60.7; 40 x 2000: 60.4 / 63.0; 64 x 4 x 8 x 128 x 1064: 52.8 / 55.5; 64 x 32 x 8 x 128 x 1250: 76.4 / 99.6 (with
+    // long sentences four still pay there: 4 x 16 x 8 x 64 x 9000: 22.5 / 20.5).
     if (segments * std::min(sa.M, 16 * MT) <= 2 * num_sms)
       return launch_dependent(attn_join_kernel<DP, 16 * MT, true>, dim3(static_cast<unsigned>(segments), std::min(sa.M, 16 * MT)),
                               dim3(32 * JN_WARPS), 0, s, io, sa);
