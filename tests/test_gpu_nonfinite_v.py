@@ -171,3 +171,46 @@ def test_cache_an_infinity_that_has_weight_stays_one(W, n_q, D, heads, H, spare)
     d.kv.close()
 
 
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_prompts_a_nan_costs_no_more_than_a_few_times_the_call(G):
+    """One that a request of many tokens shares an item with, and ones among its own, near and far: looking for them takes a
+    few times what the attention does (it took some hundred times that, and with the tokens came near the limit of waits)."""
+    import verify_bs_step_gb300 as vbs
+    n, D = 30000, 128
+    cu = i32(starts([100, n]))
+    q, k, v = tensors(100 + n, G, 1, D)
+    x = vbs.PromptAttention(G, D, kv_heads=1)
+
+    def ms():
+        best = 1e9
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            x.attend(q, k, v, cu, causal=False, out=out)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    out = torch.empty(100 + n, G, D, device="cuda", dtype=torch.bfloat16)
+    clean = ms()
+    want = out.clone()
+    v = v.clone()
+    v[50, 0, 5] = NAN
+    one = ms()
+    assert out[:100, :, 5].isnan().all()
+    out[:100, :, 5] = want[:100, :, 5]
+    assert torch.equal(out, want)
+    for p in (103, 17000, 99 + n):
+        v[p, 0, 7] = INF
+    several = ms()
+    assert (out[100:, :, 7] == INF).all()
+    out[:100, :, 5], out[100:, :, 7] = want[:100, :, 5], want[100:, :, 7]
+    assert torch.equal(out, want) and x.status() == 0
+    v[100:] = NAN                                    # all that the request has
+    all_ = ms()
+    print(f"{clean:.3f} ms, with one NaN {one:.3f}, several infinities {several:.3f}, all NaN {all_:.3f}")
+    assert out[100:].isnan().all()
+    assert max(one, several) < 20 * clean and all_ < 100 * clean, (clean, one, several, all_)
+    x.close()

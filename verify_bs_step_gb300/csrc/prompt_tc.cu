@@ -101,39 +101,60 @@ struct PtItem {
   int y1[2];                              // the end of what a row tile sees, counted from the first position
   int j0[2], j1[2];                       // its tiles
   int w0, w1;                             // tiles that every row of both sees whole: their V is used as it is
+  int odd0, odd1;                         // the first and the last tile of whose V elements were put to 0; none: odd0 > odd1
 };
 
 // Steps of 16 positions of tile j that a row tile sees some of.
 __device__ __forceinline__ int steps_of(int y1, int j) { return min(PT_N, y1 - j * PT_N + 15) >> 4; }
 
-// Adds to a chain's 32 sums of row r of row tile X, from dim c on, the elements of V in its tiles j0 .. j1 - 1 that were
-// put to 0 for the product and that the row sees, times their weights relative to the chain's reference (0 times an
-// infinity is NaN, as in the product): they are outside the tiles that every row sees whole.
+// Adds to a chain's 32 sums of a lane's row r of row tile X, from dim c on, the elements of V in its tiles j0 .. j1 - 1 that
+// were put to 0 for the product and that the row sees, times their weights relative to the chain's reference (0 times an
+// infinity is NaN, as in the product): they are outside the tiles that every row sees whole.  By a converged warp, whose
+// lanes look for such positions 32 at a time.
 __device__ __noinline__ void add_odd(const PtArgs& a, const PtItem& it, const int2* spans, int X, int r, int j0, int j1,
                                      float ref, int c, float* o) {
   const PromptArgs& p = a.p;
-  if (r >= a.TT * a.G) return;
-  const int t = X * a.TT + r / a.G, x0 = spans[t].x - it.base, x1 = spans[t].y - it.base;
+  const int lane = threadIdx.x & 31, t = X * a.TT + r / a.G;
+  const int2 sp = r < a.TT * a.G ? spans[t] : make_int2(0, 0);
+  const int x0 = sp.y > sp.x ? sp.x - it.base : INT_MAX, x1 = sp.y > sp.x ? sp.y - it.base : 0;
+  const int first = __reduce_min_sync(FULL, x0), end = __reduce_max_sync(FULL, x1);
   const uint16_t* q = p.q + static_cast<int64_t>(it.tok + t) * p.q_tok + static_cast<int64_t>(it.h * a.G + r % a.G) * p.q_head;
+  u32 nan = sp.y > sp.x ? 0u : ~0u;                       // the sums that are NaN, and stay so (or are none)
+  for (int i = 0; i < 32; ++i) nan |= o[i] == o[i] && c + i < p.D ? 0u : 1u << i;
   for (int j = j0; j < j1; ++j) {
     if (j >= it.w0 && j < it.w1) continue;
-    const int y1 = min(x1, (j + 1) * PT_N);
-    for (int y = max(x0, j * PT_N); y < y1; ++y) {
-      const uint16_t* v = p.v + static_cast<int64_t>(it.base + y) * p.v_tok + it.h * p.v_head + c;
-      u32 worst = 0;
-      for (int i = 0; i < 32 && c + i < p.D; i += 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(v + i);
-        worst = max_abs2(max_abs2(max_abs2(worst, w.x), max_abs2(w.y, w.z)), w.w);
+    const int y1 = min(end, (j + 1) * PT_N);
+    for (int y = max(first, j * PT_N); y < y1; y += 32) {
+      if (__all_sync(FULL, nan == ~0u)) return;
+      u32 bad = 0;                                        // of the lane's position
+      if (y + lane < y1) {
+        const uint16_t* v = p.v + static_cast<int64_t>(it.base + y + lane) * p.v_tok + it.h * p.v_head + c;
+        for (int i = 0; i < 32 && c + i < p.D; i += 8) {
+          float f[8];
+          Vec16<bf16_t>::unpack(*reinterpret_cast<const uint4*>(v + i), f);
+          for (int e = 0; e < 8; ++e) bad |= fabsf(f[e]) < INFINITY ? 0u : 1u << (i + e);
+        }
       }
-      if ((worst & 0x7f80u) != 0x7f80u && (worst & 0x7f800000u) != 0x7f800000u) continue;
-      const uint16_t* k = p.k + static_cast<int64_t>(it.base + y) * p.k_tok + it.h * p.k_head;
-      float s = 0.f;
-      for (int d = 0; d < p.D; ++d) s = fmaf(bf16_lo(q[d]), bf16_lo(k[d]), s);
-      const float w = ex2(s * (p.scale * LOG2E_F) - ref);
-      for (int i = 0; i < 32 && c + i < p.D; ++i) {
-        const float z = bf16_lo(v[i]);
-        if (!(fabsf(z) < INFINITY)) o[i] += z * w;
+      for (u32 which = __ballot_sync(FULL, bad != 0); which != 0; which &= which - 1) {
+        const int n = y + __ffs(which) - 1;
+        u32 dims = __shfl_sync(FULL, bad, n - y) & ~nan;
+        if (dims == 0 || n < x0 || n >= x1) continue;
+        const uint16_t* k = p.k + static_cast<int64_t>(it.base + n) * p.k_tok + it.h * p.k_head;
+        float s = 0.f, f[8], g[8];
+        for (int d = 0; d < p.D; d += 8) {
+          Vec16<bf16_t>::unpack(*reinterpret_cast<const uint4*>(q + d), f);
+          Vec16<bf16_t>::unpack(*reinterpret_cast<const uint4*>(k + d), g);
+          for (int e = 0; e < 8; ++e) s = fmaf(f[e], g[e], s);
+        }
+        const float w = ex2(s * (p.scale * LOG2E_F) - ref);
+        const uint16_t* v = p.v + static_cast<int64_t>(it.base + n) * p.v_tok + it.h * p.v_head + c;
+        for (; dims != 0; dims &= dims - 1) {
+          const int i = __ffs(dims) - 1;
+          o[i] += bf16_lo(v[i]) * w;
+          nan |= o[i] == o[i] ? 0u : 1u << i;
+        }
       }
+      __syncwarp();
     }
   }
 }
@@ -221,7 +242,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   __shared__ __align__(8) PtBars bars;
   __shared__ u32 tmem_base;
   __shared__ volatile int gone;
-  __shared__ volatile int odd;                            // an infinity or NaN of V was put to 0 (stays so)
   __shared__ __align__(16) uint4 claim;
   __shared__ PtItem ring[PT_RING];
   __shared__ int2 span[PT_RING][2 * PT_M];                // positions [x, y) of an item's tokens
@@ -264,7 +284,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     mbar_init(&bars.end, 2);
     fence_mbar_init();
     gone = 0;
-    odd = 0;
   }
   if (wid == PT_W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "r"(512)
@@ -482,7 +501,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
                 }
                 row[c] = w;
               }
-              odd = 1;
+              atomicMin(&ring[u % PT_RING].odd0, place(it.n, j));
+              atomicMax(&ring[u % PT_RING].odd1, place(it.n, j));
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -504,15 +524,16 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         }
         tc_fence_after();
         const u32 to = tm_o + X * DP + tl;
-        if (__builtin_expect(odd, 0)) {
+        const int odd0 = __shfl_sync(FULL, it.odd0, 0), odd1 = __shfl_sync(FULL, it.odd1, 0);
+        if (__builtin_expect(odd0 <= odd1, 0)) {
 #pragma unroll 1
           for (int c = 0; c < (both ? 2 * DP : DP); c += 32) {   // (the chains' sums stand side by side)
             const int Y = SPLIT ? c / DP : X, half = (it.n + 1) / 2;
             float o[32];
             tc_ld32(to + c, o);
             tc_wait_ld();
-            add_odd(a, it, span[t % PT_RING], X, r, SPLIT ? Y * half : it.j0[X], SPLIT ? (Y ? it.n : half) : it.j1[X],
-                    refs[o_turn >> Y & 1][Y][r], c % DP, o);
+            add_odd(a, it, span[t % PT_RING], X, r, max(odd0, SPLIT ? Y * half : it.j0[X]),
+                    min(odd1 + 1, SPLIT ? (Y ? it.n : half) : it.j1[X]), refs[o_turn >> Y & 1][Y][r], c % DP, o);
             tc_st32(to + c, o);
           }
           tc_wait_st();
@@ -822,6 +843,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
           x.n = n;
           x.w0 = w0;
           x.w1 = w1;
+          x.odd0 = INT_MAX;
+          x.odd1 = -1;
         }
         __syncwarp();
         if (some || last) {
