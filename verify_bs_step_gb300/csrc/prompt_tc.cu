@@ -54,6 +54,10 @@ constexpr int PT_NT = PT_SM + PT_OUT + 128;   // and warps for the loads, each r
 constexpr int PT_W_OUT = PT_SM / 32, PT_W_LOAD = PT_W_OUT + PT_OUT / 32, PT_W_MMA = PT_W_LOAD + 1;
 constexpr int PT_RING = 4;                // items on their way
 constexpr int PT_CU = 2048;               // request starts held in shared memory
+// Below so many requests every CTA looks at all of them while it waits for its first scores, from here on a launch before the
+// tiles does (us a call, the first / the second: 5000 requests of 2000 tokens x 4 heads 12.5 / 16.2; and, the CTAs looking
+// before they start, 21333 of 64000 x 8 80 / 74, 100000 of 2000 x 4 63 / 24).
+constexpr int PT_LOOK = 8192;
 constexpr int PT_STMAX = 4;
 // Items of this many tiles and more: the row tiles' products go in turn, so that one's run while the other's softmax
 // does.  Left alone both fall into step and wait together (16001 tokens: 1605 us alone, 1432 in turn; 64 x 1000, whose
@@ -229,6 +233,18 @@ __device__ __forceinline__ bool pt_wait(u64* bar, u32 parity, volatile int* gone
   return true;
 }
 
+// Tells where a request is not within the tokens: threads `at`, `at` + `step`, ... of all that look.
+__device__ __forceinline__ void check_requests(const PromptArgs& p, const int* cu, int at, int step) {
+  for (int b = at; b < p.B; b += step)
+    if (cu[b] < 0 || cu[b] > cu[b + 1] || cu[b + 1] > p.N) set_status(p.status, VBS_EINVAL);
+}
+// For so many requests that the tiles' CTAs do not look themselves.
+__global__ void __launch_bounds__(256) prompt_starts_kernel(const PromptArgs p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  check_requests(p, p.cu, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+}
+
 // SPLIT: an item is one row tile, the first and the second half of whose positions the two chains take; their sums are
 // joined when they are brought out.
 template <int DP, bool SPLIT>
@@ -294,9 +310,6 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = tid; i * every <= p.B; i += PT_NT) cu[i] = p.cu[i * every];
-  // every CTA looks at all requests: no block is certain to be launched, as others may claim its items
-  for (int b = tid; b < p.B; b += PT_NT)
-    if (p.cu[b] < 0 || p.cu[b] > p.cu[b + 1] || p.cu[b + 1] > p.N) set_status(p.status, VBS_EINVAL);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -311,6 +324,9 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PT_REGS_SM));
     const int X = wid >> 2, r = tid & (PT_M - 1);          // row tile, row
     const u32 tl = static_cast<u32>((wid & 3) * 32) << 16;  // its TMEM lanes
+    // every CTA looks at the requests while it waits for its first scores: no block is certain to be launched, as others may
+    // claim its items
+    if (p.B < PT_LOOK) check_requests(p, every == 1 ? cu : p.cu, tid, PT_SM);
     const u32 ts = tm_s + X * PT_N + tl, to = tm_o + X * DP + tl;
     const bool neg = p.scale < 0.f;
     // (a scale of 0 stays above it, so that a masked -inf stays one)
@@ -952,6 +968,9 @@ int launch_prompt_tc(const PromptArgs& p, int num_sms, cudaStream_t s) {
   const int many = batch > 1 ? static_cast<int>(items * 3 / 4 / batch) : 0;
   const PtArgs a{p, G, TT, per, static_cast<int>(tiles), batch, many,
                  (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && (p.o_tok | p.o_head) % 8 == 0};
+  if (p.B >= PT_LOOK && launch_dependent(prompt_starts_kernel, dim3(std::min((p.B + 255) / 256, 8 * num_sms)), dim3(256), 0, s,
+                                         p) != VBS_OK)
+    return VBS_ECUDA;
   if (p.D <= 64) return split ? launch_tc<64, true>(qm, km, vm, a, s) : launch_tc<64, false>(qm, km, vm, a, s);
   if (p.D <= 128) return split ? launch_tc<128, true>(qm, km, vm, a, s) : launch_tc<128, false>(qm, km, vm, a, s);
   return launch_tc<256, false>(qm, km, vm, a, s);
