@@ -115,7 +115,7 @@ __device__ __forceinline__ int steps_of(int y1, int j) { return min(PT_N, y1 - j
 // were put to 0 for the product and that the row sees, times their weights relative to the chain's reference (0 times an
 // infinity is NaN, as in the product): they are outside the tiles that every row sees whole.  By a converged warp, whose
 // lanes look for such positions 32 at a time.
-__device__ __noinline__ void add_odd(const PtArgs& a, const PtItem& it, const int2* spans, int X, int r, int j0, int j1,
+__device__ __forceinline__ void add_odd(const PtArgs& a, const PtItem& it, const int2* spans, int X, int r, int j0, int j1,
                                      float ref, int c, float* o) {
   const PromptArgs& p = a.p;
   const int lane = threadIdx.x & 31, t = X * a.TT + r / a.G;
@@ -161,6 +161,25 @@ __device__ __noinline__ void add_odd(const PtArgs& a, const PtItem& it, const in
       __syncwarp();
     }
   }
+}
+
+// The same for all sums of a row, in TMEM from `to` on (both: of two chains, side by side), with the row tiles' or chains'
+// references.  (A function of its own, loads and stores too: inline, though it hardly ever runs, it cost 5 % where items are short.)
+template <int DP, bool SPLIT>
+__device__ __noinline__ void add_odd_all(const PtArgs& a, const PtItem& it, const int2* spans, int X, int r, u32 to, bool both,
+                                         const float* ref0, const float* ref1) {
+  const int odd0 = __shfl_sync(FULL, it.odd0, 0), odd1 = __shfl_sync(FULL, it.odd1, 0), half = (it.n + 1) / 2;
+#pragma unroll 1
+  for (int c = 0; c < (both ? 2 * DP : DP); c += 32) {
+    const int Y = SPLIT ? c / DP : X;
+    float o[32];
+    tc_ld32(to + c, o);
+    tc_wait_ld();
+    add_odd(a, it, spans, X, r, max(odd0, SPLIT ? Y * half : it.j0[X]), min(odd1 + 1, SPLIT ? (Y ? it.n : half) : it.j1[X]),
+            Y ? *ref1 : *ref0, c % DP, o);
+    tc_st32(to + c, o);
+  }
+  tc_wait_st();
 }
 
 __device__ __forceinline__ void tma_load3(u32 dst, const CUtensorMap* map, u64* bar, int x, int h, int t) {
@@ -540,20 +559,8 @@ __global__ void __launch_bounds__(PT_NT, 1) prompt_tc_kernel(const __grid_consta
         }
         tc_fence_after();
         const u32 to = tm_o + X * DP + tl;
-        const int odd0 = __shfl_sync(FULL, it.odd0, 0), odd1 = __shfl_sync(FULL, it.odd1, 0);
-        if (__builtin_expect(odd0 <= odd1, 0)) {
-#pragma unroll 1
-          for (int c = 0; c < (both ? 2 * DP : DP); c += 32) {   // (the chains' sums stand side by side)
-            const int Y = SPLIT ? c / DP : X, half = (it.n + 1) / 2;
-            float o[32];
-            tc_ld32(to + c, o);
-            tc_wait_ld();
-            add_odd(a, it, span[t % PT_RING], X, r, max(odd0, SPLIT ? Y * half : it.j0[X]),
-                    min(odd1 + 1, SPLIT ? (Y ? it.n : half) : it.j1[X]), refs[o_turn >> Y & 1][Y][r], c % DP, o);
-            tc_st32(to + c, o);
-          }
-          tc_wait_st();
-        }
+        if (__builtin_expect(__any_sync(FULL, it.odd0 <= it.odd1), 0))
+          add_odd_all<DP, SPLIT>(a, it, span[t % PT_RING], X, r, to, both, &refs[o_turn & 1][0][r], &refs[o_turn >> 1][1][r]);
         float inv, other = 0.f;                           // what the sums are multiplied by (0 / 0 where every score is -inf: NaN)
         if (SPLIT) {
           const float m0 = refs[o_turn & 1][0][r], m1 = both ? refs[o_turn >> 1][1][r] : -INFINITY;
