@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(32 * JN_WARPS) attn_join_kernel(const QO io, c
 #pragma unroll
         for (int v = 0; v < V; ++v)
           q[c][v] = c < np && lane * 4 + v * 128 < DP ? __ldcg(reinterpret_cast<const float4*>(pp + r * DP + v * 128) + lane)
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       top = mm[0];
 #pragma unroll

@@ -87,7 +87,8 @@ VBS_EXPORT int rope_init(vbs_rope** out, int head_dim, int rot, int layout, cons
   if (!out) return VBS_EINVAL;
   *out = nullptr;
   if (head_dim < 1 || head_dim > vbs::ROPE_MAX_D || rot < 0 || rot > head_dim || rot % 2 != 0) return VBS_EINVAL;
-  if ((layout != VBS_ROPE_HALF && layout != VBS_ROPE_INTERLEAVED) || !std::isfinite(static_cast<float>(amplitude)) || (rot > 0 && !freq))
+  if ((layout != VBS_ROPE_HALF && layout != VBS_ROPE_INTERLEAVED) || !std::isfinite(static_cast<float>(amplitude)) ||
+      (rot > 0 && !freq))
     return VBS_EINVAL;
   unsigned long long turns[vbs::ROPE_MAX_D / 2] = {};
   for (int i = 0; i < rot / 2; ++i) {
